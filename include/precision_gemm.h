@@ -349,6 +349,196 @@ int sgemm_force_plan(int bn, int split_k);
 #define SGEMM_DEBUG_FAIL_TENSOR_MAP 4
 int sgemm_debug_flags(int flags);
 
+/* ---- layers of language models ------------------------------------------------
+ *
+ * The products of a feed-forward block, dense and spread over experts, with what
+ * surrounds them.  Here matrices are ROW-major, as layers store them: element
+ * (i, j) of a matrix with leading dimension ld is X[i*ld + j], ld >= its columns.
+ * Every operand of one call has the element type `dtype`; all sums, scores and
+ * routing weights are FP32.  SGEMM_BF16 products are exact and accumulated in
+ * FP32, each result rounded once.  SGEMM_F32 operands give FP32 accuracy (a
+ * relative error of a few 2^-22 of sum|x w| / sqrt(k), not TF32's).
+ * Operands may not overlap results, except that `residual` may be `y` itself.
+ * Status codes, streams, workspaces and threads are as for sgemm: -i names the
+ * first invalid argument, work is queued on `stream`, and the workspace comes
+ * from the stream's (sgemm_set_workspace applies).
+ */
+
+/* Element types (argument `dtype`). */
+#define SGEMM_F32 0
+#define SGEMM_BF16 1
+
+/* Activations (argument `act`): z; max(z, 0); z / (1 + exp(-z));
+ * z * Phi(z) with Phi the normal distribution (erf); and its tanh form
+ * z/2 * (1 + tanh(sqrt(2/pi) * (z + 0.044715 z^3))). */
+#define SGEMM_ACT_NONE 0
+#define SGEMM_ACT_RELU 1
+#define SGEMM_ACT_SILU 2
+#define SGEMM_ACT_GELU 3
+#define SGEMM_ACT_GELU_TANH 4
+
+/* Routing scores (argument `score`). */
+#define SGEMM_SCORE_SOFTMAX 0
+#define SGEMM_SCORE_SIGMOID 1
+
+/* Limits of the routing and expert calls. */
+#define SGEMM_MAX_EXPERTS 512
+#define SGEMM_MAX_TOP 32
+
+/*
+ * sgemm_linear -- y = act(x w^T + bias) + residual.
+ *
+ *   dtype (1); t, n, k >= 0 (2-4): x is t x k, w is n x k, y is t x n
+ *   x, ldx (5, 6), w, ldw (7, 8)
+ *   bias      n elements, or NULL (9)
+ *   act       SGEMM_ACT_* (10)
+ *   residual  t x n, or NULL; ldr (11, 12)
+ *   y, ldy (13, 14)
+ *   preact    t x n, or NULL: receives x w^T + bias, which sgemm_linear_backward
+ *             reads; ldz (15, 16)
+ *
+ * k == 0 leaves the product zero (x and w are not read).
+ */
+int sgemm_linear(int dtype, int64_t t, int64_t n, int64_t k, const void *x, int64_t ldx, const void *w,
+                 int64_t ldw, const void *bias, int act, const void *residual, int64_t ldr, void *y,
+                 int64_t ldy, void *preact, int64_t ldz, void *stream);
+
+/*
+ * sgemm_linear_backward -- the gradients of sgemm_linear for dy (the residual's
+ * is dy itself).  With dz = dy * act'(preact):
+ *
+ *     dx = dz w,   dw = dz^T x,   dbias = the sum of dz's rows.
+ *
+ *   dtype, t, n, k (1-4); dy, lddy (5, 6); x, ldx (7, 8); w, ldw (9, 10);
+ *   act (11); preact, ldz (12, 13): read unless act is SGEMM_ACT_NONE;
+ *   dx, lddx (14, 15), dw, lddw (16, 17), dbias (18): each may be NULL, which
+ *   skips that gradient (and leaves what only it needs unread).
+ *
+ * For SGEMM_BF16, dz is rounded to bfloat16 before the two products, whose
+ * tensor-core operands have that type; dbias sums it unrounded.  Sums run in a
+ * fixed order: equal inputs give equal bits.
+ */
+int sgemm_linear_backward(int dtype, int64_t t, int64_t n, int64_t k, const void *dy, int64_t lddy,
+                          const void *x, int64_t ldx, const void *w, int64_t ldw, int act,
+                          const void *preact, int64_t ldz, void *dx, int64_t lddx, void *dw,
+                          int64_t lddw, void *dbias, void *stream);
+
+/*
+ * sgemm_route -- choose `top` experts per token and their weights.
+ *
+ *   p      = softmax(logits) over the experts, or sigmoid(logits), in FP32
+ *   choice = p + balance (the balance bias steers the choice, not the weights)
+ *   groups > 1: the experts form `groups` equal runs; a run scores the sum of its
+ *            two best choices and only the group_top best runs stay
+ *   ids    = the `top` experts of the best choice, best first
+ *   weights = p[ids], divided by their sum when renormalize, times scale
+ *
+ * Equal values go to the lower index.  A NaN logit counts as -infinity.  A token
+ * whose scores of chosen experts sum to zero gets weights of zero.  Tokens with
+ * mask[token] == 0 get ids of -1 and weights of zero.
+ *
+ *   dtype of logits (1); tokens >= 0 (2); experts in [1, SGEMM_MAX_EXPERTS] (3);
+ *   top in [1, min(experts, SGEMM_MAX_TOP)] (4); logits tokens x experts, ldl
+ *   (5, 6); score (7); balance, `experts` floats or NULL (8); groups, a divisor
+ *   of experts, at most 32 (9); group_top in [1, groups] with
+ *   top <= group_top * experts / groups (10); renormalize 0 or 1 (11); scale,
+ *   finite (12); mask, one byte per token, or NULL (13); weights and ids,
+ *   tokens x top, packed (14, 15).
+ */
+int sgemm_route(int dtype, int64_t tokens, int experts, int top, const void *logits, int64_t ldl, int score,
+                const float *balance, int groups, int group_top, int renormalize, float scale,
+                const uint8_t *mask, float *weights, int32_t *ids, void *stream);
+
+/*
+ * sgemm_route_backward -- dlogits for dweights.  The choice is constant (ids as
+ * sgemm_route gave them, entries outside [0, experts) have no gradient); balance
+ * and groups therefore do not enter.  Every element of dlogits is written.
+ *
+ *   dtype of logits and dlogits (1); tokens, experts, top (2-4); dweights
+ *   tokens x top (5); logits, ldl (6, 7); ids (8); score (9); renormalize (10);
+ *   scale (11); dlogits, lddl (12, 13).
+ */
+int sgemm_route_backward(int dtype, int64_t tokens, int experts, int top, const float *dweights,
+                         const void *logits, int64_t ldl, const int32_t *ids, int score, int renormalize,
+                         float scale, void *dlogits, int64_t lddl, void *stream);
+
+/*
+ * sgemm_expert_plan -- the experts' row lists of tokens x top pairs (token,
+ * choice), pair p = token*top + choice:
+ *
+ *   counts[e]   pairs whose id is e (experts entries)
+ *   offsets[e]  the first row of expert e; offsets[experts] = rows in use
+ *   rows[r]     the pair of row r: an expert's rows hold its pairs in increasing
+ *               order; -1 from offsets[experts] on
+ *   slots[p]    the row of pair p, -1 where its id is outside [0, experts)
+ *
+ *   tokens (1), top in [1, SGEMM_MAX_TOP] (2), experts (3), ids (4), counts (5),
+ *   offsets (6), rows (7), slots (8); tokens*top < 2^31 - 1024.
+ */
+int sgemm_expert_plan(int64_t tokens, int top, int experts, const int32_t *ids, int32_t *counts,
+                      int32_t *offsets, int32_t *rows, int32_t *slots, void *stream);
+
+/*
+ * sgemm_expert_linear -- y[r] = act(w[e] x[r'] + bias[e]) for every row r of expert
+ * e's list, where r' is the row's token (gather != 0: x is tokens x k) or r
+ * itself (x is tokens*top x k).  Rows of no expert come out zero.
+ *
+ *   dtype (1); tokens, top, experts (2-4); n, k (5, 6); gather (7); x, ldx (8, 9);
+ *   w, ldw, stride_w (10-12): expert e's n x k matrix at w + e*stride_w;
+ *   bias, experts x n packed, or NULL (13); act (14); offsets, rows of
+ *   sgemm_expert_plan (15, 16); y, tokens*top x n, ldy (17, 18); preact or NULL,
+ *   ldz (19, 20).
+ */
+int sgemm_expert_linear(int dtype, int64_t tokens, int top, int experts, int64_t n, int64_t k, int gather,
+                        const void *x, int64_t ldx, const void *w, int64_t ldw, int64_t stride_w,
+                        const void *bias, int act, const int32_t *offsets, const int32_t *rows, void *y,
+                        int64_t ldy, void *preact, int64_t ldz, void *stream);
+
+/*
+ * sgemm_expert_linear_backward -- the gradients of sgemm_expert_linear for dy
+ * (tokens*top x n; rows of no expert are not read).  With gather != 0, dx is
+ * tokens x k, the sum of the token's rows taken in FP32; otherwise tokens*top x k.
+ * An expert without rows gets zero gradients.
+ *
+ *   dtype, tokens, top, experts, n, k, gather (1-7); dy, lddy (8, 9); x, ldx
+ *   (10, 11); w, ldw, stride_w (12-14); act (15); preact, ldz (16, 17); offsets,
+ *   rows, slots (18-20); dx, lddx (21, 22); dw, lddw, stride_dw (23-25); dbias,
+ *   experts x n packed (26).  dx, dw, dbias may be NULL.
+ */
+int sgemm_expert_linear_backward(int dtype, int64_t tokens, int top, int experts, int64_t n, int64_t k,
+                                 int gather, const void *dy, int64_t lddy, const void *x, int64_t ldx,
+                                 const void *w, int64_t ldw, int64_t stride_w, int act, const void *preact,
+                                 int64_t ldz, const int32_t *offsets, const int32_t *rows,
+                                 const int32_t *slots, void *dx, int64_t lddx, void *dw, int64_t lddw,
+                                 int64_t stride_dw, void *dbias, void *stream);
+
+/*
+ * sgemm_expert_combine -- y[token] = residual[token] + sum over choices of
+ * weights[token, choice] * x[slots[token, choice]], the sum in FP32 in the order of
+ * the choices; slots of -1 add nothing.
+ *
+ *   dtype (1); tokens, top (2, 3); n (4); x, tokens*top x n, ldx (5, 6); slots (7);
+ *   weights, tokens x top, or NULL for ones (8); residual or NULL, ldr (9, 10);
+ *   y, tokens x n, ldy (11, 12).
+ */
+int sgemm_expert_combine(int dtype, int64_t tokens, int top, int64_t n, const void *x, int64_t ldx,
+                         const int32_t *slots, const float *weights, const void *residual, int64_t ldr,
+                         void *y, int64_t ldy, void *stream);
+
+/*
+ * sgemm_expert_combine_backward -- the gradients of sgemm_expert_combine for dy
+ * (the residual's is dy itself): dx[slots[p]] = weights[p] * dy[token] (rows of no
+ * pair come out zero) and dweights[p] = <dy[token], x[slots[p]]> (0 for a slot of -1).
+ *
+ *   dtype, tokens, top, n (1-4); dy, lddy (5, 6); x, ldx (7, 8): read for dweights;
+ *   rows, slots (9, 10); weights or NULL (11); dx, lddx (12, 13); dweights (14).
+ *   dx and dweights may be NULL.
+ */
+int sgemm_expert_combine_backward(int dtype, int64_t tokens, int top, int64_t n, const void *dy, int64_t lddy,
+                                  const void *x, int64_t ldx, const int32_t *rows, const int32_t *slots,
+                                  const float *weights, void *dx, int64_t lddx, float *dweights,
+                                  void *stream);
+
 /* Kernels this library has launched in this process (all devices). */
 uint64_t sgemm_launch_count(void);
 

@@ -51,7 +51,23 @@ PREPS = {0: "none", 1: "copy", 2: "transpose", 3: "split"}
 EXPORTS = ("sgemm", "sgemm_host", "sgemm_host_async", "sgemm_set_host_split", "sgemm_host_split_ratio",
            "sgemm_noalloc", "sgemm_set_workspace", "sgemm_plan", "sgemm_device_status",
            "sgemm_set_wait_timeout", "sgemm_force_plan", "sgemm_debug_flags", "sgemm_launch_count",
-           "sgemm_workspace_release", "sgemm_last_error_string", "sgemm_version")
+           "sgemm_workspace_release", "sgemm_last_error_string", "sgemm_version",
+           "sgemm_linear", "sgemm_linear_backward", "sgemm_route", "sgemm_route_backward", "sgemm_expert_plan",
+           "sgemm_expert_linear", "sgemm_expert_linear_backward", "sgemm_expert_combine",
+           "sgemm_expert_combine_backward")
+
+# Layers of language models (layers.py), loaded with torch on first use.
+_LAYERS = ("linear", "linear_backward", "route", "route_backward", "ExpertPlan", "expert_plan", "expert_linear",
+           "expert_linear_backward", "expert_combine", "expert_combine_backward")
+
+
+def __getattr__(name):
+    if name in _LAYERS:
+        from . import layers
+        globals().update({n: getattr(layers, n) for n in _LAYERS})
+        return globals()[name]
+    raise AttributeError("module %r has no attribute %r" % (__name__, name))
+
 
 
 class SgemmError(RuntimeError):
@@ -121,6 +137,20 @@ def load_library(path: str | None = None):
         lib.sgemm_last_error_string.restype = ctypes.c_char_p
         lib.sgemm_version.argtypes = []
         lib.sgemm_version.restype = ctypes.c_char_p
+        sizes, experts, mat = [i64, i64, i64], [i, i64, i, i, i64, i64, i], [vp, i64]
+        for name, args in (
+                ("sgemm_linear", [i, *sizes, *mat, *mat, vp, i, *mat, *mat, *mat, vp]),
+                ("sgemm_linear_backward", [i, *sizes, *mat, *mat, *mat, i, *mat, *mat, *mat, vp, vp]),
+                ("sgemm_route", [i, i64, i, i, *mat, i, vp, i, i, i, f, vp, vp, vp, vp]),
+                ("sgemm_route_backward", [i, i64, i, i, vp, *mat, vp, i, i, f, *mat, vp]),
+                ("sgemm_expert_plan", [i64, i, i, vp, vp, vp, vp, vp, vp]),
+                ("sgemm_expert_linear", [*experts, *mat, *mat, i64, vp, i, vp, vp, *mat, *mat, vp]),
+                ("sgemm_expert_linear_backward",
+                 [*experts, *mat, *mat, *mat, i64, i, *mat, vp, vp, vp, *mat, *mat, i64, vp, vp]),
+                ("sgemm_expert_combine", [i, i64, i, i64, *mat, vp, vp, *mat, *mat, vp]),
+                ("sgemm_expert_combine_backward", [i, i64, i, i64, *mat, *mat, vp, vp, vp, *mat, vp, vp])):
+            getattr(lib, name).argtypes = args
+            getattr(lib, name).restype = i
         if path is None:
             _lib = lib
         return lib

@@ -123,6 +123,20 @@ struct GemmParams {
     int* status;             // per-device status word
 };
 
+// What an entry point outside sgemm_api.cu needs of the library's state: the
+// device of the call, its workspace, the error text and the launch count.
+struct CallContext {
+    int dev, sms;
+    int* status;
+    uint64_t timeout_ns;
+    int debug_flags;
+};
+int call_begin(CallContext* c);  // 0 or an SGEMM_ERR_* code
+int call_workspace(const CallContext& c, cudaStream_t st, size_t bytes, void** out);
+int call_fail(int code, const char* fmt, ...);
+int call_fail_cuda(cudaError_t e, const char* what);
+void call_count(int launches);
+
 // Device status values written by kernels (match SGEMM_ERR_* of the ABI).
 constexpr int kStatusTimeout = 4;
 

@@ -1,0 +1,144 @@
+// Declarations shared by the layer calls' translation units: element types,
+// activations, and the launchers of the kernels behind sgemm_linear,
+// sgemm_route, sgemm_expert_* (not part of the ABI).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/precision_gemm.h"
+#include "internal.h"
+
+namespace pg {
+
+using bf16 = __nv_bfloat16;
+
+// ---- activations (FP32) --------------------------------------------------------
+
+__device__ __forceinline__ float act_value(float z, int act) {
+    switch (act) {
+        case SGEMM_ACT_RELU:
+            return z > 0.0f ? z : (z != z ? z : 0.0f);
+        case SGEMM_ACT_SILU:
+            return z / (1.0f + expf(-z));
+        case SGEMM_ACT_GELU:
+            return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+        case SGEMM_ACT_GELU_TANH: {
+            const float u = 0.79788456080286536f * (z + 0.044715f * z * z * z);
+            return 0.5f * z * (1.0f + tanhf(u));
+        }
+        default:
+            return z;
+    }
+}
+
+__device__ __forceinline__ float act_derivative(float z, int act) {
+    switch (act) {
+        case SGEMM_ACT_RELU:
+            return z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
+        case SGEMM_ACT_SILU: {
+            const float p = 1.0f / (1.0f + expf(-z));
+            return p * (1.0f + z * (1.0f - p));
+        }
+        case SGEMM_ACT_GELU:
+            return 0.5f * (1.0f + erff(z * 0.70710678118654752f)) + z * expf(-0.5f * z * z) * 0.39894228040143268f;
+        case SGEMM_ACT_GELU_TANH: {
+            const float u = 0.79788456080286536f * (z + 0.044715f * z * z * z);
+            const float t = tanhf(u);
+            return 0.5f * (1.0f + t) + 0.5f * z * (1.0f - t * t) * 0.79788456080286536f * (1.0f + 0.134145f * z * z);
+        }
+        default:
+            return 1.0f;
+    }
+}
+
+__device__ __forceinline__ float to_float(float v) { return v; }
+__device__ __forceinline__ float to_float(bf16 v) { return __bfloat162float(v); }
+template <typename T>
+__device__ __forceinline__ T from_float(float v);
+template <>
+__device__ __forceinline__ float from_float<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ bf16 from_float<bf16>(float v) { return __float2bfloat16_rn(v); }
+
+// Expert e's rows [first, end) of its list, clamped to the rows there are.
+__device__ __forceinline__ void expert_rows(const int32_t* offsets, int e, int rows, int& first, int& end) {
+    first = min(max(offsets[e], 0), rows);
+    end = min(max(offsets[e + 1], first), rows);
+}
+
+// ---- products ---------------------------------------------------------------------
+//
+// Every layer product has the form
+//
+//     out[j][i] = epilogue(sum over k of A(i, k) * B(j, k)),   i contiguous in out,
+//
+// per group g (an expert; one group for the dense calls):
+//   forward    i = feature n, j = row,        k = feature k   A = w,  B = x
+//   dx         i = feature k, j = row,        k = feature n   A = w^T, B = dz
+//   dw         i = feature k, j = feature n,  k = row         A = x^T, B = dz^T
+// In the first two the groups share out the rows j, in the third the rows k.
+struct Operand {
+    const void* ptr;
+    int64_t ld;        // row stride, elements
+    int64_t stride;    // between groups, elements (weights)
+    bool k_contiguous; // rows run along k (else along i / j)
+    const int32_t* list;  // rows gathered: row r is the matrix's row list[r] / top (null: r)
+    int top;
+    int64_t rows;      // stored rows of the matrix (per group for weights)
+};
+
+struct Product {
+    int dtype;
+    int64_t ni, nj, nk;      // extents (nj or nk: all rows of all groups)
+    int groups;
+    const int32_t* offsets;  // groups + 1 first rows on the device (null: one group)
+    bool rows_on_k;          // dw: the groups share out k
+    Operand a, b;
+    // epilogue: z = sum + bias; preact = z; out = act(z) + residual
+    const void* bias;        // ni per group
+    int act;
+    const void* residual;
+    int64_t ldr;
+    void* out;
+    int64_t ldo;
+    int64_t out_stride;      // between groups (rows_on_k)
+    void* preact;
+    int64_t ldz;
+    bool out_f32;            // out is FP32 whatever dtype (no residual, no preact)
+};
+
+// ---- launchers -----------------------------------------------------------------------
+
+cudaError_t launch_product_simple(const Product& p, cudaStream_t st);
+
+// dz = dy * act'(z) (dz may be null), and per group the column sums of dz before
+// rounding, into dbias (groups x n; may be null).  part: bias_part_bytes().
+size_t bias_part_bytes(int64_t rows, int64_t n, int groups);
+cudaError_t launch_dact(int dtype, int64_t rows, int64_t n, const void* dy, int64_t lddy, const void* z, int64_t ldz,
+                        int act, void* dz, int64_t lddz, int groups, const int32_t* offsets, void* dbias, float* part,
+                        cudaStream_t st);
+int dact_launches(bool with_bias);
+
+// x_f32: the rows are FP32 whatever dtype.
+cudaError_t launch_combine(int dtype, bool x_f32, int64_t tokens, int top, int64_t n, const void* x, int64_t ldx,
+                           const int32_t* slots, const float* weights, const void* residual, int64_t ldr, void* y,
+                           int64_t ldy, cudaStream_t st);
+cudaError_t launch_combine_backward(int dtype, int64_t tokens, int top, int64_t n, const void* dy, int64_t lddy,
+                                    const void* x, int64_t ldx, const int32_t* rows, const int32_t* slots,
+                                    const float* weights, void* dx, int64_t lddx, float* dweights, cudaStream_t st);
+
+cudaError_t launch_route(int dtype, int64_t tokens, int experts, int top, const void* logits, int64_t ldl, int score,
+                         const float* balance, int groups, int group_top, int renorm, float scale,
+                         const uint8_t* mask, float* weights, int32_t* ids, cudaStream_t st);
+cudaError_t launch_route_backward(int dtype, int64_t tokens, int experts, int top, const float* dweights,
+                                  const void* logits, int64_t ldl, const int32_t* ids, int score, int renorm,
+                                  float scale, void* dlogits, int64_t lddl, cudaStream_t st);
+size_t plan_part_bytes(int64_t pairs, int experts);
+int plan_launches(int64_t pairs);
+cudaError_t launch_expert_plan(int64_t pairs, int experts, const int32_t* ids, int32_t* counts, int32_t* offsets,
+                               int32_t* rows, int32_t* slots, int32_t* part, cudaStream_t st);
+
+}  // namespace pg

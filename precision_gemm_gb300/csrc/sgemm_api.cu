@@ -1303,6 +1303,36 @@ int host_call(char transa, char transb, int64_t m, int64_t n, int64_t k, float a
 }
 
 }  // namespace
+
+// ---- what the layer calls (layer_api.cu) share with sgemm -------------------------
+
+int call_begin(CallContext* c) {
+    DeviceState* ds;
+    const int rc = current_device(&c->dev, &ds);
+    if (rc) return rc;
+    c->sms = ds->sms;
+    c->status = ds->status;
+    c->timeout_ns = g_timeout_ns.load();
+    c->debug_flags = g_debug.load();
+    return 0;
+}
+
+int call_workspace(const CallContext& c, cudaStream_t st, size_t bytes, void** out) {
+    return get_buffer(c.dev, st, kPurposeWorkspace, bytes, out);
+}
+
+int call_fail(int code, const char* fmt, ...) {
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(t_err, sizeof t_err, fmt, ap);
+    va_end(ap);
+    return code;
+}
+
+int call_fail_cuda(cudaError_t e, const char* what) { return fail_cuda(e, what); }
+
+void call_count(int launches) { g_launches += launches; }
+
 }  // namespace pg
 
 PG_EXPORT int sgemm_set_host_split(double q) {

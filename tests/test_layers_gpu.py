@@ -1,0 +1,437 @@
+"""Linear layers and the experts' products against their definitions in 64 bits:
+sizes from zero and one to several tiles, odd extents, strided and unaligned rows,
+empty experts, pairs of no expert, every activation, both types and directions."""
+import math
+
+import pytest
+import torch
+
+import precision_gemm_gb300 as pg
+from tests import _layers_ref as R
+
+pytestmark = pytest.mark.gpu
+DTYPES = [torch.float32, torch.bfloat16]
+IDS = {torch.float32: "f32", torch.bfloat16: "bf16"}
+
+
+@pytest.fixture(autouse=True)
+def _healthy():
+    pg.load_library()
+    pg.device_status()
+    yield
+    assert pg.device_status() == 0
+
+
+def _gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def _draw(g, dtype, *shape, std=1.0):
+    return (torch.randn(*shape, generator=g) * std).to(dtype)
+
+
+def _strided(x, pad, offset=0):
+    """A CUDA copy of matrix x whose rows are pad elements apart more than they are
+    long, its first element `offset` elements into the storage; the gaps hold NaN."""
+    r, c = x.shape
+    buf = torch.full((offset + r * (c + pad),), math.nan, dtype=x.dtype, device="cuda")
+    view = buf[offset:].view(r, c + pad)[:, :c] if r else buf[offset:].view(0, c + pad)[:, :c]
+    view.copy_(x)
+    return view
+
+
+SIZES = [(1, 1, 1), (1, 130, 3), (2, 4096, 512), (3, 64, 64), (5, 1000, 777), (8, 96, 2048), (17, 257, 129),
+         (33, 640, 256), (64, 128, 64), (130, 300, 777), (257, 513, 1000), (300, 256, 65), (1500, 300, 777)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS.get)
+@pytest.mark.parametrize("t,n,k", SIZES)
+def test_linear(dtype, t, n, k):
+    g = _gen(t * 7 + n * 3 + k)
+    x, w = _draw(g, dtype, t, k), _draw(g, dtype, n, k, std=k ** -0.5)
+    b, r = _draw(g, dtype, n), _draw(g, dtype, t, n)
+    name = R.ACTS[(t + n + k) % 5]
+    y, z = pg.linear(x.cuda(), w.cuda(), b.cuda(), name, r.cuda(), preact=True)
+    want, wz, den = R.linear(x, w, b, name, r)
+    R.close(y, want, den, dtype)
+    R.close(z, wz, den, dtype)
+    y = pg.linear(x.cuda(), w.cuda())
+    want, _, den = R.linear(x, w, None, "none", None)
+    R.close(y, want, den, dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS.get)
+@pytest.mark.parametrize("name", R.ACTS)
+@pytest.mark.parametrize("t", [4, 200])
+def test_linear_activations_over_their_range(dtype, name, t):
+    # pre-activations from -12 to 12: both tails of every activation, and its zero
+    n, k = 192, 32
+    g = _gen(5)
+    x, w = _draw(g, dtype, t, k), _draw(g, dtype, n, k, std=k ** -0.5)
+    b = torch.linspace(-12, 12, n).to(dtype)
+    x[0] = 0
+    y = pg.linear(x.cuda(), w.cuda(), b.cuda(), name)
+    want, _, den = R.linear(x, w, b, name, None)
+    R.close(y, want, den, dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS.get)
+@pytest.mark.parametrize("t,n,k,pad,offset", [(6, 70, 100, 3, 1), (140, 200, 136, 5, 3), (140, 200, 136, 8, 8),
+                                              (300, 130, 64, 1, 0), (1, 64, 72, 7, 2)])
+def test_linear_strides_and_alignment(dtype, t, n, k, pad, offset):
+    g = _gen(t + pad)
+    x, w = _draw(g, dtype, t, k), _draw(g, dtype, n, k, std=k ** -0.5)
+    b, r = _draw(g, dtype, n), _draw(g, dtype, t, n)
+    out = _strided(torch.zeros(t, n, dtype=dtype), pad, offset)
+    got = pg.linear(_strided(x, pad, offset), _strided(w, pad, offset), b.cuda(), "silu", _strided(r, pad, offset),
+                    out=out)
+    assert got is out
+    want, _, den = R.linear(x, w, b, "silu", r)
+    R.close(out, want, den, dtype)
+    gaps = out.as_strided((t, pad), (n + pad, 1), offset + n)[:t - 1]
+    assert torch.isnan(gaps).all()  # nothing between the rows was written
+    # residual and result in one tensor
+    both = r.cuda()
+    pg.linear(x.cuda(), w.cuda(), b.cuda(), "gelu", both, out=both)
+    want, _, den = R.linear(x, w, b, "gelu", r)
+    R.close(both, want, den, dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS.get)
+def test_linear_empty_extents_and_leading_dimensions(dtype):
+    g = _gen(1)
+    b, r = _draw(g, dtype, 9), _draw(g, dtype, 4, 9)
+    y = pg.linear(torch.empty(4, 0, dtype=dtype, device="cuda"), torch.empty(9, 0, dtype=dtype, device="cuda"),
+                  b.cuda(), "silu", r.cuda())
+    want, _, den = R.linear(torch.zeros(4, 0), torch.zeros(9, 0), b, "silu", r)
+    R.close(y, want, den, dtype)
+    assert pg.linear(torch.empty(0, 5, dtype=dtype, device="cuda"),
+                     torch.empty(9, 5, dtype=dtype, device="cuda")).shape == (0, 9)
+    x, w = _draw(g, dtype, 2, 3, 40), _draw(g, dtype, 24, 40)
+    y, z = pg.linear(x.cuda(), w.cuda(), preact=True)
+    assert y.shape == z.shape == (2, 3, 24)
+    want, _, den = R.linear(x.view(6, 40), w, None, "none", None)
+    R.close(y.view(6, 24), want, den, dtype)
+    dx, dw, db = pg.linear_backward(torch.empty(0, 9, dtype=dtype, device="cuda"),
+                                    torch.empty(0, 5, dtype=dtype, device="cuda"),
+                                    torch.empty(9, 5, dtype=dtype, device="cuda"))
+    assert dx.shape == (0, 5) and not dw.any() and not db.any()
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS.get)
+@pytest.mark.parametrize("t", [3, 150])
+def test_linear_infinities_and_nan_stay_in_their_rows(dtype, t):
+    n, k = 140, 200
+    g = _gen(3)
+    x, w = _draw(g, dtype, t, k), _draw(g, dtype, n, k)
+    x[1, 7], x[2, 11] = math.inf, math.nan
+    y = pg.linear(x.cuda(), w.cuda()).cpu()
+    want = (x.double() @ w.double().t())
+    finite = torch.isfinite(want)
+    assert torch.equal(torch.isfinite(y), finite)
+    assert torch.equal(torch.isnan(y), torch.isnan(want))
+    assert torch.equal(y[1].double(), want[1])  # signed infinities
+    assert finite[0].all() and not finite[1].any() and torch.isnan(want[2]).all()
+
+
+@pytest.mark.parametrize("t", [4, 300])
+def test_linear_float32_is_not_tf32(t):
+    """The 2-norm of the error stays at FP32's: the longest run of additions whose results
+    are truncated is 32 (2^-24 of the sum each, all one way), doubled for the rest."""
+    n, k = 512, 4096
+    g = _gen(t)
+    x, w = _draw(g, torch.float32, t, k), _draw(g, torch.float32, n, k, std=k ** -0.5)
+    y = pg.linear(x.cuda(), w.cuda()).double().cpu()
+    want = x.double() @ w.double().t()
+    assert float((y - want).norm() / want.norm()) < 64 * 2.0 ** -24
+
+
+def _inner(dtype, name):
+    """The rounding of dz to bfloat16 before the products (exact when dz is dy)."""
+    return R.HALF if dtype == torch.bfloat16 and name != "none" else 0.0
+
+
+def _check_backward(got, want, den, dtype, name):
+    for i, (a, b, d) in enumerate(zip(got, want, den)):
+        # the bias gradient sums unrounded terms
+        R.close(a, b, d, dtype, slope=1.0, inner=_inner(dtype, name) if i < 2 else 0.0)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS.get)
+@pytest.mark.parametrize("t,n,k", [(1, 1, 1), (1, 70, 130), (5, 64, 64), (63, 65, 66), (130, 300, 77), (257, 130, 200),
+                                   (640, 256, 384), (1300, 100, 150)])
+def test_linear_backward(dtype, t, n, k):
+    g = _gen(t + n + k)
+    name = R.ACTS[(t + n + k) % 5]
+    x, w, dy = _draw(g, dtype, t, k), _draw(g, dtype, n, k, std=k ** -0.5), _draw(g, dtype, t, n)
+    z = _draw(g, dtype, t, n, std=2.0)
+    got = pg.linear_backward(dy.cuda(), x.cuda(), w.cuda(), name, z.cuda())
+    want, den = R.linear_backward(dy, x, w, name, z)
+    _check_backward(got, want, den, dtype, name)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS.get)
+@pytest.mark.parametrize("name", ["none", "gelu"])
+def test_linear_backward_strides_and_skipped_gradients(dtype, name):
+    t, n, k = 150, 170, 90
+    g = _gen(8)
+    x, w, dy = _draw(g, dtype, t, k), _draw(g, dtype, n, k, std=k ** -0.5), _draw(g, dtype, t, n)
+    z = _draw(g, dtype, t, n)
+    args = (_strided(dy, 3, 1), _strided(x, 5, 3), _strided(w, 1, 7), name, _strided(z, 9, 5))
+    want, den = R.linear_backward(dy, x, w, name, z)
+    _check_backward(pg.linear_backward(*args), want, den, dtype, name)
+    whole = pg.linear_backward(*args)
+    dx, dw, db = pg.linear_backward(*args, need_dw=False, bias=False)
+    assert dw is None and db is None and torch.equal(dx, whole[0])
+    dx, dw, db = pg.linear_backward(*args, need_dx=False)
+    assert dx is None and torch.equal(dw, whole[1]) and torch.equal(db, whole[2])
+
+
+@pytest.mark.parametrize("name", R.ACTS)
+def test_linear_backward_against_differences(name):
+    """Directional differences of the 64-bit layer around the point, step 1e-5: their own
+    error is of order 1e-10, the FP32 gradient's 1e-6 of the terms' sizes."""
+    t, n, k = 40, 50, 60
+    g = _gen(11)
+    x, w, b = (torch.randn(*s, generator=g) for s in ((t, k), (n, k), (n,)))
+    x = torch.where(x.abs() < 1e-2, torch.full_like(x, 0.1), x)
+    w = w * k ** -0.5
+    dy = torch.randn(t, n, generator=g)
+    y, z = pg.linear(x.cuda(), w.cuda(), b.cuda(), name, preact=True)
+    dx, dw, db = pg.linear_backward(dy.cuda(), x.cuda(), w.cuda(), name, z)
+
+    def loss(x, w, b):
+        return float((R.linear(x, w, b, name, None)[0] * dy.double()).sum())
+
+    h = 1e-5
+    for i, (v, grad) in enumerate(((x, dx), (w, dw), (b, db))):
+        u = torch.randn(v.shape, generator=g, dtype=torch.float64)
+        at = [x.double(), w.double(), b.double()]
+        up, down = list(at), list(at)
+        up[i], down[i] = at[i] + h * u, at[i] - h * u
+        diff = (loss(*up) - loss(*down)) / (2 * h)
+        scale = float((grad.double().cpu().abs() * u.abs()).sum())
+        assert abs(diff - float((grad.double().cpu() * u).sum())) <= 2e-5 * scale, (name, i)
+
+
+# ---- experts -----------------------------------------------------------------------
+
+
+def _ids(g, t, top, e, kind):
+    if kind == "even":
+        return torch.stack([torch.randperm(e, generator=g)[:top] for _ in range(t)]).to(torch.int32)
+    if kind == "one":  # every pair to one expert, the others empty
+        return torch.full((t, top), e // 2, dtype=torch.int32)
+    ids = torch.randint(0, max(1, e // 2), (t, top), generator=g, dtype=torch.int32)  # half of the experts empty
+    if kind == "dropped":
+        drop = torch.rand(t, top, generator=g) < 0.3
+        ids = torch.where(drop, torch.where(torch.rand(t, top, generator=g) < 0.5, -1, e + 3).to(torch.int32), ids)
+    return ids
+
+
+def _none(t, top):
+    return torch.full((t, top), -1, dtype=torch.int32)
+
+
+@pytest.mark.parametrize("t,top,e,kind", [(1, 1, 1, "even"), (1, 8, 64, "even"), (7, 2, 5, "dropped"),
+                                          (300, 4, 12, "even"), (513, 8, 60, "dropped"), (1000, 2, 512, "half"),
+                                          (2100, 1, 16, "one"), (4000, 8, 256, "even"), (9000, 3, 300, "dropped")])
+def test_expert_plan(t, top, e, kind):
+    ids = _ids(_gen(t + e), t, top, e, kind)
+    plan = pg.expert_plan(ids.cuda(), e)
+    counts, offsets, rows, slots = R.lists(ids, e)
+    assert plan.counts.tolist() == counts and plan.offsets.tolist() == offsets
+    assert plan.rows.tolist() == rows and plan.slots.tolist() == slots
+
+
+def test_expert_plan_without_tokens_or_experts_rows():
+    plan = pg.expert_plan(torch.empty(0, 2, dtype=torch.int32, device="cuda"), 6)
+    assert plan.counts.tolist() == [0] * 6 and plan.offsets.tolist() == [0] * 7
+    plan = pg.expert_plan(_none(5, 2).cuda(), 6)
+    assert plan.offsets.tolist() == [0] * 7 and plan.rows.tolist() == [-1] * 10
+    assert plan.slots.tolist() == [[-1, -1]] * 5
+
+
+def _row_expert(plan_lists, e):
+    counts, offsets, rows, _ = plan_lists
+    return [(i, offsets[i], offsets[i + 1]) for i in range(e)]
+
+
+CASES = [(1, 1, 1, 8, 8, "even"), (1, 4, 16, 100, 72, "even"), (3, 2, 6, 64, 130, "dropped"),
+         (40, 3, 7, 65, 66, "half"), (130, 2, 5, 136, 200, "dropped"), (400, 4, 9, 257, 120, "even"),
+         (300, 2, 4, 96, 520, "one"), (700, 6, 33, 70, 90, "half")]
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS.get)
+@pytest.mark.parametrize("gather", [True, False])
+@pytest.mark.parametrize("t,top,e,n,k,kind", CASES)
+def test_expert_linear(dtype, gather, t, top, e, n, k, kind):
+    g = _gen(t + n + k)
+    ids = _ids(g, t, top, e, kind)
+    plan = pg.expert_plan(ids.cuda(), e)
+    ls = R.lists(ids, e)
+    x = _draw(g, dtype, t if gather else t * top, k)
+    w, b = _draw(g, dtype, e, n, k, std=k ** -0.5), _draw(g, dtype, e, n)
+    name = R.ACTS[(t + n) % 5]
+    y, z = pg.expert_linear(x.cuda(), w.cuda(), plan, b.cuda(), name, gather=gather, preact=True)
+    for i, first, end in _row_expert(ls, e):
+        src = torch.tensor(ls[2][first:end], dtype=torch.long) // top if gather else torch.arange(first, end)
+        want, wz, den = R.linear(x[src], w[i], b[i], name, None)
+        R.close(y[first:end], want, den, dtype)
+        R.close(z[first:end], wz, den, dtype)
+    assert not y[ls[1][-1]:].any() and not z[ls[1][-1]:].any()
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS.get)
+@pytest.mark.parametrize("gather", [True, False])
+@pytest.mark.parametrize("t,top,e,n,k,kind", CASES)
+def test_expert_linear_backward(dtype, gather, t, top, e, n, k, kind):
+    g = _gen(t + n + k + 1)
+    ids = _ids(g, t, top, e, kind)
+    plan = pg.expert_plan(ids.cuda(), e)
+    ls = R.lists(ids, e)
+    rows = t * top
+    x = _draw(g, dtype, t if gather else rows, k)
+    w = _draw(g, dtype, e, n, k, std=k ** -0.5)
+    dy, z = _draw(g, dtype, rows, n), _draw(g, dtype, rows, n)
+    dy[ls[1][-1]:] = math.nan  # rows of no expert are not read
+    name = R.ACTS[(t + n + 2) % 5]
+    dx, dw, db = pg.expert_linear_backward(dy.cuda(), x.cuda(), w.cuda(), plan, name, z.cuda(), gather=gather)
+    wx = torch.zeros(x.shape, dtype=torch.float64)
+    dxden = torch.zeros_like(wx)
+    wdw = torch.zeros(w.shape, dtype=torch.float64)
+    dwden = torch.zeros_like(wdw)
+    wdb, dbden = torch.zeros(e, n, dtype=torch.float64), torch.zeros(e, n, dtype=torch.float64)
+    for i, first, end in _row_expert(ls, e):
+        src = torch.tensor(ls[2][first:end], dtype=torch.long) // top if gather else torch.arange(first, end)
+        (a, wdw[i], wdb[i]), (d, dwden[i], dbden[i]) = R.linear_backward(dy[first:end], x[src], w[i], name,
+                                                                          z[first:end])
+        wx.index_add_(0, src, a)
+        dxden.index_add_(0, src, d)
+    _check_backward((dx, dw, db), (wx, wdw, wdb), (dxden, dwden, dbden), dtype, name)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS.get)
+def test_expert_gradients_do_not_mix_experts(dtype):
+    """A NaN or infinity in one expert's rows reaches only that expert's gradients, at
+    list lengths that end inside every kind of block."""
+    t, e, n, k = 260, 6, 72, 136
+    g = _gen(2)
+    lengths = [1, 63, 0, 65, 130, 1]
+    ids = torch.cat([torch.full((c,), i, dtype=torch.int32) for i, c in enumerate(lengths)]).view(t, 1)
+    plan = pg.expert_plan(ids.cuda(), e)
+    x, w = _draw(g, dtype, t, k), _draw(g, dtype, e, n, k)
+    dy = _draw(g, dtype, t, n)
+    dy[70] = math.nan   # expert 3
+    x[255] = math.inf   # expert 4
+    dx, dw, db = pg.expert_linear_backward(dy.cuda(), x.cuda(), w.cuda(), plan)
+    assert [bool(torch.isfinite(dw[i]).all()) for i in range(e)] == [True, True, True, False, False, True]
+    assert [bool(torch.isfinite(db[i]).all()) for i in range(e)] == [True, True, True, False, True, True]
+    assert torch.isfinite(dx).all(1).tolist() == [i != 70 for i in range(t)]
+    assert not dw[2].any() and not db[2].any()
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS.get)
+def test_expert_weight_strides(dtype):
+    t, top, e, n, k = 50, 2, 3, 40, 56
+    g = _gen(6)
+    ids = _ids(g, t, top, e, "even")
+    plan = pg.expert_plan(ids.cuda(), e)
+    x, w = _draw(g, dtype, t, k), _draw(g, dtype, e, n, k)
+    for pad, rows in ((3, 2), (8, 8)):
+        wide = torch.full((e, n + rows, k + pad), math.nan, dtype=dtype, device="cuda")
+        wide[:, :n, :k] = w.cuda()
+        y = pg.expert_linear(x.cuda(), wide[:, :n, :k], plan, gather=True)
+        assert torch.equal(y, pg.expert_linear(x.cuda(), w.cuda(), plan, gather=True))
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS.get)
+@pytest.mark.parametrize("t,top,e,n,kind", [(1, 1, 2, 1, "even"), (5, 3, 8, 70, "dropped"), (200, 8, 16, 1000, "even"),
+                                            (33, 2, 4, 2050, "dropped")])
+def test_expert_combine(dtype, t, top, e, n, kind):
+    g = _gen(t + n)
+    ids = _ids(g, t, top, e, kind)
+    plan = pg.expert_plan(ids.cuda(), e)
+    slots = torch.tensor(R.lists(ids, e)[3]).view(t, top)
+    rows, res = _draw(g, dtype, t * top, n), _draw(g, dtype, t, n)
+    weights = torch.rand(t, top, generator=g)
+    held = (slots >= 0).double()[:, :, None]
+    picked = rows.double()[slots.clamp_min(0)] * held
+    for wt, r in ((weights, res), (None, None)):
+        y = pg.expert_combine(rows.cuda(), plan, None if wt is None else wt.cuda(), None if r is None else r.cuda())
+        terms = picked * (1.0 if wt is None else wt.double()[:, :, None])
+        want, den = terms.sum(1), terms.abs().sum(1)
+        if r is not None:
+            want, den = want + r.double(), den + r.double().abs()
+        R.close(y, want, den, dtype, slope=1.0)
+    # backward: a pair's row gets its weight times its token's gradient
+    dy = _draw(g, dtype, t, n)
+    drows, dweights = pg.expert_combine_backward(dy.cuda(), rows.cuda(), plan, weights.cuda())
+    wrows = torch.zeros(t * top, n, dtype=torch.float64)
+    wrows[slots[slots >= 0]] = (weights.double()[:, :, None] * dy.double()[:, None, :])[slots >= 0]
+    R.close(drows, wrows, wrows.abs(), dtype, slope=1.0)
+    wdw, dden = (picked * dy.double()[:, None, :]).sum(2), (picked * dy.double()[:, None, :]).abs().sum(2)
+    R.close(dweights, wdw, dden, torch.float32, slope=1.0)
+
+
+# ---- streams, graphs, determinism -----------------------------------------------------
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS.get)
+def test_layers_repeat_bitwise_on_streams_and_in_graphs(dtype):
+    t, top, e, n, k = 200, 2, 8, 264, 328
+    g = _gen(4)
+    x, w = _draw(g, dtype, t, k).cuda(), _draw(g, dtype, e, n, k).cuda()
+    ids = _ids(g, t, top, e, "even").cuda()
+    logits = _draw(g, dtype, t, e).cuda()
+
+    def work():
+        weights, chosen = pg.route(logits, top)
+        plan = pg.expert_plan(ids, e)
+        h, z = pg.expert_linear(x, w, plan, act="silu", gather=True, preact=True)
+        y = pg.expert_combine(h, plan, weights)
+        dx, dw, db = pg.expert_linear_backward(h, x, w, plan, "silu", z, gather=True)
+        ly, lz = pg.linear(x, w[0], act="gelu", preact=True)
+        return [weights, chosen, h, y, dx, dw, db, ly, *pg.linear_backward(ly, x, w[0], "gelu", lz)]
+
+    first = work()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        again = work()
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(first, again))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        held = work()
+    for v in held:
+        v.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(first, held))
+
+
+def test_result_on_the_stream_that_is_given():
+    x, w = torch.randn(300, 256, device="cuda"), torch.randn(200, 256, device="cuda")
+    want = pg.linear(x, w)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for _ in range(3):
+        y = pg.linear(x, w, stream=s)
+        s.synchronize()
+        assert torch.equal(y, want)
+
+
+def test_large_offsets():
+    """Row offsets beyond 2^31 elements: the last rows of a tall matrix."""
+    t, k, n = 2 ** 20 + 3, 2100, 40
+    x = torch.empty(t, k, dtype=torch.bfloat16, device="cuda")
+    x.fill_(0)
+    tail = _draw(_gen(1), torch.bfloat16, 5, k)
+    x[-5:] = tail.cuda()
+    w = _draw(_gen(2), torch.bfloat16, n, k, std=k ** -0.5)
+    y = pg.linear(x, w.cuda())
+    want, _, den = R.linear(tail, w, None, "none", None)
+    R.close(y[-5:], want, den, torch.bfloat16)
+    assert not y[:-5].any()

@@ -130,12 +130,18 @@ struct CallContext {
     int* status;
     uint64_t timeout_ns;
     int debug_flags;
+    int force_bn, force_split;
 };
 int call_begin(CallContext* c);  // 0 or an SGEMM_ERR_* code
 int call_workspace(const CallContext& c, cudaStream_t st, size_t bytes, void** out);
 int call_fail(int code, const char* fmt, ...);
 int call_fail_cuda(cudaError_t e, const char* what);
 void call_count(int launches);
+// A bfloat16 matrix of `rows` rows of `cols` elements, ld apart, `z` of them stride
+// apart (z = 0: a 2-D map), boxes of box_rows x box_cols in the 128-byte swizzle;
+// elements outside read as zero.
+int call_encode_bf16(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, int64_t ld, int64_t z,
+                     int64_t stride, uint32_t box_cols, uint32_t box_rows);
 
 // Device status values written by kernels (match SGEMM_ERR_* of the ABI).
 constexpr int kStatusTimeout = 4;

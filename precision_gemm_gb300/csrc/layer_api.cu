@@ -15,7 +15,6 @@ namespace {
 constexpr int64_t kMaxExtent = (int64_t(1) << 31) - 1024;  // TMA coordinates (tile + box) are 32-bit
 constexpr int64_t kMaxLd = int64_t(1) << 36;               // TMA strides are < 2^40 bytes
 
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 size_t region(size_t bytes) { return (bytes + 255) / 256 * 256; }
 
 // Checks that name their argument by position and name (0 when it is fine).
@@ -65,14 +64,73 @@ int check_pairs(int64_t tokens, int top, int pos) {
     return 0;
 }
 
-int size_of(int dtype) { return dtype == SGEMM_F32 ? 4 : 2; }
+// The workspace of a call: its launch sequence runs twice, first with base == null to
+// add up what it needs (nothing is launched), then on the memory.
+struct Arena {
+    char* base = nullptr;
+    size_t used = 0;
+    void* take(size_t bytes) {
+        void* at = base + used;
+        used += region(bytes);
+        return base ? at : nullptr;
+    }
+    bool dry() const { return base == nullptr; }
+};
 
-int product(const CallContext& c, const Product& p, cudaStream_t st) {
-    (void)c;
+template <typename F>
+int with_workspace(const CallContext& c, cudaStream_t st, F body) {
+    Arena sizes;
+    PG_CHECK(body(sizes));
+    Arena memory;
+    void* ws = nullptr;
+    PG_CHECK(call_workspace(c, st, std::max<size_t>(sizes.used, 1), &ws));
+    memory.base = static_cast<char*>(ws);
+    return body(memory);
+}
+
+// o as the tensor-core kernel reads it: bfloat16 rows at 16-byte aligned addresses are
+// read in place; others, and float32, are packed into bfloat16 parts.
+int prepare(const CallContext& c, int dtype, Operand& o, int groups, int64_t cols, int64_t listed, Arena& a,
+            bool after_previous, cudaStream_t st, int* launches) {
+    if (o.parts) return 0;
+    const bool in_place = dtype == SGEMM_BF16 && (reinterpret_cast<uintptr_t>(o.ptr) & 15) == 0 && o.ld % 8 == 0 &&
+                          (groups == 1 || o.stride % 8 == 0);
+    o.parts = dtype == SGEMM_F32 ? 3 : 1;
+    if (in_place) return 0;
+    const int64_t per = o.list ? listed : o.rows, ldd = (cols + 7) / 8 * 8;
+    if (o.parts * per * groups > kMaxExtent)
+        return call_fail(SGEMM_ERR_TENSOR_MAP, "a float32 operand of %lld rows has more than (2^31-1024)/3",
+                         (long long)(per * groups));
+    bf16* dst = static_cast<bf16*>(a.take(static_cast<size_t>(o.parts) * per * groups * ldd * 2));
+    if (!a.dry()) {
+        const cudaError_t e = launch_pack(dtype, o.ptr, o.ld, o.stride, groups, per, cols, o.list, o.top, o.rows, dst,
+                                          ldd, c.sms, after_previous, st);
+        if (e != cudaSuccess) return call_fail_cuda(e, "operand packing");
+        ++*launches;
+    }
+    o.ptr = dst;
+    o.ld = ldd;
+    o.rows = per;
+    o.stride = per * ldd;
+    o.list = nullptr;
+    return 0;
+}
+
+int product(const CallContext& c, Product p, Arena& a, cudaStream_t st) {
     if (p.ni == 0 || p.nj == 0) return 0;
-    const cudaError_t e = launch_product_simple(p, st);
-    if (e != cudaSuccess) return call_fail_cuda(e, "layer product");
-    call_count(p.offsets && !p.rows_on_k ? 2 : 1);
+    int launches = 0;
+    if (p.nk > 0) {
+        const int64_t cols_a = p.a.k_contiguous ? p.nk : p.ni, cols_b = p.b.k_contiguous ? p.nk : p.nj;
+        const int64_t rows_in_lists = p.rows_on_k ? p.nk : p.nj;
+        PG_CHECK(prepare(c, p.dtype, p.a, p.rows_on_k ? 1 : p.groups, cols_a, rows_in_lists, a, false, st, &launches));
+        PG_CHECK(prepare(c, p.dtype, p.b, 1, cols_b, rows_in_lists, a, launches > 0, st, &launches));
+    }
+    const TcPlan t = plan_tc(p, c.sms, c.force_bn, c.force_split);
+    void* ws = a.take(t.part_bytes + t.count_bytes);
+    if (!a.dry()) {
+        PG_CHECK(launch_product_tc(c, p, t, p.dtype == SGEMM_F32 ? 3 : 1, ws, launches > 0, st, &launches));
+        call_count(launches);
+    }
     return 0;
 }
 
@@ -102,41 +160,36 @@ struct Backward {
     int64_t lddx, lddw, stride_dw;
 };
 
-int backward(const Backward& b, cudaStream_t st) {
-    CallContext c;
-    PG_CHECK(call_begin(&c));
-    const bool products = b.dx || b.dw;
-    const bool own_dz = b.act != SGEMM_ACT_NONE && products && b.rows > 0;
-    const bool sum_rows = b.gather && b.dx;
-    // workspace: dz, the bias sums' parts, the rows of dx before their sum per token
-    const int64_t lddz = (b.n + 7) / 8 * 8;
-    const size_t dz_bytes = own_dz ? region(b.rows * lddz * size_of(b.dtype)) : 0;
-    const size_t part_bytes = b.dbias ? region(bias_part_bytes(b.rows, b.n, b.experts)) : 0;
-    const int64_t ldrow = (b.k + 3) / 4 * 4;
-    const size_t row_bytes = sum_rows ? region(b.rows * ldrow * 4) : 0;
-    void* ws = nullptr;
-    PG_CHECK(call_workspace(c, st, dz_bytes + part_bytes + row_bytes, &ws));
-    char* at = static_cast<char*>(ws);
-    void* dz_own = own_dz ? at : nullptr;
-    at += dz_bytes;
-    float* part = reinterpret_cast<float*>(at);
-    at += part_bytes;
-    float* dx_rows = reinterpret_cast<float*>(at);
-
+int backward_steps(const CallContext& c, const Backward& b, Arena& a, cudaStream_t st) {
     cudaError_t e;
-    const void* dz = b.dy;
-    int64_t ld = b.lddy;
+    const bool products = (b.dx || b.dw) && b.rows > 0 && b.n > 0;
+    Operand dz = rows_of(b.dy, b.lddy, b.rows, true);
+    // dz = dy is read in place where the tensor cores can
+    const bool own_dz = products && (b.act != SGEMM_ACT_NONE || b.dtype == SGEMM_F32 || b.lddy % 8 != 0 ||
+                                     (reinterpret_cast<uintptr_t>(b.dy) & 15) != 0);
+    bf16* dz_own = nullptr;
+    if (own_dz) {
+        dz.parts = b.dtype == SGEMM_F32 ? 3 : 1;
+        dz.ld = (b.n + 7) / 8 * 8;
+        dz.stride = b.rows * dz.ld;
+        if (dz.parts * b.rows > kMaxExtent)
+            return call_fail(SGEMM_ERR_TENSOR_MAP, "a float32 operand of %lld rows has more than (2^31-1024)/3",
+                             (long long)b.rows);
+        dz.ptr = dz_own = static_cast<bf16*>(a.take(static_cast<size_t>(dz.parts) * dz.stride * 2));
+    }
     if (own_dz || (b.dbias && b.n > 0)) {
-        if ((e = launch_dact(b.dtype, b.rows, b.n, b.dy, b.lddy, b.z, b.ldz, b.act, dz_own, lddz, b.experts, b.offsets,
-                             b.n > 0 ? b.dbias : nullptr, part, st)) != cudaSuccess)
-            return call_fail_cuda(e, "activation backward");
-        call_count(dact_launches(b.dbias != nullptr));
-        if (own_dz) {
-            dz = dz_own;
-            ld = lddz;
+        float* part = b.dbias ? static_cast<float*>(a.take(bias_part_bytes(b.rows, b.n, b.experts))) : nullptr;
+        if (!a.dry()) {
+            if ((e = launch_dact(b.dtype, b.rows, b.n, b.dy, b.lddy, b.z, b.ldz, b.act, dz_own, dz.ld, b.experts,
+                                 b.offsets, b.dbias, part, st)) != cudaSuccess)
+                return call_fail_cuda(e, "activation backward");
+            call_count(dact_launches(b.dbias != nullptr));
         }
     }
     if (b.dx) {
+        const bool sum_rows = b.gather;
+        const int64_t ldrow = (b.k + 3) / 4 * 4;
+        float* dx_rows = sum_rows ? static_cast<float*>(a.take(static_cast<size_t>(b.rows) * ldrow * 4)) : nullptr;
         Product p{};
         p.dtype = b.dtype;
         p.ni = b.k;
@@ -146,12 +199,12 @@ int backward(const Backward& b, cudaStream_t st) {
         p.offsets = b.offsets;
         p.a = rows_of(b.w, b.ldw, b.n, false);
         p.a.stride = b.stride_w;
-        p.b = rows_of(dz, ld, b.rows, true);
+        p.b = dz;
         p.out = sum_rows ? static_cast<void*>(dx_rows) : b.dx;
         p.ldo = sum_rows ? ldrow : b.lddx;
         p.out_f32 = sum_rows;
-        PG_CHECK(product(c, p, st));
-        if (sum_rows && b.tokens > 0 && b.k > 0) {
+        PG_CHECK(product(c, p, a, st));
+        if (sum_rows && b.tokens > 0 && b.k > 0 && !a.dry()) {
             if ((e = launch_combine(b.dtype, true, b.tokens, b.top, b.k, dx_rows, ldrow, b.slots, nullptr, nullptr, 0,
                                     b.dx, b.lddx, st)) != cudaSuccess)
                 return call_fail_cuda(e, "sum of the rows' gradients");
@@ -172,13 +225,20 @@ int backward(const Backward& b, cudaStream_t st) {
             p.a.list = b.list;
             p.a.top = b.top;
         }
-        p.b = rows_of(dz, ld, b.rows, false);
+        p.b = dz;
+        p.b.k_contiguous = false;
         p.out = b.dw;
         p.ldo = b.lddw;
         p.out_stride = b.stride_dw;
-        PG_CHECK(product(c, p, st));
+        PG_CHECK(product(c, p, a, st));
     }
     return 0;
+}
+
+int backward(const Backward& b, cudaStream_t st) {
+    CallContext c;
+    PG_CHECK(call_begin(&c));
+    return with_workspace(c, st, [&](Arena& a) { return backward_steps(c, b, a, st); });
 }
 
 }  // namespace
@@ -219,7 +279,8 @@ PG_EXPORT int sgemm_linear(int dtype, int64_t t, int64_t n, int64_t k, const voi
     p.ldo = ldy;
     p.preact = preact;
     p.ldz = ldz;
-    return product(c, p, static_cast<cudaStream_t>(stream));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return with_workspace(c, st, [&](Arena& a) { return product(c, p, a, st); });
 }
 
 PG_EXPORT int sgemm_linear_backward(int dtype, int64_t t, int64_t n, int64_t k, const void* dy, int64_t lddy,
@@ -393,7 +454,8 @@ PG_EXPORT int sgemm_expert_linear(int dtype, int64_t tokens, int top, int expert
     p.ldo = ldy;
     p.preact = preact;
     p.ldz = ldz;
-    return product(c, p, static_cast<cudaStream_t>(stream));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return with_workspace(c, st, [&](Arena& a) { return product(c, p, a, st); });
 }
 
 PG_EXPORT int sgemm_expert_linear_backward(int dtype, int64_t tokens, int top, int experts, int64_t n, int64_t k,

@@ -11,9 +11,9 @@ constexpr int kSlab = 64;  // rows per block of the activation's backward pass
 // sums per group: a slab's rows may belong to several groups, whose sums go to
 // the slots slab + g of part ((slabs + groups) x n) -- slab + g grows with every
 // new slab and with every new group, so no two sums share a slot.
-template <typename T>
+template <typename T, int PARTS>
 __global__ void __launch_bounds__(256) dact_kernel(int64_t rows, int64_t n, const T* dy, int64_t lddy, const T* z,
-                                                   int64_t ldz, int act, T* dz, int64_t lddz, int groups,
+                                                   int64_t ldz, int act, bf16* dz, int64_t lddz, int groups,
                                                    const int32_t* offsets, float* part) {
     const int64_t c = static_cast<int64_t>(blockIdx.y) * 256 + threadIdx.x;
     if (c >= n) return;
@@ -37,7 +37,12 @@ __global__ void __launch_bounds__(256) dact_kernel(int64_t rows, int64_t n, cons
         if (g == groups) break;
         float d = to_float(dy[r * lddy + c]);
         if (act != SGEMM_ACT_NONE) d *= act_derivative(to_float(z[r * ldz + c]), act);
-        if (dz) dz[r * lddz + c] = from_float<T>(d);
+        if (dz) {
+            bf16 q[PARTS];
+            split_bf16<PARTS>(d, q);
+#pragma unroll
+            for (int k = 0; k < PARTS; ++k) dz[(k * rows + r) * lddz + c] = q[k];
+        }
         sum += d;
         any = true;
     }
@@ -112,26 +117,27 @@ size_t bias_part_bytes(int64_t rows, int64_t n, int groups) {
 
 int dact_launches(bool with_bias) { return with_bias ? 2 : 1; }
 
-template <typename T>
+template <typename T, int PARTS>
 static cudaError_t run_dact(int64_t rows, int64_t n, const void* dy, int64_t lddy, const void* z, int64_t ldz, int act,
-                            void* dz, int64_t lddz, int groups, const int32_t* offsets, void* dbias, float* part,
+                            bf16* dz, int64_t lddz, int groups, const int32_t* offsets, void* dbias, float* part,
                             cudaStream_t st) {
     const unsigned cols = static_cast<unsigned>((n + 255) / 256);
     const dim3 grid(static_cast<unsigned>((rows + kSlab - 1) / kSlab), cols);
     if (rows > 0)
-        dact_kernel<T><<<grid, 256, 0, st>>>(rows, n, static_cast<const T*>(dy), lddy, static_cast<const T*>(z), ldz,
-                                             act, static_cast<T*>(dz), lddz, groups, offsets, dbias ? part : nullptr);
+        dact_kernel<T, PARTS><<<grid, 256, 0, st>>>(rows, n, static_cast<const T*>(dy), lddy,
+                                                    static_cast<const T*>(z), ldz, act, dz, lddz, groups, offsets,
+                                                    dbias ? part : nullptr);
     if (dbias)
         dbias_kernel<T><<<dim3(cols, groups), 256, 0, st>>>(rows, n, offsets, part, static_cast<T*>(dbias));
     return cudaGetLastError();
 }
 
 cudaError_t launch_dact(int dtype, int64_t rows, int64_t n, const void* dy, int64_t lddy, const void* z, int64_t ldz,
-                        int act, void* dz, int64_t lddz, int groups, const int32_t* offsets, void* dbias, float* part,
+                        int act, bf16* dz, int64_t lddz, int groups, const int32_t* offsets, void* dbias, float* part,
                         cudaStream_t st) {
     return dtype == SGEMM_F32
-               ? run_dact<float>(rows, n, dy, lddy, z, ldz, act, dz, lddz, groups, offsets, dbias, part, st)
-               : run_dact<bf16>(rows, n, dy, lddy, z, ldz, act, dz, lddz, groups, offsets, dbias, part, st);
+               ? run_dact<float, 3>(rows, n, dy, lddy, z, ldz, act, dz, lddz, groups, offsets, dbias, part, st)
+               : run_dact<bf16, 1>(rows, n, dy, lddy, z, ldz, act, dz, lddz, groups, offsets, dbias, part, st);
 }
 
 template <typename T, typename TX>

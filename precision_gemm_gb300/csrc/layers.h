@@ -63,6 +63,35 @@ __device__ __forceinline__ float from_float<float>(float v) { return v; }
 template <>
 __device__ __forceinline__ bf16 from_float<bf16>(float v) { return __float2bfloat16_rn(v); }
 
+// x as PARTS bfloat16 values whose sum it is (pack_kernel explains the parts).
+template <int PARTS>
+__device__ __forceinline__ void split_bf16(float x, bf16 (&part)[PARTS]) {
+    part[0] = __float2bfloat16_rn(x);
+    if (PARTS == 3) {
+        if (!isfinite(x)) {
+            part[0] = __float2bfloat16_rn(isnan(x) ? 0.0f : copysignf(1.0f, x));
+            part[1] = __float2bfloat16_rn(0.0f);
+            part[2] = __float2bfloat16_rn(x);
+            return;
+        }
+        float x0 = __bfloat162float(part[0]);
+        if (isinf(x0)) {  // the rounding of a finite value overflowed: truncate
+            x0 = __uint_as_float(__float_as_uint(x) & 0xFFFF0000u);
+            part[0] = __float2bfloat16_rn(x0);
+        }
+        const float r1 = x - x0;
+        part[1] = __float2bfloat16_rn(r1);
+        part[2] = __float2bfloat16_rn(r1 - __bfloat162float(part[1]));
+    }
+}
+
+// The matrix row that gathered row r stands for (list[r] / top), -1 for none.
+__device__ __forceinline__ int64_t gathered_row(const int32_t* list, int top, int64_t r, int64_t rows) {
+    const int32_t pair = list[r];
+    const int32_t row = pair / top;
+    return pair >= 0 && row < rows ? row : -1;
+}
+
 // Expert e's rows [first, end) of its list, clamped to the rows there are.
 __device__ __forceinline__ void expert_rows(const int32_t* offsets, int e, int rows, int& first, int& end) {
     first = min(max(offsets[e], 0), rows);
@@ -88,6 +117,8 @@ struct Operand {
     const int32_t* list;  // rows gathered: row r is the matrix's row list[r] / top (null: r)
     int top;
     int64_t rows;      // stored rows of the matrix (per group for weights)
+    int parts;         // 0: elements of the call's dtype; 1 or 3: bfloat16 parts of it, one after
+                       // another, `stride` apart, as the tensor-core kernel reads them
 };
 
 struct Product {
@@ -112,13 +143,31 @@ struct Product {
 
 // ---- launchers -----------------------------------------------------------------------
 
-cudaError_t launch_product_simple(const Product& p, cudaStream_t st);
+// Rows (list[r] / top of src_rows, or `groups` matrices of per_group rows, `stride`
+// apart) as packed bfloat16 parts of leading dimension ldd (a multiple of 8), part
+// after part: one for bfloat16, three for float32.
+cudaError_t launch_pack(int dtype, const void* src, int64_t ld, int64_t stride, int64_t groups, int64_t per_group,
+                        int64_t cols, const int32_t* list, int top, int64_t src_rows, bf16* dst, int64_t ldd,
+                        int num_sms, bool after_previous, cudaStream_t st);
 
-// dz = dy * act'(z) (dz may be null), and per group the column sums of dz before
-// rounding, into dbias (groups x n; may be null).  part: bias_part_bytes().
+// Tensor-core products: tile width, tiles (an upper bound for grouped rows), K slices,
+// and the workspace of the slices' blocks and counters.
+struct TcPlan {
+    int bn;
+    int64_t tiles;
+    int split, split_kb;
+    size_t part_bytes, count_bytes;
+};
+TcPlan plan_tc(const Product& p, int num_sms, int force_bn, int force_split);
+int launch_product_tc(const CallContext& c, const Product& p, const TcPlan& t, int parts, void* ws,
+                      bool after_previous, cudaStream_t st, int* launches);
+
+// dz = dy * act'(z) as bfloat16 parts (one for bfloat16, three for float32, rows * lddz
+// apart; may be null), and per group the column sums of dz before rounding, into dbias
+// (groups x n; may be null).  part: bias_part_bytes().
 size_t bias_part_bytes(int64_t rows, int64_t n, int groups);
 cudaError_t launch_dact(int dtype, int64_t rows, int64_t n, const void* dy, int64_t lddy, const void* z, int64_t ldz,
-                        int act, void* dz, int64_t lddz, int groups, const int32_t* offsets, void* dbias, float* part,
+                        int act, bf16* dz, int64_t lddz, int groups, const int32_t* offsets, void* dbias, float* part,
                         cudaStream_t st);
 int dact_launches(bool with_bias);
 

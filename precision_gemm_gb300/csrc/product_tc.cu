@@ -1,0 +1,783 @@
+// The layer products (layers.h, struct Product) on the tensor cores: tcgen05 on SM
+// pairs (cta_group::2, kind::f16), bfloat16 operands, FP32 accumulators in TMEM.
+//
+//     out[j][i] = epilogue(sum over k of A(i, k) B(j, k))
+//
+// A cluster of two CTAs computes a tile of 256 i x BN j: the feature direction i,
+// which is contiguous in out, lies along TMEM lanes, so a warp's 32 lanes store 32
+// neighbouring results and a narrow BN serves few rows (a decoding step, an
+// expert's short list) without wasted weight traffic.  CTA r of the pair stages i
+// rows [128 r, 128 r + 128) of A and j rows [r BN/2, ...) of B per 64-deep k block;
+// one thread of CTA 0 issues the MMAs of both.
+//
+// Operands lie in shared memory in 128-byte swizzled rows of 64 values, either way
+// round: K-major (rows along k) or MN-major (rows along i or j, one per k), so that
+// y = x w^T, dx = dz w and dw = dz^T x all read their matrices as they are stored.
+// Rows of B (forward) or of A (dw) can be gathered through a list by the TMA unit
+// (tile::gather4), so that an expert's tokens are never copied together first.
+//
+// float32 operands come as three bfloat16 parts x = x0 + x1 + x2 (pack_kernel), whose
+// six products of weight 2^-16 and above, the smallest first, are summed over a chunk
+// of k in one accumulator.  The tensor core truncates its FP32 sums (an error of up to
+// 2^-23 of the running sum per addition, all one way), so a chunk is kept to 512 k and
+// the chunks are added in registers, rounded to nearest, by the epilogue warps.
+//
+// Warp roles as in tc2_kernel.cu: warp 0 loads, warp 1 issues MMAs, warps 2-9 drain
+// TMEM (double-buffered: a unit's epilogue overlaps the next unit's MMAs).  The kernel
+// is persistent; a unit is (tile, K slice).  With few tiles each tile's k is cut into
+// slices; every slice stores its block, and per epilogue warp the slice that arrives
+// last adds the blocks in slice order.
+#include <algorithm>
+#include <cstring>
+#include <type_traits>
+
+#include "layers.h"
+#include "pair.cuh"
+#include "ptx.cuh"
+
+namespace pg {
+namespace {
+
+constexpr int kBK = 64;        // k per ring slot (128-byte rows)
+constexpr int kBI = 128;       // i per CTA
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kGroupTiles = 8;  // rasterisation: tiles of j walked before the next tile of i
+
+template <int BN>
+struct Cfg {
+    static constexpr int BNH = BN / 2;
+    static constexpr int A_BYTES = kBI * kBK * 2;
+    static constexpr int B_BYTES = BNH * kBK * 2;
+    static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+    static constexpr int STAGES_RAW = 200 * 1024 / STAGE_BYTES;
+    static constexpr int STAGES = STAGES_RAW > 12 ? 12 : STAGES_RAW;
+    static constexpr int TABLE_BYTES = 2 * (SGEMM_MAX_EXPERTS + 1) * 4 + 8;
+    static constexpr int BAR_BYTES = (2 * STAGES + 5) * 8 + 16;
+    static constexpr size_t SMEM = 1024 + static_cast<size_t>(STAGES) * STAGE_BYTES + TABLE_BYTES + BAR_BYTES;
+    static constexpr uint32_t TMEM_COLS = 2 * BN < 32 ? 32 : 2 * BN;
+    static constexpr int CHUNKS = BN / 32;              // 32-column chunks of a tile
+    static constexpr int MINE = CHUNKS > 1 ? CHUNKS / 2 : 1;  // of one epilogue warp
+    static_assert(A_BYTES % 1024 == 0 && B_BYTES % 1024 == 0, "slots need 1 KiB alignment");
+    static_assert(TABLE_BYTES % 8 == 0, "barriers need 8-byte alignment");
+};
+
+struct Params {
+    int32_t ni, nj, nk;
+    int32_t groups;
+    const int32_t* offsets;
+    int32_t rows_on_k;
+    int32_t a_mn, b_mn;
+    int32_t segs;          // products of parts: 1 (bfloat16) or 6 (float32)
+    int32_t chunk_kb;      // k blocks per accumulation chunk
+    int32_t split, split_kb;
+    int32_t a_z, b_z;      // third coordinates per part
+    const int32_t* list;   // gathered rows: row r is list[r] / top (null: not gathered)
+    int32_t top;
+    int32_t a_rows, b_rows;  // rows per part, for gathered loads
+    int32_t a_oob, b_oob;    // a row past the matrix: reads as zeros
+    int32_t tiles_i, tiles_j;  // tiles_j: of one group (rows_on_k) or unused
+    const void* bias;
+    int32_t act;
+    const void* residual;
+    int64_t ldr;
+    void* out;
+    int64_t ldo, out_stride;
+    void* preact;
+    int64_t ldz;
+    int32_t out_f32;
+    float* part;
+    int* count;
+    uint64_t timeout_ns;
+    int* status;
+    int32_t debug_flags;
+};
+
+// The parts of A and B in segment s of a float32 product, the smallest terms first.
+__device__ __forceinline__ int a_part(int s, int segs) { return segs == 1 ? 0 : (0x201100 >> (4 * (5 - s))) & 15; }
+__device__ __forceinline__ int b_part(int s, int segs) { return segs == 1 ? 0 : (0x021010 >> (4 * (5 - s))) & 15; }
+
+template <int ACT, int N>
+__device__ __forceinline__ void apply_act(float (&v)[N]) {
+#pragma unroll
+    for (int t = 0; t < N; ++t) v[t] = act_value(v[t], ACT);
+}
+
+// Columns jb + H .. jb + H + 16 of a tile's chunk v: this thread's i, of jn columns.
+template <typename T, typename TO, int H>
+__device__ __forceinline__ void finish_half(const Params& p, const float (&chunk)[32], int g, int64_t i, int64_t jb,
+                                            int jn) {
+    constexpr int N = 16;
+    if (i >= p.ni || jn <= H) return;
+    jb += H;
+    jn -= H;
+    float v[N], r[N];
+#pragma unroll
+    for (int t = 0; t < N; ++t) v[t] = chunk[H + t];
+    if (p.residual) {
+        const T* src = static_cast<const T*>(p.residual) + jb * p.ldr + i;
+#pragma unroll
+        for (int t = 0; t < N; ++t, src += p.ldr) r[t] = t < jn ? to_float(*src) : 0.0f;
+    }
+    if (p.bias) {
+        const float b = to_float(static_cast<const T*>(p.bias)[static_cast<int64_t>(g) * p.ni + i]);
+#pragma unroll
+        for (int t = 0; t < N; ++t) v[t] += b;
+    }
+    if (p.preact) {
+        T* dst = static_cast<T*>(p.preact) + jb * p.ldz + i;
+#pragma unroll
+        for (int t = 0; t < N; ++t, dst += p.ldz)
+            if (t < jn) *dst = from_float<T>(v[t]);
+    }
+    switch (p.act) {
+        case SGEMM_ACT_RELU: apply_act<SGEMM_ACT_RELU>(v); break;
+        case SGEMM_ACT_SILU: apply_act<SGEMM_ACT_SILU>(v); break;
+        case SGEMM_ACT_GELU: apply_act<SGEMM_ACT_GELU>(v); break;
+        case SGEMM_ACT_GELU_TANH: apply_act<SGEMM_ACT_GELU_TANH>(v); break;
+        default: break;
+    }
+    if (p.residual) {
+#pragma unroll
+        for (int t = 0; t < N; ++t) v[t] += r[t];
+    }
+    TO* dst = static_cast<TO*>(p.out) + (p.rows_on_k ? g * p.out_stride : 0) + jb * p.ldo + i;
+#pragma unroll
+    for (int t = 0; t < N; ++t, dst += p.ldo)
+        if (t < jn) *dst = from_float<TO>(v[t]);
+}
+
+template <typename T, typename TO>
+__device__ __forceinline__ void finish(const Params& p, const float (&v)[32], int g, int64_t i, int64_t jb, int jn) {
+    finish_half<T, TO, 0>(p, v, g, i, jb, jn);
+    finish_half<T, TO, 16>(p, v, g, i, jb, jn);
+}
+
+// F32: float32 operands in three parts, accumulated in chunks.
+template <int BN, bool F32>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    product_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                      const __grid_constant__ CUtensorMap tmAg, const __grid_constant__ CUtensorMap tmBg,
+                      const Params p) {
+    using C = Cfg<BN>;
+    using T = typename std::conditional<F32, float, bf16>::type;
+    constexpr int S = C::STAGES;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = align_smem_1024(smem_raw);
+    int32_t* off = reinterpret_cast<int32_t*>(smem + S * C::STAGE_BYTES);  // first row of each group
+    int32_t* pre = off + SGEMM_MAX_EXPERTS + 1;                            // first tile of each group
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S * C::STAGE_BYTES + C::TABLE_BYTES);
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 2 * S + 5);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+    const uint32_t full0 = smem_u32(bars);
+    const uint32_t empty0 = smem_u32(bars + S);
+    const uint32_t acc_full0 = smem_u32(bars + 2 * S);
+    const uint32_t acc_empty0 = smem_u32(bars + 2 * S + 2);
+    const uint32_t mma_done = smem_u32(bars + 2 * S + 4);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const bool leader = rank == 0;
+    const int pair = blockIdx.x >> 1;
+    const int pairs = gridDim.x >> 1;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(full0 + 8 * s, 1);
+            mbar_init(empty0 + 8 * s, 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(acc_full0 + 8 * b, 1);
+            mbar_init(acc_empty0 + 8 * b, 2 * kEpiWarps);
+        }
+        mbar_init(mma_done, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_holder)),
+                     "r"(C::TMEM_COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    pdl_wait();
+    // The groups' rows and tiles.  Whatever the offsets hold, 0 <= off[g] <= off[g + 1] <= rows.
+    const int rows = p.rows_on_k ? p.nk : p.nj;
+    if (warp == 2) {
+        int tiles = 0, last = 0;
+        for (int g0 = 0; g0 < p.groups; g0 += 32) {
+            const int g = g0 + lane;
+            int first = 0, end = rows;
+            if (p.offsets && g < p.groups) {
+                first = min(max(p.offsets[g], 0), rows);
+                end = min(max(p.offsets[g + 1], 0), rows);
+            }
+            // running maximum: no group starts before the one before it ends
+            int top = max(first, last);
+            for (int o = 1; o < 32; o <<= 1) top = max(top, __shfl_up_sync(0xffffffffu, top, o));
+            first = top;
+            const int next = __shfl_down_sync(0xffffffffu, first, 1);
+            if (p.offsets && lane < 31 && g + 1 < p.groups) end = next;
+            end = max(end, first);
+            const int mine = g < p.groups ? (end - first + BN - 1) / BN : 0;
+            int sum = mine;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += v;
+            }
+            if (g < p.groups) {
+                off[g] = first;
+                pre[g] = tiles + sum - mine;
+                if (g == p.groups - 1) off[p.groups] = end;
+            }
+            tiles += __shfl_sync(0xffffffffu, sum, 31);
+            last = __shfl_sync(0xffffffffu, end, 31);
+        }
+        if (lane == 0) pre[p.groups] = tiles;
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    cluster_sync_all();  // both CTAs' barriers and TMEM exist before any cross-CTA traffic
+    tc_fence_after_sync();
+    const uint32_t tmem = *tmem_holder;
+    const int tiles_j = p.rows_on_k ? p.tiles_j * p.groups : pre[p.groups];
+    const int tiles = tiles_j * p.tiles_i;
+    const int units = tiles * p.split;
+
+    struct Unit {
+        int tile, slice, g;
+        int i0, j0, j_end;   // j_end: of the group
+        int k0, k_end;       // rows_on_k: the group's rows; else 0 and nk
+        int kb0, nkb;        // this slice's k blocks
+    };
+    auto unit_of = [&](int u) {
+        Unit x;
+        x.tile = u % tiles;
+        x.slice = u / tiles;
+        int tj, ti;
+        if (p.rows_on_k) {
+            const int per = p.tiles_j * p.tiles_i;
+            x.g = x.tile / per;
+            tile_coords(x.tile - x.g * per, p.tiles_j, p.tiles_i, kGroupTiles, tj, ti);
+            x.j0 = tj * BN;
+            x.j_end = p.nj;
+            x.k0 = off[x.g];
+            x.k_end = off[x.g + 1];
+        } else {
+            tile_coords(x.tile, tiles_j, p.tiles_i, kGroupTiles, tj, ti);
+            int lo = 0, hi = p.groups - 1;  // the last group whose first tile is at or before tj
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (pre[mid] <= tj)
+                    lo = mid;
+                else
+                    hi = mid - 1;
+            }
+            x.g = lo;
+            x.j0 = off[lo] + (tj - pre[lo]) * BN;
+            x.j_end = off[lo + 1];
+            x.k0 = 0;
+            x.k_end = p.nk;
+        }
+        x.i0 = ti * (2 * kBI);
+        const int kb_total = (x.k_end - x.k0 + kBK - 1) / kBK;
+        x.kb0 = x.slice * p.split_kb;
+        x.nkb = min(x.kb0 + p.split_kb, kb_total) - x.kb0;
+        if (x.nkb < 0) x.nkb = 0;
+        return x;
+    };
+
+    if (warp == 0) {
+        // ---------------- TMA loader (both CTAs) ----------------
+        if (!(p.debug_flags & 1)) {
+            if (lane == 0) {
+                prefetch_tmap(&tmA);
+                prefetch_tmap(&tmB);
+            }
+            const uint32_t full_leader0 = map_to_rank(full0, 0);
+            int it = 0;
+            bool ok = true;
+            for (int u = pair; u < units && ok; u += pairs) {
+                const Unit x = unit_of(u);
+                const int ia = x.i0 + kBI * static_cast<int>(rank);
+                const int jb = x.j0 + C::BNH * static_cast<int>(rank);
+                const bool gather_b = p.list != nullptr && !p.rows_on_k;
+                const bool gather_a = p.list != nullptr && p.rows_on_k;
+                auto source = [&](int r) {  // the gathered row r (a row past the matrix for a list entry of none)
+                    const int v = static_cast<int>(gathered_row(p.list, p.top, r, p.b_rows));
+                    return v >= 0 ? v : p.b_oob;
+                };
+                int4 rows_b = make_int4(0, 0, 0, 0);  // this lane's four gathered rows of B
+                if (gather_b && lane < C::BNH / 4) {
+                    const int r = jb + 4 * lane;
+                    rows_b.x = r < x.j_end ? source(r) : p.b_oob;
+                    rows_b.y = r + 1 < x.j_end ? source(r + 1) : p.b_oob;
+                    rows_b.z = r + 2 < x.j_end ? source(r + 2) : p.b_oob;
+                    rows_b.w = r + 3 < x.j_end ? source(r + 3) : p.b_oob;
+                }
+                for (int c0 = 0; c0 < x.nkb && ok; c0 += p.chunk_kb) {
+                    const int c1 = min(c0 + p.chunk_kb, x.nkb);
+                    for (int s = 0; s < p.segs && ok; ++s) {
+                        const int pa = a_part(s, p.segs), pb = b_part(s, p.segs);
+                        for (int kb = c0; kb < c1; ++kb, ++it) {
+                            const int slot_i = it % S;
+                            ok = __all_sync(0xffffffffu, mbar_wait_bounded(empty0 + 8 * slot_i, ((it / S) & 1) ^ 1,
+                                                                           p.timeout_ns, abort_flag));
+                            if (!ok) {
+                                if (lane == 0) raise_abort(abort_flag, p.status);
+                                break;
+                            }
+                            if (leader && lane == 0) mbar_arrive_expect_tx(full0 + 8 * slot_i, 2 * C::STAGE_BYTES);
+                            const uint32_t bar = full_leader0 + 8 * slot_i;
+                            const uint32_t slot = smem_u32(smem + slot_i * C::STAGE_BYTES);
+                            const uint32_t slot_b = slot + C::A_BYTES;
+                            const int kc = x.k0 + (x.kb0 + kb) * kBK;
+                            // a group's rows that end inside this block: the rows past them must read as
+                            // zeros, not as the next group's, so they are named one by one
+                            const bool ragged = p.rows_on_k && p.offsets != nullptr && kc + kBK > x.k_end;
+                            const int z_a = p.rows_on_k ? pa * p.a_z : pa * p.a_z + x.g;
+                            if (gather_a || ragged) {
+                                // lane: columns 64 h .. of A, rows r .. r + 3 of the block
+                                const int h = lane >> 4, r = kc + 4 * (lane & 15);
+                                int4 y;
+                                int* yy = &y.x;
+#pragma unroll
+                                for (int q = 0; q < 4; ++q) {
+                                    int row = r + q < x.k_end ? r + q : -1;
+                                    if (gather_a && row >= 0)
+                                        row = static_cast<int>(gathered_row(p.list, p.top, row, p.a_rows));
+                                    yy[q] = row >= 0 ? row + pa * p.a_rows : p.a_oob;
+                                }
+                                tma_gather4_pair(slot + 8192 * h + 512 * (lane & 15), &tmAg, ia + 64 * h, y, bar);
+                            } else if (lane == 0) {
+                                if (p.a_mn) {
+                                    tma_load_3d_pair(slot, &tmA, ia, kc, z_a, bar);
+                                    tma_load_3d_pair(slot + 8192, &tmA, ia + 64, kc, z_a, bar);
+                                } else {
+                                    tma_load_3d_pair(slot, &tmA, kc, ia, z_a, bar);
+                                }
+                            }
+                            if (gather_b) {
+                                if (lane < C::BNH / 4)
+                                    tma_gather4_pair(slot_b + 512 * lane, &tmBg, kc, rows_b, bar);
+                            } else if (ragged) {
+                                const int h = lane >> 4, r = kc + 4 * (lane & 15);
+                                int4 y;
+                                int* yy = &y.x;
+#pragma unroll
+                                for (int q = 0; q < 4; ++q)
+                                    yy[q] = r + q < x.k_end ? r + q + pb * p.b_rows : p.b_oob;
+                                if (h < C::BNH / 64)
+                                    tma_gather4_pair(slot_b + 8192 * h + 512 * (lane & 15), &tmBg, jb + 64 * h, y, bar);
+                            } else if (lane == 0) {
+                                const int z_b = pb * p.b_z;
+                                if (p.b_mn) {
+#pragma unroll
+                                    for (int h = 0; h < C::BNH / 64; ++h)
+                                        tma_load_3d_pair(slot_b + 8192 * h, &tmB, jb + 64 * h, kc, z_b, bar);
+                                } else {
+                                    tma_load_3d_pair(slot_b, &tmB, kc, jb, z_b, bar);
+                                }
+                            }
+                            __syncwarp();
+                        }
+                    }
+                }
+            }
+            if (lane == 0) pdl_trigger();
+            if (leader && lane == 0) {
+                // Let every copy of the pair land before the CTAs may retire (CTA 0's
+                // full barriers count both CTAs' bytes).
+                for (int j = max(0, it - S); j < it; ++j)
+                    mbar_wait_bounded(full0 + 8 * (j % S), (j / S) & 1, p.timeout_ns, nullptr);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---------------- MMA issuer (CTA 0 of the pair) ----------------
+        if (leader && lane == 0) {
+            const uint32_t idesc = idesc_bf16(2 * kBI, BN, p.a_mn != 0, p.b_mn != 0);
+            // K-major: 8-row atoms 1 KiB apart, a k-step of 16 is 32 bytes further along the rows.
+            // MN-major: 64-column groups 8 KiB apart, 8-k atoms 1 KiB apart, a k-step 2 KiB further.
+            const uint32_t slot0 = smem_u32(smem);
+            const uint64_t a_desc0 = smem_desc(slot0, p.a_mn ? 8192 : 16, 1024, kSwizzle128B);
+            const uint64_t b_desc0 = smem_desc(slot0 + C::A_BYTES, p.b_mn ? 8192 : 16, 1024, kSwizzle128B);
+            const uint32_t a_step = p.a_mn ? 128 : 2, b_step = p.b_mn ? 128 : 2;
+            int slot_i = 0, chunk = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int u = pair; u < units && ok; u += pairs) {
+                const Unit x = unit_of(u);
+                for (int c0 = 0; c0 < x.nkb && ok; c0 += p.chunk_kb, ++chunk) {
+                    const int steps = (min(c0 + p.chunk_kb, x.nkb) - c0) * p.segs;
+                    const int buf = chunk & 1;
+                    if (!mbar_wait_bounded(acc_empty0 + 8 * buf, ((chunk >> 1) & 1) ^ 1, p.timeout_ns, abort_flag)) {
+                        raise_abort(abort_flag, p.status);
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after_sync();
+                    const uint32_t d = tmem + buf * BN;
+                    uint32_t accumulate = 0;
+                    for (int kb = 0; kb < steps; ++kb) {
+                        if (!mbar_wait_bounded(full0 + 8 * slot_i, phase, p.timeout_ns, abort_flag)) {
+                            raise_abort(abort_flag, p.status);
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after_sync();
+                        const uint32_t o = static_cast<uint32_t>(slot_i * C::STAGE_BYTES) >> 4;
+#pragma unroll
+                        for (int kk = 0; kk < kBK / 16; ++kk) {
+                            mma_bf16_pair(d, a_desc0 + (o + kk * a_step), b_desc0 + (o + kk * b_step), idesc,
+                                          accumulate);
+                            accumulate = 1;
+                        }
+                        mma_commit_pair(empty0 + 8 * slot_i);
+                        if (++slot_i == S) {
+                            slot_i = 0;
+                            phase ^= 1;
+                        }
+                    }
+                    if (ok) mma_commit_pair(acc_full0 + 8 * buf);
+                }
+            }
+            mma_commit_pair_local(mma_done);  // every MMA issued here has completed
+            mbar_wait_bounded(mma_done, 0, p.timeout_ns, nullptr);
+        }
+        __syncwarp();
+    } else {
+        // ---------------- epilogue (warps 2..9, both CTAs) ----------------
+        const int q = warp & 3;             // TMEM lane quarter this warp may access
+        const int half = (warp - 2) >> 2;   // which of the 32-column chunks it takes
+        const uint32_t acc_empty_leader0 = map_to_rank(acc_empty0, 0);
+        const uint32_t lane_base = tmem + (static_cast<uint32_t>(32 * q) << 16);
+        const int epi = warp - 2;
+        // rows of no group are zero
+        if (!p.rows_on_k && p.offsets) {
+            const int used = off[p.groups];
+            for (int64_t j = used + blockIdx.x * kEpiWarps + epi; j < p.nj; j += gridDim.x * kEpiWarps) {
+                for (int i = lane; i < p.ni; i += 32) {
+                    if (!F32 && !p.out_f32)
+                        static_cast<T*>(p.out)[j * p.ldo + i] = from_float<T>(0.0f);
+                    else
+                        static_cast<float*>(p.out)[j * p.ldo + i] = 0.0f;
+                    if (p.preact) static_cast<T*>(p.preact)[j * p.ldz + i] = from_float<T>(0.0f);
+                }
+            }
+        }
+        auto finish_chunk = [&](const Unit& x, float(&v)[32], int c) {
+            const int64_t i = x.i0 + kBI * rank + 32 * q + lane;
+            const int64_t jb = x.j0 + 32 * c;
+            const int jn = min(32, x.j_end - x.j0 - 32 * c);
+            if (F32 || !p.out_f32)
+                finish<T, T>(p, v, x.g, i, jb, jn);
+            else
+                finish<T, float>(p, v, x.g, i, jb, jn);
+        };
+        int chunk = 0;
+        bool ok = true;
+        for (int u = pair; u < units && ok; u += pairs) {
+            const Unit x = unit_of(u);
+            const int cols = min(BN, x.j_end - x.j0);
+            // this slice's block: [column][256 i]
+            float* block = p.split > 1 ? p.part + (static_cast<int64_t>(x.tile) * p.split + x.slice) * (2 * kBI * BN) +
+                                             kBI * rank + 32 * q + lane
+                                       : nullptr;
+            float acc[F32 ? C::MINE : 1][32];
+            if (F32 || x.nkb == 0) {
+#pragma unroll
+                for (int m = 0; m < (F32 ? C::MINE : 1); ++m)
+#pragma unroll
+                    for (int t = 0; t < 32; ++t) acc[m][t] = 0.0f;
+            }
+            for (int c0 = 0; c0 < x.nkb; c0 += p.chunk_kb, ++chunk) {
+                const int buf = chunk & 1;
+                ok = __all_sync(0xffffffffu,
+                                mbar_wait_bounded(acc_full0 + 8 * buf, (chunk >> 1) & 1, p.timeout_ns, abort_flag));
+                if (!ok) {
+                    if (lane == 0) raise_abort(abort_flag, p.status);
+                    break;
+                }
+                tc_fence_after_sync();
+                if (F32) {
+#pragma unroll
+                    for (int m = 0; m < C::MINE; ++m) {
+                        const int c = half + 2 * m;
+                        if (c < C::CHUNKS && 32 * c < cols) {
+                            uint32_t v[32];
+                            tmem_ld_32x32b_x32(lane_base + buf * BN + 32 * c, v);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int t = 0; t < 32; ++t) acc[m][t] += __uint_as_float(v[t]);
+                        }
+                    }
+                } else {
+#pragma unroll 1
+                    for (int c = half; c < C::CHUNKS && 32 * c < cols; c += 2) {
+                        uint32_t v[32];
+                        tmem_ld_32x32b_x32(lane_base + buf * BN + 32 * c, v);
+                        tmem_wait_ld();
+                        float f[32];
+#pragma unroll
+                        for (int t = 0; t < 32; ++t) f[t] = __uint_as_float(v[t]);
+                        if (block) {
+#pragma unroll
+                            for (int t = 0; t < 32; ++t) block[(32 * c + t) * (2 * kBI)] = f[t];
+                        } else {
+                            finish_chunk(x, f, c);
+                        }
+                    }
+                }
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote_relaxed(acc_empty_leader0 + 8 * buf);
+            }
+            if (!ok) break;
+            if (F32) {
+#pragma unroll
+                for (int m = 0; m < C::MINE; ++m) {
+                    const int c = half + 2 * m;
+                    if (c < C::CHUNKS && 32 * c < cols) {
+                        if (block) {
+#pragma unroll
+                            for (int t = 0; t < 32; ++t) block[(32 * c + t) * (2 * kBI)] = acc[m][t];
+                        } else {
+                            finish_chunk(x, acc[m], c);
+                        }
+                    }
+                }
+            } else if (x.nkb == 0) {  // an empty sum (no k, or an expert without rows)
+#pragma unroll 1
+                for (int c = half; c < C::CHUNKS && 32 * c < cols; c += 2) {
+                    float f[32];
+#pragma unroll
+                    for (int t = 0; t < 32; ++t) f[t] = 0.0f;
+                    finish_chunk(x, f, c);
+                }
+            }
+            if (block) {
+                // Publish this slice's block; the last slice of this warp's region to arrive
+                // adds all of them in slice order.
+                __threadfence();
+                __syncwarp();
+                int arrived = 0;
+                if (lane == 0)
+                    arrived = atomicAdd(p.count + (static_cast<int64_t>(x.tile) * 2 + rank) * kEpiWarps + epi, 1);
+                arrived = __shfl_sync(0xffffffffu, arrived, 0);
+                if (arrived == p.split - 1) {
+                    __threadfence();
+                    const float* first = p.part + static_cast<int64_t>(x.tile) * p.split * (2 * kBI * BN) +
+                                         kBI * rank + 32 * q + lane;
+#pragma unroll 1
+                    for (int c = half; c < C::CHUNKS && 32 * c < cols; c += 2) {
+                        float f[32];
+#pragma unroll
+                        for (int t = 0; t < 32; ++t) f[t] = 0.0f;
+                        for (int s = 0; s < p.split; ++s) {
+                            const float* src = first + static_cast<int64_t>(s) * (2 * kBI * BN);
+                            float b[32];
+#pragma unroll
+                            for (int t = 0; t < 32; ++t) b[t] = __ldcg(src + (32 * c + t) * (2 * kBI));
+#pragma unroll
+                            for (int t = 0; t < 32; ++t) f[t] += b[t];
+                        }
+                        finish_chunk(x, f, c);
+                    }
+                }
+            }
+        }
+    }
+
+    tc_fence_before_sync();
+    __syncthreads();
+    cluster_sync_all();  // no CTA leaves while its peer may still read its shared memory or barriers
+    if (warp == 1) {
+        tc_fence_after_sync();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM_COLS)
+                     : "memory");
+    }
+}
+
+// One row per warp: x = x0 + x1 + x2 with x0 = bf16(x), x1 = bf16(x - x0), x2 =
+// bf16(x - x0 - x1); both differences are exact in FP32, so the three parts hold x's 24
+// bits (down to bfloat16's smallest subnormal, 2^-133).  Of an infinity x0 is +-1 and
+// x2 the infinity, which meets only the other operand's x0: its products are then
+// those of FP32 (see split_tf32); NaN stays in x2.  bfloat16 rows are copied (PARTS 1).
+template <typename T, int PARTS>
+__global__ void __launch_bounds__(256) pack_kernel(const T* src, int64_t ld, int64_t stride, int64_t rows,
+                                                   int64_t per_group, int64_t cols, const int32_t* list, int top,
+                                                   int64_t src_rows, bf16* dst, int64_t ldd) {
+    const int lane = threadIdx.x % 32;
+    pdl_wait();
+    for (int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32; r < rows;
+         r += static_cast<int64_t>(gridDim.x) * 8) {
+        const int64_t s = list ? gathered_row(list, top, r, src_rows) : r % per_group;
+        const bool some = s >= 0;
+        const T* in = src + (list ? 0 : r / per_group) * stride + (some ? s : 0) * ld;
+        bf16* out = dst + r * ldd;
+        for (int64_t c = lane; c < ldd; c += 32) {
+            const float v = some && c < cols ? to_float(in[c]) : 0.0f;
+            bf16 part[PARTS];
+            split_bf16<PARTS>(v, part);
+#pragma unroll
+            for (int q = 0; q < PARTS; ++q) out[q * rows * ldd + c] = part[q];
+        }
+    }
+}
+
+template <int BN, bool F32>
+cudaError_t launch(const CUtensorMap (&m)[4], const Params& p, int64_t units, bool after_previous, int num_sms,
+                   cudaStream_t st) {
+    using C = Cfg<BN>;
+    auto kern = product_tc_kernel<BN, F32>;
+    static std::atomic<uint64_t> smem_set{0};
+    cudaError_t e = set_smem_limit_once(smem_set, reinterpret_cast<const void*>(kern), static_cast<int>(C::SMEM));
+    if (e != cudaSuccess) return e;
+    const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(units, num_sms / 2));
+    return launch_kernel(after_previous, kern, dim3(static_cast<unsigned>(2 * pairs)), dim3(kThreads), C::SMEM, st,
+                         m[0], m[1], m[2], m[3], p);
+}
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+size_t region(size_t bytes) { return (bytes + 255) / 256 * 256; }
+
+}  // namespace
+
+cudaError_t launch_pack(int dtype, const void* src, int64_t ld, int64_t stride, int64_t groups, int64_t per_group,
+                        int64_t cols, const int32_t* list, int top, int64_t src_rows, bf16* dst, int64_t ldd,
+                        int num_sms, bool after_previous, cudaStream_t st) {
+    const int64_t rows = groups * per_group;
+    const dim3 grid(static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(cdiv(rows, 8), 8 * num_sms))));
+    if (dtype == SGEMM_F32)
+        return launch_kernel(after_previous, pack_kernel<float, 3>, grid, dim3(256), 0, st,
+                             static_cast<const float*>(src), ld, stride, rows, per_group, cols, list, top, src_rows,
+                             dst, ldd);
+    return launch_kernel(after_previous, pack_kernel<bf16, 1>, grid, dim3(256), 0, st, static_cast<const bf16*>(src),
+                         ld, stride, rows, per_group, cols, list, top, src_rows, dst, ldd);
+}
+
+// Tile width and K slices.  Grouped rows are cut by their average length, since the
+// lengths are known on the device alone.
+TcPlan plan_tc(const Product& p, int num_sms, int force_bn, int force_split) {
+    TcPlan t{};
+    const int pairs = std::max(num_sms / 2, 1);
+    const int64_t tiles_i = cdiv(p.ni, 2 * kBI);
+    if (p.rows_on_k) {
+        t.bn = p.nj <= 128 ? 128 : 256;
+        t.tiles = tiles_i * cdiv(p.nj, t.bn) * p.groups;
+    } else {
+        const int64_t lists = std::max<int64_t>(1, std::min<int64_t>(p.groups, p.nj));
+        const int64_t rows = cdiv(p.nj, lists);  // of a group, on average
+        t.bn = rows <= 32 ? 32 : (rows <= 64 ? 64 : (rows <= 128 ? 128 : 256));
+    }
+    if (force_bn == 64 || force_bn == 128 || force_bn == 256) t.bn = p.b.k_contiguous ? force_bn : std::max(force_bn, 128);
+    if (p.rows_on_k)
+        t.tiles = tiles_i * cdiv(p.nj, t.bn) * p.groups;
+    else
+        t.tiles = tiles_i * (cdiv(p.nj, t.bn) + (p.groups > 1 ? p.groups : 0));
+    const int64_t kb = cdiv(p.nk, kBK);
+    int64_t split = 1;
+    if (!(p.rows_on_k && p.groups > 1) && kb > 0) {
+        if (force_split > 0)
+            split = force_split;
+        else if (t.tiles < pairs)
+            split = std::min<int64_t>(pairs / t.tiles, kb / 4);
+        split = std::max<int64_t>(1, std::min(split, kb));
+    }
+    t.split_kb = static_cast<int>(kb > 0 ? cdiv(kb, split) : 1);
+    t.split = static_cast<int>(kb > 0 ? cdiv(kb, t.split_kb) : 1);
+    if (t.split > 1) {
+        t.part_bytes = region(static_cast<size_t>(t.tiles) * t.split * 2 * kBI * t.bn * 4);
+        t.count_bytes = region(static_cast<size_t>(t.tiles) * 2 * kEpiWarps * 4);
+    }
+    return t;
+}
+
+// p.a and p.b: bfloat16 matrices that TMA can read (16-byte aligned, ld and stride
+// multiples of 8), in `parts` parts one after another.
+int launch_product_tc(const CallContext& c, const Product& p, const TcPlan& t, int parts, void* ws,
+                      bool after_previous, cudaStream_t st, int* launches) {
+    Params q{};
+    q.ni = static_cast<int32_t>(p.ni);
+    q.nj = static_cast<int32_t>(p.nj);
+    q.nk = static_cast<int32_t>(p.nk);
+    q.groups = p.groups;
+    q.offsets = p.offsets;
+    q.rows_on_k = p.rows_on_k;
+    q.a_mn = !p.a.k_contiguous;
+    q.b_mn = !p.b.k_contiguous;
+    q.segs = parts == 3 ? 6 : 1;
+    q.chunk_kb = parts == 3 ? 512 / kBK : 1 << 30;
+    q.split = t.split;
+    q.split_kb = t.split_kb;
+    q.a_z = p.rows_on_k ? 1 : p.groups;
+    q.b_z = 1;
+    q.list = p.rows_on_k ? p.a.list : p.b.list;
+    q.top = p.rows_on_k ? p.a.top : p.b.top;
+    q.a_rows = static_cast<int32_t>(p.a.rows);
+    q.b_rows = static_cast<int32_t>(p.b.rows);
+    q.a_oob = static_cast<int32_t>(p.a.rows * parts);
+    q.b_oob = static_cast<int32_t>(p.b.rows * parts);
+    q.tiles_i = static_cast<int32_t>(cdiv(p.ni, 2 * kBI));
+    q.tiles_j = static_cast<int32_t>(cdiv(p.nj, t.bn));
+    q.bias = p.bias;
+    q.act = p.act;
+    q.residual = p.residual;
+    q.ldr = p.ldr;
+    q.out = p.out;
+    q.ldo = p.ldo;
+    q.out_stride = p.out_stride;
+    q.preact = p.preact;
+    q.ldz = p.ldz;
+    q.out_f32 = p.out_f32;
+    q.timeout_ns = c.timeout_ns;
+    q.status = c.status;
+    q.debug_flags = c.debug_flags;
+    if (t.split > 1) {
+        q.part = static_cast<float*>(ws);
+        q.count = reinterpret_cast<int*>(static_cast<char*>(ws) + t.part_bytes);
+        const cudaError_t e = cudaMemsetAsync(q.count, 0, t.count_bytes, st);
+        if (e != cudaSuccess) return call_fail_cuda(e, "cudaMemsetAsync (K slice counters)");
+        after_previous = false;
+    }
+    // columns of each matrix, and its box
+    const int64_t cols_a = p.a.k_contiguous ? p.nk : p.ni, cols_b = p.b.k_contiguous ? p.nk : p.nj;
+    const int64_t z_a = (p.rows_on_k ? 1 : p.groups) * static_cast<int64_t>(parts);
+    CUtensorMap m[4];
+    int rc;
+    if (p.nk == 0) {  // nothing is loaded: the maps stay unread
+        std::memset(m, 0, sizeof m);
+    } else {
+        const uint32_t box_a = p.a.k_contiguous ? kBI : kBK, box_b = p.b.k_contiguous ? t.bn / 2 : kBK;
+        if ((rc = call_encode_bf16(&m[0], p.a.ptr, cols_a, p.a.rows, p.a.ld, z_a, p.a.stride, kBK, box_a))) return rc;
+        if ((rc = call_encode_bf16(&m[1], p.b.ptr, cols_b, p.b.rows, p.b.ld, parts, p.b.stride, kBK, box_b))) return rc;
+        m[2] = m[0];
+        m[3] = m[1];
+        const bool ragged = p.rows_on_k && p.offsets;
+        if (ragged) {
+            if ((rc = call_encode_bf16(&m[2], p.a.ptr, cols_a, p.a.rows * parts, p.a.ld, 0, 0, kBK, 1))) return rc;
+        }
+        if (ragged || (q.list && !p.rows_on_k)) {
+            if ((rc = call_encode_bf16(&m[3], p.b.ptr, cols_b, p.b.rows * parts, p.b.ld, 0, 0, kBK, 1))) return rc;
+        }
+    }
+    const int64_t units = t.tiles * t.split;
+    cudaError_t e;
+    if (parts == 3)
+        e = t.bn == 32    ? launch<32, true>(m, q, units, after_previous, c.sms, st)
+            : t.bn == 64  ? launch<64, true>(m, q, units, after_previous, c.sms, st)
+            : t.bn == 128 ? launch<128, true>(m, q, units, after_previous, c.sms, st)
+                          : launch<256, true>(m, q, units, after_previous, c.sms, st);
+    else
+        e = t.bn == 32    ? launch<32, false>(m, q, units, after_previous, c.sms, st)
+            : t.bn == 64  ? launch<64, false>(m, q, units, after_previous, c.sms, st)
+            : t.bn == 128 ? launch<128, false>(m, q, units, after_previous, c.sms, st)
+                          : launch<256, false>(m, q, units, after_previous, c.sms, st);
+    if (e != cudaSuccess) return call_fail_cuda(e, "tensor-core layer product");
+    *launches += 1;
+    return 0;
+}
+
+}  // namespace pg

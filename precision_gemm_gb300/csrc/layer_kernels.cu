@@ -36,7 +36,8 @@ __global__ void __launch_bounds__(256) dact_kernel(int64_t rows, int64_t n, cons
         }
         if (g == groups) break;
         float d = to_float(dy[r * lddy + c]);
-        if (act != SGEMM_ACT_NONE) d *= act_derivative(to_float(z[r * ldz + c]), act);
+        if (act != SGEMM_ACT_NONE)
+            with_act(act, [&](auto a) { d *= act_derivative<decltype(a)::value, PARTS == 1>(to_float(z[r * ldz + c])); });
         if (dz) {
             bf16 q[PARTS];
             split_bf16<PARTS>(d, q);

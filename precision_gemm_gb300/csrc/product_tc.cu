@@ -42,6 +42,7 @@ constexpr int kBK = 64;        // k per ring slot (128-byte rows)
 constexpr int kBI = 128;       // i per CTA
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kCols = 16;      // columns (j) that an epilogue warp takes at a time
 constexpr int kGroupTiles = 8;  // rasterisation: tiles of j walked before the next tile of i
 
 template <int BN>
@@ -56,8 +57,8 @@ struct Cfg {
     static constexpr int BAR_BYTES = (2 * STAGES + 5) * 8 + 16;
     static constexpr size_t SMEM = 1024 + static_cast<size_t>(STAGES) * STAGE_BYTES + TABLE_BYTES + BAR_BYTES;
     static constexpr uint32_t TMEM_COLS = 2 * BN < 32 ? 32 : 2 * BN;
-    static constexpr int CHUNKS = BN / 32;              // 32-column chunks of a tile
-    static constexpr int MINE = CHUNKS > 1 ? CHUNKS / 2 : 1;  // of one epilogue warp
+    static constexpr int CHUNKS = BN / kCols;  // column chunks of a tile
+    static constexpr int MINE = CHUNKS / 2;    // of one epilogue warp
     static_assert(A_BYTES % 1024 == 0 && B_BYTES % 1024 == 0, "slots need 1 KiB alignment");
     static_assert(TABLE_BYTES % 8 == 0, "barriers need 8-byte alignment");
 };
@@ -70,7 +71,8 @@ struct Params {
     int32_t a_mn, b_mn;
     int32_t segs;          // products of parts: 1 (bfloat16) or 6 (float32)
     int32_t chunk_kb;      // k blocks per accumulation chunk
-    int32_t split, split_kb;
+    int32_t split, split_kb;  // K slices of the tiles from split_from on (1: none)
+    int32_t split_from;
     int32_t a_z, b_z;      // third coordinates per part
     const int32_t* list;   // gathered rows: row r is list[r] / top (null: not gathered)
     int32_t top;
@@ -97,60 +99,41 @@ struct Params {
 __device__ __forceinline__ int a_part(int s, int segs) { return segs == 1 ? 0 : (0x201100 >> (4 * (5 - s))) & 15; }
 __device__ __forceinline__ int b_part(int s, int segs) { return segs == 1 ? 0 : (0x021010 >> (4 * (5 - s))) & 15; }
 
-template <int ACT, int N>
-__device__ __forceinline__ void apply_act(float (&v)[N]) {
-#pragma unroll
-    for (int t = 0; t < N; ++t) v[t] = act_value(v[t], ACT);
-}
-
-// Columns jb + H .. jb + H + 16 of a tile's chunk v: this thread's i, of jn columns.
-template <typename T, typename TO, int H>
-__device__ __forceinline__ void finish_half(const Params& p, const float (&chunk)[32], int g, int64_t i, int64_t jb,
-                                            int jn) {
-    constexpr int N = 16;
-    if (i >= p.ni || jn <= H) return;
-    jb += H;
-    jn -= H;
-    float v[N], r[N];
-#pragma unroll
-    for (int t = 0; t < N; ++t) v[t] = chunk[H + t];
+// Columns jb .. jb + N of a tile, sums v, for this thread's i < ni; `jn` of them are rows
+// of out.
+template <typename T, typename TO>
+__device__ __forceinline__ void finish(const Params& p, float (&v)[kCols], float bias, int64_t out_base, int64_t i,
+                                       int64_t jb, int jn) {
+    constexpr int N = kCols;
+    float r[N];
     if (p.residual) {
         const T* src = static_cast<const T*>(p.residual) + jb * p.ldr + i;
+        const int64_t ld = p.ldr;
 #pragma unroll
-        for (int t = 0; t < N; ++t, src += p.ldr) r[t] = t < jn ? to_float(*src) : 0.0f;
+        for (int t = 0; t < N; ++t, src += ld) r[t] = t < jn ? to_float(*src) : 0.0f;
     }
-    if (p.bias) {
-        const float b = to_float(static_cast<const T*>(p.bias)[static_cast<int64_t>(g) * p.ni + i]);
 #pragma unroll
-        for (int t = 0; t < N; ++t) v[t] += b;
-    }
+    for (int t = 0; t < N; ++t) v[t] += bias;
     if (p.preact) {
         T* dst = static_cast<T*>(p.preact) + jb * p.ldz + i;
+        const int64_t ld = p.ldz;
 #pragma unroll
-        for (int t = 0; t < N; ++t, dst += p.ldz)
+        for (int t = 0; t < N; ++t, dst += ld)
             if (t < jn) *dst = from_float<T>(v[t]);
     }
-    switch (p.act) {
-        case SGEMM_ACT_RELU: apply_act<SGEMM_ACT_RELU>(v); break;
-        case SGEMM_ACT_SILU: apply_act<SGEMM_ACT_SILU>(v); break;
-        case SGEMM_ACT_GELU: apply_act<SGEMM_ACT_GELU>(v); break;
-        case SGEMM_ACT_GELU_TANH: apply_act<SGEMM_ACT_GELU_TANH>(v); break;
-        default: break;
-    }
+    with_act(p.act, [&](auto act) {
+#pragma unroll
+        for (int t = 0; t < N; ++t) v[t] = act_value<decltype(act)::value, std::is_same<T, bf16>::value>(v[t]);
+    });
     if (p.residual) {
 #pragma unroll
         for (int t = 0; t < N; ++t) v[t] += r[t];
     }
-    TO* dst = static_cast<TO*>(p.out) + (p.rows_on_k ? g * p.out_stride : 0) + jb * p.ldo + i;
+    TO* dst = static_cast<TO*>(p.out) + out_base + jb * p.ldo + i;
+    const int64_t ld = p.ldo;
 #pragma unroll
-    for (int t = 0; t < N; ++t, dst += p.ldo)
+    for (int t = 0; t < N; ++t, dst += ld)
         if (t < jn) *dst = from_float<TO>(v[t]);
-}
-
-template <typename T, typename TO>
-__device__ __forceinline__ void finish(const Params& p, const float (&v)[32], int g, int64_t i, int64_t jb, int jn) {
-    finish_half<T, TO, 0>(p, v, g, i, jb, jn);
-    finish_half<T, TO, 16>(p, v, g, i, jb, jn);
 }
 
 // F32: float32 operands in three parts, accumulated in chunks.
@@ -243,29 +226,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *tmem_holder;
     const int tiles_j = p.rows_on_k ? p.tiles_j * p.groups : pre[p.groups];
     const int tiles = tiles_j * p.tiles_i;
-    const int units = tiles * p.split;
+    const int whole = p.split > 1 ? min(p.split_from, tiles) : tiles;  // tiles of one slice, first
+    const int units = whole + (tiles - whole) * p.split;
 
     struct Unit {
-        int tile, slice, g;
+        int tile, slice, g;  // tile counted from `whole` on, -1 for a tile of one slice
         int i0, j0, j_end;   // j_end: of the group
         int k0, k_end;       // rows_on_k: the group's rows; else 0 and nk
         int kb0, nkb;        // this slice's k blocks
     };
     auto unit_of = [&](int u) {
         Unit x;
-        x.tile = u % tiles;
-        x.slice = u / tiles;
+        // the slices of a tile are neighbours, so that they run at one time
+        x.tile = u < whole ? -1 : (u - whole) / p.split;
+        x.slice = u < whole ? 0 : (u - whole) % p.split;
+        const int tile = u < whole ? u : whole + x.tile;
         int tj, ti;
         if (p.rows_on_k) {
             const int per = p.tiles_j * p.tiles_i;
-            x.g = x.tile / per;
-            tile_coords(x.tile - x.g * per, p.tiles_j, p.tiles_i, kGroupTiles, tj, ti);
+            x.g = tile / per;
+            tile_coords(tile - x.g * per, p.tiles_j, p.tiles_i, kGroupTiles, tj, ti);
             x.j0 = tj * BN;
             x.j_end = p.nj;
             x.k0 = off[x.g];
             x.k_end = off[x.g + 1];
         } else {
-            tile_coords(x.tile, tiles_j, p.tiles_i, kGroupTiles, tj, ti);
+            tile_coords(tile, tiles_j, p.tiles_i, kGroupTiles, tj, ti);
             int lo = 0, hi = p.groups - 1;  // the last group whose first tile is at or before tj
             while (lo < hi) {
                 const int mid = (lo + hi + 1) >> 1;
@@ -282,9 +268,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         x.i0 = ti * (2 * kBI);
         const int kb_total = (x.k_end - x.k0 + kBK - 1) / kBK;
-        x.kb0 = x.slice * p.split_kb;
-        x.nkb = min(x.kb0 + p.split_kb, kb_total) - x.kb0;
-        if (x.nkb < 0) x.nkb = 0;
+        x.kb0 = x.tile < 0 ? 0 : x.slice * p.split_kb;
+        x.nkb = x.tile < 0 ? kb_total : max(min(x.kb0 + p.split_kb, kb_total) - x.kb0, 0);
         return x;
     };
 
@@ -467,14 +452,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
             }
         }
-        auto finish_chunk = [&](const Unit& x, float(&v)[32], int c) {
+        float bias = 0.0f;  // of the unit's group and this thread's i
+        auto finish_chunk = [&](const Unit& x, float(&v)[kCols], int c) {
             const int64_t i = x.i0 + kBI * rank + 32 * q + lane;
-            const int64_t jb = x.j0 + 32 * c;
-            const int jn = min(32, x.j_end - x.j0 - 32 * c);
+            if (i >= p.ni) return;
+            const int64_t jb = x.j0 + kCols * c;
+            const int jn = x.j_end - x.j0 - kCols * c;
+            const int64_t base = p.rows_on_k ? x.g * p.out_stride : 0;
             if (F32 || !p.out_f32)
-                finish<T, T>(p, v, x.g, i, jb, jn);
+                finish<T, T>(p, v, bias, base, i, jb, jn);
             else
-                finish<T, float>(p, v, x.g, i, jb, jn);
+                finish<T, float>(p, v, bias, base, i, jb, jn);
         };
         int chunk = 0;
         bool ok = true;
@@ -482,81 +470,92 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const Unit x = unit_of(u);
             const int cols = min(BN, x.j_end - x.j0);
             // this slice's block: [column][256 i]
-            float* block = p.split > 1 ? p.part + (static_cast<int64_t>(x.tile) * p.split + x.slice) * (2 * kBI * BN) +
+            float* block = x.tile >= 0 ? p.part + (static_cast<int64_t>(x.tile) * p.split + x.slice) * (2 * kBI * BN) +
                                              kBI * rank + 32 * q + lane
                                        : nullptr;
-            float acc[F32 ? C::MINE : 1][32];
-            if (F32 || x.nkb == 0) {
-#pragma unroll
-                for (int m = 0; m < (F32 ? C::MINE : 1); ++m)
-#pragma unroll
-                    for (int t = 0; t < 32; ++t) acc[m][t] = 0.0f;
+            const int64_t i = x.i0 + kBI * rank + 32 * q + lane;
+            if (p.bias && i < p.ni) bias = to_float(static_cast<const T*>(p.bias)[static_cast<int64_t>(x.g) * p.ni + i]);
+            if (p.residual && i - lane < p.ni) {
+                // the residual comes into L2 while the MMAs run: lane t asks for column t's line
+                for (int t = kCols * half + lane % kCols + 2 * kCols * (lane / kCols); t < cols; t += 4 * kCols)
+                    prefetch_l2(static_cast<const T*>(p.residual) + (x.j0 + t) * p.ldr + i - lane);
             }
-            for (int c0 = 0; c0 < x.nkb; c0 += p.chunk_kb, ++chunk) {
+            const bool any = x.nkb > 0;  // a sum without k (k = 0, an expert without rows) is zero
+            auto wait_sums = [&]() {     // the next chunk's sums; their buffer
                 const int buf = chunk & 1;
                 ok = __all_sync(0xffffffffu,
                                 mbar_wait_bounded(acc_full0 + 8 * buf, (chunk >> 1) & 1, p.timeout_ns, abort_flag));
-                if (!ok) {
-                    if (lane == 0) raise_abort(abort_flag, p.status);
-                    break;
-                }
+                if (!ok && lane == 0) raise_abort(abort_flag, p.status);
                 tc_fence_after_sync();
-                if (F32) {
-#pragma unroll
-                    for (int m = 0; m < C::MINE; ++m) {
-                        const int c = half + 2 * m;
-                        if (c < C::CHUNKS && 32 * c < cols) {
-                            uint32_t v[32];
-                            tmem_ld_32x32b_x32(lane_base + buf * BN + 32 * c, v);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int t = 0; t < 32; ++t) acc[m][t] += __uint_as_float(v[t]);
-                        }
-                    }
-                } else {
-#pragma unroll 1
-                    for (int c = half; c < C::CHUNKS && 32 * c < cols; c += 2) {
-                        uint32_t v[32];
-                        tmem_ld_32x32b_x32(lane_base + buf * BN + 32 * c, v);
-                        tmem_wait_ld();
-                        float f[32];
-#pragma unroll
-                        for (int t = 0; t < 32; ++t) f[t] = __uint_as_float(v[t]);
-                        if (block) {
-#pragma unroll
-                            for (int t = 0; t < 32; ++t) block[(32 * c + t) * (2 * kBI)] = f[t];
-                        } else {
-                            finish_chunk(x, f, c);
-                        }
-                    }
-                }
+                ++chunk;
+                return buf;
+            };
+            auto free_sums = [&](int buf) {
                 tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_remote_relaxed(acc_empty_leader0 + 8 * buf);
-            }
-            if (!ok) break;
-            if (F32) {
+            };
+            int buf = 0;
+            if (F32 && x.nkb > p.chunk_kb) {
+                // Add the chunks; the whole sum goes back to the last one's columns, where the loop
+                // below finds it as it finds a single chunk's (kept in registers, the sums would
+                // leave it too few to have its loads in flight together).
+                float acc[C::MINE][kCols];
 #pragma unroll
-                for (int m = 0; m < C::MINE; ++m) {
-                    const int c = half + 2 * m;
-                    if (c < C::CHUNKS && 32 * c < cols) {
-                        if (block) {
+                for (int m = 0; m < C::MINE; ++m)
 #pragma unroll
-                            for (int t = 0; t < 32; ++t) block[(32 * c + t) * (2 * kBI)] = acc[m][t];
-                        } else {
-                            finish_chunk(x, acc[m], c);
+                    for (int t = 0; t < kCols; ++t) acc[m][t] = 0.0f;
+                for (int c0 = 0; c0 < x.nkb; c0 += p.chunk_kb) {
+                    buf = wait_sums();
+                    if (!ok) break;
+#pragma unroll
+                    for (int m = 0; m < C::MINE; ++m) {
+                        if (kCols * (half + 2 * m) < cols) {
+                            uint32_t v[kCols];
+                            __syncwarp();
+                            tmem_ld_32x32b_x16(lane_base + buf * BN + kCols * (half + 2 * m), v);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int t = 0; t < kCols; ++t) acc[m][t] += __uint_as_float(v[t]);
                         }
                     }
+                    if (c0 + p.chunk_kb < x.nkb) free_sums(buf);
                 }
-            } else if (x.nkb == 0) {  // an empty sum (no k, or an expert without rows)
-#pragma unroll 1
-                for (int c = half; c < C::CHUNKS && 32 * c < cols; c += 2) {
-                    float f[32];
+                if (!ok) break;
 #pragma unroll
-                    for (int t = 0; t < 32; ++t) f[t] = 0.0f;
+                for (int m = 0; m < C::MINE; ++m) {
+                    if (kCols * (half + 2 * m) < cols) {
+                        uint32_t v[kCols];
+#pragma unroll
+                        for (int t = 0; t < kCols; ++t) v[t] = __float_as_uint(acc[m][t]);
+                        __syncwarp();
+                        tmem_st_32x32b_x16(lane_base + buf * BN + kCols * (half + 2 * m), v);
+                    }
+                }
+                tmem_wait_st();
+            } else if (any) {
+                buf = wait_sums();
+                if (!ok) break;
+            }
+#pragma unroll 1
+            for (int c = half; kCols * c < cols; c += 2) {
+                uint32_t v[kCols];
+                __syncwarp();
+                if (any) {
+                    tmem_ld_32x32b_x16(lane_base + buf * BN + kCols * c, v);
+                    tmem_wait_ld();
+                }
+                float f[kCols];
+#pragma unroll
+                for (int t = 0; t < kCols; ++t) f[t] = any ? __uint_as_float(v[t]) : 0.0f;
+                if (block) {
+#pragma unroll
+                    for (int t = 0; t < kCols; ++t) block[(kCols * c + t) * (2 * kBI)] = f[t];
+                } else {
                     finish_chunk(x, f, c);
                 }
             }
+            if (any) free_sums(buf);
             if (block) {
                 // Publish this slice's block; the last slice of this warp's region to arrive
                 // adds all of them in slice order.
@@ -571,17 +570,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     const float* first = p.part + static_cast<int64_t>(x.tile) * p.split * (2 * kBI * BN) +
                                          kBI * rank + 32 * q + lane;
 #pragma unroll 1
-                    for (int c = half; c < C::CHUNKS && 32 * c < cols; c += 2) {
-                        float f[32];
+                    for (int c = half; kCols * c < cols; c += 2) {
+                        float f[kCols];
 #pragma unroll
-                        for (int t = 0; t < 32; ++t) f[t] = 0.0f;
+                        for (int t = 0; t < kCols; ++t) f[t] = 0.0f;
+#pragma unroll 4
                         for (int s = 0; s < p.split; ++s) {
-                            const float* src = first + static_cast<int64_t>(s) * (2 * kBI * BN);
-                            float b[32];
+                            const float* src = first + static_cast<int64_t>(s) * (2 * kBI * BN) + kCols * c * (2 * kBI);
+                            float b[kCols];
 #pragma unroll
-                            for (int t = 0; t < 32; ++t) b[t] = __ldcg(src + (32 * c + t) * (2 * kBI));
+                            for (int t = 0; t < kCols; ++t) b[t] = __ldcg(src + t * (2 * kBI));
 #pragma unroll
-                            for (int t = 0; t < 32; ++t) f[t] += b[t];
+                            for (int t = 0; t < kCols; ++t) f[t] += b[t];
                         }
                         finish_chunk(x, f, c);
                     }
@@ -677,20 +677,31 @@ TcPlan plan_tc(const Product& p, int num_sms, int force_bn, int force_split) {
         t.tiles = tiles_i * cdiv(p.nj, t.bn) * p.groups;
     else
         t.tiles = tiles_i * (cdiv(p.nj, t.bn) + (p.groups > 1 ? p.groups : 0));
+    // K slices.  Under a wave of tiles, all of them are cut so that the slices fill it.  Over
+    // a wave, those of a last wave that is at most half full are.  (Groups that share out k
+    // differ in length: not cut.)
     const int64_t kb = cdiv(p.nk, kBK);
-    int64_t split = 1;
+    const int64_t last = t.tiles % pairs;
+    int64_t split = 1, cut = 0;  // slices, and how many tiles (the last ones) have them
     if (!(p.rows_on_k && p.groups > 1) && kb > 0) {
-        if (force_split > 0)
+        if (force_split > 0) {
             split = force_split;
-        else if (t.tiles < pairs)
+            cut = t.tiles;
+        } else if (t.tiles < pairs) {
             split = std::min<int64_t>(pairs / t.tiles, kb / 4);
+            cut = t.tiles;
+        } else if (p.groups == 1 && last > 0 && 2 * last <= pairs) {
+            split = std::min<int64_t>({pairs / last, 4, kb / 8});
+            cut = last;
+        }
         split = std::max<int64_t>(1, std::min(split, kb));
     }
     t.split_kb = static_cast<int>(kb > 0 ? cdiv(kb, split) : 1);
     t.split = static_cast<int>(kb > 0 ? cdiv(kb, t.split_kb) : 1);
+    t.whole = t.split > 1 ? t.tiles - cut : t.tiles;
     if (t.split > 1) {
-        t.part_bytes = region(static_cast<size_t>(t.tiles) * t.split * 2 * kBI * t.bn * 4);
-        t.count_bytes = region(static_cast<size_t>(t.tiles) * 2 * kEpiWarps * 4);
+        t.part_bytes = region(static_cast<size_t>(cut) * t.split * 2 * kBI * t.bn * 4);
+        t.count_bytes = region(static_cast<size_t>(cut) * 2 * kEpiWarps * 4);
     }
     return t;
 }
@@ -712,6 +723,7 @@ int launch_product_tc(const CallContext& c, const Product& p, const TcPlan& t, i
     q.chunk_kb = parts == 3 ? 512 / kBK : 1 << 30;
     q.split = t.split;
     q.split_kb = t.split_kb;
+    q.split_from = static_cast<int32_t>(t.whole);
     q.a_z = p.rows_on_k ? 1 : p.groups;
     q.b_z = 1;
     q.list = p.rows_on_k ? p.a.list : p.b.list;
@@ -763,7 +775,7 @@ int launch_product_tc(const CallContext& c, const Product& p, const TcPlan& t, i
             if ((rc = call_encode_bf16(&m[3], p.b.ptr, cols_b, p.b.rows * parts, p.b.ld, 0, 0, kBK, 1))) return rc;
         }
     }
-    const int64_t units = t.tiles * t.split;
+    const int64_t units = t.whole + (t.tiles - t.whole) * t.split;
     cudaError_t e;
     if (parts == 3)
         e = t.bn == 32    ? launch<32, true>(m, q, units, after_previous, c.sms, st)

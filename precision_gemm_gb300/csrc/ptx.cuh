@@ -226,6 +226,10 @@ __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.lau
 #define PG_PDL_EARLY 0
 #endif
 
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+
 // ---- TMA -----------------------------------------------------------------------
 
 __device__ __forceinline__ void fence_proxy_async_smem() {

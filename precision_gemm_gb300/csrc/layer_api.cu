@@ -116,9 +116,28 @@ int prepare(const CallContext& c, int dtype, Operand& o, int groups, int64_t col
     return 0;
 }
 
+// Whether a product runs on the kernel that streams the weights once for a few rows.
+// Measured against the tensor cores (us, rows / tensor cores; calls under about 13 us
+// are bound by the host): float32, which they must first write out in parts, 8192 x
+// 2048: 8 rows 20 / 74, 16 rows 39 / 73, 32 rows 74 / 74; 64 experts of 1024 x 2048,
+// 16 rows each 344 / 478, 32 each 609 / 526.  bfloat16, 8192 x 2048: 4 rows 15.6 / 17.5,
+// 8 rows 17.5 / 17.3; 64 experts, one row each 25 / 35, two each 58 / 50.
+bool few_rows(const Product& p) {
+    if (p.rows_on_k || !p.a.k_contiguous || p.nk == 0 || p.out_f32) return false;
+    const int64_t lists = std::min<int64_t>(p.groups, p.nj);  // lists that have rows, at most
+    return p.nj <= lists * (p.dtype == SGEMM_F32 ? 16 : (p.groups == 1 ? 4 : 1));
+}
+
 int product(const CallContext& c, Product p, Arena& a, cudaStream_t st) {
     if (p.ni == 0 || p.nj == 0) return 0;
     int launches = 0;
+    if (few_rows(p)) {
+        if (a.dry()) return 0;
+        const cudaError_t e = launch_product_rows(p, c.sms, false, st);
+        if (e != cudaSuccess) return call_fail_cuda(e, "layer product of few rows");
+        call_count(1);
+        return 0;
+    }
     if (p.nk > 0) {
         const int64_t cols_a = p.a.k_contiguous ? p.nk : p.ni, cols_b = p.b.k_contiguous ? p.nk : p.nj;
         const int64_t rows_in_lists = p.rows_on_k ? p.nk : p.nj;

@@ -5,91 +5,150 @@
 namespace pg {
 namespace {
 
-constexpr int kSlab = 64;  // rows per block of the activation's backward pass
+constexpr int kSlab = 32;    // rows per block of the activation's backward pass
+constexpr int kWidth = 256;  // its columns: 32 threads of eight
 
-// dz = dy * act'(z) for a slab of 64 rows x 256 columns, and the slab's column
-// sums per group: a slab's rows may belong to several groups, whose sums go to
-// the slots slab + g of part ((slabs + groups) x n) -- slab + g grows with every
-// new slab and with every new group, so no two sums share a slot.
+// dz = dy * act'(z) for a slab of 32 rows x 256 columns, and the slab's column sums per
+// group: a slab's rows may belong to several groups, whose sums go to the slots
+// slab + g of part ((slabs + groups) x n) -- slab + g grows with every new slab and
+// with every new group, so no two sums share a slot.  Thread (l, c) takes rows l, l + 8,
+// ... of a group and eight columns; the eight threads of a column add up in order.
+// HBM-bound: reads dy and z, writes dz.
 template <typename T, int PARTS>
 __global__ void __launch_bounds__(256) dact_kernel(int64_t rows, int64_t n, const T* dy, int64_t lddy, const T* z,
                                                    int64_t ldz, int act, bf16* dz, int64_t lddz, int groups,
-                                                   const int32_t* offsets, float* part) {
-    const int64_t c = static_cast<int64_t>(blockIdx.y) * 256 + threadIdx.x;
-    if (c >= n) return;
-    const int64_t r0 = static_cast<int64_t>(blockIdx.x) * kSlab;
-    const int64_t r1 = r0 + kSlab < rows ? r0 + kSlab : rows;
+                                                   const int32_t* offsets, float* part, bool vec) {
+    __shared__ float sums[8][kWidth + 8];
+    const int64_t widths = (n + kWidth - 1) / kWidth, slab = blockIdx.x / widths;
+    const int64_t c0 = (blockIdx.x - slab * widths) * kWidth, c = c0 + 8 * (threadIdx.x % 32);
+    const int l = threadIdx.x / 32;
+    const int valid = static_cast<int>(n - c < 8 ? n - c : 8);  // <= 0: no columns here
+    const int r0 = static_cast<int>(slab * kSlab);
+    const int r1 = static_cast<int>(rows - r0 < kSlab ? rows : r0 + kSlab);
     int g = 0, first = 0, end = static_cast<int>(rows);
-    if (offsets) {
-        do expert_rows(offsets, g, static_cast<int>(rows), first, end);
-        while (end <= r0 && ++g < groups);
-    }
-    float sum = 0.0f;
-    bool any = false;
-    for (int64_t r = r0; r < r1 && g < groups; ++r) {
-        while (r >= end) {
-            if (any && part) part[(blockIdx.x + g) * n + c] = sum;
-            any = false;
-            sum = 0.0f;
-            if (++g == groups) break;
-            expert_rows(offsets, g, static_cast<int>(rows), first, end);
+    if (offsets) {  // the last group that starts at or before r0: an empty one or the slab's first
+        int lo = 0, hi = groups - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (offsets[mid] <= r0)
+                lo = mid;
+            else
+                hi = mid - 1;
         }
-        if (g == groups) break;
-        float d = to_float(dy[r * lddy + c]);
-        if (act != SGEMM_ACT_NONE)
-            with_act(act, [&](auto a) { d *= act_derivative<decltype(a)::value, PARTS == 1>(to_float(z[r * ldz + c])); });
-        if (dz) {
-            bf16 q[PARTS];
-            split_bf16<PARTS>(d, q);
+        g = lo;
+    }
+    for (; g < groups; ++g) {
+        if (offsets) expert_rows(offsets, g, static_cast<int>(rows), first, end);
+        const int a = max(first, r0), b = min(end, r1);
+        if (first >= r1) break;
+        if (a >= b) continue;
+        float sum[8] = {};
+        if (valid > 0) {
+            with_act(act, [&](auto f) {  // outside the loop, which then has several rows' loads in flight
+                constexpr int ACT = decltype(f)::value;
+#pragma unroll 4
+                for (int64_t r = a + l; r < b; r += 8) {
+                    float d[8], s[8];
+                    load8(dy + r * lddy + c, vec, valid, d);
+                    if (ACT != SGEMM_ACT_NONE) {
+                        load8(z + r * ldz + c, vec, valid, s);
 #pragma unroll
-            for (int k = 0; k < PARTS; ++k) dz[(k * rows + r) * lddz + c] = q[k];
+                        for (int t = 0; t < 8; ++t) d[t] *= act_derivative<ACT, PARTS == 1>(s[t]);
+                    }
+                    if (dz) store_parts8<PARTS>(dz + r * lddz + c, rows * lddz, d);
+#pragma unroll
+                    for (int t = 0; t < 8; ++t) sum[t] += d[t];
+                }
+            });
         }
-        sum += d;
-        any = true;
+        if (part) {
+#pragma unroll
+            for (int t = 0; t < 8; ++t) sums[l][8 * (threadIdx.x % 32) + t] = sum[t];
+            __syncthreads();
+            const int64_t col = c0 + threadIdx.x;
+            if (col < n) {
+                float s = 0.0f;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) s += sums[q][threadIdx.x];
+                part[(slab + g) * n + col] = s;
+            }
+            __syncthreads();
+        }
     }
-    if (any && part) part[(blockIdx.x + g) * n + c] = sum;
 }
 
-// dbias[g][c] = the sums of group g's slabs, in order.
+// dbias[g][c] = the sums of group g's slabs: 8 threads per column take every eighth,
+// and their sums are added in order.
 template <typename T>
 __global__ void __launch_bounds__(256) dbias_kernel(int64_t rows, int64_t n, const int32_t* offsets,
                                                     const float* part, T* dbias) {
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    const int g = blockIdx.y;
-    if (c >= n) return;
+    __shared__ float sums[8][33];
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x % 32;
+    const int g = blockIdx.y, l = threadIdx.x / 32;
     int first = 0, end = static_cast<int>(rows);
     if (offsets) expert_rows(offsets, g, static_cast<int>(rows), first, end);
     float sum = 0.0f;
-    if (end > first)
-        for (int s = first / kSlab; s <= (end - 1) / kSlab; ++s) sum += part[(static_cast<int64_t>(s) + g) * n + c];
-    dbias[g * n + c] = from_float<T>(sum);
-}
-
-template <typename T, typename TX>
-__global__ void __launch_bounds__(256) combine_kernel(int top, int64_t n, int64_t rows, const TX* x, int64_t ldx,
-                                                      const int32_t* slots, const float* weights, const T* residual,
-                                                      int64_t ldr, T* y, int64_t ldy) {
-    const int64_t t = blockIdx.x;
-    for (int64_t c = static_cast<int64_t>(blockIdx.y) * 256 + threadIdx.x; c < n; c += 256 * gridDim.y) {
-        float sum = 0.0f;
-        for (int j = 0; j < top; ++j) {
-            const int64_t s = slots[t * top + j];
-            if (s < 0 || s >= rows) continue;
-            const float v = to_float(x[s * ldx + c]);
-            sum = weights ? fmaf(weights[t * top + j], v, sum) : sum + v;
-        }
-        if (residual) sum += to_float(residual[t * ldr + c]);
-        y[t * ldy + c] = from_float<T>(sum);
+    if (c < n && end > first) {
+#pragma unroll 4
+        for (int s = first / kSlab + l; s <= (end - 1) / kSlab; s += 8) sum += part[(static_cast<int64_t>(s) + g) * n + c];
+    }
+    sums[l][threadIdx.x % 32] = sum;
+    __syncthreads();
+    if (l == 0 && c < n) {
+        for (int q = 1; q < 8; ++q) sum += sums[q][threadIdx.x];
+        dbias[g * n + c] = from_float<T>(sum);
     }
 }
 
-// One warp per row r; pair p = rows[r].
+// A thread takes eight columns of a token; its `top` rows are loaded four at a time.
+// HBM-bound on the rows.
+template <typename T, typename TX>
+__global__ void __launch_bounds__(256) combine_kernel(int64_t tokens, int top, int64_t n, const TX* x, int64_t ldx,
+                                                      const int32_t* slots, const float* weights, const T* residual,
+                                                      int64_t ldr, T* y, int64_t ldy, bool vec) {
+    const int64_t eights = (n + 7) / 8, items = tokens * eights, rows = tokens * top;
+    for (int64_t q = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; q < items;
+         q += static_cast<int64_t>(gridDim.x) * 256) {
+        const int64_t t = q / eights, c = (q - t * eights) * 8;
+        const int valid = static_cast<int>(n - c);
+        float sum[8] = {};
+        for (int j0 = 0; j0 < top; j0 += 4) {
+            float v[4][8], w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int64_t s = j0 + j < top ? slots[t * top + j0 + j] : -1;
+                w[j] = 0.0f;
+                if (s >= 0 && s < rows) {
+                    w[j] = weights ? weights[t * top + j0 + j] : 1.0f;
+                    load8(x + s * ldx + c, vec, valid, v[j]);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) v[j][k] = 0.0f;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) sum[k] = fmaf(w[j], v[j][k], sum[k]);
+        }
+        if (residual) {
+            float r[8];
+            load8(residual + t * ldr + c, vec, valid, r);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) sum[k] += r[k];
+        }
+        store8(y + t * ldy + c, vec, valid, sum);
+    }
+}
+
+// One warp per row r, eight columns per lane at a time; pair p = rows[r].  HBM-bound:
+// reads x (for the dot product), writes dx; a token's dy comes from L2 after its first use.
 template <typename T>
 __global__ void __launch_bounds__(256) combine_backward_kernel(int64_t pairs, int top, int64_t n, const T* dy,
                                                                int64_t lddy, const T* x, int64_t ldx,
                                                                const int32_t* rows, const int32_t* slots,
                                                                const float* weights, T* dx, int64_t lddx,
-                                                               float* dweights) {
+                                                               float* dweights, bool vec) {
     const int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32;
     const int lane = threadIdx.x % 32;
     if (r >= pairs) return;
@@ -99,10 +158,20 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(int64_t pairs, in
     const float w = owned ? (weights ? weights[p] : 1.0f) : 0.0f;
     const T* d = dy + (owned ? p / top : 0) * lddy;
     float dot = 0.0f;
-    for (int64_t c = lane; c < n; c += 32) {
-        const float g = owned ? to_float(d[c]) : 0.0f;
-        if (dx) dx[r * lddx + c] = from_float<T>(owned ? w * g : 0.0f);
-        if (dweights && owned) dot = fmaf(g, to_float(x[r * ldx + c]), dot);
+#pragma unroll 2
+    for (int64_t c = 8 * lane; c < n; c += 256) {
+        const int valid = static_cast<int>(n - c);
+        float g[8] = {}, v[8] = {};
+        if (owned) {
+            load8(d + c, vec, valid, g);
+            if (dweights) load8(x + r * ldx + c, vec, valid, v);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            dot = fmaf(g[k], v[k], dot);
+            g[k] *= w;
+        }
+        if (dx) store8(dx + r * lddx + c, vec, valid, g);
     }
     if (dweights && owned) {
         for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
@@ -122,14 +191,15 @@ template <typename T, int PARTS>
 static cudaError_t run_dact(int64_t rows, int64_t n, const void* dy, int64_t lddy, const void* z, int64_t ldz, int act,
                             bf16* dz, int64_t lddz, int groups, const int32_t* offsets, void* dbias, float* part,
                             cudaStream_t st) {
-    const unsigned cols = static_cast<unsigned>((n + 255) / 256);
-    const dim3 grid(static_cast<unsigned>((rows + kSlab - 1) / kSlab), cols);
+    const dim3 grid(static_cast<unsigned>(((rows + kSlab - 1) / kSlab) * ((n + kWidth - 1) / kWidth)));
+    const bool vec = rows_aligned<T>(dy, lddy) && (act == SGEMM_ACT_NONE || rows_aligned<T>(z, ldz));
     if (rows > 0)
         dact_kernel<T, PARTS><<<grid, 256, 0, st>>>(rows, n, static_cast<const T*>(dy), lddy,
                                                     static_cast<const T*>(z), ldz, act, dz, lddz, groups, offsets,
-                                                    dbias ? part : nullptr);
+                                                    dbias ? part : nullptr, vec);
     if (dbias)
-        dbias_kernel<T><<<dim3(cols, groups), 256, 0, st>>>(rows, n, offsets, part, static_cast<T*>(dbias));
+        dbias_kernel<T><<<dim3(static_cast<unsigned>((n + 31) / 32), groups), 256, 0, st>>>(rows, n, offsets, part,
+                                                                                            static_cast<T*>(dbias));
     return cudaGetLastError();
 }
 
@@ -145,10 +215,12 @@ template <typename T, typename TX>
 static cudaError_t run_combine(int64_t tokens, int top, int64_t n, const void* x, int64_t ldx, const int32_t* slots,
                                const float* weights, const void* residual, int64_t ldr, void* y, int64_t ldy,
                                cudaStream_t st) {
-    const unsigned cols = static_cast<unsigned>(n > 8 * 256 ? 8 : (n + 255) / 256);
-    combine_kernel<T, TX><<<dim3(static_cast<unsigned>(tokens), cols), 256, 0, st>>>(
-        top, n, tokens * top, static_cast<const TX*>(x), ldx, slots, weights, static_cast<const T*>(residual), ldr,
-        static_cast<T*>(y), ldy);
+    const int64_t blocks = (tokens * ((n + 7) / 8) + 255) / 256;
+    const bool vec = rows_aligned<TX>(x, ldx) && rows_aligned<T>(y, ldy) &&
+                     (residual == nullptr || rows_aligned<T>(residual, ldr));
+    combine_kernel<T, TX><<<static_cast<unsigned>(blocks < (1 << 20) ? blocks : (1 << 20)), 256, 0, st>>>(
+        tokens, top, n, static_cast<const TX*>(x), ldx, slots, weights, static_cast<const T*>(residual), ldr,
+        static_cast<T*>(y), ldy, vec);
     return cudaGetLastError();
 }
 
@@ -167,9 +239,11 @@ static cudaError_t run_combine_backward(int64_t tokens, int top, int64_t n, cons
                                         const float* weights, void* dx, int64_t lddx, float* dweights,
                                         cudaStream_t st) {
     const int64_t pairs = tokens * top;
+    const bool vec = rows_aligned<T>(dy, lddy) && (dweights == nullptr || rows_aligned<T>(x, ldx)) &&
+                     (dx == nullptr || rows_aligned<T>(dx, lddx));
     combine_backward_kernel<T><<<static_cast<unsigned>((pairs + 7) / 8), 256, 0, st>>>(
         pairs, top, n, static_cast<const T*>(dy), lddy, static_cast<const T*>(x), ldx, rows, slots, weights,
-        static_cast<T*>(dx), lddx, dweights);
+        static_cast<T*>(dx), lddx, dweights, vec);
     return cudaGetLastError();
 }
 

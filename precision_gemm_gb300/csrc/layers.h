@@ -125,6 +125,59 @@ __device__ __forceinline__ void split_bf16(float x, bf16 (&part)[PARTS]) {
     }
 }
 
+// Eight consecutive elements, `valid` of them there (the rest read as zero and are not
+// written); vec: all addresses are 16-byte aligned and whole eights may be accessed.
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, bool vec, int valid, float (&v)[8]) {
+    if (vec && valid >= 8) {
+        uint4 raw[sizeof(T) / 2];
+#pragma unroll
+        for (int q = 0; q < static_cast<int>(sizeof(T)) / 2; ++q) raw[q] = reinterpret_cast<const uint4*>(p)[q];
+        const T* e = reinterpret_cast<const T*>(raw);
+#pragma unroll
+        for (int t = 0; t < 8; ++t) v[t] = to_float(e[t]);
+    } else {
+#pragma unroll
+        for (int t = 0; t < 8; ++t) v[t] = t < valid ? to_float(p[t]) : 0.0f;
+    }
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, bool vec, int valid, const float (&v)[8]) {
+    if (vec && valid >= 8) {
+        uint4 raw[sizeof(T) / 2];
+        T* e = reinterpret_cast<T*>(raw);
+#pragma unroll
+        for (int t = 0; t < 8; ++t) e[t] = from_float<T>(v[t]);
+#pragma unroll
+        for (int q = 0; q < static_cast<int>(sizeof(T)) / 2; ++q) reinterpret_cast<uint4*>(p)[q] = raw[q];
+    } else {
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+            if (t < valid) p[t] = from_float<T>(v[t]);
+    }
+}
+// Whether every row of a matrix can be read in aligned eights.
+template <typename T>
+inline bool rows_aligned(const void* p, int64_t ld) {
+    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * sizeof(T)) % 16 == 0;
+}
+
+// Eight values as the parts of a bfloat16 matrix (16-byte aligned, part_stride apart).
+template <int PARTS>
+__device__ __forceinline__ void store_parts8(bf16* p, int64_t part_stride, const float (&v)[8]) {
+    bf16 part[8][PARTS];
+#pragma unroll
+    for (int t = 0; t < 8; ++t) split_bf16<PARTS>(v[t], part[t]);
+#pragma unroll
+    for (int q = 0; q < PARTS; ++q) {
+        uint4 raw;
+        bf16* e = reinterpret_cast<bf16*>(&raw);
+#pragma unroll
+        for (int t = 0; t < 8; ++t) e[t] = part[t][q];
+        *reinterpret_cast<uint4*>(p + q * part_stride) = raw;
+    }
+}
+
 // The matrix row that gathered row r stands for (list[r] / top), -1 for none.
 __device__ __forceinline__ int64_t gathered_row(const int32_t* list, int top, int64_t r, int64_t rows) {
     const int32_t pair = list[r];
@@ -182,6 +235,10 @@ struct Product {
 };
 
 // ---- launchers -----------------------------------------------------------------------
+
+// Forward products of few rows (b's rows along k, out of the call's dtype): one pass
+// over the weights per 16 rows of a group.
+cudaError_t launch_product_rows(const Product& p, int num_sms, bool after_previous, cudaStream_t st);
 
 // Rows (list[r] / top of src_rows, or `groups` matrices of per_group rows, `stride`
 // apart) as packed bfloat16 parts of leading dimension ldd (a multiple of 8), part

@@ -36,62 +36,68 @@ SCORES = {"softmax": 0, "sigmoid": 1}
 _DTYPES = {torch.float32: SGEMM_F32, torch.bfloat16: SGEMM_BF16}
 
 
-class _Call:
-    """The stream of one call, the device its tensors must be on, and its element
-    type; allocations inside `with` belong to the stream."""
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+if _raw_stream is None:
+    def _raw_stream(index):
+        return torch.cuda.current_stream(index).cuda_stream
 
-    __slots__ = ("handle", "device", "index", "dtype", "code", "_other")
+_Tensor, _empty, _current_device = torch.Tensor, torch.empty, torch.cuda.current_device
 
-    def __init__(self, stream, first, name, dtype=None):
-        if not isinstance(first, torch.Tensor) or not first.is_cuda:
-            raise ValueError("%s: expected a CUDA tensor" % name)
-        self.device = first.device
-        self.index = first.get_device()
-        if self.index != torch.cuda.current_device():
-            raise ValueError("%s: the tensor is on %s, the current device is cuda:%d"
-                             % (name, first.device, torch.cuda.current_device()))
-        self.dtype = first.dtype if dtype is None else dtype
-        self.code = _DTYPES.get(self.dtype)
-        if self.code is None:
-            raise ValueError("%s: expected a float32 or bfloat16 tensor, got %s" % (name, first.dtype))
-        self._other = None
-        if stream is None:
-            self.handle = torch.cuda.current_stream(self.index).cuda_stream
-        else:
-            self.handle = _stream(stream)
-            if self.handle != torch.cuda.current_stream(self.index).cuda_stream:
-                self._other = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(self.handle)
 
-    def empty(self, *shape, dtype=None):
-        if self._other is None:
-            return torch.empty(shape, dtype=self.dtype if dtype is None else dtype, device=self.device)
-        with torch.cuda.stream(self._other):
-            return torch.empty(shape, dtype=self.dtype if dtype is None else dtype, device=self.device)
+def _on(stream, f, *args, **kw):
+    """f on a stream other than the current one: results are allocated on it too."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream(stream))
+    with torch.cuda.stream(stream):
+        return f(*args, **kw)
 
-    def tensor(self, x, name, shape, dtype=None, packed=False):
-        """x checked to be a tensor of this call with the given shape; its row stride
-        (its last dimension has unit stride, all of it when packed)."""
-        if not isinstance(x, torch.Tensor):
-            raise ValueError("%s: expected a tensor, got %r" % (name, type(x)))
-        if x.dtype != (self.dtype if dtype is None else dtype):
-            raise ValueError("%s: expected a %s tensor, got %s" % (name, dtype or self.dtype, x.dtype))
-        if x.get_device() != self.index:
-            raise ValueError("%s: expected a tensor on %s, got one on %s" % (name, self.device, x.device))
-        if tuple(x.shape) != shape:
-            raise ValueError("%s: expected shape %s, got %s" % (name, shape, tuple(x.shape)))
-        if packed:
-            if not x.is_contiguous():
-                raise ValueError("%s: the tensor must be contiguous" % name)
-            return shape[-1] if shape else 1
-        cols = shape[-1]
-        if cols > 1 and x.numel() > 0 and x.stride(-1) != 1:
-            raise ValueError("%s: the last dimension must have unit stride" % name)
-        if len(shape) < 2 or shape[-2] <= 1 or x.numel() == 0:
-            return max(cols, 1)
-        ld = x.stride(-2)
-        if ld < cols:
-            raise ValueError("%s: rows must not overlap (row stride %d, %d columns)" % (name, ld, cols))
-        return ld
+
+# The checks below run on every call, before a kernel that may take 3 us: each goes
+# through its conditions once and leaves the wording of a refusal to _refuse.
+
+
+def _begin(x, name):
+    """The device index of the call's first tensor and its element type's code."""
+    if not isinstance(x, _Tensor) or not x.is_cuda:
+        raise ValueError("%s: expected a CUDA tensor, got %s" % (name, getattr(x, "device", type(x))))
+    index = x.get_device()
+    if index != _current_device():
+        raise ValueError("%s: the tensor is on %s, the current device is cuda:%d" % (name, x.device, _current_device()))
+    code = _DTYPES.get(x.dtype)
+    if code is None:
+        raise ValueError("%s: expected a float32 or bfloat16 tensor, got %s" % (name, x.dtype))
+    return index, code
+
+
+def _matrix(x, name, rows, cols, dtype, index):
+    """The row stride of x, checked to be a rows x cols matrix of the call."""
+    if isinstance(x, _Tensor) and x.dtype is dtype and x.get_device() == index and x.shape == (rows, cols):
+        ld, unit = x.stride()
+        if (unit == 1 or cols <= 1) and ld >= cols:
+            return ld if ld else 1
+        if rows <= 1 and (unit == 1 or cols <= 1) or rows == 0 or cols == 0:
+            return cols if cols else 1
+    _refuse(x, name, (rows, cols), dtype, index)
+
+
+def _packed(x, name, shape, dtype, index):
+    """x checked to be a contiguous tensor of the call."""
+    if not (isinstance(x, _Tensor) and x.dtype is dtype and x.get_device() == index and x.shape == shape and
+            x.is_contiguous()):
+        _refuse(x, name, shape, dtype, index)
+
+
+def _refuse(x, name, shape, dtype, index):
+    if not isinstance(x, _Tensor):
+        raise ValueError("%s: expected a tensor, got %r" % (name, type(x)))
+    if x.dtype != dtype:
+        raise ValueError("%s: expected a %s tensor, got %s" % (name, dtype, x.dtype))
+    if x.get_device() != index:
+        raise ValueError("%s: expected a tensor on cuda:%d, got one on %s" % (name, index, x.device))
+    if tuple(x.shape) != tuple(shape):
+        raise ValueError("%s: expected shape %s, got %s" % (name, tuple(shape), tuple(x.shape)))
+    raise ValueError("%s: strides %s: the last dimension must have unit stride and rows must not overlap (vectors and "
+                     "routing tensors must be contiguous)" % (name, x.stride()))
 
 
 def _ptr(x):
@@ -101,20 +107,20 @@ def _ptr(x):
 def _act(act):
     try:
         return ACTS[act]
-    except KeyError:
+    except (KeyError, TypeError):
         raise ValueError("act: %r is not one of %s" % (act, ", ".join(ACTS))) from None
 
 
 def _score(score):
     try:
         return SCORES[score]
-    except KeyError:
+    except (KeyError, TypeError):
         raise ValueError("score: %r is not one of %s" % (score, ", ".join(SCORES))) from None
 
 
 def _rows2d(x, name):
     """x as a matrix of its last dimension's rows, without copying."""
-    if not isinstance(x, torch.Tensor):
+    if not isinstance(x, _Tensor):
         raise ValueError("%s: expected a tensor, got %r" % (name, type(x)))
     if x.dim() == 2:
         return x
@@ -127,17 +133,10 @@ def _rows2d(x, name):
                          % (name, tuple(x.shape), x.stride())) from None
 
 
-def _matrix_shape(w, name, dims):
-    if not isinstance(w, torch.Tensor) or w.dim() != dims:
+def _shape(w, name, dims):
+    if not isinstance(w, _Tensor) or w.dim() != dims:
         raise ValueError("%s: expected a tensor of %d dimensions" % (name, dims))
-    return tuple(w.shape)
-
-
-def _result(c, given, name, shape):
-    """The caller's tensor for a result, or a new one; and its row stride."""
-    if given is None:
-        return c.empty(*shape), max(shape[-1], 1)
-    return given, c.tensor(given, name, shape)
+    return w.shape
 
 
 def linear(x, w, bias=None, act="none", residual=None, out=None, preact=None, stream=None):
@@ -145,29 +144,43 @@ def linear(x, w, bias=None, act="none", residual=None, out=None, preact=None, st
     (..., n); returns y (..., n).  preact=True also returns x w^T + bias, which
     linear_backward reads; a tensor given as out or preact is written instead.
     residual and out may be the same tensor."""
+    if stream is not None:
+        return _on(stream, linear, x, w, bias, act, residual, out, preact)
     lib = load_library()
-    x2 = _rows2d(x, "x")
-    c = _Call(stream, x2, "x")
-    n, k = _matrix_shape(w, "w", 2)
+    index, code = _begin(x, "x")
+    x2 = x if x.dim() == 2 else _rows2d(x, "x")
+    dtype = x.dtype
+    n, k = _shape(w, "w", 2)
     t = x2.shape[0]
-    ldx = c.tensor(x2, "x", (t, k))
-    ldw = c.tensor(w, "w", (n, k))
+    ldx = _matrix(x2, "x", t, k, dtype, index)
+    ldw = _matrix(w, "w", n, k, dtype, index)
     if bias is not None:
-        c.tensor(bias, "bias", (n,), packed=True)
+        _packed(bias, "bias", (n,), dtype, index)
     ldr = 0
     if residual is not None:
         residual = _rows2d(residual, "residual")
-        ldr = c.tensor(residual, "residual", (t, n))
-    y, ldy = _result(c, None if out is None else _rows2d(out, "out"), "out", (t, n))
+        ldr = _matrix(residual, "residual", t, n, dtype, index)
+    if out is None:
+        y, ldy = _empty((t, n), dtype=dtype, device=x.device), n or 1
+    else:
+        y = _rows2d(out, "out")
+        ldy = _matrix(y, "out", t, n, dtype, index)
     z, ldz = None, 0
-    if preact is not None and preact is not False:
-        z, ldz = _result(c, None if preact is True else _rows2d(preact, "preact"), "preact", (t, n))
-    rc = lib.sgemm_linear(c.code, t, n, k, x2.data_ptr(), ldx, w.data_ptr(), ldw, _ptr(bias), _act(act),
-                          _ptr(residual), ldr, y.data_ptr(), ldy, _ptr(z), ldz, c.handle)
-    _check(rc, lib)
-    y = (y if x.dim() == 2 else y.view(*x.shape[:-1], n)) if out is None else out
     if preact is True:
-        return y, z if x.dim() == 2 else z.view(*x.shape[:-1], n)
+        z, ldz = _empty((t, n), dtype=dtype, device=x.device), n or 1
+    elif preact is not None and preact is not False:
+        z = _rows2d(preact, "preact")
+        ldz = _matrix(z, "preact", t, n, dtype, index)
+    rc = lib.sgemm_linear(code, t, n, k, x2.data_ptr(), ldx, w.data_ptr(), ldw, _ptr(bias), _act(act),
+                          _ptr(residual), ldr, y.data_ptr(), ldy, _ptr(z), ldz, _raw_stream(index))
+    if rc:
+        _check(rc, lib)
+    if out is not None:
+        y = out
+    elif x2 is not x:
+        y = y.view(*x.shape[:-1], n)
+    if preact is True:
+        return y, z if x2 is x else z.view(*x.shape[:-1], n)
     return y
 
 
@@ -175,29 +188,33 @@ def linear_backward(dy, x, w, act="none", preact=None, bias=True, need_dx=True, 
     """(dx, dw, dbias) of linear for dy (..., n), with preact as linear returned it
     (needed unless act is 'none'); dbias is None unless `bias`, dx and dw unless
     needed.  The residual's gradient is dy."""
+    if stream is not None:
+        return _on(stream, linear_backward, dy, x, w, act, preact, bias, need_dx, need_dw)
     lib = load_library()
+    index, code = _begin(x, "x")
     x2, dy2 = _rows2d(x, "x"), _rows2d(dy, "dy")
-    c = _Call(stream, x2, "x")
-    n, k = _matrix_shape(w, "w", 2)
+    dtype, device = x.dtype, x.device
+    n, k = _shape(w, "w", 2)
     t = x2.shape[0]
-    code = _act(act)
-    lddy = c.tensor(dy2, "dy", (t, n))
-    ldx = c.tensor(x2, "x", (t, k))
-    ldw = c.tensor(w, "w", (n, k))
+    kind = _act(act)
+    lddy = _matrix(dy2, "dy", t, n, dtype, index)
+    ldx = _matrix(x2, "x", t, k, dtype, index)
+    ldw = _matrix(w, "w", n, k, dtype, index)
     ldz = 0
-    if code:
+    if kind:
         if preact is None:
             raise ValueError("preact: the gradient of %r needs it" % act)
         preact = _rows2d(preact, "preact")
-        ldz = c.tensor(preact, "preact", (t, n))
+        ldz = _matrix(preact, "preact", t, n, dtype, index)
     else:
         preact = None
-    dx = c.empty(t, k) if need_dx else None
-    dw = c.empty(n, k) if need_dw else None
-    db = c.empty(n) if bias else None
-    rc = lib.sgemm_linear_backward(c.code, t, n, k, dy2.data_ptr(), lddy, x2.data_ptr(), ldx, w.data_ptr(), ldw, code,
-                                   _ptr(preact), ldz, _ptr(dx), max(k, 1), _ptr(dw), max(k, 1), _ptr(db), c.handle)
-    _check(rc, lib)
+    dx = _empty((t, k), dtype=dtype, device=device) if need_dx else None
+    dw = _empty((n, k), dtype=dtype, device=device) if need_dw else None
+    db = _empty((n,), dtype=dtype, device=device) if bias else None
+    rc = lib.sgemm_linear_backward(code, t, n, k, dy2.data_ptr(), lddy, x2.data_ptr(), ldx, w.data_ptr(), ldw, kind,
+                                   _ptr(preact), ldz, _ptr(dx), k or 1, _ptr(dw), k or 1, _ptr(db), _raw_stream(index))
+    if rc:
+        _check(rc, lib)
     if dx is not None and x.dim() != 2:
         dx = dx.view(x.shape)
     return dx, dw, db
@@ -211,37 +228,46 @@ def route(logits, top, score="softmax", bias=None, groups=1, group_top=1, renorm
     alone; with groups > 1 only the group_top best groups of experts are considered,
     a group scoring the sum of its two best.  Ties go to the lower index.  Tokens
     with mask False (tokens, bool) get ids of -1 and weights of zero."""
+    if stream is not None:
+        return _on(stream, route, logits, top, score, bias, groups, group_top, renormalize, scale, mask)
     lib = load_library()
-    c = _Call(stream, logits, "logits")
-    t, e = _matrix_shape(logits, "logits", 2)
-    ldl = c.tensor(logits, "logits", (t, e))
+    index, code = _begin(logits, "logits")
+    device = logits.device
+    t, e = _shape(logits, "logits", 2)
+    ldl = _matrix(logits, "logits", t, e, logits.dtype, index)
     if bias is not None:
-        c.tensor(bias, "bias", (e,), torch.float32, packed=True)
+        _packed(bias, "bias", (e,), torch.float32, index)
     if mask is not None:
-        c.tensor(mask, "mask", (t,), torch.bool, packed=True)
+        _packed(mask, "mask", (t,), torch.bool, index)
     top = int(top)
-    weights = c.empty(t, max(top, 0), dtype=torch.float32)
-    ids = c.empty(t, max(top, 0), dtype=torch.int32)
-    rc = lib.sgemm_route(c.code, t, e, top, logits.data_ptr(), ldl, _score(score), _ptr(bias), groups, group_top,
-                         1 if renormalize else 0, scale, _ptr(mask), weights.data_ptr(), ids.data_ptr(), c.handle)
-    _check(rc, lib)
+    shape = (t, top if top > 0 else 0)
+    weights = _empty(shape, dtype=torch.float32, device=device)
+    ids = _empty(shape, dtype=torch.int32, device=device)
+    rc = lib.sgemm_route(code, t, e, top, logits.data_ptr(), ldl, _score(score), _ptr(bias), groups, group_top,
+                         1 if renormalize else 0, scale, _ptr(mask), weights.data_ptr(), ids.data_ptr(),
+                         _raw_stream(index))
+    if rc:
+        _check(rc, lib)
     return weights, ids
 
 
 def route_backward(dweights, logits, ids, score="softmax", renormalize=True, scale=1.0, stream=None):
     """dlogits of route's weights for dweights (tokens, top), the choice ids held."""
+    if stream is not None:
+        return _on(stream, route_backward, dweights, logits, ids, score, renormalize, scale)
     lib = load_library()
-    c = _Call(stream, logits, "logits")
-    t, e = _matrix_shape(logits, "logits", 2)
-    top = _matrix_shape(ids, "ids", 2)[1]
-    ldl = c.tensor(logits, "logits", (t, e))
-    c.tensor(dweights, "dweights", (t, top), torch.float32, packed=True)
-    c.tensor(ids, "ids", (t, top), torch.int32, packed=True)
-    dlogits = c.empty(t, e)
-    rc = lib.sgemm_route_backward(c.code, t, e, top, dweights.data_ptr(), logits.data_ptr(), ldl, ids.data_ptr(),
-                                  _score(score), 1 if renormalize else 0, scale, dlogits.data_ptr(), max(e, 1),
-                                  c.handle)
-    _check(rc, lib)
+    index, code = _begin(logits, "logits")
+    t, e = _shape(logits, "logits", 2)
+    top = _shape(ids, "ids", 2)[1]
+    ldl = _matrix(logits, "logits", t, e, logits.dtype, index)
+    _packed(dweights, "dweights", (t, top), torch.float32, index)
+    _packed(ids, "ids", (t, top), torch.int32, index)
+    dlogits = _empty((t, e), dtype=logits.dtype, device=logits.device)
+    rc = lib.sgemm_route_backward(code, t, e, top, dweights.data_ptr(), logits.data_ptr(), ldl, ids.data_ptr(),
+                                  _score(score), 1 if renormalize else 0, scale, dlogits.data_ptr(), e or 1,
+                                  _raw_stream(index))
+    if rc:
+        _check(rc, lib)
     return dlogits
 
 
@@ -258,35 +284,50 @@ class ExpertPlan:
 
 
 def expert_plan(ids, experts, stream=None):
-    """The row lists of ids (tokens, top): an expert's rows hold its pairs in order."""
+    """The row lists of ids (tokens, top): an expert's rows hold its pairs in order.
+    The four lists are views of one allocation."""
+    if stream is not None:
+        return _on(stream, expert_plan, ids, experts)
     lib = load_library()
-    t, top = _matrix_shape(ids, "ids", 2)
-    c = _Call(stream, ids, "ids", torch.float32)
-    c.tensor(ids, "ids", (t, top), torch.int32, packed=True)
-    counts, offsets = c.empty(experts, dtype=torch.int32), c.empty(experts + 1, dtype=torch.int32)
-    rows, slots = c.empty(t * top, dtype=torch.int32), c.empty(t, top, dtype=torch.int32)
+    t, top = _shape(ids, "ids", 2)
+    if not ids.is_cuda:
+        raise ValueError("ids: expected a CUDA tensor, got one on %s" % ids.device)
+    index = _current_device()
+    _packed(ids, "ids", (t, top), torch.int32, index)
+    experts = int(experts)
+    if experts < 1:
+        raise ValueError("experts: %d is less than 1" % experts)
+    r = t * top
+    counts, offsets, rows, slots = _empty((2 * experts + 1 + 2 * r,), dtype=torch.int32, device=ids.device).split_with_sizes(
+        (experts, experts + 1, r, r))
     rc = lib.sgemm_expert_plan(t, top, experts, ids.data_ptr(), counts.data_ptr(), offsets.data_ptr(),
-                               rows.data_ptr(), slots.data_ptr(), c.handle)
-    _check(rc, lib)
-    return ExpertPlan(counts, offsets, rows, slots)
+                               rows.data_ptr(), slots.data_ptr(), _raw_stream(index))
+    if rc:
+        _check(rc, lib)
+    return ExpertPlan(counts, offsets, rows, slots.view(t, top))
 
 
-def _plan_sizes(c, plan, experts):
+def _plan_sizes(plan, experts, index):
     if not isinstance(plan, ExpertPlan):
         raise ValueError("plan: expected an ExpertPlan, got %r" % type(plan))
-    t, top = _matrix_shape(plan.slots, "plan.slots", 2)
-    c.tensor(plan.slots, "plan.slots", (t, top), torch.int32, packed=True)
-    c.tensor(plan.rows, "plan.rows", (t * top,), torch.int32, packed=True)
+    t, top = _shape(plan.slots, "plan.slots", 2)
+    _packed(plan.slots, "plan.slots", (t, top), torch.int32, index)
+    _packed(plan.rows, "plan.rows", (t * top,), torch.int32, index)
     if experts is not None:
-        c.tensor(plan.offsets, "plan.offsets", (experts + 1,), torch.int32, packed=True)
+        _packed(plan.offsets, "plan.offsets", (experts + 1,), torch.int32, index)
     return t, top
 
 
-def _expert_weights(c, w, name="w"):
-    e, n, k = _matrix_shape(w, name, 3)
-    ld = c.tensor(w, name, (e, n, k))
-    stride = w.stride(0) if e > 1 else n * ld
-    return e, n, k, ld, stride
+def _expert_weights(w, dtype, index):
+    """experts, n, k, the row stride and the stride between experts of w."""
+    e, n, k = _shape(w, "w", 3)
+    if w.dtype is dtype and w.get_device() == index:
+        stride, ld, unit = w.stride()
+        if n <= 1 or w.numel() == 0:
+            ld = k or 1
+        if (unit == 1 or k <= 1 or w.numel() == 0) and ld >= k:
+            return e, n, k, ld, stride if e > 1 and w.numel() else n * ld
+    _refuse(w, "w", (e, n, k), dtype, index)
 
 
 def expert_linear(x, w, plan, bias=None, act="none", gather=False, out=None, preact=None, stream=None):
@@ -294,22 +335,31 @@ def expert_linear(x, w, plan, bias=None, act="none", gather=False, out=None, pre
     bias (experts, n), where r' is the row's token (gather=True, x (tokens, k)) or r
     itself (x (tokens * top, k)).  Returns (tokens * top, n) in the plan's row order,
     rows of no expert zero; preact and out are as in linear."""
+    if stream is not None:
+        return _on(stream, expert_linear, x, w, plan, bias, act, gather, out, preact)
     lib = load_library()
-    c = _Call(stream, x, "x")
-    e, n, k, ldw, stride = _expert_weights(c, w)
-    t, top = _plan_sizes(c, plan, e)
+    index, code = _begin(x, "x")
+    dtype = x.dtype
+    e, n, k, ldw, stride = _expert_weights(w, dtype, index)
+    t, top = _plan_sizes(plan, e, index)
     rows = t * top
-    ldx = c.tensor(x, "x", (t if gather else rows, k))
+    ldx = _matrix(x, "x", t if gather else rows, k, dtype, index)
     if bias is not None:
-        c.tensor(bias, "bias", (e, n), packed=True)
-    y, ldy = _result(c, out, "out", (rows, n))
+        _packed(bias, "bias", (e, n), dtype, index)
+    if out is None:
+        y, ldy = _empty((rows, n), dtype=dtype, device=x.device), n or 1
+    else:
+        y, ldy = out, _matrix(out, "out", rows, n, dtype, index)
     z, ldz = None, 0
-    if preact is not None and preact is not False:
-        z, ldz = _result(c, None if preact is True else preact, "preact", (rows, n))
-    rc = lib.sgemm_expert_linear(c.code, t, top, e, n, k, 1 if gather else 0, x.data_ptr(), ldx, w.data_ptr(), ldw,
+    if preact is True:
+        z, ldz = _empty((rows, n), dtype=dtype, device=x.device), n or 1
+    elif preact is not None and preact is not False:
+        z, ldz = preact, _matrix(preact, "preact", rows, n, dtype, index)
+    rc = lib.sgemm_expert_linear(code, t, top, e, n, k, 1 if gather else 0, x.data_ptr(), ldx, w.data_ptr(), ldw,
                                  stride, _ptr(bias), _act(act), plan.offsets.data_ptr(), plan.rows.data_ptr(),
-                                 y.data_ptr(), ldy, _ptr(z), ldz, c.handle)
-    _check(rc, lib)
+                                 y.data_ptr(), ldy, _ptr(z), ldz, _raw_stream(index))
+    if rc:
+        _check(rc, lib)
     return (y, z) if preact is True else y
 
 
@@ -317,65 +367,80 @@ def expert_linear_backward(dy, x, w, plan, act="none", preact=None, bias=True, g
                            need_dw=True, stream=None):
     """(dx, dw, dbias) of expert_linear for dy (tokens * top, n).  With gather, dx
     (tokens, k) is the sum over the token's rows."""
+    if stream is not None:
+        return _on(stream, expert_linear_backward, dy, x, w, plan, act, preact, bias, gather, need_dx, need_dw)
     lib = load_library()
-    c = _Call(stream, x, "x")
-    e, n, k, ldw, stride = _expert_weights(c, w)
-    t, top = _plan_sizes(c, plan, e)
+    index, code = _begin(x, "x")
+    dtype, device = x.dtype, x.device
+    e, n, k, ldw, stride = _expert_weights(w, dtype, index)
+    t, top = _plan_sizes(plan, e, index)
     rows = t * top
-    code = _act(act)
-    lddy = c.tensor(dy, "dy", (rows, n))
-    ldx = c.tensor(x, "x", (t if gather else rows, k))
+    kind = _act(act)
+    lddy = _matrix(dy, "dy", rows, n, dtype, index)
+    ldx = _matrix(x, "x", t if gather else rows, k, dtype, index)
     ldz = 0
-    if code:
+    if kind:
         if preact is None:
             raise ValueError("preact: the gradient of %r needs it" % act)
-        ldz = c.tensor(preact, "preact", (rows, n))
+        ldz = _matrix(preact, "preact", rows, n, dtype, index)
     else:
         preact = None
-    dx = c.empty(t if gather else rows, k) if need_dx else None
-    dw = c.empty(e, n, k) if need_dw else None
-    db = c.empty(e, n) if bias else None
+    dx = _empty((t if gather else rows, k), dtype=dtype, device=device) if need_dx else None
+    dw = _empty((e, n, k), dtype=dtype, device=device) if need_dw else None
+    db = _empty((e, n), dtype=dtype, device=device) if bias else None
     rc = lib.sgemm_expert_linear_backward(
-        c.code, t, top, e, n, k, 1 if gather else 0, dy.data_ptr(), lddy, x.data_ptr(), ldx, w.data_ptr(), ldw, stride,
-        code, _ptr(preact), ldz, plan.offsets.data_ptr(), plan.rows.data_ptr(), plan.slots.data_ptr(), _ptr(dx),
-        max(k, 1), _ptr(dw), max(k, 1), n * max(k, 1), _ptr(db), c.handle)
-    _check(rc, lib)
+        code, t, top, e, n, k, 1 if gather else 0, dy.data_ptr(), lddy, x.data_ptr(), ldx, w.data_ptr(), ldw, stride,
+        kind, _ptr(preact), ldz, plan.offsets.data_ptr(), plan.rows.data_ptr(), plan.slots.data_ptr(), _ptr(dx),
+        k or 1, _ptr(dw), k or 1, n * (k or 1), _ptr(db), _raw_stream(index))
+    if rc:
+        _check(rc, lib)
     return dx, dw, db
 
 
 def expert_combine(rows, plan, weights=None, residual=None, out=None, stream=None):
     """y (tokens, n) = residual + the sum over the token's choices of weights
     (tokens, top, float32; ones when None) times its rows (tokens * top, n)."""
+    if stream is not None:
+        return _on(stream, expert_combine, rows, plan, weights, residual, out)
     lib = load_library()
-    c = _Call(stream, rows, "rows")
-    t, top = _plan_sizes(c, plan, None)
-    n = _matrix_shape(rows, "rows", 2)[1]
-    ldx = c.tensor(rows, "rows", (t * top, n))
+    index, code = _begin(rows, "rows")
+    dtype = rows.dtype
+    t, top = _plan_sizes(plan, None, index)
+    n = _shape(rows, "rows", 2)[1]
+    ldx = _matrix(rows, "rows", t * top, n, dtype, index)
     if weights is not None:
-        c.tensor(weights, "weights", (t, top), torch.float32, packed=True)
-    ldr = c.tensor(residual, "residual", (t, n)) if residual is not None else 0
-    y, ldy = _result(c, out, "out", (t, n))
-    rc = lib.sgemm_expert_combine(c.code, t, top, n, rows.data_ptr(), ldx, plan.slots.data_ptr(), _ptr(weights),
-                                  _ptr(residual), ldr, y.data_ptr(), ldy, c.handle)
-    _check(rc, lib)
+        _packed(weights, "weights", (t, top), torch.float32, index)
+    ldr = _matrix(residual, "residual", t, n, dtype, index) if residual is not None else 0
+    if out is None:
+        y, ldy = _empty((t, n), dtype=dtype, device=rows.device), n or 1
+    else:
+        y, ldy = out, _matrix(out, "out", t, n, dtype, index)
+    rc = lib.sgemm_expert_combine(code, t, top, n, rows.data_ptr(), ldx, plan.slots.data_ptr(), _ptr(weights),
+                                  _ptr(residual), ldr, y.data_ptr(), ldy, _raw_stream(index))
+    if rc:
+        _check(rc, lib)
     return y
 
 
 def expert_combine_backward(dy, rows, plan, weights=None, need_dweights=True, stream=None):
     """(drows, dweights) of expert_combine for dy (tokens, n); dweights is None unless
     needed.  The residual's gradient is dy."""
+    if stream is not None:
+        return _on(stream, expert_combine_backward, dy, rows, plan, weights, need_dweights)
     lib = load_library()
-    c = _Call(stream, rows, "rows")
-    t, top = _plan_sizes(c, plan, None)
-    n = _matrix_shape(rows, "rows", 2)[1]
-    ldx = c.tensor(rows, "rows", (t * top, n))
-    lddy = c.tensor(dy, "dy", (t, n))
+    index, code = _begin(rows, "rows")
+    dtype, device = rows.dtype, rows.device
+    t, top = _plan_sizes(plan, None, index)
+    n = _shape(rows, "rows", 2)[1]
+    ldx = _matrix(rows, "rows", t * top, n, dtype, index)
+    lddy = _matrix(dy, "dy", t, n, dtype, index)
     if weights is not None:
-        c.tensor(weights, "weights", (t, top), torch.float32, packed=True)
-    drows = c.empty(t * top, n)
-    dweights = c.empty(t, top, dtype=torch.float32) if need_dweights else None
-    rc = lib.sgemm_expert_combine_backward(c.code, t, top, n, dy.data_ptr(), lddy, rows.data_ptr(), ldx,
+        _packed(weights, "weights", (t, top), torch.float32, index)
+    drows = _empty((t * top, n), dtype=dtype, device=device)
+    dweights = _empty((t, top), dtype=torch.float32, device=device) if need_dweights else None
+    rc = lib.sgemm_expert_combine_backward(code, t, top, n, dy.data_ptr(), lddy, rows.data_ptr(), ldx,
                                            plan.rows.data_ptr(), plan.slots.data_ptr(), _ptr(weights),
-                                           drows.data_ptr(), max(n, 1), _ptr(dweights), c.handle)
-    _check(rc, lib)
+                                           drows.data_ptr(), n or 1, _ptr(dweights), _raw_stream(index))
+    if rc:
+        _check(rc, lib)
     return drows, dweights

@@ -89,11 +89,12 @@ int with_workspace(const CallContext& c, cudaStream_t st, F body) {
 }
 
 // o as the tensor-core kernel reads it: bfloat16 rows at 16-byte aligned addresses are
-// read in place; others, and float32, are packed into bfloat16 parts.
-int prepare(const CallContext& c, int dtype, Operand& o, int groups, int64_t cols, int64_t listed, Arena& a,
-            bool after_previous, cudaStream_t st, int* launches) {
+// read in place; others, and float32, are packed into bfloat16 parts.  Listed rows are
+// copied together unless the kernel gathers them.
+int prepare(const CallContext& c, int dtype, Operand& o, int groups, int64_t cols, int64_t listed, bool gather,
+            Arena& a, bool after_previous, cudaStream_t st, int* launches) {
     if (o.parts) return 0;
-    const bool in_place = dtype == SGEMM_BF16 && (reinterpret_cast<uintptr_t>(o.ptr) & 15) == 0 && o.ld % 8 == 0 &&
+    const bool in_place = dtype == SGEMM_BF16 && (o.list == nullptr || gather) && (reinterpret_cast<uintptr_t>(o.ptr) & 15) == 0 && o.ld % 8 == 0 &&
                           (groups == 1 || o.stride % 8 == 0);
     o.parts = dtype == SGEMM_F32 ? 3 : 1;
     if (in_place) return 0;
@@ -138,13 +139,14 @@ int product(const CallContext& c, Product p, Arena& a, cudaStream_t st) {
         call_count(1);
         return 0;
     }
+    const TcPlan t = plan_tc(p, c.sms, c.force_bn, c.force_split);
     if (p.nk > 0) {
         const int64_t cols_a = p.a.k_contiguous ? p.nk : p.ni, cols_b = p.b.k_contiguous ? p.nk : p.nj;
         const int64_t rows_in_lists = p.rows_on_k ? p.nk : p.nj;
-        PG_CHECK(prepare(c, p.dtype, p.a, p.rows_on_k ? 1 : p.groups, cols_a, rows_in_lists, a, false, st, &launches));
-        PG_CHECK(prepare(c, p.dtype, p.b, 1, cols_b, rows_in_lists, a, launches > 0, st, &launches));
+        PG_CHECK(prepare(c, p.dtype, p.a, p.rows_on_k ? 1 : p.groups, cols_a, rows_in_lists, false, a, false,
+                         st, &launches));
+        PG_CHECK(prepare(c, p.dtype, p.b, 1, cols_b, rows_in_lists, t.gather, a, launches > 0, st, &launches));
     }
-    const TcPlan t = plan_tc(p, c.sms, c.force_bn, c.force_split);
     void* ws = a.take(t.part_bytes + t.count_bytes);
     if (!a.dry()) {
         PG_CHECK(launch_product_tc(c, p, t, p.dtype == SGEMM_F32 ? 3 : 1, ws, launches > 0, st, &launches));

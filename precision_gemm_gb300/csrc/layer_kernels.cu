@@ -15,7 +15,7 @@ constexpr int kWidth = 256;  // its columns: 32 threads of eight
 // ... of a group and eight columns; the eight threads of a column add up in order.
 // HBM-bound: reads dy and z, writes dz.
 template <typename T, int PARTS>
-__global__ void __launch_bounds__(256) dact_kernel(int64_t rows, int64_t n, const T* dy, int64_t lddy, const T* z,
+__global__ void __launch_bounds__(256, 4) dact_kernel(int64_t rows, int64_t n, const T* dy, int64_t lddy, const T* z,
                                                    int64_t ldz, int act, bf16* dz, int64_t lddz, int groups,
                                                    const int32_t* offsets, float* part, bool vec) {
     __shared__ float sums[8][kWidth + 8];
@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(256) dact_kernel(int64_t rows, int64_t n, cons
         if (valid > 0) {
             with_act(act, [&](auto f) {  // outside the loop, which then has several rows' loads in flight
                 constexpr int ACT = decltype(f)::value;
-#pragma unroll 4
+#pragma unroll 2
                 for (int64_t r = a + l; r < b; r += 8) {
                     float d[8], s[8];
                     load8(dy + r * lddy + c, vec, valid, d);

@@ -19,43 +19,56 @@ using bf16 = __nv_bfloat16;
 // ---- activations -----------------------------------------------------------------
 //
 // Formed in FP32.  Results that are rounded to bfloat16 (FAST) take the hardware's
-// exponential and division (a few 2^-22) and, for the normal distribution, one
+// exponential and reciprocal (a few 2^-22) and, for the normal distribution, one
 // exponential and a polynomial: Abramowitz and Stegun, Handbook of Mathematical
 // Functions, 7.1.26, erfc(x) = (a1 t + ... + a5 t^5) exp(-x^2), t = 1 / (1 + q x),
 // to 1.5e-7 -- a third of the instructions of erff, and the derivative shares its
-// exponential (8192 x 8192 elements of gelu': 229 -> 75 us with wide loads).
+// exponential.
 
-// Phi(z), and e = exp(-z^2 / 2).
-template <bool FAST>
-__device__ __forceinline__ float normal_cdf(float z, float& e) {
-    if (!FAST) {
-        e = expf(-0.5f * z * z);
-        return 0.5f * (1.0f + erff(z * 0.70710678118654752f));
-    }
-    const float x = fabsf(z) * 0.70710678118654752f;
-    const float t = __fdividef(1.0f, fmaf(0.3275911f, x, 1.0f));
-    e = __expf(-x * x);
-    float q = fmaf(1.061405429f, t, -1.453152027f);
-    q = fmaf(q, t, 1.421413741f);
-    q = fmaf(q, t, -0.284496736f);
-    q = fmaf(q, t, 0.254829592f);
-    const float tail = 0.5f * q * t * e;
-    return z >= 0.0f ? 1.0f - tail : tail;
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float reciprocal_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 1 - Phi(|z|) by the polynomial, and e = exp(-z^2 / 2).
+__device__ __forceinline__ float normal_tail(float z, float& e) {
+    const float t = reciprocal_approx(fmaf(0.23164189f, fabsf(z), 1.0f));  // 0.3275911 / sqrt(2)
+    e = exp2_approx(-0.72134752f * z * z);                                 // log2(e) / 2
+    float q = fmaf(0.5307027145f, t, -0.7265760135f);                      // the coefficients halved
+    q = fmaf(q, t, 0.7107068705f);
+    q = fmaf(q, t, -0.142248368f);
+    q = fmaf(q, t, 0.127414796f);
+    return q * t * e;
 }
 
 // 1 / (1 + exp(-z))
 template <bool FAST>
 __device__ __forceinline__ float logistic(float z) {
-    return __fdividef(1.0f, 1.0f + (FAST ? __expf(-z) : expf(-z)));
+    return FAST ? reciprocal_approx(1.0f + exp2_approx(-1.44269504f * z)) : __fdividef(1.0f, 1.0f + expf(-z));
+}
+
+// max(z, 0), NaN staying NaN
+__device__ __forceinline__ float relu(float z) {
+    float y;
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(z));
+    return y;
 }
 
 template <int ACT, bool FAST>
 __device__ __forceinline__ float act_value(float z) {
-    if (ACT == SGEMM_ACT_RELU) return z > 0.0f ? z : (z != z ? z : 0.0f);
+    if (ACT == SGEMM_ACT_RELU) return relu(z);
     if (ACT == SGEMM_ACT_SILU) return z * logistic<FAST>(z);
     if (ACT == SGEMM_ACT_GELU) {
-        float e;
-        return z * normal_cdf<FAST>(z, e);
+        if (!FAST) return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+        float e;  // z Phi(z) = max(z, 0) - |z| (1 - Phi(|z|)), the second term 0 for infinities
+        const float tail = normal_tail(z, e);
+        return fmaf(-fminf(fabsf(z), 3.4e38f), tail, relu(z));
     }
     // (1 + tanh(u)) / 2 = 1 / (1 + exp(-2 u))
     if (ACT == SGEMM_ACT_GELU_TANH) return z * logistic<FAST>(1.59576912160573072f * (z + 0.044715f * z * z * z));
@@ -67,11 +80,17 @@ __device__ __forceinline__ float act_derivative(float z) {
     if (ACT == SGEMM_ACT_RELU) return z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
     if (ACT == SGEMM_ACT_SILU) {
         const float p = logistic<FAST>(z);
-        return p * (1.0f + z * (1.0f - p));
+        return p * fmaf(z, 1.0f - p, 1.0f);
     }
     if (ACT == SGEMM_ACT_GELU) {
-        float e;
-        const float cdf = normal_cdf<FAST>(z, e);
+        float e, cdf;
+        if (FAST) {
+            const float tail = normal_tail(z, e);
+            cdf = z >= 0.0f ? 1.0f - tail : tail;
+        } else {
+            e = expf(-0.5f * z * z);
+            cdf = 0.5f * (1.0f + erff(z * 0.70710678118654752f));
+        }
         return fmaf(z * 0.39894228040143268f, e, cdf);
     }
     if (ACT == SGEMM_ACT_GELU_TANH) {
@@ -251,6 +270,7 @@ cudaError_t launch_pack(int dtype, const void* src, int64_t ld, int64_t stride, 
 // and the workspace of the slices' blocks and counters.
 struct TcPlan {
     int bn;
+    bool gather;            // listed rows of b are gathered by the kernel
     int64_t tiles, whole;  // the first `whole` tiles have one slice
     int split, split_kb;
     size_t part_bytes, count_bytes;

@@ -54,18 +54,6 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
         : "memory");
 }
 
-// Arrive on a barrier of another CTA of the cluster, releasing this thread's (and, after
-// __syncwarp, its warp's) writes.
-__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-
-// Asynchronous copy of 16 bytes to shared memory: `bytes` of them from src (not read
-// when 0), the rest zeros.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-
 // Four rows y0 .. y3 of a matrix (tile::gather4 through a tensor map with boxes of one
 // row), one under another in this CTA's shared memory, completing on the mbarrier at
 // `bar_cluster`.  A row past the matrix reads as zeros.

@@ -13,12 +13,12 @@
 // Operands lie in shared memory in 128-byte swizzled rows of 64 values, either way
 // round: K-major (rows along k) or MN-major (rows along i or j, one per k), so that
 // y = x w^T, dx = dz w and dw = dz^T x all read their matrices as they are stored.
-// Rows of B (forward) or of A (dw) can be gathered through a list (GATHER), so that an
-// expert's tokens are never copied together first: four more warps per CTA bring them
-// with 16-byte asynchronous copies into the swizzled places, several blocks in flight,
-// and arrive on the slot's barrier next to the TMA copies of the other operand.  (The
-// TMA unit's own gather of four rows was measured first: 88 cycles an instruction,
-// 0.70 ms for the 65536 x 1024 x 2048 product of 64 experts.)
+// In narrow tiles (BN <= 64) the rows of B can be gathered through a list by the TMA
+// unit (tile::gather4), so that an expert's few tokens need no copy.  Wide tiles read
+// rows that were copied together first: a gather of four 128-byte pieces takes the unit
+// 88 cycles, hidden behind the weights' time in narrow tiles only (65536 x 1024 x 2048,
+// 64 experts: 0.70 ms gathered by the TMA unit, 0.43 ms by 16-byte asynchronous copies
+// of four more warps, 0.21 ms plus a copy of 0.05 ms).
 //
 // float32 operands come as three bfloat16 parts x = x0 + x1 + x2 (pack_kernel), whose
 // six products of weight 2^-16 and above, the smallest first, are summed over a chunk
@@ -46,7 +46,6 @@ constexpr int kBK = 64;        // k per ring slot (128-byte rows)
 constexpr int kBI = 128;       // i per CTA
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 64 + 32 * kEpiWarps;
-constexpr int kGatherWarps = 4;
 constexpr int kCols = 16;      // columns (j) that an epilogue warp takes at a time
 constexpr int kGroupTiles = 8;  // rasterisation: tiles of j walked before the next tile of i
 
@@ -79,10 +78,8 @@ struct Params {
     int32_t split, split_kb;  // K slices of the tiles from split_from on (1: none)
     int32_t split_from;
     int32_t a_z, b_z;      // third coordinates per part
-    const int32_t* list;   // gathered rows: row r is list[r] / top (null: not gathered)
+    const int32_t* list;   // rows of B gathered: row r is list[r] / top (null: not gathered)
     int32_t top;
-    const bf16* src;       // the matrix they are rows of
-    int64_t src_ld;
     int32_t a_rows, b_rows;  // rows per part
     int32_t a_oob, b_oob;    // a row past the matrix: reads as zeros
     int32_t tiles_i, tiles_j;  // tiles_j: of one group (rows_on_k) or unused
@@ -143,10 +140,9 @@ __device__ __forceinline__ void finish(const Params& p, float (&v)[kCols], float
         if (t < jn) *dst = from_float<TO>(v[t]);
 }
 
-// F32: float32 operands in three parts, accumulated in chunks.  GATHER: rows of B
-// (forward) or A (rows_on_k) through p.list, bfloat16 only.
-template <int BN, bool F32, bool GATHER>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads + (GATHER ? 32 * kGatherWarps : 0), 1)
+// F32: float32 operands in three parts, accumulated in chunks.
+template <int BN, bool F32>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     product_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                       const __grid_constant__ CUtensorMap tmAg, const __grid_constant__ CUtensorMap tmBg,
                       const Params p) {
@@ -175,7 +171,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads + (GATHER ?
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
-            mbar_init(full0 + 8 * s, GATHER ? 1 + 2 * kGatherWarps : 1);
+            mbar_init(full0 + 8 * s, 1);
             mbar_init(empty0 + 8 * s, 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -284,80 +280,98 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads + (GATHER ?
     if (warp == 0) {
         // ---------------- TMA loader (both CTAs) ----------------
         if (!(p.debug_flags & 1)) {
-            if (lane == 0) {
-                prefetch_tmap(&tmA);
-                prefetch_tmap(&tmB);
-            }
             const uint32_t full_leader0 = map_to_rank(full0, 0);
-            int it = 0;
+            int it = 0, slot_i = 0;
+            uint32_t phase = 1;
             bool ok = true;
-            for (int u = pair; u < units && ok; u += pairs) {
-                const Unit x = unit_of(u);
-                const int ia = x.i0 + kBI * static_cast<int>(rank);
-                const int jb = x.j0 + C::BNH * static_cast<int>(rank);
-                // what the TMA copies bring per slot and CTA
-                const bool tma_a = !GATHER || !p.rows_on_k, tma_b = !GATHER || p.rows_on_k;
-                const uint32_t bytes = (tma_a ? C::A_BYTES : 0) + (tma_b ? C::B_BYTES : 0);
-                for (int c0 = 0; c0 < x.nkb && ok; c0 += p.chunk_kb) {
-                    const int c1 = min(c0 + p.chunk_kb, x.nkb);
-                    for (int s = 0; s < p.segs && ok; ++s) {
-                        const int pa = a_part(s, p.segs), pb = b_part(s, p.segs);
-                        for (int kb = c0; kb < c1; ++kb, ++it) {
-                            const int slot_i = it % S;
-                            ok = __all_sync(0xffffffffu, mbar_wait_bounded(empty0 + 8 * slot_i, ((it / S) & 1) ^ 1,
-                                                                           p.timeout_ns, abort_flag));
-                            if (!ok) {
-                                if (lane == 0) raise_abort(abort_flag, p.status);
-                                break;
-                            }
-                            if (leader && lane == 0) mbar_arrive_expect_tx(full0 + 8 * slot_i, 2 * bytes);
-                            const uint32_t bar = full_leader0 + 8 * slot_i;
-                            const uint32_t slot = smem_u32(smem + slot_i * C::STAGE_BYTES);
-                            const uint32_t slot_b = slot + C::A_BYTES;
-                            const int kc = x.k0 + (x.kb0 + kb) * kBK;
-                            // a group's rows that end inside this block: the rows past them must read as
-                            // zeros, not as the next group's, so they are named one by one
-                            const bool ragged = p.rows_on_k && p.offsets != nullptr && kc + kBK > x.k_end;
-                            const int z_a = p.rows_on_k ? pa * p.a_z : pa * p.a_z + x.g;
-                            if (ragged) {
-                                // lane: columns 64 h .. of an operand, rows r .. r + 3 of the block
-                                const int h = lane >> 4, r = kc + 4 * (lane & 15);
-                                int4 ya, yb;
-                                int *pya = &ya.x, *pyb = &yb.x;
+            // LISTED: some rows are named one by one (gathered rows of B, or lists that may end inside a
+            // k block), which takes the whole warp; otherwise lane 0 alone runs this.
+            auto load = [&](auto listed) {
+                constexpr bool LISTED = decltype(listed)::value;
+                for (int u = pair; u < units && ok; u += pairs) {
+                    const Unit x = unit_of(u);
+                    const int ia = x.i0 + kBI * static_cast<int>(rank);
+                    const int jb = x.j0 + C::BNH * static_cast<int>(rank);
+                    const bool gather = LISTED && p.list != nullptr;
+                    int4 rows_b = make_int4(0, 0, 0, 0);  // this lane's four gathered rows of B
+                    if (gather && lane < C::BNH / 4) {
+                        int* y = &rows_b.x;
 #pragma unroll
-                                for (int q = 0; q < 4; ++q) {
-                                    const bool in = r + q < x.k_end;
-                                    pya[q] = in ? r + q + pa * p.a_rows : p.a_oob;
-                                    pyb[q] = in ? r + q + pb * p.b_rows : p.b_oob;
+                        for (int q = 0; q < 4; ++q) {
+                            const int r = jb + 4 * lane + q;
+                            const int64_t v = r < x.j_end ? gathered_row(p.list, p.top, r, p.b_rows) : -1;
+                            y[q] = v >= 0 ? static_cast<int>(v) : p.b_oob;
+                        }
+                    }
+                    for (int c0 = 0; c0 < x.nkb && ok; c0 += p.chunk_kb) {
+                        const int c1 = min(c0 + p.chunk_kb, x.nkb);
+                        for (int s = 0; s < p.segs && ok; ++s) {
+                            const int pa = a_part(s, p.segs), pb = b_part(s, p.segs);
+                            const int z_a = p.rows_on_k ? pa * p.a_z : pa * p.a_z + x.g;
+                            const int z_b = pb * p.b_z;
+                            for (int kb = c0; kb < c1; ++kb, ++it) {
+                                ok = mbar_wait_bounded(empty0 + 8 * slot_i, phase, p.timeout_ns, abort_flag);
+                                if (LISTED) ok = __all_sync(0xffffffffu, ok);
+                                if (!ok) {
+                                    if (lane == 0) raise_abort(abort_flag, p.status);
+                                    break;
                                 }
-                                if (tma_a)
+                                if (leader && lane == 0) mbar_arrive_expect_tx(full0 + 8 * slot_i, 2 * C::STAGE_BYTES);
+                                const uint32_t bar = full_leader0 + 8 * slot_i;
+                                const uint32_t slot = smem_u32(smem) + slot_i * C::STAGE_BYTES;
+                                const uint32_t slot_b = slot + C::A_BYTES;
+                                const int kc = x.k0 + (x.kb0 + kb) * kBK;
+                                // a group's rows that end inside this block: the rows past them must read as
+                                // zeros, not as the next group's
+                                const bool ragged = LISTED && p.rows_on_k && kc + kBK > x.k_end;
+                                if (ragged) {
+                                    // lane: columns 64 h .. of an operand, rows r .. r + 3 of the block
+                                    const int h = lane >> 4, r = kc + 4 * (lane & 15);
+                                    int4 ya, yb;
+                                    int *pya = &ya.x, *pyb = &yb.x;
+#pragma unroll
+                                    for (int q = 0; q < 4; ++q) {
+                                        const bool in = r + q < x.k_end;
+                                        pya[q] = in ? r + q + pa * p.a_rows : p.a_oob;
+                                        pyb[q] = in ? r + q + pb * p.b_rows : p.b_oob;
+                                    }
                                     tma_gather4_pair(slot + 8192 * h + 512 * (lane & 15), &tmAg, ia + 64 * h, ya, bar);
-                                if (h < C::BNH / 64)
-                                    tma_gather4_pair(slot_b + 8192 * h + 512 * (lane & 15), &tmBg, jb + 64 * h, yb, bar);
-                            } else if (lane == 0) {
-                                const int z_b = pb * p.b_z;
-                                if (tma_a) {
+                                    if (h < C::BNH / 64)
+                                        tma_gather4_pair(slot_b + 8192 * h + 512 * (lane & 15), &tmBg, jb + 64 * h, yb,
+                                                         bar);
+                                } else if (lane == 0) {
                                     if (p.a_mn) {
                                         tma_load_3d_pair(slot, &tmA, ia, kc, z_a, bar);
                                         tma_load_3d_pair(slot + 8192, &tmA, ia + 64, kc, z_a, bar);
                                     } else {
                                         tma_load_3d_pair(slot, &tmA, kc, ia, z_a, bar);
                                     }
-                                }
-                                if (tma_b) {
                                     if (p.b_mn) {
 #pragma unroll
                                         for (int h = 0; h < C::BNH / 64; ++h)
                                             tma_load_3d_pair(slot_b + 8192 * h, &tmB, jb + 64 * h, kc, z_b, bar);
-                                    } else {
+                                    } else if (!gather) {
                                         tma_load_3d_pair(slot_b, &tmB, kc, jb, z_b, bar);
                                     }
                                 }
+                                if (gather && lane < C::BNH / 4)
+                                    tma_gather4_pair(slot_b + 512 * lane, &tmBg, kc, rows_b, bar);
+                                if (LISTED) __syncwarp();
+                                if (++slot_i == S) {
+                                    slot_i = 0;
+                                    phase ^= 1;
+                                }
                             }
-                            __syncwarp();
                         }
                     }
                 }
+            };
+            if (p.list != nullptr || (p.rows_on_k && p.offsets != nullptr)) {
+                load(std::true_type());
+            } else if (lane == 0) {
+                prefetch_tmap(&tmA);
+                prefetch_tmap(&tmB);
+                load(std::false_type());
             }
             if (lane == 0) pdl_trigger();
             if (leader && lane == 0) {
@@ -395,7 +409,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads + (GATHER ?
                     const uint32_t d = tmem + buf * BN;
                     uint32_t accumulate = 0;
                     for (int kb = 0; kb < steps; ++kb) {
-                        if (!mbar_wait_bounded<GATHER>(full0 + 8 * slot_i, phase, p.timeout_ns, abort_flag)) {
+                        if (!mbar_wait_bounded(full0 + 8 * slot_i, phase, p.timeout_ns, abort_flag)) {
                             raise_abort(abort_flag, p.status);
                             ok = false;
                             break;
@@ -419,94 +433,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads + (GATHER ?
             }
             mma_commit_pair_local(mma_done);  // every MMA issued here has completed
             mbar_wait_bounded(mma_done, 0, p.timeout_ns, nullptr);
-        }
-        __syncwarp();
-    } else if (GATHER && warp >= 2 + kEpiWarps) {
-        // ---------------- gathered rows (warps 10..13, both CTAs) ----------------
-        // Thread t copies 16 bytes (eight columns, chunk c) of every 16th row of the tile.
-        if (!(p.debug_flags & 1)) {
-            constexpr int LAG = S - 2;  // slots whose copies are in flight
-            const uint32_t full_leader0 = map_to_rank(full0, 0);
-            const int t = threadIdx.x - kThreads, c = t & 7, r16 = t >> 3;
-            int it = 0;
-            bool ok = true;
-            auto arrive = [&](int done) {  // this warp's copies of slot use `done` have landed
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_remote(full_leader0 + 8 * (done % S));
-            };
-            auto next_slot = [&]() {  // the shared address of the next slot, once it is free
-                ok = __all_sync(0xffffffffu, mbar_wait_bounded(empty0 + 8 * (it % S), ((it / S) & 1) ^ 1, p.timeout_ns,
-                                                               abort_flag));
-                if (!ok && lane == 0) raise_abort(abort_flag, p.status);
-                return smem_u32(smem + (it % S) * C::STAGE_BYTES);
-            };
-            auto sent = [&]() {
-                asm volatile("cp.async.commit_group;" ::: "memory");
-                if (it >= LAG) {
-                    asm volatile("cp.async.wait_group %0;" ::"n"(LAG) : "memory");
-                    arrive(it - LAG);
-                }
-                ++it;
-            };
-            for (int u = pair; u < units && ok; u += pairs) {
-                const Unit x = unit_of(u);
-                if (!p.rows_on_k) {
-                    // rows of B: j0 + BNH rank + r16 + 16 i, the same for every k block
-                    constexpr int N = C::BNH / 16;
-                    const bf16* row[N];
-#pragma unroll
-                    for (int i = 0; i < N; ++i) {
-                        const int j = x.j0 + C::BNH * static_cast<int>(rank) + r16 + 16 * i;
-                        const int64_t s = j < x.j_end ? gathered_row(p.list, p.top, j, p.b_rows) : -1;
-                        row[i] = s >= 0 ? p.src + s * p.src_ld + 8 * c : nullptr;
-                    }
-                    for (int kb = 0; kb < x.nkb; ++kb) {
-                        const uint32_t slot = next_slot() + C::A_BYTES;
-                        if (!ok) break;
-                        const int kc = (x.kb0 + kb) * kBK;
-                        const int some = min(max(2 * (p.nk - kc - 8 * c), 0), 16);  // bytes inside the row
-#pragma unroll
-                        for (int i = 0; i < N; ++i) {
-                            const int r = r16 + 16 * i, bytes = row[i] ? some : 0;
-                            cp_async16(slot + 128 * r + ((c ^ (r & 7)) << 4), bytes ? row[i] + kc : p.src, bytes);
-                        }
-                        sent();
-                    }
-                } else {
-                    // rows kc + r of A for both groups of 64 columns; r = r16 + 16 i
-                    auto rows_of = [&](int kb, int(&rows)[4]) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int k = x.k0 + (x.kb0 + kb) * kBK + r16 + 16 * i;
-                            rows[i] = k < x.k_end ? static_cast<int>(gathered_row(p.list, p.top, k, p.a_rows)) : -1;
-                        }
-                    };
-                    int rows[4], ahead[4];
-                    if (x.nkb > 0) rows_of(0, ahead);
-                    for (int kb = 0; kb < x.nkb; ++kb) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) rows[i] = ahead[i];
-                        if (kb + 1 < x.nkb) rows_of(kb + 1, ahead);
-                        const uint32_t slot = next_slot();
-                        if (!ok) break;
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int col = x.i0 + kBI * static_cast<int>(rank) + 64 * h + 8 * c;
-                            const int some = min(max(2 * (p.ni - col), 0), 16);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const int r = r16 + 16 * i, bytes = rows[i] >= 0 ? some : 0;
-                                cp_async16(slot + 8192 * h + 128 * r + ((c ^ (r & 7)) << 4),
-                                           bytes ? p.src + rows[i] * p.src_ld + col : p.src, bytes);
-                            }
-                        }
-                        sent();
-                    }
-                }
-            }
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            for (int done = max(0, it - LAG); done < it; ++done) arrive(done);
         }
         __syncwarp();
     } else {
@@ -689,33 +615,46 @@ __global__ void __launch_bounds__(256) pack_kernel(const T* src, int64_t ld, int
                                                    int64_t per_group, int64_t cols, const int32_t* list, int top,
                                                    int64_t src_rows, bf16* dst, int64_t ldd, bool vec) {
     pdl_wait();
-    const int64_t eights = ldd / 8, items = rows * eights;
+    constexpr int R = 4;  // rows of a thread, loaded together
+    const uint32_t eights = static_cast<uint32_t>(ldd / 8);
+    const int64_t items = (rows + R - 1) / R * eights;
     for (int64_t q = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; q < items;
          q += static_cast<int64_t>(gridDim.x) * 256) {
-        const int64_t r = q / eights, c = (q - r * eights) * 8;
-        float v[8] = {};
-        if (list) {
-            const int64_t s = gathered_row(list, top, r, src_rows);
-            if (s >= 0) load8(src + s * ld + c, vec, static_cast<int>(cols - c), v);
-        } else {
-            const int64_t g = r / per_group;
-            load8(src + g * stride + (r - g * per_group) * ld + c, vec, static_cast<int>(cols - c), v);
+        const int64_t r0 = items >> 32 ? q / eights : static_cast<uint32_t>(q) / eights;
+        const int64_t c = (q - r0 * eights) * 8;
+        const int valid = static_cast<int>(cols - c < 8 ? cols - c : 8);
+        float v[R][8] = {};
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const int64_t r = r0 * R + k;
+            if (r >= rows) break;
+            if (list) {
+                const int64_t s = gathered_row(list, top, r, src_rows);
+                if (s >= 0) load8(src + s * ld + c, vec, valid, v[k]);
+            } else {
+                const int64_t g = per_group == rows ? 0 : r / per_group;
+                load8(src + g * stride + (r - g * per_group) * ld + c, vec, valid, v[k]);
+            }
         }
-        store_parts8<PARTS>(dst + r * ldd + c, rows * ldd, v);
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const int64_t r = r0 * R + k;
+            if (r < rows) store_parts8<PARTS>(dst + r * ldd + c, rows * ldd, v[k]);
+        }
     }
 }
 
-template <int BN, bool F32, bool GATHER>
+template <int BN, bool F32>
 cudaError_t launch(const CUtensorMap (&m)[4], const Params& p, int64_t units, bool after_previous, int num_sms,
                    cudaStream_t st) {
     using C = Cfg<BN>;
-    auto kern = product_tc_kernel<BN, F32, GATHER>;
+    auto kern = product_tc_kernel<BN, F32>;
     static std::atomic<uint64_t> smem_set{0};
     cudaError_t e = set_smem_limit_once(smem_set, reinterpret_cast<const void*>(kern), static_cast<int>(C::SMEM));
     if (e != cudaSuccess) return e;
     const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(units, num_sms / 2));
     return launch_kernel(after_previous, kern, dim3(static_cast<unsigned>(2 * pairs)),
-                         dim3(kThreads + (GATHER ? 32 * kGatherWarps : 0)), C::SMEM, st, m[0], m[1], m[2], m[3], p);
+                         dim3(kThreads), C::SMEM, st, m[0], m[1], m[2], m[3], p);
 }
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -727,7 +666,7 @@ cudaError_t launch_pack(int dtype, const void* src, int64_t ld, int64_t stride, 
                         int64_t cols, const int32_t* list, int top, int64_t src_rows, bf16* dst, int64_t ldd,
                         int num_sms, bool after_previous, cudaStream_t st) {
     const int64_t rows = groups * per_group;
-    const dim3 grid(static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(cdiv(rows * (ldd / 8), 256),
+    const dim3 grid(static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(cdiv(cdiv(rows, 4) * (ldd / 8), 256),
                                                                                  16 * num_sms))));
     if (dtype == SGEMM_F32)
         return launch_kernel(after_previous, pack_kernel<float, 3>, grid, dim3(256), 0, st,
@@ -760,6 +699,7 @@ TcPlan plan_tc(const Product& p, int num_sms, int force_bn, int force_split) {
     // K slices.  Under a wave of tiles, all of them are cut so that the slices fill it.  Over
     // a wave, those of a last wave that is at most half full are.  (Groups that share out k
     // differ in length: not cut.)
+    t.gather = t.bn <= 64 && !p.rows_on_k;
     const int64_t kb = cdiv(p.nk, kBK);
     const int64_t last = t.tiles % pairs;
     int64_t split = 1, cut = 0;  // slices, and how many tiles (the last ones) have them
@@ -806,10 +746,8 @@ int launch_product_tc(const CallContext& c, const Product& p, const TcPlan& t, i
     q.split_from = static_cast<int32_t>(t.whole);
     q.a_z = p.rows_on_k ? 1 : p.groups;
     q.b_z = 1;
-    q.list = p.rows_on_k ? p.a.list : p.b.list;
-    q.top = p.rows_on_k ? p.a.top : p.b.top;
-    q.src = static_cast<const bf16*>(p.rows_on_k ? p.a.ptr : p.b.ptr);
-    q.src_ld = p.rows_on_k ? p.a.ld : p.b.ld;
+    q.list = p.b.list;
+    q.top = p.b.top;
     q.a_rows = static_cast<int32_t>(p.a.rows);
     q.b_rows = static_cast<int32_t>(p.b.rows);
     q.a_oob = static_cast<int32_t>(p.a.rows * parts);
@@ -852,24 +790,23 @@ int launch_product_tc(const CallContext& c, const Product& p, const TcPlan& t, i
         const bool ragged = p.rows_on_k && p.offsets;  // lists may end inside a block
         if (ragged) {
             if ((rc = call_encode_bf16(&m[2], p.a.ptr, cols_a, p.a.rows * parts, p.a.ld, 0, 0, kBK, 1))) return rc;
+        }
+        if (ragged || q.list) {
             if ((rc = call_encode_bf16(&m[3], p.b.ptr, cols_b, p.b.rows * parts, p.b.ld, 0, 0, kBK, 1))) return rc;
         }
     }
     const int64_t units = t.whole + (t.tiles - t.whole) * t.split;
     cudaError_t e;
-    auto with_bn = [&](auto f32, auto gather) {
-        constexpr bool F = decltype(f32)::value, G = decltype(gather)::value;
+    auto with_bn = [&](auto f32) {
+        constexpr bool F = decltype(f32)::value;
         switch (t.bn) {
-            case 32: return launch<32, F, G>(m, q, units, after_previous, c.sms, st);
-            case 64: return launch<64, F, G>(m, q, units, after_previous, c.sms, st);
-            case 128: return launch<128, F, G>(m, q, units, after_previous, c.sms, st);
-            default: return launch<256, F, G>(m, q, units, after_previous, c.sms, st);
+            case 32: return launch<32, F>(m, q, units, after_previous, c.sms, st);
+            case 64: return launch<64, F>(m, q, units, after_previous, c.sms, st);
+            case 128: return launch<128, F>(m, q, units, after_previous, c.sms, st);
+            default: return launch<256, F>(m, q, units, after_previous, c.sms, st);
         }
     };
-    if (parts == 3)
-        e = with_bn(std::true_type(), std::false_type());
-    else
-        e = q.list ? with_bn(std::false_type(), std::true_type()) : with_bn(std::false_type(), std::false_type());
+    e = parts == 3 ? with_bn(std::true_type()) : with_bn(std::false_type());
     if (e != cudaSuccess) return call_fail_cuda(e, "tensor-core layer product");
     *launches += 1;
     return 0;

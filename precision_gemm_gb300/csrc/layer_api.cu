@@ -92,7 +92,7 @@ int with_workspace(const CallContext& c, cudaStream_t st, F body) {
 // read in place; others, and float32, are packed into bfloat16 parts.  Listed rows are
 // copied together unless the kernel gathers them.
 int prepare(const CallContext& c, int dtype, Operand& o, int groups, int64_t cols, int64_t listed, bool gather,
-            Arena& a, bool after_previous, cudaStream_t st, int* launches) {
+            Arena& a, cudaStream_t st, int* launches) {
     if (o.parts) return 0;
     const bool in_place = dtype == SGEMM_BF16 && (o.list == nullptr || gather) && (reinterpret_cast<uintptr_t>(o.ptr) & 15) == 0 && o.ld % 8 == 0 &&
                           (groups == 1 || o.stride % 8 == 0);
@@ -105,7 +105,7 @@ int prepare(const CallContext& c, int dtype, Operand& o, int groups, int64_t col
     bf16* dst = static_cast<bf16*>(a.take(static_cast<size_t>(o.parts) * per * groups * ldd * 2));
     if (!a.dry()) {
         const cudaError_t e = launch_pack(dtype, o.ptr, o.ld, o.stride, groups, per, cols, o.list, o.top, o.rows, dst,
-                                          ldd, c.sms, after_previous, st);
+                                          ldd, c.sms, st);
         if (e != cudaSuccess) return call_fail_cuda(e, "operand packing");
         ++*launches;
     }
@@ -134,7 +134,7 @@ int product(const CallContext& c, Product p, Arena& a, cudaStream_t st) {
     int launches = 0;
     if (few_rows(p)) {
         if (a.dry()) return 0;
-        const cudaError_t e = launch_product_rows(p, c.sms, false, st);
+        const cudaError_t e = launch_product_rows(p, c.sms, st);
         if (e != cudaSuccess) return call_fail_cuda(e, "layer product of few rows");
         call_count(1);
         return 0;
@@ -143,13 +143,13 @@ int product(const CallContext& c, Product p, Arena& a, cudaStream_t st) {
     if (p.nk > 0) {
         const int64_t cols_a = p.a.k_contiguous ? p.nk : p.ni, cols_b = p.b.k_contiguous ? p.nk : p.nj;
         const int64_t rows_in_lists = p.rows_on_k ? p.nk : p.nj;
-        PG_CHECK(prepare(c, p.dtype, p.a, p.rows_on_k ? 1 : p.groups, cols_a, rows_in_lists, false, a, false,
-                         st, &launches));
-        PG_CHECK(prepare(c, p.dtype, p.b, 1, cols_b, rows_in_lists, t.gather, a, launches > 0, st, &launches));
+        PG_CHECK(prepare(c, p.dtype, p.a, p.rows_on_k ? 1 : p.groups, cols_a, rows_in_lists, false, a, st,
+                         &launches));
+        PG_CHECK(prepare(c, p.dtype, p.b, 1, cols_b, rows_in_lists, t.gather, a, st, &launches));
     }
     void* ws = a.take(t.part_bytes + t.count_bytes);
     if (!a.dry()) {
-        PG_CHECK(launch_product_tc(c, p, t, p.dtype == SGEMM_F32 ? 3 : 1, ws, launches > 0, st, &launches));
+        PG_CHECK(launch_product_tc(c, p, t, p.dtype == SGEMM_F32 ? 3 : 1, ws, st, &launches));
         call_count(launches);
     }
     return 0;

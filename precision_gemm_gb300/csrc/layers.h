@@ -253,18 +253,24 @@ struct Product {
     bool out_f32;            // out is FP32 whatever dtype (no residual, no preact)
 };
 
-// ---- launchers -----------------------------------------------------------------------
+// ---- launchers ----
+//
+// Every kernel of the layer calls waits for the kernel before it (pdl_wait) before it
+// touches global memory, so each is launched as a programmatic dependent of whatever
+// precedes it on the stream, the caller's kernels included, and its launch latency
+// hides behind that kernel's end.
+// -----------------------------------------------------------------------
 
 // Forward products of few rows (b's rows along k, out of the call's dtype): one pass
 // over the weights per 16 rows of a group.
-cudaError_t launch_product_rows(const Product& p, int num_sms, bool after_previous, cudaStream_t st);
+cudaError_t launch_product_rows(const Product& p, int num_sms, cudaStream_t st);
 
 // Rows (list[r] / top of src_rows, or `groups` matrices of per_group rows, `stride`
 // apart) as packed bfloat16 parts of leading dimension ldd (a multiple of 8), part
 // after part: one for bfloat16, three for float32.
 cudaError_t launch_pack(int dtype, const void* src, int64_t ld, int64_t stride, int64_t groups, int64_t per_group,
                         int64_t cols, const int32_t* list, int top, int64_t src_rows, bf16* dst, int64_t ldd,
-                        int num_sms, bool after_previous, cudaStream_t st);
+                        int num_sms, cudaStream_t st);
 
 // Tensor-core products: tile width, tiles (an upper bound for grouped rows), K slices,
 // and the workspace of the slices' blocks and counters.
@@ -276,8 +282,8 @@ struct TcPlan {
     size_t part_bytes, count_bytes;
 };
 TcPlan plan_tc(const Product& p, int num_sms, int force_bn, int force_split);
-int launch_product_tc(const CallContext& c, const Product& p, const TcPlan& t, int parts, void* ws,
-                      bool after_previous, cudaStream_t st, int* launches);
+int launch_product_tc(const CallContext& c, const Product& p, const TcPlan& t, int parts, void* ws, cudaStream_t st,
+                      int* launches);
 
 // dz = dy * act'(z) as bfloat16 parts (one for bfloat16, three for float32, rows * lddz
 // apart; may be null), and per group the column sums of dz before rounding, into dbias

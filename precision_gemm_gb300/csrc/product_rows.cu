@@ -58,6 +58,7 @@ __global__ void __launch_bounds__(32 * kWarps, B) product_rows_kernel(const Rows
     __shared__ float sums[kWarps][F * M];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int g = blockIdx.y, rows = static_cast<int>(p.nj);
+    pdl_trigger();
     pdl_wait();
     if (g == p.groups) {  // the rows of no expert
         const int64_t used = min(max(p.offsets[p.groups], 0), rows);
@@ -154,7 +155,7 @@ __global__ void __launch_bounds__(32 * kWarps, B) product_rows_kernel(const Rows
 }
 
 template <typename T, bool VEC, int M, int F, int U, int B>
-cudaError_t run(const Product& p, int num_sms, bool after_previous, cudaStream_t st) {
+cudaError_t run(const Product& p, int num_sms, cudaStream_t st) {
     constexpr int V = 16 / sizeof(T);
     // Enough warps to keep HBM busy: a weight row's k is shared by up to eight while there are fewer
     // than 8 B per SM and each keeps two rounds of loads.
@@ -164,35 +165,35 @@ cudaError_t run(const Product& p, int num_sms, bool after_previous, cudaStream_t
     while (q.ks < kWarps && warps * q.ks < kWarps * B * num_sms && p.nk >= 2 * q.ks * 2 * U * 32 * V) q.ks *= 2;
     const int64_t per_block = kWarps / q.ks * F;
     const dim3 grid(static_cast<unsigned>((p.ni + per_block - 1) / per_block), p.groups + (p.offsets ? 1 : 0));
-    return launch_kernel(after_previous, product_rows_kernel<T, VEC, M, F, U, B>, grid, dim3(32 * kWarps), 0, st, q);
+    return launch_kernel(true, product_rows_kernel<T, VEC, M, F, U, B>, grid, dim3(32 * kWarps), 0, st, q);
 }
 
 template <typename T, bool VEC>
-cudaError_t dispatch(const Product& p, int rows, int num_sms, bool after_previous, cudaStream_t st) {
-    if (rows <= 1) return run<T, VEC, 1, 4, 4, 2>(p, num_sms, after_previous, st);
-    if (rows <= 2) return run<T, VEC, 2, 4, 4, 2>(p, num_sms, after_previous, st);
-    if (rows <= 4) return run<T, VEC, 4, 4, 2, 2>(p, num_sms, after_previous, st);
-    if (rows <= 8) return run<T, VEC, 8, 4, 1, 2>(p, num_sms, after_previous, st);
-    return run<T, VEC, 16, 4, 1, 2>(p, num_sms, after_previous, st);
+cudaError_t dispatch(const Product& p, int rows, int num_sms, cudaStream_t st) {
+    if (rows <= 1) return run<T, VEC, 1, 4, 4, 2>(p, num_sms, st);
+    if (rows <= 2) return run<T, VEC, 2, 4, 4, 2>(p, num_sms, st);
+    if (rows <= 4) return run<T, VEC, 4, 4, 2, 2>(p, num_sms, st);
+    if (rows <= 8) return run<T, VEC, 8, 4, 1, 2>(p, num_sms, st);
+    return run<T, VEC, 16, 4, 1, 2>(p, num_sms, st);
 }
 
 template <typename T>
-cudaError_t launch(const Product& p, int rows, int num_sms, bool after_previous, cudaStream_t st) {
+cudaError_t launch(const Product& p, int rows, int num_sms, cudaStream_t st) {
     const bool vec = rows_aligned<T>(p.a.ptr, p.a.ld) && p.a.stride * sizeof(T) % 16 == 0 &&
                      rows_aligned<T>(p.b.ptr, p.b.ld);
-    return vec ? dispatch<T, true>(p, rows, num_sms, after_previous, st)
-               : dispatch<T, false>(p, rows, num_sms, after_previous, st);
+    return vec ? dispatch<T, true>(p, rows, num_sms, st)
+               : dispatch<T, false>(p, rows, num_sms, st);
 }
 
 }  // namespace
 
-cudaError_t launch_product_rows(const Product& p, int num_sms, bool after_previous, cudaStream_t st) {
+cudaError_t launch_product_rows(const Product& p, int num_sms, cudaStream_t st) {
     // Rows taken together: a dense call's; of experts twice their average, since lists differ and a
     // longer one takes another pass over its weights.
     const int64_t active = std::max<int64_t>(1, std::min<int64_t>(p.groups, p.nj));
     const int rows = static_cast<int>((p.nj + active - 1) / active) * (p.groups > 1 ? 2 : 1);
-    return p.dtype == SGEMM_F32 ? launch<float>(p, rows, num_sms, after_previous, st)
-                                : launch<bf16>(p, rows, num_sms, after_previous, st);
+    return p.dtype == SGEMM_F32 ? launch<float>(p, rows, num_sms, st)
+                                : launch<bf16>(p, rows, num_sms, st);
 }
 
 }  // namespace pg

@@ -275,17 +275,48 @@ class ExpertPlan:
     """The experts' row lists (int32 tensors): counts (experts), offsets (experts + 1),
     rows (tokens * top: the pair token * top + choice of each row, -1 for rows of no
     expert) and slots (tokens, top: the row of each pair, -1 where its id names no
-    expert)."""
+    expert).  expert_plan makes one; one can also be made of four such tensors."""
 
-    __slots__ = ("counts", "offsets", "rows", "slots")
+    __slots__ = ("tokens", "top", "experts", "index", "_store", "_lists", "_addresses")
 
     def __init__(self, counts, offsets, rows, slots):
-        self.counts, self.offsets, self.rows, self.slots = counts, offsets, rows, slots
+        tokens, top = _shape(slots, "slots", 2)
+        if not slots.is_cuda:
+            raise ValueError("slots: expected a CUDA tensor, got one on %s" % slots.device)
+        experts, index = _shape(counts, "counts", 1)[0], slots.get_device()
+        for x, name, shape in ((counts, "counts", (experts,)), (offsets, "offsets", (experts + 1,)),
+                               (rows, "rows", (tokens * top,)), (slots, "slots", (tokens, top))):
+            _packed(x, name, shape, torch.int32, index)
+        self.tokens, self.top, self.experts, self.index = tokens, top, experts, index
+        self._store, self._lists = None, (counts, offsets, rows, slots)
+        self._addresses = tuple(x.data_ptr() for x in self._lists)
+
+    @classmethod
+    def _of(cls, store, address, tokens, top, experts, index):
+        """The lists one after another in `store`; their tensors are made when asked for."""
+        self = cls.__new__(cls)
+        self.tokens, self.top, self.experts, self.index = tokens, top, experts, index
+        self._store, self._lists = store, None
+        rows = address + 4 * (2 * experts + 1)
+        self._addresses = (address, address + 4 * experts, rows, rows + 4 * tokens * top)
+        return self
+
+    def _list(self, i):
+        if self._lists is None:
+            e, r = self.experts, self.tokens * self.top
+            counts, offsets, rows, slots = self._store.split_with_sizes((e, e + 1, r, r))
+            self._lists = (counts, offsets, rows, slots.view(self.tokens, self.top))
+        return self._lists[i]
+
+    counts = property(lambda self: self._list(0))
+    offsets = property(lambda self: self._list(1))
+    rows = property(lambda self: self._list(2))
+    slots = property(lambda self: self._list(3))
 
 
 def expert_plan(ids, experts, stream=None):
     """The row lists of ids (tokens, top): an expert's rows hold its pairs in order.
-    The four lists are views of one allocation."""
+    The four lists lie in one allocation."""
     if stream is not None:
         return _on(stream, expert_plan, ids, experts)
     lib = load_library()
@@ -297,25 +328,23 @@ def expert_plan(ids, experts, stream=None):
     experts = int(experts)
     if experts < 1:
         raise ValueError("experts: %d is less than 1" % experts)
-    r = t * top
-    counts, offsets, rows, slots = _empty((2 * experts + 1 + 2 * r,), dtype=torch.int32, device=ids.device).split_with_sizes(
-        (experts, experts + 1, r, r))
-    rc = lib.sgemm_expert_plan(t, top, experts, ids.data_ptr(), counts.data_ptr(), offsets.data_ptr(),
-                               rows.data_ptr(), slots.data_ptr(), _raw_stream(index))
+    store = _empty((2 * experts + 1 + 2 * t * top,), dtype=torch.int32, device=ids.device)
+    plan = ExpertPlan._of(store, store.data_ptr(), t, top, experts, index)
+    rc = lib.sgemm_expert_plan(t, top, experts, ids.data_ptr(), *plan._addresses, _raw_stream(index))
     if rc:
         _check(rc, lib)
-    return ExpertPlan(counts, offsets, rows, slots.view(t, top))
+    return plan
 
 
 def _plan_sizes(plan, experts, index):
+    """tokens and top of a plan of the call's device, for `experts` experts (any when None)."""
     if not isinstance(plan, ExpertPlan):
         raise ValueError("plan: expected an ExpertPlan, got %r" % type(plan))
-    t, top = _shape(plan.slots, "plan.slots", 2)
-    _packed(plan.slots, "plan.slots", (t, top), torch.int32, index)
-    _packed(plan.rows, "plan.rows", (t * top,), torch.int32, index)
-    if experts is not None:
-        _packed(plan.offsets, "plan.offsets", (experts + 1,), torch.int32, index)
-    return t, top
+    if plan.index != index:
+        raise ValueError("plan: its lists are on cuda:%d, the call is on cuda:%d" % (plan.index, index))
+    if experts is not None and plan.experts != experts:
+        raise ValueError("plan: made for %d experts, the weights are of %d" % (plan.experts, experts))
+    return plan.tokens, plan.top
 
 
 def _expert_weights(w, dtype, index):
@@ -356,7 +385,7 @@ def expert_linear(x, w, plan, bias=None, act="none", gather=False, out=None, pre
     elif preact is not None and preact is not False:
         z, ldz = preact, _matrix(preact, "preact", rows, n, dtype, index)
     rc = lib.sgemm_expert_linear(code, t, top, e, n, k, 1 if gather else 0, x.data_ptr(), ldx, w.data_ptr(), ldw,
-                                 stride, _ptr(bias), _act(act), plan.offsets.data_ptr(), plan.rows.data_ptr(),
+                                 stride, _ptr(bias), _act(act), plan._addresses[1], plan._addresses[2],
                                  y.data_ptr(), ldy, _ptr(z), ldz, _raw_stream(index))
     if rc:
         _check(rc, lib)
@@ -390,8 +419,7 @@ def expert_linear_backward(dy, x, w, plan, act="none", preact=None, bias=True, g
     db = _empty((e, n), dtype=dtype, device=device) if bias else None
     rc = lib.sgemm_expert_linear_backward(
         code, t, top, e, n, k, 1 if gather else 0, dy.data_ptr(), lddy, x.data_ptr(), ldx, w.data_ptr(), ldw, stride,
-        kind, _ptr(preact), ldz, plan.offsets.data_ptr(), plan.rows.data_ptr(), plan.slots.data_ptr(), _ptr(dx),
-        k or 1, _ptr(dw), k or 1, n * (k or 1), _ptr(db), _raw_stream(index))
+        kind, _ptr(preact), ldz, *plan._addresses[1:], _ptr(dx), k or 1, _ptr(dw), k or 1, n * (k or 1), _ptr(db), _raw_stream(index))
     if rc:
         _check(rc, lib)
     return dx, dw, db
@@ -415,7 +443,7 @@ def expert_combine(rows, plan, weights=None, residual=None, out=None, stream=Non
         y, ldy = _empty((t, n), dtype=dtype, device=rows.device), n or 1
     else:
         y, ldy = out, _matrix(out, "out", t, n, dtype, index)
-    rc = lib.sgemm_expert_combine(code, t, top, n, rows.data_ptr(), ldx, plan.slots.data_ptr(), _ptr(weights),
+    rc = lib.sgemm_expert_combine(code, t, top, n, rows.data_ptr(), ldx, plan._addresses[3], _ptr(weights),
                                   _ptr(residual), ldr, y.data_ptr(), ldy, _raw_stream(index))
     if rc:
         _check(rc, lib)
@@ -439,7 +467,7 @@ def expert_combine_backward(dy, rows, plan, weights=None, need_dweights=True, st
     drows = _empty((t * top, n), dtype=dtype, device=device)
     dweights = _empty((t, top), dtype=torch.float32, device=device) if need_dweights else None
     rc = lib.sgemm_expert_combine_backward(code, t, top, n, dy.data_ptr(), lddy, rows.data_ptr(), ldx,
-                                           plan.rows.data_ptr(), plan.slots.data_ptr(), _ptr(weights),
+                                           plan._addresses[2], plan._addresses[3], _ptr(weights),
                                            drows.data_ptr(), n or 1, _ptr(dweights), _raw_stream(index))
     if rc:
         _check(rc, lib)

@@ -162,9 +162,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t acc_empty0 = smem_u32(bars + 2 * S + 2);
     const uint32_t mma_done = smem_u32(bars + 2 * S + 4);
 
-    const int warp = threadIdx.x >> 5;
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);  // known to be uniform
     const int lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_rank();
+    const uint32_t rank = __shfl_sync(0xffffffffu, cluster_rank(), 0);
     const bool leader = rank == 0;
     const int pair = blockIdx.x >> 1;
     const int pairs = gridDim.x >> 1;
@@ -225,9 +225,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     tc_fence_before_sync();
     __syncthreads();
-    cluster_sync_all();  // both CTAs' barriers and TMEM exist before any cross-CTA traffic
+    cluster_sync_all();  // every CTA's barriers and TMEM exist before any cross-CTA traffic
     tc_fence_after_sync();
-    const uint32_t tmem = *tmem_holder;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_holder, 0);
     const int tiles_j = p.rows_on_k ? p.tiles_j * p.groups : pre[p.groups];
     const int tiles = tiles_j * p.tiles_i;
     const int whole = p.split > 1 ? min(p.split_from, tiles) : tiles;  // tiles of one slice, first
@@ -284,12 +284,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             int it = 0, slot_i = 0;
             uint32_t phase = 1;
             bool ok = true;
-            // LISTED: some rows are named one by one (gathered rows of B, or lists that may end inside a
-            // k block), which takes the whole warp; otherwise lane 0 alone runs this.
+            // The warp runs as one, an elected lane issues.  LISTED: some rows are named one by one
+            // (gathered rows of B, or lists that may end inside a k block), four by each lane.
             auto load = [&](auto listed) {
                 constexpr bool LISTED = decltype(listed)::value;
                 for (int u = pair; u < units && ok; u += pairs) {
-                    const Unit x = unit_of(u);
+                    Unit x = unit_of(u);
+                    // known to be uniform from here on: operands of the copies
+                    x.i0 = __shfl_sync(0xffffffffu, x.i0, 0);
+                    x.j0 = __shfl_sync(0xffffffffu, x.j0, 0);
+                    x.g = __shfl_sync(0xffffffffu, x.g, 0);
+                    x.k0 = __shfl_sync(0xffffffffu, x.k0, 0);
+                    x.k_end = __shfl_sync(0xffffffffu, x.k_end, 0);
+                    x.kb0 = __shfl_sync(0xffffffffu, x.kb0, 0);
+                    x.nkb = __shfl_sync(0xffffffffu, x.nkb, 0);
                     const int ia = x.i0 + kBI * static_cast<int>(rank);
                     const int jb = x.j0 + C::BNH * static_cast<int>(rank);
                     const bool gather = LISTED && p.list != nullptr;
@@ -310,8 +318,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             const int z_a = p.rows_on_k ? pa * p.a_z : pa * p.a_z + x.g;
                             const int z_b = pb * p.b_z;
                             for (int kb = c0; kb < c1; ++kb, ++it) {
-                                ok = mbar_wait_bounded(empty0 + 8 * slot_i, phase, p.timeout_ns, abort_flag);
-                                if (LISTED) ok = __all_sync(0xffffffffu, ok);
+                                ok = __all_sync(0xffffffffu, mbar_wait_bounded(empty0 + 8 * slot_i, phase, p.timeout_ns,
+                                                                               abort_flag));
                                 if (!ok) {
                                     if (lane == 0) raise_abort(abort_flag, p.status);
                                     break;
@@ -339,24 +347,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                     if (h < C::BNH / 64)
                                         tma_gather4_pair(slot_b + 8192 * h + 512 * (lane & 15), &tmBg, jb + 64 * h, yb,
                                                          bar);
-                                } else if (lane == 0) {
+                                } else {
                                     if (p.a_mn) {
-                                        tma_load_3d_pair(slot, &tmA, ia, kc, z_a, bar);
-                                        tma_load_3d_pair(slot + 8192, &tmA, ia + 64, kc, z_a, bar);
+                                        tma_load_3d_pair_warp(slot, &tmA, ia, kc, z_a, bar);
+                                        tma_load_3d_pair_warp(slot + 8192, &tmA, ia + 64, kc, z_a, bar);
                                     } else {
-                                        tma_load_3d_pair(slot, &tmA, kc, ia, z_a, bar);
+                                        tma_load_3d_pair_warp(slot, &tmA, kc, ia, z_a, bar);
                                     }
                                     if (p.b_mn) {
 #pragma unroll
                                         for (int h = 0; h < C::BNH / 64; ++h)
-                                            tma_load_3d_pair(slot_b + 8192 * h, &tmB, jb + 64 * h, kc, z_b, bar);
+                                            tma_load_3d_pair_warp(slot_b + 8192 * h, &tmB, jb + 64 * h, kc, z_b, bar);
                                     } else if (!gather) {
-                                        tma_load_3d_pair(slot_b, &tmB, kc, jb, z_b, bar);
+                                        tma_load_3d_pair_warp(slot_b, &tmB, kc, jb, z_b, bar);
                                     }
                                 }
                                 if (gather && lane < C::BNH / 4)
                                     tma_gather4_pair(slot_b + 512 * lane, &tmBg, kc, rows_b, bar);
-                                if (LISTED) __syncwarp();
                                 if (++slot_i == S) {
                                     slot_i = 0;
                                     phase ^= 1;
@@ -368,9 +375,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             };
             if (p.list != nullptr || (p.rows_on_k && p.offsets != nullptr)) {
                 load(std::true_type());
-            } else if (lane == 0) {
-                prefetch_tmap(&tmA);
-                prefetch_tmap(&tmB);
+            } else {
                 load(std::false_type());
             }
             if (lane == 0) pdl_trigger();
@@ -384,7 +389,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp == 1) {
         // ---------------- MMA issuer (CTA 0 of the pair) ----------------
-        if (leader && lane == 0) {
+        // The warp runs as one: what the MMAs are given is uniform, and one lane issues.
+        if (leader) {
             const uint32_t idesc = idesc_bf16(2 * kBI, BN, p.a_mn != 0, p.b_mn != 0);
             // K-major: 8-row atoms 1 KiB apart, a k-step of 16 is 32 bytes further along the rows.
             // MN-major: 64-column groups 8 KiB apart, 8-k atoms 1 KiB apart, a k-step 2 KiB further.
@@ -396,42 +402,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             uint32_t phase = 0;
             bool ok = true;
             for (int u = pair; u < units && ok; u += pairs) {
-                const Unit x = unit_of(u);
-                for (int c0 = 0; c0 < x.nkb && ok; c0 += p.chunk_kb, ++chunk) {
-                    const int steps = (min(c0 + p.chunk_kb, x.nkb) - c0) * p.segs;
+                const int nkb = __shfl_sync(0xffffffffu, unit_of(u).nkb, 0);
+                for (int c0 = 0; c0 < nkb && ok; c0 += p.chunk_kb, ++chunk) {
+                    const int steps = (min(c0 + p.chunk_kb, nkb) - c0) * p.segs;
                     const int buf = chunk & 1;
-                    if (!mbar_wait_bounded(acc_empty0 + 8 * buf, ((chunk >> 1) & 1) ^ 1, p.timeout_ns, abort_flag)) {
-                        raise_abort(abort_flag, p.status);
-                        ok = false;
-                        break;
-                    }
+                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(acc_empty0 + 8 * buf, ((chunk >> 1) & 1) ^ 1,
+                                                                   p.timeout_ns, abort_flag));
+                    if (!ok) break;
                     tc_fence_after_sync();
                     const uint32_t d = tmem + buf * BN;
                     uint32_t accumulate = 0;
                     for (int kb = 0; kb < steps; ++kb) {
-                        if (!mbar_wait_bounded(full0 + 8 * slot_i, phase, p.timeout_ns, abort_flag)) {
-                            raise_abort(abort_flag, p.status);
-                            ok = false;
-                            break;
-                        }
+                        ok = __all_sync(0xffffffffu,
+                                        mbar_wait_bounded(full0 + 8 * slot_i, phase, p.timeout_ns, abort_flag));
+                        if (!ok) break;
                         tc_fence_after_sync();
                         const uint32_t o = static_cast<uint32_t>(slot_i * C::STAGE_BYTES) >> 4;
 #pragma unroll
                         for (int kk = 0; kk < kBK / 16; ++kk) {
-                            mma_bf16_pair(d, a_desc0 + (o + kk * a_step), b_desc0 + (o + kk * b_step), idesc,
-                                          accumulate);
+                            mma_bf16_pair_warp(d, a_desc0 + (o + kk * a_step), b_desc0 + (o + kk * b_step), idesc,
+                                               accumulate);
                             accumulate = 1;
                         }
-                        mma_commit_pair(empty0 + 8 * slot_i);
+                        mma_commit_pair_warp(empty0 + 8 * slot_i);
                         if (++slot_i == S) {
                             slot_i = 0;
                             phase ^= 1;
                         }
                     }
-                    if (ok) mma_commit_pair(acc_full0 + 8 * buf);
+                    if (ok) mma_commit_pair_warp(acc_full0 + 8 * buf);
                 }
             }
-            mma_commit_pair_local(mma_done);  // every MMA issued here has completed
+            if (!ok && lane == 0) raise_abort(abort_flag, p.status);
+            mma_commit_pair_local_warp(mma_done);  // every MMA issued here has completed
             mbar_wait_bounded(mma_done, 0, p.timeout_ns, nullptr);
         }
         __syncwarp();
@@ -577,14 +580,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         float f[kCols];
 #pragma unroll
                         for (int t = 0; t < kCols; ++t) f[t] = 0.0f;
-#pragma unroll 4
-                        for (int s = 0; s < p.split; ++s) {
-                            const float* src = first + static_cast<int64_t>(s) * (2 * kBI * BN) + kCols * c * (2 * kBI);
-                            float b[kCols];
+                        for (int s0 = 0; s0 < p.split; s0 += 4) {  // four slices' loads in flight
+                            float b[4][kCols];
 #pragma unroll
-                            for (int t = 0; t < kCols; ++t) b[t] = __ldcg(src + t * (2 * kBI));
+                            for (int s = 0; s < 4; ++s) {
+                                const float* src =
+                                    first + static_cast<int64_t>(s0 + s) * (2 * kBI * BN) + kCols * c * (2 * kBI);
 #pragma unroll
-                            for (int t = 0; t < kCols; ++t) f[t] += b[t];
+                                for (int t = 0; t < kCols; ++t)
+                                    b[s][t] = s0 + s < p.split ? __ldcg(src + t * (2 * kBI)) : 0.0f;
+                            }
+#pragma unroll
+                            for (int s = 0; s < 4; ++s)
+#pragma unroll
+                                for (int t = 0; t < kCols; ++t) f[t] += b[s][t];
                         }
                         finish_chunk(x, f, c);
                     }
@@ -678,9 +687,32 @@ cudaError_t launch(const CUtensorMap (&m)[4], const Params& p, int64_t units, bo
     static std::atomic<uint64_t> smem_set{0};
     cudaError_t e = set_smem_limit_once(smem_set, reinterpret_cast<const void*>(kern), static_cast<int>(C::SMEM));
     if (e != cudaSuccess) return e;
-    const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(units, num_sms / 2));
-    return launch_kernel(after_previous, kern, dim3(static_cast<unsigned>(2 * pairs)),
-                         dim3(kThreads), C::SMEM, st, m[0], m[1], m[2], m[3], p);
+    // Clusters that are resident together (they must fit inside GPCs), asked once per device; a
+    // persistent grid beyond them would run a second time around.
+    static std::atomic<int> resident[64];
+    int dev = 0;
+    cudaGetDevice(&dev);
+    int most = dev >= 0 && dev < 64 ? resident[dev].load() : 0;
+    if (most <= 0) {
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        cfg.gridDim = dim3(2, 1, 1);
+        cfg.blockDim = dim3(kThreads, 1, 1);
+        cfg.dynamicSmemBytes = C::SMEM;
+        if (cudaOccupancyMaxActiveClusters(&most, kern, &cfg) != cudaSuccess || most <= 0) {
+            cudaGetLastError();
+            most = num_sms / 2;
+        }
+        if (dev >= 0 && dev < 64) resident[dev] = most;
+    }
+    const int64_t clusters = std::max<int64_t>(1, std::min<int64_t>(units, most));
+    return launch_kernel(after_previous, kern, dim3(static_cast<unsigned>(2 * clusters)), dim3(kThreads), C::SMEM,
+                         st, m[0], m[1], m[2], m[3], p);
 }
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -712,17 +744,16 @@ cudaError_t launch_pack(int dtype, const void* src, int64_t ld, int64_t stride, 
 // lengths are known on the device alone.
 TcPlan plan_tc(const Product& p, int num_sms, int force_bn, int force_split) {
     TcPlan t{};
-    const int pairs = std::max(num_sms / 2, 1);
     const int64_t tiles_i = cdiv(p.ni, 2 * kBI);
     if (p.rows_on_k) {
         t.bn = p.nj <= 128 ? 128 : 256;
-        t.tiles = tiles_i * cdiv(p.nj, t.bn) * p.groups;
     } else {
         const int64_t lists = std::max<int64_t>(1, std::min<int64_t>(p.groups, p.nj));
         const int64_t rows = cdiv(p.nj, lists);  // of a group, on average
         t.bn = rows <= 32 ? 32 : (rows <= 64 ? 64 : (rows <= 128 ? 128 : 256));
     }
     if (force_bn == 64 || force_bn == 128 || force_bn == 256) t.bn = p.b.k_contiguous ? force_bn : std::max(force_bn, 128);
+    const int pairs = std::max(num_sms / 2, 1);
     if (p.rows_on_k)
         t.tiles = tiles_i * cdiv(p.nj, t.bn) * p.groups;
     else

@@ -279,6 +279,7 @@ struct TcPlan {
     bool gather;            // listed rows of b are gathered by the kernel
     int64_t tiles, whole;  // the first `whole` tiles have one slice
     int split, split_kb;
+    bool halved;            // the others are halved along j instead of cut along k
     size_t part_bytes, count_bytes;
 };
 TcPlan plan_tc(const Product& p, int num_sms, int force_bn, int force_split);

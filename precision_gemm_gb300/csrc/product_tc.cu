@@ -75,7 +75,8 @@ struct Params {
     int32_t a_mn, b_mn;
     int32_t segs;          // products of parts: 1 (bfloat16) or 6 (float32)
     int32_t chunk_kb;      // k blocks per accumulation chunk
-    int32_t split, split_kb;  // K slices of the tiles from split_from on (1: none)
+    int32_t split, split_kb;  // K slices of the tiles from split_from on (1: none) ...
+    int32_t halved;           // ... or their two halves along j, each a unit of its own
     int32_t split_from;
     int32_t a_z, b_z;      // third coordinates per part
     const int32_t* list;   // rows of B gathered: row r is list[r] / top (null: not gathered)
@@ -230,21 +231,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_holder, 0);
     const int tiles_j = p.rows_on_k ? p.tiles_j * p.groups : pre[p.groups];
     const int tiles = tiles_j * p.tiles_i;
-    const int whole = p.split > 1 ? min(p.split_from, tiles) : tiles;  // tiles of one slice, first
-    const int units = whole + (tiles - whole) * p.split;
+    const int cuts = p.halved ? 2 : p.split;
+    const int whole = cuts > 1 ? min(p.split_from, tiles) : tiles;  // tiles of one unit, first
+    const int units = whole + (tiles - whole) * cuts;
 
     struct Unit {
-        int tile, slice, g;  // tile counted from `whole` on, -1 for a tile of one slice
-        int i0, j0, j_end;   // j_end: of the group
+        int tile, slice, g;  // tile counted from `whole` on, -1 for a unit of one slice
+        int i0, j0, j_end;   // j_end: of the group (of the half)
+        int n;               // width of its MMAs
         int k0, k_end;       // rows_on_k: the group's rows; else 0 and nk
         int kb0, nkb;        // this slice's k blocks
     };
     auto unit_of = [&](int u) {
         Unit x;
         // the slices of a tile are neighbours, so that they run at one time
-        x.tile = u < whole ? -1 : (u - whole) / p.split;
-        x.slice = u < whole ? 0 : (u - whole) % p.split;
-        const int tile = u < whole ? u : whole + x.tile;
+        const int cut = u < whole ? 0 : (u - whole) % cuts;
+        const int tile = u < whole ? u : whole + (u - whole) / cuts;
+        x.tile = u < whole || p.halved ? -1 : tile - whole;
+        x.slice = p.halved ? 0 : cut;
         int tj, ti;
         if (p.rows_on_k) {
             const int per = p.tiles_j * p.tiles_i;
@@ -271,9 +275,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             x.k_end = p.nk;
         }
         x.i0 = ti * (2 * kBI);
+        if (p.halved && u >= whole) {
+            x.j0 += cut * (BN / 2);
+            x.j_end = min(x.j_end, x.j0 + BN / 2);
+        }
+        // the narrowest MMAs that hold the unit's columns (B read in groups of 64 columns: 128 at least)
+        x.n = BN;
+        while (x.n > (p.b_mn ? 128 : 32) && x.j_end - x.j0 <= x.n / 2) x.n /= 2;
         const int kb_total = (x.k_end - x.k0 + kBK - 1) / kBK;
         x.kb0 = x.tile < 0 ? 0 : x.slice * p.split_kb;
         x.nkb = x.tile < 0 ? kb_total : max(min(x.kb0 + p.split_kb, kb_total) - x.kb0, 0);
+        if (x.j0 >= x.j_end) x.nkb = 0;  // a half past the end
         return x;
     };
 
@@ -298,8 +310,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     x.k_end = __shfl_sync(0xffffffffu, x.k_end, 0);
                     x.kb0 = __shfl_sync(0xffffffffu, x.kb0, 0);
                     x.nkb = __shfl_sync(0xffffffffu, x.nkb, 0);
+                    x.n = __shfl_sync(0xffffffffu, x.n, 0);
                     const int ia = x.i0 + kBI * static_cast<int>(rank);
-                    const int jb = x.j0 + C::BNH * static_cast<int>(rank);
+                    const int jb = x.j0 + x.n / 2 * static_cast<int>(rank);
                     const bool gather = LISTED && p.list != nullptr;
                     int4 rows_b = make_int4(0, 0, 0, 0);  // this lane's four gathered rows of B
                     if (gather && lane < C::BNH / 4) {
@@ -391,7 +404,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // ---------------- MMA issuer (CTA 0 of the pair) ----------------
         // The warp runs as one: what the MMAs are given is uniform, and one lane issues.
         if (leader) {
-            const uint32_t idesc = idesc_bf16(2 * kBI, BN, p.a_mn != 0, p.b_mn != 0);
             // K-major: 8-row atoms 1 KiB apart, a k-step of 16 is 32 bytes further along the rows.
             // MN-major: 64-column groups 8 KiB apart, 8-k atoms 1 KiB apart, a k-step 2 KiB further.
             const uint32_t slot0 = smem_u32(smem);
@@ -402,7 +414,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             uint32_t phase = 0;
             bool ok = true;
             for (int u = pair; u < units && ok; u += pairs) {
-                const int nkb = __shfl_sync(0xffffffffu, unit_of(u).nkb, 0);
+                const Unit x = unit_of(u);
+                const int nkb = __shfl_sync(0xffffffffu, x.nkb, 0);
+                const uint32_t idesc =
+                    idesc_bf16(2 * kBI, __shfl_sync(0xffffffffu, x.n, 0), p.a_mn != 0, p.b_mn != 0);
                 for (int c0 = 0; c0 < nkb && ok; c0 += p.chunk_kb, ++chunk) {
                     const int steps = (min(c0 + p.chunk_kb, nkb) - c0) * p.segs;
                     const int buf = chunk & 1;
@@ -758,9 +773,10 @@ TcPlan plan_tc(const Product& p, int num_sms, int force_bn, int force_split) {
         t.tiles = tiles_i * cdiv(p.nj, t.bn) * p.groups;
     else
         t.tiles = tiles_i * (cdiv(p.nj, t.bn) + (p.groups > 1 ? p.groups : 0));
-    // K slices.  Under a wave of tiles, all of them are cut so that the slices fill it.  Over
-    // a wave, those of a last wave that is at most half full are.  (Groups that share out k
-    // differ in length: not cut.)
+    // Under a wave of tiles, all are cut along k so that the slices fill it (not groups that share
+    // out k, whose lengths differ).  Over a wave, the tiles of a last wave that is at most half full
+    // are cut into halves along j, whose MMAs of N = 128 run at 0.9 of the rate (4096^3 bfloat16:
+    // cut in two along k 84.6 us, the slices' blocks written and added; halves 76.7).
     t.gather = t.bn <= 64 && !p.rows_on_k;
     const int64_t kb = cdiv(p.nk, kBK);
     const int64_t last = t.tiles % pairs;
@@ -772,15 +788,14 @@ TcPlan plan_tc(const Product& p, int num_sms, int force_bn, int force_split) {
         } else if (t.tiles < pairs) {
             split = std::min<int64_t>(pairs / t.tiles, kb / 4);
             cut = t.tiles;
-        } else if (p.groups == 1 && last > 0 && 2 * last <= pairs) {
-            split = std::min<int64_t>({pairs / last, 4, kb / 8});
-            cut = last;
         }
         split = std::max<int64_t>(1, std::min(split, kb));
     }
     t.split_kb = static_cast<int>(kb > 0 ? cdiv(kb, split) : 1);
     t.split = static_cast<int>(kb > 0 ? cdiv(kb, t.split_kb) : 1);
-    t.whole = t.split > 1 ? t.tiles - cut : t.tiles;
+    t.halved = force_split == 0 && t.split == 1 && t.bn == 256 && p.groups == 1 && t.tiles > pairs && last > 0 &&
+               2 * last <= pairs;
+    t.whole = t.split > 1 ? t.tiles - cut : (t.halved ? t.tiles - last : t.tiles);
     if (t.split > 1) {
         t.part_bytes = region(static_cast<size_t>(cut) * t.split * 2 * kBI * t.bn * 4);
         t.count_bytes = region(static_cast<size_t>(cut) * 2 * kEpiWarps * 4);
@@ -805,6 +820,7 @@ int launch_product_tc(const CallContext& c, const Product& p, const TcPlan& t, i
     q.chunk_kb = parts == 3 ? 512 / kBK : 1 << 30;
     q.split = t.split;
     q.split_kb = t.split_kb;
+    q.halved = t.halved;
     q.split_from = static_cast<int32_t>(t.whole);
     q.a_z = p.rows_on_k ? 1 : p.groups;
     q.b_z = 1;
@@ -857,7 +873,7 @@ int launch_product_tc(const CallContext& c, const Product& p, const TcPlan& t, i
             if ((rc = call_encode_bf16(&m[3], p.b.ptr, cols_b, p.b.rows * parts, p.b.ld, 0, 0, kBK, 1))) return rc;
         }
     }
-    const int64_t units = t.whole + (t.tiles - t.whole) * t.split;
+    const int64_t units = t.whole + (t.tiles - t.whole) * (t.halved ? 2 : t.split);
     cudaError_t e;
     auto with_bn = [&](auto f32) {
         constexpr bool F = decltype(f32)::value;

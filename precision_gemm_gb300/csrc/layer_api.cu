@@ -125,6 +125,7 @@ int prepare(const CallContext& c, int dtype, Operand& o, int groups, int64_t col
 // 8 rows 17.5 / 17.3; 64 experts, one row each 25 / 35, two each 58 / 50.
 bool few_rows(const Product& p) {
     if (p.rows_on_k || !p.a.k_contiguous || p.nk == 0 || p.out_f32) return false;
+    if (p.b.rows * p.b.ld >= int64_t(1) << 32) return false;  // its row offsets are 32-bit
     const int64_t lists = std::min<int64_t>(p.groups, p.nj);  // lists that have rows, at most
     return p.nj <= lists * (p.dtype == SGEMM_F32 ? 16 : (p.groups == 1 ? 4 : 1));
 }

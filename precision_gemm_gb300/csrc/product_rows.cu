@@ -78,17 +78,17 @@ __global__ void __launch_bounds__(32 * kWarps, B) product_rows_kernel(const Rows
     // this warp's steps of 32 V elements
     const int64_t steps = (p.nk + 32 * V - 1) / (32 * V);
     const int64_t s0 = steps * part / ks, s1 = steps * (part + 1) / ks;
-    const T* w[F];
-#pragma unroll
-    for (int f = 0; f < F; ++f)
-        w[f] = static_cast<const T*>(p.a.ptr) + g * p.a.stride + min(i0 + f, p.ni - 1) * p.a.ld + lane * V;
+    const bool all = i0 + F <= p.ni;  // F weight rows are there
+    const int64_t ldw = p.a.ld;
+    const T* w = static_cast<const T*>(p.a.ptr) + g * p.a.stride + min(i0, p.ni - 1) * ldw + lane * V;
     for (int j0 = first; j0 < end; j0 += M) {
-        const T* x[M];
+        const T* x = static_cast<const T*>(p.b.ptr) + lane * V;
+        uint32_t row[M];  // element offsets of the rows (the launcher keeps them under 2^32)
 #pragma unroll
         for (int m = 0; m < M; ++m) {
             const int64_t j = min(j0 + m, end - 1);
             const int64_t r = p.b.list ? max(gathered_row(p.b.list, p.b.top, j, p.b.rows), int64_t(0)) : j;
-            x[m] = static_cast<const T*>(p.b.ptr) + r * p.b.ld + lane * V;
+            row[m] = static_cast<uint32_t>(r * p.b.ld);
         }
         float acc[F][M] = {};
         auto add = [&](const uint4(&raw)[F], const uint4& xr, int m) {
@@ -103,19 +103,20 @@ __global__ void __launch_bounds__(32 * kWarps, B) product_rows_kernel(const Rows
             }
         };
         int64_t s = s0;
-        if (VEC) {
+        if (VEC && all) {
             const int64_t whole = min(s1, p.nk / (32 * V));  // steps without an end of a row
             for (; s + U <= whole; s += U) {
                 uint4 raw[U][F];
 #pragma unroll
                 for (int u = 0; u < U; ++u)
 #pragma unroll
-                    for (int f = 0; f < F; ++f) raw[u][f] = __ldcs(reinterpret_cast<const uint4*>(w[f] + (s + u) * 32 * V));
+                    for (int f = 0; f < F; ++f)
+                        raw[u][f] = __ldcs(reinterpret_cast<const uint4*>(w + f * ldw + (s + u) * 32 * V));
 #pragma unroll
                 for (int u = 0; u < U; ++u)
 #pragma unroll
                     for (int m = 0; m < M; ++m)
-                        add(raw[u], *reinterpret_cast<const uint4*>(x[m] + (s + u) * 32 * V), m);
+                        add(raw[u], *reinterpret_cast<const uint4*>(x + row[m] + (s + u) * 32 * V), m);
             }
         }
 #pragma unroll 1
@@ -123,9 +124,9 @@ __global__ void __launch_bounds__(32 * kWarps, B) product_rows_kernel(const Rows
             const int64_t c = s * 32 * V, valid = p.nk - c - lane * V;
             uint4 raw[F];
 #pragma unroll
-            for (int f = 0; f < F; ++f) raw[f] = load16(w[f] + c, VEC, valid);
+            for (int f = 0; f < F; ++f) raw[f] = load16(w + (i0 + f < p.ni ? f : 0) * ldw + c, VEC, valid);
 #pragma unroll
-            for (int m = 0; m < M; ++m) add(raw, load16(x[m] + c, VEC, valid), m);
+            for (int m = 0; m < M; ++m) add(raw, load16(x + row[m] + c, VEC, valid), m);
         }
 #pragma unroll
         for (int f = 0; f < F; ++f)
@@ -170,11 +171,21 @@ cudaError_t run(const Product& p, int num_sms, cudaStream_t st) {
 
 template <typename T, bool VEC>
 cudaError_t dispatch(const Product& p, int rows, int num_sms, cudaStream_t st) {
-    if (rows <= 1) return run<T, VEC, 1, 4, 4, 2>(p, num_sms, st);
-    if (rows <= 2) return run<T, VEC, 2, 4, 4, 2>(p, num_sms, st);
-    if (rows <= 4) return run<T, VEC, 4, 4, 2, 2>(p, num_sms, st);
-    if (rows <= 8) return run<T, VEC, 8, 4, 1, 2>(p, num_sms, st);
-    return run<T, VEC, 16, 4, 1, 2>(p, num_sms, st);
+    switch (rows) {
+        case 1: return run<T, VEC, 1, 4, 4, 2>(p, num_sms, st);
+        case 2: return run<T, VEC, 2, 4, 4, 2>(p, num_sms, st);
+        case 3: return run<T, VEC, 3, 4, 4, 2>(p, num_sms, st);
+        case 4: return run<T, VEC, 4, 4, 2, 2>(p, num_sms, st);
+        case 5: return run<T, VEC, 5, 4, 2, 2>(p, num_sms, st);
+        case 6: return run<T, VEC, 6, 4, 2, 2>(p, num_sms, st);
+        case 7:
+        case 8: return run<T, VEC, 8, 4, 2, 2>(p, num_sms, st);
+        case 9:
+        case 10:
+        case 11:
+        case 12: return run<T, VEC, 12, 4, 1, 2>(p, num_sms, st);
+        default: return run<T, VEC, 16, 4, 1, 2>(p, num_sms, st);
+    }
 }
 
 template <typename T>

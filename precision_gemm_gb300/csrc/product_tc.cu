@@ -755,50 +755,71 @@ cudaError_t launch_pack(int dtype, const void* src, int64_t ld, int64_t stride, 
                          rows_aligned<bf16>(src, ld) && stride % 8 == 0);
 }
 
-// Tile width and K slices.  Grouped rows are cut by their average length, since the
+// Tile width, K slices and the last wave, by an estimate of the kernel's time in us:
+//     waves * steps * step(bn) + end(bn) [+ kSplit]
+// with one step per k block and product of parts.  Measured at 4864 x 4096 x 4096
+// (whole waves at every width): a step of all pairs takes 0.34 us at 256 columns, 0.19
+// at 128, 0.14 at 64 (operand feed: A's 128 rows per CTA are loaded whatever the width);
+// the end is the last tile's epilogue, which no MMAs hide (most with a residual, whose
+// reads it waits for); kSplit what clearing counters, storing and adding the slices'
+// blocks took.  Against the widest tile that the rows fill and a K split under one wave:
+// 300 x 4096 x 4096 bfloat16 29.6 -> 16.2 us, 1000^3 25 -> 13, 1500 x 3000 x 777 float32
+// with residual 67 -> 56.  Grouped rows are counted by their average length, since the
 // lengths are known on the device alone.
 TcPlan plan_tc(const Product& p, int num_sms, int force_bn, int force_split) {
-    TcPlan t{};
-    const int64_t tiles_i = cdiv(p.ni, 2 * kBI);
-    if (p.rows_on_k) {
-        t.bn = p.nj <= 128 ? 128 : 256;
-    } else {
-        const int64_t lists = std::max<int64_t>(1, std::min<int64_t>(p.groups, p.nj));
-        const int64_t rows = cdiv(p.nj, lists);  // of a group, on average
-        t.bn = rows <= 32 ? 32 : (rows <= 64 ? 64 : (rows <= 128 ? 128 : 256));
-    }
-    if (force_bn == 64 || force_bn == 128 || force_bn == 256) t.bn = p.b.k_contiguous ? force_bn : std::max(force_bn, 128);
+    static constexpr double kSplit = 12.0;
     const int pairs = std::max(num_sms / 2, 1);
-    if (p.rows_on_k)
-        t.tiles = tiles_i * cdiv(p.nj, t.bn) * p.groups;
-    else
-        t.tiles = tiles_i * (cdiv(p.nj, t.bn) + (p.groups > 1 ? p.groups : 0));
-    // Under a wave of tiles, all are cut along k so that the slices fill it (not groups that share
-    // out k, whose lengths differ).  Over a wave, the tiles of a last wave that is at most half full
-    // are cut into halves along j, whose MMAs of N = 128 run at 0.9 of the rate (4096^3 bfloat16:
-    // cut in two along k 84.6 us, the slices' blocks written and added; halves 76.7).
-    t.gather = t.bn <= 64 && !p.rows_on_k;
-    const int64_t kb = cdiv(p.nk, kBK);
-    const int64_t last = t.tiles % pairs;
-    int64_t split = 1, cut = 0;  // slices, and how many tiles (the last ones) have them
-    if (!(p.rows_on_k && p.groups > 1) && kb > 0) {
-        if (force_split > 0) {
-            split = force_split;
-            cut = t.tiles;
-        } else if (t.tiles < pairs) {
-            split = std::min<int64_t>(pairs / t.tiles, kb / 4);
-            cut = t.tiles;
+    const int64_t tiles_i = cdiv(p.ni, 2 * kBI), kb = cdiv(p.nk, kBK);
+    const int64_t lists = p.rows_on_k ? 1 : std::max<int64_t>(1, std::min<int64_t>(p.groups, p.nj));
+    const double segs = p.dtype == SGEMM_F32 ? 6.0 : 1.0;
+    // groups that share out k hold a group's part of it each, on average
+    const double steps = segs * (p.rows_on_k && p.groups > 1 ? std::max(1.0, static_cast<double>(kb) / p.groups) : kb);
+    TcPlan best{};
+    double best_us = 0.0;
+    for (int bn : {256, 128, 64, 32}) {
+        if (bn < 128 && !p.b.k_contiguous) break;
+        if (force_bn && bn != (p.b.k_contiguous ? force_bn : std::max(force_bn, 128)) && force_bn <= 256) continue;
+        const double step = bn == 256 ? 0.34 : (bn == 128 ? 0.19 : (bn == 64 ? 0.14 : 0.12));
+        const double end = (bn == 256 ? 4.0 : (bn == 128 ? 2.0 : 1.0)) * (p.residual ? 3.0 : 1.0);
+        const int64_t tiles = p.rows_on_k ? tiles_i * cdiv(p.nj, bn) * p.groups
+                                          : tiles_i * lists * cdiv(cdiv(p.nj, lists), bn);
+        TcPlan t{};
+        t.bn = bn;
+        t.split = 1;
+        t.split_kb = static_cast<int>(std::max<int64_t>(kb, 1));
+        // a last wave at most half full: its tiles' halves along j, whose MMAs of N = 128 take 0.56 of
+        // the time (4096^3 bfloat16: cut in two along k 84.6 us, halves 76.7)
+        const int64_t waves = cdiv(tiles, pairs), last = tiles % pairs;
+        t.halved = bn == 256 && force_split == 0 && p.groups == 1 && waves > 1 && last > 0 && 2 * last <= pairs;
+        t.whole = last;  // for now: the tiles of the last wave
+        double us = (t.halved ? static_cast<double>(waves) - 0.44 : static_cast<double>(waves)) * steps * step + end;
+        // K slices that fill the wave (not groups that share out k: their lengths differ)
+        if (!(p.rows_on_k && p.groups > 1) && kb > 1 && (force_split > 0 || 2 * tiles <= pairs)) {
+            const int64_t want = force_split > 0 ? std::min<int64_t>(force_split, kb)
+                                                 : std::min<int64_t>(pairs / tiles, std::max<int64_t>(kb / 4, 1));
+            const int64_t split_kb = cdiv(kb, want), split = cdiv(kb, split_kb);
+            const double cut_us = segs * split_kb * step + end + kSplit;
+            if (split > 1 && (force_split > 0 || cut_us < us)) {
+                us = cut_us;
+                t.split = static_cast<int>(split);
+                t.split_kb = static_cast<int>(split_kb);
+                t.halved = false;
+            }
         }
-        split = std::max<int64_t>(1, std::min(split, kb));
+        if (best.bn == 0 || us < best_us) {
+            best = t;
+            best_us = us;
+        }
     }
-    t.split_kb = static_cast<int>(kb > 0 ? cdiv(kb, split) : 1);
-    t.split = static_cast<int>(kb > 0 ? cdiv(kb, t.split_kb) : 1);
-    t.halved = force_split == 0 && t.split == 1 && t.bn == 256 && p.groups == 1 && t.tiles > pairs && last > 0 &&
-               2 * last <= pairs;
-    t.whole = t.split > 1 ? t.tiles - cut : (t.halved ? t.tiles - last : t.tiles);
+    TcPlan t = best;
+    const int64_t last = t.whole;
+    t.tiles = p.rows_on_k ? tiles_i * cdiv(p.nj, t.bn) * p.groups
+                          : tiles_i * (cdiv(p.nj, t.bn) + (p.groups > 1 ? p.groups : 0));
+    t.whole = t.split > 1 ? 0 : (t.halved ? t.tiles - last : t.tiles);
+    t.gather = t.bn <= 64 && !p.rows_on_k;
     if (t.split > 1) {
-        t.part_bytes = region(static_cast<size_t>(cut) * t.split * 2 * kBI * t.bn * 4);
-        t.count_bytes = region(static_cast<size_t>(cut) * 2 * kEpiWarps * 4);
+        t.part_bytes = region(static_cast<size_t>(t.tiles) * t.split * 2 * kBI * t.bn * 4);
+        t.count_bytes = region(static_cast<size_t>(t.tiles) * 2 * kEpiWarps * 4);
     }
     return t;
 }

@@ -89,12 +89,13 @@ int with_workspace(const CallContext& c, cudaStream_t st, F body) {
 }
 
 // o as the tensor-core kernel reads it: bfloat16 rows at 16-byte aligned addresses are
-// read in place; others, and float32, are packed into bfloat16 parts.  Listed rows are
-// copied together unless the kernel gathers them.
-int prepare(const CallContext& c, int dtype, Operand& o, int groups, int64_t cols, int64_t listed, bool gather,
-            Arena& a, cudaStream_t st, int* launches) {
+// read in place; others, and float32, are packed into bfloat16 parts (a job is added).
+// Listed rows are copied together unless the kernel gathers them.
+int prepare(int dtype, Operand& o, int groups, int64_t cols, int64_t listed, bool gather, Arena& a, PackJob* jobs,
+            int* count) {
     if (o.parts) return 0;
-    const bool in_place = dtype == SGEMM_BF16 && (o.list == nullptr || gather) && (reinterpret_cast<uintptr_t>(o.ptr) & 15) == 0 && o.ld % 8 == 0 &&
+    const bool in_place = dtype == SGEMM_BF16 && (o.list == nullptr || gather) &&
+                          (reinterpret_cast<uintptr_t>(o.ptr) & 15) == 0 && o.ld % 8 == 0 &&
                           (groups == 1 || o.stride % 8 == 0);
     o.parts = dtype == SGEMM_F32 ? 3 : 1;
     if (in_place) return 0;
@@ -103,12 +104,8 @@ int prepare(const CallContext& c, int dtype, Operand& o, int groups, int64_t col
         return call_fail(SGEMM_ERR_TENSOR_MAP, "a float32 operand of %lld rows has more than (2^31-1024)/3",
                          (long long)(per * groups));
     bf16* dst = static_cast<bf16*>(a.take(static_cast<size_t>(o.parts) * per * groups * ldd * 2));
-    if (!a.dry()) {
-        const cudaError_t e = launch_pack(dtype, o.ptr, o.ld, o.stride, groups, per, cols, o.list, o.top, o.rows, dst,
-                                          ldd, c.sms, st);
-        if (e != cudaSuccess) return call_fail_cuda(e, "operand packing");
-        ++*launches;
-    }
+    PackJob& j = jobs[(*count)++];
+    j = PackJob{o.ptr, o.ld, o.stride, groups, per, cols, o.list, o.top, o.rows, dst, ldd, false};
     o.ptr = dst;
     o.ld = ldd;
     o.rows = per;
@@ -144,9 +141,15 @@ int product(const CallContext& c, Product p, Arena& a, cudaStream_t st) {
     if (p.nk > 0) {
         const int64_t cols_a = p.a.k_contiguous ? p.nk : p.ni, cols_b = p.b.k_contiguous ? p.nk : p.nj;
         const int64_t rows_in_lists = p.rows_on_k ? p.nk : p.nj;
-        PG_CHECK(prepare(c, p.dtype, p.a, p.rows_on_k ? 1 : p.groups, cols_a, rows_in_lists, false, a, st,
-                         &launches));
-        PG_CHECK(prepare(c, p.dtype, p.b, 1, cols_b, rows_in_lists, t.gather, a, st, &launches));
+        PackJob jobs[2];
+        int count = 0;
+        PG_CHECK(prepare(p.dtype, p.a, p.rows_on_k ? 1 : p.groups, cols_a, rows_in_lists, false, a, jobs, &count));
+        PG_CHECK(prepare(p.dtype, p.b, 1, cols_b, rows_in_lists, t.gather, a, jobs, &count));
+        if (count > 0 && !a.dry()) {
+            const cudaError_t e = launch_pack(p.dtype, jobs, count, c.sms, st);
+            if (e != cudaSuccess) return call_fail_cuda(e, "operand packing");
+            ++launches;
+        }
     }
     void* ws = a.take(t.part_bytes + t.count_bytes);
     if (!a.dry()) {

@@ -267,10 +267,18 @@ cudaError_t launch_product_rows(const Product& p, int num_sms, cudaStream_t st);
 
 // Rows (list[r] / top of src_rows, or `groups` matrices of per_group rows, `stride`
 // apart) as packed bfloat16 parts of leading dimension ldd (a multiple of 8), part
-// after part: one for bfloat16, three for float32.
-cudaError_t launch_pack(int dtype, const void* src, int64_t ld, int64_t stride, int64_t groups, int64_t per_group,
-                        int64_t cols, const int32_t* list, int top, int64_t src_rows, bf16* dst, int64_t ldd,
-                        int num_sms, cudaStream_t st);
+// after part: one for bfloat16, three for float32.  One launch for up to two matrices.
+struct PackJob {
+    const void* src;
+    int64_t ld, stride, groups, per_group, cols;
+    const int32_t* list;
+    int top;
+    int64_t src_rows;
+    bf16* dst;
+    int64_t ldd;
+    bool vec;  // set by launch_pack
+};
+cudaError_t launch_pack(int dtype, const PackJob* jobs, int count, int num_sms, cudaStream_t st);
 
 // Tensor-core products: tile width, tiles (an upper bound for grouped rows), K slices,
 // and the workspace of the slices' blocks and counters.

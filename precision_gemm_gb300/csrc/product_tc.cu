@@ -632,39 +632,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // bfloat16's smallest subnormal, 2^-133).  Of an infinity x0 is +-1 and x2 the
 // infinity, which meets only the other operand's x0: its products are then those of
 // FP32 (see split_tf32); NaN stays in x2.  bfloat16 rows are copied (PARTS 1).
-// A thread takes eight columns of a row: 16-byte accesses where the source allows
-// them.  HBM-bound: 10 bytes moved per float32 element.
-template <typename T, int PARTS>
-__global__ void __launch_bounds__(256) pack_kernel(const T* src, int64_t ld, int64_t stride, int64_t rows,
-                                                   int64_t per_group, int64_t cols, const int32_t* list, int top,
-                                                   int64_t src_rows, bf16* dst, int64_t ldd, bool vec) {
+// A thread takes eight columns of R rows: 16-byte accesses where the source allows
+// them, R rows' loads in flight.  HBM-bound: 10 bytes moved per float32 element (64
+// matrices of 1024 x 2048: 215 us, 6.2 TB/s).  blockIdx.y: the matrix.
+struct PackJobs {
+    PackJob job[2];
+};
+template <typename T, int PARTS, int R>
+__global__ void __launch_bounds__(256) pack_kernel(const PackJobs jobs) {
     pdl_trigger();
     pdl_wait();
-    constexpr int R = 4;  // rows of a thread, loaded together
-    const uint32_t eights = static_cast<uint32_t>(ldd / 8);
+    const PackJob& j = jobs.job[blockIdx.y];
+    const T* src = static_cast<const T*>(j.src);
+    const int64_t rows = j.groups * j.per_group;
+    const uint32_t eights = static_cast<uint32_t>(j.ldd / 8);
     const int64_t items = (rows + R - 1) / R * eights;
     for (int64_t q = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; q < items;
          q += static_cast<int64_t>(gridDim.x) * 256) {
         const int64_t r0 = items >> 32 ? q / eights : static_cast<uint32_t>(q) / eights;
         const int64_t c = (q - r0 * eights) * 8;
-        const int valid = static_cast<int>(cols - c < 8 ? cols - c : 8);
+        const int valid = static_cast<int>(j.cols - c < 8 ? j.cols - c : 8);
         float v[R][8] = {};
 #pragma unroll
         for (int k = 0; k < R; ++k) {
             const int64_t r = r0 * R + k;
             if (r >= rows) break;
-            if (list) {
-                const int64_t s = gathered_row(list, top, r, src_rows);
-                if (s >= 0) load8(src + s * ld + c, vec, valid, v[k]);
+            if (j.list) {
+                const int64_t s = gathered_row(j.list, j.top, r, j.src_rows);
+                if (s >= 0) load8(src + s * j.ld + c, j.vec, valid, v[k]);
             } else {
-                const int64_t g = per_group == rows ? 0 : r / per_group;
-                load8(src + g * stride + (r - g * per_group) * ld + c, vec, valid, v[k]);
+                const int64_t g = j.groups == 1 ? 0 : r / j.per_group;
+                load8(src + g * j.stride + (r - g * j.per_group) * j.ld + c, j.vec, valid, v[k]);
             }
         }
 #pragma unroll
         for (int k = 0; k < R; ++k) {
             const int64_t r = r0 * R + k;
-            if (r < rows) store_parts8<PARTS>(dst + r * ldd + c, rows * ldd, v[k]);
+            if (r < rows) store_parts8<PARTS>(j.dst + r * j.ldd + c, rows * j.ldd, v[k]);
         }
     }
 }
@@ -735,24 +739,30 @@ size_t region(size_t bytes) { return (bytes + 255) / 256 * 256; }
 
 }  // namespace
 
-cudaError_t launch_pack(int dtype, const void* src, int64_t ld, int64_t stride, int64_t groups, int64_t per_group,
-                        int64_t cols, const int32_t* list, int top, int64_t src_rows, bf16* dst, int64_t ldd,
-                        int num_sms, cudaStream_t st) {
-    const int64_t rows = groups * per_group;
-    const dim3 grid(static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(cdiv(cdiv(rows, 4) * (ldd / 8), 256),
-                                                                                 16 * num_sms))));
-    if (dtype == SGEMM_F32)
-        return launch_kernel(true, pack_kernel<float, 3>, grid, dim3(256), 0, st,
-                             static_cast<const float*>(src), ld, stride, rows, per_group, cols, list, top, src_rows,
-                             dst, ldd, rows_aligned<float>(src, ld) && stride % 4 == 0);
+cudaError_t launch_pack(int dtype, const PackJob* jobs, int count, int num_sms, cudaStream_t st) {
+    PackJobs all{};
+    int64_t most = 0;
+    for (int q = 0; q < count; ++q) {
+        PackJob& j = all.job[q];
+        j = jobs[q];
+        j.vec = dtype == SGEMM_F32 ? rows_aligned<float>(j.src, j.ld) && (j.groups == 1 || j.stride % 4 == 0)
+                                   : rows_aligned<bf16>(j.src, j.ld) && (j.groups == 1 || j.stride % 8 == 0);
+        most = std::max(most, j.groups * j.per_group * (j.ldd / 8));
+    }
+    const PackJob& j = all.job[0];
     // whole eights of a row exist where the rows are aligned and their stride covers them
-    if (list && rows_aligned<bf16>(src, ld) && ld >= ldd && ldd / 8 <= 256 * 65535)
+    if (dtype == SGEMM_BF16 && count == 1 && j.list && j.vec && j.ld >= j.ldd && j.ldd / 8 <= 256 * 65535)
         return launch_kernel(true, copy_rows_kernel,
-                             dim3(static_cast<unsigned>(cdiv(rows, 8)), static_cast<unsigned>(cdiv(ldd / 8, 256))),
-                             dim3(256), 0, st, static_cast<const bf16*>(src), ld, rows, list, top, src_rows, dst, ldd);
-    return launch_kernel(true, pack_kernel<bf16, 1>, grid, dim3(256), 0, st, static_cast<const bf16*>(src),
-                         ld, stride, rows, per_group, cols, list, top, src_rows, dst, ldd,
-                         rows_aligned<bf16>(src, ld) && stride % 8 == 0);
+                             dim3(static_cast<unsigned>(cdiv(j.per_group, 8)), static_cast<unsigned>(cdiv(j.ldd / 8, 256))),
+                             dim3(256), 0, st, static_cast<const bf16*>(j.src), j.ld, j.per_group, j.list, j.top,
+                             j.src_rows, j.dst, j.ldd);
+    // four rows per thread once that leaves each SM 2048 threads
+    const int r = most / 4 >= int64_t(2048) * num_sms ? 4 : 1;
+    const dim3 grid(static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(cdiv(cdiv(most, r), 256), 16 * num_sms))),
+                    static_cast<unsigned>(count));
+    auto kern = dtype == SGEMM_F32 ? (r == 4 ? pack_kernel<float, 3, 4> : pack_kernel<float, 3, 1>)
+                                   : (r == 4 ? pack_kernel<bf16, 1, 4> : pack_kernel<bf16, 1, 1>);
+    return launch_kernel(true, kern, grid, dim3(256), 0, st, all);
 }
 
 // Tile width, K slices and the last wave, by an estimate of the kernel's time in us:

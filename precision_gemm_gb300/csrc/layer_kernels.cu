@@ -6,20 +6,25 @@
 namespace pg {
 namespace {
 
-constexpr int kSlab = 32;    // rows per block of the activation's backward pass
-constexpr int kWidth = 256;  // its columns: 32 threads of eight
+constexpr int kWidth = 256;  // columns per block of the activation's backward pass: 32 threads of eight
 
-// dz = dy * act'(z) for a slab of 32 rows x 256 columns, and the slab's column sums per
+// Its rows: 128, so that a thread has sixteen to load, or 32 while that makes fewer than
+// four blocks per SM (1300 x 1000 float32 13 -> 9 us).
+int slab_rows(int64_t rows, int64_t n) {
+    return ((rows + 127) / 128) * ((n + kWidth - 1) / kWidth) >= 4 * 152 ? 128 : 32;
+}
+
+// dz = dy * act'(z) for a slab of rows x 256 columns, and the slab's column sums per
 // group: a slab's rows may belong to several groups, whose sums go to the slots
 // slab + g of part ((slabs + groups) x n) -- slab + g grows with every new slab and
 // with every new group, so no two sums share a slot.  Thread (l, c) takes rows l, l + 8,
 // ... of a group and eight columns; the eight threads of a column add up in order.
 // HBM-bound: reads dy and z, writes dz
-// (8192 x 8192 bfloat16, gelu: 96 us, 4.2 TB/s).
+// (8192 x 8192 bfloat16, gelu: 71 us, 5.6 TB/s).
 template <typename T, int PARTS>
-__global__ void __launch_bounds__(256, 4) dact_kernel(int64_t rows, int64_t n, const T* dy, int64_t lddy, const T* z,
+__global__ void __launch_bounds__(256, 3) dact_kernel(int64_t rows, int64_t n, const T* dy, int64_t lddy, const T* z,
                                                    int64_t ldz, int act, bf16* dz, int64_t lddz, int groups,
-                                                   const int32_t* offsets, float* part, bool vec) {
+                                                   const int32_t* offsets, float* part, int slab_size, bool vec) {
     __shared__ float sums[8][kWidth + 8];
     pdl_trigger();
     pdl_wait();
@@ -27,19 +32,15 @@ __global__ void __launch_bounds__(256, 4) dact_kernel(int64_t rows, int64_t n, c
     const int64_t c0 = (blockIdx.x - slab * widths) * kWidth, c = c0 + 8 * (threadIdx.x % 32);
     const int l = threadIdx.x / 32;
     const int valid = static_cast<int>(n - c < 8 ? n - c : 8);  // <= 0: no columns here
-    const int r0 = static_cast<int>(slab * kSlab);
-    const int r1 = static_cast<int>(rows - r0 < kSlab ? rows : r0 + kSlab);
+    const int r0 = static_cast<int>(slab * slab_size);
+    const int r1 = static_cast<int>(rows - r0 < slab_size ? rows : r0 + slab_size);
     int g = 0, first = 0, end = static_cast<int>(rows);
     if (offsets) {  // the last group that starts at or before r0: an empty one or the slab's first
-        int lo = 0, hi = groups - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (offsets[mid] <= r0)
-                lo = mid;
-            else
-                hi = mid - 1;
-        }
-        g = lo;
+        int before = 0;
+        for (int q = 0; q < groups; q += 256)
+            before += __syncthreads_count(q + static_cast<int>(threadIdx.x) < groups &&
+                                          offsets[min(q + static_cast<int>(threadIdx.x), groups - 1)] <= r0);
+        g = max(before - 1, 0);
     }
     for (; g < groups; ++g) {
         if (offsets) expert_rows(offsets, g, static_cast<int>(rows), first, end);
@@ -47,21 +48,49 @@ __global__ void __launch_bounds__(256, 4) dact_kernel(int64_t rows, int64_t n, c
         if (first >= r1) break;
         if (a >= b) continue;
         float sum[8] = {};
+        auto one = [&](auto f, int64_t r, float(&d)[8], const float(&s)[8]) {
+            constexpr int ACT = decltype(f)::value;
+#pragma unroll
+            for (int t = 0; t < 8; ++t) {
+                if (ACT != SGEMM_ACT_NONE) d[t] *= act_derivative<ACT, PARTS == 1>(s[t]);
+                sum[t] += d[t];
+            }
+            if (dz) store_parts8<PARTS>(dz + r * lddz + c, rows * lddz, d);
+        };
+        // The choices are made outside the row loops, which then have R rows' loads in flight.
         if (valid > 0) {
-            with_act(act, [&](auto f) {  // outside the loop, which then has several rows' loads in flight
-                constexpr int ACT = decltype(f)::value;
-#pragma unroll 2
-                for (int64_t r = a + l; r < b; r += 8) {
-                    float d[8], s[8];
-                    load8(dy + r * lddy + c, vec, valid, d);
-                    if (ACT != SGEMM_ACT_NONE) {
-                        load8(z + r * ldz + c, vec, valid, s);
+            with_act(act, [&](auto f) {
+                constexpr bool Z = decltype(f)::value != SGEMM_ACT_NONE;
+                constexpr int N = sizeof(T) / 2, R = 4 / N;  // 16-byte words of eight elements; rows
+                int64_t r = a + l;
+                if (vec && valid == 8) {
+                    for (; r + 8 * (R - 1) < b; r += 8 * R) {
+                        uint4 d[R][N], s[R][N];
 #pragma unroll
-                        for (int t = 0; t < 8; ++t) d[t] *= act_derivative<ACT, PARTS == 1>(s[t]);
+                        for (int k = 0; k < R; ++k)
+#pragma unroll
+                            for (int q = 0; q < N; ++q) {
+                                d[k][q] = __ldcs(reinterpret_cast<const uint4*>(dy + (r + 8 * k) * lddy + c) + q);
+                                if (Z) s[k][q] = __ldcs(reinterpret_cast<const uint4*>(z + (r + 8 * k) * ldz + c) + q);
+                            }
+#pragma unroll
+                        for (int k = 0; k < R; ++k) {
+                            float df[8], sf[8];
+#pragma unroll
+                            for (int t = 0; t < 8; ++t) {
+                                df[t] = to_float(reinterpret_cast<const T*>(d[k])[t]);
+                                if (Z) sf[t] = to_float(reinterpret_cast<const T*>(s[k])[t]);
+                            }
+                            one(f, r + 8 * k, df, sf);
+                        }
                     }
-                    if (dz) store_parts8<PARTS>(dz + r * lddz + c, rows * lddz, d);
-#pragma unroll
-                    for (int t = 0; t < 8; ++t) sum[t] += d[t];
+                }
+#pragma unroll 1
+                for (; r < b; r += 8) {
+                    float df[8], sf[8];
+                    load8(dy + r * lddy + c, vec, valid, df);
+                    if (Z) load8(z + r * ldz + c, vec, valid, sf);
+                    one(f, r, df, sf);
                 }
             });
         }
@@ -85,7 +114,7 @@ __global__ void __launch_bounds__(256, 4) dact_kernel(int64_t rows, int64_t n, c
 // and their sums are added in order.
 template <typename T>
 __global__ void __launch_bounds__(256) dbias_kernel(int64_t rows, int64_t n, const int32_t* offsets,
-                                                    const float* part, T* dbias) {
+                                                    const float* part, T* dbias, int slab_size) {
     __shared__ float sums[8][33];
     pdl_trigger();
     pdl_wait();
@@ -96,7 +125,7 @@ __global__ void __launch_bounds__(256) dbias_kernel(int64_t rows, int64_t n, con
     float sum = 0.0f;
     if (c < n && end > first) {
 #pragma unroll 4
-        for (int s = first / kSlab + l; s <= (end - 1) / kSlab; s += 8) sum += part[(static_cast<int64_t>(s) + g) * n + c];
+        for (int s = first / slab_size + l; s <= (end - 1) / slab_size; s += 8) sum += part[(static_cast<int64_t>(s) + g) * n + c];
     }
     sums[l][threadIdx.x % 32] = sum;
     __syncthreads();
@@ -192,7 +221,8 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(int64_t pairs, in
 }  // namespace
 
 size_t bias_part_bytes(int64_t rows, int64_t n, int groups) {
-    return static_cast<size_t>((rows + kSlab - 1) / kSlab + groups) * n * 4;
+    const int slab = slab_rows(rows, n);
+    return static_cast<size_t>((rows + slab - 1) / slab + groups) * n * 4;
 }
 
 int dact_launches(bool with_bias) { return with_bias ? 2 : 1; }
@@ -201,15 +231,16 @@ template <typename T, int PARTS>
 static cudaError_t run_dact(int64_t rows, int64_t n, const void* dy, int64_t lddy, const void* z, int64_t ldz, int act,
                             bf16* dz, int64_t lddz, int groups, const int32_t* offsets, void* dbias, float* part,
                             cudaStream_t st) {
-    const dim3 grid(static_cast<unsigned>(((rows + kSlab - 1) / kSlab) * ((n + kWidth - 1) / kWidth)));
+    const int slab = slab_rows(rows, n);
+    const dim3 grid(static_cast<unsigned>(((rows + slab - 1) / slab) * ((n + kWidth - 1) / kWidth)));
     const bool vec = rows_aligned<T>(dy, lddy) && (act == SGEMM_ACT_NONE || rows_aligned<T>(z, ldz));
     cudaError_t e = cudaSuccess;
     if (rows > 0)
         e = launch_kernel(true, dact_kernel<T, PARTS>, grid, dim3(256), 0, st, rows, n, static_cast<const T*>(dy), lddy,
-                          static_cast<const T*>(z), ldz, act, dz, lddz, groups, offsets, dbias ? part : nullptr, vec);
+                          static_cast<const T*>(z), ldz, act, dz, lddz, groups, offsets, dbias ? part : nullptr, slab, vec);
     if (dbias && e == cudaSuccess)
         e = launch_kernel(true, dbias_kernel<T>, dim3(static_cast<unsigned>((n + 31) / 32), groups), dim3(256), 0, st,
-                          rows, n, offsets, static_cast<const float*>(part), static_cast<T*>(dbias));
+                          rows, n, offsets, static_cast<const float*>(part), static_cast<T*>(dbias), slab);
     return e;
 }
 

@@ -146,6 +146,7 @@ template <int BN, bool F32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     product_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                       const __grid_constant__ CUtensorMap tmAg, const __grid_constant__ CUtensorMap tmBg,
+                      const __grid_constant__ CUtensorMap tmA16, const __grid_constant__ CUtensorMap tmB16,
                       const Params p) {
     using C = Cfg<BN>;
     using T = typename std::conditional<F32, float, bf16>::type;
@@ -337,29 +338,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                     if (lane == 0) raise_abort(abort_flag, p.status);
                                     break;
                                 }
-                                if (leader && lane == 0) mbar_arrive_expect_tx(full0 + 8 * slot_i, 2 * C::STAGE_BYTES);
+                                const int kc = x.k0 + (x.kb0 + kb) * kBK;
+                                // A group's rows may end inside this block.  The rows past them must read as
+                                // zeros, not as the next group's: whole runs of 16 come in boxes of 16 rows,
+                                // the last, partial one row by row, and the MMAs stop after it.
+                                const int left = LISTED && p.rows_on_k ? x.k_end - kc : kBK;
+                                const bool ragged = LISTED && left < kBK;
+                                if (leader && lane == 0)
+                                    mbar_arrive_expect_tx(full0 + 8 * slot_i,
+                                                          2 * (ragged ? C::STAGE_BYTES / 4 * ((left + 15) / 16)
+                                                                      : C::STAGE_BYTES));
                                 const uint32_t bar = full_leader0 + 8 * slot_i;
                                 const uint32_t slot = smem_u32(smem) + slot_i * C::STAGE_BYTES;
                                 const uint32_t slot_b = slot + C::A_BYTES;
-                                const int kc = x.k0 + (x.kb0 + kb) * kBK;
-                                // a group's rows that end inside this block: the rows past them must read as
-                                // zeros, not as the next group's
-                                const bool ragged = LISTED && p.rows_on_k && kc + kBK > x.k_end;
                                 if (ragged) {
-                                    // lane: columns 64 h .. of an operand, rows r .. r + 3 of the block
-                                    const int h = lane >> 4, r = kc + 4 * (lane & 15);
-                                    int4 ya, yb;
-                                    int *pya = &ya.x, *pyb = &yb.x;
+                                    const int runs = left / 16;
+                                    if (lane < 16) {
+                                        // run q of 64 columns: A's two groups, then B's
+                                        const int q = lane >> 2, h = lane & 1;
+                                        if (q < runs && (lane & 2) == 0)
+                                            tma_load_3d_pair(slot + 8192 * h + 2048 * q, &tmA16, ia + 64 * h,
+                                                             kc + 16 * q, z_a, bar);
+                                        else if (q < runs && h < C::BNH / 64)
+                                            tma_load_3d_pair(slot_b + 8192 * h + 2048 * q, &tmB16, jb + 64 * h,
+                                                             kc + 16 * q, z_b, bar);
+                                    } else if (left % 16 != 0) {
+                                        const int q = (lane >> 2) & 3, h = lane & 1, r = kc + 16 * runs + 4 * q;
+                                        const bool of_a = (lane & 2) == 0;
+                                        int4 y;
+                                        int* py = &y.x;
 #pragma unroll
-                                    for (int q = 0; q < 4; ++q) {
-                                        const bool in = r + q < x.k_end;
-                                        pya[q] = in ? r + q + pa * p.a_rows : p.a_oob;
-                                        pyb[q] = in ? r + q + pb * p.b_rows : p.b_oob;
+                                        for (int k = 0; k < 4; ++k)
+                                            py[k] = r + k < x.k_end ? r + k + (of_a ? pa * p.a_rows : pb * p.b_rows)
+                                                                    : (of_a ? p.a_oob : p.b_oob);
+                                        const uint32_t at = 8192 * h + 2048 * runs + 512 * q;
+                                        if (of_a)
+                                            tma_gather4_pair(slot + at, &tmAg, ia + 64 * h, y, bar);
+                                        else if (h < C::BNH / 64)
+                                            tma_gather4_pair(slot_b + at, &tmBg, jb + 64 * h, y, bar);
                                     }
-                                    tma_gather4_pair(slot + 8192 * h + 512 * (lane & 15), &tmAg, ia + 64 * h, ya, bar);
-                                    if (h < C::BNH / 64)
-                                        tma_gather4_pair(slot_b + 8192 * h + 512 * (lane & 15), &tmBg, jb + 64 * h, yb,
-                                                         bar);
+                                    __syncwarp();
                                 } else {
                                     if (p.a_mn) {
                                         tma_load_3d_pair_warp(slot, &tmA, ia, kc, z_a, bar);
@@ -410,12 +428,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const uint64_t a_desc0 = smem_desc(slot0, p.a_mn ? 8192 : 16, 1024, kSwizzle128B);
             const uint64_t b_desc0 = smem_desc(slot0 + C::A_BYTES, p.b_mn ? 8192 : 16, 1024, kSwizzle128B);
             const uint32_t a_step = p.a_mn ? 128 : 2, b_step = p.b_mn ? 128 : 2;
+            const bool ragged = p.rows_on_k && p.offsets != nullptr;
             int slot_i = 0, chunk = 0;
             uint32_t phase = 0;
             bool ok = true;
             for (int u = pair; u < units && ok; u += pairs) {
                 const Unit x = unit_of(u);
                 const int nkb = __shfl_sync(0xffffffffu, x.nkb, 0);
+                const int group_rows = __shfl_sync(0xffffffffu, x.k_end - x.k0, 0);
                 const uint32_t idesc =
                     idesc_bf16(2 * kBI, __shfl_sync(0xffffffffu, x.n, 0), p.a_mn != 0, p.b_mn != 0);
                 for (int c0 = 0; c0 < nkb && ok; c0 += p.chunk_kb, ++chunk) {
@@ -433,8 +453,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         if (!ok) break;
                         tc_fence_after_sync();
                         const uint32_t o = static_cast<uint32_t>(slot_i * C::STAGE_BYTES) >> 4;
+                        // a group's last block stops at its last run of 16 rows
+                        const int left = ragged ? group_rows - (kb % (min(c0 + p.chunk_kb, nkb) - c0) + c0) * kBK : kBK;
 #pragma unroll
                         for (int kk = 0; kk < kBK / 16; ++kk) {
+                            if (16 * kk >= left) break;
                             mma_bf16_pair_warp(d, a_desc0 + (o + kk * a_step), b_desc0 + (o + kk * b_step), idesc,
                                                accumulate);
                             accumulate = 1;
@@ -699,7 +722,7 @@ __global__ void __launch_bounds__(256) copy_rows_kernel(const bf16* src, int64_t
 }
 
 template <int BN, bool F32>
-cudaError_t launch(const CUtensorMap (&m)[4], const Params& p, int64_t units, bool after_previous, int num_sms,
+cudaError_t launch(const CUtensorMap (&m)[6], const Params& p, int64_t units, bool after_previous, int num_sms,
                    cudaStream_t st) {
     using C = Cfg<BN>;
     auto kern = product_tc_kernel<BN, F32>;
@@ -731,7 +754,7 @@ cudaError_t launch(const CUtensorMap (&m)[4], const Params& p, int64_t units, bo
     }
     const int64_t clusters = std::max<int64_t>(1, std::min<int64_t>(units, most));
     return launch_kernel(after_previous, kern, dim3(static_cast<unsigned>(2 * clusters)), dim3(kThreads), C::SMEM,
-                         st, m[0], m[1], m[2], m[3], p);
+                         st, m[0], m[1], m[2], m[3], m[4], m[5], p);
 }
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -886,7 +909,7 @@ int launch_product_tc(const CallContext& c, const Product& p, const TcPlan& t, i
     // columns of each matrix, and its box
     const int64_t cols_a = p.a.k_contiguous ? p.nk : p.ni, cols_b = p.b.k_contiguous ? p.nk : p.nj;
     const int64_t z_a = (p.rows_on_k ? 1 : p.groups) * static_cast<int64_t>(parts);
-    CUtensorMap m[4];
+    CUtensorMap m[6];
     int rc;
     if (p.nk == 0) {  // nothing is loaded: the maps stay unread
         std::memset(m, 0, sizeof m);
@@ -894,11 +917,13 @@ int launch_product_tc(const CallContext& c, const Product& p, const TcPlan& t, i
         const uint32_t box_a = p.a.k_contiguous ? kBI : kBK, box_b = p.b.k_contiguous ? t.bn / 2 : kBK;
         if ((rc = call_encode_bf16(&m[0], p.a.ptr, cols_a, p.a.rows, p.a.ld, z_a, p.a.stride, kBK, box_a))) return rc;
         if ((rc = call_encode_bf16(&m[1], p.b.ptr, cols_b, p.b.rows, p.b.ld, parts, p.b.stride, kBK, box_b))) return rc;
-        m[2] = m[0];
-        m[3] = m[1];
+        m[2] = m[4] = m[0];
+        m[3] = m[5] = m[1];
         const bool ragged = p.rows_on_k && p.offsets;  // lists may end inside a block
         if (ragged) {
             if ((rc = call_encode_bf16(&m[2], p.a.ptr, cols_a, p.a.rows * parts, p.a.ld, 0, 0, kBK, 1))) return rc;
+            if ((rc = call_encode_bf16(&m[4], p.a.ptr, cols_a, p.a.rows, p.a.ld, z_a, p.a.stride, kBK, 16))) return rc;
+            if ((rc = call_encode_bf16(&m[5], p.b.ptr, cols_b, p.b.rows, p.b.ld, parts, p.b.stride, kBK, 16))) return rc;
         }
         if (ragged || q.list) {
             if ((rc = call_encode_bf16(&m[3], p.b.ptr, cols_b, p.b.rows * parts, p.b.ld, 0, 0, kBK, 1))) return rc;

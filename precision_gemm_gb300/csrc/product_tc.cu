@@ -136,9 +136,14 @@ __device__ __forceinline__ void finish(const Params& p, float (&v)[kCols], float
     }
     TO* dst = static_cast<TO*>(p.out) + out_base + jb * p.ldo + i;
     const int64_t ld = p.ldo;
+    if (jn >= N) {
 #pragma unroll
-    for (int t = 0; t < N; ++t, dst += ld)
-        if (t < jn) *dst = from_float<TO>(v[t]);
+        for (int t = 0; t < N; ++t, dst += ld) *dst = from_float<TO>(v[t]);
+    } else {
+#pragma unroll
+        for (int t = 0; t < N; ++t, dst += ld)
+            if (t < jn) *dst = from_float<TO>(v[t]);
+    }
 }
 
 // F32: float32 operands in three parts, accumulated in chunks.
@@ -583,15 +588,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
 #pragma unroll 1
             for (int c = half; kCols * c < cols; c += 2) {
-                uint32_t v[kCols];
+                float f[kCols];
                 __syncwarp();
                 if (any) {
+                    uint32_t v[kCols];
                     tmem_ld_32x32b_x16(lane_base + buf * BN + kCols * c, v);
                     tmem_wait_ld();
-                }
-                float f[kCols];
 #pragma unroll
-                for (int t = 0; t < kCols; ++t) f[t] = any ? __uint_as_float(v[t]) : 0.0f;
+                    for (int t = 0; t < kCols; ++t) f[t] = __uint_as_float(v[t]);
+                } else {
+#pragma unroll
+                    for (int t = 0; t < kCols; ++t) f[t] = 0.0f;
+                }
                 if (block) {
 #pragma unroll
                     for (int t = 0; t < kCols; ++t) block[(kCols * c + t) * (2 * kBI)] = f[t];

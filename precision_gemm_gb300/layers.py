@@ -288,7 +288,7 @@ class ExpertPlan:
                                (rows, "rows", (tokens * top,)), (slots, "slots", (tokens, top))):
             _packed(x, name, shape, torch.int32, index)
         self.tokens, self.top, self.experts, self.index = tokens, top, experts, index
-        self._store, self._lists = None, (counts, offsets, rows, slots)
+        self._store, self._lists = None, [counts, offsets, rows, slots]
         self._addresses = tuple(x.data_ptr() for x in self._lists)
 
     @classmethod
@@ -296,17 +296,22 @@ class ExpertPlan:
         """The lists one after another in `store`; their tensors are made when asked for."""
         self = cls.__new__(cls)
         self.tokens, self.top, self.experts, self.index = tokens, top, experts, index
-        self._store, self._lists = store, None
+        self._store, self._lists = store, [None] * 4
         rows = address + 4 * (2 * experts + 1)
         self._addresses = (address, address + 4 * experts, rows, rows + 4 * tokens * top)
         return self
 
     def _list(self, i):
-        if self._lists is None:
+        x = self._lists[i]
+        if x is None:
             e, r = self.experts, self.tokens * self.top
-            counts, offsets, rows, slots = self._store.split_with_sizes((e, e + 1, r, r))
-            self._lists = (counts, offsets, rows, slots.view(self.tokens, self.top))
-        return self._lists[i]
+            at = (0, e, 2 * e + 1, 2 * e + 1 + r)[i]
+            if i == 3:
+                x = self._store.as_strided((self.tokens, self.top), (self.top, 1), at)
+            else:
+                x = self._store.as_strided(((e, e + 1, r)[i],), (1,), at)
+            self._lists[i] = x
+        return x
 
     counts = property(lambda self: self._list(0))
     offsets = property(lambda self: self._list(1))

@@ -64,17 +64,18 @@ int check_pairs(int64_t tokens, int top, int pos) {
     return 0;
 }
 
-// The workspace of a call: its launch sequence runs twice, first with base == null to
-// add up what it needs (nothing is launched), then on the memory.
+// The workspace of a call: its launch sequence runs twice, first dry to add up what it
+// needs (nothing is launched), then on the memory.
 struct Arena {
     char* base = nullptr;
     size_t used = 0;
+    bool counting = true;
     void* take(size_t bytes) {
-        void* at = base + used;
+        char* at = base + used;
         used += region(bytes);
-        return base ? at : nullptr;
+        return counting ? nullptr : at;
     }
-    bool dry() const { return base == nullptr; }
+    bool dry() const { return counting; }
 };
 
 template <typename F>
@@ -83,8 +84,9 @@ int with_workspace(const CallContext& c, cudaStream_t st, F body) {
     PG_CHECK(body(sizes));
     Arena memory;
     void* ws = nullptr;
-    PG_CHECK(call_workspace(c, st, std::max<size_t>(sizes.used, 1), &ws));
+    PG_CHECK(call_workspace(c, st, sizes.used, &ws));
     memory.base = static_cast<char*>(ws);
+    memory.counting = false;
     return body(memory);
 }
 

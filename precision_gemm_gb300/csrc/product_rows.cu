@@ -21,6 +21,15 @@ struct RowsParams {
     int ks;      // warps that share a weight row's k, 1 to kWarps
 };
 
+// 16 bytes of a weight row: read once, so they take no place in L1, which holds x.
+__device__ __forceinline__ uint4 stream16(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
 // 16 bytes of consecutive elements, `valid` of them there.
 template <typename T>
 __device__ __forceinline__ uint4 load16(const T* p, bool vec, int64_t valid) {
@@ -105,19 +114,29 @@ __global__ void __launch_bounds__(32 * kWarps, B) product_rows_kernel(const Rows
         int64_t s = s0;
         if (VEC && all) {
             const int64_t whole = min(s1, p.nk / (32 * V));  // steps without an end of a row
-            for (; s + U <= whole; s += U) {
-                uint4 raw[U][F];
+            // U steps' weights are on their way at any time: a step's registers are filled again as
+            // soon as it is used
+            uint4 raw[U][F];
+            auto fetch = [&](uint4(&to)[F], int64_t at) {
+                if (at < whole) {
 #pragma unroll
-                for (int u = 0; u < U; ++u)
+                    for (int f = 0; f < F; ++f) to[f] = stream16(w + f * ldw + at * 32 * V);
+                }
+            };
 #pragma unroll
-                    for (int f = 0; f < F; ++f)
-                        raw[u][f] = __ldcs(reinterpret_cast<const uint4*>(w + f * ldw + (s + u) * 32 * V));
+            for (int u = 0; u < U; ++u) fetch(raw[u], s + u);
+            for (; s < whole; s += U) {
 #pragma unroll
-                for (int u = 0; u < U; ++u)
+                for (int u = 0; u < U; ++u) {
+                    if (s + u < whole) {
 #pragma unroll
-                    for (int m = 0; m < M; ++m)
-                        add(raw[u], *reinterpret_cast<const uint4*>(x + row[m] + (s + u) * 32 * V), m);
+                        for (int m = 0; m < M; ++m)
+                            add(raw[u], *reinterpret_cast<const uint4*>(x + row[m] + (s + u) * 32 * V), m);
+                        fetch(raw[u], s + u + U);
+                    }
+                }
             }
+            s = whole > s0 ? whole : s0;
         }
 #pragma unroll 1
         for (; s < s1; ++s) {

@@ -435,3 +435,148 @@ def test_large_offsets():
     want, _, den = R.linear(tail, w, None, "none", None)
     R.close(y[-5:], want, den, torch.bfloat16)
     assert not y[:-5].any()
+
+
+# ---- limits of float32, empty extents, failure detection --------------------------------
+
+
+@pytest.mark.parametrize("t", [2, 90])
+def test_float32_range(t):
+    """Values near the largest float, whose first part would round to infinity, and small
+    ones: the three bfloat16 parts keep 24 bits down to about 2^-109 (the last part then
+    still is a normal bfloat16 or exact)."""
+    n, k = 70, 130
+    g = _gen(t)
+    x, w = torch.randn(t, k, generator=g), torch.randn(n, k, generator=g)
+    big = x.clone()
+    big[:, 3] = torch.finfo(torch.float32).max * torch.sign(x[:, 3])
+    small = x * 2.0 ** -100
+    for a, scale in ((big, 2.0 ** -20), (small, 2.0 ** 20)):
+        b = w * scale
+        y = pg.linear(a.cuda(), b.cuda())
+        want, _, den = R.linear(a, b, None, "none", None)
+        R.close(y, want, den, torch.float32)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS.get)
+def test_gradients_of_empty_extents(dtype):
+    def empty(*shape):
+        return torch.empty(*shape, dtype=dtype, device="cuda")
+
+    dx, dw, db = pg.linear_backward(empty(7, 0), empty(7, 5), empty(0, 5))
+    assert dx.shape == (7, 5) and not dx.any() and dw.shape == (0, 5) and db.shape == (0,)
+    dx, dw, db = pg.linear_backward(torch.ones(7, 3, dtype=dtype, device="cuda"), empty(7, 0), empty(3, 0))
+    assert dx.shape == (7, 0) and dw.shape == (3, 0) and db.tolist() == [7.0] * 3
+    plan = pg.expert_plan(torch.empty(0, 2, dtype=torch.int32, device="cuda"), 3)
+    w = torch.ones(3, 4, 6, dtype=dtype, device="cuda")
+    assert pg.expert_linear(empty(0, 6), w, plan, gather=True).shape == (0, 4)
+    dx, dw, db = pg.expert_linear_backward(empty(0, 4), empty(0, 6), w, plan, gather=True)
+    assert dx.shape == (0, 6) and not dw.any() and not db.any()
+    assert pg.expert_combine(empty(0, 4), plan).shape == (0, 4)
+    plan = pg.expert_plan(_none(5, 2).cuda(), 3)  # tokens, but none of them has an expert
+    x = torch.ones(5, 6, dtype=dtype, device="cuda")
+    y, z = pg.expert_linear(x, w, plan, gather=True, preact=True)
+    assert not y.any() and not z.any()
+    dx, dw, db = pg.expert_linear_backward(y, x, w, plan, gather=True)
+    assert not dx.any() and not dw.any() and not db.any()
+    drows, dweights = pg.expert_combine_backward(x, torch.ones(10, 6, dtype=dtype, device="cuda"), plan,
+                                                 torch.ones(5, 2, device="cuda"))
+    assert not drows.any() and not dweights.any()
+
+
+@pytest.mark.parametrize("bn,split", [(64, 0), (128, 0), (256, 0), (128, 3), (256, 7)])
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS.get)
+def test_linear_every_tile_width_and_k_slices(dtype, bn, split):
+    t, n, k = 400, 600, 1100
+    g = _gen(bn + split)
+    x, w = _draw(g, dtype, t, k), _draw(g, dtype, n, k, std=k ** -0.5)
+    b, r = _draw(g, dtype, n), _draw(g, dtype, t, n)
+    dy = _draw(g, dtype, t, n)
+    pg.force_plan(bn, split)
+    try:
+        y, z = pg.linear(x.cuda(), w.cuda(), b.cuda(), "gelu", r.cuda(), preact=True)
+        again = pg.linear(x.cuda(), w.cuda(), b.cuda(), "gelu", r.cuda())
+        grads = pg.linear_backward(dy.cuda(), x.cuda(), w.cuda())
+    finally:
+        pg.force_plan(0, 0)
+    want, wz, den = R.linear(x, w, b, "gelu", r)
+    R.close(y, want, den, dtype)
+    R.close(z, wz, den, dtype)
+    assert torch.equal(y, again)  # slices are added in a fixed order
+    want, den = R.linear_backward(dy, x, w, "none", z.cpu())
+    _check_backward(grads, want, den, dtype, "none")
+
+
+def test_half_tiles_of_a_last_wave():
+    """More tiles of 256 x 256 than SM pairs by a few: the last wave's run as halves, the
+    very last of them past the rows' end."""
+    pairs = torch.cuda.get_device_properties(0).multi_processor_count // 2
+    t, n, k = 256 * (pairs + 5) - 200, 250, 1024  # one row of tiles; the last tile holds 56 rows
+    g = _gen(3)
+    x, w = _draw(g, torch.bfloat16, t, k), _draw(g, torch.bfloat16, n, k, std=k ** -0.5)
+    pg.force_plan(256, 0)
+    try:
+        y = pg.linear(x.cuda(), w.cuda())
+    finally:
+        pg.force_plan(0, 0)
+    want, _, den = R.linear(x, w, None, "none", None)
+    R.close(y, want, den, torch.bfloat16)
+
+
+def test_expired_wait_is_reported():
+    """A loader that issues nothing (a test hook): the kernel's bounded waits run out, the
+    call's status says so, and the next call is right again."""
+    x, w = torch.randn(300, 256, device="cuda").bfloat16(), torch.randn(200, 256, device="cuda").bfloat16()
+    want = pg.linear(x, w)
+    limit = pg.set_wait_timeout(50_000_000)
+    flags = pg.debug_flags(pg.SGEMM_DEBUG_STALL_PRODUCER)
+    try:
+        pg.linear(x, w)
+        assert pg.device_status() == pg.SGEMM_ERR_TIMEOUT
+    finally:
+        pg.debug_flags(flags)
+        pg.set_wait_timeout(limit)
+    assert torch.equal(pg.linear(x, w), want) and pg.device_status() == 0
+
+
+def test_injected_host_faults_fail_cleanly():
+    x, w = torch.randn(300, 256, device="cuda").bfloat16(), torch.randn(200, 256, device="cuda").bfloat16()
+    pg.linear(x, w)
+    before = pg.launch_count()
+    pg.debug_flags(pg.SGEMM_DEBUG_FAIL_TENSOR_MAP)
+    try:
+        with pytest.raises(pg.SgemmError) as e:
+            pg.linear(x, w)
+        assert e.value.code == pg.SGEMM_ERR_TENSOR_MAP
+    finally:
+        pg.debug_flags(0)
+    pg.debug_flags(pg.SGEMM_DEBUG_FAIL_ALLOC)
+    s = torch.cuda.Stream()  # without a workspace yet
+    try:
+        with pytest.raises(pg.SgemmError) as e:
+            pg.linear(x.float(), w.float(), stream=s)
+        assert e.value.code == pg.SGEMM_ERR_ALLOC
+    finally:
+        pg.debug_flags(0)
+    assert pg.launch_count() == before
+
+
+def test_given_workspace_is_used_and_its_size_checked():
+    x, w = torch.randn(300, 256, device="cuda"), torch.randn(200, 256, device="cuda")
+    want = pg.linear(x, w)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    try:
+        pg.set_workspace(torch.empty(8 << 20, dtype=torch.uint8, device="cuda"), stream=s)
+        graph = torch.cuda.CUDAGraph()  # nothing is allocated: the first call can be captured
+        with torch.cuda.graph(graph, stream=s):
+            y = pg.linear(x, w)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
+        pg.set_workspace(torch.empty(1024, dtype=torch.uint8, device="cuda"), stream=s)
+        with pytest.raises(pg.SgemmError) as e:
+            pg.linear(x, w, stream=s)
+        assert e.value.code == pg.SGEMM_ERR_WORKSPACE
+    finally:
+        pg.set_workspace(None, stream=s)

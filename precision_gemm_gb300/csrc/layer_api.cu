@@ -101,7 +101,7 @@ int prepare(int dtype, Operand& o, int groups, int64_t cols, int64_t listed, boo
                           (groups == 1 || o.stride % 8 == 0);
     o.parts = dtype == SGEMM_F32 ? 3 : 1;
     if (in_place) return 0;
-    const int64_t per = o.list ? listed : o.rows, ldd = (cols + 7) / 8 * 8;
+    const int64_t per = o.list ? listed : o.rows, ldd = packed_ld(cols);
     if (o.parts * per * groups > kMaxExtent)
         return call_fail(SGEMM_ERR_TENSOR_MAP, "a float32 operand of %lld rows has more than (2^31-1024)/3",
                          (long long)(per * groups));
@@ -113,6 +113,7 @@ int prepare(int dtype, Operand& o, int groups, int64_t cols, int64_t listed, boo
     o.rows = per;
     o.stride = per * ldd;
     o.list = nullptr;
+    o.packed = true;
     return 0;
 }
 
@@ -197,8 +198,9 @@ int backward_steps(const CallContext& c, const Backward& b, Arena& a, cudaStream
     bf16* dz_own = nullptr;
     if (own_dz) {
         dz.parts = b.dtype == SGEMM_F32 ? 3 : 1;
-        dz.ld = (b.n + 7) / 8 * 8;
+        dz.ld = packed_ld(b.n);
         dz.stride = b.rows * dz.ld;
+        dz.packed = true;
         if (dz.parts * b.rows > kMaxExtent)
             return call_fail(SGEMM_ERR_TENSOR_MAP, "a float32 operand of %lld rows has more than (2^31-1024)/3",
                              (long long)b.rows);

@@ -676,7 +676,7 @@ __global__ void __launch_bounds__(256) pack_kernel(const PackJobs jobs) {
     const PackJob& j = jobs.job[blockIdx.y];
     const T* src = static_cast<const T*>(j.src);
     const int64_t rows = j.groups * j.per_group;
-    const uint32_t eights = static_cast<uint32_t>(j.ldd / 8);
+    const uint32_t eights = static_cast<uint32_t>((j.cols + 7) / 8);
     const int64_t items = (rows + R - 1) / R * eights;
     for (int64_t q = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; q < items;
          q += static_cast<int64_t>(gridDim.x) * 256) {
@@ -709,14 +709,14 @@ __global__ void __launch_bounds__(256) pack_kernel(const PackJobs jobs) {
 // the 16-byte block of its last element; no product reads those.  Bound by the writes
 // (65536 rows of 2048: 50 us, 5.4 TB/s).
 __global__ void __launch_bounds__(256) copy_rows_kernel(const bf16* src, int64_t ld, int64_t rows, const int32_t* list,
-                                                        int top, int64_t src_rows, bf16* dst, int64_t ldd) {
+                                                        int top, int64_t src_rows, bf16* dst, int64_t ldd, int eights) {
     pdl_trigger();
     pdl_wait();
     const int lane = threadIdx.x % 32;
     const int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32;
     if (r >= rows) return;
     const int64_t s = gathered_row(list, top, r, src_rows);
-    const int eights = static_cast<int>(ldd / 8), first = blockIdx.y * 256;
+    const int first = blockIdx.y * 256;
     const uint4* in = reinterpret_cast<const uint4*>(src + (s >= 0 ? s : 0) * ld) + first;
     uint4* out = reinterpret_cast<uint4*>(dst + r * ldd) + first;
     uint4 v[8];
@@ -778,15 +778,15 @@ cudaError_t launch_pack(int dtype, const PackJob* jobs, int count, int num_sms, 
         j = jobs[q];
         j.vec = dtype == SGEMM_F32 ? rows_aligned<float>(j.src, j.ld) && (j.groups == 1 || j.stride % 4 == 0)
                                    : rows_aligned<bf16>(j.src, j.ld) && (j.groups == 1 || j.stride % 8 == 0);
-        most = std::max(most, j.groups * j.per_group * (j.ldd / 8));
+        most = std::max(most, j.groups * j.per_group * cdiv(j.cols, 8));
     }
     const PackJob& j = all.job[0];
     // whole eights of a row exist where the rows are aligned and their stride covers them
-    if (dtype == SGEMM_BF16 && count == 1 && j.list && j.vec && j.ld >= j.ldd && j.ldd / 8 <= 256 * 65535)
+    if (dtype == SGEMM_BF16 && count == 1 && j.list && j.vec && j.ld >= cdiv(j.cols, 8) * 8 && cdiv(j.cols, 8) <= 256 * 65535)
         return launch_kernel(true, copy_rows_kernel,
-                             dim3(static_cast<unsigned>(cdiv(j.per_group, 8)), static_cast<unsigned>(cdiv(j.ldd / 8, 256))),
+                             dim3(static_cast<unsigned>(cdiv(j.per_group, 8)), static_cast<unsigned>(cdiv(j.cols, 8 * 256))),
                              dim3(256), 0, st, static_cast<const bf16*>(j.src), j.ld, j.per_group, j.list, j.top,
-                             j.src_rows, j.dst, j.ldd);
+                             j.src_rows, j.dst, j.ldd, static_cast<int>(cdiv(j.cols, 8)));
     // four rows per thread once that leaves each SM 2048 threads
     const int r = most / 4 >= int64_t(2048) * num_sms ? 4 : 1;
     const dim3 grid(static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(cdiv(cdiv(most, r), 256), 16 * num_sms))),
@@ -914,8 +914,10 @@ int launch_product_tc(const CallContext& c, const Product& p, const TcPlan& t, i
         if (e != cudaSuccess) return call_fail_cuda(e, "cudaMemsetAsync (K slice counters)");
     }
     const bool after_previous = t.split == 1;  // no memset in between
-    // columns of each matrix, and its box
-    const int64_t cols_a = p.a.k_contiguous ? p.nk : p.ni, cols_b = p.b.k_contiguous ? p.nk : p.nj;
+    // Columns of each matrix.  Packed rows along i or j count as whole: boxes that reach past
+    // a matrix load slower, and what lies there only meets results that are not stored.
+    const int64_t cols_a = p.a.k_contiguous ? p.nk : (p.a.packed ? p.a.ld : p.ni);
+    const int64_t cols_b = p.b.k_contiguous ? p.nk : (p.b.packed ? p.b.ld : p.nj);
     const int64_t z_a = (p.rows_on_k ? 1 : p.groups) * static_cast<int64_t>(parts);
     CUtensorMap m[6];
     int rc;

@@ -580,3 +580,35 @@ def test_given_workspace_is_used_and_its_size_checked():
         assert e.value.code == pg.SGEMM_ERR_WORKSPACE
     finally:
         pg.set_workspace(None, stream=s)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS.get)
+def test_gradients_over_a_workspace_of_nan(dtype):
+    """What lies in the workspace before a call (here NaN everywhere) reaches no result, with
+    rows long enough to be padded to whole lines."""
+    t, n, k, e, top = 150, 530, 1100, 4, 2
+    g = _gen(12)
+    x, w, dy = _draw(g, dtype, t, k), _draw(g, dtype, e, n, k, std=k ** -0.5), _draw(g, dtype, t * top, n)
+    z = _draw(g, dtype, t * top, n)
+    ids = _ids(g, t, top, e, "dropped").cuda()
+    plan = pg.expert_plan(ids, e)
+    xc, wc, dyc, zc = (v.cuda() for v in (x, w, dy, z))
+    want, den = R.linear_backward(dy[:t], x, w[0], "gelu", z[:t])
+    experts = pg.expert_linear_backward(dyc, xc, wc, plan, "gelu", zc, gather=True)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    try:
+        space = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+        for call in (lambda: pg.linear_backward(dyc[:t], xc, wc[0], "gelu", zc[:t], stream=s),
+                     lambda: pg.expert_linear_backward(dyc, xc, wc, plan, "gelu", zc, gather=True, stream=s)):
+            space.fill_(255)
+            torch.cuda.synchronize()
+            pg.set_workspace(space, stream=s)
+            got = call()
+            torch.cuda.synchronize()
+            if got[1].dim() == 2:
+                _check_backward(got, want, den, dtype, "gelu")
+            else:
+                assert all(torch.equal(a, b) and bool(torch.isfinite(a).all()) for a, b in zip(got, experts))
+    finally:
+        pg.set_workspace(None, stream=s)

@@ -90,15 +90,19 @@ int with_workspace(const CallContext& c, cudaStream_t st, F body) {
     return body(memory);
 }
 
+// Whether o's rows start at 16-byte boundaries: what wide loads, and TMA of bfloat16, need.
+bool rows_on_16(int dtype, const Operand& o, int groups) {
+    const int64_t unit = dtype == SGEMM_F32 ? 4 : 8;
+    return (reinterpret_cast<uintptr_t>(o.ptr) & 15) == 0 && o.ld % unit == 0 && (groups == 1 || o.stride % unit == 0);
+}
+
 // o as the tensor-core kernel reads it: bfloat16 rows at 16-byte aligned addresses are
 // read in place; others, and float32, are packed into bfloat16 parts (a job is added).
 // Listed rows are copied together unless the kernel gathers them.
 int prepare(int dtype, Operand& o, int groups, int64_t cols, int64_t listed, bool gather, Arena& a, PackJob* jobs,
             int* count) {
     if (o.parts) return 0;
-    const bool in_place = dtype == SGEMM_BF16 && (o.list == nullptr || gather) &&
-                          (reinterpret_cast<uintptr_t>(o.ptr) & 15) == 0 && o.ld % 8 == 0 &&
-                          (groups == 1 || o.stride % 8 == 0);
+    const bool in_place = dtype == SGEMM_BF16 && (o.list == nullptr || gather) && rows_on_16(dtype, o, groups);
     o.parts = dtype == SGEMM_F32 ? 3 : 1;
     if (in_place) return 0;
     const int64_t per = o.list ? listed : o.rows, ldd = packed_ld(cols);
@@ -118,16 +122,27 @@ int prepare(int dtype, Operand& o, int groups, int64_t cols, int64_t listed, boo
 }
 
 // Whether a product runs on the kernel that streams the weights once for a few rows.
-// Measured against the tensor cores (us, rows / tensor cores; calls under about 13 us
-// are bound by the host): float32, which they must first write out in parts, 8192 x
-// 2048: 8 rows 20 / 74, 16 rows 39 / 73, 32 rows 74 / 74; 64 experts of 1024 x 2048,
-// 16 rows each 344 / 478, 32 each 609 / 526.  bfloat16, 8192 x 2048: 4 rows 15.6 / 17.5,
-// 8 rows 17.5 / 17.3; 64 experts, one row each 25 / 35, two each 58 / 50.
+// Measured against the tensor cores (us, rows / tensor cores):
+// float32, whose weights those read in parts that are written first:
+//   one matrix, 8192 x 2048: 8 rows 17 / 61, 16 rows 28 / 61, 24 rows 50 / 61; 2048 x 2048:
+//   16 rows 14 / 24, 24 rows 25 / 25; 1000 x 777: 16 rows 13 / 18, 24 rows 22 / 18;
+//   64 experts of 1024 x 2048 with uneven lists: 16 rows each on average 257 / 370, 24 rows
+//   350 / 372, 32 rows 437 / 387; rows at other than 16-byte boundaries: 4096 x 4095, 16
+//   rows 31 / 59; experts of 1024 x 2047, 16 rows 354 / 383;
+// bfloat16 at 16-byte boundaries, where L2 still holds much of the matrix:
+//   4096 x 4096: 1 row 5.4 / 13, 4 rows 9.9 / 13; 8192 x 8192: 1 row 27 / 26, 4 rows 32 / 26;
+//   64 experts: 8 pairs 11 / 14, 64 pairs 38 / 38, 128 pairs 62 / 38;
+// bfloat16 at others, which the tensor cores read from a copy:
+//   4096 x 4095: 4 rows 13 / 27, 8 rows 23 / 28; 8192 x 8191: 4 rows 52 / 90, 8 rows 105 / 90;
+//   64 experts of 1024 x 2047: 64 pairs 74 / 165, 256 pairs 142 / 180, 1024 pairs 429 / 181.
 bool few_rows(const Product& p) {
     if (p.rows_on_k || !p.a.k_contiguous || p.nk == 0 || p.out_f32) return false;
     if (p.b.rows * p.b.ld >= int64_t(1) << 32) return false;  // its row offsets are 32-bit
     const int64_t lists = std::min<int64_t>(p.groups, p.nj);  // lists that have rows, at most
-    return p.nj <= lists * (p.dtype == SGEMM_F32 ? 16 : (p.groups == 1 ? 4 : 1));
+    const bool aligned = rows_on_16(p.dtype, p.a, p.groups);
+    if (p.dtype == SGEMM_F32) return p.nj <= lists * (p.groups > 1 && aligned ? 24 : 16);
+    if (!aligned) return p.nj <= lists * 4;
+    return p.groups > 1 ? p.nj <= lists : p.nj <= 4 && p.ni * p.nk <= int64_t(1) << 25;
 }
 
 int product(const CallContext& c, Product p, Arena& a, cudaStream_t st) {

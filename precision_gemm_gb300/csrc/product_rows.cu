@@ -30,16 +30,18 @@ __device__ __forceinline__ uint4 stream16(const void* p) {
     return v;
 }
 
-// 16 bytes of consecutive elements, `valid` of them there.
-template <typename T>
-__device__ __forceinline__ uint4 load16(const T* p, bool vec, int64_t valid) {
-    constexpr int V = 16 / sizeof(T);
-    if (vec && valid >= V) return *reinterpret_cast<const uint4*>(p);
+// A lane's 16 bytes of a step, `left` elements of the row there from p on: consecutive
+// elements (VEC), or every 32nd, so that a warp's single loads fall on one line where rows
+// start anywhere (4096 x 4095 float32: one row 20 -> 10 us, 16 rows 57 -> 31).  FULL: the row reaches past the step.
+template <typename T, bool VEC, bool FULL>
+__device__ __forceinline__ uint4 load16(const T* p, int64_t left) {
+    constexpr int V = 16 / sizeof(T), apart = VEC ? 1 : 32;
+    if (VEC && (FULL || left >= V)) return *reinterpret_cast<const uint4*>(p);
     uint4 raw = make_uint4(0, 0, 0, 0);
     T* e = reinterpret_cast<T*>(&raw);
 #pragma unroll
     for (int t = 0; t < V; ++t)
-        if (t < valid) e[t] = p[t];
+        if (FULL || t * apart < left) e[t] = p[t * apart];
     return raw;
 }
 
@@ -89,9 +91,10 @@ __global__ void __launch_bounds__(32 * kWarps, B) product_rows_kernel(const Rows
     const int64_t s0 = steps * part / ks, s1 = steps * (part + 1) / ks;
     const bool all = i0 + F <= p.ni;  // F weight rows are there
     const int64_t ldw = p.a.ld;
-    const T* w = static_cast<const T*>(p.a.ptr) + g * p.a.stride + min(i0, p.ni - 1) * ldw + lane * V;
+    const int at_lane = VEC ? lane * V : lane;
+    const T* w = static_cast<const T*>(p.a.ptr) + g * p.a.stride + min(i0, p.ni - 1) * ldw + at_lane;
     for (int j0 = first; j0 < end; j0 += M) {
-        const T* x = static_cast<const T*>(p.b.ptr) + lane * V;
+        const T* x = static_cast<const T*>(p.b.ptr) + at_lane;
         uint32_t row[M];  // element offsets of the rows (the launcher keeps them under 2^32)
 #pragma unroll
         for (int m = 0; m < M; ++m) {
@@ -112,7 +115,7 @@ __global__ void __launch_bounds__(32 * kWarps, B) product_rows_kernel(const Rows
             }
         };
         int64_t s = s0;
-        if (VEC && all) {
+        if (all) {
             const int64_t whole = min(s1, p.nk / (32 * V));  // steps without an end of a row
             // U steps' weights are on their way at any time: a step's registers are filled again as
             // soon as it is used
@@ -120,7 +123,10 @@ __global__ void __launch_bounds__(32 * kWarps, B) product_rows_kernel(const Rows
             auto fetch = [&](uint4(&to)[F], int64_t at) {
                 if (at < whole) {
 #pragma unroll
-                    for (int f = 0; f < F; ++f) to[f] = stream16(w + f * ldw + at * 32 * V);
+                    for (int f = 0; f < F; ++f) {
+                        const T* from = w + f * ldw + at * 32 * V;
+                        to[f] = VEC ? stream16(from) : load16<T, VEC, true>(from, 0);
+                    }
                 }
             };
 #pragma unroll
@@ -131,7 +137,7 @@ __global__ void __launch_bounds__(32 * kWarps, B) product_rows_kernel(const Rows
                     if (s + u < whole) {
 #pragma unroll
                         for (int m = 0; m < M; ++m)
-                            add(raw[u], *reinterpret_cast<const uint4*>(x + row[m] + (s + u) * 32 * V), m);
+                            add(raw[u], load16<T, VEC, true>(x + row[m] + (s + u) * 32 * V, 0), m);
                         fetch(raw[u], s + u + U);
                     }
                 }
@@ -140,12 +146,12 @@ __global__ void __launch_bounds__(32 * kWarps, B) product_rows_kernel(const Rows
         }
 #pragma unroll 1
         for (; s < s1; ++s) {
-            const int64_t c = s * 32 * V, valid = p.nk - c - lane * V;
+            const int64_t c = s * 32 * V, left = p.nk - c - at_lane;
             uint4 raw[F];
 #pragma unroll
-            for (int f = 0; f < F; ++f) raw[f] = load16(w + (i0 + f < p.ni ? f : 0) * ldw + c, VEC, valid);
+            for (int f = 0; f < F; ++f) raw[f] = load16<T, VEC, false>(w + (i0 + f < p.ni ? f : 0) * ldw + c, left);
 #pragma unroll
-            for (int m = 0; m < M; ++m) add(raw, load16(x + row[m] + c, VEC, valid), m);
+            for (int m = 0; m < M; ++m) add(raw, load16<T, VEC, false>(x + row[m] + c, left), m);
         }
 #pragma unroll
         for (int f = 0; f < F; ++f)
@@ -190,27 +196,35 @@ cudaError_t run(const Product& p, int num_sms, cudaStream_t st) {
 
 template <typename T, bool VEC>
 cudaError_t dispatch(const Product& p, int rows, int num_sms, cudaStream_t st) {
+    constexpr int U = VEC || sizeof(T) == 4 ? 4 : 2;  // bfloat16 loaded one by one: four would spill
     switch (rows) {
-        case 1: return run<T, VEC, 1, 4, 4, 2>(p, num_sms, st);
-        case 2: return run<T, VEC, 2, 4, 4, 2>(p, num_sms, st);
-        case 3: return run<T, VEC, 3, 4, 4, 2>(p, num_sms, st);
-        case 4: return run<T, VEC, 4, 4, 2, 2>(p, num_sms, st);
-        case 5: return run<T, VEC, 5, 4, 2, 2>(p, num_sms, st);
-        case 6: return run<T, VEC, 6, 4, 2, 2>(p, num_sms, st);
-        case 7:
-        case 8: return run<T, VEC, 8, 4, 2, 2>(p, num_sms, st);
-        case 9:
-        case 10:
-        case 11:
-        case 12: return run<T, VEC, 12, 4, 1, 2>(p, num_sms, st);
-        default: return run<T, VEC, 16, 4, 1, 2>(p, num_sms, st);
+        case 1: return run<T, VEC, 1, 4, U, 2>(p, num_sms, st);
+        case 2: return run<T, VEC, 2, 4, U, 2>(p, num_sms, st);
+        case 3: return run<T, VEC, 3, 4, U, 2>(p, num_sms, st);
+        default: break;
     }
+    // more than four rows of bfloat16 are a longer list's, in further passes (few_rows)
+    if constexpr (std::is_same<T, float>::value) {
+        switch (rows) {
+            case 4: break;
+            case 5: return run<T, VEC, 5, 4, 2, 2>(p, num_sms, st);
+            case 6: return run<T, VEC, 6, 4, 2, 2>(p, num_sms, st);
+            case 7:
+            case 8: return run<T, VEC, 8, 4, 2, 2>(p, num_sms, st);
+            case 9:
+            case 10:
+            case 11:
+            case 12: return run<T, VEC, 12, 4, 1, 2>(p, num_sms, st);
+            default: return run<T, VEC, 16, 4, 1, 2>(p, num_sms, st);
+        }
+    }
+    return run<T, VEC, 4, 4, 2, 2>(p, num_sms, st);
 }
 
 template <typename T>
 cudaError_t launch(const Product& p, int rows, int num_sms, cudaStream_t st) {
     const bool vec = rows_aligned<T>(p.a.ptr, p.a.ld) && p.a.stride * sizeof(T) % 16 == 0 &&
-                     rows_aligned<T>(p.b.ptr, p.b.ld);
+                     rows_aligned<T>(p.b.ptr, p.b.rows == 1 ? 0 : p.b.ld);
     return vec ? dispatch<T, true>(p, rows, num_sms, st)
                : dispatch<T, false>(p, rows, num_sms, st);
 }

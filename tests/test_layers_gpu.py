@@ -612,3 +612,40 @@ def test_gradients_over_a_workspace_of_nan(dtype):
                 assert all(torch.equal(a, b) and bool(torch.isfinite(a).all()) for a, b in zip(got, experts))
     finally:
         pg.set_workspace(None, stream=s)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS.get)
+@pytest.mark.parametrize("pad_x,pad_w", [(0, 0), (1, 0), (0, 3), (5, 1)])
+@pytest.mark.parametrize("t", [1, 2, 3, 4, 5, 16, 17])
+def test_linear_few_rows_of_any_alignment(dtype, t, pad_x, pad_w):
+    """Rows long enough for whole steps of a warp's loads and an end, wherever they start."""
+    n, k = 70, 2104
+    g = _gen(t + 10 * pad_x + pad_w)
+    x, w, r = _draw(g, dtype, t, k), _draw(g, dtype, n, k, std=k ** -0.5), _draw(g, dtype, t, n)
+    y, z = pg.linear(_strided(x, pad_x, pad_x), _strided(w, pad_w, pad_w), None, "silu", r.cuda(), preact=True)
+    want, wz, den = R.linear(x, w, None, "silu", r)
+    R.close(y, want, den, dtype)
+    R.close(z, wz, den, dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS.get)
+@pytest.mark.parametrize("t,top,e,k", [(2, 4, 16, 2047), (20, 4, 16, 1031), (60, 4, 16, 1031), (40, 4, 8, 1032)])
+def test_expert_linear_few_rows_of_any_alignment(dtype, t, top, e, k):
+    n = 50
+    g = _gen(t + k)
+    ids = _ids(g, t, top, e, "dropped")
+    ls = R.lists(ids, e)
+    x, w = _draw(g, dtype, t, k), _draw(g, dtype, e, n, k, std=k ** -0.5)
+    y = pg.expert_linear(x.cuda(), w.cuda(), pg.expert_plan(ids.cuda(), e), None, "gelu", gather=True)
+    for i, first, end in _row_expert(ls, e):
+        src = torch.tensor(ls[2][first:end], dtype=torch.long) // top
+        want, _, den = R.linear(x[src], w[i], None, "gelu", None)
+        R.close(y[first:end], want, den, dtype)
+    assert not y[ls[1][-1]:].any()
+
+
+def test_linear_few_rows_of_a_large_matrix():
+    x, w = _draw(_gen(3), torch.bfloat16, 4, 4096), _draw(_gen(4), torch.bfloat16, 8320, 4096, std=4096 ** -0.5)
+    for t in (1, 4):
+        want, _, den = R.linear(x[:t], w, None, "none", None)
+        R.close(pg.linear(x[:t].cuda(), w.cuda()), want, den, torch.bfloat16)

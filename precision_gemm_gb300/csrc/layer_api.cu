@@ -130,7 +130,7 @@ int prepare(int dtype, Operand& o, int groups, int64_t cols, int64_t listed, boo
 //   350 / 372, 32 rows 437 / 387; rows at other than 16-byte boundaries: 4096 x 4095, 16
 //   rows 31 / 59; experts of 1024 x 2047, 16 rows 354 / 383;
 // bfloat16 at 16-byte boundaries, where L2 still holds much of the matrix:
-//   4096 x 4096: 1 row 5.4 / 13, 4 rows 9.9 / 13; 8192 x 8192: 1 row 27 / 26, 4 rows 32 / 26;
+//   4096 x 4096: 1 row 5.5 / 13, 4 rows 9.8 / 13; 8192 x 8192: 1 row 27 / 26, 4 rows 32 / 26;
 //   64 experts: 8 pairs 11 / 14, 64 pairs 38 / 38, 128 pairs 62 / 38;
 // bfloat16 at others, which the tensor cores read from a copy:
 //   4096 x 4095: 4 rows 13 / 27, 8 rows 23 / 28; 8192 x 8191: 4 rows 52 / 90, 8 rows 105 / 90;

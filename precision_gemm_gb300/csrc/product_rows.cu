@@ -6,6 +6,8 @@
 // are: the tensor-core path would first write them out in bfloat16 parts (10 bytes
 // per weight and 6 more to read them again).  A sum is formed by 32 lanes, each over
 // every 32nd group of k, in FP32; its warps' parts are added in order.
+// HBM-bound: 8192 x 8192 float32, one row, 43 us (6.2 TB/s); 4096 x 4096 bfloat16, from
+// HBM, 8.1 us (4.1 TB/s, start and end of the kernel included).
 #include <algorithm>
 
 #include "layers.h"
@@ -196,11 +198,16 @@ cudaError_t run(const Product& p, int num_sms, cudaStream_t st) {
 
 template <typename T, bool VEC>
 cudaError_t dispatch(const Product& p, int rows, int num_sms, cudaStream_t st) {
-    constexpr int U = VEC || sizeof(T) == 4 ? 4 : 2;  // bfloat16 loaded one by one: four would spill
+    // Up to three rows of float32, two of bfloat16, have registers for eight weight rows at once:
+    // x is read half as often (HBM to registers, 8192 x 8192 float32, one row: four weight rows of
+    // four steps 49.8 us, eight of two 43.5, eight of one 43.4; 2048 x 2048: 6.8, 6.0, 5.2;
+    // 4096 x 4096 bfloat16: 8.7, 8.1, 9.5).  bfloat16 loaded one by one would spill.
+    constexpr bool f32 = sizeof(T) == 4;
+    constexpr int F = f32 || VEC ? 8 : 4, U = f32 ? 1 : 2;
     switch (rows) {
-        case 1: return run<T, VEC, 1, 4, U, 2>(p, num_sms, st);
-        case 2: return run<T, VEC, 2, 4, U, 2>(p, num_sms, st);
-        case 3: return run<T, VEC, 3, 4, U, 2>(p, num_sms, st);
+        case 1: return run<T, VEC, 1, F, U, 2>(p, num_sms, st);
+        case 2: return run<T, VEC, 2, F, U, 2>(p, num_sms, st);
+        case 3: return run<T, VEC, 3, f32 ? 8 : 4, f32 ? 1 : (VEC ? 4 : 2), 2>(p, num_sms, st);
         default: break;
     }
     // more than four rows of bfloat16 are a longer list's, in further passes (few_rows)

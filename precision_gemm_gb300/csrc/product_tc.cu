@@ -18,7 +18,7 @@
 // rows that were copied together first: a gather of four 128-byte pieces takes the unit
 // 88 cycles, hidden behind the weights' time in narrow tiles only (65536 x 1024 x 2048,
 // 64 experts: 0.70 ms gathered by the TMA unit, 0.43 ms by 16-byte asynchronous copies
-// of four more warps, 0.21 ms plus a copy of 0.05 ms).
+// of four more warps, 0.18 ms plus a copy of 0.05 ms).
 //
 // float32 operands come as three bfloat16 parts x = x0 + x1 + x2 (pack_kernel), whose
 // six products of weight 2^-16 and above, the smallest first, are summed over a chunk

@@ -124,8 +124,8 @@ int prepare(int dtype, Operand& o, int groups, int64_t cols, int64_t listed, boo
 // Whether a product runs on the kernel that streams the weights once for a few rows.
 // Measured against the tensor cores (us, rows / tensor cores).
 // float32, whose weights those read in parts that are written first:
-//   one matrix, 8192 x 2048: 8 rows 17 / 60, 16 rows 28 / 60, 24 rows 50 / 60; 2048 x 2048:
-//   16 rows 14 / 24, 24 rows 25 / 25; 4096 x 64: 4 rows 4.0 / 6.9, 16 rows 11 / 6.8;
+//   one matrix, 8192 x 2048: 8 rows 17 / 52, 16 rows 28 / 52, 24 rows 50 / 52; 2048 x 2048:
+//   16 rows 14 / 20, 24 rows 25 / 20; 4096 x 64: 4 rows 4.0 / 6.9, 16 rows 11 / 6.8;
 //   60 experts of 1024 x k with uneven lists, k = 64: 1 row each 12 / 18, 4 rows 33 / 20;
 //   128: 4 rows 26 / 30, 8 rows 42 / 30; 256: 8 rows 49 / 53, 16 rows 72 / 54; 512: 16 rows
 //   99 / 100; 2048 (64 experts): 24 rows 350 / 372, 32 rows 437 / 387 -- every pass over a
@@ -133,7 +133,8 @@ int prepare(int dtype, Operand& o, int groups, int64_t cols, int64_t listed, boo
 //   rows at other than 16-byte boundaries: 4096 x 4095, 16 rows 31 / 59; 64 experts of 1024 x
 //   2047, 16 rows 354 / 383.
 // bfloat16 at 16-byte boundaries, where L2 still holds much of the matrix:
-//   4096 x 4096: 1 row 5.5 / 13, 4 rows 9.8 / 13; 8192 x 8192: 1 row 27 / 26, 4 rows 32 / 26;
+//   4096 x 4096: 1 row 5.5 / 8.8, 2 rows 7.3 / 8.8, 4 rows 9.8 / 8.8; 2048 x 8192: 2 rows
+//   7.4 / 9.5, 4 rows 10.3 / 9.5; 8192 x 8192: 1 row 27 / 26, 4 rows 32 / 26;
 //   64 experts of 1024 x 2048: 8 pairs 11 / 14, 32 pairs 24 / 26, 64 pairs 38 / 38; 60 of
 //   1024 x 64: 5 pairs 8.0 / 5.3; of 1024 x 256: 5 pairs 5.9 / 6.2.
 // bfloat16 at others, which the tensor cores read from a copy:
@@ -148,7 +149,7 @@ bool few_rows(const Product& p) {
         return p.groups == 1 ? p.nj <= std::min<int64_t>(16, p.nk / 8 + 1)
                              : p.nj <= lists * std::min<int64_t>(aligned ? 24 : 16, p.nk / 32 + 1);
     if (!aligned) return p.nj <= lists * std::min<int64_t>(4, p.nk / 64 + 1);
-    return p.groups == 1 ? p.nj <= 4 && p.ni * p.nk <= int64_t(1) << 25 : 2 * p.nj <= p.groups && p.nk >= 256;
+    return p.groups == 1 ? p.nj <= 3 && p.ni * p.nk <= int64_t(1) << 25 : 2 * p.nj <= p.groups && p.nk >= 256;
 }
 
 int product(const CallContext& c, Product p, Arena& a, cudaStream_t st) {
@@ -175,7 +176,7 @@ int product(const CallContext& c, Product p, Arena& a, cudaStream_t st) {
             ++launches;
         }
     }
-    void* ws = a.take(t.part_bytes + t.count_bytes);
+    void* ws = a.take(t.part_bytes + t.info_bytes);
     if (!a.dry()) {
         PG_CHECK(launch_product_tc(c, p, t, p.dtype == SGEMM_F32 ? 3 : 1, ws, st, &launches));
         call_count(launches);

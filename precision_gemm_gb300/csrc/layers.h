@@ -350,7 +350,7 @@ struct TcPlan {
     int64_t tiles, whole;  // the first `whole` tiles have one slice
     int split, split_kb;
     bool halved;            // the others are halved along j instead of cut along k
-    size_t part_bytes, count_bytes;
+    size_t part_bytes, info_bytes;
 };
 TcPlan plan_tc(const Product& p, int num_sms, int force_bn, int force_split);
 int launch_product_tc(const CallContext& c, const Product& p, const TcPlan& t, int parts, void* ws, cudaStream_t st,

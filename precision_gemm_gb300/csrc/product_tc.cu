@@ -29,8 +29,9 @@
 // Warp roles as in tc2_kernel.cu: warp 0 loads, warp 1 issues MMAs, warps 2-9 drain
 // TMEM (double-buffered: a unit's epilogue overlaps the next unit's MMAs).  The kernel
 // is persistent; a unit is (tile, K slice).  With few tiles each tile's k is cut into
-// slices; every slice stores its block, and per epilogue warp the slice that arrives
-// last adds the blocks in slice order.
+// slices; every slice stores its block, and sum_slices_kernel adds the blocks in slice
+// order on all SMs (100 x 100 x 30000 bfloat16: 11 us, 27 when the slice that arrived last
+// added them; 16 rows of 2048 x 8192: 9.5 and 14.4).
 #include <algorithm>
 #include <cstring>
 #include <type_traits>
@@ -93,8 +94,8 @@ struct Params {
     void* preact;
     int64_t ldz;
     int32_t out_f32;
-    float* part;
-    int* count;
+    float* part;  // the slices' blocks
+    int4* info;   // {tiles cut in slices}, then of each {i0, j0, j_end, group}
     uint64_t timeout_ns;
     int* status;
     int32_t debug_flags;
@@ -106,10 +107,9 @@ __device__ __forceinline__ int b_part(int s, int segs) { return segs == 1 ? 0 : 
 
 // Columns jb .. jb + N of a tile, sums v, for this thread's i < ni; `jn` of them are rows
 // of out.
-template <typename T, typename TO>
-__device__ __forceinline__ void finish(const Params& p, float (&v)[kCols], float bias, int64_t out_base, int64_t i,
+template <typename T, typename TO, int N>
+__device__ __forceinline__ void finish(const Params& p, float (&v)[N], float bias, int64_t out_base, int64_t i,
                                        int64_t jb, int jn) {
-    constexpr int N = kCols;
     float r[N];
     if (p.residual) {
         const T* src = static_cast<const T*>(p.residual) + jb * p.ldr + i;
@@ -501,6 +501,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
             }
         }
+        if (p.part && blockIdx.x == 0 && epi == 0 && lane == 0) p.info[0] = make_int4(tiles - whole, 0, 0, 0);
         float bias = 0.0f;  // of the unit's group and this thread's i
         auto finish_chunk = [&](const Unit& x, float(&v)[kCols], int c) {
             const int64_t i = x.i0 + kBI * rank + 32 * q + lane;
@@ -608,43 +609,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
             }
             if (any) free_sums(buf);
-            if (block) {
-                // Publish this slice's block; the last slice of this warp's region to arrive
-                // adds all of them in slice order.
-                __threadfence();
-                __syncwarp();
-                int arrived = 0;
-                if (lane == 0)
-                    arrived = atomicAdd(p.count + (static_cast<int64_t>(x.tile) * 2 + rank) * kEpiWarps + epi, 1);
-                arrived = __shfl_sync(0xffffffffu, arrived, 0);
-                if (arrived == p.split - 1) {
-                    __threadfence();
-                    const float* first = p.part + static_cast<int64_t>(x.tile) * p.split * (2 * kBI * BN) +
-                                         kBI * rank + 32 * q + lane;
-#pragma unroll 1
-                    for (int c = half; kCols * c < cols; c += 2) {
-                        float f[kCols];
-#pragma unroll
-                        for (int t = 0; t < kCols; ++t) f[t] = 0.0f;
-                        for (int s0 = 0; s0 < p.split; s0 += 4) {  // four slices' loads in flight
-                            float b[4][kCols];
-#pragma unroll
-                            for (int s = 0; s < 4; ++s) {
-                                const float* src =
-                                    first + static_cast<int64_t>(s0 + s) * (2 * kBI * BN) + kCols * c * (2 * kBI);
-#pragma unroll
-                                for (int t = 0; t < kCols; ++t)
-                                    b[s][t] = s0 + s < p.split ? __ldcg(src + t * (2 * kBI)) : 0.0f;
-                            }
-#pragma unroll
-                            for (int s = 0; s < 4; ++s)
-#pragma unroll
-                                for (int t = 0; t < kCols; ++t) f[t] += b[s][t];
-                        }
-                        finish_chunk(x, f, c);
-                    }
-                }
-            }
+            if (block && x.slice == 0 && rank == 0 && epi == 0 && lane == 0)
+                p.info[1 + x.tile] = make_int4(x.i0, x.j0, x.j_end, x.g);
         }
     }
 
@@ -656,6 +622,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM_COLS)
                      : "memory");
     }
+}
+
+// The tiles that were cut along k: thread i of a block adds the slices of kSumCols columns
+// in their order and finishes them.  The tiles' places are checked against the matrix, since
+// a product that gave up (a wait that expired) may not have written them.
+constexpr int kSumCols = 4;
+template <bool F32>
+__global__ void __launch_bounds__(2 * kBI) sum_slices_kernel(const Params p, int bn, int most) {
+    using T = typename std::conditional<F32, float, bf16>::type;
+    pdl_trigger();
+    pdl_wait();
+    const int per = bn / kSumCols, tile = blockIdx.x / per, c0 = (blockIdx.x - tile * per) * kSumCols;
+    if (tile >= min(p.info[0].x, most)) return;
+    const int4 at = p.info[1 + tile];
+    const int64_t i = static_cast<int64_t>(at.x) + threadIdx.x;
+    const int jn = at.z - at.y - c0;
+    if (at.x < 0 || i >= p.ni || at.y < 0 || at.z > p.nj || jn <= 0 || at.w < 0 || at.w >= p.groups) return;
+    const float* src = p.part + static_cast<int64_t>(tile) * p.split * (2 * kBI * bn) + c0 * (2 * kBI) + threadIdx.x;
+    float v[kSumCols] = {};
+    for (int s0 = 0; s0 < p.split; s0 += 8) {
+        float b[8][kSumCols];
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+#pragma unroll
+            for (int t = 0; t < kSumCols; ++t)
+                b[s][t] = s0 + s < p.split
+                              ? __ldcg(src + static_cast<int64_t>(s0 + s) * (2 * kBI * bn) + t * (2 * kBI))
+                              : 0.0f;
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+#pragma unroll
+            for (int t = 0; t < kSumCols; ++t) v[t] += b[s][t];
+    }
+    const float bias =
+        p.bias ? to_float(static_cast<const T*>(p.bias)[static_cast<int64_t>(at.w) * p.ni + i]) : 0.0f;
+    const int64_t base = p.rows_on_k ? at.w * p.out_stride : 0;
+    if (F32 || !p.out_f32)
+        finish<T, T>(p, v, bias, base, i, at.y + c0, jn);
+    else
+        finish<T, float>(p, v, bias, base, i, at.y + c0, jn);
 }
 
 // x = x0 + x1 + x2 with x0 = bf16(x), x1 = bf16(x - x0), x2 = bf16(x - x0 - x1); both
@@ -730,8 +736,7 @@ __global__ void __launch_bounds__(256) copy_rows_kernel(const bf16* src, int64_t
 }
 
 template <int BN, bool F32>
-cudaError_t launch(const CUtensorMap (&m)[6], const Params& p, int64_t units, bool after_previous, int num_sms,
-                   cudaStream_t st) {
+cudaError_t launch(const CUtensorMap (&m)[6], const Params& p, int64_t units, int num_sms, cudaStream_t st) {
     using C = Cfg<BN>;
     auto kern = product_tc_kernel<BN, F32>;
     static std::atomic<uint64_t> smem_set{0};
@@ -761,7 +766,7 @@ cudaError_t launch(const CUtensorMap (&m)[6], const Params& p, int64_t units, bo
         if (dev >= 0 && dev < 64) resident[dev] = most;
     }
     const int64_t clusters = std::max<int64_t>(1, std::min<int64_t>(units, most));
-    return launch_kernel(after_previous, kern, dim3(static_cast<unsigned>(2 * clusters)), dim3(kThreads), C::SMEM,
+    return launch_kernel(true, kern, dim3(static_cast<unsigned>(2 * clusters)), dim3(kThreads), C::SMEM,
                          st, m[0], m[1], m[2], m[3], m[4], m[5], p);
 }
 
@@ -797,18 +802,19 @@ cudaError_t launch_pack(int dtype, const PackJob* jobs, int count, int num_sms, 
 }
 
 // Tile width, K slices and the last wave, by an estimate of the kernel's time in us:
-//     waves * steps * step(bn) + end(bn) [+ kSplit]
+//     waves * steps * step(bn) + end(bn) [+ kSplit + kBlockMB * MB of the slices' blocks]
 // with one step per k block and product of parts.  Measured at 4864 x 4096 x 4096
 // (whole waves at every width): a step of all pairs takes 0.34 us at 256 columns, 0.19
 // at 128, 0.14 at 64 (operand feed: A's 128 rows per CTA are loaded whatever the width);
 // the end is the last tile's epilogue, which no MMAs hide (most with a residual, whose
-// reads it waits for); kSplit what clearing counters, storing and adding the slices'
-// blocks took.  Against the widest tile that the rows fill and a K split under one wave:
-// 300 x 4096 x 4096 bfloat16 29.6 -> 16.2 us, 1000^3 25 -> 13, 1500 x 3000 x 777 float32
-// with residual 67 -> 56.  Grouped rows are counted by their average length, since the
-// lengths are known on the device alone.
+// reads it waits for); kSplit and kBlockMB are the adding kernel and the blocks' way to it.
+// Against tiles that are not cut: 16 rows of 4096 x 4096 bfloat16 12.7 -> 8.8 us, of 2048 x
+// 8192 21.6 -> 9.5; float32, 40 rows of 2048 x 2048 42 -> 20, 400 rows 43 -> 33, 700^3 18.3
+// -> 16.9.  Tile widths: 1500 x 3000 x 777 float32 with residual at 256 columns 67, at 128
+// 42.  Grouped rows are counted by their average length, since the lengths are known on the
+// device alone.
 TcPlan plan_tc(const Product& p, int num_sms, int force_bn, int force_split) {
-    static constexpr double kSplit = 12.0;
+    static constexpr double kSplit = 2.0, kBlockMB = 0.2;
     const int pairs = std::max(num_sms / 2, 1);
     const int64_t tiles_i = cdiv(p.ni, 2 * kBI), kb = cdiv(p.nk, kBK);
     const int64_t lists = p.rows_on_k ? 1 : std::max<int64_t>(1, std::min<int64_t>(p.groups, p.nj));
@@ -834,12 +840,15 @@ TcPlan plan_tc(const Product& p, int num_sms, int force_bn, int force_split) {
         t.halved = bn == 256 && force_split == 0 && p.groups == 1 && waves > 1 && last > 0 && 2 * last <= pairs;
         t.whole = last;  // for now: the tiles of the last wave
         double us = (t.halved ? static_cast<double>(waves) - 0.44 : static_cast<double>(waves)) * steps * step + end;
-        // K slices that fill the wave (not groups that share out k: their lengths differ)
-        if (!(p.rows_on_k && p.groups > 1) && kb > 1 && (force_split > 0 || 2 * tiles <= pairs)) {
+        // K slices that fill one, two or three waves (not groups that share out k: their lengths differ)
+        for (int64_t w = 1; w <= 3 && !(p.rows_on_k && p.groups > 1) && kb > 1; ++w) {
             const int64_t want = force_split > 0 ? std::min<int64_t>(force_split, kb)
-                                                 : std::min<int64_t>(pairs / tiles, std::max<int64_t>(kb / 4, 1));
+                                                 : std::min<int64_t>(w * pairs / tiles, std::max<int64_t>(kb / 4, 1));
+            if (want < 2) continue;
             const int64_t split_kb = cdiv(kb, want), split = cdiv(kb, split_kb);
-            const double cut_us = segs * split_kb * step + end + kSplit;
+            const double blocks_mb = static_cast<double>(tiles) * split * bn * (2 * kBI * 4) * 1e-6;
+            const double cut_us =
+                static_cast<double>(cdiv(tiles * split, pairs)) * segs * split_kb * step + end + kSplit + kBlockMB * blocks_mb;
             if (split > 1 && (force_split > 0 || cut_us < us)) {
                 us = cut_us;
                 t.split = static_cast<int>(split);
@@ -860,7 +869,7 @@ TcPlan plan_tc(const Product& p, int num_sms, int force_bn, int force_split) {
     t.gather = t.bn <= 64 && !p.rows_on_k;
     if (t.split > 1) {
         t.part_bytes = region(static_cast<size_t>(t.tiles) * t.split * 2 * kBI * t.bn * 4);
-        t.count_bytes = region(static_cast<size_t>(t.tiles) * 2 * kEpiWarps * 4);
+        t.info_bytes = region(static_cast<size_t>(t.tiles + 1) * sizeof(int4));
     }
     return t;
 }
@@ -909,11 +918,8 @@ int launch_product_tc(const CallContext& c, const Product& p, const TcPlan& t, i
     q.debug_flags = c.debug_flags;
     if (t.split > 1) {
         q.part = static_cast<float*>(ws);
-        q.count = reinterpret_cast<int*>(static_cast<char*>(ws) + t.part_bytes);
-        const cudaError_t e = cudaMemsetAsync(q.count, 0, t.count_bytes, st);
-        if (e != cudaSuccess) return call_fail_cuda(e, "cudaMemsetAsync (K slice counters)");
+        q.info = reinterpret_cast<int4*>(static_cast<char*>(ws) + t.part_bytes);
     }
-    const bool after_previous = t.split == 1;  // no memset in between
     // Columns of each matrix.  Packed rows along i or j count as whole: boxes that reach past
     // a matrix load slower, and what lies there only meets results that are not stored.
     const int64_t cols_a = p.a.k_contiguous ? p.nk : (p.a.packed ? p.a.ld : p.ni);
@@ -944,15 +950,22 @@ int launch_product_tc(const CallContext& c, const Product& p, const TcPlan& t, i
     auto with_bn = [&](auto f32) {
         constexpr bool F = decltype(f32)::value;
         switch (t.bn) {
-            case 32: return launch<32, F>(m, q, units, after_previous, c.sms, st);
-            case 64: return launch<64, F>(m, q, units, after_previous, c.sms, st);
-            case 128: return launch<128, F>(m, q, units, after_previous, c.sms, st);
-            default: return launch<256, F>(m, q, units, after_previous, c.sms, st);
+            case 32: return launch<32, F>(m, q, units, c.sms, st);
+            case 64: return launch<64, F>(m, q, units, c.sms, st);
+            case 128: return launch<128, F>(m, q, units, c.sms, st);
+            default: return launch<256, F>(m, q, units, c.sms, st);
         }
     };
     e = parts == 3 ? with_bn(std::true_type()) : with_bn(std::false_type());
     if (e != cudaSuccess) return call_fail_cuda(e, "tensor-core layer product");
     *launches += 1;
+    if (t.split > 1) {
+        auto sum = parts == 3 ? sum_slices_kernel<true> : sum_slices_kernel<false>;
+        e = launch_kernel(true, sum, dim3(static_cast<unsigned>(t.tiles * (t.bn / kSumCols))), dim3(2 * kBI), 0, st, q,
+                          t.bn, static_cast<int>(t.tiles));
+        if (e != cudaSuccess) return call_fail_cuda(e, "sum of K slices");
+        *launches += 1;
+    }
     return 0;
 }
 

@@ -666,3 +666,52 @@ def test_expert_linear_short_rows(dtype, k, t):
         want, _, den = R.linear(x[src], w[i], None, "silu", None)
         R.close(y[first:end], want, den, dtype)
     assert not y[ls[1][-1]:].any()
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS.get)
+@pytest.mark.parametrize("t,n,k", [(20, 300, 4100), (40, 513, 2050), (300, 257, 1537)])
+def test_k_slices_with_every_part_of_the_epilogue(dtype, t, n, k):
+    g = _gen(t)
+    x, w, b = _draw(g, dtype, t, k), _draw(g, dtype, n, k, std=k ** -0.5), _draw(g, dtype, n)
+    r, dy = _draw(g, dtype, t, n), _draw(g, dtype, t, n)
+    want, wz, den = R.linear(x, w, b, "gelu", r)
+    grads, dens = R.linear_backward(dy, x, w, "silu", wz.to(dtype))
+    try:
+        for split in (0, 2, 5, 9):
+            pg.force_plan(0, split)
+            y, z = pg.linear(_strided(x, 3, 1), w.cuda(), b.cuda(), "gelu", _strided(r, 5, 2), preact=True)
+            R.close(y, want, den, dtype)
+            R.close(z, wz, den, dtype)
+            got = pg.linear_backward(dy.cuda(), x.cuda(), w.cuda(), "silu", wz.to(dtype).cuda())
+            _check_backward(got, grads, dens, dtype, "silu")
+    finally:
+        pg.force_plan(0, 0)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS.get)
+@pytest.mark.parametrize("split", [0, 3, 8])
+def test_k_slices_of_experts(dtype, split):
+    """Lists of uneven lengths, some empty, cut along k."""
+    t, top, e, n, k = 70, 2, 5, 200, 1100
+    g = _gen(21)
+    ids = _ids(g, t, top, e, "dropped")
+    ls = R.lists(ids, e)
+    x, w, b = _draw(g, dtype, t, k), _draw(g, dtype, e, n, k, std=k ** -0.5), _draw(g, dtype, e, n)
+    plan = pg.expert_plan(ids.cuda(), e)
+    try:
+        pg.force_plan(0, split)
+        y, z = pg.expert_linear(x.cuda(), w.cuda(), plan, b.cuda(), "relu", gather=True, preact=True)
+        dx, _, _ = pg.expert_linear_backward(y, x.cuda(), w.cuda(), plan, gather=True, bias=False, need_dw=False)
+    finally:
+        pg.force_plan(0, 0)
+    wx, xden = torch.zeros(t, k, dtype=torch.float64), torch.zeros(t, k, dtype=torch.float64)
+    for i, first, end in _row_expert(ls, e):
+        src = torch.tensor(ls[2][first:end], dtype=torch.long) // top
+        want, wz, den = R.linear(x[src], w[i], b[i], "relu", None)
+        R.close(y[first:end], want, den, dtype)
+        R.close(z[first:end], wz, den, dtype)
+        got = y[first:end].cpu().double()
+        wx.index_add_(0, src, got @ w[i].double())
+        xden.index_add_(0, src, got.abs() @ w[i].double().abs())
+    R.close(dx, wx, xden, dtype, slope=1.0)
+    assert not y[ls[1][-1]:].any() and not z[ls[1][-1]:].any()

@@ -864,7 +864,7 @@ TcPlan plan_tc(const Product& p, int num_sms, int force_bn, int force_split) {
     TcPlan t = best;
     const int64_t last = t.whole;
     t.tiles = p.rows_on_k ? tiles_i * cdiv(p.nj, t.bn) * p.groups
-                          : tiles_i * (cdiv(p.nj, t.bn) + (p.groups > 1 ? p.groups : 0));
+                          : tiles_i * (cdiv(p.nj, t.bn) + (p.groups > 1 ? lists : 0));
     t.whole = t.split > 1 ? 0 : (t.halved ? t.tiles - last : t.tiles);
     t.gather = t.bn <= 64 && !p.rows_on_k;
     if (t.split > 1) {

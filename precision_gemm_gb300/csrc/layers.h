@@ -343,7 +343,7 @@ inline int64_t packed_ld(int64_t cols) {
 cudaError_t launch_pack(int dtype, const PackJob* jobs, int count, int num_sms, cudaStream_t st);
 
 // Tensor-core products: tile width, tiles (an upper bound for grouped rows), K slices,
-// and the workspace of the slices' blocks and counters.
+// and the workspace of the slices' blocks and their places.
 struct TcPlan {
     int bn;
     bool gather;            // listed rows of b are gathered by the kernel

@@ -440,7 +440,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int u = pair; u < units && ok; u += pairs) {
                 const Unit x = unit_of(u);
                 const int nkb = __shfl_sync(0xffffffffu, x.nkb, 0);
-                const int group_rows = __shfl_sync(0xffffffffu, x.k_end - x.k0, 0);
+                const int rows_left = __shfl_sync(0xffffffffu, x.k_end - x.k0 - x.kb0 * kBK, 0);  // from kb0 on
                 const uint32_t idesc =
                     idesc_bf16(2 * kBI, __shfl_sync(0xffffffffu, x.n, 0), p.a_mn != 0, p.b_mn != 0);
                 for (int c0 = 0; c0 < nkb && ok; c0 += p.chunk_kb, ++chunk) {
@@ -459,7 +459,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         tc_fence_after_sync();
                         const uint32_t o = static_cast<uint32_t>(slot_i * C::STAGE_BYTES) >> 4;
                         // a group's last block stops at its last run of 16 rows
-                        const int left = ragged ? group_rows - (kb % (min(c0 + p.chunk_kb, nkb) - c0) + c0) * kBK : kBK;
+                        const int left = ragged ? rows_left - (kb % (min(c0 + p.chunk_kb, nkb) - c0) + c0) * kBK : kBK;
 #pragma unroll
                         for (int kk = 0; kk < kBK / 16; ++kk) {
                             if (16 * kk >= left) break;

@@ -715,3 +715,30 @@ def test_k_slices_of_experts(dtype, split):
         xden.index_add_(0, src, got.abs() @ w[i].double().abs())
     R.close(dx, wx, xden, dtype, slope=1.0)
     assert not y[ls[1][-1]:].any() and not z[ls[1][-1]:].any()
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS.get)
+@pytest.mark.parametrize("split", [0, 2, 3, 7])
+@pytest.mark.parametrize("gather", [True, False])
+def test_k_slices_of_one_experts_gradient(dtype, split, gather):
+    """One expert's rows as k of dw, cut into slices of which the last ends inside a block (700 of
+    1000 pairs) or is empty, the rows after it NaN."""
+    t, n, k, kept = 1000, 72, 136, 700
+    g = _gen(31)
+    ids = torch.full((t, 1), -1, dtype=torch.int32)
+    ids[torch.randperm(t, generator=g)[:kept]] = 0
+    plan = pg.expert_plan(ids.cuda(), 1)
+    src = torch.nonzero(ids[:, 0] == 0)[:, 0]
+    x, w = _draw(g, dtype, t, k), _draw(g, dtype, 1, n, k, std=k ** -0.5)
+    dy, z = _draw(g, dtype, t, n), _draw(g, dtype, t, n)
+    dy[kept:] = math.nan
+    rows = src if gather else torch.arange(kept)
+    if not gather:
+        x[kept:] = math.nan
+    try:
+        pg.force_plan(0, split)
+        _, dw, db = pg.expert_linear_backward(dy.cuda(), x.cuda(), w.cuda(), plan, "silu", z.cuda(), gather=gather)
+    finally:
+        pg.force_plan(0, 0)
+    want, den = R.linear_backward(dy[:kept], x[rows], w[0], "silu", z[:kept])
+    _check_backward((dw[0], db[0]), want[1:], den[1:], dtype, "silu")

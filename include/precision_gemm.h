@@ -486,7 +486,9 @@ int sgemm_expert_plan(int64_t tokens, int top, int experts, const int32_t *ids, 
 /*
  * sgemm_expert_linear -- y[r] = act(w[e] x[r'] + bias[e]) for every row r of expert
  * e's list, where r' is the row's token (gather != 0: x is tokens x k) or r
- * itself (x is tokens*top x k).  Rows of no expert come out zero.
+ * itself (x is tokens*top x k).  Rows of no expert come out zero.  Where a caller's
+ * own list holds an entry that is no pair (outside [0, tokens*top)), its gathered row
+ * reads as zeros.
  *
  *   dtype (1); tokens, top, experts (2-4); n, k (5, 6); gather (7); x, ldx (8, 9);
  *   w, ldw, stride_w (10-12): expert e's n x k matrix at w + e*stride_w;

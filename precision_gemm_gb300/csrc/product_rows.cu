@@ -101,6 +101,7 @@ __global__ void __launch_bounds__(32 * kWarps, B) product_rows_kernel(const Rows
 #pragma unroll
         for (int m = 0; m < M; ++m) {
             const int64_t j = min(j0 + m, end - 1);
+            // a row that the list does not name loads row 0, and its sums are dropped below
             const int64_t r = p.b.list ? max(gathered_row(p.b.list, p.b.top, j, p.b.rows), int64_t(0)) : j;
             row[m] = static_cast<uint32_t>(r * p.b.ld);
         }
@@ -170,6 +171,7 @@ __global__ void __launch_bounds__(32 * kWarps, B) product_rows_kernel(const Rows
             if (i < p.ni && j < end) {
                 float z = 0.0f;
                 for (int k = 0; k < ks; ++k) z += sums[li / F * ks + k][li % F * M + m];
+                if (p.b.list && gathered_row(p.b.list, p.b.top, j, p.b.rows) < 0) z = 0.0f;  // it reads as zeros
                 if (p.bias) z += to_float(static_cast<const T*>(p.bias)[g * p.ni + i]);
                 if (p.preact) static_cast<T*>(p.preact)[j * p.ldz + i] = from_float<T>(z);
                 float y = 0.0f;

@@ -275,7 +275,8 @@ class ExpertPlan:
     """The experts' row lists (int32 tensors): counts (experts), offsets (experts + 1),
     rows (tokens * top: the pair token * top + choice of each row, -1 for rows of no
     expert) and slots (tokens, top: the row of each pair, -1 where its id names no
-    expert).  expert_plan makes one; one can also be made of four such tensors."""
+    expert).  expert_plan makes one; one can also be made of four such tensors, where an
+    entry of rows inside an expert's list may name no pair (-1): gathered, it reads as zeros."""
 
     __slots__ = ("tokens", "top", "experts", "index", "_store", "_lists", "_addresses")
 

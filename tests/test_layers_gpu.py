@@ -742,3 +742,44 @@ def test_k_slices_of_one_experts_gradient(dtype, split, gather):
         pg.force_plan(0, 0)
     want, den = R.linear_backward(dy[:kept], x[rows], w[0], "silu", z[:kept])
     _check_backward((dw[0], db[0]), want[1:], den[1:], dtype, "silu")
+
+
+# ---- rows without a pair, other empty shapes, long sums ---------------------------------
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS.get)
+@pytest.mark.parametrize("capacity,k", [(2, 1031), (3, 520), (40, 520)])
+def test_listed_rows_of_no_pair_read_as_zeros(dtype, capacity, k):
+    """Lists of a fixed capacity whose ends name no pair (-1, or a pair past the last), in a plan
+    made of four tensors: such a row is act(bias) whichever kernel the sizes lead to, and adds
+    nothing to dw."""
+    e, n = 6, 72
+    t = e * capacity
+    g = _gen(capacity + k)
+    rows = torch.randperm(t, generator=g).to(torch.int32).view(e, capacity)
+    rows[:, capacity - 1] = -1
+    rows[2, capacity - 1] = t + 5
+    rows[4] = -1
+    rows = rows.reshape(-1)
+    slots = torch.full((t, 1), -1, dtype=torch.int32)
+    held = (rows >= 0) & (rows < t)
+    at = torch.nonzero(held)[:, 0]
+    slots[rows[held].long(), 0] = at.to(torch.int32)
+    plan = pg.ExpertPlan(torch.full((e,), capacity, dtype=torch.int32, device="cuda"),
+                         torch.arange(0, t + 1, capacity, dtype=torch.int32, device="cuda"), rows.cuda(), slots.cuda())
+    x, w, b = _draw(g, dtype, t, k), _draw(g, dtype, e, n, k, std=k ** -0.5), _draw(g, dtype, e, n)
+    dy, z = _draw(g, dtype, t, n), _draw(g, dtype, t, n)
+    read = torch.where(held[:, None], x[rows.clamp(0, t - 1).long()], torch.zeros((), dtype=dtype))
+    y = pg.expert_linear(x.cuda(), w.cuda(), plan, b.cuda(), "silu", gather=True)
+    _, dw, _ = pg.expert_linear_backward(dy.cuda(), x.cuda(), w.cuda(), plan, "silu", z.cuda(), gather=True)
+    for i in range(e):
+        part = slice(i * capacity, (i + 1) * capacity)
+        want, _, den = R.linear(read[part], w[i], b[i], "silu", None)
+        R.close(y[part], want, den, dtype)
+        (_, want, _), (_, den, _) = R.linear_backward(dy[part], read[part], w[i], "silu", z[part])
+        R.close(dw[i], want, den, dtype, slope=1.0, inner=_inner(dtype, "silu"))
+    # whatever token 0 holds, a row of no pair does not see it
+    x[0] = math.nan
+    again = pg.expert_linear(x.cuda(), w.cuda(), plan, b.cuda(), "silu", gather=True)
+    sees = (rows == 0).cuda()
+    assert torch.isnan(again[sees]).all() and torch.equal(again[~sees], y[~sees])

@@ -358,7 +358,8 @@ int sgemm_debug_flags(int flags);
  * (i, j) of a matrix with leading dimension ld is X[i*ld + j], ld >= its columns.
  * Every operand of one call has the element type `dtype`; all sums, scores and
  * routing weights are FP32.  SGEMM_BF16 products are exact and accumulated in
- * FP32, each result rounded once.  SGEMM_F32 products have FP32 accuracy, not
+ * FP32, each result rounded once; the tensor cores truncate their sums, which loses
+ * at most 2^-13 of the sum of the terms' magnitudes, whatever its length.  SGEMM_F32 products have FP32 accuracy, not
  * TF32's (relative error in the 2-norm under 1e-6 at k = 4096): the tensor cores
  * take each operand as three bfloat16 parts, which hold its 24 bits from 2^-109
  * up (below, the low bits are lost, down to 2^-133); such an operand has at most

@@ -23,8 +23,10 @@
 // float32 operands come as three bfloat16 parts x = x0 + x1 + x2 (pack_kernel), whose
 // six products of weight 2^-16 and above, the smallest first, are summed over a chunk
 // of k in one accumulator.  The tensor core truncates its FP32 sums (an error of up to
-// 2^-23 of the running sum per addition, all one way), so a chunk is kept to 512 k and
-// the chunks are added in registers, rounded to nearest, by the epilogue warps.
+// 2^-23 of the running sum per addition of 16 k, all one way), so a chunk is kept to 512 k
+// and the chunks are added in registers, rounded to nearest, by the epilogue warps.
+// bfloat16 sums are kept to chunks of 16384 k, which lose at most 2^-13 of the terms'
+// magnitudes, a sixteenth of what rounding the result may.
 //
 // Warp roles as in tc2_kernel.cu: warp 0 loads, warp 1 issues MMAs, warps 2-9 drain
 // TMEM (double-buffered: a unit's epilogue overlaps the next unit's MMAs).  The kernel
@@ -44,6 +46,8 @@ namespace pg {
 namespace {
 
 constexpr int kBK = 64;        // k per ring slot (128-byte rows)
+constexpr int kChunkF32 = 512;     // k summed in one accumulator
+constexpr int kChunkBf16 = 16384;
 constexpr int kBI = 128;       // i per CTA
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 64 + 32 * kEpiWarps;
@@ -295,6 +299,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         return x;
     };
 
+    // The accumulator that a chunk takes (`next`) and the phase bits of both, kept alike by the MMA
+    // issuer and the epilogue.  float32's many chunks alternate.  bfloat16's first chunk keeps its
+    // accumulator until the unit ends, the others all take the second and are added to it there.
+    auto take_buffer = [](int& next, uint32_t& phases, bool first) {
+        phases ^= 1u << next;
+        if (F32 || first) next ^= 1;
+    };
+
     if (warp == 0) {
         // ---------------- TMA loader (both CTAs) ----------------
         if (!(p.debug_flags & 1)) {
@@ -434,8 +446,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const uint64_t b_desc0 = smem_desc(slot0 + C::A_BYTES, p.b_mn ? 8192 : 16, 1024, kSwizzle128B);
             const uint32_t a_step = p.a_mn ? 128 : 2, b_step = p.b_mn ? 128 : 2;
             const bool ragged = p.rows_on_k && p.offsets != nullptr;
-            int slot_i = 0, chunk = 0;
-            uint32_t phase = 0;
+            int slot_i = 0, next = 0;
+            uint32_t phase = 0, acc_phase = 0;
             bool ok = true;
             for (int u = pair; u < units && ok; u += pairs) {
                 const Unit x = unit_of(u);
@@ -443,12 +455,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const int rows_left = __shfl_sync(0xffffffffu, x.k_end - x.k0 - x.kb0 * kBK, 0);  // from kb0 on
                 const uint32_t idesc =
                     idesc_bf16(2 * kBI, __shfl_sync(0xffffffffu, x.n, 0), p.a_mn != 0, p.b_mn != 0);
-                for (int c0 = 0; c0 < nkb && ok; c0 += p.chunk_kb, ++chunk) {
+                for (int c0 = 0; c0 < nkb && ok; c0 += p.chunk_kb) {
                     const int steps = (min(c0 + p.chunk_kb, nkb) - c0) * p.segs;
-                    const int buf = chunk & 1;
-                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(acc_empty0 + 8 * buf, ((chunk >> 1) & 1) ^ 1,
+                    const int buf = next;
+                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(acc_empty0 + 8 * buf, ((acc_phase >> buf) & 1) ^ 1,
                                                                    p.timeout_ns, abort_flag));
                     if (!ok) break;
+                    take_buffer(next, acc_phase, c0 == 0);
                     tc_fence_after_sync();
                     const uint32_t d = tmem + buf * BN;
                     uint32_t accumulate = 0;
@@ -514,7 +527,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             else
                 finish<T, float>(p, v, bias, base, i, jb, jn);
         };
-        int chunk = 0;
+        int next = 0;
+        uint32_t acc_phase = 0;
         bool ok = true;
         for (int u = pair; u < units && ok; u += pairs) {
             const Unit x = unit_of(u);
@@ -531,13 +545,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     prefetch_l2(static_cast<const T*>(p.residual) + (x.j0 + t) * p.ldr + i - lane);
             }
             const bool any = x.nkb > 0;  // a sum without k (k = 0, an expert without rows) is zero
-            auto wait_sums = [&]() {     // the next chunk's sums; their buffer
-                const int buf = chunk & 1;
+            auto wait_sums = [&](bool first) {  // the next chunk's sums; their buffer
+                const int buf = next;
                 ok = __all_sync(0xffffffffu,
-                                mbar_wait_bounded(acc_full0 + 8 * buf, (chunk >> 1) & 1, p.timeout_ns, abort_flag));
+                                mbar_wait_bounded(acc_full0 + 8 * buf, (acc_phase >> buf) & 1, p.timeout_ns, abort_flag));
                 if (!ok && lane == 0) raise_abort(abort_flag, p.status);
                 tc_fence_after_sync();
-                ++chunk;
+                take_buffer(next, acc_phase, first);
                 return buf;
             };
             auto free_sums = [&](int buf) {
@@ -556,7 +570,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int t = 0; t < kCols; ++t) acc[m][t] = 0.0f;
                 for (int c0 = 0; c0 < x.nkb; c0 += p.chunk_kb) {
-                    buf = wait_sums();
+                    buf = wait_sums(c0 == 0);
                     if (!ok) break;
 #pragma unroll
                     for (int m = 0; m < C::MINE; ++m) {
@@ -584,7 +598,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 tmem_wait_st();
             } else if (any) {
-                buf = wait_sums();
+                buf = wait_sums(true);
+                if (!ok) break;
+                // bfloat16: the further chunks are added to the first one's columns, 16 at a time (with a
+                // whole tile's sums in registers the kernel is slower where k is short too: dw of 32768
+                // rows of 64 experts 149 us, then 173)
+#pragma unroll 1
+                for (int c0 = p.chunk_kb; !F32 && c0 < x.nkb; c0 += p.chunk_kb) {
+                    const int more = wait_sums(false);
+                    if (!ok) break;
+#pragma unroll 1
+                    for (int c = half; kCols * c < cols; c += 2) {
+                        uint32_t v[kCols], sum[kCols];
+                        __syncwarp();
+                        tmem_ld_32x32b_x16(lane_base + more * BN + kCols * c, v);
+                        tmem_ld_32x32b_x16(lane_base + buf * BN + kCols * c, sum);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int t = 0; t < kCols; ++t)
+                            sum[t] = __float_as_uint(__uint_as_float(sum[t]) + __uint_as_float(v[t]));
+                        __syncwarp();
+                        tmem_st_32x32b_x16(lane_base + buf * BN + kCols * c, sum);
+                    }
+                    tmem_wait_st();
+                    free_sums(more);
+                }
                 if (!ok) break;
             }
 #pragma unroll 1
@@ -888,7 +926,7 @@ int launch_product_tc(const CallContext& c, const Product& p, const TcPlan& t, i
     q.a_mn = !p.a.k_contiguous;
     q.b_mn = !p.b.k_contiguous;
     q.segs = parts == 3 ? 6 : 1;
-    q.chunk_kb = parts == 3 ? 512 / kBK : 1 << 30;
+    q.chunk_kb = (parts == 3 ? kChunkF32 : kChunkBf16) / kBK;
     q.split = t.split;
     q.split_kb = t.split_kb;
     q.halved = t.halved;

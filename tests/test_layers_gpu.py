@@ -783,3 +783,49 @@ def test_listed_rows_of_no_pair_read_as_zeros(dtype, capacity, k):
     again = pg.expert_linear(x.cuda(), w.cuda(), plan, b.cuda(), "silu", gather=True)
     sees = (rows == 0).cuda()
     assert torch.isnan(again[sees]).all() and torch.equal(again[~sees], y[~sees])
+
+
+def _half_spacing(v):
+    """Half the distance of bfloat16 values around v (8 significant bits)."""
+    return torch.exp2(torch.floor(torch.log2(v.abs())) - 8)
+
+
+# The tensor core truncates its FP32 sums: an error of at most 2^-23 of the running sum for each
+# addition of 16 k, all one way.  A run of additions is kept to 16384 k for bfloat16, so the
+# errors of 1024 of them, 2^-13 of the sum of the terms' magnitudes, bound what is lost; the runs
+# are added rounded to nearest (2^-18 for 64 of them).
+LONG = 2.0 ** -13 + 2.0 ** -18
+
+
+def test_bfloat16_gradient_over_a_million_rows_of_one_sign():
+    t, n, k, e = 2 ** 20 + 37, 72, 136, 2
+    ids = torch.zeros(t, 1, dtype=torch.int32, device="cuda")
+    plan = pg.expert_plan(ids, e)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.rand(t, k, generator=g, device="cuda").bfloat16()
+    dy = torch.rand(t, n, generator=g, device="cuda").bfloat16()
+    w = torch.zeros(e, n, k, dtype=torch.bfloat16, device="cuda")
+    for gather in (True, False):
+        _, dw, _ = pg.expert_linear_backward(dy, x, w, plan, gather=gather, bias=False, need_dx=False)
+        want = dy.double().t() @ x.double()
+        assert ((dw[0].double() - want).abs() <= _half_spacing(want) + LONG * want).all()
+        assert not dw[1].any()
+
+
+@pytest.mark.parametrize("t", [40, 300])
+def test_bfloat16_sums_of_one_sign_over_a_long_k(t):
+    """Forward products whose k is no multiple of a run, in one slice and in several."""
+    n, k = 200, 5 * 16384 + 1000
+    g = torch.Generator(device="cuda").manual_seed(t)
+    x = torch.rand(t, k, generator=g, device="cuda").bfloat16()
+    w = torch.rand(n, k, generator=g, device="cuda").bfloat16()
+    b = torch.rand(n, generator=g, device="cuda").bfloat16()
+    want = x.double() @ w.double().t() + b.double()
+    try:
+        for bn in (64, 128, 256):
+            for split in (1, 3):
+                pg.force_plan(bn, split)
+                y = pg.linear(x, w, b)
+                assert ((y.double() - want).abs() <= _half_spacing(want) + LONG * want).all(), (bn, split)
+    finally:
+        pg.force_plan(0, 0)

@@ -243,10 +243,13 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
     }
 }
 
-// With q_j = p[ids_j], w_j = scale q_j / (sum q)^renorm:
-//   dq_j = scale (dw_j - sum(dw q) / sum(q)) / sum(q), or scale dw_j;
-//   softmax: dx_e = p_e (dp_e - sum(dp p)); sigmoid: dx_e = dp_e p_e (1 - p_e).
-// The chosen scores are picked, and their gradients placed, through shared memory.
+// With q_j = p[ids_j], r_j = q_j / (sum q)^renorm, w_j = scale r_j, the gradient of a
+// chosen expert's score times that score is
+//   g_j = r_j scale (dw_j - sum(dw r)) renormalised, r_j scale dw_j otherwise,
+// which stays finite where the scores are so small that their gradient does not, and
+//   softmax: dx_e = g_e - p_e sum(g), sum(g) being 0 when renormalised;
+//   sigmoid: dx_e = g_e (1 - p_e).
+// The chosen scores are picked, and g placed, through shared memory.
 // Reads and writes the logits once; 65536 x 128 float32: 21 us where half of them lies in
 // L2 (3.2 TB/s), its softmax and shuffles as long as its bytes.
 template <typename T, int V, int L>
@@ -278,23 +281,23 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
         my_d[first + v] = 0.0f;
     }
     __syncwarp();
-    const float q = id >= 0 ? my_p[id] : 0.0f;
-    float dq = dw;
+    float r = id >= 0 ? my_p[id] : 0.0f, g = dw, dot = 0.0f;
     if (renorm) {
-        const float sq = lanes_sum<L>(q), sdq = lanes_sum<L>(dw * q);
-        dq = sq > 0.0f && id >= 0 ? (dw - sdq / sq) / sq : 0.0f;
+        const float sq = lanes_sum<L>(r);
+        r = sq > 0.0f ? r / sq : 0.0f;
+        g = dw - lanes_sum<L>(dw * r);
     }
-    const float dot = lanes_sum<L>(dq * q);  // sum(dp p)
-    for (int j = 0; j < top; ++j) {          // in order: an expert may be named twice
-        if (l == j && id >= 0) my_d[id] += dq;
+    g *= r;
+    if (!renorm) dot = lanes_sum<L>(g);
+    for (int j = 0; j < top; ++j) {  // in order: an expert may be named twice
+        if (l == j && id >= 0) my_d[id] += g;
         __syncwarp();
     }
     if (!some) return;
     float d[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        const float dp = my_d[first + v];
-        d[v] = score == SGEMM_SCORE_SIGMOID ? dp * p[v] * (1.0f - p[v]) : p[v] * (dp - dot);
+        d[v] = score == SGEMM_SCORE_SIGMOID ? my_d[first + v] * (1.0f - p[v]) : fmaf(-p[v], dot, my_d[first + v]);
     }
     T* out = dlogits + t * lddl + first;
     if (vec_out && V % 8 == 0 && first + V <= experts) {

@@ -195,3 +195,30 @@ def test_route_strided_logits_and_no_tokens():
     w, i = pg.route(torch.empty(0, 64, device="cuda"), 5)
     assert w.shape == i.shape == (0, 5)
     assert pg.route_backward(torch.empty(0, 5, device="cuda"), torch.empty(0, 64, device="cuda"), i).shape == (0, 64)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("low", [-60.0, -80.0, -86.0])
+def test_route_backward_of_renormalised_weights_of_tiny_scores(score, low):
+    """Chosen experts (by the balance bias) whose scores are close to the smallest floats: their
+    renormalised weights, and so the gradients, are of the usual size.  Each is a score's ratio:
+    the scores' relative errors (2^-21, and 2^-23 / 2^-126 of a half unit near the smallest normal
+    float) times the sizes of dw, and the rounding of the ratios' sums."""
+    t, e, top = 9, 64, 6
+    g = _gen(int(-low))
+    logits = low - torch.rand(t, e, generator=g)
+    if score == "softmax":
+        logits[:, e - 1] = 0.0  # takes all of the softmax
+    dw = torch.randn(t, top, generator=g) * 100
+    balance = torch.zeros(e)
+    balance[:top] = 4.0
+    weights, ids = pg.route(logits.cuda(), top, score, bias=balance.cuda(), scale=2.5)
+    assert int(ids.max()) < top
+    x = logits.double()
+    q = torch.gather(torch.softmax(x, 1) if score == "softmax" else torch.sigmoid(x), 1, ids.cpu().long())
+    w = q / q.sum(1, keepdim=True)
+    assert ((weights.cpu().double() - 2.5 * w).abs() <= 2.0 ** -18 * 2.5 * w).all()
+    got = pg.route_backward(dw.cuda(), logits.cuda(), ids, score, scale=2.5)
+    d = 2.5 * w * (dw.double() - (w * dw.double()).sum(1, keepdim=True)) * (1 - q if score == "sigmoid" else 1)
+    want = torch.zeros(t, e, dtype=torch.float64).scatter_(1, ids.cpu().long(), d)
+    assert ((got.double().cpu() - want).abs() <= 2.0 ** -17 * 2.5 * dw.double().abs().sum(1, keepdim=True)).all()

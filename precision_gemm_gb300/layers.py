@@ -26,6 +26,8 @@ a failed call SgemmError.
 """
 from __future__ import annotations
 
+import math
+
 import torch
 
 from . import _check, _stream, load_library
@@ -127,7 +129,7 @@ def _rows2d(x, name):
     if x.dim() < 2:
         raise ValueError("%s: expected at least two dimensions, got shape %s" % (name, tuple(x.shape)))
     try:
-        return x.view(-1, x.shape[-1])
+        return x.view(math.prod(x.shape[:-1]), x.shape[-1])
     except RuntimeError:
         raise ValueError("%s: the leading dimensions of shape %s, strides %s do not form rows of one stride"
                          % (name, tuple(x.shape), x.stride())) from None

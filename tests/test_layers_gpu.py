@@ -829,3 +829,16 @@ def test_bfloat16_sums_of_one_sign_over_a_long_k(t):
                 assert ((y.double() - want).abs() <= _half_spacing(want) + LONG * want).all(), (bn, split)
     finally:
         pg.force_plan(0, 0)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS.get)
+@pytest.mark.parametrize("n,k", [(9, 0), (0, 5), (0, 0)])
+def test_leading_dimensions_over_empty_rows(dtype, n, k):
+    x = torch.ones(2, 3, k, dtype=dtype, device="cuda")
+    w = torch.ones(n, k, dtype=dtype, device="cuda")
+    b = torch.arange(n, device="cuda").to(dtype)
+    y, z = pg.linear(x, w, b, residual=torch.ones(2, 3, n, dtype=dtype, device="cuda"), preact=True)
+    assert y.shape == z.shape == (2, 3, n)
+    assert torch.equal(z, b.expand(2, 3, n)) and torch.equal(y, z + 1)
+    dx, dw, db = pg.linear_backward(torch.ones(2, 3, n, dtype=dtype, device="cuda"), x, w, "silu", z)
+    assert dx.shape == (2, 3, k) and dw.shape == (n, k) and db.shape == (n,) and not dx.any()

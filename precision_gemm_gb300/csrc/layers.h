@@ -47,10 +47,14 @@ __device__ __forceinline__ float normal_tail(float z, float& e) {
     return q * t * e;
 }
 
-// 1 / (1 + exp(-z))
+// 1 / (1 + exp(-z)).  In float32 as exp(z) / (1 + exp(z)) for negative z, so that no divisor passes
+// 2^126, where __fdividef gives zero, and a logistic down to the subnormal floats is kept.  For
+// bfloat16 it is zero from z = -87.3 on, and with it silu's values under 1e-36.
 template <bool FAST>
 __device__ __forceinline__ float logistic(float z) {
-    return FAST ? reciprocal_approx(1.0f + exp2_approx(-1.44269504f * z)) : __fdividef(1.0f, 1.0f + expf(-z));
+    if (FAST) return reciprocal_approx(1.0f + exp2_approx(-1.44269504f * z));
+    const float e = expf(-fabsf(z));
+    return __fdividef(z < 0.0f ? e : 1.0f, 1.0f + e);
 }
 
 // max(z, 0), NaN staying NaN

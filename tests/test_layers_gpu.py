@@ -842,3 +842,19 @@ def test_leading_dimensions_over_empty_rows(dtype, n, k):
     assert torch.equal(z, b.expand(2, 3, n)) and torch.equal(y, z + 1)
     dx, dw, db = pg.linear_backward(torch.ones(2, 3, n, dtype=dtype, device="cuda"), x, w, "silu", z)
     assert dx.shape == (2, 3, k) and dw.shape == (n, k) and db.shape == (n,) and not dx.any()
+
+
+@pytest.mark.parametrize("t", [1, 200])
+def test_float32_silu_where_its_logistic_is_below_the_normal_floats(t):
+    """From z of -87.3 on, 1 / (1 + exp(-z)) is subnormal (absolute error 2^-150, which z makes
+    at most 2^-143) while z times it is not yet: exp is good to 2^-22, the products to 2^-24."""
+    n = 64
+    z = torch.linspace(-88.5, -80, n)
+    y = pg.linear(torch.zeros(t, 8, device="cuda"), torch.zeros(n, 8, device="cuda"), z.cuda(), "silu")
+    want = (z.double() / (1 + torch.exp(-z.double()))).expand(t, n)
+    assert ((y.double().cpu() - want).abs() <= 2.0 ** -21 * want.abs() + 2.0 ** -142).all()
+    # its derivative, the slope of a gradient of ones
+    dz = torch.exp(z.double()) * (1 + z.double())
+    _, _, db = pg.linear_backward(torch.ones(1, n, device="cuda"), torch.zeros(1, 8, device="cuda"),
+                                  torch.zeros(n, 8, device="cuda"), "silu", z[None].cuda())
+    assert ((db.double().cpu() - dz).abs() <= 2.0 ** -20 * dz.abs() + 2.0 ** -142).all()

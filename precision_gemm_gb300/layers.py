@@ -33,6 +33,7 @@ import torch
 from . import _check, _stream, load_library
 
 SGEMM_F32, SGEMM_BF16 = 0, 1
+MAX_EXPERTS = 512  # SGEMM_MAX_EXPERTS
 ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 SCORES = {"softmax": 0, "sigmoid": 1}
 _DTYPES = {torch.float32: SGEMM_F32, torch.bfloat16: SGEMM_BF16}
@@ -133,6 +134,14 @@ def _rows2d(x, name):
     except RuntimeError:
         raise ValueError("%s: the leading dimensions of shape %s, strides %s do not form rows of one stride"
                          % (name, tuple(x.shape), x.stride())) from None
+
+
+def _count(v, name):
+    """v as the library's 32-bit integer, which would otherwise be cut off without a word."""
+    v = int(v)
+    if not -1 << 31 <= v < 1 << 31:
+        raise ValueError("%s: %d does not fit in 32 bits" % (name, v))
+    return v
 
 
 def _shape(w, name, dims):
@@ -241,8 +250,8 @@ def route(logits, top, score="softmax", bias=None, groups=1, group_top=1, renorm
         _packed(bias, "bias", (e,), torch.float32, index)
     if mask is not None:
         _packed(mask, "mask", (t,), torch.bool, index)
-    top = int(top)
-    shape = (t, top if top > 0 else 0)
+    top, groups, group_top = _count(top, "top"), _count(groups, "groups"), _count(group_top, "group_top")
+    shape = (t, top if 0 < top <= e else 0)  # the library refuses any other top
     weights = _empty(shape, dtype=torch.float32, device=device)
     ids = _empty(shape, dtype=torch.int32, device=device)
     rc = lib.sgemm_route(code, t, e, top, logits.data_ptr(), ldl, _score(score), _ptr(bias), groups, group_top,
@@ -333,10 +342,11 @@ def expert_plan(ids, experts, stream=None):
         raise ValueError("ids: expected a CUDA tensor, got one on %s" % ids.device)
     index = _current_device()
     _packed(ids, "ids", (t, top), torch.int32, index)
-    experts = int(experts)
+    experts = _count(experts, "experts")
     if experts < 1:
         raise ValueError("experts: %d is less than 1" % experts)
-    store = _empty((2 * experts + 1 + 2 * t * top,), dtype=torch.int32, device=ids.device)
+    # more experts than SGEMM_MAX_EXPERTS are the library's to refuse, before it writes a list
+    store = _empty((2 * min(experts, MAX_EXPERTS) + 1 + 2 * t * top,), dtype=torch.int32, device=ids.device)
     plan = ExpertPlan._of(store, store.data_ptr(), t, top, experts, index)
     rc = lib.sgemm_expert_plan(t, top, experts, ids.data_ptr(), *plan._addresses, _raw_stream(index))
     if rc:

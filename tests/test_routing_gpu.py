@@ -222,3 +222,19 @@ def test_route_backward_of_renormalised_weights_of_tiny_scores(score, low):
     d = 2.5 * w * (dw.double() - (w * dw.double()).sum(1, keepdim=True)) * (1 - q if score == "sigmoid" else 1)
     want = torch.zeros(t, e, dtype=torch.float64).scatter_(1, ids.cpu().long(), d)
     assert ((got.double().cpu() - want).abs() <= 2.0 ** -17 * 2.5 * dw.double().abs().sum(1, keepdim=True)).all()
+
+
+def test_counts_are_checked_before_results_are_allocated():
+    logits, ids = torch.zeros(1, 16, device="cuda"), torch.zeros(1, 2, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    held = torch.cuda.memory_allocated()
+    for call in (lambda: pg.route(logits, 1 << 24), lambda: pg.expert_plan(ids, 1 << 24)):
+        with pytest.raises(pg.SgemmError):
+            call()
+    for call in (lambda: pg.route(logits, (1 << 32) + 2), lambda: pg.expert_plan(ids, (1 << 32) + 2),
+                 lambda: pg.route(logits, 2, groups=(1 << 32) + 1),
+                 lambda: pg.route(logits, 2, groups=2, group_top=(1 << 32) + 1)):
+        with pytest.raises(ValueError):  # beyond the 32 bits of the library's argument
+            call()
+    assert torch.cuda.max_memory_allocated() - held < 1 << 20

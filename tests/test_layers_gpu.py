@@ -858,3 +858,14 @@ def test_float32_silu_where_its_logistic_is_below_the_normal_floats(t):
     _, _, db = pg.linear_backward(torch.ones(1, n, device="cuda"), torch.zeros(1, 8, device="cuda"),
                                   torch.zeros(n, 8, device="cuda"), "silu", z[None].cuda())
     assert ((db.double().cpu() - dz).abs() <= 2.0 ** -20 * dz.abs() + 2.0 ** -142).all()
+
+
+@pytest.mark.parametrize("t", [4, 40, 300])
+def test_float32_accuracy_on_values_of_one_sign(t):
+    """The stated error in the 2-norm at k = 4096, where errors that all point one way add up."""
+    n, k = 512, 4096
+    g = _gen(t)
+    x, w = torch.rand(t, k, generator=g), torch.rand(n, k, generator=g)
+    y = pg.linear(x.cuda(), w.cuda()).double().cpu()
+    want = x.double() @ w.double().t()
+    assert float((y - want).norm() / want.norm()) < 1e-6

@@ -229,10 +229,10 @@ int backward_steps(const CallContext& c, const Backward& b, Arena& a, cudaStream
         dz.ptr = dz_own = static_cast<bf16*>(a.take(static_cast<size_t>(dz.parts) * dz.stride * 2));
     }
     if (own_dz || (b.dbias && b.n > 0)) {
-        float* part = b.dbias ? static_cast<float*>(a.take(bias_part_bytes(b.rows, b.n, b.experts))) : nullptr;
+        float* part = b.dbias ? static_cast<float*>(a.take(bias_part_bytes(b.rows, b.n, b.experts, c.sms))) : nullptr;
         if (!a.dry()) {
             if ((e = launch_dact(b.dtype, b.rows, b.n, b.dy, b.lddy, b.z, b.ldz, b.act, dz_own, dz.ld, b.experts,
-                                 b.offsets, b.dbias, part, st)) != cudaSuccess)
+                                 b.offsets, b.dbias, part, c.sms, st)) != cudaSuccess)
                 return call_fail_cuda(e, "activation backward");
             call_count(dact_launches(b.dbias != nullptr));
         }

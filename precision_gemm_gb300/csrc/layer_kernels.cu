@@ -10,8 +10,8 @@ constexpr int kWidth = 256;  // columns per block of the activation's backward p
 
 // Its rows: 128, so that a thread has sixteen to load, or 32 while that makes fewer than
 // four blocks per SM (1300 x 1000 float32 13 -> 9 us).
-int slab_rows(int64_t rows, int64_t n) {
-    return ((rows + 127) / 128) * ((n + kWidth - 1) / kWidth) >= 4 * 152 ? 128 : 32;
+int slab_rows(int64_t rows, int64_t n, int num_sms) {
+    return ((rows + 127) / 128) * ((n + kWidth - 1) / kWidth) >= int64_t(4) * num_sms ? 128 : 32;
 }
 
 // dz = dy * act'(z) for a slab of rows x 256 columns, and the slab's column sums per
@@ -280,8 +280,8 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(int64_t pairs, in
 
 }  // namespace
 
-size_t bias_part_bytes(int64_t rows, int64_t n, int groups) {
-    const int slab = slab_rows(rows, n);
+size_t bias_part_bytes(int64_t rows, int64_t n, int groups, int num_sms) {
+    const int slab = slab_rows(rows, n, num_sms);
     return static_cast<size_t>((rows + slab - 1) / slab + groups) * n * 4;
 }
 
@@ -290,8 +290,8 @@ int dact_launches(bool with_bias) { return with_bias ? 2 : 1; }
 template <typename T, int PARTS>
 static cudaError_t run_dact(int64_t rows, int64_t n, const void* dy, int64_t lddy, const void* z, int64_t ldz, int act,
                             bf16* dz, int64_t lddz, int groups, const int32_t* offsets, void* dbias, float* part,
-                            cudaStream_t st) {
-    const int slab = slab_rows(rows, n);
+                            int num_sms, cudaStream_t st) {
+    const int slab = slab_rows(rows, n, num_sms);
     const dim3 grid(static_cast<unsigned>(((rows + slab - 1) / slab) * ((n + kWidth - 1) / kWidth)));
     const bool vec = rows_aligned<T>(dy, lddy) && (act == SGEMM_ACT_NONE || rows_aligned<T>(z, ldz));
     cudaError_t e = cudaSuccess;
@@ -306,10 +306,10 @@ static cudaError_t run_dact(int64_t rows, int64_t n, const void* dy, int64_t ldd
 
 cudaError_t launch_dact(int dtype, int64_t rows, int64_t n, const void* dy, int64_t lddy, const void* z, int64_t ldz,
                         int act, bf16* dz, int64_t lddz, int groups, const int32_t* offsets, void* dbias, float* part,
-                        cudaStream_t st) {
+                        int num_sms, cudaStream_t st) {
     return dtype == SGEMM_F32
-               ? run_dact<float, 3>(rows, n, dy, lddy, z, ldz, act, dz, lddz, groups, offsets, dbias, part, st)
-               : run_dact<bf16, 1>(rows, n, dy, lddy, z, ldz, act, dz, lddz, groups, offsets, dbias, part, st);
+               ? run_dact<float, 3>(rows, n, dy, lddy, z, ldz, act, dz, lddz, groups, offsets, dbias, part, num_sms, st)
+               : run_dact<bf16, 1>(rows, n, dy, lddy, z, ldz, act, dz, lddz, groups, offsets, dbias, part, num_sms, st);
 }
 
 template <typename T, typename TX>

@@ -363,10 +363,10 @@ int launch_product_tc(const CallContext& c, const Product& p, const TcPlan& t, i
 // dz = dy * act'(z) as bfloat16 parts (one for bfloat16, three for float32, rows * lddz
 // apart; may be null), and per group the column sums of dz before rounding, into dbias
 // (groups x n; may be null).  part: bias_part_bytes().
-size_t bias_part_bytes(int64_t rows, int64_t n, int groups);
+size_t bias_part_bytes(int64_t rows, int64_t n, int groups, int num_sms);
 cudaError_t launch_dact(int dtype, int64_t rows, int64_t n, const void* dy, int64_t lddy, const void* z, int64_t ldz,
                         int act, bf16* dz, int64_t lddz, int groups, const int32_t* offsets, void* dbias, float* part,
-                        cudaStream_t st);
+                        int num_sms, cudaStream_t st);
 int dact_launches(bool with_bias);
 
 // x_f32: the rows are FP32 whatever dtype.

@@ -367,7 +367,8 @@ int sgemm_debug_flags(int flags);
  * Operands may not overlap results, except that `residual` may be `y` itself.
  * Status codes, streams, workspaces and threads are as for sgemm: -i names the
  * first invalid argument, work is queued on `stream`, and the workspace comes
- * from the stream's (sgemm_set_workspace applies).
+ * from the stream's (sgemm_set_workspace applies; SGEMM_ERR_WORKSPACE's text says how
+ * many bytes a call needs).
  */
 
 /* Element types (argument `dtype`). */

@@ -319,8 +319,10 @@ struct Product {
 // hides behind that kernel's end.
 // -----------------------------------------------------------------------
 
-// Forward products of few rows (b's rows along k, out of the call's dtype): one pass
-// over the weights per 16 rows of a group.
+// Forward products of few rows (b's rows along k, out of the call's dtype).  One pass over a
+// group's weights serves up to 4 rows of bfloat16 or 16 of float32, the number chosen once per
+// launch from the rows of a dense call or twice the lists' average length; a longer list takes
+// further passes.
 cudaError_t launch_product_rows(const Product& p, int num_sms, cudaStream_t st);
 
 // Rows (list[r] / top of src_rows, or `groups` matrices of per_group rows, `stride`

@@ -497,7 +497,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else {
         // ---------------- epilogue (warps 2..9, both CTAs) ----------------
         const int q = warp & 3;             // TMEM lane quarter this warp may access
-        const int half = (warp - 2) >> 2;   // which of the 32-column chunks it takes
+        const int half = (warp - 2) >> 2;   // it takes every other 16 columns
         const uint32_t acc_empty_leader0 = map_to_rank(acc_empty0, 0);
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(32 * q) << 16);
         const int epi = warp - 2;
@@ -848,8 +848,9 @@ cudaError_t launch_pack(int dtype, const PackJob* jobs, int count, int num_sms, 
 // reads it waits for); kSplit and kBlockMB are the adding kernel and the blocks' way to it.
 // Against tiles that are not cut: 16 rows of 4096 x 4096 bfloat16 12.7 -> 8.8 us, of 2048 x
 // 8192 21.6 -> 9.5; float32, 40 rows of 2048 x 2048 42 -> 20, 400 rows 43 -> 33, 700^3 18.3
-// -> 16.9.  Tile widths: 1500 x 3000 x 777 float32 with residual at 256 columns 67, at 128
-// 42.  Grouped rows are counted by their average length, since the lengths are known on the
+// -> 16.9.  Tile widths: 1500 x 3000 x 777 float32 with residual takes 40 us from cold caches
+// at 256 columns (72 tiles, one wave, whose epilogue nothing hides) as at 128 (two waves).
+// Grouped rows are counted by their average length, since the lengths are known on the
 // device alone.
 TcPlan plan_tc(const Product& p, int num_sms, int force_bn, int force_split) {
     static constexpr double kSplit = 2.0, kBlockMB = 0.2;

@@ -23,6 +23,10 @@ when None); results are allocated on that stream.  Tensors that were made on ano
 stream must be ready on it and stay alive until its work is done, as for any
 asynchronous call.  A bad tensor raises ValueError before the library is called,
 a failed call SgemmError.
+
+autograd records none of these calls: a result has no grad_fn, also where its inputs
+require gradients.  The _backward functions are called as they are, or from a
+torch.autograd.Function of the caller's.
 """
 from __future__ import annotations
 

@@ -431,6 +431,37 @@ int sgemm_linear_backward(int dtype, int64_t t, int64_t n, int64_t k, const void
                           int64_t lddw, void *dbias, void *stream);
 
 /*
+ * sgemm_layer_norm -- of each row of x: mean = sum x / n, rstd = (sum (x - mean)^2 / n +
+ * eps)^-1/2, y = (x - mean) rstd w + bias, the squares taken around the mean.
+ *
+ *   dtype (1); t >= 0, n >= 1 (2, 3): x and y are t x n; x, ldx (4, 5); w and bias, n
+ *   elements each, or NULL for ones and zeros (6, 7); eps >= 0 (8); y, ldy (9, 10); mean
+ *   and rstd, t floats each, or NULL (11, 12): sgemm_layer_norm_backward reads them.
+ *
+ * A NaN or infinity makes its own row NaN.
+ */
+int sgemm_layer_norm(int dtype, int64_t t, int64_t n, const void *x, int64_t ldx, const void *w,
+                     const void *bias, float eps, void *y, int64_t ldy, float *mean, float *rstd,
+                     void *stream);
+
+/*
+ * sgemm_layer_norm_backward -- the gradients of sgemm_layer_norm for dy.  With
+ * h = (x - mean) rstd and g = dy w:
+ *
+ *     dx = rstd (g - sum g / n - h sum(g h) / n) + residual,
+ *     dw = the sum over rows of dy h,   dbias = the sum of dy's rows.
+ *
+ *   dtype, t, n (1-3); dy, lddy (4, 5); x, ldx (6, 7); w or NULL (8); mean, rstd
+ *   (9, 10); residual, t x n, or NULL: a gradient that reaches x past the norm, added to
+ *   dx; ldr (11, 12); dx, lddx (13, 14), dw (15), dbias (16): each may be NULL, which
+ *   skips it.  residual may be dx itself.  Sums run in a fixed order.
+ */
+int sgemm_layer_norm_backward(int dtype, int64_t t, int64_t n, const void *dy, int64_t lddy,
+                              const void *x, int64_t ldx, const void *w, const float *mean,
+                              const float *rstd, const void *residual, int64_t ldr, void *dx,
+                              int64_t lddx, void *dw, void *dbias, void *stream);
+
+/*
  * sgemm_route -- choose `top` experts per token and their weights.
  *
  *   p      = softmax(logits) over the experts, or sigmoid(logits), in FP32

@@ -375,6 +375,55 @@ PG_EXPORT int sgemm_linear_backward(int dtype, int64_t t, int64_t n, int64_t k, 
     return backward(b, static_cast<cudaStream_t>(stream));
 }
 
+PG_EXPORT int sgemm_layer_norm(int dtype, int64_t t, int64_t n, const void* x, int64_t ldx, const void* w,
+                               const void* bias, float eps, void* y, int64_t ldy, float* mean, float* rstd,
+                               void* stream) {
+    PG_CHECK(check_dtype(dtype, 1));
+    PG_CHECK(check_extent(t, 2, "t"));
+    PG_CHECK(check_extent(n, 3, "n", 1));
+    PG_CHECK(check_matrix(x, t > 0, n, ldx, 4, "x"));
+    if (!(eps >= 0.0f) || std::isinf(eps)) return call_fail(-8, "argument 8 (eps): %g is not a number from 0 on", eps);
+    PG_CHECK(check_matrix(y, t > 0, n, ldy, 9, "y"));
+    if (t == 0) return 0;
+    CallContext c;
+    PG_CHECK(call_begin(&c));
+    const cudaError_t e = launch_norm(dtype, t, n, x, ldx, w, bias, eps, y, ldy, mean, rstd, c.sms,
+                                      static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return call_fail_cuda(e, "layer norm");
+    call_count(1);
+    return 0;
+}
+
+PG_EXPORT int sgemm_layer_norm_backward(int dtype, int64_t t, int64_t n, const void* dy, int64_t lddy, const void* x,
+                                        int64_t ldx, const void* w, const float* mean, const float* rstd,
+                                        const void* residual, int64_t ldr, void* dx, int64_t lddx, void* dw,
+                                        void* dbias, void* stream) {
+    PG_CHECK(check_dtype(dtype, 1));
+    PG_CHECK(check_extent(t, 2, "t"));
+    PG_CHECK(check_extent(n, 3, "n", 1));
+    const bool any = dx || dw || dbias, some = any && t > 0;
+    PG_CHECK(check_matrix(dy, some, n, lddy, 4, "dy"));
+    PG_CHECK(check_matrix(x, some, n, ldx, 6, "x"));
+    PG_CHECK(check_pointer(mean, some, 9, "mean"));
+    PG_CHECK(check_pointer(rstd, some, 10, "rstd"));
+    PG_CHECK(check_matrix(residual, false, n, ldr, 11, "residual"));
+    PG_CHECK(check_matrix(dx, false, n, lddx, 13, "dx"));
+    if (!any || (t == 0 && !dw && !dbias)) return 0;
+    CallContext c;
+    PG_CHECK(call_begin(&c));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool sums = dw || dbias;
+    return with_workspace(c, st, [&](Arena& a) {
+        float* part = sums ? static_cast<float*>(a.take(norm_part_bytes(t, n, c.sms))) : nullptr;
+        if (a.dry()) return 0;
+        const cudaError_t e = launch_norm_backward(dtype, t, n, dy, lddy, x, ldx, w, mean, rstd, residual, ldr, dx, lddx,
+                                                   dw, dbias, part, c.sms, st);
+        if (e != cudaSuccess) return call_fail_cuda(e, "layer norm backward");
+        call_count(norm_backward_launches(t, n, dx != nullptr, sums));
+        return 0;
+    });
+}
+
 PG_EXPORT int sgemm_route(int dtype, int64_t tokens, int experts, int top, const void* logits, int64_t ldl, int score,
                           const float* balance, int groups, int group_top, int renormalize, float scale,
                           const uint8_t* mask, float* weights, int32_t* ids, void* stream) {

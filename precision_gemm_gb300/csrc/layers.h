@@ -379,6 +379,16 @@ cudaError_t launch_combine_backward(int dtype, int64_t tokens, int top, int64_t 
                                     const void* x, int64_t ldx, const int32_t* rows, const int32_t* slots,
                                     const float* weights, void* dx, int64_t lddx, float* dweights, cudaStream_t st);
 
+// Layer norm (norm.cu).  part: norm_part_bytes(), read where dw or db is asked for.
+cudaError_t launch_norm(int dtype, int64_t rows, int64_t n, const void* x, int64_t ldx, const void* w, const void* b,
+                        float eps, void* y, int64_t ldy, float* mean, float* rstd, int num_sms, cudaStream_t st);
+size_t norm_part_bytes(int64_t rows, int64_t n, int num_sms);
+int norm_backward_launches(int64_t rows, int64_t n, bool dx, bool sums);
+cudaError_t launch_norm_backward(int dtype, int64_t rows, int64_t n, const void* dy, int64_t lddy, const void* x,
+                                 int64_t ldx, const void* w, const float* mean, const float* rstd,
+                                 const void* residual, int64_t ldr, void* dx, int64_t lddx, void* dw, void* db,
+                                 float* part, int num_sms, cudaStream_t st);
+
 cudaError_t launch_route(int dtype, int64_t tokens, int experts, int top, const void* logits, int64_t ldl, int score,
                          const float* balance, int groups, int group_top, int renorm, float scale,
                          const uint8_t* mask, float* weights, int32_t* ids, cudaStream_t st);

@@ -7,6 +7,8 @@ and call the library; all arithmetic runs in its kernels.
 
     y             = linear(x, w, bias, act, residual)           act(x w^T + bias) + residual
     dx, dw, dbias = linear_backward(dy, x, w, act, preact)
+    y             = layer_norm(x, w, bias, eps)
+    dx, dw, dbias = layer_norm_backward(dy, x, w, mean, rstd, residual)
     weights, ids  = route(logits, top, score, ...)
     dlogits       = route_backward(dweights, logits, ids, score, ...)
     plan          = expert_plan(ids, experts)                    the experts' row lists
@@ -228,6 +230,77 @@ def linear_backward(dy, x, w, act="none", preact=None, bias=True, need_dx=True, 
     db = _empty((n,), dtype=dtype, device=device) if bias else None
     rc = lib.sgemm_linear_backward(code, t, n, k, dy2.data_ptr(), lddy, x2.data_ptr(), ldx, w.data_ptr(), ldw, kind,
                                    _ptr(preact), ldz, _ptr(dx), k or 1, _ptr(dw), k or 1, _ptr(db), _raw_stream(index))
+    if rc:
+        _check(rc, lib)
+    if dx is not None and x.dim() != 2:
+        dx = dx.view(x.shape)
+    return dx, dw, db
+
+
+def layer_norm(x, w=None, bias=None, eps=1e-5, stats=False, out=None, stream=None):
+    """y = (x - mean) rstd w + bias for the rows of x (..., n), w and bias (n) or None,
+    with rstd = (variance + eps)^-1/2; returns y.  stats=True also returns mean and rstd
+    (float32, one of each row), which layer_norm_backward reads; a tensor given as out is
+    written instead."""
+    if stream is not None:
+        return _on(stream, layer_norm, x, w, bias, eps, stats, out)
+    lib = load_library()
+    index, code = _begin(x, "x")
+    x2 = x if x.dim() == 2 else _rows2d(x, "x")
+    dtype, device = x.dtype, x.device
+    t, n = x2.shape
+    ldx = _matrix(x2, "x", t, n, dtype, index)
+    if w is not None:
+        _packed(w, "w", (n,), dtype, index)
+    if bias is not None:
+        _packed(bias, "bias", (n,), dtype, index)
+    if out is None:
+        y, ldy = _empty((t, n), dtype=dtype, device=device), n or 1
+    else:
+        y = _rows2d(out, "out")
+        ldy = _matrix(y, "out", t, n, dtype, index)
+    mean = rstd = None
+    if stats:
+        mean = _empty(x.shape[:-1], dtype=torch.float32, device=device)
+        rstd = _empty(x.shape[:-1], dtype=torch.float32, device=device)
+    rc = lib.sgemm_layer_norm(code, t, n, x2.data_ptr(), ldx, _ptr(w), _ptr(bias), eps, y.data_ptr(), ldy, _ptr(mean),
+                              _ptr(rstd), _raw_stream(index))
+    if rc:
+        _check(rc, lib)
+    if out is not None:
+        y = out
+    elif x2 is not x:
+        y = y.view(x.shape)
+    return (y, mean, rstd) if stats else y
+
+
+def layer_norm_backward(dy, x, w, mean, rstd, residual=None, bias=True, need_dx=True, need_dw=True, stream=None):
+    """(dx, dw, dbias) of layer_norm for dy (..., n), with the mean and rstd that it
+    returned.  residual (..., n), a gradient that reaches x past the norm, is added to dx.
+    dbias is None unless `bias`, dx and dw unless needed (dw is None too where w is)."""
+    if stream is not None:
+        return _on(stream, layer_norm_backward, dy, x, w, mean, rstd, residual, bias, need_dx, need_dw)
+    lib = load_library()
+    index, code = _begin(x, "x")
+    x2, dy2 = _rows2d(x, "x"), _rows2d(dy, "dy")
+    dtype, device = x.dtype, x.device
+    t, n = x2.shape
+    lddy = _matrix(dy2, "dy", t, n, dtype, index)
+    ldx = _matrix(x2, "x", t, n, dtype, index)
+    if w is not None:
+        _packed(w, "w", (n,), dtype, index)
+    _packed(mean, "mean", x.shape[:-1], torch.float32, index)
+    _packed(rstd, "rstd", x.shape[:-1], torch.float32, index)
+    ldr = 0
+    if residual is not None:
+        residual = _rows2d(residual, "residual")
+        ldr = _matrix(residual, "residual", t, n, dtype, index)
+    dx = _empty((t, n), dtype=dtype, device=device) if need_dx else None
+    dw = _empty((n,), dtype=dtype, device=device) if need_dw and w is not None else None
+    db = _empty((n,), dtype=dtype, device=device) if bias else None
+    rc = lib.sgemm_layer_norm_backward(code, t, n, dy2.data_ptr(), lddy, x2.data_ptr(), ldx, _ptr(w), mean.data_ptr(),
+                                       rstd.data_ptr(), _ptr(residual), ldr, _ptr(dx), n or 1, _ptr(dw), _ptr(db),
+                                       _raw_stream(index))
     if rc:
         _check(rc, lib)
     if dx is not None and x.dim() != 2:

@@ -431,6 +431,42 @@ int sgemm_linear_backward(int dtype, int64_t t, int64_t n, int64_t k, const void
                           int64_t lddw, void *dbias, void *stream);
 
 /*
+ * sgemm_gated_linear -- y = act(g) v with g = x wg^T + bg and v = x wv^T + bv: a gated
+ * feed-forward block up to its last product.  w holds both matrices, wg's n rows and
+ * then wv's; bias likewise.
+ *
+ *   dtype (1); t, n, k >= 0 (2-4): x is t x k, w is 2n x k, y is t x n, 2n < 2^31-1024
+ *   x, ldx (5, 6), w, ldw (7, 8)
+ *   bias      2n elements, or NULL (9)
+ *   act       SGEMM_ACT_* (10)
+ *   y, ldy (11, 12)
+ *   preact    t x 2n, or NULL: receives [g v], which sgemm_gated_linear_backward reads;
+ *             ldz (13, 14)
+ *
+ * act(g) v is formed in FP32 and rounded once.  k == 0 leaves the products zero.
+ */
+int sgemm_gated_linear(int dtype, int64_t t, int64_t n, int64_t k, const void *x, int64_t ldx, const void *w,
+                       int64_t ldw, const void *bias, int act, void *y, int64_t ldy, void *preact,
+                       int64_t ldz, void *stream);
+
+/*
+ * sgemm_gated_linear_backward -- the gradients of sgemm_gated_linear for dy (t x n).
+ * With [g v] = preact and dz = [dy v act'(g), dy act(g)]:
+ *
+ *     dx = dz w,   dw = dz^T x,   dbias = the sum of dz's rows.
+ *
+ *   dtype, t, n, k (1-4); dy, lddy (5, 6); x, ldx (7, 8); w, ldw (9, 10); act (11);
+ *   preact, ldz (12, 13); dx, lddx (14, 15), dw (2n x k), lddw (16, 17), dbias (2n)
+ *   (18): each may be NULL, which skips that gradient.
+ *
+ * dz is rounded, and sums are ordered, as in sgemm_linear_backward.
+ */
+int sgemm_gated_linear_backward(int dtype, int64_t t, int64_t n, int64_t k, const void *dy, int64_t lddy,
+                                const void *x, int64_t ldx, const void *w, int64_t ldw, int act,
+                                const void *preact, int64_t ldz, void *dx, int64_t lddx, void *dw,
+                                int64_t lddw, void *dbias, void *stream);
+
+/*
  * sgemm_layer_norm -- of each row of x: mean = sum x / n, rstd = (sum (x - mean)^2 / n +
  * eps)^-1/2, y = (x - mean) rstd w + bias, the squares taken around the mean.
  *

@@ -148,6 +148,7 @@ bool few_rows(const Product& p) {
     if (p.dtype == SGEMM_F32)
         return p.groups == 1 ? p.nj <= std::min<int64_t>(16, p.nk / 8 + 1)
                              : p.nj <= lists * std::min<int64_t>(aligned ? 24 : 16, p.nk / 32 + 1);
+    if (p.gated) return p.nj <= (aligned ? 3 : std::min<int64_t>(4, p.nk / 64 + 1));
     if (!aligned) return p.nj <= lists * std::min<int64_t>(4, p.nk / 64 + 1);
     return p.groups == 1 ? p.nj <= 3 && p.ni * p.nk <= int64_t(1) << 25 : 2 * p.nj <= p.groups && p.nk >= 256;
 }
@@ -208,6 +209,7 @@ struct Backward {
     int act;
     void *dx, *dw, *dbias;
     int64_t lddx, lddw, stride_dw;
+    bool gated;  // dy has n / 2 columns, z and dz have n
 };
 
 int backward_steps(const CallContext& c, const Backward& b, Arena& a, cudaStream_t st) {
@@ -215,7 +217,7 @@ int backward_steps(const CallContext& c, const Backward& b, Arena& a, cudaStream
     const bool products = (b.dx || b.dw) && b.rows > 0 && b.n > 0;
     Operand dz = rows_of(b.dy, b.lddy, b.rows, true);
     // dz = dy is read in place where the tensor cores can
-    const bool own_dz = products && (b.act != SGEMM_ACT_NONE || b.dtype == SGEMM_F32 || b.lddy % 8 != 0 ||
+    const bool own_dz = products && (b.gated || b.act != SGEMM_ACT_NONE || b.dtype == SGEMM_F32 || b.lddy % 8 != 0 ||
                                      (reinterpret_cast<uintptr_t>(b.dy) & 15) != 0);
     bf16* dz_own = nullptr;
     if (own_dz) {
@@ -228,7 +230,17 @@ int backward_steps(const CallContext& c, const Backward& b, Arena& a, cudaStream
                              (long long)b.rows);
         dz.ptr = dz_own = static_cast<bf16*>(a.take(static_cast<size_t>(dz.parts) * dz.stride * 2));
     }
-    if (own_dz || (b.dbias && b.n > 0)) {
+    if (b.gated && (own_dz || (b.dbias && b.n > 0))) {
+        // (dz is formed for its sums alone too: its place is then the call's own)
+        if (!own_dz) dz_own = static_cast<bf16*>(a.take(static_cast<size_t>(b.dtype == SGEMM_F32 ? 3 : 1) * b.rows * packed_ld(b.n) * 2));
+        float* part = b.dbias ? static_cast<float*>(a.take(gate_part_bytes(b.rows, b.n / 2, c.sms))) : nullptr;
+        if (!a.dry()) {
+            if ((e = launch_dgate(b.dtype, b.rows, b.n / 2, b.dy, b.lddy, b.z, b.ldz, b.act, dz_own, packed_ld(b.n),
+                                  b.dbias, part, c.sms, st)) != cudaSuccess)
+                return call_fail_cuda(e, "gate backward");
+            call_count(dact_launches(b.dbias != nullptr));
+        }
+    } else if (own_dz || (b.dbias && b.n > 0)) {
         float* part = b.dbias ? static_cast<float*>(a.take(bias_part_bytes(b.rows, b.n, b.experts, c.sms))) : nullptr;
         if (!a.dry()) {
             if ((e = launch_dact(b.dtype, b.rows, b.n, b.dy, b.lddy, b.z, b.ldz, b.act, dz_own, dz.ld, b.experts,
@@ -372,6 +384,84 @@ PG_EXPORT int sgemm_linear_backward(int dtype, int64_t t, int64_t n, int64_t k, 
     b.lddw = lddw;
     b.dbias = dbias;
     if (!dx && !dw && !dbias) return 0;
+    return backward(b, static_cast<cudaStream_t>(stream));
+}
+
+PG_EXPORT int sgemm_gated_linear(int dtype, int64_t t, int64_t n, int64_t k, const void* x, int64_t ldx, const void* w,
+                                 int64_t ldw, const void* bias, int act, void* y, int64_t ldy, void* preact,
+                                 int64_t ldz, void* stream) {
+    PG_CHECK(check_dtype(dtype, 1));
+    PG_CHECK(check_extent(t, 2, "t"));
+    PG_CHECK(check_extent(n, 3, "n", 0, kMaxExtent / 2));
+    PG_CHECK(check_extent(k, 4, "k"));
+    const bool some = t > 0 && n > 0;
+    PG_CHECK(check_matrix(x, some && k > 0, k, ldx, 5, "x"));
+    PG_CHECK(check_matrix(w, some && k > 0, k, ldw, 7, "w"));
+    PG_CHECK(check_act(act, 10));
+    PG_CHECK(check_matrix(y, some, n, ldy, 11, "y"));
+    PG_CHECK(check_matrix(preact, false, 2 * n, ldz, 13, "preact"));
+    if (!some) return 0;
+    CallContext c;
+    PG_CHECK(call_begin(&c));
+    Product p{};
+    p.dtype = dtype;
+    p.ni = n;
+    p.nj = t;
+    p.nk = k;
+    p.groups = 1;
+    p.a = rows_of(w, ldw, 2 * n, true);
+    p.b = rows_of(x, ldx, t, true);
+    p.bias = bias;
+    p.act = act;
+    p.out = y;
+    p.ldo = ldy;
+    p.preact = preact;
+    p.ldz = ldz;
+    p.gated = true;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return with_workspace(c, st, [&](Arena& a) { return product(c, p, a, st); });
+}
+
+PG_EXPORT int sgemm_gated_linear_backward(int dtype, int64_t t, int64_t n, int64_t k, const void* dy, int64_t lddy,
+                                          const void* x, int64_t ldx, const void* w, int64_t ldw, int act,
+                                          const void* preact, int64_t ldz, void* dx, int64_t lddx, void* dw,
+                                          int64_t lddw, void* dbias, void* stream) {
+    PG_CHECK(check_dtype(dtype, 1));
+    PG_CHECK(check_extent(t, 2, "t"));
+    PG_CHECK(check_extent(n, 3, "n", 0, kMaxExtent / 2));
+    PG_CHECK(check_extent(k, 4, "k"));
+    const bool any = dx || dw || dbias, some = t > 0 && n > 0;
+    PG_CHECK(check_matrix(dy, some && any, n, lddy, 5, "dy"));
+    PG_CHECK(check_matrix(x, some && k > 0 && dw, k, ldx, 7, "x"));
+    PG_CHECK(check_matrix(w, some && k > 0 && dx, k, ldw, 9, "w"));
+    PG_CHECK(check_act(act, 11));
+    PG_CHECK(check_matrix(preact, some && any, 2 * n, ldz, 12, "preact"));
+    PG_CHECK(check_matrix(dx, false, k, lddx, 14, "dx"));
+    PG_CHECK(check_matrix(dw, false, k, lddw, 16, "dw"));
+    if (!any) return 0;
+    Backward b{};
+    b.dtype = dtype;
+    b.rows = t;
+    b.n = 2 * n;
+    b.k = k;
+    b.experts = 1;
+    b.tokens = t;
+    b.top = 1;
+    b.dy = dy;
+    b.lddy = lddy;
+    b.x = x;
+    b.ldx = ldx;
+    b.w = w;
+    b.ldw = ldw;
+    b.act = act;
+    b.z = preact;
+    b.ldz = ldz;
+    b.dx = dx;
+    b.lddx = lddx;
+    b.dw = dw;
+    b.lddw = lddw;
+    b.dbias = dbias;
+    b.gated = true;
     return backward(b, static_cast<cudaStream_t>(stream));
 }
 

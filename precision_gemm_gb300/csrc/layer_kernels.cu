@@ -118,6 +118,108 @@ __global__ void __launch_bounds__(256, 4) dact_kernel(int64_t rows, int64_t n, c
     }
 }
 
+// dz = [dy v act'(g), dy act(g)] for a slab of rows x 256 columns of z = [g v], and the slab's
+// sums of its 2 n columns in part (slabs x 2 n), with the threads laid out as in dact_kernel.
+// HBM-bound: reads dy and z, writes dz.
+template <typename T, int PARTS>
+__global__ void __launch_bounds__(256, 2) dgate_kernel(int64_t rows, int64_t n, const T* dy, int64_t lddy, const T* z,
+                                                       int64_t ldz, int act, bf16* dz, int64_t lddz, float* part,
+                                                       int slab_size, bool vec) {
+    __shared__ float sums[8][kWidth + 8];
+    pdl_trigger();
+    pdl_wait();
+    const int64_t widths = (n + kWidth - 1) / kWidth, slab = blockIdx.x / widths;
+    const int64_t c0 = (blockIdx.x - slab * widths) * kWidth, c = c0 + 8 * (threadIdx.x % 32);
+    const int l = threadIdx.x / 32;
+    const int valid = static_cast<int>(n - c < 8 ? n - c : 8);  // <= 0: no columns here
+    const int64_t r0 = slab * slab_size, r1 = rows - r0 < slab_size ? rows : r0 + slab_size;
+    const bool whole = valid == 8 && n % 8 == 0;  // of dz too, whose second half starts at column n
+    float sum[2][8] = {};
+    auto one = [&](auto f, int64_t r, const float(&d)[8], const float(&g)[8], const float(&v)[8]) {
+        float dg[8], dv[8];
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+            float value, slope;
+            act_both<decltype(f)::value, PARTS == 1>(g[t], value, slope);
+            dg[t] = d[t] * v[t] * slope;
+            dv[t] = d[t] * value;
+            sum[0][t] += dg[t];
+            sum[1][t] += dv[t];
+        }
+        bf16* at = dz + r * lddz + c;
+        if (whole) {
+            store_parts8<PARTS>(at, rows * lddz, dg);
+            store_parts8<PARTS>(at + n, rows * lddz, dv);
+        } else {
+#pragma unroll
+            for (int t = 0; t < 8; ++t) {
+                if (t >= valid) break;
+                bf16 a[PARTS], b[PARTS];
+                split_bf16<PARTS>(dg[t], a);
+                split_bf16<PARTS>(dv[t], b);
+#pragma unroll
+                for (int q = 0; q < PARTS; ++q) {
+                    at[q * rows * lddz + t] = a[q];
+                    at[q * rows * lddz + n + t] = b[q];
+                }
+            }
+        }
+    };
+    if (valid > 0) {
+        with_act(act, [&](auto f) {
+            constexpr int N = sizeof(T) / 2, R = 2 / N;  // 16-byte words of eight elements; rows
+            int64_t r = r0 + l;
+            if (vec && valid == 8) {
+                for (; r + 8 * (R - 1) < r1; r += 8 * R) {
+                    uint4 d[R][N], g[R][N], v[R][N];
+#pragma unroll
+                    for (int k = 0; k < R; ++k)
+#pragma unroll
+                        for (int q = 0; q < N; ++q) {
+                            d[k][q] = __ldcs(reinterpret_cast<const uint4*>(dy + (r + 8 * k) * lddy + c) + q);
+                            g[k][q] = __ldcs(reinterpret_cast<const uint4*>(z + (r + 8 * k) * ldz + c) + q);
+                            v[k][q] = __ldcs(reinterpret_cast<const uint4*>(z + (r + 8 * k) * ldz + n + c) + q);
+                        }
+#pragma unroll
+                    for (int k = 0; k < R; ++k) {
+                        float df[8], gf[8], vf[8];
+#pragma unroll
+                        for (int t = 0; t < 8; ++t) {
+                            df[t] = to_float(reinterpret_cast<const T*>(d[k])[t]);
+                            gf[t] = to_float(reinterpret_cast<const T*>(g[k])[t]);
+                            vf[t] = to_float(reinterpret_cast<const T*>(v[k])[t]);
+                        }
+                        one(f, r + 8 * k, df, gf, vf);
+                    }
+                }
+            }
+#pragma unroll 1
+            for (; r < r1; r += 8) {
+                float df[8], gf[8], vf[8];
+                load8(dy + r * lddy + c, vec, valid, df);
+                load8(z + r * ldz + c, vec, valid, gf);
+                load8(z + r * ldz + n + c, vec, valid, vf);
+                one(f, r, df, gf, vf);
+            }
+        });
+    }
+    if (!part) return;
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+#pragma unroll
+        for (int t = 0; t < 8; ++t) sums[l][8 * (threadIdx.x % 32) + t] = sum[which][t];
+        __syncthreads();
+        const int64_t col = c0 + threadIdx.x;
+        if (col < n) {
+            float s = 0.0f;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) s += sums[q][threadIdx.x];
+            part[slab * 2 * n + which * n + col] = s;
+        }
+        __syncthreads();
+    }
+}
+
 // dbias[g][c] = the sums of group g's slabs: 8 threads per column take every eighth,
 // and their sums are added in order.
 template <typename T>
@@ -302,6 +404,34 @@ static cudaError_t run_dact(int64_t rows, int64_t n, const void* dy, int64_t ldd
         e = launch_kernel(true, dbias_kernel<T>, dim3(static_cast<unsigned>((n + 31) / 32), groups), dim3(256), 0, st,
                           rows, n, offsets, static_cast<const float*>(part), static_cast<T*>(dbias), slab);
     return e;
+}
+
+size_t gate_part_bytes(int64_t rows, int64_t n, int num_sms) {
+    const int slab = slab_rows(rows, n, num_sms);
+    return static_cast<size_t>((rows + slab - 1) / slab) * 2 * n * 4;
+}
+
+template <typename T, int PARTS>
+static cudaError_t run_dgate(int64_t rows, int64_t n, const void* dy, int64_t lddy, const void* z, int64_t ldz, int act,
+                             bf16* dz, int64_t lddz, void* dbias, float* part, int num_sms, cudaStream_t st) {
+    const int slab = slab_rows(rows, n, num_sms);
+    const dim3 grid(static_cast<unsigned>(((rows + slab - 1) / slab) * ((n + kWidth - 1) / kWidth)));
+    const bool vec = n % 8 == 0 && rows_aligned<T>(dy, lddy) && rows_aligned<T>(z, ldz);
+    cudaError_t e = cudaSuccess;
+    if (rows > 0)
+        e = launch_kernel(true, dgate_kernel<T, PARTS>, grid, dim3(256), 0, st, rows, n, static_cast<const T*>(dy), lddy,
+                          static_cast<const T*>(z), ldz, act, dz, lddz, dbias ? part : nullptr, slab, vec);
+    if (dbias && e == cudaSuccess)
+        e = launch_kernel(true, dbias_kernel<T>, dim3(static_cast<unsigned>((2 * n + 31) / 32), 1), dim3(256), 0, st,
+                          rows, 2 * n, static_cast<const int32_t*>(nullptr), static_cast<const float*>(part),
+                          static_cast<T*>(dbias), slab);
+    return e;
+}
+
+cudaError_t launch_dgate(int dtype, int64_t rows, int64_t n, const void* dy, int64_t lddy, const void* z, int64_t ldz,
+                         int act, bf16* dz, int64_t lddz, void* dbias, float* part, int num_sms, cudaStream_t st) {
+    return dtype == SGEMM_F32 ? run_dgate<float, 3>(rows, n, dy, lddy, z, ldz, act, dz, lddz, dbias, part, num_sms, st)
+                              : run_dgate<bf16, 1>(rows, n, dy, lddy, z, ldz, act, dz, lddz, dbias, part, num_sms, st);
 }
 
 cudaError_t launch_dact(int dtype, int64_t rows, int64_t n, const void* dy, int64_t lddy, const void* z, int64_t ldz,

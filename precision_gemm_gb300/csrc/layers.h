@@ -105,6 +105,24 @@ __device__ __forceinline__ float act_derivative(float z) {
     return 1.0f;
 }
 
+// Both at once: they share the exponential.
+template <int ACT, bool FAST>
+__device__ __forceinline__ void act_both(float z, float& value, float& slope) {
+    if (ACT == SGEMM_ACT_SILU) {
+        const float p = logistic<FAST>(z);
+        value = z * p;
+        slope = p * fmaf(z, 1.0f - p, 1.0f);
+    } else if (ACT == SGEMM_ACT_GELU && FAST) {
+        float e;
+        const float tail = normal_tail(z, e);
+        value = fmaf(-fminf(fabsf(z), 3.4e38f), tail, relu(z));
+        slope = fmaf(z * 0.39894228040143268f, e, z >= 0.0f ? 1.0f - tail : tail);
+    } else {
+        value = act_value<ACT, FAST>(z);
+        slope = act_derivative<ACT, FAST>(z);
+    }
+}
+
 // Two values at once, their multiplies and adds in packed instructions: the activation's
 // backward pass is bound by instructions as much as by memory.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
@@ -309,6 +327,9 @@ struct Product {
     void* preact;
     int64_t ldz;
     bool out_f32;            // out is FP32 whatever dtype (no residual, no preact)
+    // A has 2 ni rows and out = act(g) v with g of row i, v of row ni + i; bias and preact hold
+    // both, the gate's first (one group, rows along k, no residual).
+    bool gated;
 };
 
 // ---- launchers ----
@@ -370,6 +391,11 @@ cudaError_t launch_dact(int dtype, int64_t rows, int64_t n, const void* dy, int6
                         int act, bf16* dz, int64_t lddz, int groups, const int32_t* offsets, void* dbias, float* part,
                         int num_sms, cudaStream_t st);
 int dact_launches(bool with_bias);
+// The same for out = act(g) v: z = [g v] and dz = [dy v act'(g), dy act(g)] have 2 n columns, dbias 2 n
+// entries (one group).
+size_t gate_part_bytes(int64_t rows, int64_t n, int num_sms);
+cudaError_t launch_dgate(int dtype, int64_t rows, int64_t n, const void* dy, int64_t lddy, const void* z, int64_t ldz,
+                         int act, bf16* dz, int64_t lddz, void* dbias, float* part, int num_sms, cudaStream_t st);
 
 // x_f32: the rows are FP32 whatever dtype.
 cudaError_t launch_combine(int dtype, bool x_f32, int64_t tokens, int top, int64_t n, const void* x, int64_t ldx,

@@ -63,8 +63,9 @@ __device__ __forceinline__ void unpack(const uint4& raw, float (&v)[8]) {
 }
 
 // M rows of x at a time, F weight rows per warp, U steps of loads in flight (VEC: all
-// rows at 16-byte boundaries), B blocks per SM.
-template <typename T, bool VEC, int M, int F, int U, int B>
+// rows at 16-byte boundaries), B blocks per SM.  GATED: half of a warp's weight rows are the
+// gate's, the others those of what it gates, ni rows further on.
+template <typename T, bool VEC, bool GATED, int M, int F, int U, int B>
 __global__ void __launch_bounds__(32 * kWarps, B) product_rows_kernel(const RowsParams q) {
     constexpr int V = 16 / sizeof(T);
     const Product& p = q.p;
@@ -85,15 +86,17 @@ __global__ void __launch_bounds__(32 * kWarps, B) product_rows_kernel(const Rows
     int first = 0, end = rows;
     if (p.offsets) expert_rows(p.offsets, g, rows, first, end);
     if (first >= end) return;
-    const int ks = q.ks, per_block = kWarps / ks * F;
+    constexpr int FO = GATED ? F / 2 : F;  // results of a warp
+    const int ks = q.ks, per_block = kWarps / ks * FO;
     const int part = warp % ks;
-    const int64_t i0 = static_cast<int64_t>(blockIdx.x) * per_block + warp / ks * F;
+    const int64_t i0 = static_cast<int64_t>(blockIdx.x) * per_block + warp / ks * FO;
     // this warp's steps of 32 V elements
     const int64_t steps = (p.nk + 32 * V - 1) / (32 * V);
     const int64_t s0 = steps * part / ks, s1 = steps * (part + 1) / ks;
-    const bool all = i0 + F <= p.ni;  // F weight rows are there
+    const bool all = i0 + FO <= p.ni;  // F weight rows are there
     const int64_t ldw = p.a.ld;
     const int at_lane = VEC ? lane * V : lane;
+    const int64_t up = GATED ? p.ni * ldw : 0;  // from the gate's rows to the others
     const T* w = static_cast<const T*>(p.a.ptr) + g * p.a.stride + min(i0, p.ni - 1) * ldw + at_lane;
     for (int j0 = first; j0 < end; j0 += M) {
         const T* x = static_cast<const T*>(p.b.ptr) + at_lane;
@@ -127,7 +130,7 @@ __global__ void __launch_bounds__(32 * kWarps, B) product_rows_kernel(const Rows
                 if (at < whole) {
 #pragma unroll
                     for (int f = 0; f < F; ++f) {
-                        const T* from = w + f * ldw + at * 32 * V;
+                        const T* from = w + (f < FO ? f * ldw : up + (f - FO) * ldw) + at * 32 * V;
                         to[f] = VEC ? stream16(from) : load16<T, VEC, true>(from, 0);
                     }
                 }
@@ -152,7 +155,7 @@ __global__ void __launch_bounds__(32 * kWarps, B) product_rows_kernel(const Rows
             const int64_t c = s * 32 * V, left = p.nk - c - at_lane;
             uint4 raw[F];
 #pragma unroll
-            for (int f = 0; f < F; ++f) raw[f] = load16<T, VEC, false>(w + (i0 + f < p.ni ? f : 0) * ldw + c, left);
+            for (int f = 0; f < F; ++f) raw[f] = load16<T, VEC, false>(w + (i0 + f % FO < p.ni ? f % FO : 0) * ldw + (f < FO ? 0 : up) + c, left);
 #pragma unroll
             for (int m = 0; m < M; ++m) add(raw, load16<T, VEC, false>(x + row[m] + c, left), m);
         }
@@ -170,12 +173,19 @@ __global__ void __launch_bounds__(32 * kWarps, B) product_rows_kernel(const Rows
             const int64_t j = j0 + m;
             if (i < p.ni && j < end) {
                 float z = 0.0f;
-                for (int k = 0; k < ks; ++k) z += sums[li / F * ks + k][li % F * M + m];
+                for (int k = 0; k < ks; ++k) z += sums[li / FO * ks + k][li % FO * M + m];
+                float v = 0.0f;
+                if (GATED) {
+                    for (int k = 0; k < ks; ++k) v += sums[li / FO * ks + k][(FO + li % FO) * M + m];
+                    if (p.bias) v += to_float(static_cast<const T*>(p.bias)[p.ni + i]);
+                    if (p.preact) static_cast<T*>(p.preact)[j * p.ldz + p.ni + i] = from_float<T>(v);
+                }
                 if (p.b.list && gathered_row(p.b.list, p.b.top, j, p.b.rows) < 0) z = 0.0f;  // it reads as zeros
                 if (p.bias) z += to_float(static_cast<const T*>(p.bias)[g * p.ni + i]);
                 if (p.preact) static_cast<T*>(p.preact)[j * p.ldz + i] = from_float<T>(z);
                 float y = 0.0f;
                 with_act(p.act, [&](auto a) { y = act_value<decltype(a)::value, std::is_same<T, bf16>::value>(z); });
+                if (GATED) y *= v;
                 if (p.residual) y += to_float(static_cast<const T*>(p.residual)[j * p.ldr + i]);
                 static_cast<T*>(p.out)[j * p.ldo + i] = from_float<T>(y);
             }
@@ -184,22 +194,23 @@ __global__ void __launch_bounds__(32 * kWarps, B) product_rows_kernel(const Rows
     }
 }
 
-template <typename T, bool VEC, int M, int F, int U, int B>
+template <typename T, bool VEC, bool GATED, int M, int F, int U, int B>
 cudaError_t run(const Product& p, int num_sms, cudaStream_t st) {
     constexpr int V = 16 / sizeof(T);
     // Enough warps to keep HBM busy: a weight row's k is shared by up to eight while there are fewer
     // than 4 B per SM (half of those that fit) and each keeps two rounds of loads (8192 x 2048
     // float32, five rows: with at least 8 B 17.8 us, 4 B 15.8; 2048 x 8192: 17.9, 15.7, 2 B 25.7).
     const int64_t active = std::max<int64_t>(1, std::min<int64_t>(p.groups, p.nj));
-    const int64_t warps = (p.ni + F - 1) / F * active;
+    constexpr int FO = GATED ? F / 2 : F;
+    const int64_t warps = (p.ni + FO - 1) / FO * active;
     RowsParams q{p, 1};
     while (q.ks < kWarps && warps * q.ks * 2 < kWarps * B * num_sms && p.nk >= 2 * q.ks * 2 * U * 32 * V) q.ks *= 2;
-    const int64_t per_block = kWarps / q.ks * F;
+    const int64_t per_block = kWarps / q.ks * FO;
     const dim3 grid(static_cast<unsigned>((p.ni + per_block - 1) / per_block), p.groups + (p.offsets ? 1 : 0));
-    return launch_kernel(true, product_rows_kernel<T, VEC, M, F, U, B>, grid, dim3(32 * kWarps), 0, st, q);
+    return launch_kernel(true, product_rows_kernel<T, VEC, GATED, M, F, U, B>, grid, dim3(32 * kWarps), 0, st, q);
 }
 
-template <typename T, bool VEC>
+template <typename T, bool VEC, bool GATED>
 cudaError_t dispatch(const Product& p, int rows, int num_sms, cudaStream_t st) {
     // Up to three rows of float32, two of bfloat16, have registers for eight weight rows at once:
     // x is read half as often (HBM to registers, 8192 x 8192 float32, one row: four weight rows of
@@ -208,35 +219,37 @@ cudaError_t dispatch(const Product& p, int rows, int num_sms, cudaStream_t st) {
     constexpr bool f32 = sizeof(T) == 4;
     constexpr int F = f32 || VEC ? 8 : 4, U = f32 ? 1 : 2;
     switch (rows) {
-        case 1: return run<T, VEC, 1, F, U, 2>(p, num_sms, st);
-        case 2: return run<T, VEC, 2, F, U, 2>(p, num_sms, st);
-        case 3: return run<T, VEC, 3, f32 ? 8 : 4, f32 ? 1 : (VEC ? 4 : 2), 2>(p, num_sms, st);
+        case 1: return run<T, VEC, GATED, 1, F, U, 2>(p, num_sms, st);
+        case 2: return run<T, VEC, GATED, 2, F, U, 2>(p, num_sms, st);
+        case 3: return run<T, VEC, GATED, 3, f32 ? 8 : 4, f32 ? 1 : (VEC ? 4 : 2), 2>(p, num_sms, st);
         default: break;
     }
     // more than four rows of bfloat16 are a longer list's, in further passes (few_rows)
     if constexpr (std::is_same<T, float>::value) {
         switch (rows) {
             case 4: break;
-            case 5: return run<T, VEC, 5, 4, 2, 2>(p, num_sms, st);
-            case 6: return run<T, VEC, 6, 4, 2, 2>(p, num_sms, st);
+            case 5: return run<T, VEC, GATED, 5, 4, 2, 2>(p, num_sms, st);
+            case 6: return run<T, VEC, GATED, 6, 4, 2, 2>(p, num_sms, st);
             case 7:
-            case 8: return run<T, VEC, 8, 4, 2, 2>(p, num_sms, st);
+            case 8: return run<T, VEC, GATED, 8, 4, 2, 2>(p, num_sms, st);
             case 9:
             case 10:
             case 11:
-            case 12: return run<T, VEC, 12, 4, 1, 2>(p, num_sms, st);
-            default: return run<T, VEC, 16, 4, 1, 2>(p, num_sms, st);
+            case 12: return run<T, VEC, GATED, 12, 4, 1, 2>(p, num_sms, st);
+            default: return run<T, VEC, GATED, 16, 4, 1, 2>(p, num_sms, st);
         }
     }
-    return run<T, VEC, 4, 4, 2, 2>(p, num_sms, st);
+    return run<T, VEC, GATED, 4, 4, 2, 2>(p, num_sms, st);
 }
 
 template <typename T>
 cudaError_t launch(const Product& p, int rows, int num_sms, cudaStream_t st) {
     const bool vec = rows_aligned<T>(p.a.ptr, p.a.ld) && p.a.stride * sizeof(T) % 16 == 0 &&
                      rows_aligned<T>(p.b.ptr, p.b.rows == 1 ? 0 : p.b.ld);
-    return vec ? dispatch<T, true>(p, rows, num_sms, st)
-               : dispatch<T, false>(p, rows, num_sms, st);
+    if (p.gated)
+        return vec ? dispatch<T, true, true>(p, rows, num_sms, st) : dispatch<T, false, true>(p, rows, num_sms, st);
+    return vec ? dispatch<T, true, false>(p, rows, num_sms, st)
+               : dispatch<T, false, false>(p, rows, num_sms, st);
 }
 
 }  // namespace

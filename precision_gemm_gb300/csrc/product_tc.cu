@@ -54,10 +54,13 @@ constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kCols = 16;      // columns (j) that an epilogue warp takes at a time
 constexpr int kGroupTiles = 8;  // rasterisation: tiles of j walked before the next tile of i
 
-template <int BN>
+// GATED: rows of A come in pairs, i (the gate's) and ni + i, each with an accumulator of its own.
+template <int BN, bool GATED>
 struct Cfg {
     static constexpr int BNH = BN / 2;
-    static constexpr int A_BYTES = kBI * kBK * 2;
+    static constexpr int COLS = GATED ? 2 * BN : BN;  // of the accumulators of a unit
+    static constexpr int A_TILE = kBI * kBK * 2;
+    static constexpr int A_BYTES = GATED ? 2 * A_TILE : A_TILE;
     static constexpr int B_BYTES = BNH * kBK * 2;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
     static constexpr int STAGES_RAW = 200 * 1024 / STAGE_BYTES;
@@ -65,9 +68,9 @@ struct Cfg {
     static constexpr int TABLE_BYTES = 2 * (SGEMM_MAX_EXPERTS + 1) * 4 + 8;
     static constexpr int BAR_BYTES = (2 * STAGES + 5) * 8 + 16;
     static constexpr size_t SMEM = 1024 + static_cast<size_t>(STAGES) * STAGE_BYTES + TABLE_BYTES + BAR_BYTES;
-    static constexpr uint32_t TMEM_COLS = 2 * BN < 32 ? 32 : 2 * BN;
-    static constexpr int CHUNKS = BN / kCols;  // column chunks of a tile
-    static constexpr int MINE = CHUNKS / 2;    // of one epilogue warp
+    static constexpr uint32_t TMEM_COLS = 2 * COLS < 32 ? 32 : 2 * COLS;
+    static constexpr int CHUNKS = COLS / kCols;  // column chunks of the accumulators
+    static constexpr int MINE = CHUNKS / 2;      // of one epilogue warp
     static_assert(A_BYTES % 1024 == 0 && B_BYTES % 1024 == 0, "slots need 1 KiB alignment");
     static_assert(TABLE_BYTES % 8 == 0, "barriers need 8-byte alignment");
 };
@@ -150,14 +153,44 @@ __device__ __forceinline__ void finish(const Params& p, float (&v)[N], float bia
     }
 }
 
+// The same of a gated product: sums g of the gate and v of what it gates, out = act(g) v.
+template <typename T, int N>
+__device__ __forceinline__ void finish_gated(const Params& p, float (&g)[N], float (&v)[N], float bias_g, float bias_v,
+                                             int64_t i, int64_t jb, int jn) {
+#pragma unroll
+    for (int t = 0; t < N; ++t) {
+        g[t] += bias_g;
+        v[t] += bias_v;
+    }
+    if (p.preact) {
+        T* dst = static_cast<T*>(p.preact) + jb * p.ldz + i;
+        const int64_t ld = p.ldz;
+#pragma unroll
+        for (int t = 0; t < N; ++t, dst += ld)
+            if (t < jn) {
+                dst[0] = from_float<T>(g[t]);
+                dst[p.ni] = from_float<T>(v[t]);
+            }
+    }
+    with_act(p.act, [&](auto act) {
+#pragma unroll
+        for (int t = 0; t < N; ++t) v[t] *= act_value<decltype(act)::value, std::is_same<T, bf16>::value>(g[t]);
+    });
+    T* dst = static_cast<T*>(p.out) + jb * p.ldo + i;
+    const int64_t ld = p.ldo;
+#pragma unroll
+    for (int t = 0; t < N; ++t, dst += ld)
+        if (t < jn) *dst = from_float<T>(v[t]);
+}
+
 // F32: float32 operands in three parts, accumulated in chunks.
-template <int BN, bool F32>
+template <int BN, bool F32, bool GATED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     product_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                       const __grid_constant__ CUtensorMap tmAg, const __grid_constant__ CUtensorMap tmBg,
                       const __grid_constant__ CUtensorMap tmA16, const __grid_constant__ CUtensorMap tmB16,
                       const Params p) {
-    using C = Cfg<BN>;
+    using C = Cfg<BN, GATED>;
     using T = typename std::conditional<F32, float, bf16>::type;
     constexpr int S = C::STAGES;
     extern __shared__ uint8_t smem_raw[];
@@ -401,6 +434,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                         tma_load_3d_pair_warp(slot + 8192, &tmA, ia + 64, kc, z_a, bar);
                                     } else {
                                         tma_load_3d_pair_warp(slot, &tmA, kc, ia, z_a, bar);
+                                        if (GATED)
+                                            tma_load_3d_pair_warp(slot + C::A_TILE, &tmA, kc, p.ni + ia, z_a, bar);
                                     }
                                     if (p.b_mn) {
 #pragma unroll
@@ -463,7 +498,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if (!ok) break;
                     take_buffer(next, acc_phase, c0 == 0);
                     tc_fence_after_sync();
-                    const uint32_t d = tmem + buf * BN;
+                    const uint32_t d = tmem + buf * C::COLS;
                     uint32_t accumulate = 0;
                     for (int kb = 0; kb < steps; ++kb) {
                         ok = __all_sync(0xffffffffu,
@@ -478,6 +513,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             if (16 * kk >= left) break;
                             mma_bf16_pair_warp(d, a_desc0 + (o + kk * a_step), b_desc0 + (o + kk * b_step), idesc,
                                                accumulate);
+                            if (GATED)
+                                mma_bf16_pair_warp(d + BN, a_desc0 + (o + kk * a_step + (C::A_TILE >> 4)),
+                                                   b_desc0 + (o + kk * b_step), idesc, accumulate);
                             accumulate = 1;
                         }
                         mma_commit_pair_warp(empty0 + 8 * slot_i);
@@ -515,14 +553,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
         }
         if (p.part && blockIdx.x == 0 && epi == 0 && lane == 0) p.info[0] = make_int4(tiles - whole, 0, 0, 0);
-        float bias = 0.0f;  // of the unit's group and this thread's i
-        auto finish_chunk = [&](const Unit& x, float(&v)[kCols], int c) {
+        float bias = 0.0f, bias_v = 0.0f;  // of the unit's group and this thread's i
+        auto finish_chunk = [&](const Unit& x, float(&v)[kCols], float(&up)[kCols], int c) {
             const int64_t i = x.i0 + kBI * rank + 32 * q + lane;
             if (i >= p.ni) return;
             const int64_t jb = x.j0 + kCols * c;
             const int jn = x.j_end - x.j0 - kCols * c;
             const int64_t base = p.rows_on_k ? x.g * p.out_stride : 0;
-            if (F32 || !p.out_f32)
+            if (GATED)
+                finish_gated<T>(p, v, up, bias, bias_v, i, jb, jn);
+            else if (F32 || !p.out_f32)
                 finish<T, T>(p, v, bias, base, i, jb, jn);
             else
                 finish<T, float>(p, v, bias, base, i, jb, jn);
@@ -534,11 +574,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const Unit x = unit_of(u);
             const int cols = min(BN, x.j_end - x.j0);
             // this slice's block: [column][256 i]
-            float* block = x.tile >= 0 ? p.part + (static_cast<int64_t>(x.tile) * p.split + x.slice) * (2 * kBI * BN) +
+            float* block = x.tile >= 0 ? p.part + (static_cast<int64_t>(x.tile) * p.split + x.slice) * (2 * kBI * C::COLS) +
                                              kBI * rank + 32 * q + lane
                                        : nullptr;
             const int64_t i = x.i0 + kBI * rank + 32 * q + lane;
             if (p.bias && i < p.ni) bias = to_float(static_cast<const T*>(p.bias)[static_cast<int64_t>(x.g) * p.ni + i]);
+            if (GATED && p.bias && i < p.ni) bias_v = to_float(static_cast<const T*>(p.bias)[p.ni + i]);
             if (p.residual && i - lane < p.ni) {
                 // the residual comes into L2 while the MMAs run: lane t asks for column t's line
                 for (int t = kCols * half + lane % kCols + 2 * kCols * (lane / kCols); t < cols; t += 4 * kCols)
@@ -574,10 +615,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if (!ok) break;
 #pragma unroll
                     for (int m = 0; m < C::MINE; ++m) {
-                        if (kCols * (half + 2 * m) < cols) {
+                        if (kCols * (half + 2 * m) % BN < cols) {
                             uint32_t v[kCols];
                             __syncwarp();
-                            tmem_ld_32x32b_x16(lane_base + buf * BN + kCols * (half + 2 * m), v);
+                            tmem_ld_32x32b_x16(lane_base + buf * C::COLS + kCols * (half + 2 * m), v);
                             tmem_wait_ld();
 #pragma unroll
                             for (int t = 0; t < kCols; ++t) acc[m][t] += __uint_as_float(v[t]);
@@ -588,12 +629,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (!ok) break;
 #pragma unroll
                 for (int m = 0; m < C::MINE; ++m) {
-                    if (kCols * (half + 2 * m) < cols) {
+                    if (kCols * (half + 2 * m) % BN < cols) {
                         uint32_t v[kCols];
 #pragma unroll
                         for (int t = 0; t < kCols; ++t) v[t] = __float_as_uint(acc[m][t]);
                         __syncwarp();
-                        tmem_st_32x32b_x16(lane_base + buf * BN + kCols * (half + 2 * m), v);
+                        tmem_st_32x32b_x16(lane_base + buf * C::COLS + kCols * (half + 2 * m), v);
                     }
                 }
                 tmem_wait_st();
@@ -608,17 +649,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     const int more = wait_sums(false);
                     if (!ok) break;
 #pragma unroll 1
-                    for (int c = half; kCols * c < cols; c += 2) {
+                    for (int c = half; c < C::CHUNKS; c += 2) {
+                        if (kCols * c % BN >= cols) continue;
                         uint32_t v[kCols], sum[kCols];
                         __syncwarp();
-                        tmem_ld_32x32b_x16(lane_base + more * BN + kCols * c, v);
-                        tmem_ld_32x32b_x16(lane_base + buf * BN + kCols * c, sum);
+                        tmem_ld_32x32b_x16(lane_base + more * C::COLS + kCols * c, v);
+                        tmem_ld_32x32b_x16(lane_base + buf * C::COLS + kCols * c, sum);
                         tmem_wait_ld();
 #pragma unroll
                         for (int t = 0; t < kCols; ++t)
                             sum[t] = __float_as_uint(__uint_as_float(sum[t]) + __uint_as_float(v[t]));
                         __syncwarp();
-                        tmem_st_32x32b_x16(lane_base + buf * BN + kCols * c, sum);
+                        tmem_st_32x32b_x16(lane_base + buf * C::COLS + kCols * c, sum);
                     }
                     tmem_wait_st();
                     free_sums(more);
@@ -627,12 +669,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
 #pragma unroll 1
             for (int c = half; kCols * c < cols; c += 2) {
-                float f[kCols];
+                float f[kCols], up[kCols] = {};
                 __syncwarp();
                 if (any) {
-                    uint32_t v[kCols];
-                    tmem_ld_32x32b_x16(lane_base + buf * BN + kCols * c, v);
+                    uint32_t v[kCols], u[kCols];
+                    tmem_ld_32x32b_x16(lane_base + buf * C::COLS + kCols * c, v);
+                    if (GATED) tmem_ld_32x32b_x16(lane_base + buf * C::COLS + BN + kCols * c, u);
                     tmem_wait_ld();
+                    if (GATED)
+#pragma unroll
+                        for (int t = 0; t < kCols; ++t) up[t] = __uint_as_float(u[t]);
 #pragma unroll
                     for (int t = 0; t < kCols; ++t) f[t] = __uint_as_float(v[t]);
                 } else {
@@ -641,9 +687,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 if (block) {
 #pragma unroll
-                    for (int t = 0; t < kCols; ++t) block[(kCols * c + t) * (2 * kBI)] = f[t];
+                    for (int t = 0; t < kCols; ++t) {
+                        block[(kCols * c + t) * (2 * kBI)] = f[t];
+                        if (GATED) block[(BN + kCols * c + t) * (2 * kBI)] = up[t];
+                    }
                 } else {
-                    finish_chunk(x, f, c);
+                    finish_chunk(x, f, up, c);
                 }
             }
             if (any) free_sums(buf);
@@ -666,7 +715,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // in their order and finishes them.  The tiles' places are checked against the matrix, since
 // a product that gave up (a wait that expired) may not have written them.
 constexpr int kSumCols = 4;
-template <bool F32>
+template <bool F32, bool GATED>
 __global__ void __launch_bounds__(2 * kBI) sum_slices_kernel(const Params p, int bn, int most) {
     using T = typename std::conditional<F32, float, bf16>::type;
     pdl_trigger();
@@ -677,21 +726,32 @@ __global__ void __launch_bounds__(2 * kBI) sum_slices_kernel(const Params p, int
     const int64_t i = static_cast<int64_t>(at.x) + threadIdx.x;
     const int jn = at.z - at.y - c0;
     if (at.x < 0 || i >= p.ni || at.y < 0 || at.z > p.nj || jn <= 0 || at.w < 0 || at.w >= p.groups) return;
-    const float* src = p.part + static_cast<int64_t>(tile) * p.split * (2 * kBI * bn) + c0 * (2 * kBI) + threadIdx.x;
-    float v[kSumCols] = {};
-    for (int s0 = 0; s0 < p.split; s0 += 8) {
-        float b[8][kSumCols];
+    const int slice = 2 * kBI * bn * (GATED ? 2 : 1);
+    auto sum = [&](int column, float(&v)[kSumCols]) {
+        const float* src = p.part + static_cast<int64_t>(tile) * p.split * slice + column * (2 * kBI) + threadIdx.x;
 #pragma unroll
-        for (int s = 0; s < 8; ++s)
+        for (int t = 0; t < kSumCols; ++t) v[t] = 0.0f;
+        for (int s0 = 0; s0 < p.split; s0 += 8) {
+            float b[8][kSumCols];
 #pragma unroll
-            for (int t = 0; t < kSumCols; ++t)
-                b[s][t] = s0 + s < p.split
-                              ? __ldcg(src + static_cast<int64_t>(s0 + s) * (2 * kBI * bn) + t * (2 * kBI))
-                              : 0.0f;
+            for (int s = 0; s < 8; ++s)
 #pragma unroll
-        for (int s = 0; s < 8; ++s)
+                for (int t = 0; t < kSumCols; ++t)
+                    b[s][t] = s0 + s < p.split ? __ldcg(src + static_cast<int64_t>(s0 + s) * slice + t * (2 * kBI)) : 0.0f;
 #pragma unroll
-            for (int t = 0; t < kSumCols; ++t) v[t] += b[s][t];
+            for (int s = 0; s < 8; ++s)
+#pragma unroll
+                for (int t = 0; t < kSumCols; ++t) v[t] += b[s][t];
+        }
+    };
+    float v[kSumCols];
+    sum(c0, v);
+    if (GATED) {
+        float up[kSumCols];
+        sum(bn + c0, up);
+        const T* b = static_cast<const T*>(p.bias);
+        finish_gated<T>(p, v, up, b ? to_float(b[i]) : 0.0f, b ? to_float(b[p.ni + i]) : 0.0f, i, at.y + c0, jn);
+        return;
     }
     const float bias =
         p.bias ? to_float(static_cast<const T*>(p.bias)[static_cast<int64_t>(at.w) * p.ni + i]) : 0.0f;
@@ -773,10 +833,10 @@ __global__ void __launch_bounds__(256) copy_rows_kernel(const bf16* src, int64_t
         if (first + 32 * k + lane < eights) out[32 * k + lane] = v[k];
 }
 
-template <int BN, bool F32>
+template <int BN, bool F32, bool GATED>
 cudaError_t launch(const CUtensorMap (&m)[6], const Params& p, int64_t units, int num_sms, cudaStream_t st) {
-    using C = Cfg<BN>;
-    auto kern = product_tc_kernel<BN, F32>;
+    using C = Cfg<BN, GATED>;
+    auto kern = product_tc_kernel<BN, F32, GATED>;
     static std::atomic<uint64_t> smem_set{0};
     cudaError_t e = set_smem_limit_once(smem_set, reinterpret_cast<const void*>(kern), static_cast<int>(C::SMEM));
     if (e != cudaSuccess) return e;
@@ -858,15 +918,18 @@ TcPlan plan_tc(const Product& p, int num_sms, int force_bn, int force_split) {
     const int64_t tiles_i = cdiv(p.ni, 2 * kBI), kb = cdiv(p.nk, kBK);
     const int64_t lists = p.rows_on_k ? 1 : std::max<int64_t>(1, std::min<int64_t>(p.groups, p.nj));
     const double segs = p.dtype == SGEMM_F32 ? 6.0 : 1.0;
+    const int accs = p.gated ? 2 : 1, widest = 256 / accs;  // accumulators of a tile; TMEM holds 512 columns
     // groups that share out k hold a group's part of it each, on average
     const double steps = segs * (p.rows_on_k && p.groups > 1 ? std::max(1.0, static_cast<double>(kb) / p.groups) : kb);
     TcPlan best{};
     double best_us = 0.0;
     for (int bn : {256, 128, 64, 32}) {
         if (bn < 128 && !p.b.k_contiguous) break;
-        if (force_bn && bn != (p.b.k_contiguous ? force_bn : std::max(force_bn, 128)) && force_bn <= 256) continue;
-        const double step = bn == 256 ? 0.34 : (bn == 128 ? 0.19 : (bn == 64 ? 0.14 : 0.12));
-        const double end = (bn == 256 ? 4.0 : (bn == 128 ? 2.0 : 1.0)) * (p.residual ? 3.0 : 1.0);
+        if (bn > widest) continue;
+        if (force_bn && bn != std::min(p.b.k_contiguous ? force_bn : std::max(force_bn, 128), widest) && force_bn <= 256) continue;
+        const double step = p.gated ? (bn == 128 ? 0.36 : (bn == 64 ? 0.26 : 0.23))
+                                    : (bn == 256 ? 0.34 : (bn == 128 ? 0.19 : (bn == 64 ? 0.14 : 0.12)));
+        const double end = (bn * accs == 256 ? 4.0 : (bn * accs == 128 ? 2.0 : 1.0)) * (p.residual ? 3.0 : 1.0);
         const int64_t tiles = p.rows_on_k ? tiles_i * cdiv(p.nj, bn) * p.groups
                                           : tiles_i * lists * cdiv(cdiv(p.nj, lists), bn);
         TcPlan t{};
@@ -876,7 +939,7 @@ TcPlan plan_tc(const Product& p, int num_sms, int force_bn, int force_split) {
         // a last wave at most half full: its tiles' halves along j, whose MMAs of N = 128 take 0.56 of
         // the time (4096^3 bfloat16: cut in two along k 84.6 us, halves 76.7)
         const int64_t waves = cdiv(tiles, pairs), last = tiles % pairs;
-        t.halved = bn == 256 && force_split == 0 && p.groups == 1 && waves > 1 && last > 0 && 2 * last <= pairs;
+        t.halved = bn == widest && force_split == 0 && p.groups == 1 && waves > 1 && last > 0 && 2 * last <= pairs;
         t.whole = last;  // for now: the tiles of the last wave
         double us = (t.halved ? static_cast<double>(waves) - 0.44 : static_cast<double>(waves)) * steps * step + end;
         // K slices that fill one, two or three waves (not groups that share out k: their lengths differ)
@@ -885,7 +948,7 @@ TcPlan plan_tc(const Product& p, int num_sms, int force_bn, int force_split) {
                                                  : std::min<int64_t>(w * pairs / tiles, std::max<int64_t>(kb / 4, 1));
             if (want < 2) continue;
             const int64_t split_kb = cdiv(kb, want), split = cdiv(kb, split_kb);
-            const double blocks_mb = static_cast<double>(tiles) * split * bn * (2 * kBI * 4) * 1e-6;
+            const double blocks_mb = static_cast<double>(tiles) * split * bn * accs * (2 * kBI * 4) * 1e-6;
             const double cut_us =
                 static_cast<double>(cdiv(tiles * split, pairs)) * segs * split_kb * step + end + kSplit + kBlockMB * blocks_mb;
             if (split > 1 && (force_split > 0 || cut_us < us)) {
@@ -907,7 +970,7 @@ TcPlan plan_tc(const Product& p, int num_sms, int force_bn, int force_split) {
     t.whole = t.split > 1 ? 0 : (t.halved ? t.tiles - last : t.tiles);
     t.gather = t.bn <= 64 && !p.rows_on_k;
     if (t.split > 1) {
-        t.part_bytes = region(static_cast<size_t>(t.tiles) * t.split * 2 * kBI * t.bn * 4);
+        t.part_bytes = region(static_cast<size_t>(t.tiles) * t.split * 2 * kBI * t.bn * accs * 4);
         t.info_bytes = region(static_cast<size_t>(t.tiles + 1) * sizeof(int4));
     }
     return t;
@@ -986,20 +1049,28 @@ int launch_product_tc(const CallContext& c, const Product& p, const TcPlan& t, i
     }
     const int64_t units = t.whole + (t.tiles - t.whole) * (t.halved ? 2 : t.split);
     cudaError_t e;
-    auto with_bn = [&](auto f32) {
-        constexpr bool F = decltype(f32)::value;
+    auto with_bn = [&](auto f32, auto gated) {
+        constexpr bool F = decltype(f32)::value, G = decltype(gated)::value;
         switch (t.bn) {
-            case 32: return launch<32, F>(m, q, units, c.sms, st);
-            case 64: return launch<64, F>(m, q, units, c.sms, st);
-            case 128: return launch<128, F>(m, q, units, c.sms, st);
-            default: return launch<256, F>(m, q, units, c.sms, st);
+            case 32: return launch<32, F, G>(m, q, units, c.sms, st);
+            case 64: return launch<64, F, G>(m, q, units, c.sms, st);
+            case 128: return launch<128, F, G>(m, q, units, c.sms, st);
+            default: break;
         }
+        if constexpr (G)
+            return cudaErrorInvalidValue;
+        else
+            return launch<256, F, G>(m, q, units, c.sms, st);
     };
-    e = parts == 3 ? with_bn(std::true_type()) : with_bn(std::false_type());
+    if (p.gated)
+        e = parts == 3 ? with_bn(std::true_type(), std::true_type()) : with_bn(std::false_type(), std::true_type());
+    else
+        e = parts == 3 ? with_bn(std::true_type(), std::false_type()) : with_bn(std::false_type(), std::false_type());
     if (e != cudaSuccess) return call_fail_cuda(e, "tensor-core layer product");
     *launches += 1;
     if (t.split > 1) {
-        auto sum = parts == 3 ? sum_slices_kernel<true> : sum_slices_kernel<false>;
+        auto sum = p.gated ? (parts == 3 ? sum_slices_kernel<true, true> : sum_slices_kernel<false, true>)
+                           : (parts == 3 ? sum_slices_kernel<true, false> : sum_slices_kernel<false, false>);
         e = launch_kernel(true, sum, dim3(static_cast<unsigned>(t.tiles * (t.bn / kSumCols))), dim3(2 * kBI), 0, st, q,
                           t.bn, static_cast<int>(t.tiles));
         if (e != cudaSuccess) return call_fail_cuda(e, "sum of K slices");

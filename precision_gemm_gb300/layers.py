@@ -7,6 +7,8 @@ and call the library; all arithmetic runs in its kernels.
 
     y             = linear(x, w, bias, act, residual)           act(x w^T + bias) + residual
     dx, dw, dbias = linear_backward(dy, x, w, act, preact)
+    y             = gated_linear(x, w, bias, act)                act(g) v with [g v] = x w^T + bias
+    dx, dw, dbias = gated_linear_backward(dy, x, w, preact, act)
     y             = layer_norm(x, w, bias, eps)
     dx, dw, dbias = layer_norm_backward(dy, x, w, mean, rstd, residual)
     weights, ids  = route(logits, top, score, ...)
@@ -230,6 +232,83 @@ def linear_backward(dy, x, w, act="none", preact=None, bias=True, need_dx=True, 
     db = _empty((n,), dtype=dtype, device=device) if bias else None
     rc = lib.sgemm_linear_backward(code, t, n, k, dy2.data_ptr(), lddy, x2.data_ptr(), ldx, w.data_ptr(), ldw, kind,
                                    _ptr(preact), ldz, _ptr(dx), k or 1, _ptr(dw), k or 1, _ptr(db), _raw_stream(index))
+    if rc:
+        _check(rc, lib)
+    if dx is not None and x.dim() != 2:
+        dx = dx.view(x.shape)
+    return dx, dw, db
+
+
+def _halves(w):
+    """n and k of a gated layer's weights (2n, k)."""
+    rows, k = _shape(w, "w", 2)
+    if rows % 2:
+        raise ValueError("w: %d rows are not the gate's and as many more" % rows)
+    return rows // 2, k
+
+
+def gated_linear(x, w, bias=None, act="silu", out=None, preact=None, stream=None):
+    """y = act(g) v with [g v] = x w^T + bias for x (..., k), w (2n, k) -- the gate's n rows,
+    then those of what it gates -- and bias (2n); returns y (..., n).  preact=True also
+    returns [g v] (..., 2n), which gated_linear_backward reads; a tensor given as out or
+    preact is written instead."""
+    if stream is not None:
+        return _on(stream, gated_linear, x, w, bias, act, out, preact)
+    lib = load_library()
+    index, code = _begin(x, "x")
+    x2 = x if x.dim() == 2 else _rows2d(x, "x")
+    dtype = x.dtype
+    n, k = _halves(w)
+    t = x2.shape[0]
+    ldx = _matrix(x2, "x", t, k, dtype, index)
+    ldw = _matrix(w, "w", 2 * n, k, dtype, index)
+    if bias is not None:
+        _packed(bias, "bias", (2 * n,), dtype, index)
+    if out is None:
+        y, ldy = _empty((t, n), dtype=dtype, device=x.device), n or 1
+    else:
+        y = _rows2d(out, "out")
+        ldy = _matrix(y, "out", t, n, dtype, index)
+    z, ldz = None, 0
+    if preact is True:
+        z, ldz = _empty((t, 2 * n), dtype=dtype, device=x.device), 2 * n or 1
+    elif preact is not None and preact is not False:
+        z = _rows2d(preact, "preact")
+        ldz = _matrix(z, "preact", t, 2 * n, dtype, index)
+    rc = lib.sgemm_gated_linear(code, t, n, k, x2.data_ptr(), ldx, w.data_ptr(), ldw, _ptr(bias), _act(act),
+                                y.data_ptr(), ldy, _ptr(z), ldz, _raw_stream(index))
+    if rc:
+        _check(rc, lib)
+    if out is not None:
+        y = out
+    elif x2 is not x:
+        y = y.view(*x.shape[:-1], n)
+    if preact is True:
+        return y, z if x2 is x else z.view(*x.shape[:-1], 2 * n)
+    return y
+
+
+def gated_linear_backward(dy, x, w, preact, act="silu", bias=True, need_dx=True, need_dw=True, stream=None):
+    """(dx, dw, dbias) of gated_linear for dy (..., n), with preact (..., 2n) as gated_linear
+    returned it; dbias is None unless `bias`, dx and dw unless needed."""
+    if stream is not None:
+        return _on(stream, gated_linear_backward, dy, x, w, preact, act, bias, need_dx, need_dw)
+    lib = load_library()
+    index, code = _begin(x, "x")
+    x2, dy2, preact = _rows2d(x, "x"), _rows2d(dy, "dy"), _rows2d(preact, "preact")
+    dtype, device = x.dtype, x.device
+    n, k = _halves(w)
+    t = x2.shape[0]
+    lddy = _matrix(dy2, "dy", t, n, dtype, index)
+    ldx = _matrix(x2, "x", t, k, dtype, index)
+    ldw = _matrix(w, "w", 2 * n, k, dtype, index)
+    ldz = _matrix(preact, "preact", t, 2 * n, dtype, index)
+    dx = _empty((t, k), dtype=dtype, device=device) if need_dx else None
+    dw = _empty((2 * n, k), dtype=dtype, device=device) if need_dw else None
+    db = _empty((2 * n,), dtype=dtype, device=device) if bias else None
+    rc = lib.sgemm_gated_linear_backward(code, t, n, k, dy2.data_ptr(), lddy, x2.data_ptr(), ldx, w.data_ptr(), ldw,
+                                         _act(act), preact.data_ptr(), ldz, _ptr(dx), k or 1, _ptr(dw), k or 1,
+                                         _ptr(db), _raw_stream(index))
     if rc:
         _check(rc, lib)
     if dx is not None and x.dim() != 2:

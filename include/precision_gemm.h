@@ -388,6 +388,9 @@ int sgemm_debug_flags(int flags);
 #define SGEMM_SCORE_SOFTMAX 0
 #define SGEMM_SCORE_SIGMOID 1
 
+/* Values along k that share a scale in 8-bit matrices. */
+#define SGEMM_BLOCK 128
+
 /* Limits of the routing and expert calls. */
 #define SGEMM_MAX_EXPERTS 512
 #define SGEMM_MAX_TOP 32
@@ -465,6 +468,45 @@ int sgemm_gated_linear_backward(int dtype, int64_t t, int64_t n, int64_t k, cons
                                 const void *x, int64_t ldx, const void *w, int64_t ldw, int act,
                                 const void *preact, int64_t ldz, void *dx, int64_t lddx, void *dw,
                                 int64_t lddw, void *dbias, void *stream);
+
+/*
+ * sgemm_quantize -- the e4m3 values (8-bit floating point: 4 exponent bits, 3 of mantissa,
+ * largest 448) and float32 scales that stand for x: of each block of block_rows x
+ * SGEMM_BLOCK elements (cut off at x's edges)
+ *
+ *     scale = max(largest |x| / 448, 2^-126),   q = x / scale as a float32 number, rounded
+ *                                                   to the nearest e4m3, ties to even.
+ *
+ *   dtype of x (1); t, k >= 0 (2, 3); block_rows: 1 for the activations of
+ *   sgemm_block_linear, SGEMM_BLOCK for its weights (4); x, t x k, ldx (5, 6); q, t x k
+ *   bytes, ldq (7, 8); scales, ceil(t / block_rows) x ceil(k / SGEMM_BLOCK), lds (9, 10).
+ *
+ * A block that holds a NaN has the scale NaN, one that holds an infinity the scale infinity
+ * and NaN in the infinity's place.
+ */
+int sgemm_quantize(int dtype, int64_t t, int64_t k, int block_rows, const void *x, int64_t ldx,
+                   uint8_t *q, int64_t ldq, float *scales, int64_t lds, void *stream);
+
+/*
+ * sgemm_block_linear -- y = act(x w^T + bias) + residual with w (n x k) in e4m3, a scale for
+ * each SGEMM_BLOCK x SGEMM_BLOCK of it, and x (t x k) in e4m3, a scale for each 1 x
+ * SGEMM_BLOCK of it; or x of the call's dtype, which the call rounds so (sgemm_quantize with
+ * block_rows 1).
+ *
+ *   dtype of bias, residual, y, and of x where x_scales is NULL (1); t, n, k >= 0 (2-4);
+ *   x, ldx (5, 6); x_scales, t x ceil(k / SGEMM_BLOCK), or NULL, ldxs (7, 8); w, ldw
+ *   (9, 10); w_scales, ceil(n / SGEMM_BLOCK) x ceil(k / SGEMM_BLOCK), ldws (11, 12);
+ *   bias, n elements, or NULL (13); act (14); residual, t x n, or NULL, ldr (15, 16): may
+ *   be y itself; y, ldy (17, 18).
+ *
+ * A block's products are summed by the tensor cores, the blocks' sums scaled and added in
+ * FP32 in the order of k.  e4m3 rows that start at 16-byte boundaries (address and ld) are
+ * read in place, others copied first.  k == 0 leaves the product zero.
+ */
+int sgemm_block_linear(int dtype, int64_t t, int64_t n, int64_t k, const void *x, int64_t ldx,
+                       const float *x_scales, int64_t ldxs, const uint8_t *w, int64_t ldw,
+                       const float *w_scales, int64_t ldws, const void *bias, int act,
+                       const void *residual, int64_t ldr, void *y, int64_t ldy, void *stream);
 
 /*
  * sgemm_layer_norm -- of each row of x: mean = sum x / n, rstd = (sum (x - mean)^2 / n +

@@ -53,13 +53,13 @@ EXPORTS = ("sgemm", "sgemm_host", "sgemm_host_async", "sgemm_set_host_split", "s
            "sgemm_set_wait_timeout", "sgemm_force_plan", "sgemm_debug_flags", "sgemm_launch_count",
            "sgemm_workspace_release", "sgemm_last_error_string", "sgemm_version",
            "sgemm_linear", "sgemm_linear_backward", "sgemm_gated_linear", "sgemm_gated_linear_backward",
-           "sgemm_layer_norm", "sgemm_layer_norm_backward", "sgemm_route", "sgemm_route_backward", "sgemm_expert_plan",
+           "sgemm_quantize", "sgemm_block_linear", "sgemm_layer_norm", "sgemm_layer_norm_backward", "sgemm_route", "sgemm_route_backward", "sgemm_expert_plan",
            "sgemm_expert_linear", "sgemm_expert_linear_backward", "sgemm_expert_combine",
            "sgemm_expert_combine_backward")
 
 # Layers of language models (layers.py), loaded with torch on first use.
-_LAYERS = ("linear", "linear_backward", "gated_linear", "gated_linear_backward", "layer_norm",
-           "layer_norm_backward", "route", "route_backward", "ExpertPlan", "expert_plan", "expert_linear",
+_LAYERS = ("linear", "linear_backward", "gated_linear", "gated_linear_backward", "quantize",
+           "block_linear", "layer_norm", "layer_norm_backward", "route", "route_backward", "ExpertPlan", "expert_plan", "expert_linear",
            "expert_linear_backward", "expert_combine", "expert_combine_backward")
 
 
@@ -145,6 +145,8 @@ def load_library(path: str | None = None):
                 ("sgemm_linear_backward", [i, *sizes, *mat, *mat, *mat, i, *mat, *mat, *mat, vp, vp]),
                 ("sgemm_gated_linear", [i, *sizes, *mat, *mat, vp, i, *mat, *mat, vp]),
                 ("sgemm_gated_linear_backward", [i, *sizes, *mat, *mat, *mat, i, *mat, *mat, *mat, vp, vp]),
+                ("sgemm_quantize", [i, i64, i64, i, *mat, *mat, *mat, vp]),
+                ("sgemm_block_linear", [i, *sizes, *mat, *mat, *mat, *mat, vp, i, *mat, *mat, vp]),
                 ("sgemm_layer_norm", [i, i64, i64, *mat, vp, vp, f, *mat, vp, vp, vp]),
                 ("sgemm_layer_norm_backward", [i, i64, i64, *mat, *mat, vp, vp, vp, *mat, *mat, vp, vp, vp]),
                 ("sgemm_route", [i, i64, i, i, *mat, i, vp, i, i, i, f, vp, vp, vp, vp]),

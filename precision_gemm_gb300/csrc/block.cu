@@ -1,0 +1,605 @@
+// Products of 8-bit matrices: e4m3 values with a float32 scale for each block of 128.
+//
+//     q = e4m3(x / s),  s = max(largest |x| of the block / 448, 2^-126);
+//     y[j][i] = act(sum over blocks kb of 128 k of
+//                   sx[j][kb] sw[i / 128][kb] sum over k in kb of xq[j][k] wq[i][k] + bias[i]) + residual[j][i]
+//
+// The tensor cores sum a block's 128 products (kind::f8f6f4, FP32 accumulators in TMEM); the
+// scales are any FP32 numbers, so each block's sums leave TMEM and are added in registers,
+// scaled, while the next block's are formed in another buffer.
+//
+// A cluster of two CTAs computes a tile of 256 rows j x BN features i (cta_group::2).  Rows of x lie
+// along TMEM lanes: a thread has one row, hence one sx per block, and its warp's columns are of one
+// 128 x 128 block of w, hence one sw: a block's promotion is one FMA per element, and results
+// leave in 16-byte stores.  Warps 0 and 1 load and issue as in product_tc.cu; warps 2 to 9
+// promote and finish, each its quarter of the lanes and half of the columns.
+//
+// For few rows the tiles' k is cut into slices, whose scaled sums are added in slice order by
+// block_sum_kernel.
+#include <cuda_fp8.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "layers.h"
+#include "pair.cuh"
+#include "ptx.cuh"
+
+namespace pg {
+namespace {
+
+constexpr int kBlock = 128;  // values that share a scale, and bytes of a shared-memory row
+constexpr float kLargest = 448.0f;
+constexpr int kRows = 128;   // rows of x per CTA
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kCols = 16;    // columns of a TMEM load
+constexpr int kGroupTiles = 8;
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// ---- quantization ----------------------------------------------------------------
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+// NaN where the block holds one, infinity where it holds one: its values are then NaN or 0.
+__device__ __forceinline__ float block_scale(float largest) { return max_nan(largest / kLargest, 1.17549435e-38f); }
+
+__device__ __forceinline__ float largest8(const float (&v)[8]) {
+    float m = 0.0f;
+#pragma unroll
+    for (int t = 0; t < 8; ++t) m = max_nan(m, fabsf(v[t]));
+    return m;
+}
+
+// The quotients are FP32 numbers, rounded to the nearest e4m3, ties to even.
+__device__ __forceinline__ void put8(uint8_t* q, bool vec, int valid, const float (&v)[8], float scale) {
+    uint32_t w[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * h] / scale, v[4 * h + 1] / scale), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * h + 2] / scale, v[4 * h + 3] / scale), __NV_SATFINITE, __NV_E4M3);
+        w[h] = lo | hi << 16;
+    }
+    if (vec && valid >= 8) {
+        *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[1]);
+    } else {
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+            if (t < valid) q[t] = static_cast<uint8_t>(w[t / 4] >> (8 * (t % 4)));
+    }
+}
+
+// Blocks of 1 x 128: sixteen lanes to each.  HBM-bound: reads x, writes a byte per value.
+template <typename T>
+__global__ void __launch_bounds__(256) quantize_rows_kernel(int64_t rows, int64_t cols, const T* x, int64_t ldx, uint8_t* q,
+                                                            int64_t ldq, float* scales, int64_t lds, bool vec_x,
+                                                            bool vec_q) {
+    pdl_trigger();
+    pdl_wait();
+    const int lane = threadIdx.x % 16;
+    const int64_t blocks = (cols + kBlock - 1) / kBlock, count = rows * blocks;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * 16;
+    for (int64_t b0 = static_cast<int64_t>(blockIdx.x) * 16 + threadIdx.x / 32 * 2; b0 < count; b0 += step) {
+        const int64_t b = b0 + threadIdx.x / 16 % 2;  // a warp's halves stay together
+        const int64_t r = b < count ? b / blocks : 0, c = (b - r * blocks) * kBlock + 8 * lane;
+        const int valid = b < count ? static_cast<int>(min(cols - c, int64_t(8))) : 0;
+        float v[8];
+        load8(x + r * ldx + (valid > 0 ? c : 0), vec_x, valid, v);
+        float m = largest8(v);
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float scale = block_scale(m);
+        if (valid > 0) put8(q + r * ldq + c, vec_q, valid, v, scale);
+        if (lane == 0 && b < count) scales[r * lds + (b - r * blocks)] = scale;
+    }
+}
+
+// Blocks of 128 x 128: a thread block to each, its values kept in registers.
+template <typename T>
+__global__ void __launch_bounds__(256) quantize_blocks_kernel(int64_t rows, int64_t cols, const T* x, int64_t ldx,
+                                                              uint8_t* q, int64_t ldq, float* scales, int64_t lds,
+                                                              bool vec_x, bool vec_q) {
+    __shared__ float slots[8];
+    pdl_trigger();
+    pdl_wait();
+    const int64_t across = (cols + kBlock - 1) / kBlock, br = blockIdx.x / across, bc = blockIdx.x - br * across;
+    const int64_t c = bc * kBlock + 8 * (threadIdx.x % 16);
+    const int valid = static_cast<int>(min(cols - c, int64_t(8)));
+    float v[8][8], m = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const int64_t r = br * kBlock + 16 * k + threadIdx.x / 16;
+        load8(x + (r < rows && valid > 0 ? r * ldx + c : 0), vec_x, r < rows ? valid : 0, v[k]);
+        m = max_nan(m, largest8(v[k]));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (threadIdx.x % 32 == 0) slots[threadIdx.x / 32] = m;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 8; ++k) m = max_nan(m, slots[k]);
+    const float scale = block_scale(m);
+    if (threadIdx.x == 0) scales[br * lds + bc] = scale;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const int64_t r = br * kBlock + 16 * k + threadIdx.x / 16;
+        if (r < rows && valid > 0) put8(q + r * ldq + c, vec_q, valid, v[k], scale);
+    }
+}
+
+__global__ void __launch_bounds__(256) copy_bytes_kernel(const uint8_t* src, int64_t ld, int64_t rows, int64_t cols,
+                                                         uint8_t* dst, int64_t ldd) {
+    pdl_trigger();
+    pdl_wait();
+    const int64_t words = (cols + 3) / 4, count = rows * words;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < count;
+         i += static_cast<int64_t>(gridDim.x) * 256) {
+        const int64_t r = i / words, c = 4 * (i - r * words);
+        uint32_t w = 0;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+            if (c + t < cols) w |= static_cast<uint32_t>(src[r * ld + c + t]) << (8 * t);
+        *reinterpret_cast<uint32_t*>(dst + r * ldd + c) = w;
+    }
+}
+
+// ---- product ---------------------------------------------------------------------
+
+template <int BN>
+struct Cfg {
+    static constexpr int A_BYTES = kRows * kBlock;
+    static constexpr int B_BYTES = BN / 2 * kBlock;
+    static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+    static constexpr int STAGES_RAW = 200 * 1024 / STAGE_BYTES;
+    static constexpr int STAGES = STAGES_RAW > 10 ? 10 : STAGES_RAW;
+    static constexpr int BUFFERS = BN == 256 ? 2 : 4;  // of TMEM: blocks of k on their way
+    static constexpr uint32_t TMEM_COLS = BUFFERS * BN;
+    static constexpr int MINE = BN / 2;                // columns of an epilogue warp
+    static constexpr int BAR_BYTES = (2 * STAGES + 2 * BUFFERS + 1) * 8 + 16;
+    static constexpr size_t SMEM = 1024 + static_cast<size_t>(STAGES) * STAGE_BYTES + BAR_BYTES;
+    static_assert(A_BYTES % 1024 == 0 && B_BYTES % 1024 == 0, "slots need 1 KiB alignment");
+};
+
+struct Params {
+    int32_t t, n, kbs;
+    int32_t tiles_t, tiles_n;
+    int32_t split, split_kb;
+    const float* x_scales;
+    int64_t ldxs;
+    const float* w_scales;
+    int64_t ldws;
+    const void* bias;
+    int32_t act;
+    const void* residual;
+    int64_t ldr;
+    void* y;
+    int64_t ldy;
+    int32_t vec;        // y, residual and bias in 16-byte accesses
+    float* part;        // slices' sums, [slice][t][ldp]
+    int64_t ldp;
+    uint64_t timeout_ns;
+    int* status;
+    int32_t debug_flags;
+};
+
+// Eight columns from i on of row j, sums v: the epilogue.
+template <typename T, int ACT>
+__device__ __forceinline__ void finish8(const Params& p, int64_t j, int64_t i, float (&v)[8]) {
+    const int valid = static_cast<int>(min(p.n - i, int64_t(8)));
+    if (valid <= 0) return;
+    if (p.bias) {
+        float b[8];
+        load8(static_cast<const T*>(p.bias) + i, p.vec, valid, b);
+#pragma unroll
+        for (int t = 0; t < 8; ++t) v[t] += b[t];
+    }
+#pragma unroll
+    for (int t = 0; t < 8; ++t) v[t] = act_value<ACT, std::is_same<T, bf16>::value>(v[t]);
+    if (p.residual) {
+        float r[8];
+        load8(static_cast<const T*>(p.residual) + j * p.ldr + i, p.vec, valid, r);
+#pragma unroll
+        for (int t = 0; t < 8; ++t) v[t] += r[t];
+    }
+    store8(static_cast<T*>(p.y) + j * p.ldy + i, p.vec, valid, v);
+}
+
+template <int BN, typename T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    block_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, const Params p) {
+    using C = Cfg<BN>;
+    constexpr int S = C::STAGES, NB = C::BUFFERS;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = align_smem_1024(smem_raw);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S * C::STAGE_BYTES);
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 2 * S + 2 * NB + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+    const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + S);
+    const uint32_t acc_full0 = smem_u32(bars + 2 * S), acc_empty0 = smem_u32(bars + 2 * S + NB);
+    const uint32_t mma_done = smem_u32(bars + 2 * S + 2 * NB);
+
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);  // known to be uniform
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = __shfl_sync(0xffffffffu, cluster_rank(), 0);
+    const bool leader = rank == 0;
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(full0 + 8 * s, 1);
+            mbar_init(empty0 + 8 * s, 1);
+        }
+        for (int b = 0; b < NB; ++b) {
+            mbar_init(acc_full0 + 8 * b, 1);
+            mbar_init(acc_empty0 + 8 * b, 2 * kEpiWarps);
+        }
+        mbar_init(mma_done, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_holder)),
+                     "r"(C::TMEM_COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    pdl_wait();
+    tc_fence_before_sync();
+    __syncthreads();
+    cluster_sync_all();  // every CTA's barriers and TMEM exist before any cross-CTA traffic
+    tc_fence_after_sync();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_holder, 0);
+    const int units = p.tiles_t * p.tiles_n * p.split;
+
+    struct Unit {
+        int j0, i0, slice, kb0, nkb;
+    };
+    auto unit_of = [&](int u) {
+        Unit x;
+        const int tile = u / p.split;  // the slices of a tile are neighbours, so that they run at one time
+        x.slice = u - tile * p.split;
+        int tt, tn;
+        tile_coords(tile, p.tiles_t, p.tiles_n, kGroupTiles, tt, tn);
+        x.j0 = tt * (2 * kRows);
+        x.i0 = tn * BN;
+        x.kb0 = x.slice * p.split_kb;
+        x.nkb = max(min(x.kb0 + p.split_kb, p.kbs) - x.kb0, 0);
+        return x;
+    };
+
+    if (warp == 0) {
+        // ---------------- TMA loader (both CTAs) ----------------
+        if (!(p.debug_flags & 1)) {
+            const uint32_t full_leader0 = map_to_rank(full0, 0);
+            int it = 0, slot_i = 0;
+            uint32_t phase = 1;
+            bool ok = true;
+            for (int u = pair; u < units && ok; u += pairs) {
+                const Unit x = unit_of(u);
+                const int ja = __shfl_sync(0xffffffffu, x.j0 + kRows * static_cast<int>(rank), 0);
+                const int ib = __shfl_sync(0xffffffffu, x.i0 + BN / 2 * static_cast<int>(rank), 0);
+                const int kb0 = __shfl_sync(0xffffffffu, x.kb0, 0), nkb = __shfl_sync(0xffffffffu, x.nkb, 0);
+                for (int kb = 0; kb < nkb; ++kb, ++it) {
+                    ok = __all_sync(0xffffffffu,
+                                    mbar_wait_bounded(empty0 + 8 * slot_i, phase, p.timeout_ns, abort_flag));
+                    if (!ok) {
+                        if (lane == 0) raise_abort(abort_flag, p.status);
+                        break;
+                    }
+                    if (leader && lane == 0) mbar_arrive_expect_tx(full0 + 8 * slot_i, 2 * C::STAGE_BYTES);
+                    const uint32_t bar = full_leader0 + 8 * slot_i;
+                    const uint32_t slot = smem_u32(smem) + slot_i * C::STAGE_BYTES;
+                    tma_load_3d_pair_warp(slot, &tmX, (kb0 + kb) * kBlock, ja, 0, bar);
+                    tma_load_3d_pair_warp(slot + C::A_BYTES, &tmW, (kb0 + kb) * kBlock, ib, 0, bar);
+                    if (++slot_i == S) {
+                        slot_i = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            if (lane == 0) pdl_trigger();
+            if (leader && lane == 0) {
+                // Let every copy of the pair land before the CTAs may retire (CTA 0's full barriers
+                // count both CTAs' bytes).
+                for (int q = max(0, it - S); q < it; ++q)
+                    mbar_wait_bounded(full0 + 8 * (q % S), (q / S) & 1, p.timeout_ns, nullptr);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---------------- MMA issuer (CTA 0 of the pair) ----------------
+        if (leader) {
+            const uint32_t slot0 = smem_u32(smem);
+            const uint64_t a_desc0 = smem_desc(slot0, 16, 1024, kSwizzle128B);
+            const uint64_t b_desc0 = smem_desc(slot0 + C::A_BYTES, 16, 1024, kSwizzle128B);
+            const uint32_t idesc = idesc_e4m3(2 * kRows, BN);
+            int slot_i = 0, buf = 0;
+            uint32_t phase = 0, acc_phase = 1;
+            bool ok = true;
+            for (int u = pair; u < units && ok; u += pairs) {
+                const int nkb = __shfl_sync(0xffffffffu, unit_of(u).nkb, 0);
+                for (int kb = 0; kb < nkb; ++kb) {
+                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(acc_empty0 + 8 * buf, acc_phase, p.timeout_ns, abort_flag)) &&
+                         __all_sync(0xffffffffu, mbar_wait_bounded(full0 + 8 * slot_i, phase, p.timeout_ns, abort_flag));
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                    const uint32_t o = static_cast<uint32_t>(slot_i * C::STAGE_BYTES) >> 4;
+#pragma unroll
+                    for (int kk = 0; kk < kBlock / 32; ++kk)
+                        mma_e4m3_pair_warp(tmem + buf * BN, a_desc0 + (o + 2 * kk), b_desc0 + (o + 2 * kk), idesc, kk > 0);
+                    mma_commit_pair_warp(empty0 + 8 * slot_i);
+                    mma_commit_pair_warp(acc_full0 + 8 * buf);
+                    if (++slot_i == S) {
+                        slot_i = 0;
+                        phase ^= 1;
+                    }
+                    if (++buf == NB) {
+                        buf = 0;
+                        acc_phase ^= 1;
+                    }
+                }
+            }
+            if (!ok && lane == 0) raise_abort(abort_flag, p.status);
+            mma_commit_pair_local_warp(mma_done);  // every MMA issued here has completed
+            mbar_wait_bounded(mma_done, 0, p.timeout_ns, nullptr);
+        }
+        __syncwarp();
+    } else {
+        // ---------------- promotion and epilogue (warps 2..9, both CTAs) ----------------
+        const int q = warp & 3;            // TMEM lane quarter this warp may access
+        const int half = (warp - 2) >> 2;  // its half of the columns
+        const uint32_t acc_empty_leader0 = map_to_rank(acc_empty0, 0);
+        const uint32_t base = tmem + (static_cast<uint32_t>(32 * q) << 16) + C::MINE * half;
+        int buf = 0;
+        uint32_t acc_phase = 0;
+        bool ok = true;
+        for (int u = pair; u < units && ok; u += pairs) {
+            const Unit x = unit_of(u);
+            const int row0 = x.j0 + kRows * static_cast<int>(rank) + 32 * q;
+            const int64_t j = row0 + lane;
+            const int i0 = x.i0 + C::MINE * half;
+            const bool there = row0 < p.t && i0 < p.n;  // of the warp
+            // this row's and these columns' scales, four blocks at a time, four ahead
+            const float* sx = p.x_scales + (j < p.t ? j : 0) * p.ldxs;
+            const float* sw = p.w_scales + (there ? i0 / kBlock : 0) * p.ldws;
+            float next[4];
+            auto scales = [&](int kb) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int at = x.kb0 + kb + r;
+                    next[r] = kb + r < x.nkb ? sx[at] * sw[at] : 0.0f;
+                }
+            };
+            scales(0);
+            if (p.residual && j < p.t && i0 < p.n) {
+                // the residual comes into L2 while the MMAs run
+                const T* r = static_cast<const T*>(p.residual) + j * p.ldr + i0;
+                for (int c = 0; c < C::MINE && i0 + c < p.n; c += 128 / static_cast<int>(sizeof(T))) prefetch_l2(r + c);
+            }
+            float2 acc[C::MINE / 2];
+#pragma unroll
+            for (int c = 0; c < C::MINE / 2; ++c) acc[c] = make_float2(0.0f, 0.0f);
+            for (int g = 0; g < x.nkb && ok; g += 4) {
+                float s[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) s[r] = next[r];
+                scales(g + 4);
+#pragma unroll 1
+                for (int kb = g; kb < min(g + 4, x.nkb); ++kb) {
+                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(acc_full0 + 8 * buf, acc_phase, p.timeout_ns, abort_flag));
+                    if (!ok) {
+                        if (lane == 0) raise_abort(abort_flag, p.status);
+                        break;
+                    }
+                    tc_fence_after_sync();
+                    const float2 scale = both(s[0]);
+#pragma unroll
+                    for (int r = 0; r < 3; ++r) s[r] = s[r + 1];
+                    const uint32_t at = base + buf * BN;
+                    auto free_buffer = [&]() {
+                        tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_remote_relaxed(acc_empty_leader0 + 8 * buf);
+                    };
+                    if (there) {
+                        uint32_t v[2][kCols];
+                        __syncwarp();
+                        tmem_ld_32x32b_x16(at, v[0]);
+#pragma unroll
+                        for (int c = 0; c < C::MINE / kCols; ++c) {
+                            tmem_wait_ld(v[c & 1]);
+                            if (c + 1 < C::MINE / kCols)
+                                tmem_ld_32x32b_x16(at + kCols * (c + 1), v[(c + 1) & 1]);
+                            else
+                                free_buffer();
+#pragma unroll
+                            for (int k = 0; k < kCols / 2; ++k)
+                                acc[kCols / 2 * c + k] =
+                                    fma2(make_float2(__uint_as_float(v[c & 1][2 * k]), __uint_as_float(v[c & 1][2 * k + 1])),
+                                         scale, acc[kCols / 2 * c + k]);
+                        }
+                    } else {
+                        free_buffer();
+                    }
+                    if (++buf == NB) {
+                        buf = 0;
+                        acc_phase ^= 1;
+                    }
+                }
+            }
+            if (!ok || j >= p.t) continue;
+            if (p.part) {
+                float* dst = p.part + (static_cast<int64_t>(x.slice) * p.t + j) * p.ldp + i0;
+#pragma unroll
+                for (int c = 0; c < C::MINE / 2; c += 2)
+                    if (i0 + 2 * c < p.n)  // rows are whole multiples of eight there
+                        *reinterpret_cast<float4*>(dst + 2 * c) = make_float4(acc[c].x, acc[c].y, acc[c + 1].x, acc[c + 1].y);
+            } else {
+                with_act(p.act, [&](auto act) {
+#pragma unroll
+                    for (int c = 0; c < C::MINE / 2; c += 4) {
+                        float f[8];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            f[2 * k] = acc[c + k].x;
+                            f[2 * k + 1] = acc[c + k].y;
+                        }
+                        finish8<T, decltype(act)::value>(p, j, i0 + 2 * c, f);
+                    }
+                });
+            }
+        }
+    }
+
+    tc_fence_before_sync();
+    __syncthreads();
+    cluster_sync_all();  // no CTA leaves while its peer may still read its shared memory or barriers
+    if (warp == 1) {
+        tc_fence_after_sync();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM_COLS)
+                     : "memory");
+    }
+}
+
+// The slices' sums of eight columns, added in slice order, and the epilogue.
+template <typename T>
+__global__ void __launch_bounds__(256) block_sum_kernel(const Params p) {
+    pdl_trigger();
+    pdl_wait();
+    const int64_t eights = p.ldp / 8, item = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    const int64_t j = item / eights, i = 8 * (item - j * eights);
+    if (j >= p.t) return;
+    const float* src = p.part + j * p.ldp + i;
+    float v[8] = {};
+#pragma unroll 4
+    for (int s = 0; s < p.split; ++s, src += p.t * p.ldp) {
+        const float4 a = __ldcg(reinterpret_cast<const float4*>(src)), b = __ldcg(reinterpret_cast<const float4*>(src) + 1);
+        v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
+        v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+    }
+    with_act(p.act, [&](auto act) { finish8<T, decltype(act)::value>(p, j, i, v); });
+}
+
+template <int BN, typename T>
+cudaError_t run(const CUtensorMap& x, const CUtensorMap& w, const Params& p, int num_sms, cudaStream_t st) {
+    using C = Cfg<BN>;
+    auto kern = block_kernel<BN, T>;
+    static std::atomic<uint64_t> smem_set{0};
+    cudaError_t e = set_smem_limit_once(smem_set, reinterpret_cast<const void*>(kern), static_cast<int>(C::SMEM));
+    if (e != cudaSuccess) return e;
+    static std::atomic<int> resident[64];
+    const int most = resident_pairs(reinterpret_cast<const void*>(kern), kThreads, C::SMEM, num_sms, resident);
+    const int64_t units = static_cast<int64_t>(p.tiles_t) * p.tiles_n * p.split;
+    return launch_kernel(true, kern, dim3(static_cast<unsigned>(2 * std::min<int64_t>(units, most))), dim3(kThreads),
+                         C::SMEM, st, x, w, p);
+}
+
+}  // namespace
+
+cudaError_t launch_quantize(int dtype, int64_t rows, int64_t cols, int block_rows, const void* x, int64_t ldx, uint8_t* q,
+                            int64_t ldq, float* scales, int64_t lds, int num_sms, cudaStream_t st) {
+    const bool vec_q = (reinterpret_cast<uintptr_t>(q) & 7) == 0 && ldq % 8 == 0;
+    auto go = [&](auto zero) {
+        using T = decltype(zero);
+        const bool vec_x = rows_aligned<T>(x, ldx);
+        const int64_t across = cdiv(cols, kBlock);
+        if (block_rows == 1)
+            return launch_kernel(true, quantize_rows_kernel<T>,
+                                 dim3(static_cast<unsigned>(std::min<int64_t>(cdiv(rows * across, 16), int64_t(64) * num_sms))),
+                                 dim3(256), 0, st, rows, cols, static_cast<const T*>(x), ldx, q, ldq, scales, lds, vec_x,
+                                 vec_q);
+        return launch_kernel(true, quantize_blocks_kernel<T>, dim3(static_cast<unsigned>(cdiv(rows, kBlock) * across)),
+                             dim3(256), 0, st, rows, cols, static_cast<const T*>(x), ldx, q, ldq, scales, lds, vec_x, vec_q);
+    };
+    return dtype == SGEMM_F32 ? go(float()) : go(bf16());
+}
+
+cudaError_t launch_copy_bytes(const uint8_t* src, int64_t ld, int64_t rows, int64_t cols, uint8_t* dst, int64_t ldd,
+                              int num_sms, cudaStream_t st) {
+    const int64_t blocks = std::min<int64_t>(cdiv(rows * cdiv(cols, 4), 256), int64_t(16) * num_sms);
+    return launch_kernel(true, copy_bytes_kernel, dim3(static_cast<unsigned>(std::max<int64_t>(blocks, 1))), dim3(256), 0, st,
+                         src, ld, rows, cols, dst, ldd);
+}
+
+BlockPlan plan_block(int64_t t, int64_t n, int64_t k, int num_sms, int force_bn, int force_split) {
+    const int pairs = std::max(num_sms / 2, 1);
+    const int64_t kb = cdiv(k, kBlock);
+    BlockPlan best{};
+    double best_us = 0.0;
+    for (int bn : {256, 128, 64}) {
+        if (force_bn && force_bn <= 256 && bn != force_bn) continue;
+        const double step = bn == 256 ? 0.36 : (bn == 128 ? 0.20 : 0.15), end = bn == 256 ? 4.0 : (bn == 128 ? 2.5 : 1.5);
+        const int64_t tiles = cdiv(t, 2 * kRows) * cdiv(n, bn);
+        for (int64_t want = 1; want <= std::max<int64_t>(kb, 1); ++want) {
+            if (force_split ? want != std::min<int64_t>(force_split, std::max<int64_t>(kb, 1)) : want > 1 && tiles * want > 3 * pairs) continue;
+            const int64_t split_kb = std::max<int64_t>(cdiv(kb, want), 1), split = std::max<int64_t>(cdiv(kb, split_kb), 1);
+            const double us = static_cast<double>(cdiv(tiles * split, pairs)) * (split_kb * step + end) +
+                              (split > 1 ? 2.5 + 1e-6 * split * t * n * 4 * 0.3 : 0.0);
+            if (best.bn == 0 || us < best_us) {
+                best_us = us;
+                best = BlockPlan{bn, static_cast<int>(split), static_cast<int>(split_kb), 0};
+            }
+        }
+    }
+    if (best.split > 1) best.part_bytes = static_cast<size_t>(best.split) * t * cdiv(n, 8) * 8 * 4;
+    return best;
+}
+
+int launch_block(const CallContext& c, const BlockProduct& b, const BlockPlan& plan, float* part, cudaStream_t st,
+                 int* launches) {
+    Params p{};
+    p.t = static_cast<int32_t>(b.t);
+    p.n = static_cast<int32_t>(b.n);
+    p.kbs = static_cast<int32_t>(cdiv(b.k, kBlock));
+    p.tiles_t = static_cast<int32_t>(cdiv(b.t, 2 * kRows));
+    p.tiles_n = static_cast<int32_t>(cdiv(b.n, plan.bn));
+    p.split = plan.split;
+    p.split_kb = plan.split_kb;
+    p.x_scales = b.x_scales;
+    p.ldxs = b.ldxs;
+    p.w_scales = b.w_scales;
+    p.ldws = b.ldws;
+    p.bias = b.bias;
+    p.act = b.act;
+    p.residual = b.residual;
+    p.ldr = b.ldr;
+    p.y = b.y;
+    p.ldy = b.ldy;
+    auto aligned = [&](const void* q, int64_t ld) {
+        return b.dtype == SGEMM_F32 ? rows_aligned<float>(q, ld) : rows_aligned<bf16>(q, ld);
+    };
+    p.vec = aligned(b.y, b.ldy) && aligned(b.residual, b.ldr) && aligned(b.bias, 0);
+    p.part = plan.split > 1 ? part : nullptr;
+    p.ldp = cdiv(b.n, 8) * 8;
+    p.timeout_ns = c.timeout_ns;
+    p.status = c.status;
+    p.debug_flags = c.debug_flags;
+    CUtensorMap x{}, w{};
+    if (b.k > 0) {
+        int rc;
+        if ((rc = call_encode_u8(&x, b.x, b.k, b.t, b.ldx, kRows))) return rc;
+        if ((rc = call_encode_u8(&w, b.w, b.k, b.n, b.ldw, static_cast<uint32_t>(plan.bn / 2)))) return rc;
+    }
+    auto go = [&](auto zero) {
+        using T = decltype(zero);
+        cudaError_t e;
+        switch (plan.bn) {
+            case 64: e = run<64, T>(x, w, p, c.sms, st); break;
+            case 128: e = run<128, T>(x, w, p, c.sms, st); break;
+            default: e = run<256, T>(x, w, p, c.sms, st); break;
+        }
+        if (e != cudaSuccess || p.part == nullptr) return e;
+        return launch_kernel(true, block_sum_kernel<T>, dim3(static_cast<unsigned>(cdiv(b.t * (p.ldp / 8), 256))), dim3(256),
+                             0, st, p);
+    };
+    const cudaError_t e = b.dtype == SGEMM_F32 ? go(float()) : go(bf16());
+    if (e != cudaSuccess) return call_fail_cuda(e, "block product");
+    *launches += plan.split > 1 ? 2 : 1;
+    return 0;
+}
+
+}  // namespace pg

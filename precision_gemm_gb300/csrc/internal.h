@@ -75,6 +75,32 @@ inline cudaError_t set_smem_limit_once(std::atomic<uint64_t>& done, const void* 
     return e;
 }
 
+// Clusters of two CTAs of a kernel that are resident together (they must fit inside GPCs), asked
+// once per device (`known`: a static of the launcher); a persistent grid beyond them would run a
+// second time around.
+inline int resident_pairs(const void* kern, int threads, size_t smem, int num_sms, std::atomic<int> (&known)[64]) {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    int most = dev >= 0 && dev < 64 ? known[dev].load() : 0;
+    if (most > 0) return most;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3(2, 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    if (cudaOccupancyMaxActiveClusters(&most, kern, &cfg) != cudaSuccess || most <= 0) {
+        cudaGetLastError();
+        most = num_sms / 2;
+    }
+    if (dev >= 0 && dev < 64) known[dev] = most;
+    return most;
+}
+
 // Tile geometry common to every GEMM kernel: BM rows of C per CTA.
 constexpr int kBM = 128;
 // FFMA kernel: K block staged per ring slot.
@@ -142,6 +168,8 @@ void call_count(int launches);
 // elements outside read as zero.
 int call_encode_bf16(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, int64_t ld, int64_t z,
                      int64_t stride, uint32_t box_cols, uint32_t box_rows);
+// The same of bytes, one matrix as a 3-D map, boxes of box_rows rows of 128.
+int call_encode_u8(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, int64_t ld, uint32_t box_rows);
 
 // Device status values written by kernels (match SGEMM_ERR_* of the ABI).
 constexpr int kStatusTimeout = 4;

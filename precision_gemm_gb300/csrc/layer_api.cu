@@ -39,6 +39,7 @@ int check_matrix(const void* p, bool used, int64_t cols, int64_t ld, int pos, co
 int check_pointer(const void* p, bool used, int pos, const char* name) {
     return used && p == nullptr ? call_fail(-pos, "argument %d (%s): null pointer", pos, name) : 0;
 }
+int64_t blocks_of(int64_t k) { return (k + SGEMM_BLOCK - 1) / SGEMM_BLOCK; }
 int check_act(int act, int pos) {
     return act >= SGEMM_ACT_NONE && act <= SGEMM_ACT_GELU_TANH
                ? 0
@@ -463,6 +464,94 @@ PG_EXPORT int sgemm_gated_linear_backward(int dtype, int64_t t, int64_t n, int64
     b.dbias = dbias;
     b.gated = true;
     return backward(b, static_cast<cudaStream_t>(stream));
+}
+
+PG_EXPORT int sgemm_quantize(int dtype, int64_t t, int64_t k, int block_rows, const void* x, int64_t ldx, uint8_t* q,
+                             int64_t ldq, float* scales, int64_t lds, void* stream) {
+    PG_CHECK(check_dtype(dtype, 1));
+    PG_CHECK(check_extent(t, 2, "t"));
+    PG_CHECK(check_extent(k, 3, "k"));
+    if (block_rows != 1 && block_rows != SGEMM_BLOCK)
+        return call_fail(-4, "argument 4 (block_rows): %d is not 1 or %d", block_rows, SGEMM_BLOCK);
+    const bool some = t > 0 && k > 0;
+    PG_CHECK(check_matrix(x, some, k, ldx, 5, "x"));
+    PG_CHECK(check_matrix(q, some, k, ldq, 7, "q"));
+    PG_CHECK(check_matrix(scales, some, blocks_of(k), lds, 9, "scales"));
+    if (!some) return 0;
+    CallContext c;
+    PG_CHECK(call_begin(&c));
+    const cudaError_t e = launch_quantize(dtype, t, k, block_rows, x, ldx, q, ldq, scales, lds, c.sms,
+                                          static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return call_fail_cuda(e, "quantization");
+    call_count(1);
+    return 0;
+}
+
+// e4m3 rows where TMA can read them: in place, or copied.
+static int place_bytes(const CallContext& c, const uint8_t*& p, int64_t& ld, int64_t rows, int64_t k, Arena& a,
+                       cudaStream_t st) {
+    if (rows == 1) ld = (k + 15) / 16 * 16;
+    if ((reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 16 == 0) return 0;
+    const int64_t ldd = (k + 15) / 16 * 16;
+    uint8_t* dst = static_cast<uint8_t*>(a.take(static_cast<size_t>(rows) * ldd));
+    if (!a.dry()) {
+        const cudaError_t e = launch_copy_bytes(p, ld, rows, k, dst, ldd, c.sms, st);
+        if (e != cudaSuccess) return call_fail_cuda(e, "copy of 8-bit rows");
+        call_count(1);
+    }
+    p = dst;
+    ld = ldd;
+    return 0;
+}
+
+PG_EXPORT int sgemm_block_linear(int dtype, int64_t t, int64_t n, int64_t k, const void* x, int64_t ldx,
+                                 const float* x_scales, int64_t ldxs, const uint8_t* w, int64_t ldw,
+                                 const float* w_scales, int64_t ldws, const void* bias, int act, const void* residual,
+                                 int64_t ldr, void* y, int64_t ldy, void* stream) {
+    PG_CHECK(check_dtype(dtype, 1));
+    PG_CHECK(check_extent(t, 2, "t"));
+    PG_CHECK(check_extent(n, 3, "n"));
+    PG_CHECK(check_extent(k, 4, "k"));
+    const bool some = t > 0 && n > 0;
+    PG_CHECK(check_matrix(x, some && k > 0, k, ldx, 5, "x"));
+    PG_CHECK(check_matrix(x_scales, false, blocks_of(k), ldxs, 7, "x_scales"));
+    PG_CHECK(check_matrix(w, some && k > 0, k, ldw, 9, "w"));
+    PG_CHECK(check_matrix(w_scales, some && k > 0, blocks_of(k), ldws, 11, "w_scales"));
+    PG_CHECK(check_act(act, 14));
+    PG_CHECK(check_matrix(residual, false, n, ldr, 15, "residual"));
+    PG_CHECK(check_matrix(y, some, n, ldy, 17, "y"));
+    if (!some) return 0;
+    CallContext c;
+    PG_CHECK(call_begin(&c));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const BlockPlan plan = plan_block(t, n, k, c.sms, c.force_bn, c.force_split);
+    return with_workspace(c, st, [&](Arena& a) {
+        BlockProduct p{dtype, t, n, k, static_cast<const uint8_t*>(x), ldx, x_scales, ldxs, w, ldw, w_scales, ldws, bias,
+                       act, residual, ldr, y, ldy};
+        int launches = 0;
+        if (k > 0 && x_scales == nullptr) {
+            const int64_t ldq = (k + 15) / 16 * 16, lds = blocks_of(k);
+            uint8_t* q = static_cast<uint8_t*>(a.take(static_cast<size_t>(t) * ldq));
+            float* scales = static_cast<float*>(a.take(static_cast<size_t>(t) * lds * 4));
+            if (!a.dry()) {
+                const cudaError_t e = launch_quantize(dtype, t, k, 1, x, ldx, q, ldq, scales, lds, c.sms, st);
+                if (e != cudaSuccess) return call_fail_cuda(e, "quantization");
+                ++launches;
+            }
+            p.x = q;
+            p.ldx = ldq;
+            p.x_scales = scales;
+            p.ldxs = lds;
+        } else if (k > 0) {
+            PG_CHECK(place_bytes(c, p.x, p.ldx, t, k, a, st));
+        }
+        if (k > 0) PG_CHECK(place_bytes(c, p.w, p.ldw, n, k, a, st));
+        float* part = static_cast<float*>(a.take(plan.part_bytes));
+        if (a.dry()) return 0;
+        PG_CHECK(launch_block(c, p, plan, part, st, &launches));
+        call_count(launches);
+        return 0;
+    });
 }
 
 PG_EXPORT int sgemm_layer_norm(int dtype, int64_t t, int64_t n, const void* x, int64_t ldx, const void* w,

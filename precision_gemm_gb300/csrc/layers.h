@@ -405,6 +405,40 @@ cudaError_t launch_combine_backward(int dtype, int64_t tokens, int top, int64_t 
                                     const void* x, int64_t ldx, const int32_t* rows, const int32_t* slots,
                                     const float* weights, void* dx, int64_t lddx, float* dweights, cudaStream_t st);
 
+// e4m3 values with a scale for each 1 x 128 (block_rows 1) or 128 x 128 of the matrix (block.cu).
+cudaError_t launch_quantize(int dtype, int64_t rows, int64_t cols, int block_rows, const void* x, int64_t ldx, uint8_t* q,
+                            int64_t ldq, float* scales, int64_t lds, int num_sms, cudaStream_t st);
+// Rows of bytes copied to 16-byte boundaries.
+cudaError_t launch_copy_bytes(const uint8_t* src, int64_t ld, int64_t rows, int64_t cols, uint8_t* dst, int64_t ldd,
+                              int num_sms, cudaStream_t st);
+// y = act(x w^T + bias) + residual of such matrices: x with scales of 1 x 128, w of 128 x 128, rows
+// at 16-byte boundaries.
+struct BlockProduct {
+    int dtype;  // of bias, residual and y
+    int64_t t, n, k;
+    const uint8_t* x;
+    int64_t ldx;
+    const float* x_scales;
+    int64_t ldxs;
+    const uint8_t* w;
+    int64_t ldw;
+    const float* w_scales;
+    int64_t ldws;
+    const void* bias;
+    int act;
+    const void* residual;
+    int64_t ldr;
+    void* y;
+    int64_t ldy;
+};
+struct BlockPlan {
+    int bn, split, split_kb;
+    size_t part_bytes;
+};
+BlockPlan plan_block(int64_t t, int64_t n, int64_t k, int num_sms, int force_bn, int force_split);
+int launch_block(const CallContext& c, const BlockProduct& p, const BlockPlan& plan, float* part, cudaStream_t st,
+                 int* launches);
+
 // Layer norm (norm.cu).  part: norm_part_bytes(), read where dw or db is asked for.
 cudaError_t launch_norm(int dtype, int64_t rows, int64_t n, const void* x, int64_t ldx, const void* w, const void* b,
                         float eps, void* y, int64_t ldy, float* mean, float* rstd, int num_sms, cudaStream_t st);

@@ -840,29 +840,8 @@ cudaError_t launch(const CUtensorMap (&m)[6], const Params& p, int64_t units, in
     static std::atomic<uint64_t> smem_set{0};
     cudaError_t e = set_smem_limit_once(smem_set, reinterpret_cast<const void*>(kern), static_cast<int>(C::SMEM));
     if (e != cudaSuccess) return e;
-    // Clusters that are resident together (they must fit inside GPCs), asked once per device; a
-    // persistent grid beyond them would run a second time around.
     static std::atomic<int> resident[64];
-    int dev = 0;
-    cudaGetDevice(&dev);
-    int most = dev >= 0 && dev < 64 ? resident[dev].load() : 0;
-    if (most <= 0) {
-        cudaLaunchConfig_t cfg = {};
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = 2;
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        cfg.gridDim = dim3(2, 1, 1);
-        cfg.blockDim = dim3(kThreads, 1, 1);
-        cfg.dynamicSmemBytes = C::SMEM;
-        if (cudaOccupancyMaxActiveClusters(&most, kern, &cfg) != cudaSuccess || most <= 0) {
-            cudaGetLastError();
-            most = num_sms / 2;
-        }
-        if (dev >= 0 && dev < 64) resident[dev] = most;
-    }
+    const int most = resident_pairs(reinterpret_cast<const void*>(kern), kThreads, C::SMEM, num_sms, resident);
     const int64_t clusters = std::max<int64_t>(1, std::min<int64_t>(units, most));
     return launch_kernel(true, kern, dim3(static_cast<unsigned>(2 * clusters)), dim3(kThreads), C::SMEM,
                          st, m[0], m[1], m[2], m[3], m[4], m[5], p);

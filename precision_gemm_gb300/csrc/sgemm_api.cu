@@ -1335,8 +1335,9 @@ int call_fail_cuda(cudaError_t e, const char* what) { return fail_cuda(e, what);
 
 void call_count(int launches) { g_launches += launches; }
 
-int call_encode_bf16(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, int64_t ld, int64_t z,
-                     int64_t stride, uint32_t box_cols, uint32_t box_rows) {
+// bytes: 2 (bfloat16) or 1
+static int encode_swizzled(CUtensorMap* map, int bytes, const void* base, int64_t cols, int64_t rows, int64_t ld,
+                           int64_t z, int64_t stride, uint32_t box_cols, uint32_t box_rows) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return fail(SGEMM_ERR_TENSOR_MAP, "cuTensorMapEncodeTiled is unavailable from the driver");
     if (g_debug.load() & SGEMM_DEBUG_FAIL_TENSOR_MAP)
@@ -1344,19 +1345,26 @@ int call_encode_bf16(CUtensorMap* map, const void* base, int64_t cols, int64_t r
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
                                 static_cast<cuuint64_t>(z)};
     // a single matrix needs no stride between matrices, but the map wants one
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2,
-                                   static_cast<cuuint64_t>(z > 1 ? stride : ld * rows) * 2};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * bytes,
+                                   static_cast<cuuint64_t>(z > 1 ? stride : ld * rows) * bytes};
     const cuuint32_t box[3] = {box_cols, box_rows, 1};
     const cuuint32_t elem[3] = {1, 1, 1};
-    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, z > 0 ? 3 : 2, const_cast<void*>(base), dims, strides,
+    const CUresult r = fn(map, bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, z > 0 ? 3 : 2, const_cast<void*>(base), dims, strides,
                           box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS)
         return fail(SGEMM_ERR_TENSOR_MAP,
-                    "cuTensorMapEncodeTiled (bfloat16) failed (%d) for %lld matrices of %lld x %lld, ld %lld, stride %lld",
-                    static_cast<int>(r), (long long)z, (long long)rows, (long long)cols, (long long)ld,
+                    "cuTensorMapEncodeTiled (%d-byte elements) failed (%d) for %lld matrices of %lld x %lld, ld %lld, stride %lld",
+                    bytes, static_cast<int>(r), (long long)z, (long long)rows, (long long)cols, (long long)ld,
                     (long long)stride);
     return 0;
+}
+int call_encode_bf16(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, int64_t ld, int64_t z,
+                     int64_t stride, uint32_t box_cols, uint32_t box_rows) {
+    return encode_swizzled(map, 2, base, cols, rows, ld, z, stride, box_cols, box_rows);
+}
+int call_encode_u8(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, int64_t ld, uint32_t box_rows) {
+    return encode_swizzled(map, 1, base, cols, rows, ld, 1, 0, 128, box_rows);
 }
 
 }  // namespace pg

@@ -9,6 +9,8 @@ and call the library; all arithmetic runs in its kernels.
     dx, dw, dbias = linear_backward(dy, x, w, act, preact)
     y             = gated_linear(x, w, bias, act)                act(g) v with [g v] = x w^T + bias
     dx, dw, dbias = gated_linear_backward(dy, x, w, preact, act)
+    q, scales     = quantize(w, 128)                             8-bit values, a scale per block
+    y             = block_linear(x, q, scales, bias, act, residual)
     y             = layer_norm(x, w, bias, eps)
     dx, dw, dbias = layer_norm_backward(dy, x, w, mean, rstd, residual)
     weights, ids  = route(logits, top, score, ...)
@@ -19,7 +21,7 @@ and call the library; all arithmetic runs in its kernels.
     y             = expert_combine(rows, plan, weights, residual)
     drows, dweights = expert_combine_backward(dy, rows, plan, weights)
 
-Tensors are float32 or bfloat16 (one type per call) on the current CUDA device,
+Tensors are float32 or bfloat16 (one type per call; 8-bit weights aside) on the current CUDA device,
 with a last dimension of unit stride and rows at any stride that does not overlap
 them.  Sums, scores and routing weights are FP32.  `act` is 'none', 'relu',
 'silu', 'gelu' or 'gelu_tanh'.  Work is queued on `stream` (torch's current stream
@@ -44,6 +46,8 @@ SGEMM_F32, SGEMM_BF16 = 0, 1
 MAX_EXPERTS = 512  # SGEMM_MAX_EXPERTS
 ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 SCORES = {"softmax": 0, "sigmoid": 1}
+BLOCK = 128  # SGEMM_BLOCK
+_E4M3 = torch.float8_e4m3fn
 _DTYPES = {torch.float32: SGEMM_F32, torch.bfloat16: SGEMM_BF16}
 
 
@@ -314,6 +318,85 @@ def gated_linear_backward(dy, x, w, preact, act="silu", bias=True, need_dx=True,
     if dx is not None and x.dim() != 2:
         dx = dx.view(x.shape)
     return dx, dw, db
+
+
+def quantize(x, rows=1, stream=None):
+    """(q, scales): x in e4m3 (torch.float8_e4m3fn, x's shape) with a float32 scale for each
+    block of `rows` x 128 elements: rows=1 for the activations of block_linear, x (..., k),
+    scales (..., ceil(k / 128)); rows=128 for its weights, x (n, k), scales (ceil(n / 128),
+    ceil(k / 128)).  scale = max(largest magnitude / 448, 2^-126), q = x / scale rounded to
+    nearest.  Rows of q are a multiple of 16 bytes apart, where block_linear reads them in place."""
+    if stream is not None:
+        return _on(stream, quantize, x, rows)
+    lib = load_library()
+    index, code = _begin(x, "x")
+    rows = _count(rows, "rows")
+    if rows != 1 and x.dim() != 2:
+        raise ValueError("x: blocks of %d rows need a tensor of two dimensions, got shape %s" % (rows, tuple(x.shape)))
+    x2 = _rows2d(x, "x")
+    t, k = x2.shape
+    ldx = _matrix(x2, "x", t, k, x.dtype, index)
+    ldq, across = -(-k // 16) * 16 or 1, -(-k // BLOCK)
+    q = _empty((t, ldq), dtype=torch.uint8, device=x.device).view(_E4M3)[:, :k]
+    scales = _empty((t if rows == 1 else -(-t // BLOCK), across), dtype=torch.float32, device=x.device)
+    rc = lib.sgemm_quantize(code, t, k, rows, x2.data_ptr(), ldx, q.data_ptr(), ldq, scales.data_ptr(), across or 1,
+                            _raw_stream(index))
+    if rc:
+        _check(rc, lib)
+    if x2 is not x:
+        q, scales = q.unflatten(0, x.shape[:-1]), scales.view(*x.shape[:-1], across)
+    return q, scales
+
+
+def block_linear(x, w, scales, bias=None, act="none", residual=None, x_scales=None, out=None, dtype=None, stream=None):
+    """y = act(x w^T + bias) + residual with 8-bit weights: w (n, k) in e4m3 and scales
+    (ceil(n / 128), ceil(k / 128)) as quantize(_, 128) makes them.  x (..., k) is float32 or
+    bfloat16, which the call rounds to e4m3 as quantize does, or e4m3 with x_scales (...,
+    ceil(k / 128)); the result is of x's type, or of `dtype` (bfloat16) for an e4m3 x, and so
+    are bias (n) and residual (..., n).  residual and out may be the same tensor."""
+    if stream is not None:
+        return _on(stream, block_linear, x, w, scales, bias, act, residual, x_scales, out, dtype)
+    lib = load_library()
+    if x_scales is None:
+        index, code = _begin(x, "x")
+        if dtype is not None and dtype is not x.dtype:
+            raise ValueError("dtype: the result of a %s x has its type" % x.dtype)
+        dtype = x.dtype
+    else:
+        index, _ = _begin(x_scales, "x_scales")
+        dtype = torch.bfloat16 if dtype is None else dtype
+        code = _DTYPES.get(dtype)
+        if code is None:
+            raise ValueError("dtype: %r is not torch.float32 or torch.bfloat16" % (dtype,))
+    x2 = _rows2d(x, "x")
+    n, k = _shape(w, "w", 2)
+    t, across = x2.shape[0], -(-k // BLOCK)
+    ldx = _matrix(x2, "x", t, k, dtype if x_scales is None else _E4M3, index)
+    ldxs = 0
+    if x_scales is not None:
+        x_scales = _rows2d(x_scales, "x_scales")
+        ldxs = _matrix(x_scales, "x_scales", t, across, torch.float32, index)
+    ldw = _matrix(w, "w", n, k, _E4M3, index)
+    ldws = _matrix(scales, "scales", -(-n // BLOCK), across, torch.float32, index)
+    if bias is not None:
+        _packed(bias, "bias", (n,), dtype, index)
+    ldr = 0
+    if residual is not None:
+        residual = _rows2d(residual, "residual")
+        ldr = _matrix(residual, "residual", t, n, dtype, index)
+    if out is None:
+        y, ldy = _empty((t, n), dtype=dtype, device=x.device), n or 1
+    else:
+        y = _rows2d(out, "out")
+        ldy = _matrix(y, "out", t, n, dtype, index)
+    rc = lib.sgemm_block_linear(code, t, n, k, x2.data_ptr(), ldx, _ptr(x_scales), ldxs, w.data_ptr(), ldw,
+                                scales.data_ptr(), ldws, _ptr(bias), _act(act), _ptr(residual), ldr, y.data_ptr(), ldy,
+                                _raw_stream(index))
+    if rc:
+        _check(rc, lib)
+    if out is not None:
+        return out
+    return y if x2 is x else y.view(*x.shape[:-1], n)
 
 
 def layer_norm(x, w=None, bias=None, eps=1e-5, stats=False, out=None, stream=None):

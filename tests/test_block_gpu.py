@@ -1,0 +1,342 @@
+"""8-bit matrices with a scale per block: their making bit for bit, and products with them
+against the sums of the values they stand for in 64 bits: one row to several tiles, odd
+extents, strided and unaligned rows, every activation, forced tile widths and K slices."""
+import math
+
+import pytest
+import torch
+
+import precision_gemm_gb300 as pg
+from tests import _layers_ref as R
+
+pytestmark = pytest.mark.gpu
+DTYPES = [torch.float32, torch.bfloat16]
+IDS = {torch.float32: "f32", torch.bfloat16: "bf16"}
+E4M3 = torch.float8_e4m3fn
+
+
+@pytest.fixture(autouse=True)
+def _healthy():
+    pg.load_library()
+    pg.device_status()
+    yield
+    assert pg.device_status() == 0
+
+
+def _gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def _draw(g, dtype, *shape, std=1.0):
+    return (torch.randn(*shape, generator=g) * std).to(dtype)
+
+
+def _strided(x, pad, offset=0):
+    r, c = x.shape
+    fill = 0x7F if x.dtype == E4M3 else math.nan  # e4m3's NaN
+    raw = torch.uint8 if x.dtype == E4M3 else x.dtype
+    buf = torch.full((offset + r * (c + pad),), fill, dtype=raw, device="cuda")
+    view = buf[offset:].view(r, c + pad)[:, :c]
+    view.copy_(x.view(raw) if x.dtype == E4M3 else x)
+    return view.view(E4M3) if x.dtype == E4M3 else view
+
+
+def quantized(x, rows):
+    """q and scales by the definition, in float32 on the CPU, a block at a time."""
+    x = x.float()
+    t, k = x.shape
+    q, scales = torch.empty(t, k, dtype=E4M3), torch.empty(-(-t // rows), -(-k // 128))
+    for i in range(0, t, rows):
+        for j in range(0, k, 128):
+            b = x[i:i + rows, j:j + 128]
+            s = torch.clamp_min(b.abs().max() / torch.tensor(448.0), torch.finfo(torch.float32).tiny)
+            scales[i // rows, j // 128] = s
+            q[i:i + rows, j:j + 128] = (b / s).to(E4M3)
+    return q, scales
+
+
+def values(q, scales, rows):
+    """The values that an 8-bit matrix stands for, in 64 bits."""
+    t, k = q.shape
+    spread = scales.double().repeat_interleave(rows, 0)[:t].repeat_interleave(128, 1)[:, :k]
+    return q.float().double() * spread
+
+
+def _bits(x):
+    return x.cpu().contiguous().view(torch.uint8 if x.dtype == E4M3 else torch.int32)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS.get)
+@pytest.mark.parametrize("rows", [1, 128])
+@pytest.mark.parametrize("t,k", [(1, 1), (3, 127), (2, 128), (5, 129), (130, 300), (260, 777), (128, 1024), (40, 4096)])
+def test_quantize(dtype, rows, t, k):
+    g = _gen(t + k)
+    # spreads from far below to far above one, so that scales differ from block to block
+    x = (_draw(g, torch.float32, t, k) * torch.exp2(torch.randint(-20, 20, (t, 1), generator=g).float())).to(dtype)
+    q, scales = pg.quantize(x.cuda(), rows)
+    wq, ws = quantized(x, rows)
+    assert q.dtype == E4M3 and q.shape == x.shape and q.stride(0) % 16 == 0
+    assert torch.equal(_bits(scales), _bits(ws)) and torch.equal(_bits(q), _bits(wq))
+
+
+def test_quantize_every_bfloat16_quotient():
+    """All 2^16 bfloat16 numbers but NaN and infinities, in blocks of their own magnitude and under
+    a large neighbour: ties, subnormal results, the smallest scale."""
+    u = torch.arange(0x7F80, dtype=torch.int32)
+    x = torch.cat([u, u | 0x8000]).to(torch.int16).view(torch.bfloat16)
+    near = x.view(-1, 128)
+    far = x.clone().view(-1, 64)
+    far = torch.cat([far, far.roll(1, 0)], 1)
+    for m in (near, far):
+        q, scales = pg.quantize(m.cuda())
+        wq, ws = quantized(m, 1)
+        assert torch.equal(_bits(scales), _bits(ws)) and torch.equal(_bits(q), _bits(wq))
+
+
+@pytest.mark.parametrize("rows", [1, 128])
+def test_quantize_zeros_infinities_nan_and_strides(rows):
+    x = torch.randn(140, 400, generator=_gen(2))
+    x[0, :128] = 0
+    x[1, 130], x[2, 300] = math.inf, math.nan
+    x[130:, 384:] = 0
+    q, scales = pg.quantize(_strided(x, 3, 1), rows)
+    wq, ws = quantized(x, rows)
+    assert torch.equal(torch.isnan(scales.cpu()), torch.isnan(ws))
+    assert torch.equal(torch.nan_to_num(scales.cpu()), torch.nan_to_num(ws))
+    assert torch.equal(torch.isnan(q.cpu().float()), torch.isnan(wq.float()))
+    assert torch.equal(torch.nan_to_num(q.cpu().float()), torch.nan_to_num(wq.float()))
+    if rows == 1:
+        assert scales[0, 0] == 2.0 ** -126 and scales[1, 1] == math.inf and math.isnan(scales[2, 2])
+    q3, s3 = pg.quantize(torch.randn(2, 3, 200, device="cuda"))
+    assert q3.shape == (2, 3, 200) and s3.shape == (2, 3, 2)
+    q0, s0 = pg.quantize(torch.empty(0, 200, device="cuda"), rows)
+    assert q0.shape == (0, 200) and s0.shape == (0, 2)
+
+
+def product(xq, xs, wq, ws, bias, name, residual):
+    """y, and the sums of its terms' magnitudes, of matrices as they are stored."""
+    x, w = values(xq, xs, 1), values(wq, ws, 128)
+    return R.linear(x, w, bias, name, residual)[::2]
+
+
+def _weights(g, n, k):
+    q, s = pg.quantize(_draw(g, torch.float32, n, k, std=k ** -0.5).cuda(), 128)
+    return q, s
+
+
+SIZES = [(1, 1, 1), (1, 130, 3), (1, 4096, 512), (2, 64, 128), (5, 1000, 777), (17, 257, 129), (33, 640, 256),
+         (128, 128, 1024), (130, 300, 777), (257, 513, 1000), (300, 256, 65), (1500, 300, 777), (600, 1030, 4100)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS.get)
+@pytest.mark.parametrize("t,n,k", SIZES)
+def test_block_linear(dtype, t, n, k):
+    g = _gen(t * 7 + n * 3 + k)
+    x = _draw(g, dtype, t, k)
+    b, r = _draw(g, dtype, n), _draw(g, dtype, t, n)
+    w, s = _weights(g, n, k)
+    name = R.ACTS[(t + n + k) % 5]
+    y = pg.block_linear(x.cuda(), w, s, b.cuda(), name, r.cuda())
+    xq, xs = pg.quantize(x.cuda())
+    want, den = product(xq.cpu(), xs.cpu(), w.cpu(), s.cpu(), b, name, r)
+    R.close(y, want, den, dtype)
+    # x in 8 bits already
+    again = pg.block_linear(xq, w, s, b.cuda(), name, r.cuda(), x_scales=xs, dtype=dtype)
+    assert torch.equal(y, again)
+    y = pg.block_linear(x.cuda(), w, s)
+    want, den = product(xq.cpu(), xs.cpu(), w.cpu(), s.cpu(), None, "none", None)
+    R.close(y, want, den, dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS.get)
+@pytest.mark.parametrize("name", R.ACTS)
+@pytest.mark.parametrize("t", [2, 200])
+def test_block_activations_over_their_range(dtype, name, t):
+    n, k = 192, 32
+    g = _gen(5)
+    x, b = _draw(g, dtype, t, k), torch.linspace(-12, 12, n).to(dtype)
+    x[0] = 0
+    w, s = _weights(g, n, k)
+    y = pg.block_linear(x.cuda(), w, s, b.cuda(), name)
+    want, den = product(*(v.cpu() for v in pg.quantize(x.cuda())), w.cpu(), s.cpu(), b, name, None)
+    R.close(y, want, den, dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS.get)
+@pytest.mark.parametrize("t,n,k,pad,offset", [(2, 70, 100, 3, 1), (140, 200, 136, 5, 3), (140, 200, 136, 8, 8),
+                                              (300, 136, 256, 16, 16), (300, 130, 64, 1, 0), (1, 64, 72, 7, 2)])
+def test_block_strides_and_alignment(dtype, t, n, k, pad, offset):
+    g = _gen(t + pad)
+    x, b, r = _draw(g, dtype, t, k), _draw(g, dtype, n), _draw(g, dtype, t, n)
+    w, s = _weights(g, n, k)
+    out = _strided(torch.zeros(t, n, dtype=dtype), pad, offset)
+    ws, ss = _strided(w, pad, offset), _strided(s, pad, offset)
+    got = pg.block_linear(_strided(x, pad, offset), ws, ss, b.cuda(), "silu", _strided(r, pad, offset), out=out)
+    assert got is out
+    xq, xs = pg.quantize(x.cuda())
+    want, den = product(xq.cpu(), xs.cpu(), w.cpu(), s.cpu(), b, "silu", r)
+    R.close(out, want, den, dtype)
+    gaps = out.as_strided((t, pad), (n + pad, 1), offset + n)[:t - 1]
+    assert torch.isnan(gaps).all()
+    y = pg.block_linear(_strided(xq, pad, offset), ws, ss, b.cuda(), "silu", r.cuda(),
+                        x_scales=_strided(xs, pad, offset), dtype=dtype)
+    assert torch.equal(y, out)
+    both = r.cuda()
+    assert pg.block_linear(x.cuda(), w, s, b.cuda(), "silu", both, out=both) is both
+    assert torch.equal(both, y)
+
+
+def test_block_scales_meet_their_blocks():
+    """Every block's scale a power of two of its own and small whole numbers as values: each sum
+    is exact, so a scale at another block shows."""
+    t, n, k = 300, 520, 700
+    g = _gen(9)
+    xq = torch.randint(-3, 4, (t, k), generator=g).float().to(E4M3)
+    wq = torch.randint(-3, 4, (n, k), generator=g).float().to(E4M3)
+    xs = torch.exp2(torch.randint(-2, 3, (t, 6), generator=g).float())
+    ws = torch.exp2(torch.randint(-2, 3, (5, 6), generator=g).float())
+    want = values(xq, xs, 1) @ values(wq, ws, 128).t()
+    for tt in (1, 20, t):
+        y = pg.block_linear(xq[:tt].cuda(), wq.cuda(), ws.cuda(), x_scales=xs[:tt].cuda(), dtype=torch.float32)
+        assert torch.equal(y.double().cpu(), want[:tt])
+
+
+def test_block_sums_are_float32():
+    """Results whose terms cancel to 2^-20 of them: a tensor core that kept fewer bits of a block's
+    sum than FP32 does would lose them.  The products are whole numbers, their sums below 2^24."""
+    t, n, k = 130, 200, 512
+    g = _gen(12)
+    x = torch.randint(0, 2, (t, k), generator=g).float() * 448
+    w = torch.randint(0, 2, (n, k), generator=g).float() * 448
+    x[:, ::7], w[:, ::5] = 1, -1
+    xs, ws = torch.ones(t, 4), torch.ones(2, 4)
+    want = x.double() @ w.double().t()
+    y = pg.block_linear(x.to(E4M3).cuda(), w.to(E4M3).cuda(), ws.cuda(), x_scales=xs.cuda(), dtype=torch.float32)
+    den = x.double().abs() @ w.double().abs().t()
+    R.close(y, want, den, torch.float32)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS.get)
+@pytest.mark.parametrize("t", [3, 150])
+def test_block_infinities_and_nan_stay_in_their_rows(dtype, t):
+    g = _gen(3)
+    x = _draw(g, dtype, t, 200)
+    x[1, 7], x[2, 150] = math.inf, math.nan
+    w, s = _weights(g, 140, 200)
+    y = pg.block_linear(x.cuda(), w, s).cpu()
+    assert torch.isnan(y).all(1).tolist() == [i in (1, 2) for i in range(t)]
+    assert torch.isfinite(y).all(1).tolist() == [i not in (1, 2) for i in range(t)]
+
+
+@pytest.mark.parametrize("bn,split", [(64, 0), (128, 0), (256, 0), (64, 3), (128, 9), (256, 2)])
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS.get)
+def test_block_every_tile_width_and_k_slices(dtype, bn, split):
+    t, n, k = 400, 600, 1100
+    g = _gen(bn + split)
+    x, b, r = _draw(g, dtype, t, k), _draw(g, dtype, n), _draw(g, dtype, t, n)
+    w, s = _weights(g, n, k)
+    pg.force_plan(bn, split)
+    try:
+        y = pg.block_linear(x.cuda(), w, s, b.cuda(), "gelu", r.cuda())
+        again = pg.block_linear(x.cuda(), w, s, b.cuda(), "gelu", r.cuda())
+    finally:
+        pg.force_plan(0, 0)
+    want, den = product(*(v.cpu() for v in pg.quantize(x.cuda())), w.cpu(), s.cpu(), b, "gelu", r)
+    R.close(y, want, den, dtype)
+    assert torch.equal(y, again)
+
+
+def test_block_more_tiles_than_a_wave():
+    pairs = torch.cuda.get_device_properties(0).multi_processor_count // 2
+    t, n, k = 256 * (pairs + 5) - 200, 250, 512
+    g = _gen(3)
+    x = _draw(g, torch.bfloat16, t, k)
+    w, s = _weights(g, n, k)
+    y = pg.block_linear(x.cuda(), w, s, act="relu")
+    want, den = product(*(v.cpu() for v in pg.quantize(x.cuda())), w.cpu(), s.cpu(), None, "relu", None)
+    R.close(y, want, den, torch.bfloat16)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS.get)
+def test_block_empty_extents_and_leading_dimensions(dtype):
+    g = _gen(1)
+    b, r = _draw(g, dtype, 9), _draw(g, dtype, 4, 9)
+    w, s = pg.quantize(torch.empty(9, 0, device="cuda"), 128)
+    y = pg.block_linear(torch.empty(4, 0, dtype=dtype, device="cuda"), w, s, b.cuda(), "silu", r.cuda())
+    want, _, den = R.linear(torch.zeros(4, 0), torch.zeros(9, 0), b, "silu", r)
+    R.close(y, want, den, dtype)
+    w, s = _weights(g, 24, 200)
+    assert pg.block_linear(torch.empty(0, 200, dtype=dtype, device="cuda"), w, s).shape == (0, 24)
+    x = _draw(g, dtype, 2, 3, 200).cuda()
+    y = pg.block_linear(x, w, s)
+    assert y.shape == (2, 3, 24)
+    assert torch.equal(y.view(6, 24), pg.block_linear(x.view(6, 200), w, s))
+    xq, xs = pg.quantize(x)
+    assert torch.equal(y, pg.block_linear(xq, w, s, x_scales=xs, dtype=dtype))
+
+
+def test_block_repeats_bitwise_on_streams_and_in_graphs():
+    g = _gen(4)
+    x = _draw(g, torch.bfloat16, 300, 1000).cuda()
+    w, s = _weights(g, 500, 1000)
+
+    def work():
+        q, qs = pg.quantize(x)
+        return [qs, pg.block_linear(x, w, s), pg.block_linear(x[:1], w, s, act="gelu"), pg.block_linear(x[:40], w, s),
+                pg.block_linear(q, w, s, x_scales=qs)]
+
+    first = work()
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        again = work()
+    st.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(first, again))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=st):
+        held = work()
+    for v in held:
+        v.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(first, held))
+
+
+def test_block_expired_wait_is_reported():
+    g = _gen(5)
+    x = _draw(g, torch.bfloat16, 300, 512).cuda()
+    w, s = _weights(g, 400, 512)
+    want = pg.block_linear(x, w, s)
+    limit = pg.set_wait_timeout(50_000_000)
+    flags = pg.debug_flags(pg.SGEMM_DEBUG_STALL_PRODUCER)
+    try:
+        pg.block_linear(x, w, s)
+        assert pg.device_status() == pg.SGEMM_ERR_TIMEOUT
+    finally:
+        pg.debug_flags(flags)
+        pg.set_wait_timeout(limit)
+    assert torch.equal(pg.block_linear(x, w, s), want) and pg.device_status() == 0
+
+
+def test_block_binding_refuses_mismatched_tensors():
+    x = torch.randn(6, 200, device="cuda")
+    w, s = pg.quantize(torch.randn(140, 200, device="cuda"), 128)
+    xq, xs = pg.quantize(x)
+    before = pg.launch_count()
+    bad = [lambda: pg.block_linear(x, w.view(torch.uint8), s), lambda: pg.block_linear(x, w.float(), s),
+           lambda: pg.block_linear(x, w[:, :199], s), lambda: pg.block_linear(x, w, s[:1]),
+           lambda: pg.block_linear(x, w, s.double()), lambda: pg.block_linear(x, w, s.t()),
+           lambda: pg.block_linear(x.half(), w, s), lambda: pg.block_linear(xq, w, s),
+           lambda: pg.block_linear(x, w, s, x_scales=xs), lambda: pg.block_linear(xq, w, s, x_scales=xs[:5]),
+           lambda: pg.block_linear(x, w, s, dtype=torch.bfloat16), lambda: pg.block_linear(x, w, s, act="sine"),
+           lambda: pg.block_linear(xq, w, s, x_scales=xs, dtype=torch.float16),
+           lambda: pg.block_linear(xq, w, s, torch.randn(140, device="cuda"), x_scales=xs),
+           lambda: pg.block_linear(x, w, s, out=x), lambda: pg.quantize(x.double()), lambda: pg.quantize(x.t()),
+           lambda: pg.quantize(x.view(2, 3, 200), 128)]
+    for call in bad:
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(pg.SgemmError):
+        pg.quantize(x, 64)
+    assert pg.launch_count() == before

@@ -10,9 +10,9 @@
 //
 // A cluster of two CTAs computes a tile of 256 rows j x BN features i (cta_group::2).  Rows of x lie
 // along TMEM lanes: a thread has one row, hence one sx per block, and its warp's columns are of one
-// 128 x 128 block of w, hence one sw: a block's promotion is one FMA per element, and results
-// leave in 16-byte stores.  Warps 0 and 1 load and issue as in product_tc.cu; warps 2 to 9
-// promote and finish, each its quarter of the lanes and half of the columns.
+// 128 x 128 block of w, hence one sw: a block's promotion is one FMA per element.  Warps 0 and 1
+// load and issue as in product_tc.cu; warps 4 to 11 promote and finish, each its quarter of the
+// lanes and half of the columns, whose sums take half of the register file (setmaxnreg).
 //
 // For few rows the tiles' k is cut into slices, whose scaled sums are added in slice order by
 // block_sum_kernel.
@@ -32,8 +32,13 @@ constexpr int kBlock = 128;  // values that share a scale, and bytes of a shared
 constexpr float kLargest = 448.0f;
 constexpr int kRows = 128;   // rows of x per CTA
 constexpr int kEpiWarps = 8;
-constexpr int kThreads = 64 + 32 * kEpiWarps;
-constexpr int kCols = 16;    // columns of a TMEM load
+constexpr int kThreads = 128 + 32 * kEpiWarps;
+constexpr int kCols = 32;    // columns of a TMEM load
+// Registers per thread: 168 at launch, the most that 384 threads can have; 4 warps give theirs to 8.
+constexpr int kRegsFew = 56, kRegsMany = 224;
+static_assert(4 * kRegsFew + 8 * kRegsMany <= 12 * 168, "the shares must be there");
+constexpr int kScaleSlots = 8;  // blocks of k whose scales are ready or on their way
+constexpr int kOutBytes = 64;   // row of a box that results leave through
 constexpr int kGroupTiles = 8;
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -76,8 +81,8 @@ __device__ __forceinline__ void put8(uint8_t* q, bool vec, int valid, const floa
 // Blocks of 1 x 128: sixteen lanes to each.  HBM-bound: reads x, writes a byte per value.
 template <typename T>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(int64_t rows, int64_t cols, const T* x, int64_t ldx, uint8_t* q,
-                                                            int64_t ldq, float* scales, int64_t lds, bool vec_x,
-                                                            bool vec_q) {
+                                                            int64_t ldq, float* scales, int64_t s_row, int64_t s_block,
+                                                            bool vec_x, bool vec_q) {
     pdl_trigger();
     pdl_wait();
     const int lane = threadIdx.x % 16;
@@ -94,7 +99,7 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(int64_t rows, int64_
         for (int o = 8; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
         const float scale = block_scale(m);
         if (valid > 0) put8(q + r * ldq + c, vec_q, valid, v, scale);
-        if (lane == 0 && b < count) scales[r * lds + (b - r * blocks)] = scale;
+        if (lane == 0 && b < count) scales[r * s_row + (b - r * blocks) * s_block] = scale;
     }
 }
 
@@ -154,13 +159,15 @@ struct Cfg {
     static constexpr int A_BYTES = kRows * kBlock;
     static constexpr int B_BYTES = BN / 2 * kBlock;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-    static constexpr int STAGES_RAW = 200 * 1024 / STAGE_BYTES;
+    static constexpr int STAGES_RAW = 184 * 1024 / STAGE_BYTES;
     static constexpr int STAGES = STAGES_RAW > 10 ? 10 : STAGES_RAW;
     static constexpr int BUFFERS = BN == 256 ? 2 : 4;  // of TMEM: blocks of k on their way
     static constexpr uint32_t TMEM_COLS = BUFFERS * BN;
     static constexpr int MINE = BN / 2;                // columns of an epilogue warp
-    static constexpr int BAR_BYTES = (2 * STAGES + 2 * BUFFERS + 1) * 8 + 16;
-    static constexpr size_t SMEM = 1024 + static_cast<size_t>(STAGES) * STAGE_BYTES + BAR_BYTES;
+    static constexpr int BAR_BYTES = (2 * STAGES + 2 * BUFFERS + 2 * kScaleSlots + 1) * 8 + 16;
+    static constexpr int OUT_BYTES = kEpiWarps * 2 * 32 * kOutBytes;        // two boxes of 32 rows per warp
+    static constexpr int SCALE_BYTES = kScaleSlots * 2 * kRows * 4;         // of the rows, for each half of the columns
+    static constexpr size_t SMEM = 1024 + static_cast<size_t>(STAGES) * STAGE_BYTES + OUT_BYTES + SCALE_BYTES + BAR_BYTES;
     static_assert(A_BYTES % 1024 == 0 && B_BYTES % 1024 == 0, "slots need 1 KiB alignment");
 };
 
@@ -169,7 +176,7 @@ struct Params {
     int32_t tiles_t, tiles_n;
     int32_t split, split_kb;
     const float* x_scales;
-    int64_t ldxs;
+    int64_t xs_row, xs_block;  // strides along rows and along blocks of k
     const float* w_scales;
     int64_t ldws;
     const void* bias;
@@ -179,6 +186,7 @@ struct Params {
     void* y;
     int64_t ldy;
     int32_t vec;        // y, residual and bias in 16-byte accesses
+    int32_t tma_out;    // y leaves through the tensor map tmY (the slices' sums always do)
     float* part;        // slices' sums, [slice][t][ldp]
     int64_t ldp;
     uint64_t timeout_ns;
@@ -186,14 +194,13 @@ struct Params {
     int32_t debug_flags;
 };
 
-// Eight columns from i on of row j, sums v: the epilogue.
+// Eight columns from i on of row j: results of sums v (those past n are of no use).
 template <typename T, int ACT>
-__device__ __forceinline__ void finish8(const Params& p, int64_t j, int64_t i, float (&v)[8]) {
+__device__ __forceinline__ void result8(const Params& p, int64_t j, int64_t i, float (&v)[8]) {
     const int valid = static_cast<int>(min(p.n - i, int64_t(8)));
-    if (valid <= 0) return;
     if (p.bias) {
         float b[8];
-        load8(static_cast<const T*>(p.bias) + i, p.vec, valid, b);
+        load8(static_cast<const T*>(p.bias) + (valid > 0 ? i : 0), p.vec, valid, b);
 #pragma unroll
         for (int t = 0; t < 8; ++t) v[t] += b[t];
     }
@@ -201,26 +208,33 @@ __device__ __forceinline__ void finish8(const Params& p, int64_t j, int64_t i, f
     for (int t = 0; t < 8; ++t) v[t] = act_value<ACT, std::is_same<T, bf16>::value>(v[t]);
     if (p.residual) {
         float r[8];
-        load8(static_cast<const T*>(p.residual) + j * p.ldr + i, p.vec, valid, r);
+        load8(static_cast<const T*>(p.residual) + (valid > 0 ? j * p.ldr + i : 0), p.vec, valid, r);
 #pragma unroll
         for (int t = 0; t < 8; ++t) v[t] += r[t];
     }
-    store8(static_cast<T*>(p.y) + j * p.ldy + i, p.vec, valid, v);
+}
+template <typename T>
+__device__ __forceinline__ void store_result8(const Params& p, int64_t j, int64_t i, const float (&v)[8]) {
+    const int valid = static_cast<int>(min(p.n - i, int64_t(8)));
+    if (valid > 0) store8(static_cast<T*>(p.y) + j * p.ldy + i, p.vec, valid, v);
 }
 
 template <int BN, typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    block_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, const Params p) {
+    block_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+                 const __grid_constant__ CUtensorMap tmY, const Params p) {
     using C = Cfg<BN>;
     constexpr int S = C::STAGES, NB = C::BUFFERS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = align_smem_1024(smem_raw);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S * C::STAGE_BYTES);
-    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 2 * S + 2 * NB + 1);
+    float* scale_ring = reinterpret_cast<float*>(smem + S * C::STAGE_BYTES + C::OUT_BYTES);  // [slot][half][row]
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S * C::STAGE_BYTES + C::OUT_BYTES + C::SCALE_BYTES);
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 2 * S + 2 * NB + 2 * kScaleSlots + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
     const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + S);
     const uint32_t acc_full0 = smem_u32(bars + 2 * S), acc_empty0 = smem_u32(bars + 2 * S + NB);
-    const uint32_t mma_done = smem_u32(bars + 2 * S + 2 * NB);
+    const uint32_t scale_full0 = smem_u32(bars + 2 * S + 2 * NB), scale_empty0 = scale_full0 + 8 * kScaleSlots;
+    const uint32_t mma_done = scale_empty0 + 8 * kScaleSlots;
 
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);  // known to be uniform
     const int lane = threadIdx.x & 31;
@@ -236,6 +250,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int b = 0; b < NB; ++b) {
             mbar_init(acc_full0 + 8 * b, 1);
             mbar_init(acc_empty0 + 8 * b, 2 * kEpiWarps);
+        }
+        for (int b = 0; b < kScaleSlots; ++b) {
+            mbar_init(scale_full0 + 8 * b, 1);
+            mbar_init(scale_empty0 + 8 * b, kEpiWarps);
         }
         mbar_init(mma_done, 1);
         *abort_flag = 0;
@@ -271,110 +289,158 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         return x;
     };
 
-    if (warp == 0) {
-        // ---------------- TMA loader (both CTAs) ----------------
-        if (!(p.debug_flags & 1)) {
-            const uint32_t full_leader0 = map_to_rank(full0, 0);
-            int it = 0, slot_i = 0;
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
+        if (warp == 0) {
+            // ---------------- TMA loader (both CTAs) ----------------
+            if (!(p.debug_flags & 1)) {
+                const uint32_t full_leader0 = map_to_rank(full0, 0);
+                int it = 0, slot_i = 0;
+                uint32_t phase = 1;
+                bool ok = true;
+                for (int u = pair; u < units && ok; u += pairs) {
+                    const Unit x = unit_of(u);
+                    const int ja = __shfl_sync(0xffffffffu, x.j0 + kRows * static_cast<int>(rank), 0);
+                    const int ib = __shfl_sync(0xffffffffu, x.i0 + BN / 2 * static_cast<int>(rank), 0);
+                    const int kb0 = __shfl_sync(0xffffffffu, x.kb0, 0), nkb = __shfl_sync(0xffffffffu, x.nkb, 0);
+                    for (int kb = 0; kb < nkb; ++kb, ++it) {
+                        ok = __all_sync(0xffffffffu,
+                                        mbar_wait_short(empty0 + 8 * slot_i, phase, p.timeout_ns, abort_flag));
+                        if (!ok) {
+                            if (lane == 0) raise_abort(abort_flag, p.status);
+                            break;
+                        }
+                        if (leader && lane == 0) mbar_arrive_expect_tx(full0 + 8 * slot_i, 2 * C::STAGE_BYTES);
+                        const uint32_t bar = full_leader0 + 8 * slot_i;
+                        const uint32_t slot = smem_u32(smem) + slot_i * C::STAGE_BYTES;
+                        tma_load_3d_pair_warp(slot, &tmX, (kb0 + kb) * kBlock, ja, 0, bar);
+                        tma_load_3d_pair_warp(slot + C::A_BYTES, &tmW, (kb0 + kb) * kBlock, ib, 0, bar);
+                        if (++slot_i == S) {
+                            slot_i = 0;
+                            phase ^= 1;
+                        }
+                    }
+                }
+                if (lane == 0) pdl_trigger();
+                if (leader && lane == 0) {
+                    // Let every copy of the pair land before the CTAs may retire (CTA 0's full barriers
+                    // count both CTAs' bytes).
+                    for (int q = max(0, it - S); q < it; ++q)
+                        mbar_wait_bounded(full0 + 8 * (q % S), (q / S) & 1, p.timeout_ns, nullptr);
+                }
+            }
+            __syncwarp();
+        } else if (warp == 1) {
+            // ---------------- MMA issuer (CTA 0 of the pair) ----------------
+            if (leader) {
+                const uint32_t slot0 = smem_u32(smem);
+                const uint64_t a_desc0 = smem_desc(slot0, 16, 1024, kSwizzle128B);
+                const uint64_t b_desc0 = smem_desc(slot0 + C::A_BYTES, 16, 1024, kSwizzle128B);
+                const uint32_t idesc = idesc_e4m3(2 * kRows, BN);
+                int slot_i = 0, buf = 0;
+                uint32_t phase = 0, acc_phase = 1;
+                bool ok = true;
+                for (int u = pair; u < units && ok; u += pairs) {
+                    const int nkb = __shfl_sync(0xffffffffu, unit_of(u).nkb, 0);
+                    for (int kb = 0; kb < nkb; ++kb) {
+                        ok = __all_sync(0xffffffffu, mbar_wait_short(acc_empty0 + 8 * buf, acc_phase, p.timeout_ns, abort_flag)) &&
+                             __all_sync(0xffffffffu, mbar_wait_short(full0 + 8 * slot_i, phase, p.timeout_ns, abort_flag));
+                        if (!ok) break;
+                        tc_fence_after_sync();
+                        const uint32_t o = static_cast<uint32_t>(slot_i * C::STAGE_BYTES) >> 4;
+    #pragma unroll
+                        for (int kk = 0; kk < kBlock / 32; ++kk)
+                            mma_e4m3_pair_warp(tmem + buf * BN, a_desc0 + (o + 2 * kk), b_desc0 + (o + 2 * kk), idesc, kk > 0);
+                        mma_commit_pair_warp(empty0 + 8 * slot_i);
+                        mma_commit_pair_warp(acc_full0 + 8 * buf);
+                        if (++slot_i == S) {
+                            slot_i = 0;
+                            phase ^= 1;
+                        }
+                        if (++buf == NB) {
+                            buf = 0;
+                            acc_phase ^= 1;
+                        }
+                    }
+                }
+                if (!ok && lane == 0) raise_abort(abort_flag, p.status);
+                mma_commit_pair_local_warp(mma_done);  // every MMA issued here has completed
+                mbar_wait_bounded(mma_done, 0, p.timeout_ns, nullptr);
+            }
+            __syncwarp();
+        } else if (warp == 2) {
+            // ---------------- scales (both CTAs) ----------------
+            // sx sw of this CTA's rows and each half of the columns, several blocks of k ahead of their use
+            int slot = 0;
             uint32_t phase = 1;
             bool ok = true;
             for (int u = pair; u < units && ok; u += pairs) {
                 const Unit x = unit_of(u);
-                const int ja = __shfl_sync(0xffffffffu, x.j0 + kRows * static_cast<int>(rank), 0);
-                const int ib = __shfl_sync(0xffffffffu, x.i0 + BN / 2 * static_cast<int>(rank), 0);
-                const int kb0 = __shfl_sync(0xffffffffu, x.kb0, 0), nkb = __shfl_sync(0xffffffffu, x.nkb, 0);
-                for (int kb = 0; kb < nkb; ++kb, ++it) {
-                    ok = __all_sync(0xffffffffu,
-                                    mbar_wait_bounded(empty0 + 8 * slot_i, phase, p.timeout_ns, abort_flag));
-                    if (!ok) {
-                        if (lane == 0) raise_abort(abort_flag, p.status);
-                        break;
-                    }
-                    if (leader && lane == 0) mbar_arrive_expect_tx(full0 + 8 * slot_i, 2 * C::STAGE_BYTES);
-                    const uint32_t bar = full_leader0 + 8 * slot_i;
-                    const uint32_t slot = smem_u32(smem) + slot_i * C::STAGE_BYTES;
-                    tma_load_3d_pair_warp(slot, &tmX, (kb0 + kb) * kBlock, ja, 0, bar);
-                    tma_load_3d_pair_warp(slot + C::A_BYTES, &tmW, (kb0 + kb) * kBlock, ib, 0, bar);
-                    if (++slot_i == S) {
-                        slot_i = 0;
-                        phase ^= 1;
-                    }
-                }
-            }
-            if (lane == 0) pdl_trigger();
-            if (leader && lane == 0) {
-                // Let every copy of the pair land before the CTAs may retire (CTA 0's full barriers
-                // count both CTAs' bytes).
-                for (int q = max(0, it - S); q < it; ++q)
-                    mbar_wait_bounded(full0 + 8 * (q % S), (q / S) & 1, p.timeout_ns, nullptr);
-            }
-        }
-        __syncwarp();
-    } else if (warp == 1) {
-        // ---------------- MMA issuer (CTA 0 of the pair) ----------------
-        if (leader) {
-            const uint32_t slot0 = smem_u32(smem);
-            const uint64_t a_desc0 = smem_desc(slot0, 16, 1024, kSwizzle128B);
-            const uint64_t b_desc0 = smem_desc(slot0 + C::A_BYTES, 16, 1024, kSwizzle128B);
-            const uint32_t idesc = idesc_e4m3(2 * kRows, BN);
-            int slot_i = 0, buf = 0;
-            uint32_t phase = 0, acc_phase = 1;
-            bool ok = true;
-            for (int u = pair; u < units && ok; u += pairs) {
-                const int nkb = __shfl_sync(0xffffffffu, unit_of(u).nkb, 0);
-                for (int kb = 0; kb < nkb; ++kb) {
-                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(acc_empty0 + 8 * buf, acc_phase, p.timeout_ns, abort_flag)) &&
-                         __all_sync(0xffffffffu, mbar_wait_bounded(full0 + 8 * slot_i, phase, p.timeout_ns, abort_flag));
-                    if (!ok) break;
-                    tc_fence_after_sync();
-                    const uint32_t o = static_cast<uint32_t>(slot_i * C::STAGE_BYTES) >> 4;
+                const int j0 = x.j0 + kRows * static_cast<int>(rank) + lane;
+                const float *sx[4], *sw[2];
 #pragma unroll
-                    for (int kk = 0; kk < kBlock / 32; ++kk)
-                        mma_e4m3_pair_warp(tmem + buf * BN, a_desc0 + (o + 2 * kk), b_desc0 + (o + 2 * kk), idesc, kk > 0);
-                    mma_commit_pair_warp(empty0 + 8 * slot_i);
-                    mma_commit_pair_warp(acc_full0 + 8 * buf);
-                    if (++slot_i == S) {
-                        slot_i = 0;
-                        phase ^= 1;
+                for (int r = 0; r < 4; ++r) sx[r] = p.x_scales + min(j0 + 32 * r, p.t - 1) * p.xs_row + x.kb0 * p.xs_block;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) sw[h] = p.w_scales + min(x.i0 + C::MINE * h, p.n - 1) / kBlock * p.ldws + x.kb0;
+                constexpr int U = 2;  // blocks whose loads are in flight together
+                for (int kb = 0; kb < x.nkb && ok; kb += U) {
+                    float a[U][4], b[U][2];
+#pragma unroll
+                    for (int d = 0; d < U; ++d) {
+                        const int at = min(kb + d, x.nkb - 1);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) a[d][r] = __ldg(sx[r] + at * p.xs_block);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) b[d][h] = __ldg(sw[h] + at);
                     }
-                    if (++buf == NB) {
-                        buf = 0;
-                        acc_phase ^= 1;
+#pragma unroll
+                    for (int d = 0; d < U; ++d) {
+                        if (kb + d >= x.nkb) break;
+                        ok = __all_sync(0xffffffffu, mbar_wait_short(scale_empty0 + 8 * slot, phase, p.timeout_ns, abort_flag));
+                        if (!ok) {
+                            if (lane == 0) raise_abort(abort_flag, p.status);
+                            break;
+                        }
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) scale_ring[(2 * slot + h) * kRows + 32 * r + lane] = a[d][r] * b[d][h];
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(scale_full0 + 8 * slot);
+                        if (++slot == kScaleSlots) {
+                            slot = 0;
+                            phase ^= 1;
+                        }
                     }
                 }
             }
-            if (!ok && lane == 0) raise_abort(abort_flag, p.status);
-            mma_commit_pair_local_warp(mma_done);  // every MMA issued here has completed
-            mbar_wait_bounded(mma_done, 0, p.timeout_ns, nullptr);
+            __syncwarp();
         }
-        __syncwarp();
     } else {
-        // ---------------- promotion and epilogue (warps 2..9, both CTAs) ----------------
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMany));
+        // ---------------- promotion and epilogue (warps 4..11, both CTAs) ----------------
         const int q = warp & 3;            // TMEM lane quarter this warp may access
-        const int half = (warp - 2) >> 2;  // its half of the columns
+        const int half = (warp - 4) >> 2;  // its half of the columns
         const uint32_t acc_empty_leader0 = map_to_rank(acc_empty0, 0);
         const uint32_t base = tmem + (static_cast<uint32_t>(32 * q) << 16) + C::MINE * half;
+        uint8_t* out = smem + S * C::STAGE_BYTES + (warp - 4) * (2 * 32 * kOutBytes);
+        int boxes = 0;  // sent on their way
+        auto free_buffer = [&](int b) {
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote_relaxed(acc_empty_leader0 + 8 * b);
+        };
         int buf = 0;
         uint32_t acc_phase = 0;
         bool ok = true;
+        int slot = 0;
+        uint32_t scale_phase = 0;
         for (int u = pair; u < units && ok; u += pairs) {
             const Unit x = unit_of(u);
             const int row0 = x.j0 + kRows * static_cast<int>(rank) + 32 * q;
             const int64_t j = row0 + lane;
             const int i0 = x.i0 + C::MINE * half;
             const bool there = row0 < p.t && i0 < p.n;  // of the warp
-            // this row's and these columns' scales, four blocks at a time, four ahead
-            const float* sx = p.x_scales + (j < p.t ? j : 0) * p.ldxs;
-            const float* sw = p.w_scales + (there ? i0 / kBlock : 0) * p.ldws;
-            float next[4];
-            auto scales = [&](int kb) {
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int at = x.kb0 + kb + r;
-                    next[r] = kb + r < x.nkb ? sx[at] * sw[at] : 0.0f;
-                }
-            };
-            scales(0);
             if (p.residual && j < p.t && i0 < p.n) {
                 // the residual comes into L2 while the MMAs run
                 const T* r = static_cast<const T*>(p.residual) + j * p.ldr + i0;
@@ -383,76 +449,126 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             float2 acc[C::MINE / 2];
 #pragma unroll
             for (int c = 0; c < C::MINE / 2; ++c) acc[c] = make_float2(0.0f, 0.0f);
-            for (int g = 0; g < x.nkb && ok; g += 4) {
-                float s[4];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) s[r] = next[r];
-                scales(g + 4);
-#pragma unroll 1
-                for (int kb = g; kb < min(g + 4, x.nkb); ++kb) {
-                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(acc_full0 + 8 * buf, acc_phase, p.timeout_ns, abort_flag));
-                    if (!ok) {
-                        if (lane == 0) raise_abort(abort_flag, p.status);
-                        break;
-                    }
-                    tc_fence_after_sync();
-                    const float2 scale = both(s[0]);
-#pragma unroll
-                    for (int r = 0; r < 3; ++r) s[r] = s[r + 1];
+            int last = 0;  // the buffer of the last block, which the results go through
+            for (int kb = 0; kb < x.nkb; ++kb) {
+                ok = __all_sync(0xffffffffu, mbar_wait_short(scale_full0 + 8 * slot, scale_phase, p.timeout_ns, abort_flag));
+                const float s = scale_ring[(2 * slot + half) * kRows + 32 * q + lane];
+                ok = ok && __all_sync(0xffffffffu, mbar_wait_short(acc_full0 + 8 * buf, acc_phase, p.timeout_ns, abort_flag));
+                if (!ok) {
+                    if (lane == 0) raise_abort(abort_flag, p.status);
+                    break;
+                }
+                tc_fence_after_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(scale_empty0 + 8 * slot);
+                if (there) {
+                    const float2 scale = both(s);
                     const uint32_t at = base + buf * BN;
-                    auto free_buffer = [&]() {
-                        tc_fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_remote_relaxed(acc_empty_leader0 + 8 * buf);
-                    };
-                    if (there) {
-                        uint32_t v[2][kCols];
-                        __syncwarp();
-                        tmem_ld_32x32b_x16(at, v[0]);
+                    uint32_t v[2][kCols];
+                    tmem_ld_32x32b_x32(at, v[0]);
 #pragma unroll
-                        for (int c = 0; c < C::MINE / kCols; ++c) {
-                            tmem_wait_ld(v[c & 1]);
-                            if (c + 1 < C::MINE / kCols)
-                                tmem_ld_32x32b_x16(at + kCols * (c + 1), v[(c + 1) & 1]);
-                            else
-                                free_buffer();
+                    for (int c = 0; c < C::MINE / kCols; ++c) {
+                        tmem_wait_ld(v[c & 1]);
+                        if (c + 1 < C::MINE / kCols)
+                            tmem_ld_32x32b_x32(at + kCols * (c + 1), v[(c + 1) & 1]);
+                        else if (kb + 1 < x.nkb)
+                            free_buffer(buf);
 #pragma unroll
-                            for (int k = 0; k < kCols / 2; ++k)
-                                acc[kCols / 2 * c + k] =
-                                    fma2(make_float2(__uint_as_float(v[c & 1][2 * k]), __uint_as_float(v[c & 1][2 * k + 1])),
-                                         scale, acc[kCols / 2 * c + k]);
-                        }
-                    } else {
-                        free_buffer();
+                        for (int k = 0; k < kCols / 2; ++k)
+                            acc[kCols / 2 * c + k] =
+                                fma2(make_float2(__uint_as_float(v[c & 1][2 * k]), __uint_as_float(v[c & 1][2 * k + 1])),
+                                     scale, acc[kCols / 2 * c + k]);
                     }
-                    if (++buf == NB) {
-                        buf = 0;
-                        acc_phase ^= 1;
-                    }
+                } else if (kb + 1 < x.nkb) {
+                    free_buffer(buf);
+                }
+                last = buf;
+                if (++buf == NB) {
+                    buf = 0;
+                    acc_phase ^= 1;
+                }
+                if (++slot == kScaleSlots) {
+                    slot = 0;
+                    scale_phase ^= 1;
                 }
             }
-            if (!ok || j >= p.t) continue;
-            if (p.part) {
-                float* dst = p.part + (static_cast<int64_t>(x.slice) * p.t + j) * p.ldp + i0;
+            if (!ok) break;
+            // The results go back to the warp's own columns of the last buffer and from there, 16 at a
+            // time, through the epilogue: a loop, where registers would want it written out.
+            const uint32_t at = base + last * BN;
+            if (there) {
 #pragma unroll
-                for (int c = 0; c < C::MINE / 2; c += 2)
-                    if (i0 + 2 * c < p.n)  // rows are whole multiples of eight there
-                        *reinterpret_cast<float4*>(dst + 2 * c) = make_float4(acc[c].x, acc[c].y, acc[c + 1].x, acc[c + 1].y);
-            } else {
-                with_act(p.act, [&](auto act) {
+                for (int c = 0; c < C::MINE / kCols; ++c) {
+                    uint32_t v[kCols];
 #pragma unroll
-                    for (int c = 0; c < C::MINE / 2; c += 4) {
-                        float f[8];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            f[2 * k] = acc[c + k].x;
-                            f[2 * k + 1] = acc[c + k].y;
-                        }
-                        finish8<T, decltype(act)::value>(p, j, i0 + 2 * c, f);
+                    for (int k = 0; k < kCols / 2; ++k) {
+                        v[2 * k] = __float_as_uint(acc[kCols / 2 * c + k].x);
+                        v[2 * k + 1] = __float_as_uint(acc[kCols / 2 * c + k].y);
                     }
-                });
+                    __syncwarp();
+                    tmem_st_32x32b_x32(at + kCols * c, v);
+                }
+                tmem_wait_st();
+                // The columns as elements TO, a box of 64 bytes of 32 rows at a time, through shared memory (the
+                // 64-byte swizzle) and TMA where the result's rows allow it.
+                auto emit = [&](auto element, bool tma, int z, auto results) {
+                    using TO = decltype(element);
+                    constexpr int BOX = kOutBytes / static_cast<int>(sizeof(TO)), N = static_cast<int>(sizeof(TO)) / 2;
+#pragma unroll 1
+                    for (int c = 0; c < C::MINE && i0 + c < p.n; c += BOX) {
+                        uint32_t v[BOX];
+                        __syncwarp();
+                        if constexpr (BOX == 32)
+                            tmem_ld_32x32b_x32(at + c, v);
+                        else
+                            tmem_ld_32x32b_x16(at + c, v);
+                        uint8_t* box = out + (boxes & 1) * (32 * kOutBytes);
+                        if (tma) {
+                            if (lane == 0) bulk_wait_read_all_but_one();  // the box before the last one is read
+                            __syncwarp();
+                        }
+                        tmem_wait_ld(v);
+#pragma unroll
+                        for (int h = 0; h < BOX; h += 8) {
+                            float f[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(v[h + k]);
+                            if (j < p.t) results(c + h, f);
+                            if (tma) {
+                                TO e[8];
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) e[k] = from_float<TO>(f[k]);
+#pragma unroll
+                                for (int k = 0; k < N; ++k)  // N 16-byte words of eight elements
+                                    *reinterpret_cast<uint4*>(box + kOutBytes * lane + 16 * ((h / 8 * N + k) ^ ((lane >> 1) & 3))) =
+                                        reinterpret_cast<const uint4*>(e)[k];
+                            } else if (j < p.t) {
+                                store_result8<TO>(p, j, i0 + c + h, f);
+                            }
+                        }
+                        if (tma) {
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) {
+                                tma_store_3d(&tmY, smem_u32(box), i0 + c, row0, z);
+                                bulk_commit();
+                            }
+                            ++boxes;
+                        }
+                    }
+                };
+                if (p.part)
+                    emit(float(), true, x.slice, [](int, float(&)[8]) {});
+                else
+                    with_act(p.act, [&](auto act) {
+                        emit(T(), p.tma_out != 0, 0,
+                             [&](int c, float(&f)[8]) { result8<T, decltype(act)::value>(p, j, i0 + c, f); });
+                    });
             }
+            if (x.nkb > 0) free_buffer(last);
         }
+        if (lane == 0) bulk_wait_read();  // the boxes must stay until they are read
+        __syncwarp();
     }
 
     tc_fence_before_sync();
@@ -481,11 +597,12 @@ __global__ void __launch_bounds__(256) block_sum_kernel(const Params p) {
         v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
         v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
     }
-    with_act(p.act, [&](auto act) { finish8<T, decltype(act)::value>(p, j, i, v); });
+    with_act(p.act, [&](auto act) { result8<T, decltype(act)::value>(p, j, i, v); });
+    store_result8<T>(p, j, i, v);
 }
 
 template <int BN, typename T>
-cudaError_t run(const CUtensorMap& x, const CUtensorMap& w, const Params& p, int num_sms, cudaStream_t st) {
+cudaError_t run(const CUtensorMap (&m)[3], const Params& p, int num_sms, cudaStream_t st) {
     using C = Cfg<BN>;
     auto kern = block_kernel<BN, T>;
     static std::atomic<uint64_t> smem_set{0};
@@ -495,13 +612,13 @@ cudaError_t run(const CUtensorMap& x, const CUtensorMap& w, const Params& p, int
     const int most = resident_pairs(reinterpret_cast<const void*>(kern), kThreads, C::SMEM, num_sms, resident);
     const int64_t units = static_cast<int64_t>(p.tiles_t) * p.tiles_n * p.split;
     return launch_kernel(true, kern, dim3(static_cast<unsigned>(2 * std::min<int64_t>(units, most))), dim3(kThreads),
-                         C::SMEM, st, x, w, p);
+                         C::SMEM, st, m[0], m[1], m[2], p);
 }
 
 }  // namespace
 
 cudaError_t launch_quantize(int dtype, int64_t rows, int64_t cols, int block_rows, const void* x, int64_t ldx, uint8_t* q,
-                            int64_t ldq, float* scales, int64_t lds, int num_sms, cudaStream_t st) {
+                            int64_t ldq, float* scales, int64_t s_row, int64_t s_block, int num_sms, cudaStream_t st) {
     const bool vec_q = (reinterpret_cast<uintptr_t>(q) & 7) == 0 && ldq % 8 == 0;
     auto go = [&](auto zero) {
         using T = decltype(zero);
@@ -510,10 +627,10 @@ cudaError_t launch_quantize(int dtype, int64_t rows, int64_t cols, int block_row
         if (block_rows == 1)
             return launch_kernel(true, quantize_rows_kernel<T>,
                                  dim3(static_cast<unsigned>(std::min<int64_t>(cdiv(rows * across, 16), int64_t(64) * num_sms))),
-                                 dim3(256), 0, st, rows, cols, static_cast<const T*>(x), ldx, q, ldq, scales, lds, vec_x,
-                                 vec_q);
+                                 dim3(256), 0, st, rows, cols, static_cast<const T*>(x), ldx, q, ldq, scales, s_row, s_block,
+                                 vec_x, vec_q);
         return launch_kernel(true, quantize_blocks_kernel<T>, dim3(static_cast<unsigned>(cdiv(rows, kBlock) * across)),
-                             dim3(256), 0, st, rows, cols, static_cast<const T*>(x), ldx, q, ldq, scales, lds, vec_x, vec_q);
+                             dim3(256), 0, st, rows, cols, static_cast<const T*>(x), ldx, q, ldq, scales, s_row, vec_x, vec_q);
     };
     return dtype == SGEMM_F32 ? go(float()) : go(bf16());
 }
@@ -560,7 +677,8 @@ int launch_block(const CallContext& c, const BlockProduct& b, const BlockPlan& p
     p.split = plan.split;
     p.split_kb = plan.split_kb;
     p.x_scales = b.x_scales;
-    p.ldxs = b.ldxs;
+    p.xs_row = b.xs_row;
+    p.xs_block = b.xs_block;
     p.w_scales = b.w_scales;
     p.ldws = b.ldws;
     p.bias = b.bias;
@@ -578,19 +696,25 @@ int launch_block(const CallContext& c, const BlockProduct& b, const BlockPlan& p
     p.timeout_ns = c.timeout_ns;
     p.status = c.status;
     p.debug_flags = c.debug_flags;
-    CUtensorMap x{}, w{};
+    CUtensorMap m[3] = {};
+    int rc;
     if (b.k > 0) {
-        int rc;
-        if ((rc = call_encode_u8(&x, b.x, b.k, b.t, b.ldx, kRows))) return rc;
-        if ((rc = call_encode_u8(&w, b.w, b.k, b.n, b.ldw, static_cast<uint32_t>(plan.bn / 2)))) return rc;
+        if ((rc = call_encode_3d(&m[0], 1, b.x, b.k, b.t, b.ldx, 1, 0, kBlock, kRows))) return rc;
+        if ((rc = call_encode_3d(&m[1], 1, b.w, b.k, b.n, b.ldw, 1, 0, kBlock, static_cast<uint32_t>(plan.bn / 2)))) return rc;
+    }
+    if (p.part) {
+        if ((rc = call_encode_3d(&m[2], 4, p.part, b.n, b.t, p.ldp, plan.split, b.t * p.ldp, kOutBytes, 32))) return rc;
+    } else if (aligned(b.y, b.ldy)) {
+        p.tma_out = 1;
+        if ((rc = call_encode_3d(&m[2], b.dtype == SGEMM_F32 ? 4 : 2, b.y, b.n, b.t, b.ldy, 1, 0, kOutBytes, 32))) return rc;
     }
     auto go = [&](auto zero) {
         using T = decltype(zero);
         cudaError_t e;
         switch (plan.bn) {
-            case 64: e = run<64, T>(x, w, p, c.sms, st); break;
-            case 128: e = run<128, T>(x, w, p, c.sms, st); break;
-            default: e = run<256, T>(x, w, p, c.sms, st); break;
+            case 64: e = run<64, T>(m, p, c.sms, st); break;
+            case 128: e = run<128, T>(m, p, c.sms, st); break;
+            default: e = run<256, T>(m, p, c.sms, st); break;
         }
         if (e != cudaSuccess || p.part == nullptr) return e;
         return launch_kernel(true, block_sum_kernel<T>, dim3(static_cast<unsigned>(cdiv(b.t * (p.ldp / 8), 256))), dim3(256),

@@ -480,7 +480,7 @@ PG_EXPORT int sgemm_quantize(int dtype, int64_t t, int64_t k, int block_rows, co
     if (!some) return 0;
     CallContext c;
     PG_CHECK(call_begin(&c));
-    const cudaError_t e = launch_quantize(dtype, t, k, block_rows, x, ldx, q, ldq, scales, lds, c.sms,
+    const cudaError_t e = launch_quantize(dtype, t, k, block_rows, x, ldx, q, ldq, scales, lds, 1, c.sms,
                                           static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return call_fail_cuda(e, "quantization");
     call_count(1);
@@ -526,22 +526,24 @@ PG_EXPORT int sgemm_block_linear(int dtype, int64_t t, int64_t n, int64_t k, con
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const BlockPlan plan = plan_block(t, n, k, c.sms, c.force_bn, c.force_split);
     return with_workspace(c, st, [&](Arena& a) {
-        BlockProduct p{dtype, t, n, k, static_cast<const uint8_t*>(x), ldx, x_scales, ldxs, w, ldw, w_scales, ldws, bias,
+        BlockProduct p{dtype, t, n, k, static_cast<const uint8_t*>(x), ldx, x_scales, ldxs, 1, w, ldw, w_scales, ldws, bias,
                        act, residual, ldr, y, ldy};
         int launches = 0;
         if (k > 0 && x_scales == nullptr) {
-            const int64_t ldq = (k + 15) / 16 * 16, lds = blocks_of(k);
+            // scales of neighbouring rows side by side: the product's lanes are rows
+            const int64_t ldq = (k + 15) / 16 * 16;
             uint8_t* q = static_cast<uint8_t*>(a.take(static_cast<size_t>(t) * ldq));
-            float* scales = static_cast<float*>(a.take(static_cast<size_t>(t) * lds * 4));
+            float* scales = static_cast<float*>(a.take(static_cast<size_t>(t) * blocks_of(k) * 4));
             if (!a.dry()) {
-                const cudaError_t e = launch_quantize(dtype, t, k, 1, x, ldx, q, ldq, scales, lds, c.sms, st);
+                const cudaError_t e = launch_quantize(dtype, t, k, 1, x, ldx, q, ldq, scales, 1, t, c.sms, st);
                 if (e != cudaSuccess) return call_fail_cuda(e, "quantization");
                 ++launches;
             }
             p.x = q;
             p.ldx = ldq;
             p.x_scales = scales;
-            p.ldxs = lds;
+            p.xs_row = 1;
+            p.xs_block = t;
         } else if (k > 0) {
             PG_CHECK(place_bytes(c, p.x, p.ldx, t, k, a, st));
         }

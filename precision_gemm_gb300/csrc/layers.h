@@ -405,9 +405,10 @@ cudaError_t launch_combine_backward(int dtype, int64_t tokens, int top, int64_t 
                                     const void* x, int64_t ldx, const int32_t* rows, const int32_t* slots,
                                     const float* weights, void* dx, int64_t lddx, float* dweights, cudaStream_t st);
 
-// e4m3 values with a scale for each 1 x 128 (block_rows 1) or 128 x 128 of the matrix (block.cu).
+// e4m3 values with a scale for each 1 x 128 (block_rows 1) or 128 x 128 of the matrix (block.cu), the
+// scales s_row apart along rows and s_block along blocks of k (1 for 128 x 128).
 cudaError_t launch_quantize(int dtype, int64_t rows, int64_t cols, int block_rows, const void* x, int64_t ldx, uint8_t* q,
-                            int64_t ldq, float* scales, int64_t lds, int num_sms, cudaStream_t st);
+                            int64_t ldq, float* scales, int64_t s_row, int64_t s_block, int num_sms, cudaStream_t st);
 // Rows of bytes copied to 16-byte boundaries.
 cudaError_t launch_copy_bytes(const uint8_t* src, int64_t ld, int64_t rows, int64_t cols, uint8_t* dst, int64_t ldd,
                               int num_sms, cudaStream_t st);
@@ -419,7 +420,7 @@ struct BlockProduct {
     const uint8_t* x;
     int64_t ldx;
     const float* x_scales;
-    int64_t ldxs;
+    int64_t xs_row, xs_block;
     const uint8_t* w;
     int64_t ldw;
     const float* w_scales;

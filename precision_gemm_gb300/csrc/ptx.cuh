@@ -91,6 +91,17 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
     }
 }
 
+// The same for waits of a microsecond or less: the timer, whose first reading takes about as long,
+// is looked at only after kSpins tests.
+constexpr int kSpins = 64;
+__device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity, uint64_t timeout_ns,
+                                                const volatile int* abort_flag) {
+#pragma unroll 1
+    for (int i = 0; i < kSpins; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    return mbar_wait_bounded(bar, parity, timeout_ns, abort_flag);
+}
+
 // A warp's wait for a phase of `bar`: lane 0 alone polls (bounded); once it has
 // seen the phase complete, every lane runs its own wait, which then succeeds at
 // its first test and gives that lane the acquire ordering on the data the phase
@@ -273,10 +284,23 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t sr
                  : "memory");
 }
 
+// The same in a 3-D tensor.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int32_t x, int32_t y, int32_t z) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(src), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 
 // Wait until every committed bulk store has finished reading shared memory.
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+
+// Wait until every one of them but the last has.
+__device__ __forceinline__ void bulk_wait_read_all_but_one() {
+    asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+}
 
 // ---- tcgen05 -----------------------------------------------------------------------
 
@@ -340,12 +364,19 @@ __device__ __forceinline__ void tmem_wait_ld() {
 
 // The same, naming the registers that the loads before it fill: nothing that uses them moves ahead
 // of the wait.
-__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[16]) {
+template <int N>
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[N]) {
+    static_assert(N == 16 || N == 32, "one load's registers");
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
                    "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
                  :
                  : "memory");
+    if (N == 32)
+        asm volatile(""
+                     : "+r"(r[N - 16]), "+r"(r[N - 15]), "+r"(r[N - 14]), "+r"(r[N - 13]), "+r"(r[N - 12]),
+                       "+r"(r[N - 11]), "+r"(r[N - 10]), "+r"(r[N - 9]), "+r"(r[N - 8]), "+r"(r[N - 7]), "+r"(r[N - 6]),
+                       "+r"(r[N - 5]), "+r"(r[N - 4]), "+r"(r[N - 3]), "+r"(r[N - 2]), "+r"(r[N - 1]));
 }
 
 // 32 consecutive 32-bit columns of the warp's 32 TMEM lanes: thread t gets

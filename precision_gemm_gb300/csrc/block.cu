@@ -37,8 +37,9 @@ constexpr int kCols = 32;    // columns of a TMEM load
 // Registers per thread: 168 at launch, the most that 384 threads can have; 4 warps give theirs to 8.
 constexpr int kRegsFew = 56, kRegsMany = 224;
 static_assert(4 * kRegsFew + 8 * kRegsMany <= 12 * 168, "the shares must be there");
-constexpr int kScaleSlots = 8;  // blocks of k whose scales are ready or on their way
-constexpr int kOutBytes = 64;   // row of a box that results leave through
+constexpr int kScales = 4;      // blocks of k whose scales come together
+constexpr int kScaleSlots = 2;  // such groups ready or on their way
+constexpr int kOutBytes = 64;   // of each row of a warp's results, on their way out together
 constexpr int kGroupTiles = 8;
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -157,23 +158,25 @@ __global__ void __launch_bounds__(256) copy_bytes_kernel(const uint8_t* src, int
 template <int BN>
 struct Cfg {
     static constexpr int A_BYTES = kRows * kBlock;
-    static constexpr int B_BYTES = BN / 2 * kBlock;
+    static constexpr int B_BYTES = BN * kBlock;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-    static constexpr int STAGES_RAW = 184 * 1024 / STAGE_BYTES;
+    static constexpr int STAGES_RAW = 192 * 1024 / STAGE_BYTES;
     static constexpr int STAGES = STAGES_RAW > 10 ? 10 : STAGES_RAW;
-    static constexpr int BUFFERS = BN == 256 ? 2 : 4;  // of TMEM: blocks of k on their way
-    static constexpr uint32_t TMEM_COLS = BUFFERS * BN;
-    static constexpr int MINE = BN / 2;                // columns of an epilogue warp
-    static constexpr int BAR_BYTES = (2 * STAGES + 2 * BUFFERS + 2 * kScaleSlots + 1) * 8 + 16;
-    static constexpr int OUT_BYTES = kEpiWarps * 2 * 32 * kOutBytes;        // two boxes of 32 rows per warp
-    static constexpr int SCALE_BYTES = kScaleSlots * 2 * kRows * 4;         // of the rows, for each half of the columns
+    static constexpr int MINE = BN / 2;                // columns of an epilogue warp: a half of the tile's
+    static constexpr int BUFFERS = BN == 256 ? 2 : 4;  // of TMEM, for each half: blocks of k on their way
+    static constexpr uint32_t TMEM_COLS = 2 * BUFFERS * MINE;
+    static constexpr int HALF_BYTES = B_BYTES / 2;     // of w in a slot
+    static constexpr int BAR_BYTES = (2 * STAGES + 4 * BUFFERS + 2 * kScaleSlots + 1) * 8 + 16;
+    static constexpr int OUT_BYTES = kEpiWarps * 32 * kOutBytes;
+    static constexpr int SCALE_BYTES = kScaleSlots * 2 * kRows * kScales * 4;  // of the rows, for each half of the columns
     static constexpr size_t SMEM = 1024 + static_cast<size_t>(STAGES) * STAGE_BYTES + OUT_BYTES + SCALE_BYTES + BAR_BYTES;
-    static_assert(A_BYTES % 1024 == 0 && B_BYTES % 1024 == 0, "slots need 1 KiB alignment");
+    static_assert(A_BYTES % 1024 == 0 && HALF_BYTES % 1024 == 0, "slots need 1 KiB alignment");
 };
 
 struct Params {
     int32_t t, n, kbs;
-    int32_t tiles_t, tiles_n;
+    int32_t tiles_t, tiles_n;  // tiles of 256 rows, whose halves a pair of CTAs shares (paired), or of 128
+    int32_t paired;
     int32_t split, split_kb;
     const float* x_scales;
     int64_t xs_row, xs_block;  // strides along rows and along blocks of k
@@ -186,12 +189,16 @@ struct Params {
     void* y;
     int64_t ldy;
     int32_t vec;        // y, residual and bias in 16-byte accesses
-    int32_t tma_out;    // y leaves through the tensor map tmY (the slices' sums always do)
     float* part;        // slices' sums, [slice][t][ldp]
     int64_t ldp;
     uint64_t timeout_ns;
     int* status;
     int32_t debug_flags;
+};
+
+struct Rows {  // of a matrix
+    void* ptr;
+    int64_t ld;
 };
 
 // Eight columns from i on of row j: results of sums v (those past n are of no use).
@@ -221,35 +228,33 @@ __device__ __forceinline__ void store_result8(const Params& p, int64_t j, int64_
 
 template <int BN, typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    block_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
-                 const __grid_constant__ CUtensorMap tmY, const Params p) {
+    block_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, const Params p) {
     using C = Cfg<BN>;
     constexpr int S = C::STAGES, NB = C::BUFFERS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = align_smem_1024(smem_raw);
-    float* scale_ring = reinterpret_cast<float*>(smem + S * C::STAGE_BYTES + C::OUT_BYTES);  // [slot][half][row]
+    float4* scale_ring = reinterpret_cast<float4*>(smem + S * C::STAGE_BYTES + C::OUT_BYTES);  // [slot][half][row]
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S * C::STAGE_BYTES + C::OUT_BYTES + C::SCALE_BYTES);
-    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 2 * S + 2 * NB + 2 * kScaleSlots + 1);
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 2 * S + 4 * NB + 2 * kScaleSlots + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
     const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + S);
-    const uint32_t acc_full0 = smem_u32(bars + 2 * S), acc_empty0 = smem_u32(bars + 2 * S + NB);
-    const uint32_t scale_full0 = smem_u32(bars + 2 * S + 2 * NB), scale_empty0 = scale_full0 + 8 * kScaleSlots;
+    const uint32_t acc_full0 = smem_u32(bars + 2 * S), acc_empty0 = smem_u32(bars + 2 * S + 2 * NB);  // [half][buffer]
+    const uint32_t scale_full0 = smem_u32(bars + 2 * S + 4 * NB), scale_empty0 = scale_full0 + 8 * kScaleSlots;
     const uint32_t mma_done = scale_empty0 + 8 * kScaleSlots;
 
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);  // known to be uniform
     const int lane = threadIdx.x & 31;
     const uint32_t rank = __shfl_sync(0xffffffffu, cluster_rank(), 0);
-    const bool leader = rank == 0;
-    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const int first = p.paired ? blockIdx.x >> 1 : blockIdx.x, step = p.paired ? gridDim.x >> 1 : gridDim.x;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
             mbar_init(full0 + 8 * s, 1);
-            mbar_init(empty0 + 8 * s, 1);
+            mbar_init(empty0 + 8 * s, p.paired ? 2 : 1);
         }
-        for (int b = 0; b < NB; ++b) {
+        for (int b = 0; b < 2 * NB; ++b) {
             mbar_init(acc_full0 + 8 * b, 1);
-            mbar_init(acc_empty0 + 8 * b, 2 * kEpiWarps);
+            mbar_init(acc_empty0 + 8 * b, kEpiWarps / 2);
         }
         for (int b = 0; b < kScaleSlots; ++b) {
             mbar_init(scale_full0 + 8 * b, 1);
@@ -260,15 +265,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         fence_mbar_init();
     }
     if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_holder)),
-                     "r"(C::TMEM_COLS)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        tmem_alloc(smem_u32(tmem_holder), C::TMEM_COLS);
+        tmem_relinquish();
     }
     pdl_wait();
     tc_fence_before_sync();
     __syncthreads();
-    cluster_sync_all();  // every CTA's barriers and TMEM exist before any cross-CTA traffic
+    cluster_sync_all();  // every CTA's barriers exist before any cross-CTA traffic
     tc_fence_after_sync();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_holder, 0);
     const int units = p.tiles_t * p.tiles_n * p.split;
@@ -282,7 +285,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         x.slice = u - tile * p.split;
         int tt, tn;
         tile_coords(tile, p.tiles_t, p.tiles_n, kGroupTiles, tt, tn);
-        x.j0 = tt * (2 * kRows);
+        x.j0 = p.paired ? tt * (2 * kRows) + kRows * static_cast<int>(rank) : tt * kRows;
         x.i0 = tn * BN;
         x.kb0 = x.slice * p.split_kb;
         x.nkb = max(min(x.kb0 + p.split_kb, p.kbs) - x.kb0, 0);
@@ -292,29 +295,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
         if (warp == 0) {
-            // ---------------- TMA loader (both CTAs) ----------------
+            // ---------------- TMA loader ----------------
             if (!(p.debug_flags & 1)) {
-                const uint32_t full_leader0 = map_to_rank(full0, 0);
                 int it = 0, slot_i = 0;
                 uint32_t phase = 1;
                 bool ok = true;
-                for (int u = pair; u < units && ok; u += pairs) {
+                for (int u = first; u < units && ok; u += step) {
                     const Unit x = unit_of(u);
-                    const int ja = __shfl_sync(0xffffffffu, x.j0 + kRows * static_cast<int>(rank), 0);
-                    const int ib = __shfl_sync(0xffffffffu, x.i0 + BN / 2 * static_cast<int>(rank), 0);
+                    const int ja = __shfl_sync(0xffffffffu, x.j0, 0), ib = __shfl_sync(0xffffffffu, x.i0, 0);
                     const int kb0 = __shfl_sync(0xffffffffu, x.kb0, 0), nkb = __shfl_sync(0xffffffffu, x.nkb, 0);
                     for (int kb = 0; kb < nkb; ++kb, ++it) {
-                        ok = __all_sync(0xffffffffu,
-                                        mbar_wait_short(empty0 + 8 * slot_i, phase, p.timeout_ns, abort_flag));
+                        ok = mbar_wait_short_warp(empty0 + 8 * slot_i, phase, p.timeout_ns, abort_flag);
                         if (!ok) {
                             if (lane == 0) raise_abort(abort_flag, p.status);
                             break;
                         }
-                        if (leader && lane == 0) mbar_arrive_expect_tx(full0 + 8 * slot_i, 2 * C::STAGE_BYTES);
-                        const uint32_t bar = full_leader0 + 8 * slot_i;
+                        const uint32_t bar = full0 + 8 * slot_i;
+                        if (lane == 0) mbar_arrive_expect_tx(bar, C::STAGE_BYTES);
                         const uint32_t slot = smem_u32(smem) + slot_i * C::STAGE_BYTES;
-                        tma_load_3d_pair_warp(slot, &tmX, (kb0 + kb) * kBlock, ja, 0, bar);
-                        tma_load_3d_pair_warp(slot + C::A_BYTES, &tmW, (kb0 + kb) * kBlock, ib, 0, bar);
+                        const uint32_t w_slot = slot + C::A_BYTES + C::HALF_BYTES * rank;
+                        const int k0 = (kb0 + kb) * kBlock;
+                        tma_load_3d_warp(slot, &tmX, k0, ja, 0, bar);
+                        if (p.paired) {  // each CTA brings half of w's rows for both
+                            tma_load_3d_multicast_warp(w_slot, &tmW, k0, ib + C::MINE * static_cast<int>(rank), 0, bar, 3);
+                        } else {
+                            tma_load_3d_warp(slot + C::A_BYTES, &tmW, k0, ib, 0, bar);
+                            tma_load_3d_warp(slot + C::A_BYTES + C::HALF_BYTES, &tmW, k0, ib + C::MINE, 0, bar);
+                        }
                         if (++slot_i == S) {
                             slot_i = 0;
                             phase ^= 1;
@@ -322,95 +329,103 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (lane == 0) pdl_trigger();
-                if (leader && lane == 0) {
-                    // Let every copy of the pair land before the CTAs may retire (CTA 0's full barriers
-                    // count both CTAs' bytes).
+                if (lane == 0) {
+                    // Let every copy land before the CTA may retire, the other CTA's among them.
                     for (int q = max(0, it - S); q < it; ++q)
                         mbar_wait_bounded(full0 + 8 * (q % S), (q / S) & 1, p.timeout_ns, nullptr);
+                    // ... and the other CTA's releases of the slots, which arrive in this one's barriers.
+                    for (int q = max(0, it - S); q < it && p.paired && ok; ++q)
+                        ok = mbar_wait_bounded(empty0 + 8 * (q % S), (q / S) & 1, p.timeout_ns, abort_flag);
                 }
             }
             __syncwarp();
         } else if (warp == 1) {
-            // ---------------- MMA issuer (CTA 0 of the pair) ----------------
-            if (leader) {
-                const uint32_t slot0 = smem_u32(smem);
-                const uint64_t a_desc0 = smem_desc(slot0, 16, 1024, kSwizzle128B);
-                const uint64_t b_desc0 = smem_desc(slot0 + C::A_BYTES, 16, 1024, kSwizzle128B);
-                const uint32_t idesc = idesc_e4m3(2 * kRows, BN);
-                int slot_i = 0, buf = 0;
-                uint32_t phase = 0, acc_phase = 1;
-                bool ok = true;
-                for (int u = pair; u < units && ok; u += pairs) {
-                    const int nkb = __shfl_sync(0xffffffffu, unit_of(u).nkb, 0);
-                    for (int kb = 0; kb < nkb; ++kb) {
-                        ok = __all_sync(0xffffffffu, mbar_wait_short(acc_empty0 + 8 * buf, acc_phase, p.timeout_ns, abort_flag)) &&
-                             __all_sync(0xffffffffu, mbar_wait_short(full0 + 8 * slot_i, phase, p.timeout_ns, abort_flag));
+            // ---------------- MMA issuer ----------------
+            const uint32_t slot0 = smem_u32(smem);
+            const uint64_t a_desc0 = smem_desc(slot0, 16, 1024, kSwizzle128B);
+            const uint64_t b_desc0 = smem_desc(slot0 + C::A_BYTES, 16, 1024, kSwizzle128B);
+            const uint32_t idesc = idesc_e4m3(kRows, C::MINE);
+            int slot_i = 0, buf = 0;
+            uint32_t phase = 0, acc_phase = 1;
+            bool ok = true;
+            for (int u = first; u < units && ok; u += step) {
+                const int nkb = __shfl_sync(0xffffffffu, unit_of(u).nkb, 0);
+                for (int kb = 0; kb < nkb; ++kb) {
+                    ok = mbar_wait_short_warp(full0 + 8 * slot_i, phase, p.timeout_ns, abort_flag);
+                    const uint32_t o = static_cast<uint32_t>(slot_i * C::STAGE_BYTES) >> 4;
+                    // The halves' accumulators come and go by themselves, so that a buffer is filled while the
+                    // other half's is, not both halves', before it can be drained.
+#pragma unroll
+                    for (int h = 0; h < 2 && ok; ++h) {
+                        const int b = NB * h + buf;
+                        ok = mbar_wait_short_warp(acc_empty0 + 8 * b, acc_phase, p.timeout_ns, abort_flag);
                         if (!ok) break;
                         tc_fence_after_sync();
-                        const uint32_t o = static_cast<uint32_t>(slot_i * C::STAGE_BYTES) >> 4;
-    #pragma unroll
+#pragma unroll
                         for (int kk = 0; kk < kBlock / 32; ++kk)
-                            mma_e4m3_pair_warp(tmem + buf * BN, a_desc0 + (o + 2 * kk), b_desc0 + (o + 2 * kk), idesc, kk > 0);
-                        mma_commit_pair_warp(empty0 + 8 * slot_i);
-                        mma_commit_pair_warp(acc_full0 + 8 * buf);
-                        if (++slot_i == S) {
-                            slot_i = 0;
-                            phase ^= 1;
-                        }
-                        if (++buf == NB) {
-                            buf = 0;
-                            acc_phase ^= 1;
-                        }
+                            mma_e4m3_warp(tmem + b * C::MINE, a_desc0 + (o + 2 * kk),
+                                               b_desc0 + (o + (C::HALF_BYTES >> 4) * h + 2 * kk), idesc, kk > 0);
+                        mma_commit_warp(acc_full0 + 8 * b);
+                    }
+                    if (!ok) break;
+                    if (p.paired)
+                        mma_commit_multicast_warp(empty0 + 8 * slot_i, 3);
+                    else
+                        mma_commit_warp(empty0 + 8 * slot_i);
+                    if (++slot_i == S) {
+                        slot_i = 0;
+                        phase ^= 1;
+                    }
+                    if (++buf == NB) {
+                        buf = 0;
+                        acc_phase ^= 1;
                     }
                 }
-                if (!ok && lane == 0) raise_abort(abort_flag, p.status);
-                mma_commit_pair_local_warp(mma_done);  // every MMA issued here has completed
-                mbar_wait_bounded(mma_done, 0, p.timeout_ns, nullptr);
             }
+            if (!ok && lane == 0) raise_abort(abort_flag, p.status);
+            mma_commit_warp(mma_done);  // every MMA issued here has completed
+            mbar_wait_bounded(mma_done, 0, p.timeout_ns, nullptr);
             __syncwarp();
         } else if (warp == 2) {
-            // ---------------- scales (both CTAs) ----------------
+            // ---------------- scales ----------------
             // sx sw of this CTA's rows and each half of the columns, several blocks of k ahead of their use
             int slot = 0;
             uint32_t phase = 1;
             bool ok = true;
-            for (int u = pair; u < units && ok; u += pairs) {
+            for (int u = first; u < units && ok; u += step) {
                 const Unit x = unit_of(u);
-                const int j0 = x.j0 + kRows * static_cast<int>(rank) + lane;
+                const int j0 = x.j0 + lane;
                 const float *sx[4], *sw[2];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) sx[r] = p.x_scales + min(j0 + 32 * r, p.t - 1) * p.xs_row + x.kb0 * p.xs_block;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) sw[h] = p.w_scales + min(x.i0 + C::MINE * h, p.n - 1) / kBlock * p.ldws + x.kb0;
-                constexpr int U = 2;  // blocks whose loads are in flight together
-                for (int kb = 0; kb < x.nkb && ok; kb += U) {
-                    float a[U][4], b[U][2];
+                for (int kb = 0; kb < x.nkb && ok; kb += kScales) {
+                    float a[4][kScales], b[2][kScales];
 #pragma unroll
-                    for (int d = 0; d < U; ++d) {
+                    for (int d = 0; d < kScales; ++d) {
                         const int at = min(kb + d, x.nkb - 1);
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) a[d][r] = __ldg(sx[r] + at * p.xs_block);
+                        for (int r = 0; r < 4; ++r) a[r][d] = __ldg(sx[r] + at * p.xs_block);
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) b[d][h] = __ldg(sw[h] + at);
+                        for (int h = 0; h < 2; ++h) b[h][d] = __ldg(sw[h] + at);
+                    }
+                    ok = mbar_wait_short_warp(scale_empty0 + 8 * slot, phase, p.timeout_ns, abort_flag);
+                    if (!ok) {
+                        if (lane == 0) raise_abort(abort_flag, p.status);
+                        break;
                     }
 #pragma unroll
-                    for (int d = 0; d < U; ++d) {
-                        if (kb + d >= x.nkb) break;
-                        ok = __all_sync(0xffffffffu, mbar_wait_short(scale_empty0 + 8 * slot, phase, p.timeout_ns, abort_flag));
-                        if (!ok) {
-                            if (lane == 0) raise_abort(abort_flag, p.status);
-                            break;
-                        }
+                    for (int h = 0; h < 2; ++h)
 #pragma unroll
-                        for (int h = 0; h < 2; ++h)
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) scale_ring[(2 * slot + h) * kRows + 32 * r + lane] = a[d][r] * b[d][h];
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(scale_full0 + 8 * slot);
-                        if (++slot == kScaleSlots) {
-                            slot = 0;
-                            phase ^= 1;
-                        }
+                        for (int r = 0; r < 4; ++r)
+                            scale_ring[(2 * slot + h) * kRows + 32 * r + lane] =
+                                make_float4(a[r][0] * b[h][0], a[r][1] * b[h][1], a[r][2] * b[h][2], a[r][3] * b[h][3]);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(scale_full0 + 8 * slot);
+                    if (++slot == kScaleSlots) {
+                        slot = 0;
+                        phase ^= 1;
                     }
                 }
             }
@@ -418,26 +433,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMany));
-        // ---------------- promotion and epilogue (warps 4..11, both CTAs) ----------------
+        // ---------------- promotion and epilogue (warps 4..11) ----------------
         const int q = warp & 3;            // TMEM lane quarter this warp may access
         const int half = (warp - 4) >> 2;  // its half of the columns
-        const uint32_t acc_empty_leader0 = map_to_rank(acc_empty0, 0);
-        const uint32_t base = tmem + (static_cast<uint32_t>(32 * q) << 16) + C::MINE * half;
-        uint8_t* out = smem + S * C::STAGE_BYTES + (warp - 4) * (2 * 32 * kOutBytes);
-        int boxes = 0;  // sent on their way
+        const uint32_t my_empty0 = acc_empty0 + 8 * NB * half;
+        const uint32_t base = tmem + (static_cast<uint32_t>(32 * q) << 16) + NB * C::MINE * half;
+        const uint32_t my_full0 = acc_full0 + 8 * NB * half;
+        uint8_t* out = smem + S * C::STAGE_BYTES + (warp - 4) * (32 * kOutBytes);
+        const bool one = lane == 0;
         auto free_buffer = [&](int b) {
             tc_fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive_remote_relaxed(acc_empty_leader0 + 8 * b);
+            mbar_arrive_if(one, my_empty0 + 8 * b);
         };
         int buf = 0;
         uint32_t acc_phase = 0;
         bool ok = true;
         int slot = 0;
         uint32_t scale_phase = 0;
-        for (int u = pair; u < units && ok; u += pairs) {
+        for (int u = first; u < units && ok; u += step) {
             const Unit x = unit_of(u);
-            const int row0 = x.j0 + kRows * static_cast<int>(rank) + 32 * q;
+            const int row0 = x.j0 + 32 * q;
             const int64_t j = row0 + lane;
             const int i0 = x.i0 + C::MINE * half;
             const bool there = row0 < p.t && i0 < p.n;  // of the warp
@@ -450,52 +466,89 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int c = 0; c < C::MINE / 2; ++c) acc[c] = make_float2(0.0f, 0.0f);
             int last = 0;  // the buffer of the last block, which the results go through
-            for (int kb = 0; kb < x.nkb; ++kb) {
-                ok = __all_sync(0xffffffffu, mbar_wait_short(scale_full0 + 8 * slot, scale_phase, p.timeout_ns, abort_flag));
-                const float s = scale_ring[(2 * slot + half) * kRows + 32 * q + lane];
-                ok = ok && __all_sync(0xffffffffu, mbar_wait_short(acc_full0 + 8 * buf, acc_phase, p.timeout_ns, abort_flag));
-                if (!ok) {
-                    if (lane == 0) raise_abort(abort_flag, p.status);
-                    break;
-                }
-                tc_fence_after_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(scale_empty0 + 8 * slot);
-                if (there) {
-                    const float2 scale = both(s);
-                    const uint32_t at = base + buf * BN;
-                    uint32_t v[2][kCols];
-                    tmem_ld_32x32b_x32(at, v[0]);
+            float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);  // scales of the next blocks
+            // A block's sums come in chunks of 32 columns, two on their way at a time; while the last two are
+            // added, the next block's first two are asked for, if its barrier (tested before) lets them.
+            constexpr int CHUNKS = C::MINE / kCols;
+            uint32_t v[2][kCols];
+            float2 scale = make_float2(0.0f, 0.0f);
+            auto add_chunk = [&](int c) {
 #pragma unroll
-                    for (int c = 0; c < C::MINE / kCols; ++c) {
-                        tmem_wait_ld(v[c & 1]);
-                        if (c + 1 < C::MINE / kCols)
-                            tmem_ld_32x32b_x32(at + kCols * (c + 1), v[(c + 1) & 1]);
-                        else if (kb + 1 < x.nkb)
-                            free_buffer(buf);
-#pragma unroll
-                        for (int k = 0; k < kCols / 2; ++k)
-                            acc[kCols / 2 * c + k] =
-                                fma2(make_float2(__uint_as_float(v[c & 1][2 * k]), __uint_as_float(v[c & 1][2 * k + 1])),
-                                     scale, acc[kCols / 2 * c + k]);
-                    }
-                } else if (kb + 1 < x.nkb) {
-                    free_buffer(buf);
-                }
-                last = buf;
+                for (int k = 0; k < kCols / 2; ++k)
+                    acc[kCols / 2 * c + k] =
+                        fma2(make_float2(__uint_as_float(v[c & 1][2 * k]), __uint_as_float(v[c & 1][2 * k + 1])), scale,
+                             acc[kCols / 2 * c + k]);
+            };
+            auto advance = [&]() {  // to the next buffer
                 if (++buf == NB) {
                     buf = 0;
                     acc_phase ^= 1;
                 }
-                if (++slot == kScaleSlots) {
-                    slot = 0;
-                    scale_phase ^= 1;
+            };
+            if (x.nkb > 0) {
+                ok = mbar_wait_short_warp(my_full0 + 8 * buf, acc_phase, p.timeout_ns, abort_flag);
+                tc_fence_after_sync();
+                if (ok && there) {
+                    tmem_ld_32x32b_x32(base + buf * C::MINE, v[0]);
+                    if (CHUNKS > 1) tmem_ld_32x32b_x32(base + buf * C::MINE + kCols, v[1]);
                 }
             }
-            if (!ok) break;
+#pragma unroll 1
+            for (int kb = 0; kb < x.nkb && ok; ++kb) {
+                if (kb % kScales == 0) {
+                    ok = mbar_wait_short_warp(scale_full0 + 8 * slot, scale_phase, p.timeout_ns, abort_flag);
+                    if (!ok) break;
+                    s = scale_ring[(2 * slot + half) * kRows + 32 * q + lane];
+                    __syncwarp();
+                    mbar_arrive_if(one, scale_empty0 + 8 * slot);
+                    if (++slot == kScaleSlots) {
+                        slot = 0;
+                        scale_phase ^= 1;
+                    }
+                }
+                scale = both(s.x);
+                s = make_float4(s.y, s.z, s.w, 0.0f);
+                last = buf;
+                const bool more = kb + 1 < x.nkb;
+                if (!there) {
+                    if (more) free_buffer(buf);
+                    advance();
+                    if (more) ok = mbar_wait_short_warp(my_full0 + 8 * buf, acc_phase, p.timeout_ns, abort_flag);
+                    continue;
+                }
+                const uint32_t at = base + buf * C::MINE;
+                tmem_wait_ld(v[0]);
+                if (CHUNKS > 1) tmem_wait_ld(v[1]);
+#pragma unroll
+                for (int c = 0; c + 2 < CHUNKS; ++c) {
+                    add_chunk(c);
+                    tmem_ld_32x32b_x32(at + kCols * (c + 2), v[c & 1]);
+                }
+                advance();
+                const bool ready = more && mbar_try_wait(my_full0 + 8 * buf, acc_phase);
+                if (CHUNKS > 2) {
+                    tmem_wait_ld(v[0]);
+                    tmem_wait_ld(v[1]);
+                }
+                if (more) free_buffer(last);
+                if (CHUNKS > 1) add_chunk(CHUNKS - 2);
+                else add_chunk(0);
+                if (more) {
+                    ok = __all_sync(0xffffffffu, ready) ||
+                         mbar_wait_short_warp(my_full0 + 8 * buf, acc_phase, p.timeout_ns, abort_flag);
+                    tc_fence_after_sync();
+                    if (ok) tmem_ld_32x32b_x32(base + buf * C::MINE, v[0]);
+                }
+                if (CHUNKS > 1) add_chunk(CHUNKS - 1);
+                if (CHUNKS > 1 && more && ok) tmem_ld_32x32b_x32(base + buf * C::MINE + kCols, v[1]);
+            }
+            if (!ok) {
+                if (lane == 0) raise_abort(abort_flag, p.status);
+                break;
+            }
             // The results go back to the warp's own columns of the last buffer and from there, 16 at a
             // time, through the epilogue: a loop, where registers would want it written out.
-            const uint32_t at = base + last * BN;
+            const uint32_t at = base + last * C::MINE;
             if (there) {
 #pragma unroll
                 for (int c = 0; c < C::MINE / kCols; ++c) {
@@ -509,66 +562,64 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     tmem_st_32x32b_x32(at + kCols * c, v);
                 }
                 tmem_wait_st();
-                // The columns as elements TO, a box of 64 bytes of 32 rows at a time, through shared memory (the
-                // 64-byte swizzle) and TMA where the result's rows allow it.
-                auto emit = [&](auto element, bool tma, int z, auto results) {
+                // The columns as elements TO, 64 bytes of 32 rows at a time.  They change places in shared memory
+                // (16-byte words, swizzled so that eight rows' words fall on all banks), so that four lanes write
+                // a row's 64 bytes together.
+                auto emit = [&](auto element, Rows rows_of, bool vec, auto results) {
                     using TO = decltype(element);
-                    constexpr int BOX = kOutBytes / static_cast<int>(sizeof(TO)), N = static_cast<int>(sizeof(TO)) / 2;
+                    constexpr int SPAN = kOutBytes / static_cast<int>(sizeof(TO)), N = static_cast<int>(sizeof(TO)) / 2;
+                    TO* const to = static_cast<TO*>(rows_of.ptr);
 #pragma unroll 1
-                    for (int c = 0; c < C::MINE && i0 + c < p.n; c += BOX) {
-                        uint32_t v[BOX];
+                    for (int c = 0; c < C::MINE && i0 + c < p.n; c += SPAN) {
+                        uint32_t v[SPAN];
                         __syncwarp();
-                        if constexpr (BOX == 32)
+                        if constexpr (SPAN == 32)
                             tmem_ld_32x32b_x32(at + c, v);
                         else
                             tmem_ld_32x32b_x16(at + c, v);
-                        uint8_t* box = out + (boxes & 1) * (32 * kOutBytes);
-                        if (tma) {
-                            if (lane == 0) bulk_wait_read_all_but_one();  // the box before the last one is read
-                            __syncwarp();
-                        }
                         tmem_wait_ld(v);
+                        const bool whole = vec && i0 + c + SPAN <= p.n;
 #pragma unroll
-                        for (int h = 0; h < BOX; h += 8) {
+                        for (int h = 0; h < SPAN; h += 8) {
                             float f[8];
 #pragma unroll
                             for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(v[h + k]);
                             if (j < p.t) results(c + h, f);
-                            if (tma) {
+                            if (whole) {
                                 TO e[8];
 #pragma unroll
                                 for (int k = 0; k < 8; ++k) e[k] = from_float<TO>(f[k]);
 #pragma unroll
                                 for (int k = 0; k < N; ++k)  // N 16-byte words of eight elements
-                                    *reinterpret_cast<uint4*>(box + kOutBytes * lane + 16 * ((h / 8 * N + k) ^ ((lane >> 1) & 3))) =
+                                    *reinterpret_cast<uint4*>(out + kOutBytes * lane + 16 * ((h / 8 * N + k) ^ ((lane >> 1) & 3))) =
                                         reinterpret_cast<const uint4*>(e)[k];
                             } else if (j < p.t) {
-                                store_result8<TO>(p, j, i0 + c + h, f);
+                                const int valid = static_cast<int>(min(p.n - (i0 + c + h), 8));
+                                if (valid > 0) store8(to + j * rows_of.ld + i0 + c + h, vec, valid, f);
                             }
                         }
-                        if (tma) {
-                            fence_proxy_async_smem();
+                        if (whole) {
                             __syncwarp();
-                            if (lane == 0) {
-                                tma_store_3d(&tmY, smem_u32(box), i0 + c, row0, z);
-                                bulk_commit();
+#pragma unroll
+                            for (int r = 0; r < 32; r += 8) {
+                                const int row = r + lane / 4;
+                                const uint4 w = *reinterpret_cast<const uint4*>(out + kOutBytes * row + 16 * ((lane & 3) ^ ((row >> 1) & 3)));
+                                if (row0 + row < p.t)
+                                    *(reinterpret_cast<uint4*>(to + (row0 + row) * rows_of.ld + i0 + c) + (lane & 3)) = w;
                             }
-                            ++boxes;
                         }
                     }
                 };
                 if (p.part)
-                    emit(float(), true, x.slice, [](int, float(&)[8]) {});
+                    emit(float(), {p.part + static_cast<int64_t>(x.slice) * p.t * p.ldp, p.ldp}, true, [](int, float(&)[8]) {});
                 else
                     with_act(p.act, [&](auto act) {
-                        emit(T(), p.tma_out != 0, 0,
+                        emit(T(), {p.y, p.ldy}, p.vec != 0,
                              [&](int c, float(&f)[8]) { result8<T, decltype(act)::value>(p, j, i0 + c, f); });
                     });
             }
             if (x.nkb > 0) free_buffer(last);
         }
-        if (lane == 0) bulk_wait_read();  // the boxes must stay until they are read
-        __syncwarp();
     }
 
     tc_fence_before_sync();
@@ -576,8 +627,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     cluster_sync_all();  // no CTA leaves while its peer may still read its shared memory or barriers
     if (warp == 1) {
         tc_fence_after_sync();
-        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM_COLS)
-                     : "memory");
+        tmem_dealloc(tmem, C::TMEM_COLS);
     }
 }
 
@@ -602,7 +652,7 @@ __global__ void __launch_bounds__(256) block_sum_kernel(const Params p) {
 }
 
 template <int BN, typename T>
-cudaError_t run(const CUtensorMap (&m)[3], const Params& p, int num_sms, cudaStream_t st) {
+cudaError_t run(const CUtensorMap (&m)[2], const Params& p, int num_sms, cudaStream_t st) {
     using C = Cfg<BN>;
     auto kern = block_kernel<BN, T>;
     static std::atomic<uint64_t> smem_set{0};
@@ -611,8 +661,9 @@ cudaError_t run(const CUtensorMap (&m)[3], const Params& p, int num_sms, cudaStr
     static std::atomic<int> resident[64];
     const int most = resident_pairs(reinterpret_cast<const void*>(kern), kThreads, C::SMEM, num_sms, resident);
     const int64_t units = static_cast<int64_t>(p.tiles_t) * p.tiles_n * p.split;
-    return launch_kernel(true, kern, dim3(static_cast<unsigned>(2 * std::min<int64_t>(units, most))), dim3(kThreads),
-                         C::SMEM, st, m[0], m[1], m[2], p);
+    const int64_t clusters = std::min<int64_t>(p.paired ? units : cdiv(units, 2), most);
+    return launch_kernel(true, kern, dim3(static_cast<unsigned>(2 * clusters)), dim3(kThreads),
+                         C::SMEM, st, m[0], m[1], p);
 }
 
 }  // namespace
@@ -643,18 +694,19 @@ cudaError_t launch_copy_bytes(const uint8_t* src, int64_t ld, int64_t rows, int6
 }
 
 BlockPlan plan_block(int64_t t, int64_t n, int64_t k, int num_sms, int force_bn, int force_split) {
-    const int pairs = std::max(num_sms / 2, 1);
+    const bool paired = t > kRows;
+    const int at_once = std::max(paired ? num_sms / 2 : num_sms, 1);
     const int64_t kb = cdiv(k, kBlock);
     BlockPlan best{};
     double best_us = 0.0;
     for (int bn : {256, 128, 64}) {
         if (force_bn && force_bn <= 256 && bn != force_bn) continue;
         const double step = bn == 256 ? 0.36 : (bn == 128 ? 0.20 : 0.15), end = bn == 256 ? 4.0 : (bn == 128 ? 2.5 : 1.5);
-        const int64_t tiles = cdiv(t, 2 * kRows) * cdiv(n, bn);
+        const int64_t tiles = cdiv(t, paired ? 2 * kRows : kRows) * cdiv(n, bn);
         for (int64_t want = 1; want <= std::max<int64_t>(kb, 1); ++want) {
-            if (force_split ? want != std::min<int64_t>(force_split, std::max<int64_t>(kb, 1)) : want > 1 && tiles * want > 3 * pairs) continue;
+            if (force_split ? want != std::min<int64_t>(force_split, std::max<int64_t>(kb, 1)) : want > 1 && tiles * want > 3 * at_once) continue;
             const int64_t split_kb = std::max<int64_t>(cdiv(kb, want), 1), split = std::max<int64_t>(cdiv(kb, split_kb), 1);
-            const double us = static_cast<double>(cdiv(tiles * split, pairs)) * (split_kb * step + end) +
+            const double us = static_cast<double>(cdiv(tiles * split, at_once)) * (split_kb * step + end) +
                               (split > 1 ? 2.5 + 1e-6 * split * t * n * 4 * 0.3 : 0.0);
             if (best.bn == 0 || us < best_us) {
                 best_us = us;
@@ -672,7 +724,8 @@ int launch_block(const CallContext& c, const BlockProduct& b, const BlockPlan& p
     p.t = static_cast<int32_t>(b.t);
     p.n = static_cast<int32_t>(b.n);
     p.kbs = static_cast<int32_t>(cdiv(b.k, kBlock));
-    p.tiles_t = static_cast<int32_t>(cdiv(b.t, 2 * kRows));
+    p.paired = b.t > kRows;
+    p.tiles_t = static_cast<int32_t>(cdiv(b.t, p.paired ? 2 * kRows : kRows));
     p.tiles_n = static_cast<int32_t>(cdiv(b.n, plan.bn));
     p.split = plan.split;
     p.split_kb = plan.split_kb;
@@ -696,17 +749,11 @@ int launch_block(const CallContext& c, const BlockProduct& b, const BlockPlan& p
     p.timeout_ns = c.timeout_ns;
     p.status = c.status;
     p.debug_flags = c.debug_flags;
-    CUtensorMap m[3] = {};
-    int rc;
+    CUtensorMap m[2] = {};
     if (b.k > 0) {
-        if ((rc = call_encode_3d(&m[0], 1, b.x, b.k, b.t, b.ldx, 1, 0, kBlock, kRows))) return rc;
-        if ((rc = call_encode_3d(&m[1], 1, b.w, b.k, b.n, b.ldw, 1, 0, kBlock, static_cast<uint32_t>(plan.bn / 2)))) return rc;
-    }
-    if (p.part) {
-        if ((rc = call_encode_3d(&m[2], 4, p.part, b.n, b.t, p.ldp, plan.split, b.t * p.ldp, kOutBytes, 32))) return rc;
-    } else if (aligned(b.y, b.ldy)) {
-        p.tma_out = 1;
-        if ((rc = call_encode_3d(&m[2], b.dtype == SGEMM_F32 ? 4 : 2, b.y, b.n, b.t, b.ldy, 1, 0, kOutBytes, 32))) return rc;
+        int rc;
+        if ((rc = call_encode_u8(&m[0], b.x, b.k, b.t, b.ldx, kRows))) return rc;
+        if ((rc = call_encode_u8(&m[1], b.w, b.k, b.n, b.ldw, static_cast<uint32_t>(plan.bn / 2)))) return rc;
     }
     auto go = [&](auto zero) {
         using T = decltype(zero);

@@ -168,10 +168,8 @@ void call_count(int launches);
 // elements outside read as zero.
 int call_encode_bf16(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, int64_t ld, int64_t z,
                      int64_t stride, uint32_t box_cols, uint32_t box_rows);
-// The same as a 3-D map of elements of 1 (bytes), 2 (bfloat16) or 4 bytes (float), boxes of box_rows
-// rows of 128 or 64 bytes in the swizzle of that width.
-int call_encode_3d(CUtensorMap* map, int bytes, const void* base, int64_t cols, int64_t rows, int64_t ld, int64_t z,
-                   int64_t stride, int box_bytes, uint32_t box_rows);
+// The same of bytes, one matrix as a 3-D map, boxes of box_rows rows of 128.
+int call_encode_u8(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, int64_t ld, uint32_t box_rows);
 
 // Device status values written by kernels (match SGEMM_ERR_* of the ABI).
 constexpr int kStatusTimeout = 4;

@@ -1335,7 +1335,7 @@ int call_fail_cuda(cudaError_t e, const char* what) { return fail_cuda(e, what);
 
 void call_count(int launches) { g_launches += launches; }
 
-// bytes: 1, 2 (bfloat16) or 4 (float)
+// bytes: 2 (bfloat16) or 1
 static int encode_swizzled(CUtensorMap* map, int bytes, const void* base, int64_t cols, int64_t rows, int64_t ld,
                            int64_t z, int64_t stride, uint32_t box_cols, uint32_t box_rows) {
     EncodeTiledFn fn = encode_fn();
@@ -1349,12 +1349,8 @@ static int encode_swizzled(CUtensorMap* map, int bytes, const void* base, int64_
                                    static_cast<cuuint64_t>(z > 1 ? stride : ld * rows) * bytes};
     const cuuint32_t box[3] = {box_cols, box_rows, 1};
     const cuuint32_t elem[3] = {1, 1, 1};
-    const CUtensorMapDataType type = bytes == 2   ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                     : bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
-                                                  : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
-    const CUresult r = fn(map, type, z > 0 ? 3 : 2, const_cast<void*>(base), dims, strides,
-                          box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          box_cols * static_cast<uint32_t>(bytes) == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+    const CUresult r = fn(map, bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, z > 0 ? 3 : 2, const_cast<void*>(base), dims, strides,
+                          box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS)
         return fail(SGEMM_ERR_TENSOR_MAP,
@@ -1367,10 +1363,8 @@ int call_encode_bf16(CUtensorMap* map, const void* base, int64_t cols, int64_t r
                      int64_t stride, uint32_t box_cols, uint32_t box_rows) {
     return encode_swizzled(map, 2, base, cols, rows, ld, z, stride, box_cols, box_rows);
 }
-int call_encode_3d(CUtensorMap* map, int bytes, const void* base, int64_t cols, int64_t rows, int64_t ld, int64_t z,
-                   int64_t stride, int box_bytes, uint32_t box_rows) {
-    return encode_swizzled(map, bytes, base, cols, rows, ld, z, stride, static_cast<uint32_t>(box_bytes / bytes),
-                           box_rows);
+int call_encode_u8(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, int64_t ld, uint32_t box_rows) {
+    return encode_swizzled(map, 1, base, cols, rows, ld, 1, 0, 128, box_rows);
 }
 
 }  // namespace pg

@@ -163,10 +163,10 @@ struct Cfg {
     static constexpr int STAGES_RAW = 192 * 1024 / STAGE_BYTES;
     static constexpr int STAGES = STAGES_RAW > 10 ? 10 : STAGES_RAW;
     static constexpr int MINE = BN / 2;                // columns of an epilogue warp: a half of the tile's
-    static constexpr int BUFFERS = BN == 256 ? 2 : 4;  // of TMEM, for each half: blocks of k on their way
-    static constexpr uint32_t TMEM_COLS = 2 * BUFFERS * MINE;
+    static constexpr int BUFFERS = BN == 256 ? 2 : 4;  // of TMEM: blocks of k on their way
+    static constexpr uint32_t TMEM_COLS = BUFFERS * BN;
     static constexpr int HALF_BYTES = B_BYTES / 2;     // of w in a slot
-    static constexpr int BAR_BYTES = (2 * STAGES + 4 * BUFFERS + 2 * kScaleSlots + 1) * 8 + 16;
+    static constexpr int BAR_BYTES = (2 * STAGES + 2 * BUFFERS + 2 * kScaleSlots + 1) * 8 + 16;
     static constexpr int OUT_BYTES = kEpiWarps * 32 * kOutBytes;
     static constexpr int SCALE_BYTES = kScaleSlots * 2 * kRows * kScales * 4;  // of the rows, for each half of the columns
     static constexpr size_t SMEM = 1024 + static_cast<size_t>(STAGES) * STAGE_BYTES + OUT_BYTES + SCALE_BYTES + BAR_BYTES;
@@ -235,11 +235,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint8_t* smem = align_smem_1024(smem_raw);
     float4* scale_ring = reinterpret_cast<float4*>(smem + S * C::STAGE_BYTES + C::OUT_BYTES);  // [slot][half][row]
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S * C::STAGE_BYTES + C::OUT_BYTES + C::SCALE_BYTES);
-    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 2 * S + 4 * NB + 2 * kScaleSlots + 1);
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 2 * S + 2 * NB + 2 * kScaleSlots + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
     const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + S);
-    const uint32_t acc_full0 = smem_u32(bars + 2 * S), acc_empty0 = smem_u32(bars + 2 * S + 2 * NB);  // [half][buffer]
-    const uint32_t scale_full0 = smem_u32(bars + 2 * S + 4 * NB), scale_empty0 = scale_full0 + 8 * kScaleSlots;
+    const uint32_t acc_full0 = smem_u32(bars + 2 * S), acc_empty0 = smem_u32(bars + 2 * S + NB);
+    const uint32_t scale_full0 = smem_u32(bars + 2 * S + 2 * NB), scale_empty0 = scale_full0 + 8 * kScaleSlots;
     const uint32_t mma_done = scale_empty0 + 8 * kScaleSlots;
 
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);  // known to be uniform
@@ -252,9 +252,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_init(full0 + 8 * s, 1);
             mbar_init(empty0 + 8 * s, p.paired ? 2 : 1);
         }
-        for (int b = 0; b < 2 * NB; ++b) {
+        for (int b = 0; b < NB; ++b) {
             mbar_init(acc_full0 + 8 * b, 1);
-            mbar_init(acc_empty0 + 8 * b, kEpiWarps / 2);
+            mbar_init(acc_empty0 + 8 * b, kEpiWarps);
         }
         for (int b = 0; b < kScaleSlots; ++b) {
             mbar_init(scale_full0 + 8 * b, 1);
@@ -344,34 +344,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const uint32_t slot0 = smem_u32(smem);
             const uint64_t a_desc0 = smem_desc(slot0, 16, 1024, kSwizzle128B);
             const uint64_t b_desc0 = smem_desc(slot0 + C::A_BYTES, 16, 1024, kSwizzle128B);
-            const uint32_t idesc = idesc_e4m3(kRows, C::MINE);
+            const uint32_t idesc = idesc_e4m3(kRows, BN);
             int slot_i = 0, buf = 0;
             uint32_t phase = 0, acc_phase = 1;
             bool ok = true;
+            // A barrier's test takes 130 cycles to answer, a quarter of a block's time: the next block's are asked
+            // for before this one's MMAs are issued.
+            bool ready = false, free = false;
+            auto sure = [&](bool answer, uint32_t bar, uint32_t parity) {
+                return __all_sync(0xffffffffu, answer) ||
+                       __all_sync(0xffffffffu, mbar_wait_short(bar, parity, p.timeout_ns, abort_flag));
+            };
             for (int u = first; u < units && ok; u += step) {
                 const int nkb = __shfl_sync(0xffffffffu, unit_of(u).nkb, 0);
                 for (int kb = 0; kb < nkb; ++kb) {
-                    ok = mbar_wait_short_warp(full0 + 8 * slot_i, phase, p.timeout_ns, abort_flag);
-                    const uint32_t o = static_cast<uint32_t>(slot_i * C::STAGE_BYTES) >> 4;
-                    // The halves' accumulators come and go by themselves, so that a buffer is filled while the
-                    // other half's is, not both halves', before it can be drained.
-#pragma unroll
-                    for (int h = 0; h < 2 && ok; ++h) {
-                        const int b = NB * h + buf;
-                        ok = mbar_wait_short_warp(acc_empty0 + 8 * b, acc_phase, p.timeout_ns, abort_flag);
-                        if (!ok) break;
-                        tc_fence_after_sync();
-#pragma unroll
-                        for (int kk = 0; kk < kBlock / 32; ++kk)
-                            mma_e4m3_warp(tmem + b * C::MINE, a_desc0 + (o + 2 * kk),
-                                               b_desc0 + (o + (C::HALF_BYTES >> 4) * h + 2 * kk), idesc, kk > 0);
-                        mma_commit_warp(acc_full0 + 8 * b);
-                    }
+                    ok = sure(ready, full0 + 8 * slot_i, phase) && sure(free, acc_empty0 + 8 * buf, acc_phase);
                     if (!ok) break;
-                    if (p.paired)
-                        mma_commit_multicast_warp(empty0 + 8 * slot_i, 3);
-                    else
-                        mma_commit_warp(empty0 + 8 * slot_i);
+                    tc_fence_after_sync();
+                    const uint32_t o = static_cast<uint32_t>(slot_i * C::STAGE_BYTES) >> 4, empty = empty0 + 8 * slot_i;
+                    const int b = buf;
                     if (++slot_i == S) {
                         slot_i = 0;
                         phase ^= 1;
@@ -380,6 +371,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         buf = 0;
                         acc_phase ^= 1;
                     }
+                    ready = mbar_test(full0 + 8 * slot_i, phase);
+                    free = mbar_test(acc_empty0 + 8 * buf, acc_phase);
+#pragma unroll
+                    for (int kk = 0; kk < kBlock / 32; ++kk)
+                        mma_e4m3_warp(tmem + b * BN, a_desc0 + (o + 2 * kk), b_desc0 + (o + 2 * kk), idesc, kk > 0);
+                    mma_commit_warp(acc_full0 + 8 * b);
+                    if (p.paired)
+                        mma_commit_multicast_warp(empty, 3);
+                    else
+                        mma_commit_warp(empty);
                 }
             }
             if (!ok && lane == 0) raise_abort(abort_flag, p.status);
@@ -436,15 +437,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // ---------------- promotion and epilogue (warps 4..11) ----------------
         const int q = warp & 3;            // TMEM lane quarter this warp may access
         const int half = (warp - 4) >> 2;  // its half of the columns
-        const uint32_t my_empty0 = acc_empty0 + 8 * NB * half;
-        const uint32_t base = tmem + (static_cast<uint32_t>(32 * q) << 16) + NB * C::MINE * half;
-        const uint32_t my_full0 = acc_full0 + 8 * NB * half;
+                const uint32_t base = tmem + (static_cast<uint32_t>(32 * q) << 16) + C::MINE * half;
         uint8_t* out = smem + S * C::STAGE_BYTES + (warp - 4) * (32 * kOutBytes);
         const bool one = lane == 0;
         auto free_buffer = [&](int b) {
             tc_fence_before_sync();
             __syncwarp();
-            mbar_arrive_if(one, my_empty0 + 8 * b);
+            mbar_arrive_relaxed_if(one, acc_empty0 + 8 * b);
         };
         int buf = 0;
         uint32_t acc_phase = 0;
@@ -466,9 +465,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int c = 0; c < C::MINE / 2; ++c) acc[c] = make_float2(0.0f, 0.0f);
             int last = 0;  // the buffer of the last block, which the results go through
-            float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);  // scales of the next blocks
-            // A block's sums come in chunks of 32 columns, two on their way at a time; while the last two are
-            // added, the next block's first two are asked for, if its barrier (tested before) lets them.
             constexpr int CHUNKS = C::MINE / kCols;
             uint32_t v[2][kCols];
             float2 scale = make_float2(0.0f, 0.0f);
@@ -479,68 +475,80 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         fma2(make_float2(__uint_as_float(v[c & 1][2 * k]), __uint_as_float(v[c & 1][2 * k + 1])), scale,
                              acc[kCols / 2 * c + k]);
             };
+            auto wait_sums = [&]() {
+                ok &= mbar_wait_short_warp(acc_full0 + 8 * buf, acc_phase, p.timeout_ns, abort_flag);
+                tc_fence_after_sync();
+            };
+            auto first_chunks = [&]() {
+                tmem_ld_32x32b_x32(base + buf * BN, v[0]);
+                if (CHUNKS > 1) tmem_ld_32x32b_x32(base + buf * BN + kCols, v[1]);
+            };
             auto advance = [&]() {  // to the next buffer
+                last = buf;
                 if (++buf == NB) {
                     buf = 0;
                     acc_phase ^= 1;
                 }
             };
+            // (After a wait that ran out, the loop goes on without waiting: a branch for it in here would cost
+            // every block.)
             if (x.nkb > 0) {
-                ok = mbar_wait_short_warp(my_full0 + 8 * buf, acc_phase, p.timeout_ns, abort_flag);
-                tc_fence_after_sync();
-                if (ok && there) {
-                    tmem_ld_32x32b_x32(base + buf * C::MINE, v[0]);
-                    if (CHUNKS > 1) tmem_ld_32x32b_x32(base + buf * C::MINE + kCols, v[1]);
-                }
+                wait_sums();
+                if (there) first_chunks();
             }
 #pragma unroll 1
-            for (int kb = 0; kb < x.nkb && ok; ++kb) {
-                if (kb % kScales == 0) {
-                    ok = mbar_wait_short_warp(scale_full0 + 8 * slot, scale_phase, p.timeout_ns, abort_flag);
-                    if (!ok) break;
-                    s = scale_ring[(2 * slot + half) * kRows + 32 * q + lane];
-                    __syncwarp();
-                    mbar_arrive_if(one, scale_empty0 + 8 * slot);
-                    if (++slot == kScaleSlots) {
-                        slot = 0;
-                        scale_phase ^= 1;
-                    }
+            for (int g = 0; g < x.nkb; g += kScales) {
+                ok &= mbar_wait_short_warp(scale_full0 + 8 * slot, scale_phase, p.timeout_ns, abort_flag);
+                float4 s = scale_ring[(2 * slot + half) * kRows + 32 * q + lane];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(scale_empty0 + 8 * slot);
+                if (++slot == kScaleSlots) {
+                    slot = 0;
+                    scale_phase ^= 1;
                 }
-                scale = both(s.x);
-                s = make_float4(s.y, s.z, s.w, 0.0f);
-                last = buf;
-                const bool more = kb + 1 < x.nkb;
+                const int blocks = min(x.nkb - g, kScales);
                 if (!there) {
-                    if (more) free_buffer(buf);
-                    advance();
-                    if (more) ok = mbar_wait_short_warp(my_full0 + 8 * buf, acc_phase, p.timeout_ns, abort_flag);
+                    for (int r = 0; r < blocks; ++r) {
+                        advance();
+                        if (g + r + 1 < x.nkb) {
+                            free_buffer(last);
+                            wait_sums();
+                        }
+                    }
                     continue;
                 }
-                const uint32_t at = base + buf * C::MINE;
-                tmem_wait_ld(v[0]);
-                if (CHUNKS > 1) tmem_wait_ld(v[1]);
-#pragma unroll
-                for (int c = 0; c + 2 < CHUNKS; ++c) {
-                    add_chunk(c);
-                    tmem_ld_32x32b_x32(at + kCols * (c + 2), v[c & 1]);
-                }
-                advance();
-                const bool ready = more && mbar_try_wait(my_full0 + 8 * buf, acc_phase);
-                if (CHUNKS > 2) {
+                // A block's sums come in chunks of 32 columns, two on their way at a time; while the last of them
+                // is added, the next block's barrier is tested, which takes 130 cycles to answer.
+#pragma unroll 1
+                for (int r = 0; r < blocks; ++r) {
+                    const bool more = g + r + 1 < x.nkb;
+                    const uint32_t at = base + buf * BN;
+                    scale = both(s.x);
+                    s = make_float4(s.y, s.z, s.w, 0.0f);
+                    advance();
                     tmem_wait_ld(v[0]);
-                    tmem_wait_ld(v[1]);
+                    if (CHUNKS > 1) tmem_wait_ld(v[1]);
+#pragma unroll
+                    for (int c = 0; c + 2 < CHUNKS; ++c) {
+                        add_chunk(c);
+                        tmem_ld_32x32b_x32(at + kCols * (c + 2), v[c & 1]);
+                    }
+                    if (CHUNKS > 2) {
+                        tmem_wait_ld(v[0]);
+                        tmem_wait_ld(v[1]);
+                    }
+                    if (more) free_buffer(last);
+                    if (CHUNKS > 1) add_chunk(CHUNKS - 2);
+                    bool ready = true;
+                    if (more) ready = mbar_try_wait(acc_full0 + 8 * buf, acc_phase);
+                    add_chunk(CHUNKS - 1);
+                    if (more) {
+                        if (!__all_sync(0xffffffffu, ready))
+                            ok &= mbar_wait_short_warp(acc_full0 + 8 * buf, acc_phase, p.timeout_ns, abort_flag);
+                        tc_fence_after_sync();
+                        first_chunks();
+                    }
                 }
-                if (more) free_buffer(last);
-                if (CHUNKS > 1) add_chunk(CHUNKS - 2);
-                else add_chunk(0);
-                if (more) {
-                    ok = __all_sync(0xffffffffu, ready) ||
-                         mbar_wait_short_warp(my_full0 + 8 * buf, acc_phase, p.timeout_ns, abort_flag);
-                    tc_fence_after_sync();
-                    if (ok) tmem_ld_32x32b_x32(base + buf * C::MINE, v[0]);
-                }
-                if (CHUNKS > 1) add_chunk(CHUNKS - 1);
-                if (CHUNKS > 1 && more && ok) tmem_ld_32x32b_x32(base + buf * C::MINE + kCols, v[1]);
             }
             if (!ok) {
                 if (lane == 0) raise_abort(abort_flag, p.status);
@@ -548,7 +556,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             // The results go back to the warp's own columns of the last buffer and from there, 16 at a
             // time, through the epilogue: a loop, where registers would want it written out.
-            const uint32_t at = base + last * C::MINE;
+            const uint32_t at = base + last * BN;
             if (there) {
 #pragma unroll
                 for (int c = 0; c < C::MINE / kCols; ++c) {

@@ -55,52 +55,99 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 __device__ __forceinline__ float block_scale(float largest) { return max_nan(largest / kLargest, 1.17549435e-38f); }
 
 __device__ __forceinline__ float largest8(const float (&v)[8]) {
-    float m = 0.0f;
+    float m = 0.0f;  // its sign is of no use
 #pragma unroll
-    for (int t = 0; t < 8; ++t) m = max_nan(m, fabsf(v[t]));
-    return m;
+    for (int t = 0; t < 8; ++t) asm("max.NaN.xorsign.abs.f32 %0, %0, %1;" : "+f"(m) : "f"(v[t]));
+    return fabsf(m);
 }
 
-// The quotients are FP32 numbers, rounded to the nearest e4m3, ties to even.
-__device__ __forceinline__ void put8(uint8_t* q, bool vec, int valid, const float (&v)[8], float scale) {
-    uint32_t w[2];
+// The quotients v / scale are FP32 numbers, rounded to the nearest e4m3, ties to even.  Where nothing
+// can over- or underflow on the way (plain) they are formed by Markstein's method (IBM Journal of
+// Research and Development 34, 1990): with r the rounded reciprocal, q = v r, and the remainder
+// v - q scale, which a fused multiply-add gives exactly, q + (v - q scale) r rounds as the quotient
+// does.  (A quotient of zero takes v's sign.)
+struct Divisor {
+    float scale, r;
+    bool plain;
+};
+__device__ __forceinline__ Divisor divisor(float scale) {
+    return {scale, 1.0f / scale, scale > 8.6736174e-19f && scale < 1.1529215e18f};  // 2^-60, 2^60
+}
+__device__ __forceinline__ uint2 round8(const float (&v)[8], const Divisor& d) {
+    float2 f[4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * h] / scale, v[4 * h + 1] / scale), __NV_SATFINITE, __NV_E4M3);
-        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * h + 2] / scale, v[4 * h + 3] / scale), __NV_SATFINITE, __NV_E4M3);
-        w[h] = lo | hi << 16;
+    for (int t = 0; t < 4; ++t) {
+        const float2 x = make_float2(v[2 * t], v[2 * t + 1]);
+        const float2 a = mul2(x, both(d.r)), rest = fma2(a, both(-d.scale), x);
+        const float2 y = fma2(rest, both(d.r), a);
+        f[t] = make_float2(copysignf(y.x, x.x), copysignf(y.y, x.y));
     }
+    if (!d.plain) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) f[t] = make_float2(v[2 * t] / d.scale, v[2 * t + 1] / d.scale);
+    }
+    uint32_t h[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) h[t] = __nv_cvt_float2_to_fp8x2(f[t], __NV_SATFINITE, __NV_E4M3);
+    return make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+}
+__device__ __forceinline__ void put8(uint8_t* q, bool vec, int valid, const uint2& w) {
     if (vec && valid >= 8) {
-        *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[1]);
+        *reinterpret_cast<uint2*>(q) = w;
     } else {
 #pragma unroll
         for (int t = 0; t < 8; ++t)
-            if (t < valid) q[t] = static_cast<uint8_t>(w[t / 4] >> (8 * (t % 4)));
+            if (t < valid) q[t] = static_cast<uint8_t>((t < 4 ? w.x : w.y) >> (8 * (t % 4)));
     }
 }
 
-// Blocks of 1 x 128: sixteen lanes to each.  HBM-bound: reads x, writes a byte per value.
-template <typename T>
+// Blocks of 1 x 128: sixteen lanes to each, R neighbouring blocks of a row with their loads in
+// flight.  VEC: whole eights at 16-byte boundaries (8 in q).  HBM-bound: reads x, writes a byte per
+// value.
+template <typename T, int R, bool VEC>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(int64_t rows, int64_t cols, const T* x, int64_t ldx, uint8_t* q,
-                                                            int64_t ldq, float* scales, int64_t s_row, int64_t s_block,
-                                                            bool vec_x, bool vec_q) {
+                                                            int64_t ldq, float* scales, int64_t s_row, int64_t s_block) {
     pdl_trigger();
     pdl_wait();
     const int lane = threadIdx.x % 16;
-    const int64_t blocks = (cols + kBlock - 1) / kBlock, count = rows * blocks;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * 16;
-    for (int64_t b0 = static_cast<int64_t>(blockIdx.x) * 16 + threadIdx.x / 32 * 2; b0 < count; b0 += step) {
-        const int64_t b = b0 + threadIdx.x / 16 % 2;  // a warp's halves stay together
-        const int64_t r = b < count ? b / blocks : 0, c = (b - r * blocks) * kBlock + 8 * lane;
-        const int valid = b < count ? static_cast<int>(min(cols - c, int64_t(8))) : 0;
-        float v[8];
-        load8(x + r * ldx + (valid > 0 ? c : 0), vec_x, valid, v);
-        float m = largest8(v);
+    const uint32_t blocks = static_cast<uint32_t>((cols + kBlock - 1) / kBlock), per_row = (blocks + R - 1) / R;
+    const int64_t group = static_cast<int64_t>(blockIdx.x) * 16 + threadIdx.x / 16;
+    const int64_t r = group >> 32 ? group / per_row : static_cast<uint32_t>(group) / per_row;
+    const uint32_t first = static_cast<uint32_t>(group - r * per_row) * R;
+    const bool there = r < rows;
+    const int64_t c0 = static_cast<int64_t>(first) * kBlock + 8 * lane;
+    const T* from = x + (there ? r * ldx : 0);
+    float v[R][8];
+    if (VEC) {
+        constexpr int N = static_cast<int>(sizeof(T)) / 2;
+        uint4 raw[R][N];
+#pragma unroll
+        for (int k = 0; k < R; ++k)
+#pragma unroll
+            for (int h = 0; h < N; ++h)
+                raw[k][h] = there && c0 + k * kBlock < cols ? __ldcs(reinterpret_cast<const uint4*>(from + c0 + k * kBlock) + h)
+                                                            : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int k = 0; k < R; ++k)
+#pragma unroll
+            for (int t = 0; t < 8; ++t) v[k][t] = to_float(reinterpret_cast<const T*>(raw[k])[t]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const int64_t c = c0 + k * kBlock;
+            load8(from + c, false, there && c < cols ? static_cast<int>(min(cols - c, int64_t(8))) : 0, v[k]);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+        float m = largest8(v[k]);
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
         const float scale = block_scale(m);
-        if (valid > 0) put8(q + r * ldq + c, vec_q, valid, v, scale);
-        if (lane == 0 && b < count) scales[r * s_row + (b - r * blocks) * s_block] = scale;
+        const int64_t c = c0 + k * kBlock;
+        const uint2 w = round8(v[k], divisor(scale));
+        if (there && c < cols) put8(q + r * ldq + c, VEC, VEC ? 8 : static_cast<int>(min(cols - c, int64_t(8))), w);
+        if (there && lane == 0 && first + k < blocks) scales[r * s_row + (first + k) * s_block] = scale;
     }
 }
 
@@ -130,10 +177,11 @@ __global__ void __launch_bounds__(256) quantize_blocks_kernel(int64_t rows, int6
     for (int k = 0; k < 8; ++k) m = max_nan(m, slots[k]);
     const float scale = block_scale(m);
     if (threadIdx.x == 0) scales[br * lds + bc] = scale;
+    const Divisor d = divisor(scale);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
         const int64_t r = br * kBlock + 16 * k + threadIdx.x / 16;
-        if (r < rows && valid > 0) put8(q + r * ldq + c, vec_q, valid, v[k], scale);
+        if (r < rows && valid > 0) put8(q + r * ldq + c, vec_q, valid, round8(v[k], d));
     }
 }
 
@@ -683,11 +731,16 @@ cudaError_t launch_quantize(int dtype, int64_t rows, int64_t cols, int block_row
         using T = decltype(zero);
         const bool vec_x = rows_aligned<T>(x, ldx);
         const int64_t across = cdiv(cols, kBlock);
-        if (block_rows == 1)
-            return launch_kernel(true, quantize_rows_kernel<T>,
-                                 dim3(static_cast<unsigned>(std::min<int64_t>(cdiv(rows * across, 16), int64_t(64) * num_sms))),
-                                 dim3(256), 0, st, rows, cols, static_cast<const T*>(x), ldx, q, ldq, scales, s_row, s_block,
-                                 vec_x, vec_q);
+        if (block_rows == 1) {
+            const bool vec = vec_x && vec_q && cols % 8 == 0;
+            // several blocks' loads per thread once that leaves each SM its threads
+            constexpr int R = 8 / static_cast<int>(sizeof(T));
+            const bool many = rows * across >= int64_t(R * 128) * num_sms;
+            auto kern = many ? (vec ? quantize_rows_kernel<T, R, true> : quantize_rows_kernel<T, R, false>)
+                             : (vec ? quantize_rows_kernel<T, 1, true> : quantize_rows_kernel<T, 1, false>);
+            return launch_kernel(true, kern, dim3(static_cast<unsigned>(cdiv(rows * cdiv(across, many ? R : 1), 16))), dim3(256),
+                                 0, st, rows, cols, static_cast<const T*>(x), ldx, q, ldq, scales, s_row, s_block);
+        }
         return launch_kernel(true, quantize_blocks_kernel<T>, dim3(static_cast<unsigned>(cdiv(rows, kBlock) * across)),
                              dim3(256), 0, st, rows, cols, static_cast<const T*>(x), ldx, q, ldq, scales, s_row, vec_x, vec_q);
     };

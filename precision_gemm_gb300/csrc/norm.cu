@@ -214,8 +214,9 @@ struct NormBackwardParams {
     int warps;
 };
 
-// Teams walk over rows, the next row's loads on their way while a row is worked on.
-template <typename T, bool VEC, int V, int NT, int B>
+// Teams walk over rows, the next row's loads on their way while a row is worked on (AHEAD; rows of
+// float32 leave no registers for it).
+template <typename T, bool VEC, int V, int NT, int B, bool AHEAD>
 __global__ void __launch_bounds__(NT, B) norm_backward_kernel(const NormBackwardParams p) {
     __shared__ float2 slots[2][NT / kWarp];
     extern __shared__ float sums[];  // [team][8 V][team threads], where a block has several teams
@@ -226,60 +227,82 @@ __global__ void __launch_bounds__(NT, B) norm_backward_kernel(const NormBackward
     // every team of a block runs as many rounds, since they meet at its barriers
     const int64_t rounds = (p.rows - static_cast<int64_t>(blockIdx.x) * teams + step - 1) / step;
     int64_t row = static_cast<int64_t>(blockIdx.x) * teams + threadIdx.x / team;
-    Raw<T> w[V], xv[V], dv[V], rv[V];
-    float dw[V][8] = {}, db[V][8] = {};
-    float mean = 0.0f, rstd = 0.0f;
+    struct Row {
+        Raw<T> x[V], dy[V], r[V];
+        float mean, rstd;
+    };
+    Raw<T> w[V];
+    float2 dw[V][4] = {}, db[V][4] = {};
 #pragma unroll
     for (int j = 0; j < V; ++j)
         if (p.w) fetch<T, VEC, false>(static_cast<const T*>(p.w), n, tid, team, j, w[j]);
-    auto load = [&](int64_t r) {
+    auto load = [&](Row& to, int64_t r) {
         const int64_t there = r < p.rows ? n : 0;
         if (r >= p.rows) r = 0;
-        mean = there ? p.mean[r] : 0.0f;
-        rstd = there ? p.rstd[r] : 0.0f;
+        to.mean = there ? p.mean[r] : 0.0f;
+        to.rstd = there ? p.rstd[r] : 0.0f;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            fetch<T, VEC, true>(static_cast<const T*>(p.x) + r * p.ldx, there, tid, team, j, xv[j]);
-            fetch<T, VEC, true>(static_cast<const T*>(p.dy) + r * p.lddy, there, tid, team, j, dv[j]);
+            fetch<T, VEC, true>(static_cast<const T*>(p.x) + r * p.ldx, there, tid, team, j, to.x[j]);
+            fetch<T, VEC, true>(static_cast<const T*>(p.dy) + r * p.lddy, there, tid, team, j, to.dy[j]);
             if (p.residual)
-                fetch<T, VEC, true>(static_cast<const T*>(p.residual) + r * p.ldr, there, tid, team, j, rv[j]);
+                fetch<T, VEC, true>(static_cast<const T*>(p.residual) + r * p.ldr, there, tid, team, j, to.r[j]);
         }
     };
-    load(row);
+    Row at, next;
+    if (AHEAD) load(next, row);
     const float inv = 1.0f / static_cast<float>(n);
     for (int64_t round = 0; round < rounds; ++round, row += step) {
+        if (AHEAD) {
+            at = next;
+            if (round + 1 < rounds) load(next, row + step);
+        } else {
+            load(at, row);
+        }
         const bool there = row < p.rows;
-        float h[V][8], g[V][8], res[V][8];
-        float s1 = 0.0f, s2 = 0.0f;
-        const float scale = rstd;
+        // two elements' (x - mean) rstd and dy w, formed again where they are needed; past the row's end
+        // dy is zero, and h must not meet it as an infinity
+        auto pair = [&](int j, int t, float2& h, float2& g, float2& d) {
+            d = make_float2(at.dy[j][2 * t], at.dy[j][2 * t + 1]);
+            const float2 x = make_float2(at.x[j][2 * t], at.x[j][2 * t + 1]);
+            h = mul2(add2(x, both(-at.mean)), both(at.rstd));
+            if (!VEC && (column<VEC>(tid, team, j, 2 * t) >= n || column<VEC>(tid, team, j, 2 * t + 1) >= n)) {
+                if (column<VEC>(tid, team, j, 2 * t) >= n) h.x = 0.0f;
+                h.y = 0.0f;
+            }
+            if (VEC && column<VEC>(tid, team, j, 0) >= n) h = both(0.0f);
+            g = p.w ? mul2(d, make_float2(w[j][2 * t], w[j][2 * t + 1])) : d;
+        };
+        float2 s1 = both(0.0f), s2 = both(0.0f);
 #pragma unroll
         for (int j = 0; j < V; ++j)
 #pragma unroll
-            for (int t = 0; t < 8; ++t) {
-                const float d = dv[j][t];
-                // zero past the row's end, as dy is
-                h[j][t] = there && column<VEC>(tid, team, j, t) < n ? (xv[j][t] - mean) * scale : 0.0f;
-                g[j][t] = p.w ? d * w[j][t] : d;
-                dw[j][t] = fmaf(d, h[j][t], dw[j][t]);
-                db[j][t] += d;
-                s1 += g[j][t];
-                s2 = fmaf(g[j][t], h[j][t], s2);
-                res[j][t] = p.residual ? rv[j][t] : 0.0f;
+            for (int t = 0; t < 4; ++t) {
+                float2 h, g, d;
+                pair(j, t, h, g, d);
+                dw[j][t] = fma2(d, h, dw[j][t]);
+                db[j][t] = add2(db[j][t], d);
+                s1 = add2(s1, g);
+                s2 = fma2(g, h, s2);
             }
-        if (round + 1 < rounds) load(row + step);
         if (p.dx) {
             // two places for the sums, taken in turn: one barrier a round
-            const float2 s = team_sum2(make_float2(s1, s2), p.warps, slots[round & 1]);
-            s1 = s.x * inv;
-            s2 = s.y * inv;
+            const float2 s = team_sum2(make_float2(s1.x + s1.y, s2.x + s2.y), p.warps, slots[round & 1]);
             if (there) {
                 T* dx = static_cast<T*>(p.dx) + row * p.lddx;
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
                     float o[8];
 #pragma unroll
-                    for (int t = 0; t < 8; ++t)
-                        o[t] = fmaf(scale, g[j][t] - fmaf(h[j][t], s2, s1), res[j][t]);
+                    for (int t = 0; t < 4; ++t) {
+                        float2 h, g, d;
+                        pair(j, t, h, g, d);
+                        const float2 v = fma2(h, both(-s.y * inv), add2(g, both(-s.x * inv)));
+                        const float2 r = p.residual ? make_float2(at.r[j][2 * t], at.r[j][2 * t + 1]) : both(0.0f);
+                        const float2 y = fma2(v, both(at.rstd), r);
+                        o[2 * t] = y.x;
+                        o[2 * t + 1] = y.y;
+                    }
                     put<T, VEC>(dx, n, tid, team, j, o);
                 }
             }
@@ -289,13 +312,14 @@ __global__ void __launch_bounds__(NT, B) norm_backward_kernel(const NormBackward
     float* out = p.part + static_cast<int64_t>(blockIdx.x) * 2 * n;
 #pragma unroll
     for (int which = 0; which < 2; ++which, out += n) {
-        float(&mine)[V][8] = which ? db : dw;
+        float2(&mine)[V][4] = which ? db : dw;
+        auto value = [&](int j, int t) { return t & 1 ? mine[j][t / 2].y : mine[j][t / 2].x; };
         if (teams > 1) {  // the block's first team adds the others' sums in order
             __syncthreads();
 #pragma unroll
             for (int j = 0; j < V; ++j)
 #pragma unroll
-                for (int t = 0; t < 8; ++t) sums[(threadIdx.x / team * (8 * V) + 8 * j + t) * team + tid] = mine[j][t];
+                for (int t = 0; t < 8; ++t) sums[(threadIdx.x / team * (8 * V) + 8 * j + t) * team + tid] = value(j, t);
             __syncthreads();
             for (int q = threadIdx.x; q < 8 * V * team; q += blockDim.x) {
                 const int jt = q / team;
@@ -311,7 +335,7 @@ __global__ void __launch_bounds__(NT, B) norm_backward_kernel(const NormBackward
 #pragma unroll
                 for (int t = 0; t < 8; ++t) {
                     const int64_t c = column<VEC>(tid, team, j, t);
-                    if (c < n) out[c] = mine[j][t];
+                    if (c < n) out[c] = value(j, t);
                 }
         }
     }
@@ -377,29 +401,36 @@ __global__ void __launch_bounds__(256) norm_columns_kernel(const NormBackwardPar
     }
 }
 
-// dw (blockIdx.y 0) and db (1): the blocks' sums, added in order by eight warps with an
-// eighth of them each, and those in order.
+// dw (blockIdx.y 0) and db (1): the blocks' sums, added in order by 32 warps with a 32nd of them
+// each, and those in order.
+__device__ __forceinline__ float sum_range(const float* part, int64_t stride, int64_t a, int64_t b) {
+    float s = 0.0f;
+    for (; a + 8 <= b; a += 8) {
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = __ldcg(part + (a + k) * stride);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s += v[k];
+    }
+    for (; a < b; ++a) s += __ldcg(part + a * stride);
+    return s;
+}
 template <typename T>
-__global__ void __launch_bounds__(256) norm_sum_kernel(int64_t n, int64_t blocks, const float* part, T* dw, T* db) {
-    __shared__ float sums[8][kWarp];
+__global__ void __launch_bounds__(1024) norm_sum_kernel(int64_t n, int64_t blocks, const float* part, T* dw, T* db) {
+    __shared__ float sums[32][kWarp + 1];
     pdl_trigger();
     pdl_wait();
     const int lane = threadIdx.x % kWarp, l = threadIdx.x / kWarp;
     const int64_t c = static_cast<int64_t>(blockIdx.x) * kWarp + lane;
     T* out = blockIdx.y ? db : dw;
     if (!out) return;
-    float s = 0.0f;
-    if (c < n) {
-        const int64_t a = blocks * l / 8, b = blocks * (l + 1) / 8;
-#pragma unroll 8
-        for (int64_t q = a; q < b; ++q) s += part[(2 * q + blockIdx.y) * n + c];
-    }
-    sums[l][lane] = s;
+    sums[l][lane] = c < n ? sum_range(part + blockIdx.y * n + c, 2 * n, blocks * l / 32, blocks * (l + 1) / 32) : 0.0f;
     __syncthreads();
-    if (l == 0 && c < n) {
-        for (int q = 1; q < 8; ++q) s += sums[q][lane];
-        out[c] = from_float<T>(s);
-    }
+    if (l > 0) return;
+    float s = 0.0f;
+#pragma unroll
+    for (int q = 0; q < 32; ++q) s += sums[q][lane];
+    if (c < n) out[c] = from_float<T>(s);
 }
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -431,35 +462,44 @@ cudaError_t norm(const NormParams& p, int num_sms, cudaStream_t st) {
     return run_norm<T, VEC, 1, 256>(p, st);
 }
 
-// The backward pass's shape: rows held in registers up to kHeld columns.
+// The backward pass's shape: rows held in registers up to kHeld columns, eight of them per thread
+// (sixteen of bfloat16 from 2048 on).
 constexpr int64_t kHeld = 8192;
 struct BackwardShape {
     int v, nt, blocks_per_sm, warps, teams;
     int64_t blocks;
 };
-BackwardShape backward_shape(int64_t rows, int64_t n, int num_sms) {
+BackwardShape backward_shape(int dtype, int64_t rows, int64_t n, int num_sms) {
     BackwardShape s{};
-    s.v = n > 2048 ? 2 : 1;
+    s.v = dtype == SGEMM_BF16 && n > 2048 ? 2 : 1;
     s.warps = team_warps(n, s.v);
     s.nt = std::max(s.warps * kWarp, 256);
-    s.blocks_per_sm = s.nt == 256 ? 2 : 1;
+    s.blocks_per_sm = s.v == 2 ? (s.nt == 256 ? 2 : 1) : 1024 / s.nt;
     s.teams = s.nt / (s.warps * kWarp);
     s.blocks = std::min<int64_t>(cdiv(rows, s.teams), static_cast<int64_t>(s.blocks_per_sm) * num_sms);
     return s;
 }
 
-template <typename T, bool VEC, int V, int NT, int B>
+template <typename T, bool VEC, int V, int NT, int B, bool AHEAD>
 cudaError_t run_backward(const NormBackwardParams& p, const BackwardShape& s, cudaStream_t st) {
     const size_t smem = s.teams > 1 && p.part ? static_cast<size_t>(s.nt) * 8 * V * 4 : 0;
-    return launch_kernel(true, norm_backward_kernel<T, VEC, V, NT, B>, dim3(static_cast<unsigned>(s.blocks)),
+    return launch_kernel(true, norm_backward_kernel<T, VEC, V, NT, B, AHEAD>, dim3(static_cast<unsigned>(s.blocks)),
                          dim3(s.nt), smem, st, p);
 }
 
 template <typename T, bool VEC>
 cudaError_t norm_backward(NormBackwardParams p, const BackwardShape& s, cudaStream_t st) {
     p.warps = s.warps;
-    if (s.nt > 256) return run_backward<T, VEC, 2, 512, 1>(p, s, st);
-    return s.v == 2 ? run_backward<T, VEC, 2, 256, 2>(p, s, st) : run_backward<T, VEC, 1, 256, 2>(p, s, st);
+    if constexpr (std::is_same<T, bf16>::value) {
+        if (s.v == 2)
+            return s.nt > 256 ? run_backward<T, VEC, 2, 512, 1, true>(p, s, st)
+                              : run_backward<T, VEC, 2, 256, 2, true>(p, s, st);
+        return run_backward<T, VEC, 1, 256, 4, true>(p, s, st);
+    } else {
+        if (s.nt > 512) return run_backward<T, VEC, 1, 1024, 1, false>(p, s, st);
+        return s.nt > 256 ? run_backward<T, VEC, 1, 512, 2, false>(p, s, st)
+                          : run_backward<T, VEC, 1, 256, 4, false>(p, s, st);
+    }
 }
 
 template <typename T>
@@ -468,7 +508,7 @@ cudaError_t backward(const NormBackwardParams& p, T* dw, T* db, int num_sms, cud
     int64_t blocks = 0;
     cudaError_t e = cudaSuccess;
     if (p.rows > 0 && p.n <= kHeld) {
-        const BackwardShape s = backward_shape(p.rows, p.n, num_sms);
+        const BackwardShape s = backward_shape(std::is_same<T, bf16>::value ? SGEMM_BF16 : SGEMM_F32, p.rows, p.n, num_sms);
         blocks = s.blocks;
         const bool vec = p.n % 8 == 0 && rows_aligned<T>(p.dy, p.lddy) && rows_aligned<T>(p.x, p.ldx) &&
                          rows_aligned<T>(p.w, 0) && rows_aligned<T>(p.residual, p.ldr) && rows_aligned<T>(p.dx, p.lddx);
@@ -482,7 +522,7 @@ cudaError_t backward(const NormBackwardParams& p, T* dw, T* db, int num_sms, cud
                               dim3(256), 0, st, p);
     }
     if (sums && e == cudaSuccess)
-        e = launch_kernel(true, norm_sum_kernel<T>, dim3(static_cast<unsigned>(cdiv(p.n, kWarp)), 2), dim3(256), 0, st,
+        e = launch_kernel(true, norm_sum_kernel<T>, dim3(static_cast<unsigned>(cdiv(p.n, kWarp)), 2), dim3(1024), 0, st,
                           p.n, blocks, static_cast<const float*>(p.part), dw, db);
     return e;
 }
@@ -501,9 +541,9 @@ cudaError_t launch_norm(int dtype, int64_t rows, int64_t n, const void* x, int64
     return dtype == SGEMM_F32 ? go(float()) : go(bf16());
 }
 
-size_t norm_part_bytes(int64_t rows, int64_t n, int num_sms) {
+size_t norm_part_bytes(int dtype, int64_t rows, int64_t n, int num_sms) {
     if (rows == 0) return 0;
-    return static_cast<size_t>(n <= kHeld ? backward_shape(rows, n, num_sms).blocks : cdiv(rows, kSlab)) * 2 * n * 4;
+    return static_cast<size_t>(n <= kHeld ? backward_shape(dtype, rows, n, num_sms).blocks : cdiv(rows, kSlab)) * 2 * n * 4;
 }
 
 int norm_backward_launches(int64_t rows, int64_t n, bool dx, bool sums) {

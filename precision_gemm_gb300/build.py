@@ -16,7 +16,7 @@ LIB = os.path.join(HERE, "libprecision_gemm.so")
 INCLUDE = os.path.join(ROOT, "include")
 
 SOURCES = ["sgemm_api.cu", "ffma_kernel.cu", "tc_kernel.cu", "tc2_kernel.cu", "aux_kernels.cu", "layer_api.cu",
-           "product_tc.cu", "product_rows.cu", "layer_kernels.cu", "norm.cu", "block.cu", "routing.cu"]
+           "product_tc.cu", "product_rows.cu", "layer_kernels.cu", "norm.cu", "block.cu", "block_rows.cu", "routing.cu"]
 # Host-only C++ (the CPU co-worker of the hybrid column split), compiled by the host compiler.
 HOST_SOURCES = ["host_sgemm.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

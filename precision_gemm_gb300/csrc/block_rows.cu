@@ -1,0 +1,230 @@
+// Products with 8-bit weights (block.cu) for a few rows of x, up to eight: a decoding step.  Reading
+// the weights once is all there is to do, so they stream into registers, 16 bytes per lane and load,
+// several loads in flight, and meet x in warp-level matrix instructions (m16n8k32, e4m3, FP32 sums):
+// 16 weight rows by eight rows of x take two of them per 64 k and 1 KiB of weights.
+//
+// The order of k inside an instruction is free as long as both operands have it, so a lane's 16
+// bytes of a weight row serve as they lie in memory: of a row's 64 k, lane c of four has k 16 c to 16
+// c + 15, whose words 0 and 1 are one instruction's k and words 2 and 3 the next one's.
+//
+// Each block rounds the rows of x it needs to e4m3 itself (they come from L2, while the first
+// weights are on their way from HBM): a launch less.  Up to eight warps share a weight row's k; their sums
+// are added in order.
+#include <cuda_fp8.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "block.cuh"
+#include "layers.h"
+#include "ptx.cuh"
+
+namespace pg {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kMostRows = 8;     // columns of a matrix instruction
+constexpr int kGroup = 16;       // weight rows of a warp
+constexpr int kAhead = 2;        // blocks of 128 k on their way
+constexpr size_t kMostShared = 96 * 1024;
+
+struct RowsParams {
+    BlockProduct b;
+    bool raw;      // x is of the call's type, not e4m3
+    bool vec;      // x in 16-byte loads (raw)
+    int ks;        // warps that share a weight row's k
+    int kbs;
+    int x_stride;  // of the rows of x in shared memory, bytes: the banks of two rows differ
+};
+
+__device__ __forceinline__ uint4 stream16(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+// The first `valid` bytes of v, zeros behind them.
+__device__ __forceinline__ uint4 keep_bytes(uint4 v, int valid) {
+    uint32_t* w = &v.x;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        const int bytes = valid - 4 * t;
+        w[t] = bytes >= 4 ? w[t] : (bytes <= 0 ? 0u : w[t] & ((1u << (8 * bytes)) - 1));
+    }
+    return v;
+}
+
+// c += a b: a 16 rows x 32 k, b 32 k x 8 columns, both e4m3.
+__device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+template <typename T>
+__global__ void __launch_bounds__(32 * kWarps, 2) block_rows_kernel(const RowsParams q) {
+    extern __shared__ __align__(16) uint8_t xs[];  // x's rows in e4m3, then their scales
+    __shared__ float sums[kWarps][kGroup][kMostRows + 1];
+    const BlockProduct& p = q.b;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, c4 = lane % 4;
+    const int t = static_cast<int>(p.t), kbs = q.kbs;
+    float* x_scale = reinterpret_cast<float*>(xs + static_cast<size_t>(t) * q.x_stride);  // [row][block]
+    pdl_trigger();
+    pdl_wait();
+    const int part = warp % q.ks;
+    const int64_t i0 = (static_cast<int64_t>(blockIdx.x) * (kWarps / q.ks) + warp / q.ks) * kGroup;
+    // this warp's blocks of k, the whole ones of them up to whole
+    const int kb0 = kbs * part / q.ks, kb1 = kbs * (part + 1) / q.ks;
+    const int whole = min(kb1, static_cast<int>(p.k / SGEMM_BLOCK));
+    const uint8_t* w0 = p.w + min(i0 + g, p.n - 1) * p.ldw + 16 * c4;
+    const uint8_t* w1 = p.w + min(i0 + g + 8, p.n - 1) * p.ldw + 16 * c4;
+    uint4 raw[kAhead][2][2];  // [block][half][row g or g + 8]
+    auto fetch = [&](uint4(&to)[2][2], int kb) {
+        if (kb < whole) {
+            const int64_t at = static_cast<int64_t>(kb) * SGEMM_BLOCK;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                to[h][0] = stream16(w0 + at + 64 * h);
+                to[h][1] = stream16(w1 + at + 64 * h);
+            }
+        }
+    };
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) fetch(raw[u], kb0 + u);
+
+    // x: sixteen lanes to a block of 128
+    const int l16 = threadIdx.x % 16;
+    for (int r = 0; r < t; ++r) {
+        uint8_t* to = xs + r * q.x_stride;
+        for (int kb2 = warp; 2 * kb2 < kbs; kb2 += kWarps) {
+            const int kb = 2 * kb2 + lane / 16, at = kb * SGEMM_BLOCK + 8 * l16;
+            const int valid = kb < kbs ? static_cast<int>(min(max(p.k - at, int64_t(0)), int64_t(8))) : 0;
+            uint2 word = make_uint2(0, 0);
+            if (q.raw) {
+                float v[8];
+                load8(reinterpret_cast<const T*>(p.x) + r * p.ldx + (valid > 0 ? at : 0), q.vec, valid, v);
+                float m = largest8(v);
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+                const float scale = block_scale(m);
+                word = round8(v, divisor(scale));
+                if (kb < kbs && l16 == 0) x_scale[r * kbs + kb] = scale;
+            } else {
+                const uint8_t* from = p.x + r * p.ldx + at;
+                if (valid == 8) {  // rows start at 16-byte boundaries
+                    word = *reinterpret_cast<const uint2*>(from);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (e < valid) (e < 4 ? word.x : word.y) |= static_cast<uint32_t>(from[e]) << (8 * (e % 4));
+                }
+                if (kb < kbs && l16 == 0) x_scale[r * kbs + kb] = p.x_scales[r * p.xs_row + kb * p.xs_block];
+            }
+            if (kb < kbs) *reinterpret_cast<uint2*>(to + at) = word;
+        }
+    }
+    __syncthreads();
+
+    const float* sw = p.w_scales + min(i0, p.n - 1) / SGEMM_BLOCK * p.ldws;
+    const uint8_t* x_row = xs + min(g, t - 1) * q.x_stride + 16 * c4;
+    const float* sx0 = x_scale + min(2 * c4, t - 1) * kbs;
+    const float* sx1 = x_scale + min(2 * c4 + 1, t - 1) * kbs;
+    float acc[4] = {};
+    auto add_block = [&](const uint4(&a)[2][2], int kb, float s) {
+        float c[4] = {};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (g < t) x = *reinterpret_cast<const uint4*>(x_row + kb * SGEMM_BLOCK + 64 * h);
+            mma_e4m3(c, a[h][0].x, a[h][1].x, a[h][0].y, a[h][1].y, x.x, x.y);
+            mma_e4m3(c, a[h][0].z, a[h][1].z, a[h][0].w, a[h][1].w, x.z, x.w);
+        }
+        const float s0 = sx0[kb] * s, s1 = sx1[kb] * s;
+        acc[0] = fmaf(c[0], s0, acc[0]);
+        acc[1] = fmaf(c[1], s1, acc[1]);
+        acc[2] = fmaf(c[2], s0, acc[2]);
+        acc[3] = fmaf(c[3], s1, acc[3]);
+    };
+    float next_sw = kb0 < kb1 ? __ldg(sw + kb0) : 0.0f;
+    for (int kb = kb0; kb < whole; kb += kAhead) {
+#pragma unroll
+        for (int d = 0; d < kAhead; ++d) {
+            if (kb + d >= whole) break;
+            const float s = next_sw;
+            if (kb + d + 1 < kb1) next_sw = __ldg(sw + kb + d + 1);
+            add_block(raw[d], kb + d, s);
+            fetch(raw[d], kb + d + kAhead);
+        }
+    }
+    if (whole < kb1) {  // the last block, which k cuts: what lies behind it in memory is no value
+        const int64_t at = static_cast<int64_t>(whole) * SGEMM_BLOCK;
+        uint4 a[2][2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int left = static_cast<int>(p.k - at) - 64 * h - 16 * c4;
+            a[h][0] = a[h][1] = make_uint4(0, 0, 0, 0);
+            if (left > 0) {  // (a row's last 16 bytes end inside the 16-byte block of its last one)
+                a[h][0] = keep_bytes(stream16(w0 + at + 64 * h), left);
+                a[h][1] = keep_bytes(stream16(w1 + at + 64 * h), left);
+            }
+        }
+        add_block(a, whole, next_sw);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sums[warp][g + 8 * (e / 2)][2 * c4 + e % 2] = acc[e];
+    __syncthreads();
+    const int per_block = kWarps / q.ks * kGroup;
+    for (int v = threadIdx.x; v < per_block * t; v += 32 * kWarps) {
+        const int m = v / per_block, li = v - m * per_block;  // neighbouring threads: neighbouring features
+        const int64_t i = static_cast<int64_t>(blockIdx.x) * per_block + li;
+        if (i >= p.n) continue;
+        float z = 0.0f;
+        for (int k = 0; k < q.ks; ++k) z += sums[li / kGroup * q.ks + k][li % kGroup][m];
+        if (p.bias) z += to_float(static_cast<const T*>(p.bias)[i]);
+        float y = 0.0f;
+        with_act(p.act, [&](auto a) { y = act_value<decltype(a)::value, std::is_same<T, bf16>::value>(z); });
+        if (p.residual) y += to_float(static_cast<const T*>(p.residual)[m * p.ldr + i]);
+        static_cast<T*>(p.y)[m * p.ldy + i] = from_float<T>(y);
+    }
+}
+
+}  // namespace
+
+// Shared memory of x's rows and scales.
+static size_t rows_shared(int64_t t, int64_t k) {
+    const int64_t kbs = (k + SGEMM_BLOCK - 1) / SGEMM_BLOCK;
+    return static_cast<size_t>(t) * (kbs * SGEMM_BLOCK + 64 + kbs * 4);
+}
+
+bool block_few_rows(int64_t t, int64_t k) { return t <= kMostRows && k > 0 && rows_shared(t, k) <= kMostShared; }
+
+cudaError_t launch_block_rows(const BlockProduct& b, int num_sms, cudaStream_t st) {
+    RowsParams q{};
+    q.b = b;
+    q.raw = b.x_scales == nullptr;
+    q.kbs = static_cast<int>((b.k + SGEMM_BLOCK - 1) / SGEMM_BLOCK);
+    q.x_stride = q.kbs * SGEMM_BLOCK + 64;
+    q.vec = b.dtype == SGEMM_F32 ? rows_aligned<float>(b.x, b.t == 1 ? 0 : b.ldx) : rows_aligned<bf16>(b.x, b.t == 1 ? 0 : b.ldx);
+    // a weight row's k is shared while there are fewer than sixteen warps per SM and each keeps two blocks
+    const int64_t groups = (b.n + kGroup - 1) / kGroup;
+    q.ks = 1;
+    while (q.ks < kWarps && groups * q.ks < int64_t(8) * num_sms && q.kbs >= 2 * kAhead * q.ks) q.ks *= 2;
+    const int64_t per_block = kWarps / q.ks * kGroup;
+    const size_t smem = rows_shared(b.t, b.k);
+    auto go = [&](auto zero) {
+        using T = decltype(zero);
+        auto kern = block_rows_kernel<T>;
+        static std::atomic<uint64_t> smem_set{0};
+        const cudaError_t e = set_smem_limit_once(smem_set, reinterpret_cast<const void*>(kern), static_cast<int>(kMostShared));
+        if (e != cudaSuccess) return e;
+        return launch_kernel(true, kern, dim3(static_cast<unsigned>((b.n + per_block - 1) / per_block)), dim3(32 * kWarps),
+                             smem, st, q);
+    };
+    return b.dtype == SGEMM_F32 ? go(float()) : go(bf16());
+}
+
+}  // namespace pg

@@ -149,7 +149,7 @@ bool few_rows(const Product& p) {
     if (p.dtype == SGEMM_F32)
         return p.groups == 1 ? p.nj <= std::min<int64_t>(16, p.nk / 8 + 1)
                              : p.nj <= lists * std::min<int64_t>(aligned ? 24 : 16, p.nk / 32 + 1);
-    if (p.gated) return p.nj <= (aligned ? 3 : std::min<int64_t>(4, p.nk / 64 + 1));
+    if (p.gated) return p.nj <= (aligned ? 2 : std::min<int64_t>(4, p.nk / 64 + 1));
     if (!aligned) return p.nj <= lists * std::min<int64_t>(4, p.nk / 64 + 1);
     return p.groups == 1 ? p.nj <= 3 && p.ni * p.nk <= int64_t(1) << 25 : 2 * p.nj <= p.groups && p.nk >= 256;
 }
@@ -524,12 +524,15 @@ PG_EXPORT int sgemm_block_linear(int dtype, int64_t t, int64_t n, int64_t k, con
     CallContext c;
     PG_CHECK(call_begin(&c));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool few = block_few_rows(t, k) && c.force_bn == 0 && c.force_split == 0;
     const BlockPlan plan = plan_block(t, n, k, c.sms, c.force_bn, c.force_split);
     return with_workspace(c, st, [&](Arena& a) {
         BlockProduct p{dtype, t, n, k, static_cast<const uint8_t*>(x), ldx, x_scales, ldxs, 1, w, ldw, w_scales, ldws, bias,
                        act, residual, ldr, y, ldy};
         int launches = 0;
-        if (k > 0 && x_scales == nullptr) {
+        if (few && x_scales == nullptr && t <= kRawRows) {
+            // the kernel rounds x itself
+        } else if (k > 0 && x_scales == nullptr) {
             // scales of neighbouring rows side by side: the product's lanes are rows
             const int64_t ldq = (k + 15) / 16 * 16;
             uint8_t* q = static_cast<uint8_t*>(a.take(static_cast<size_t>(t) * ldq));
@@ -548,8 +551,14 @@ PG_EXPORT int sgemm_block_linear(int dtype, int64_t t, int64_t n, int64_t k, con
             PG_CHECK(place_bytes(c, p.x, p.ldx, t, k, a, st));
         }
         if (k > 0) PG_CHECK(place_bytes(c, p.w, p.ldw, n, k, a, st));
-        float* part = static_cast<float*>(a.take(plan.part_bytes));
+        float* part = few ? nullptr : static_cast<float*>(a.take(plan.part_bytes));
         if (a.dry()) return 0;
+        if (few) {
+            const cudaError_t e = launch_block_rows(p, c.sms, st);
+            if (e != cudaSuccess) return call_fail_cuda(e, "block product of few rows");
+            call_count(1);
+            return 0;
+        }
         PG_CHECK(launch_block(c, p, plan, part, st, &launches));
         call_count(launches);
         return 0;

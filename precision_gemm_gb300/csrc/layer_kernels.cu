@@ -406,15 +406,22 @@ static cudaError_t run_dact(int64_t rows, int64_t n, const void* dy, int64_t ldd
     return e;
 }
 
-size_t gate_part_bytes(int64_t rows, int64_t n, int num_sms) {
+// Slabs of the gate's backward pass: as slab_rows, down to 8 rows (one per thread) while that makes
+// fewer than four blocks per SM.
+static int gate_slab_rows(int64_t rows, int64_t n, int num_sms) {
     const int slab = slab_rows(rows, n, num_sms);
+    return slab > 32 || ((rows + 31) / 32) * ((n + kWidth - 1) / kWidth) >= int64_t(4) * num_sms ? slab : 8;
+}
+
+size_t gate_part_bytes(int64_t rows, int64_t n, int num_sms) {
+    const int slab = gate_slab_rows(rows, n, num_sms);
     return static_cast<size_t>((rows + slab - 1) / slab) * 2 * n * 4;
 }
 
 template <typename T, int PARTS>
 static cudaError_t run_dgate(int64_t rows, int64_t n, const void* dy, int64_t lddy, const void* z, int64_t ldz, int act,
                              bf16* dz, int64_t lddz, void* dbias, float* part, int num_sms, cudaStream_t st) {
-    const int slab = slab_rows(rows, n, num_sms);
+    const int slab = gate_slab_rows(rows, n, num_sms);
     const dim3 grid(static_cast<unsigned>(((rows + slab - 1) / slab) * ((n + kWidth - 1) / kWidth)));
     const bool vec = n % 8 == 0 && rows_aligned<T>(dy, lddy) && rows_aligned<T>(z, ldz);
     cudaError_t e = cudaSuccess;

@@ -440,6 +440,11 @@ BlockPlan plan_block(int64_t t, int64_t n, int64_t k, int num_sms, int force_bn,
 int launch_block(const CallContext& c, const BlockProduct& p, const BlockPlan& plan, float* part, cudaStream_t st,
                  int* launches);
 
+// The same for up to eight rows (block_few_rows), x of the call's type (x_scales null) or e4m3.
+constexpr int kRawRows = 2;  // of x that each thread block rounds by itself rather than a kernel before it
+bool block_few_rows(int64_t t, int64_t k);
+cudaError_t launch_block_rows(const BlockProduct& p, int num_sms, cudaStream_t st);
+
 // Layer norm (norm.cu).  part: norm_part_bytes(), read where dw or db is asked for.
 cudaError_t launch_norm(int dtype, int64_t rows, int64_t n, const void* x, int64_t ldx, const void* w, const void* b,
                         float eps, void* y, int64_t ldy, float* mean, float* rstd, int num_sms, cudaStream_t st);

@@ -604,7 +604,7 @@ PG_EXPORT int sgemm_layer_norm_backward(int dtype, int64_t t, int64_t n, const v
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool sums = dw || dbias;
     return with_workspace(c, st, [&](Arena& a) {
-        float* part = sums ? static_cast<float*>(a.take(norm_part_bytes(dtype, t, n, c.sms))) : nullptr;
+        float* part = sums ? static_cast<float*>(a.take(norm_part_bytes(t, n, c.sms))) : nullptr;
         if (a.dry()) return 0;
         const cudaError_t e = launch_norm_backward(dtype, t, n, dy, lddy, x, ldx, w, mean, rstd, residual, ldr, dx, lddx,
                                                    dw, dbias, part, c.sms, st);

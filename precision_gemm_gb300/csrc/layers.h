@@ -448,7 +448,7 @@ cudaError_t launch_block_rows(const BlockProduct& p, int num_sms, cudaStream_t s
 // Layer norm (norm.cu).  part: norm_part_bytes(), read where dw or db is asked for.
 cudaError_t launch_norm(int dtype, int64_t rows, int64_t n, const void* x, int64_t ldx, const void* w, const void* b,
                         float eps, void* y, int64_t ldy, float* mean, float* rstd, int num_sms, cudaStream_t st);
-size_t norm_part_bytes(int dtype, int64_t rows, int64_t n, int num_sms);
+size_t norm_part_bytes(int64_t rows, int64_t n, int num_sms);
 int norm_backward_launches(int64_t rows, int64_t n, bool dx, bool sums);
 cudaError_t launch_norm_backward(int dtype, int64_t rows, int64_t n, const void* dy, int64_t lddy, const void* x,
                                  int64_t ldx, const void* w, const float* mean, const float* rstd,

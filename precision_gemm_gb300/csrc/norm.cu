@@ -5,15 +5,20 @@
 //     g = dy w,  dx = rstd (g - sum g / n - h sum(g h) / n) + residual,
 //     dw = sum over rows of dy h,  db = sum over rows of dy.
 //
-// A team of W warps takes a row and keeps it in registers: one pass over memory, the
-// mean first and then the squares around it, so that a mean far from zero costs no
-// bits.  HBM-bound: a row is read once and its result written once.
+// HBM-bound: a row is read once and its result written once.  A team of warps takes a row, 64 bytes
+// per thread where the row is long enough, and walks on by as many rows as there are teams; a
+// row's sums cost two or three trips through a team's warps, which other teams' rows hide.  The
+// next rows are on their way meanwhile, by asynchronous copies into places in shared memory that
+// only the thread itself reads: no barrier is needed for them, and no registers are held.  The
+// mean is formed first and then the squares around it, so that a mean far from zero costs no bits.
 //
-// In the backward pass a thread's columns stay the same from row to row, so the sums
-// for dw and db stay in its registers; a block's teams add theirs in order, and
-// norm_sum_kernel adds the blocks' sums in order: equal inputs give equal bits.
-// Rows too wide for the registers are read again for each of the passes.
+// In the backward pass a thread's columns stay the same from row to row, so the sums for dw and
+// db stay in its registers; a block's teams add theirs in order, and norm_sum_kernel adds the
+// blocks' sums in order: equal inputs give equal bits.  Rows too wide for that are read again for
+// each of the passes.
 #include <algorithm>
+#include <initializer_list>
+#include <utility>
 
 #include "layers.h"
 #include "ptx.cuh"
@@ -22,53 +27,125 @@ namespace pg {
 namespace {
 
 constexpr int kWarp = 32;
+constexpr int kMostThreads = 512;                            // of a block
+constexpr int kForwardThreads = 1024;  // of an SM: 64 registers each
+constexpr int kBackwardBlocks = 2;     // of 256 threads in the backward pass, whose sums take registers
 
-// Column `t` of a thread's vector j: eight neighbours (VEC: 16-byte accesses), or every
-// team-th column, so that a warp's single accesses fall on one line where rows start
-// anywhere.
-template <bool VEC>
-__device__ __forceinline__ int64_t column(int tid, int team, int j, int t) {
-    return VEC ? 8 * (tid + static_cast<int64_t>(team) * j) + t : tid + static_cast<int64_t>(team) * (8 * j + t);
+// The widest access that rows allow, in elements: G of them lie side by side and 16 bytes are the
+// most.  A thread has vectors of eight elements, 8 / G accesses, each side by side with its
+// neighbours': element t of vector j is column(tid, team, j, t).
+template <int G>
+__device__ __forceinline__ int column(int tid, int team, int j, int t) {
+    return G * (tid + team * (8 / G * j + t / G)) + t % G;
 }
 
-// A thread's eight elements as they are stored, loaded without a use of them in between.
+// A thread's eight elements as they are stored, taken and put two at a time (a bfloat16 is the upper half
+// of its float).
 template <typename T>
 struct Raw {
     uint4 q[sizeof(T) / 2];
-    __device__ __forceinline__ float operator[](int t) const { return to_float(reinterpret_cast<const T*>(q)[t]); }
+    __device__ __forceinline__ float2 pair(int t) const {
+        if constexpr (sizeof(T) == 2) {
+            const uint32_t w = reinterpret_cast<const uint32_t*>(q)[t];
+            return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+        } else {
+            return reinterpret_cast<const float2*>(q)[t];
+        }
+    }
+    __device__ __forceinline__ void set(int t, float2 v) {
+        if constexpr (sizeof(T) == 2)
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(reinterpret_cast<uint32_t*>(q)[t]) : "f"(v.y), "f"(v.x));
+        else
+            reinterpret_cast<float2*>(q)[t] = v;
+    }
 };
 
-// Row p's elements of vector j, zero past n (n is a multiple of 8 where VEC).
-template <typename T, bool VEC, bool STREAM>
-__device__ __forceinline__ void fetch(const T* p, int64_t n, int tid, int team, int j, Raw<T>& v) {
-    if (VEC) {
-        const int64_t c = column<VEC>(tid, team, j, 0);
+template <int BYTES>
+struct Word;
+template <>
+struct Word<2> { using type = uint16_t; };
+template <>
+struct Word<4> { using type = uint32_t; };
+template <>
+struct Word<8> { using type = uint2; };
+template <>
+struct Word<16> { using type = uint4; };
+
+// Vector j of a row at p, zeros past n (a multiple of G).
+template <typename T, int G>
+__device__ __forceinline__ void fetch(const T* p, int n, int tid, int team, int j, Raw<T>& v) {
+    using W = typename Word<G * sizeof(T)>::type;
+    W* to = reinterpret_cast<W*>(v.q);
 #pragma unroll
-        for (int q = 0; q < static_cast<int>(sizeof(T)) / 2; ++q) {
-            const uint4* at = reinterpret_cast<const uint4*>(p + c) + q;
-            v.q[q] = c < n ? (STREAM ? __ldcs(at) : *at) : make_uint4(0, 0, 0, 0);
-        }
-    } else {
-        T* e = reinterpret_cast<T*>(v.q);
-#pragma unroll
-        for (int t = 0; t < 8; ++t) {
-            const int64_t c = column<VEC>(tid, team, j, t);
-            e[t] = c < n ? p[c] : from_float<T>(0.0f);
-        }
+    for (int a = 0; a < 8 / G; ++a) {
+        const int c = column<G>(tid, team, j, G * a);
+        to[a] = c < n ? *reinterpret_cast<const W*>(p + c) : W{};
     }
 }
-template <typename T, bool VEC>
-__device__ __forceinline__ void put(T* p, int64_t n, int tid, int team, int j, const float (&v)[8]) {
-    if (VEC) {
-        const int64_t c = column<VEC>(tid, team, j, 0);
-        if (c < n) store8(p + c, true, 8, v);
-    } else {
+template <typename T, int G>
+__device__ __forceinline__ void put(T* p, int n, int tid, int team, int j, const Raw<T>& raw) {
+    using W = typename Word<G * sizeof(T)>::type;
 #pragma unroll
-        for (int t = 0; t < 8; ++t) {
-            const int64_t c = column<VEC>(tid, team, j, t);
-            if (c < n) p[c] = from_float<T>(v[t]);
+    for (int a = 0; a < 8 / G; ++a) {
+        const int c = column<G>(tid, team, j, G * a);
+        if (c < n) *reinterpret_cast<W*>(p + c) = reinterpret_cast<const W*>(raw.q)[a];
+    }
+}
+
+// A thread's places in shared memory: S stages of A arrays of V vectors, each access beside the
+// neighbouring threads'.  Single bfloat16 elements are too small to be copied asynchronously; such
+// rows are loaded where they are used.
+template <typename T, int G, int V, int A, int S, int NT>
+struct Stages {
+    static constexpr bool ASYNC = G * sizeof(T) >= 4;
+    static constexpr int BYTES = G * static_cast<int>(sizeof(T)), ACCESSES = 8 / G;
+    static constexpr int ARRAY = V * ACCESSES * BYTES * NT, STAGE = A * ARRAY;  // bytes
+    static constexpr size_t SHARED = ASYNC ? static_cast<size_t>(S) * STAGE : 0;
+    uint8_t* base;  // this thread's
+    __device__ __forceinline__ explicit Stages(uint8_t* memory, int n, int tid, int team)
+        : base(memory + BYTES * threadIdx.x) {
+        if constexpr (BYTES == 16) {  // what lies past the rows' end is zero, and no copy goes there
+            using W = typename Word<BYTES>::type;
+#pragma unroll
+            for (int k = 0; k < V * ACCESSES; ++k)
+                if (G * (tid + team * k) >= n)
+                    for (int q = 0; q < S * A; ++q) *reinterpret_cast<W*>(base + q * ARRAY + k * (BYTES * NT)) = W{};
         }
     }
+    // The row at p starts on its way.
+    __device__ __forceinline__ void start(int stage, int array, const T* p, int n, int tid, int team) const {
+        if constexpr (ASYNC) {
+            const uint32_t to = smem_u32(base) + stage * STAGE + array * ARRAY;
+#pragma unroll
+            for (int k = 0; k < V * ACCESSES; ++k) {
+                const int c = G * (tid + team * k);
+                if constexpr (BYTES == 16) {
+                    if (c < n)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + k * (BYTES * NT)), "l"(p + c) : "memory");
+                } else {  // (a branch for each of many small copies costs more than copies of nothing)
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(to + k * (BYTES * NT)),
+                                 "l"(c < n ? p + c : p), "n"(BYTES), "r"(c < n ? BYTES : 0)
+                                 : "memory");
+                }
+            }
+        }
+    }
+    // The row that was started, or the one at p where it could not be.
+    __device__ __forceinline__ void read(int stage, int array, const T* p, int n, int tid, int team, int j, Raw<T>& v) const {
+        if constexpr (ASYNC) {
+            using W = typename Word<BYTES>::type;
+            const uint8_t* from = base + stage * STAGE + array * ARRAY + j * (ACCESSES * BYTES * NT);
+#pragma unroll
+            for (int a = 0; a < ACCESSES; ++a) reinterpret_cast<W*>(v.q)[a] = *reinterpret_cast<const W*>(from + a * (BYTES * NT));
+        } else {
+            fetch<T, G>(p, n, tid, team, j, v);
+        }
+    }
+};
+__device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void wait_copies() {  // all but the last N groups
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -77,31 +154,49 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// The sum of v over a team of `warps` warps, the same in each of its threads; `slots` holds
-// a place for each warp of the block and is free again after the next call's barrier.
-__device__ __forceinline__ float team_sum(float v, int warps, float* slots) {
-    v = warp_sum(v);
-    if (warps == 1) return v;
-    const int warp = threadIdx.x / kWarp;
-    if (threadIdx.x % kWarp == 0) slots[warp] = v;
-    __syncthreads();
-    const int first = warp / warps * warps;
-    v = 0.0f;
-    for (int w = 0; w < warps; ++w) v += slots[first + w];
-    return v;
-}
+// A team of `warps` warps (a power of two, 16 at most) of a block.
+struct Team {
+    int warps, index, warp, lane;
+    __device__ __forceinline__ explicit Team(int w)
+        : warps(w), index(threadIdx.x / (w * kWarp)), warp(threadIdx.x / kWarp), lane(threadIdx.x % kWarp) {}
+    // a barrier of its threads alone (the block has at most eight teams; barrier 0 is the block's)
+    __device__ __forceinline__ void barrier() const {
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + index), "r"(warps * kWarp) : "memory");
+    }
+    // The sum of v over the team, the same in each thread; `slots` holds a place for each warp of the block
+    // and is free again after the team's next barrier.
+    __device__ __forceinline__ float sum(float v, float* slots) const {
+        v = warp_sum(v);
+        if (warps == 1) return v;
+        if (lane == 0) slots[warp] = v;
+        barrier();
+        v = slots[index * warps + (lane & (warps - 1))];
+        for (int o = warps / 2; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+        return v;
+    }
+    // Two sums at once, one in each half of a warp.
+    __device__ __forceinline__ float2 sum2(float2 v, float2* slots) const {
+        const bool upper = lane >= 16;
+        float s = (upper ? v.y : v.x) + __shfl_xor_sync(0xffffffffu, upper ? v.x : v.y, 16);
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (warps > 1) {
+            float* place = reinterpret_cast<float*>(slots) + (upper ? 1 : 0);
+            if (lane % 16 == 0) place[2 * warp] = s;
+            barrier();
+            s = place[2 * (index * warps + (lane & (warps - 1)))];
+            for (int o = warps / 2; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+        }
+        return make_float2(__shfl_sync(0xffffffffu, s, 0), __shfl_sync(0xffffffffu, s, 16));
+    }
+};
 
-// Two sums with one barrier.
-__device__ __forceinline__ float2 team_sum2(float2 v, int warps, float2* slots) {
-    v = make_float2(warp_sum(v.x), warp_sum(v.y));
-    if (warps == 1) return v;
-    const int warp = threadIdx.x / kWarp;
-    if (threadIdx.x % kWarp == 0) slots[warp] = v;
+// The sum over a block of 32 warps.
+__device__ __forceinline__ float block_sum(float v, float* slots) {
+    v = warp_sum(v);
+    if (threadIdx.x % kWarp == 0) slots[threadIdx.x / kWarp] = v;
     __syncthreads();
-    const int first = warp / warps * warps;
-    v = make_float2(0.0f, 0.0f);
-    for (int w = 0; w < warps; ++w) v = make_float2(v.x + slots[first + w].x, v.y + slots[first + w].y);
-    return v;
+    return warp_sum(slots[threadIdx.x % kWarp]);
 }
 
 struct NormParams {
@@ -116,54 +211,84 @@ struct NormParams {
     int warps;  // of a team
 };
 
-// V vectors of eight per thread.  16384 rows of 2048 float32: see the launcher.
-template <typename T, bool VEC, int V, int NT>
-__global__ void __launch_bounds__(NT) norm_kernel(const NormParams p) {
-    __shared__ float slots[2][NT / kWarp];
+// V vectors of eight per thread, S rows on their way per team.
+template <typename T, int G, int V, int S, int NT>
+__global__ void __launch_bounds__(NT, kForwardThreads / NT) norm_kernel(const NormParams p) {
+    __shared__ float slots[4][NT / kWarp];
+    extern __shared__ __align__(16) uint8_t memory[];
+    const Team whole(p.warps);
+    const int team = p.warps * kWarp, tid = threadIdx.x - whole.index * team, teams = NT / team;
+    const int n = static_cast<int>(p.n);
+    const Stages<T, G, V, 1, S, NT> stages(memory, n, tid, team);
     pdl_trigger();
     pdl_wait();
-    const int team = p.warps * kWarp, tid = threadIdx.x % team;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x / team) + threadIdx.x / team;
-    const bool there = row < p.rows;
-    const int64_t n = there ? p.n : 0;
-    const T* x = static_cast<const T*>(p.x) + (there ? row : 0) * p.ldx;
-    Raw<T> v[V];
+    const int64_t step = static_cast<int64_t>(gridDim.x) * teams;
+    int64_t row = static_cast<int64_t>(blockIdx.x) * teams + whole.index;
+    const T *w = static_cast<const T*>(p.w), *b = static_cast<const T*>(p.b);
+    auto start = [&](int stage, int64_t r) {
+        if (r < p.rows) stages.start(stage, 0, static_cast<const T*>(p.x) + r * p.ldx, n, tid, team);
+        commit_copies();
+    };
 #pragma unroll
-    for (int j = 0; j < V; ++j) fetch<T, VEC, true>(x, n, tid, team, j, v[j]);
-    float sum = 0.0f;
+    for (int s = 0; s + 1 < S; ++s) start(s, row + s * step);
+    const float inv = 1.0f / static_cast<float>(n);
+    int stage = 0, turn = 0;
+    for (; row < p.rows; row += step) {
+        start(stage == 0 ? S - 1 : stage - 1, row + (S - 1) * step);
+        wait_copies<S - 1>();
+        float2 v[V][4], sum = both(0.0f);
 #pragma unroll
-    for (int j = 0; j < V; ++j)
+        for (int j = 0; j < V; ++j) {
+            Raw<T> raw;
+            stages.read(stage, 0, static_cast<const T*>(p.x) + row * p.ldx, n, tid, team, j, raw);
 #pragma unroll
-        for (int t = 0; t < 8; ++t) sum += v[j][t];
-    const float count = static_cast<float>(p.n);
-    const float mean = team_sum(sum, p.warps, slots[0]) / count;
-    sum = 0.0f;
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-#pragma unroll
-        for (int t = 0; t < 8; ++t) {
-            const float d = v[j][t] - mean;
-            if (column<VEC>(tid, team, j, t) < n) sum = fmaf(d, d, sum);
+            for (int t = 0; t < 4; ++t) {
+                v[j][t] = raw.pair(t);
+                sum = add2(sum, v[j][t]);
+            }
         }
-    const float rstd = 1.0f / sqrtf(team_sum(sum, p.warps, slots[1]) / count + p.eps);
-    if (!there) return;
-    if (tid == 0) {
-        if (p.mean) p.mean[row] = mean;
-        if (p.rstd) p.rstd[row] = rstd;
-    }
-    T* y = static_cast<T*>(p.y) + row * p.ldy;
+        // two places for each sum, taken in turn: one barrier per sum
+        const float mean = whole.sum(sum.x + sum.y, slots[turn]) * inv;
+        sum = both(0.0f);
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        Raw<T> w, b;
-        if (p.w) fetch<T, VEC, false>(static_cast<const T*>(p.w), n, tid, team, j, w);
-        if (p.b) fetch<T, VEC, false>(static_cast<const T*>(p.b), n, tid, team, j, b);
-        float o[8];
+        for (int j = 0; j < V; ++j)
 #pragma unroll
-        for (int t = 0; t < 8; ++t) {
-            const float h = (v[j][t] - mean) * rstd;
-            o[t] = fmaf(h, p.w ? w[t] : 1.0f, p.b ? b[t] : 0.0f);
+            for (int t = 0; t < 4; ++t) {
+                v[j][t] = add2(v[j][t], both(-mean));
+                if (G == 1) {
+                    if (column<G>(tid, team, j, 2 * t) < n) sum.x = fmaf(v[j][t].x, v[j][t].x, sum.x);
+                    if (column<G>(tid, team, j, 2 * t + 1) < n) sum.y = fmaf(v[j][t].y, v[j][t].y, sum.y);
+                } else if (column<G>(tid, team, j, 2 * t / G * G) < n) {
+                    sum = fma2(v[j][t], v[j][t], sum);
+                }
+            }
+        const float rstd = 1.0f / sqrtf(whole.sum(sum.x + sum.y, slots[turn + 1]) * inv + p.eps);
+        turn ^= 2;
+        if (tid == 0) {
+            if (p.mean) p.mean[row] = mean;
+            if (p.rstd) p.rstd[row] = rstd;
         }
-        put<T, VEC>(y, n, tid, team, j, o);
+        T* y = static_cast<T*>(p.y) + row * p.ldy;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            Raw<T> wj, bj;
+            if (w) fetch<T, G>(w, n, tid, team, j, wj);
+            if (b) fetch<T, G>(b, n, tid, team, j, bj);
+            Raw<T> o;
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                float2 z = mul2(v[j][t], both(rstd));
+                if (w && b)
+                    z = fma2(z, wj.pair(t), bj.pair(t));
+                else if (w)
+                    z = mul2(z, wj.pair(t));
+                else if (b)
+                    z = add2(z, bj.pair(t));
+                o.set(t, z);
+            }
+            put<T, G>(y, n, tid, team, j, o);
+        }
+        stage = stage + 1 == S ? 0 : stage + 1;
     }
 }
 
@@ -180,13 +305,13 @@ __global__ void __launch_bounds__(1024) norm_wide_kernel(const NormParams p) {
     float sum = 0.0f;
     for (int64_t c = threadIdx.x; c < p.n; c += 1024) sum += to_float(x[c]);
     const float count = static_cast<float>(p.n);
-    const float mean = team_sum(sum, 32, slots[0]) / count;
+    const float mean = block_sum(sum, slots[0]) / count;
     sum = 0.0f;
     for (int64_t c = threadIdx.x; c < p.n; c += 1024) {
         const float d = to_float(x[c]) - mean;
         sum = fmaf(d, d, sum);
     }
-    const float rstd = 1.0f / sqrtf(team_sum(sum, 32, slots[1]) / count + p.eps);
+    const float rstd = 1.0f / sqrtf(block_sum(sum, slots[1]) / count + p.eps);
     if (threadIdx.x == 0) {
         if (p.mean) p.mean[row] = mean;
         if (p.rstd) p.rstd[row] = rstd;
@@ -214,99 +339,94 @@ struct NormBackwardParams {
     int warps;
 };
 
-// Teams walk over rows, the next row's loads on their way while a row is worked on (AHEAD; rows of
-// float32 leave no registers for it).
-template <typename T, bool VEC, int V, int NT, int B, bool AHEAD>
-__global__ void __launch_bounds__(NT, B) norm_backward_kernel(const NormBackwardParams p) {
+template <typename T, int G, int V, int S, int NT, int B>
+__global__ void __launch_bounds__(NT, B)
+    norm_backward_kernel(const NormBackwardParams p) {
     __shared__ float2 slots[2][NT / kWarp];
-    extern __shared__ float sums[];  // [team][8 V][team threads], where a block has several teams
+    extern __shared__ __align__(16) uint8_t memory[];
+    const Team whole(p.warps);
+    const int team = p.warps * kWarp, tid = threadIdx.x - whole.index * team, teams = NT / team;
+    const int n = static_cast<int>(p.n);
+    const Stages<T, G, V, 3, S, NT> stages(memory, n, tid, team);
     pdl_trigger();
     pdl_wait();
-    const int team = p.warps * kWarp, tid = threadIdx.x % team, teams = blockDim.x / team;
-    const int64_t n = p.n, step = static_cast<int64_t>(gridDim.x) * teams;
-    // every team of a block runs as many rounds, since they meet at its barriers
-    const int64_t rounds = (p.rows - static_cast<int64_t>(blockIdx.x) * teams + step - 1) / step;
-    int64_t row = static_cast<int64_t>(blockIdx.x) * teams + threadIdx.x / team;
-    struct Row {
-        Raw<T> x[V], dy[V], r[V];
-        float mean, rstd;
-    };
-    Raw<T> w[V];
-    float2 dw[V][4] = {}, db[V][4] = {};
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-        if (p.w) fetch<T, VEC, false>(static_cast<const T*>(p.w), n, tid, team, j, w[j]);
-    auto load = [&](Row& to, int64_t r) {
-        const int64_t there = r < p.rows ? n : 0;
-        if (r >= p.rows) r = 0;
-        to.mean = there ? p.mean[r] : 0.0f;
-        to.rstd = there ? p.rstd[r] : 0.0f;
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            fetch<T, VEC, true>(static_cast<const T*>(p.x) + r * p.ldx, there, tid, team, j, to.x[j]);
-            fetch<T, VEC, true>(static_cast<const T*>(p.dy) + r * p.lddy, there, tid, team, j, to.dy[j]);
-            if (p.residual)
-                fetch<T, VEC, true>(static_cast<const T*>(p.residual) + r * p.ldr, there, tid, team, j, to.r[j]);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * teams;
+    int64_t row = static_cast<int64_t>(blockIdx.x) * teams + whole.index;
+    auto start = [&](int stage, int64_t r) {
+        if (r < p.rows) {
+            stages.start(stage, 0, static_cast<const T*>(p.x) + r * p.ldx, n, tid, team);
+            stages.start(stage, 1, static_cast<const T*>(p.dy) + r * p.lddy, n, tid, team);
+            if (p.residual) stages.start(stage, 2, static_cast<const T*>(p.residual) + r * p.ldr, n, tid, team);
         }
+        commit_copies();
     };
-    Row at, next;
-    if (AHEAD) load(next, row);
+#pragma unroll
+    for (int s = 0; s + 1 < S; ++s) start(s, row + s * step);
+    float2 w[V][4], dw[V][4] = {}, db[V][4] = {};
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        Raw<T> raw;
+        if (p.w) fetch<T, G>(static_cast<const T*>(p.w), n, tid, team, j, raw);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) w[j][t] = p.w ? raw.pair(t) : both(1.0f);
+    }
+    float next_mean = 0.0f, next_rstd = 0.0f;
+    auto statistics = [&](int64_t r) {
+        next_mean = r < p.rows ? p.mean[r] : 0.0f;
+        next_rstd = r < p.rows ? p.rstd[r] : 0.0f;
+    };
+    statistics(row);
     const float inv = 1.0f / static_cast<float>(n);
-    for (int64_t round = 0; round < rounds; ++round, row += step) {
-        if (AHEAD) {
-            at = next;
-            if (round + 1 < rounds) load(next, row + step);
-        } else {
-            load(at, row);
-        }
-        const bool there = row < p.rows;
-        // two elements' (x - mean) rstd and dy w, formed again where they are needed; past the row's end
-        // dy is zero, and h must not meet it as an infinity
-        auto pair = [&](int j, int t, float2& h, float2& g, float2& d) {
-            d = make_float2(at.dy[j][2 * t], at.dy[j][2 * t + 1]);
-            const float2 x = make_float2(at.x[j][2 * t], at.x[j][2 * t + 1]);
-            h = mul2(add2(x, both(-at.mean)), both(at.rstd));
-            if (!VEC && (column<VEC>(tid, team, j, 2 * t) >= n || column<VEC>(tid, team, j, 2 * t + 1) >= n)) {
-                if (column<VEC>(tid, team, j, 2 * t) >= n) h.x = 0.0f;
-                h.y = 0.0f;
-            }
-            if (VEC && column<VEC>(tid, team, j, 0) >= n) h = both(0.0f);
-            g = p.w ? mul2(d, make_float2(w[j][2 * t], w[j][2 * t + 1])) : d;
+    int stage = 0, turn = 0;
+    for (; row < p.rows; row += step) {
+        start(stage == 0 ? S - 1 : stage - 1, row + (S - 1) * step);
+        const float mean = next_mean, rstd = next_rstd;
+        statistics(row + step);
+        wait_copies<S - 1>();
+        auto read = [&](int j, Raw<T>& x, Raw<T>& dy) {
+            stages.read(stage, 0, static_cast<const T*>(p.x) + row * p.ldx, n, tid, team, j, x);
+            stages.read(stage, 1, static_cast<const T*>(p.dy) + row * p.lddy, n, tid, team, j, dy);
         };
         float2 s1 = both(0.0f), s2 = both(0.0f);
 #pragma unroll
-        for (int j = 0; j < V; ++j)
+        for (int j = 0; j < V; ++j) {
+            Raw<T> x, dy;
+            read(j, x, dy);
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-                float2 h, g, d;
-                pair(j, t, h, g, d);
-                dw[j][t] = fma2(d, h, dw[j][t]);
+                // past the row's end x and dy are zero
+                const float2 d = dy.pair(t), c = add2(x.pair(t), both(-mean)), g = p.w ? mul2(d, w[j][t]) : d;
+                dw[j][t] = fma2(mul2(d, both(rstd)), c, dw[j][t]);
                 db[j][t] = add2(db[j][t], d);
                 s1 = add2(s1, g);
-                s2 = fma2(g, h, s2);
-            }
-        if (p.dx) {
-            // two places for the sums, taken in turn: one barrier a round
-            const float2 s = team_sum2(make_float2(s1.x + s1.y, s2.x + s2.y), p.warps, slots[round & 1]);
-            if (there) {
-                T* dx = static_cast<T*>(p.dx) + row * p.lddx;
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    float o[8];
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        float2 h, g, d;
-                        pair(j, t, h, g, d);
-                        const float2 v = fma2(h, both(-s.y * inv), add2(g, both(-s.x * inv)));
-                        const float2 r = p.residual ? make_float2(at.r[j][2 * t], at.r[j][2 * t + 1]) : both(0.0f);
-                        const float2 y = fma2(v, both(at.rstd), r);
-                        o[2 * t] = y.x;
-                        o[2 * t + 1] = y.y;
-                    }
-                    put<T, VEC>(dx, n, tid, team, j, o);
-                }
+                s2 = fma2(g, c, s2);
             }
         }
+        if (p.dx) {
+            // two places for the sums, taken in turn: one barrier a round
+            const float2 s = whole.sum2(make_float2(s1.x + s1.y, s2.x + s2.y), slots[turn]);
+            turn ^= 1;
+            // dx = rstd g - rstd sum g / n - (x - mean) rstd^3 sum(g (x - mean)) / n + residual
+            const float2 a = both(-rstd * (rstd * s.y * inv) * rstd), c0 = both(-rstd * (s.x * inv));
+            T* dx = static_cast<T*>(p.dx) + row * p.lddx;
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                Raw<T> x, dy, r;
+                read(j, x, dy);
+                if (p.residual)
+                    stages.read(stage, 2, static_cast<const T*>(p.residual) + row * p.ldr, n, tid, team, j, r);
+                Raw<T> o;
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    const float2 scale = p.w ? mul2(w[j][t], both(rstd)) : both(rstd);
+                    float2 y = fma2(dy.pair(t), scale, fma2(add2(x.pair(t), both(-mean)), a, c0));
+                    if (p.residual) y = add2(y, r.pair(t));
+                    o.set(t, y);
+                }
+                put<T, G>(dx, n, tid, team, j, o);
+            }
+        }
+        stage = stage + 1 == S ? 0 : stage + 1;
     }
     if (!p.part) return;
     float* out = p.part + static_cast<int64_t>(blockIdx.x) * 2 * n;
@@ -315,15 +435,17 @@ __global__ void __launch_bounds__(NT, B) norm_backward_kernel(const NormBackward
         float2(&mine)[V][4] = which ? db : dw;
         auto value = [&](int j, int t) { return t & 1 ? mine[j][t / 2].y : mine[j][t / 2].x; };
         if (teams > 1) {  // the block's first team adds the others' sums in order
+            float* sums = reinterpret_cast<float*>(memory);  // [team][8 V][team threads]
+            wait_copies<0>();
             __syncthreads();
 #pragma unroll
             for (int j = 0; j < V; ++j)
 #pragma unroll
-                for (int t = 0; t < 8; ++t) sums[(threadIdx.x / team * (8 * V) + 8 * j + t) * team + tid] = value(j, t);
+                for (int t = 0; t < 8; ++t) sums[(whole.index * (8 * V) + 8 * j + t) * team + tid] = value(j, t);
             __syncthreads();
             for (int q = threadIdx.x; q < 8 * V * team; q += blockDim.x) {
                 const int jt = q / team;
-                const int64_t c = column<VEC>(q % team, team, jt / 8, jt % 8);
+                const int c = column<G>(q % team, team, jt / 8, jt % 8);
                 if (c >= n) continue;
                 float s = 0.0f;
                 for (int k = 0; k < teams; ++k) s += sums[k * (8 * V) * team + q];
@@ -334,7 +456,7 @@ __global__ void __launch_bounds__(NT, B) norm_backward_kernel(const NormBackward
             for (int j = 0; j < V; ++j)
 #pragma unroll
                 for (int t = 0; t < 8; ++t) {
-                    const int64_t c = column<VEC>(tid, team, j, t);
+                    const int c = column<G>(tid, team, j, t);
                     if (c < n) out[c] = value(j, t);
                 }
         }
@@ -344,7 +466,7 @@ __global__ void __launch_bounds__(NT, B) norm_backward_kernel(const NormBackward
 // dx of rows of any width, a block to each.
 template <typename T>
 __global__ void __launch_bounds__(1024) norm_backward_wide_kernel(const NormBackwardParams p) {
-    __shared__ float2 slots[32];
+    __shared__ float slots[2][32];
     pdl_trigger();
     pdl_wait();
     const int64_t row = blockIdx.x;
@@ -359,9 +481,8 @@ __global__ void __launch_bounds__(1024) norm_backward_wide_kernel(const NormBack
         s2 = fmaf(g, (to_float(x[c]) - mean) * rstd, s2);
     }
     const float inv = 1.0f / static_cast<float>(p.n);
-    const float2 s = team_sum2(make_float2(s1, s2), 32, slots);
-    s1 = s.x * inv;
-    s2 = s.y * inv;
+    s1 = block_sum(s1, slots[0]) * inv;
+    s2 = block_sum(s2, slots[1]) * inv;
     T* dx = static_cast<T*>(p.dx) + row * p.lddx;
     const T* r = p.residual ? static_cast<const T*>(p.residual) + row * p.ldr : nullptr;
     for (int64_t c = threadIdx.x; c < p.n; c += 1024) {
@@ -442,64 +563,112 @@ int team_warps(int64_t n, int v) {
     return w;
 }
 
-template <typename T, bool VEC, int V, int NT>
-cudaError_t run_norm(NormParams p, cudaStream_t st) {
-    p.warps = team_warps(p.n, V);
-    const int threads = std::max(p.warps * kWarp, 256);
-    return launch_kernel(true, norm_kernel<T, VEC, V, NT>,
-                         dim3(static_cast<unsigned>(cdiv(p.rows, threads / (p.warps * kWarp)))), dim3(threads), 0, st, p);
-}
-
-template <typename T, bool VEC>
-cudaError_t norm(const NormParams& p, int num_sms, cudaStream_t st) {
-    if (p.n > 32 * kWarp * 32)
-        return launch_kernel(true, norm_wide_kernel<T>, dim3(static_cast<unsigned>(p.rows)), dim3(1024), 0, st, p);
-    if (p.n > 8 * kWarp * 32) return run_norm<T, VEC, 4, 1024>(p, st);
-    // fewer elements per thread while the SMs are not full
-    const int64_t vectors = p.rows * cdiv(p.n, 8), full = int64_t(1024) * num_sms;
-    if (p.n > 8 * kWarp * 16 || vectors >= 4 * full) return run_norm<T, VEC, 4, 256>(p, st);
-    if (p.n > 8 * kWarp * 8 || vectors >= 2 * full) return run_norm<T, VEC, 2, 256>(p, st);
-    return run_norm<T, VEC, 1, 256>(p, st);
-}
-
-// The backward pass's shape: rows held in registers up to kHeld columns, eight of them per thread
-// (sixteen of bfloat16 from 2048 on).
-constexpr int64_t kHeld = 8192;
-struct BackwardShape {
-    int v, nt, blocks_per_sm, warps, teams;
+// Rows are held by teams: 64 bytes per thread, less where one warp then holds the row, twice as much
+// where 512 threads hold it no other way.
+constexpr int64_t kHeld = 16384;
+struct Shape {
+    int v, threads, warps, teams;
     int64_t blocks;
 };
-BackwardShape backward_shape(int dtype, int64_t rows, int64_t n, int num_sms) {
-    BackwardShape s{};
-    s.v = dtype == SGEMM_BF16 && n > 2048 ? 2 : 1;
+template <typename T>
+Shape shape_of(int64_t rows, int64_t n, int most_v, int small_blocks, int large_blocks, int num_sms) {
+    Shape s{};
+    s.v = 1;
+    while (s.v < most_v && s.v * kWarp * 8 < n) s.v *= 2;
+    while (s.v * kMostThreads * 8 < n) s.v *= 2;
     s.warps = team_warps(n, s.v);
-    s.nt = std::max(s.warps * kWarp, 256);
-    s.blocks_per_sm = s.v == 2 ? (s.nt == 256 ? 2 : 1) : 1024 / s.nt;
-    s.teams = s.nt / (s.warps * kWarp);
-    s.blocks = std::min<int64_t>(cdiv(rows, s.teams), static_cast<int64_t>(s.blocks_per_sm) * num_sms);
+    s.threads = std::max(s.warps * kWarp, 256);
+    s.teams = s.threads / (s.warps * kWarp);
+    s.blocks = std::min<int64_t>(cdiv(rows, s.teams), static_cast<int64_t>(s.threads > 256 ? large_blocks : small_blocks) * num_sms);
     return s;
 }
 
-template <typename T, bool VEC, int V, int NT, int B, bool AHEAD>
-cudaError_t run_backward(const NormBackwardParams& p, const BackwardShape& s, cudaStream_t st) {
-    const size_t smem = s.teams > 1 && p.part ? static_cast<size_t>(s.nt) * 8 * V * 4 : 0;
-    return launch_kernel(true, norm_backward_kernel<T, VEC, V, NT, B, AHEAD>, dim3(static_cast<unsigned>(s.blocks)),
-                         dim3(s.nt), smem, st, p);
+// Rows of single elements take eight per thread: their addresses are many.
+int most_vectors(int access, int most) { return access == 1 ? 1 : most; }
+template <typename T>
+Shape backward_shape(int64_t rows, int64_t n, int access, int num_sms) {
+    return shape_of<T>(rows, n, most_vectors(access, 2), kBackwardBlocks, 1, num_sms);
 }
 
-template <typename T, bool VEC>
-cudaError_t norm_backward(NormBackwardParams p, const BackwardShape& s, cudaStream_t st) {
-    p.warps = s.warps;
-    if constexpr (std::is_same<T, bf16>::value) {
-        if (s.v == 2)
-            return s.nt > 256 ? run_backward<T, VEC, 2, 512, 1, true>(p, s, st)
-                              : run_backward<T, VEC, 2, 256, 2, true>(p, s, st);
-        return run_backward<T, VEC, 1, 256, 4, true>(p, s, st);
-    } else {
-        if (s.nt > 512) return run_backward<T, VEC, 1, 1024, 1, false>(p, s, st);
-        return s.nt > 256 ? run_backward<T, VEC, 1, 512, 2, false>(p, s, st)
-                          : run_backward<T, VEC, 1, 256, 4, false>(p, s, st);
+// The widest access (elements) that every row allows.
+template <typename T>
+int widest(int64_t n, std::initializer_list<std::pair<const void*, int64_t>> rows) {
+    for (int g : {static_cast<int>(16 / sizeof(T)), 4}) {
+        bool ok = n % g == 0;
+        for (const auto& r : rows)
+            ok = ok && reinterpret_cast<uintptr_t>(r.first) % (g * sizeof(T)) == 0 && r.second % g == 0;
+        if (ok) return g;
     }
+    return 1;
+}
+// f(integral_constant<widest access>)
+template <typename T, typename F>
+cudaError_t with_access(int g, F f) {
+    if (g == 1) return f(std::integral_constant<int, 1>());
+    if (sizeof(T) == 2 && g == 8) return f(std::integral_constant<int, sizeof(T) == 2 ? 8 : 4>());
+    return f(std::integral_constant<int, 4>());
+}
+
+template <typename F, typename P>
+cudaError_t launch_rows(F kern, std::atomic<uint64_t>& done, size_t shared, const P& p, const Shape& s, cudaStream_t st) {
+    const cudaError_t e = set_smem_limit_once(done, reinterpret_cast<const void*>(kern), static_cast<int>(shared));
+    if (e != cudaSuccess) return e;
+    return launch_kernel(true, kern, dim3(static_cast<unsigned>(s.blocks)), dim3(s.threads), shared, st, p);
+}
+
+// Stages: an SM's shared memory holds three rows of 64 bytes per thread in the forward pass, two of each
+// of the backward pass's three matrices; more of less, and of twice as much one row.
+template <typename T, int G, int V>
+cudaError_t run_norm(const NormParams& p, const Shape& s, cudaStream_t st) {
+    constexpr int BYTES = 8 * V * static_cast<int>(sizeof(T)), S = BYTES > 64 ? 1 : (BYTES == 64 ? 3 : 6);
+    // (two kernels by their blocks' size, so that each has one limit of shared memory)
+    static std::atomic<uint64_t> done[2];
+    if (s.threads > 256)
+        return launch_rows(norm_kernel<T, G, V, S, kMostThreads>, done[0], Stages<T, G, V, 1, S, kMostThreads>::SHARED, p, s, st);
+    return launch_rows(norm_kernel<T, G, V, S, 256>, done[1], Stages<T, G, V, 1, S, 256>::SHARED, p, s, st);
+}
+template <typename T, int G, int V>
+cudaError_t run_backward(const NormBackwardParams& p, const Shape& s, cudaStream_t st) {
+    constexpr int BYTES = 8 * V * static_cast<int>(sizeof(T)), S = BYTES > 64 ? 1 : 128 / BYTES;
+    if (s.threads > 256) {
+        static std::atomic<uint64_t> done{0};
+        return launch_rows(norm_backward_kernel<T, G, V, S, kMostThreads, 1>, done, Stages<T, G, V, 3, S, kMostThreads>::SHARED,
+                           p, s, st);
+    }
+    constexpr int B = kBackwardBlocks;
+    static std::atomic<uint64_t> done{0};
+    // the teams' sums use the same memory
+    return launch_rows(norm_backward_kernel<T, G, V, S, 256, B>, done,
+                       std::max(Stages<T, G, V, 3, S, 256>::SHARED, static_cast<size_t>(256) * 8 * V * 4), p, s, st);
+}
+// f(widest access, vectors per thread) as constants
+template <typename T, typename F>
+cudaError_t with_shape(int g, int v, F f) {
+    return with_access<T>(g, [&](auto access) {
+        if (v == 1) return f(access, std::integral_constant<int, 1>());
+        if (v == 2) return f(access, std::integral_constant<int, 2>());
+        return f(access, std::integral_constant<int, 4>());
+    });
+}
+
+template <typename T>
+cudaError_t norm(NormParams p, int num_sms, cudaStream_t st) {
+    if (p.n > kHeld)
+        return launch_kernel(true, norm_wide_kernel<T>, dim3(static_cast<unsigned>(p.rows)), dim3(1024), 0, st, p);
+    const int access = widest<T>(p.n, {{p.x, p.ldx}, {p.y, p.ldy}, {p.w, 0}, {p.b, 0}});
+    const Shape s = shape_of<T>(p.rows, p.n, most_vectors(access, 8 / static_cast<int>(sizeof(T))), kForwardThreads / 256,
+                                kForwardThreads / kMostThreads, num_sms);
+    p.warps = s.warps;
+    return with_shape<T>(access, s.v, [&](auto g, auto v) {
+        return run_norm<T, decltype(g)::value, decltype(v)::value>(p, s, st);
+    });
+}
+template <typename T>
+cudaError_t norm_backward(NormBackwardParams p, const Shape& s, int access, cudaStream_t st) {
+    p.warps = s.warps;
+    return with_shape<T>(access, s.v, [&](auto g, auto v) {
+        return run_backward<T, decltype(g)::value, decltype(v)::value>(p, s, st);
+    });
 }
 
 template <typename T>
@@ -508,11 +677,10 @@ cudaError_t backward(const NormBackwardParams& p, T* dw, T* db, int num_sms, cud
     int64_t blocks = 0;
     cudaError_t e = cudaSuccess;
     if (p.rows > 0 && p.n <= kHeld) {
-        const BackwardShape s = backward_shape(std::is_same<T, bf16>::value ? SGEMM_BF16 : SGEMM_F32, p.rows, p.n, num_sms);
+        const int access = widest<T>(p.n, {{p.dy, p.lddy}, {p.x, p.ldx}, {p.w, 0}, {p.residual, p.ldr}, {p.dx, p.lddx}});
+        const Shape s = backward_shape<T>(p.rows, p.n, access, num_sms);
         blocks = s.blocks;
-        const bool vec = p.n % 8 == 0 && rows_aligned<T>(p.dy, p.lddy) && rows_aligned<T>(p.x, p.ldx) &&
-                         rows_aligned<T>(p.w, 0) && rows_aligned<T>(p.residual, p.ldr) && rows_aligned<T>(p.dx, p.lddx);
-        e = vec ? norm_backward<T, true>(p, s, st) : norm_backward<T, false>(p, s, st);
+        e = norm_backward<T>(p, s, access, st);
     } else if (p.rows > 0) {
         blocks = cdiv(p.rows, kSlab);
         if (p.dx)
@@ -532,18 +700,15 @@ cudaError_t backward(const NormBackwardParams& p, T* dw, T* db, int num_sms, cud
 cudaError_t launch_norm(int dtype, int64_t rows, int64_t n, const void* x, int64_t ldx, const void* w, const void* b,
                         float eps, void* y, int64_t ldy, float* mean, float* rstd, int num_sms, cudaStream_t st) {
     const NormParams p{rows, n, x, ldx, w, b, eps, y, ldy, mean, rstd, 1};
-    auto go = [&](auto zero) {
-        using T = decltype(zero);
-        const bool vec = n % 8 == 0 && rows_aligned<T>(x, ldx) && rows_aligned<T>(y, ldy) && rows_aligned<T>(w, 0) &&
-                         rows_aligned<T>(b, 0);
-        return vec ? norm<T, true>(p, num_sms, st) : norm<T, false>(p, num_sms, st);
-    };
-    return dtype == SGEMM_F32 ? go(float()) : go(bf16());
+    return dtype == SGEMM_F32 ? norm<float>(p, num_sms, st) : norm<bf16>(p, num_sms, st);
 }
 
-size_t norm_part_bytes(int dtype, int64_t rows, int64_t n, int num_sms) {
+// (whatever the rows' alignment turns out to be)
+size_t norm_part_bytes(int64_t rows, int64_t n, int num_sms) {
     if (rows == 0) return 0;
-    return static_cast<size_t>(n <= kHeld ? backward_shape(dtype, rows, n, num_sms).blocks : cdiv(rows, kSlab)) * 2 * n * 4;
+    int64_t blocks = cdiv(rows, kSlab);
+    if (n <= kHeld) blocks = std::min<int64_t>(rows, int64_t(kBackwardBlocks) * num_sms);
+    return static_cast<size_t>(blocks) * 2 * n * 4;
 }
 
 int norm_backward_launches(int64_t rows, int64_t n, bool dx, bool sums) {

@@ -159,7 +159,7 @@ struct Team {
     int warps, index, warp, lane;
     __device__ __forceinline__ explicit Team(int w)
         : warps(w), index(threadIdx.x / (w * kWarp)), warp(threadIdx.x / kWarp), lane(threadIdx.x % kWarp) {}
-    // a barrier of its threads alone (the block has at most eight teams; barrier 0 is the block's)
+    // a barrier of its threads alone (at most eight teams have several warps; barrier 0 is the block's)
     __device__ __forceinline__ void barrier() const {
         asm volatile("bar.sync %0, %1;" ::"r"(1 + index), "r"(warps * kWarp) : "memory");
     }
@@ -208,7 +208,8 @@ struct NormParams {
     void* y;
     int64_t ldy;
     float *mean, *rstd;
-    int warps;  // of a team
+    int warps;       // of a team
+    bool shared_wb;  // w and b have places in shared memory
 };
 
 // V vectors of eight per thread, S rows on their way per team.
@@ -231,6 +232,32 @@ __global__ void __launch_bounds__(NT, kForwardThreads / NT) norm_kernel(const No
     };
 #pragma unroll
     for (int s = 0; s + 1 < S; ++s) start(s, row + s * step);
+    // w and b stay in registers or, where they are too many, in shared memory: a thread reads what it
+    // put there (and every team puts the same); for teams of a whole block that would leave too little for the rows
+    constexpr bool KEEP = V * sizeof(T) <= 4;
+    constexpr int BYTES = G * static_cast<int>(sizeof(T));
+    Raw<T> kept_w[KEEP ? V : 1], kept_b[KEEP ? V : 1];
+    uint8_t* const shared_w = memory + Stages<T, G, V, 1, S, NT>::SHARED + BYTES * tid;
+    uint8_t* const shared_b = shared_w + BYTES * team * (V * (8 / G));
+    auto place = [&](uint8_t* base, int j, int a) {
+        return reinterpret_cast<typename Word<BYTES>::type*>(base + BYTES * team * (j * (8 / G) + a));
+    };
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        Raw<T> wj, bj;
+        if (w) fetch<T, G>(w, n, tid, team, j, wj);
+        if (b) fetch<T, G>(b, n, tid, team, j, bj);
+        if (KEEP) {
+            kept_w[KEEP ? j : 0] = wj;
+            kept_b[KEEP ? j : 0] = bj;
+        } else if (p.shared_wb) {
+#pragma unroll
+            for (int a = 0; a < 8 / G; ++a) {
+                *place(shared_w, j, a) = reinterpret_cast<const typename Word<BYTES>::type*>(wj.q)[a];
+                *place(shared_b, j, a) = reinterpret_cast<const typename Word<BYTES>::type*>(bj.q)[a];
+            }
+        }
+    }
     const float inv = 1.0f / static_cast<float>(n);
     int stage = 0, turn = 0;
     for (; row < p.rows; row += step) {
@@ -269,25 +296,41 @@ __global__ void __launch_bounds__(NT, kForwardThreads / NT) norm_kernel(const No
             if (p.rstd) p.rstd[row] = rstd;
         }
         T* y = static_cast<T*>(p.y) + row * p.ldy;
+        auto write = [&](auto with_w, auto with_b) {
+            constexpr bool W = decltype(with_w)::value, B = decltype(with_b)::value;
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            Raw<T> wj, bj;
-            if (w) fetch<T, G>(w, n, tid, team, j, wj);
-            if (b) fetch<T, G>(b, n, tid, team, j, bj);
-            Raw<T> o;
+            for (int j = 0; j < V; ++j) {
+                Raw<T> wj, bj, o;
+                if (KEEP) {
+                    wj = kept_w[KEEP ? j : 0];
+                    bj = kept_b[KEEP ? j : 0];
+                } else if (!p.shared_wb) {
+                    if (W) fetch<T, G>(w, n, tid, team, j, wj);
+                    if (B) fetch<T, G>(b, n, tid, team, j, bj);
+                } else {
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                float2 z = mul2(v[j][t], both(rstd));
-                if (w && b)
-                    z = fma2(z, wj.pair(t), bj.pair(t));
-                else if (w)
-                    z = mul2(z, wj.pair(t));
-                else if (b)
-                    z = add2(z, bj.pair(t));
-                o.set(t, z);
+                    for (int a = 0; a < 8 / G; ++a) {
+                        if (W) reinterpret_cast<typename Word<BYTES>::type*>(wj.q)[a] = *place(shared_w, j, a);
+                        if (B) reinterpret_cast<typename Word<BYTES>::type*>(bj.q)[a] = *place(shared_b, j, a);
+                    }
+                }
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    const float2 h = mul2(v[j][t], both(rstd));
+                    o.set(t, W && B ? fma2(h, wj.pair(t), bj.pair(t))
+                                    : (W ? mul2(h, wj.pair(t)) : (B ? add2(h, bj.pair(t)) : h)));
+                }
+                put<T, G>(y, n, tid, team, j, o);
             }
-            put<T, G>(y, n, tid, team, j, o);
-        }
+        };
+        if (w && b)
+            write(std::true_type(), std::true_type());
+        else if (w)
+            write(std::true_type(), std::false_type());
+        else if (b)
+            write(std::false_type(), std::true_type());
+        else
+            write(std::false_type(), std::false_type());
         stage = stage + 1 == S ? 0 : stage + 1;
     }
 }
@@ -395,7 +438,7 @@ __global__ void __launch_bounds__(NT, B)
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 // past the row's end x and dy are zero
-                const float2 d = dy.pair(t), c = add2(x.pair(t), both(-mean)), g = p.w ? mul2(d, w[j][t]) : d;
+                const float2 d = dy.pair(t), c = add2(x.pair(t), both(-mean)), g = mul2(d, w[j][t]);
                 dw[j][t] = fma2(mul2(d, both(rstd)), c, dw[j][t]);
                 db[j][t] = add2(db[j][t], d);
                 s1 = add2(s1, g);
@@ -411,17 +454,16 @@ __global__ void __launch_bounds__(NT, B)
             T* dx = static_cast<T*>(p.dx) + row * p.lddx;
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                Raw<T> x, dy, r;
+                Raw<T> x, dy, r{};
                 read(j, x, dy);
                 if (p.residual)
                     stages.read(stage, 2, static_cast<const T*>(p.residual) + row * p.ldr, n, tid, team, j, r);
                 Raw<T> o;
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
-                    const float2 scale = p.w ? mul2(w[j][t], both(rstd)) : both(rstd);
-                    float2 y = fma2(dy.pair(t), scale, fma2(add2(x.pair(t), both(-mean)), a, c0));
-                    if (p.residual) y = add2(y, r.pair(t));
-                    o.set(t, y);
+                    // (w is ones where there is none, r zeros)
+                    const float2 y = fma2(dy.pair(t), mul2(w[j][t], both(rstd)), fma2(add2(x.pair(t), both(-mean)), a, c0));
+                    o.set(t, add2(y, r.pair(t)));
                 }
                 put<T, G>(dx, n, tid, team, j, o);
             }
@@ -616,16 +658,29 @@ cudaError_t launch_rows(F kern, std::atomic<uint64_t>& done, size_t shared, cons
     return launch_kernel(true, kern, dim3(static_cast<unsigned>(s.blocks)), dim3(s.threads), shared, st, p);
 }
 
-// Stages: an SM's shared memory holds three rows of 64 bytes per thread in the forward pass, two of each
-// of the backward pass's three matrices; more of less, and of twice as much one row.
+// Stages: an SM's shared memory holds two rows of 64 bytes per thread in the forward pass beside w and b,
+// two of each of the backward pass's three matrices; more of less, and of twice as much one row.
+template <typename T, int G, int V, int S, int NT>
+cudaError_t run_norm(NormParams p, Shape s, int num_sms, cudaStream_t st) {
+    static std::atomic<uint64_t> done{0};
+    constexpr int VECTOR = 8 * V * static_cast<int>(sizeof(T));  // bytes of a thread
+    s.teams = NT / (s.warps * kWarp);
+    s.blocks = std::min<int64_t>(cdiv(p.rows, s.teams), static_cast<int64_t>(kForwardThreads / NT) * num_sms);
+    p.shared_wb = VECTOR > 32 && s.teams > 1;
+    auto kern = norm_kernel<T, G, V, S, NT>;
+    const size_t most = Stages<T, G, V, 1, S, NT>::SHARED + (VECTOR > 32 ? VECTOR * NT : 0);
+    const cudaError_t e = set_smem_limit_once(done, reinterpret_cast<const void*>(kern), static_cast<int>(most));
+    if (e != cudaSuccess) return e;
+    const size_t smem = Stages<T, G, V, 1, S, NT>::SHARED + (p.shared_wb ? 2 * VECTOR * (s.warps * kWarp) : 0);
+    return launch_kernel(true, kern, dim3(static_cast<unsigned>(s.blocks)), dim3(NT), smem, st, p);
+}
+// 64 bytes per thread: blocks of 512, so that more teams share w and b.
 template <typename T, int G, int V>
-cudaError_t run_norm(const NormParams& p, const Shape& s, cudaStream_t st) {
-    constexpr int BYTES = 8 * V * static_cast<int>(sizeof(T)), S = BYTES > 64 ? 1 : (BYTES == 64 ? 3 : 6);
-    // (two kernels by their blocks' size, so that each has one limit of shared memory)
-    static std::atomic<uint64_t> done[2];
-    if (s.threads > 256)
-        return launch_rows(norm_kernel<T, G, V, S, kMostThreads>, done[0], Stages<T, G, V, 1, S, kMostThreads>::SHARED, p, s, st);
-    return launch_rows(norm_kernel<T, G, V, S, 256>, done[1], Stages<T, G, V, 1, S, 256>::SHARED, p, s, st);
+cudaError_t run_norm(const NormParams& p, const Shape& s, int num_sms, cudaStream_t st) {
+    constexpr int VECTOR = 8 * V * static_cast<int>(sizeof(T)), S = VECTOR > 64 ? 1 : (VECTOR == 64 ? 2 : 6);
+    constexpr int SMALL = (VECTOR > 32) ? kMostThreads : 256;
+    return s.threads > 256 ? run_norm<T, G, V, S, kMostThreads>(p, s, num_sms, st)
+                           : run_norm<T, G, V, S, SMALL>(p, s, num_sms, st);
 }
 template <typename T, int G, int V>
 cudaError_t run_backward(const NormBackwardParams& p, const Shape& s, cudaStream_t st) {
@@ -660,7 +715,7 @@ cudaError_t norm(NormParams p, int num_sms, cudaStream_t st) {
                                 kForwardThreads / kMostThreads, num_sms);
     p.warps = s.warps;
     return with_shape<T>(access, s.v, [&](auto g, auto v) {
-        return run_norm<T, decltype(g)::value, decltype(v)::value>(p, s, st);
+        return run_norm<T, decltype(g)::value, decltype(v)::value>(p, s, num_sms, st);
     });
 }
 template <typename T>
@@ -699,7 +754,7 @@ cudaError_t backward(const NormBackwardParams& p, T* dw, T* db, int num_sms, cud
 
 cudaError_t launch_norm(int dtype, int64_t rows, int64_t n, const void* x, int64_t ldx, const void* w, const void* b,
                         float eps, void* y, int64_t ldy, float* mean, float* rstd, int num_sms, cudaStream_t st) {
-    const NormParams p{rows, n, x, ldx, w, b, eps, y, ldy, mean, rstd, 1};
+    const NormParams p{rows, n, x, ldx, w, b, eps, y, ldy, mean, rstd, 1, false};
     return dtype == SGEMM_F32 ? norm<float>(p, num_sms, st) : norm<bf16>(p, num_sms, st);
 }
 

@@ -180,6 +180,7 @@ struct Params {
     int32_t t, n, kbs;
     int32_t tiles_t, tiles_n;  // tiles of 256 rows, whose halves a pair of CTAs shares (paired), or of 128
     int32_t paired;
+    float inv_split, inv_t;    // reciprocals of split and tiles_t
     int32_t split, split_kb;
     const float* x_scales;
     int64_t xs_row, xs_block;  // strides along rows and along blocks of k
@@ -204,29 +205,23 @@ struct Rows {  // of a matrix
     int64_t ld;
 };
 
-// Eight columns from i on of row j: results of sums v (those past n are of no use).
-template <typename T, int ACT>
-__device__ __forceinline__ void result8(const Params& p, int64_t j, int64_t i, float (&v)[8]) {
-    const int valid = static_cast<int>(min(p.n - i, int64_t(8)));
-    if (p.bias) {
-        float b[8];
-        load8(static_cast<const T*>(p.bias) + (valid > 0 ? i : 0), p.vec, valid, b);
+// Results of the sums v of N columns from i on of row j (clamped to the rows there are), whole: all of
+// them are columns of y, and eights of them lie at 16-byte boundaries.
+template <typename T, int ACT, int N>
+__device__ __forceinline__ void results(const Params& p, int64_t j, int64_t i, bool whole, float (&v)[N]) {
+    auto add = [&](const T* from) {
 #pragma unroll
-        for (int t = 0; t < 8; ++t) v[t] += b[t];
-    }
+        for (int h = 0; h < N; h += 8) {
+            float b[8];
+            load8(from + h, whole, whole ? 8 : static_cast<int>(min(p.n - i - h, int64_t(8))), b);
 #pragma unroll
-    for (int t = 0; t < 8; ++t) v[t] = act_value<ACT, std::is_same<T, bf16>::value>(v[t]);
-    if (p.residual) {
-        float r[8];
-        load8(static_cast<const T*>(p.residual) + (valid > 0 ? j * p.ldr + i : 0), p.vec, valid, r);
+            for (int t = 0; t < 8; ++t) v[h + t] += b[t];
+        }
+    };
+    if (p.bias) add(static_cast<const T*>(p.bias) + i);
 #pragma unroll
-        for (int t = 0; t < 8; ++t) v[t] += r[t];
-    }
-}
-template <typename T>
-__device__ __forceinline__ void store_result8(const Params& p, int64_t j, int64_t i, const float (&v)[8]) {
-    const int valid = static_cast<int>(min(p.n - i, int64_t(8)));
-    if (valid > 0) store8(static_cast<T*>(p.y) + j * p.ldy + i, p.vec, valid, v);
+    for (int t = 0; t < N; ++t) v[t] = act_value<ACT, std::is_same<T, bf16>::value>(v[t]);
+    if (p.residual) add(static_cast<const T*>(p.residual) + j * p.ldr + i);
 }
 
 template <int BN, typename T>
@@ -282,12 +277,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     struct Unit {
         int j0, i0, slice, kb0, nkb;
     };
+    // a / b by b's reciprocal, a step up or down where that is off: the compiler's division of integers
+    // would take a unit's every warp 150 cycles each
+    auto divide = [](int a, int b, float inv, int& rest) {
+        int q = __float2int_rz(static_cast<float>(a) * inv);
+        rest = a - q * b;
+        while (rest < 0) --q, rest += b;
+        while (rest >= b) ++q, rest -= b;
+        return q;
+    };
     auto unit_of = [&](int u) {
         Unit x;
-        const int tile = u / p.split;  // the slices of a tile are neighbours, so that they run at one time
-        x.slice = u - tile * p.split;
+        const int tile = divide(u, p.split, p.inv_split, x.slice);  // the slices of a tile are neighbours
         int tt, tn;
-        tile_coords(tile, p.tiles_t, p.tiles_n, kGroupTiles, tt, tn);
+        if (p.tiles_t <= kGroupTiles)
+            tn = divide(tile, p.tiles_t, p.inv_t, tt);
+        else
+            tile_coords(tile, p.tiles_t, p.tiles_n, kGroupTiles, tt, tn);
         x.j0 = p.paired ? tt * (2 * kRows) + kRows * static_cast<int>(rank) : tt * kRows;
         x.i0 = tn * BN;
         x.kb0 = x.slice * p.split_kb;
@@ -576,10 +582,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 // The columns as elements TO, 64 bytes of 32 rows at a time.  They change places in shared memory
                 // (16-byte words, swizzled so that eight rows' words fall on all banks), so that four lanes write
                 // a row's 64 bytes together.
-                auto emit = [&](auto element, Rows rows_of, bool vec, auto results) {
+                auto emit = [&](auto element, Rows rows_of, bool vec, auto finish) {
                     using TO = decltype(element);
                     constexpr int SPAN = kOutBytes / static_cast<int>(sizeof(TO)), N = static_cast<int>(sizeof(TO)) / 2;
-                    TO* const to = static_cast<TO*>(rows_of.ptr);
+                    TO* const mine = static_cast<TO*>(rows_of.ptr) + (j < p.t ? j : 0) * rows_of.ld + i0;
+                    TO* const shared_out = static_cast<TO*>(rows_of.ptr) + (row0 + lane / 4) * rows_of.ld + i0 +
+                                           (lane & 3) * (16 / static_cast<int>(sizeof(TO)));
+                    const int rows_left = p.t - row0 - lane / 4;
 #pragma unroll 1
                     for (int c = 0; c < C::MINE && i0 + c < p.n; c += SPAN) {
                         uint32_t v[SPAN];
@@ -589,44 +598,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         else
                             tmem_ld_32x32b_x16(at + c, v);
                         tmem_wait_ld(v);
+                        float f[SPAN];
+#pragma unroll
+                        for (int k = 0; k < SPAN; ++k) f[k] = __uint_as_float(v[k]);
                         const bool whole = vec && i0 + c + SPAN <= p.n;
+                        finish(i0 + c, whole, f);
+                        if (whole) {
 #pragma unroll
-                        for (int h = 0; h < SPAN; h += 8) {
-                            float f[8];
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(v[h + k]);
-                            if (j < p.t) results(c + h, f);
-                            if (whole) {
+                            for (int h = 0; h < SPAN; h += 8) {
                                 TO e[8];
 #pragma unroll
-                                for (int k = 0; k < 8; ++k) e[k] = from_float<TO>(f[k]);
+                                for (int k = 0; k < 8; ++k) e[k] = from_float<TO>(f[h + k]);
 #pragma unroll
                                 for (int k = 0; k < N; ++k)  // N 16-byte words of eight elements
                                     *reinterpret_cast<uint4*>(out + kOutBytes * lane + 16 * ((h / 8 * N + k) ^ ((lane >> 1) & 3))) =
                                         reinterpret_cast<const uint4*>(e)[k];
-                            } else if (j < p.t) {
-                                const int valid = static_cast<int>(min(p.n - (i0 + c + h), 8));
-                                if (valid > 0) store8(to + j * rows_of.ld + i0 + c + h, vec, valid, f);
                             }
-                        }
-                        if (whole) {
                             __syncwarp();
+                            uint4 w[4];
 #pragma unroll
-                            for (int r = 0; r < 32; r += 8) {
-                                const int row = r + lane / 4;
-                                const uint4 w = *reinterpret_cast<const uint4*>(out + kOutBytes * row + 16 * ((lane & 3) ^ ((row >> 1) & 3)));
-                                if (row0 + row < p.t)
-                                    *(reinterpret_cast<uint4*>(to + (row0 + row) * rows_of.ld + i0 + c) + (lane & 3)) = w;
+                            for (int r = 0; r < 4; ++r) {
+                                const int row = 8 * r + lane / 4;
+                                w[r] = *reinterpret_cast<const uint4*>(out + kOutBytes * row + 16 * ((lane & 3) ^ ((row >> 1) & 3)));
                             }
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+                                if (8 * r < rows_left) *reinterpret_cast<uint4*>(shared_out + c + 8 * r * rows_of.ld) = w[r];
+                        } else if (j < p.t) {
+#pragma unroll
+                            for (int k = 0; k < SPAN; ++k)
+                                if (i0 + c + k < p.n) mine[c + k] = from_float<TO>(f[k]);
                         }
                     }
                 };
                 if (p.part)
-                    emit(float(), {p.part + static_cast<int64_t>(x.slice) * p.t * p.ldp, p.ldp}, true, [](int, float(&)[8]) {});
+                    emit(float(), {p.part + static_cast<int64_t>(x.slice) * p.t * p.ldp, p.ldp}, true,
+                         [](int, bool, auto&) {});
                 else
                     with_act(p.act, [&](auto act) {
-                        emit(T(), {p.y, p.ldy}, p.vec != 0,
-                             [&](int c, float(&f)[8]) { result8<T, decltype(act)::value>(p, j, i0 + c, f); });
+                        emit(T(), {p.y, p.ldy}, p.vec != 0, [&](int i, bool whole, auto& f) {
+                            results<T, decltype(act)::value>(p, j < p.t ? j : 0, i, whole, f);
+                        });
                     });
             }
             if (x.nkb > 0) free_buffer(last);
@@ -658,8 +670,9 @@ __global__ void __launch_bounds__(256) block_sum_kernel(const Params p) {
         v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
         v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
     }
-    with_act(p.act, [&](auto act) { result8<T, decltype(act)::value>(p, j, i, v); });
-    store_result8<T>(p, j, i, v);
+    const int valid = static_cast<int>(min(p.n - i, int64_t(8)));
+    with_act(p.act, [&](auto act) { results<T, decltype(act)::value>(p, j, i, p.vec && valid == 8, v); });
+    store8(static_cast<T*>(p.y) + j * p.ldy + i, p.vec, valid, v);
 }
 
 template <int BN, typename T>
@@ -744,6 +757,8 @@ int launch_block(const CallContext& c, const BlockProduct& b, const BlockPlan& p
     p.tiles_t = static_cast<int32_t>(cdiv(b.t, p.paired ? 2 * kRows : kRows));
     p.tiles_n = static_cast<int32_t>(cdiv(b.n, plan.bn));
     p.split = plan.split;
+    p.inv_split = 1.0f / static_cast<float>(p.split);
+    p.inv_t = 1.0f / static_cast<float>(p.tiles_t);
     p.split_kb = plan.split_kb;
     p.x_scales = b.x_scales;
     p.xs_row = b.xs_row;

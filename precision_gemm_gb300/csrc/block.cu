@@ -446,7 +446,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // ---------------- promotion and epilogue (warps 4..11) ----------------
         const int q = warp & 3;            // TMEM lane quarter this warp may access
         const int half = (warp - 4) >> 2;  // its half of the columns
-                const uint32_t base = tmem + (static_cast<uint32_t>(32 * q) << 16) + C::MINE * half;
+        const uint32_t base = tmem + (static_cast<uint32_t>(32 * q) << 16) + C::MINE * half;
         uint8_t* out = smem + S * C::STAGE_BYTES + (warp - 4) * (32 * kOutBytes);
         const bool one = lane == 0;
         auto free_buffer = [&](int b) {
@@ -601,7 +601,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         float f[SPAN];
 #pragma unroll
                         for (int k = 0; k < SPAN; ++k) f[k] = __uint_as_float(v[k]);
-                        const bool whole = vec && i0 + c + SPAN <= p.n;
+                        const bool whole = vec && p.n - i0 - c >= SPAN;
                         finish(i0 + c, whole, f);
                         if (whole) {
 #pragma unroll
@@ -664,7 +664,7 @@ __global__ void __launch_bounds__(256) block_sum_kernel(const Params p) {
     if (j >= p.t) return;
     const float* src = p.part + j * p.ldp + i;
     float v[8] = {};
-#pragma unroll 4
+#pragma unroll 8
     for (int s = 0; s < p.split; ++s, src += p.t * p.ldp) {
         const float4 a = __ldcg(reinterpret_cast<const float4*>(src)), b = __ldcg(reinterpret_cast<const float4*>(src) + 1);
         v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
@@ -730,13 +730,14 @@ BlockPlan plan_block(int64_t t, int64_t n, int64_t k, int num_sms, int force_bn,
     double best_us = 0.0;
     for (int bn : {256, 128, 64}) {
         if (force_bn && force_bn <= 256 && bn != force_bn) continue;
-        const double step = bn == 256 ? 0.36 : (bn == 128 ? 0.20 : 0.15), end = bn == 256 ? 4.0 : (bn == 128 ? 2.5 : 1.5);
+        // microseconds of a block of k and of a tile's ends, measured at 1024 x 4096 by k of 4096 and 14336
+        const double step = bn == 256 ? 0.40 : (bn == 128 ? 0.22 : 0.18), end = bn == 256 ? 3.2 : (bn == 128 ? 1.9 : 1.5);
         const int64_t tiles = cdiv(t, paired ? 2 * kRows : kRows) * cdiv(n, bn);
         for (int64_t want = 1; want <= std::max<int64_t>(kb, 1); ++want) {
             if (force_split ? want != std::min<int64_t>(force_split, std::max<int64_t>(kb, 1)) : want > 1 && tiles * want > 3 * at_once) continue;
             const int64_t split_kb = std::max<int64_t>(cdiv(kb, want), 1), split = std::max<int64_t>(cdiv(kb, split_kb), 1);
             const double us = static_cast<double>(cdiv(tiles * split, at_once)) * (split_kb * step + end) +
-                              (split > 1 ? 2.5 + 1e-6 * split * t * n * 4 * 0.3 : 0.0);
+                              (split > 1 ? 1.0 + 0.12 * split + 8e-7 * split * t * n : 0.0);
             if (best.bn == 0 || us < best_us) {
                 best_us = us;
                 best = BlockPlan{bn, static_cast<int>(split), static_cast<int>(split_kb), 0};

@@ -530,7 +530,7 @@ PG_EXPORT int sgemm_block_linear(int dtype, int64_t t, int64_t n, int64_t k, con
         BlockProduct p{dtype, t, n, k, static_cast<const uint8_t*>(x), ldx, x_scales, ldxs, 1, w, ldw, w_scales, ldws, bias,
                        act, residual, ldr, y, ldy};
         int launches = 0;
-        if (few && x_scales == nullptr && t <= kRawRows) {
+        if (few && x_scales == nullptr && t * k <= kRawValues) {
             // the kernel rounds x itself
         } else if (k > 0 && x_scales == nullptr) {
             // scales of neighbouring rows side by side: the product's lanes are rows

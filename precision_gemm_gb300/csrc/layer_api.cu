@@ -141,6 +141,10 @@ int prepare(int dtype, Operand& o, int groups, int64_t cols, int64_t listed, boo
 // bfloat16 at others, which the tensor cores read from a copy:
 //   4096 x 4095: 4 rows 13 / 27, 8 rows 23 / 28; 8192 x 8191: 4 rows 52 / 90, 8 rows 105 / 90;
 //   64 experts of 1024 x 2047: 64 pairs 74 / 165, 256 pairs 142 / 180, 1024 pairs 429 / 181.
+// Gated products, whose rows of weights come in pairs (all cold):
+//   bfloat16 4864 x 4096: 1 row 18.7 / 20.7, 2 rows 21.9 / 21.5, 3 rows 46 / 21.3; 8192 x 2048: 15.8 / 20.1,
+//   17.1 / 19.6; 14336 x 4096: 43.6 / 41.3, 48.4 / 41.4; 4864 x 4095: 4 rows 34 / 62;
+//   float32 4864 x 4096: 1 row 32 / 123, 8 rows 47 / 123, 16 rows 79 / 122; 1024 x 1024: 16 rows 11 / 22.
 bool few_rows(const Product& p) {
     if (p.rows_on_k || !p.a.k_contiguous || p.nk == 0 || p.out_f32) return false;
     if (p.b.rows * p.b.ld >= int64_t(1) << 32) return false;  // its row offsets are 32-bit
@@ -149,7 +153,7 @@ bool few_rows(const Product& p) {
     if (p.dtype == SGEMM_F32)
         return p.groups == 1 ? p.nj <= std::min<int64_t>(16, p.nk / 8 + 1)
                              : p.nj <= lists * std::min<int64_t>(aligned ? 24 : 16, p.nk / 32 + 1);
-    if (p.gated) return p.nj <= (aligned ? 2 : std::min<int64_t>(4, p.nk / 64 + 1));
+    if (p.gated && aligned) return p.nj <= 2 && p.ni * p.nk <= int64_t(1) << 25;
     if (!aligned) return p.nj <= lists * std::min<int64_t>(4, p.nk / 64 + 1);
     return p.groups == 1 ? p.nj <= 3 && p.ni * p.nk <= int64_t(1) << 25 : 2 * p.nj <= p.groups && p.nk >= 256;
 }

@@ -20,6 +20,10 @@
 // 64 experts: 0.70 ms gathered by the TMA unit, 0.43 ms by 16-byte asynchronous copies
 // of four more warps, 0.18 ms plus a copy of 0.05 ms).
 //
+// A gated layer's products (Product::gated) stage two tiles of A, the gate's rows and the gated ones, per
+// tile of B: their sums meet in the epilogue's registers, out = act(g) v, and x is read once for both (2048
+// rows, 8192 features of 4096, bfloat16: 175 us, 1.57 PFLOP/s over 2 x 8192 rows of weights).
+//
 // float32 operands come as three bfloat16 parts x = x0 + x1 + x2 (pack_kernel), whose
 // six products of weight 2^-16 and above, the smallest first, are summed over a chunk
 // of k in one accumulator.  The tensor core truncates its FP32 sums (an error of up to
@@ -906,6 +910,7 @@ TcPlan plan_tc(const Product& p, int num_sms, int force_bn, int force_split) {
         if (bn < 128 && !p.b.k_contiguous) break;
         if (bn > widest) continue;
         if (force_bn && bn != std::min(p.b.k_contiguous ? force_bn : std::max(force_bn, 128), widest) && force_bn <= 256) continue;
+        // (two accumulators: 16 to 2048 rows of 1024 to 4864 x 777 to 4096 within 4% of the best forced plan)
         const double step = p.gated ? (bn == 128 ? 0.36 : (bn == 64 ? 0.26 : 0.23))
                                     : (bn == 256 ? 0.34 : (bn == 128 ? 0.19 : (bn == 64 ? 0.14 : 0.12)));
         const double end = (bn * accs == 256 ? 4.0 : (bn * accs == 128 ? 2.0 : 1.0)) * (p.residual ? 3.0 : 1.0);

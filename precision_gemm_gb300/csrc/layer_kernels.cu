@@ -119,21 +119,26 @@ __global__ void __launch_bounds__(256, 4) dact_kernel(int64_t rows, int64_t n, c
 }
 
 // dz = [dy v act'(g), dy act(g)] for a slab of rows x 256 columns of z = [g v], and the slab's
-// sums of its 2 n columns in part (slabs x 2 n), with the threads laid out as in dact_kernel.
+// sums of its 2 n columns in part (slabs x 2 n), with the threads laid out as in dact_kernel: thread
+// (l, c) takes rows l, l + 8, ... and eight columns, neighbouring ones where all rows are whole eights at
+// 16-byte boundaries (VEC), else every 32nd, so that a warp's single elements are neighbours.
 // HBM-bound: reads dy and z, writes dz.
-template <typename T, int PARTS>
+template <typename T, int PARTS, bool VEC>
 __global__ void __launch_bounds__(256, 2) dgate_kernel(int64_t rows, int64_t n, const T* dy, int64_t lddy, const T* z,
                                                        int64_t ldz, int act, bf16* dz, int64_t lddz, float* part,
-                                                       int slab_size, bool vec) {
+                                                       int slab_size) {
     __shared__ float sums[8][kWidth + 8];
     pdl_trigger();
     pdl_wait();
     const int64_t widths = (n + kWidth - 1) / kWidth, slab = blockIdx.x / widths;
-    const int64_t c0 = (blockIdx.x - slab * widths) * kWidth, c = c0 + 8 * (threadIdx.x % 32);
-    const int l = threadIdx.x / 32;
-    const int valid = static_cast<int>(n - c < 8 ? n - c : 8);  // <= 0: no columns here
+    const int64_t c0 = (blockIdx.x - slab * widths) * kWidth;
+    const int lane = threadIdx.x % 32, l = threadIdx.x / 32;
+    auto column = [&](int t) { return VEC ? 8 * lane + t : lane + 32 * t; };
+    const int width = static_cast<int>(min(n - c0, int64_t(kWidth)));
     const int64_t r0 = slab * slab_size, r1 = rows - r0 < slab_size ? rows : r0 + slab_size;
-    const bool whole = valid == 8 && n % 8 == 0;  // of dz too, whose second half starts at column n
+    dy += c0;
+    z += c0;
+    dz += c0;
     float sum[2][8] = {};
     auto one = [&](auto f, int64_t r, const float(&d)[8], const float(&g)[8], const float(&v)[8]) {
         float dg[8], dv[8];
@@ -146,30 +151,31 @@ __global__ void __launch_bounds__(256, 2) dgate_kernel(int64_t rows, int64_t n, 
             sum[0][t] += dg[t];
             sum[1][t] += dv[t];
         }
-        bf16* at = dz + r * lddz + c;
-        if (whole) {
+        bf16* at = dz + r * lddz + column(0);
+        if (VEC) {
             store_parts8<PARTS>(at, rows * lddz, dg);
             store_parts8<PARTS>(at + n, rows * lddz, dv);
         } else {
+            uint32_t a[PARTS][4], b[PARTS][4];
+            split8<PARTS>(dg, a);
+            split8<PARTS>(dv, b);
 #pragma unroll
             for (int t = 0; t < 8; ++t) {
-                if (t >= valid) break;
-                bf16 a[PARTS], b[PARTS];
-                split_bf16<PARTS>(dg[t], a);
-                split_bf16<PARTS>(dv[t], b);
+                if (column(t) >= width) break;
 #pragma unroll
                 for (int q = 0; q < PARTS; ++q) {
-                    at[q * rows * lddz + t] = a[q];
-                    at[q * rows * lddz + n + t] = b[q];
+                    at[q * rows * lddz + 32 * t] = __ushort_as_bfloat16(static_cast<uint16_t>(a[q][t / 2] >> (16 * (t % 2))));
+                    at[q * rows * lddz + n + 32 * t] = __ushort_as_bfloat16(static_cast<uint16_t>(b[q][t / 2] >> (16 * (t % 2))));
                 }
             }
         }
     };
-    if (valid > 0) {
+    if (column(0) < width) {
         with_act(act, [&](auto f) {
-            constexpr int N = sizeof(T) / 2, R = 2 / N;  // 16-byte words of eight elements; rows
+            constexpr int N = sizeof(T) / 2, R = VEC ? 2 / N : 1;  // 16-byte words of eight elements; rows
             int64_t r = r0 + l;
-            if (vec && valid == 8) {
+            if (VEC) {
+                const int c = column(0);
                 for (; r + 8 * (R - 1) < r1; r += 8 * R) {
                     uint4 d[R][N], g[R][N], v[R][N];
 #pragma unroll
@@ -196,9 +202,20 @@ __global__ void __launch_bounds__(256, 2) dgate_kernel(int64_t rows, int64_t n, 
 #pragma unroll 1
             for (; r < r1; r += 8) {
                 float df[8], gf[8], vf[8];
-                load8(dy + r * lddy + c, vec, valid, df);
-                load8(z + r * ldz + c, vec, valid, gf);
-                load8(z + r * ldz + n + c, vec, valid, vf);
+                if (VEC) {
+                    load8(dy + r * lddy + column(0), true, 8, df);
+                    load8(z + r * ldz + column(0), true, 8, gf);
+                    load8(z + r * ldz + n + column(0), true, 8, vf);
+                } else {
+#pragma unroll
+                    for (int t = 0; t < 8; ++t) {
+                        const int c = column(t);
+                        const bool there = c < width;
+                        df[t] = there ? to_float(dy[r * lddy + c]) : 0.0f;
+                        gf[t] = there ? to_float(z[r * ldz + c]) : 0.0f;
+                        vf[t] = there ? to_float(z[r * ldz + n + c]) : 0.0f;
+                    }
+                }
                 one(f, r, df, gf, vf);
             }
         });
@@ -207,7 +224,7 @@ __global__ void __launch_bounds__(256, 2) dgate_kernel(int64_t rows, int64_t n, 
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
 #pragma unroll
-        for (int t = 0; t < 8; ++t) sums[l][8 * (threadIdx.x % 32) + t] = sum[which][t];
+        for (int t = 0; t < 8; ++t) sums[l][column(t)] = sum[which][t];
         __syncthreads();
         const int64_t col = c0 + threadIdx.x;
         if (col < n) {
@@ -426,8 +443,9 @@ static cudaError_t run_dgate(int64_t rows, int64_t n, const void* dy, int64_t ld
     const bool vec = n % 8 == 0 && rows_aligned<T>(dy, lddy) && rows_aligned<T>(z, ldz);
     cudaError_t e = cudaSuccess;
     if (rows > 0)
-        e = launch_kernel(true, dgate_kernel<T, PARTS>, grid, dim3(256), 0, st, rows, n, static_cast<const T*>(dy), lddy,
-                          static_cast<const T*>(z), ldz, act, dz, lddz, dbias ? part : nullptr, slab, vec);
+        e = launch_kernel(true, vec ? dgate_kernel<T, PARTS, true> : dgate_kernel<T, PARTS, false>, grid, dim3(256), 0, st,
+                          rows, n, static_cast<const T*>(dy), lddy, static_cast<const T*>(z), ldz, act, dz, lddz,
+                          dbias ? part : nullptr, slab);
     if (dbias && e == cudaSuccess)
         e = launch_kernel(true, dbias_kernel<T>, dim3(static_cast<unsigned>((2 * n + 31) / 32), 1), dim3(256), 0, st,
                           rows, 2 * n, static_cast<const int32_t*>(nullptr), static_cast<const float*>(part),

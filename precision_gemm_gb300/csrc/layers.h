@@ -256,20 +256,57 @@ inline bool rows_aligned(const void* p, int64_t ld) {
     return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * sizeof(T)) % 16 == 0;
 }
 
+__device__ __forceinline__ uint32_t pack2(float2 v) {
+    uint32_t w;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(v.y), "f"(v.x));
+    return w;
+}
+__device__ __forceinline__ float2 unpack2(uint32_t w) {  // a bfloat16 is the upper half of its float
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
+// The parts of eight values, two to a word.  Values that no part's rounding carries to infinity take packed
+// arithmetic, which gives split_bf16's bits; a comparison with the largest bfloat16 tells.
+template <int PARTS>
+__device__ __forceinline__ void split8(const float (&v)[8], uint32_t (&part)[PARTS][4]) {
+    if (PARTS == 1) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) part[0][t] = pack2(make_float2(v[2 * t], v[2 * t + 1]));
+        return;
+    }
+    float m = 0.0f;  // NaN where one is; its sign is of no use
+#pragma unroll
+    for (int t = 0; t < 8; ++t) asm("max.NaN.xorsign.abs.f32 %0, %0, %1;" : "+f"(m) : "f"(v[t]));
+    if (fabsf(m) <= 3.3895314e38f) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            float2 rest = make_float2(v[2 * t], v[2 * t + 1]);
+#pragma unroll
+            for (int q = 0; q < PARTS; ++q) {
+                part[q][t] = pack2(rest);
+                if (q + 1 < PARTS) rest = fma2(unpack2(part[q][t]), make_float2(-1.0f, -1.0f), rest);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            bf16 a[PARTS], b[PARTS];
+            split_bf16<PARTS>(v[2 * t], a);
+            split_bf16<PARTS>(v[2 * t + 1], b);
+#pragma unroll
+            for (int q = 0; q < PARTS; ++q)
+                part[q][t] = __bfloat16_as_ushort(a[q]) | static_cast<uint32_t>(__bfloat16_as_ushort(b[q])) << 16;
+        }
+    }
+}
 // Eight values as the parts of a bfloat16 matrix (16-byte aligned, part_stride apart).
 template <int PARTS>
 __device__ __forceinline__ void store_parts8(bf16* p, int64_t part_stride, const float (&v)[8]) {
-    bf16 part[8][PARTS];
+    uint32_t part[PARTS][4];
+    split8<PARTS>(v, part);
 #pragma unroll
-    for (int t = 0; t < 8; ++t) split_bf16<PARTS>(v[t], part[t]);
-#pragma unroll
-    for (int q = 0; q < PARTS; ++q) {
-        uint4 raw;
-        bf16* e = reinterpret_cast<bf16*>(&raw);
-#pragma unroll
-        for (int t = 0; t < 8; ++t) e[t] = part[t][q];
-        *reinterpret_cast<uint4*>(p + q * part_stride) = raw;
-    }
+    for (int q = 0; q < PARTS; ++q)
+        *reinterpret_cast<uint4*>(p + q * part_stride) = make_uint4(part[q][0], part[q][1], part[q][2], part[q][3]);
 }
 
 // The matrix row that gathered row r stands for (list[r] / top), -1 for none.

@@ -17,8 +17,8 @@
 // blocks' sums in order: equal inputs give equal bits.  Rows too wide for that are read again for
 // each of the passes.
 //
-// Measured (L2 cold), forward and backward without residual: 16384 x 2048 float32 48 and 68 us (5.6 and
-// 5.9 TB/s), 16384 x 4096 bfloat16 65 and 84 us (4.1 and 4.8 TB/s: 15 instructions per 32 elements hold the
+// Measured (L2 cold), forward and backward without residual: 16384 x 2048 float32 48 and 69 us (5.6 and
+// 5.8 TB/s), 16384 x 4096 bfloat16 65 and 84 us (4.1 and 4.8 TB/s: 15 instructions per 32 elements hold the
 // forward pass up), 512 x 4096 bfloat16 7 and 14 us, 1 x 4096 4 and 6 us.
 #include <algorithm>
 #include <initializer_list>

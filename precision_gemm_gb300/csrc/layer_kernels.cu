@@ -122,11 +122,13 @@ __global__ void __launch_bounds__(256, 4) dact_kernel(int64_t rows, int64_t n, c
 // sums of its 2 n columns in part (slabs x 2 n), with the threads laid out as in dact_kernel: thread
 // (l, c) takes rows l, l + 8, ... and eight columns, neighbouring ones where all rows are whole eights at
 // 16-byte boundaries (VEC), else every 32nd, so that a warp's single elements are neighbours.
-// HBM-bound: reads dy and z, writes dz.
+// HBM-bound: reads dy and z, writes dz.  bfloat16 runs best with as many threads as fit (8192 x 4096, gelu, with
+// dbias: 64 us, 5.2 TB/s; 79 with half as many of two rows' loads each), float32, whose dz are three parts,
+// with half of them (147 us, 5.5 TB/s; 163).
 template <typename T, int PARTS, bool VEC>
-__global__ void __launch_bounds__(256, 2) dgate_kernel(int64_t rows, int64_t n, const T* dy, int64_t lddy, const T* z,
-                                                       int64_t ldz, int act, bf16* dz, int64_t lddz, float* part,
-                                                       int slab_size) {
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2)
+    dgate_kernel(int64_t rows, int64_t n, const T* dy, int64_t lddy, const T* z, int64_t ldz, int act, bf16* dz,
+                 int64_t lddz, float* part, int slab_size) {
     __shared__ float sums[8][kWidth + 8];
     pdl_trigger();
     pdl_wait();
@@ -172,50 +174,25 @@ __global__ void __launch_bounds__(256, 2) dgate_kernel(int64_t rows, int64_t n, 
     };
     if (column(0) < width) {
         with_act(act, [&](auto f) {
-            constexpr int N = sizeof(T) / 2, R = VEC ? 2 / N : 1;  // 16-byte words of eight elements; rows
-            int64_t r = r0 + l;
-            if (VEC) {
-                const int c = column(0);
-                for (; r + 8 * (R - 1) < r1; r += 8 * R) {
-                    uint4 d[R][N], g[R][N], v[R][N];
-#pragma unroll
-                    for (int k = 0; k < R; ++k)
-#pragma unroll
-                        for (int q = 0; q < N; ++q) {
-                            d[k][q] = __ldcs(reinterpret_cast<const uint4*>(dy + (r + 8 * k) * lddy + c) + q);
-                            g[k][q] = __ldcs(reinterpret_cast<const uint4*>(z + (r + 8 * k) * ldz + c) + q);
-                            v[k][q] = __ldcs(reinterpret_cast<const uint4*>(z + (r + 8 * k) * ldz + n + c) + q);
-                        }
-#pragma unroll
-                    for (int k = 0; k < R; ++k) {
-                        float df[8], gf[8], vf[8];
-#pragma unroll
-                        for (int t = 0; t < 8; ++t) {
-                            df[t] = to_float(reinterpret_cast<const T*>(d[k])[t]);
-                            gf[t] = to_float(reinterpret_cast<const T*>(g[k])[t]);
-                            vf[t] = to_float(reinterpret_cast<const T*>(v[k])[t]);
-                        }
-                        one(f, r + 8 * k, df, gf, vf);
-                    }
-                }
-            }
-#pragma unroll 1
-            for (; r < r1; r += 8) {
-                float df[8], gf[8], vf[8];
+            auto load = [&](const T* from, float(&v)[8]) {
                 if (VEC) {
-                    load8(dy + r * lddy + column(0), true, 8, df);
-                    load8(z + r * ldz + column(0), true, 8, gf);
-                    load8(z + r * ldz + n + column(0), true, 8, vf);
+                    constexpr int N = sizeof(T) / 2;  // 16-byte words of eight elements
+                    uint4 raw[N];
+#pragma unroll
+                    for (int q = 0; q < N; ++q) raw[q] = __ldcs(reinterpret_cast<const uint4*>(from + column(0)) + q);
+#pragma unroll
+                    for (int t = 0; t < 8; ++t) v[t] = to_float(reinterpret_cast<const T*>(raw)[t]);
                 } else {
 #pragma unroll
-                    for (int t = 0; t < 8; ++t) {
-                        const int c = column(t);
-                        const bool there = c < width;
-                        df[t] = there ? to_float(dy[r * lddy + c]) : 0.0f;
-                        gf[t] = there ? to_float(z[r * ldz + c]) : 0.0f;
-                        vf[t] = there ? to_float(z[r * ldz + n + c]) : 0.0f;
-                    }
+                    for (int t = 0; t < 8; ++t) v[t] = column(t) < width ? to_float(from[column(t)]) : 0.0f;
                 }
+            };
+#pragma unroll 1
+            for (int64_t r = r0 + l; r < r1; r += 8) {
+                float df[8], gf[8], vf[8];
+                load(dy + r * lddy, df);
+                load(z + r * ldz, gf);
+                load(z + r * ldz + n, vf);
                 one(f, r, df, gf, vf);
             }
         });

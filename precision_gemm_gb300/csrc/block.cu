@@ -742,8 +742,9 @@ BlockPlan plan_block(int64_t t, int64_t n, int64_t k, int num_sms, int force_bn,
         // microseconds of a block of k and of a tile's ends, measured at 1024 x 4096 by k of 4096 and 14336
         const double step = bn == 256 ? 0.40 : (bn == 128 ? 0.22 : 0.18), end = bn == 256 ? 3.2 : (bn == 128 ? 1.9 : 1.5);
         const int64_t tiles = cdiv(t, paired ? 2 * kRows : kRows) * cdiv(n, bn);
-        for (int64_t want = 1; want <= std::max<int64_t>(kb, 1); ++want) {
-            if (force_split ? want != std::min<int64_t>(force_split, std::max<int64_t>(kb, 1)) : want > 1 && tiles * want > 3 * at_once) continue;
+        const int64_t forced = std::min<int64_t>(force_split, std::max<int64_t>(kb, 1));
+        const int64_t most = force_split ? forced : std::max<int64_t>(std::min<int64_t>(kb, 3 * at_once / tiles), 1);
+        for (int64_t want = force_split ? forced : 1; want <= most; ++want) {
             const int64_t split_kb = std::max<int64_t>(cdiv(kb, want), 1), split = std::max<int64_t>(cdiv(kb, split_kb), 1);
             const double us = static_cast<double>(cdiv(tiles * split, at_once)) * (split_kb * step + end) +
                               (split > 1 ? 1.0 + 0.12 * split + 8e-7 * split * t * n : 0.0);

@@ -513,8 +513,9 @@ int sgemm_block_linear(int dtype, int64_t t, int64_t n, int64_t k, const void *x
  * eps)^-1/2, y = (x - mean) rstd w + bias, the squares taken around the mean.
  *
  *   dtype (1); t >= 0, n >= 1 (2, 3): x and y are t x n; x, ldx (4, 5); w and bias, n
- *   elements each, or NULL for ones and zeros (6, 7); eps >= 0 (8); y, ldy (9, 10); mean
- *   and rstd, t floats each, or NULL (11, 12): sgemm_layer_norm_backward reads them.
+ *   elements each, or NULL for ones and zeros (6, 7); eps >= 0 (8); y, which may be x
+ *   with its ld, ldy (9, 10); mean and rstd, t floats each, or NULL (11, 12):
+ *   sgemm_layer_norm_backward reads them.
  *
  * A NaN or infinity makes its own row NaN.
  */

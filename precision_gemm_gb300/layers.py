@@ -402,8 +402,8 @@ def block_linear(x, w, scales, bias=None, act="none", residual=None, x_scales=No
 def layer_norm(x, w=None, bias=None, eps=1e-5, stats=False, out=None, stream=None):
     """y = (x - mean) rstd w + bias for the rows of x (..., n), w and bias (n) or None,
     with rstd = (variance + eps)^-1/2; returns y.  stats=True also returns mean and rstd
-    (float32, one of each row), which layer_norm_backward reads; a tensor given as out is
-    written instead."""
+    (float32, one of each row), which layer_norm_backward reads; a tensor given as out,
+    which may be x, is written instead."""
     if stream is not None:
         return _on(stream, layer_norm, x, w, bias, eps, stats, out)
     lib = load_library()

@@ -93,6 +93,21 @@ def test_quantize_every_bfloat16_quotient():
         assert torch.equal(_bits(scales), _bits(ws)) and torch.equal(_bits(q), _bits(wq))
 
 
+def test_quantize_random_quotients():
+    """Two million float32 numbers of every magnitude, some blocks with values far below their
+    largest, against the divisions of the definition."""
+    g = _gen(8)
+    for dtype in DTYPES:
+        x = torch.randn(2048, 1024, generator=g)
+        x *= torch.exp2(torch.randint(-120, 120, (2048, 8), generator=g).float()).repeat_interleave(128, 1)
+        x = torch.where(torch.rand(x.shape, generator=g) < 0.05, x * 2.0 ** -20, x).to(dtype)
+        q, scales = pg.quantize(x.cuda())
+        b = x.float().view(2048, 8, 128)
+        ws = torch.clamp_min(b.abs().amax(2) / torch.tensor(448.0), torch.finfo(torch.float32).tiny)
+        wq = (b / ws[:, :, None]).to(E4M3).view(2048, 1024)
+        assert torch.equal(_bits(scales), _bits(ws)) and torch.equal(_bits(q), _bits(wq))
+
+
 @pytest.mark.parametrize("rows", [1, 128])
 def test_quantize_zeros_infinities_nan_and_strides(rows):
     x = torch.randn(140, 400, generator=_gen(2))
@@ -184,6 +199,18 @@ def test_block_strides_and_alignment(dtype, t, n, k, pad, offset):
     both = r.cuda()
     assert pg.block_linear(x.cuda(), w, s, b.cuda(), "silu", both, out=both) is both
     assert torch.equal(both, y)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS.get)
+@pytest.mark.parametrize("t,n,k", [(1, 300, 256), (7, 333, 500), (40, 96, 2048), (300, 520, 256), (300, 77, 300)])
+def test_block_residual_in_place(dtype, t, n, k):
+    """residual and out may be the same tensor, in every kernel that finishes a product."""
+    g = _gen(t + n)
+    x, r = _draw(g, dtype, t, k).cuda(), _draw(g, dtype, t, n).cuda()
+    w, s = _weights(g, n, k)
+    want = pg.block_linear(x, w, s, act="silu", residual=r)
+    assert pg.block_linear(x, w, s, act="silu", residual=r, out=r) is r
+    assert torch.equal(r, want)
 
 
 def test_block_scales_meet_their_blocks():

@@ -256,6 +256,24 @@ def test_norm_repeats_bitwise_on_streams_and_in_graphs(dtype):
     assert torch.equal(y, first[0])
 
 
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS.get)
+@pytest.mark.parametrize("t,n", [(5, 64), (300, 777), (700, 4096), (9, 16384), (4, 16386)])
+def test_norm_in_place(dtype, t, n):
+    """y over x, and dx over the gradient that is added to it."""
+    g = torch.Generator().manual_seed(n)
+    x, dy, r = (_draw(g, dtype, t, n).cuda() for _ in range(3))
+    w = _draw(g, dtype, n).cuda()
+    want, mean, rstd = pg.layer_norm(x, w, w, stats=True)
+    dx = pg.layer_norm_backward(dy, x, w, mean, rstd, r)[0]
+    lib, code = pg.load_library(), 0 if dtype == torch.float32 else 1
+    rc = lib.sgemm_layer_norm_backward(code, t, n, dy.data_ptr(), n, x.data_ptr(), n, w.data_ptr(), mean.data_ptr(),
+                                       rstd.data_ptr(), r.data_ptr(), n, r.data_ptr(), n, None, None,
+                                       torch.cuda.current_stream().cuda_stream)
+    assert rc == 0 and torch.equal(r, dx)
+    y = x.clone()
+    assert pg.layer_norm(y, w, w, out=y) is y and torch.equal(y, want)
+
+
 def test_norm_large_offsets():
     """Rows that start beyond 2^31 elements, the last ones of a tall matrix."""
     t, n = 2 ** 20 + 3, 2100

@@ -18,6 +18,13 @@ IDS = {torch.float32: "f32", torch.bfloat16: "bf16"}
 UNITS = 168 * 2.0 ** -24
 
 
+@pytest.fixture(scope="module", autouse=True)
+def _release():
+    """Streams come back from torch's pool of 32: they leave here without workspaces."""
+    yield
+    pg.workspace_release()
+
+
 @pytest.fixture(autouse=True)
 def _healthy():
     pg.load_library()

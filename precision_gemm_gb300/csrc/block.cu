@@ -23,8 +23,9 @@
 //
 // Bound: what a CTA's shared memory gives its MMAs.  A block of 128 x 256 x 128 reads 48 KiB of
 // operands that TMA wrote there before (768 cycles at 128 bytes each); it takes 785.
-// Measured with quantized x, bfloat16 results (L2 cold): 4096 x 8192 x 4096 124 us (2.2 PFLOP/s),
-// 1024 x 4096 x 4096 28 us, 64 x 4096 x 4096 16 us.
+// Measured with quantized x, bfloat16 results (L2 cold): 4096 x 8192 x 4096 127 us (2.2 PFLOP/s), of
+// which a unit's loop takes four fifths; with bias and gelu 148, with bias, silu and residual 145 (180 while
+// each lane read its own row's); 1024 x 4096 x 4096 26 us, 64 x 4096 x 4096 14 us.
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -48,6 +49,7 @@ constexpr int kRegsFew = 56, kRegsMany = 224;
 static_assert(4 * kRegsFew + 8 * kRegsMany <= 12 * 168, "the shares must be there");
 constexpr int kScales = 4;      // blocks of k whose scales come together
 constexpr int kScaleSlots = 2;  // such groups ready or on their way
+constexpr int kBiasSlots = 3;   // units whose bias is there or in use: the scales run two groups ahead, of two units at most
 constexpr int kOutBytes = 64;   // of each row of a warp's results, on their way out together
 constexpr int kGroupTiles = 8;
 
@@ -181,7 +183,8 @@ struct Cfg {
     static constexpr int BAR_BYTES = (2 * STAGES + 2 * BUFFERS + 2 * kScaleSlots + 1) * 8 + 16;
     static constexpr int OUT_BYTES = kEpiWarps * 32 * kOutBytes;
     static constexpr int SCALE_BYTES = kScaleSlots * 2 * kRows * kScales * 4;  // of the rows, for each half of the columns
-    static constexpr size_t SMEM = 1024 + static_cast<size_t>(STAGES) * STAGE_BYTES + OUT_BYTES + SCALE_BYTES + BAR_BYTES;
+    static constexpr int BIAS_BYTES = kBiasSlots * BN * 4;
+    static constexpr size_t SMEM = 1024 + static_cast<size_t>(STAGES) * STAGE_BYTES + OUT_BYTES + SCALE_BYTES + BIAS_BYTES + BAR_BYTES;
     static_assert(A_BYTES % 1024 == 0 && HALF_BYTES % 1024 == 0, "slots need 1 KiB alignment");
 };
 
@@ -214,22 +217,18 @@ struct Rows {  // of a matrix
     int64_t ld;
 };
 
-// Results of the sums v of N columns from i on of row j (clamped to the rows there are), whole: all of
-// them are columns of y, and eights of them lie at 16-byte boundaries.
-template <typename T, int ACT, int N>
-__device__ __forceinline__ void results(const Params& p, int64_t j, int64_t i, bool whole, float (&v)[N]) {
+// Results of the sums v of eight columns from i on of row j, `valid` of them there.
+template <typename T, int ACT>
+__device__ __forceinline__ void results(const Params& p, int64_t j, int64_t i, int valid, float (&v)[8]) {
     auto add = [&](const T* from) {
+        float b[8];
+        load8(from, p.vec, valid, b);
 #pragma unroll
-        for (int h = 0; h < N; h += 8) {
-            float b[8];
-            load8(from + h, whole, whole ? 8 : static_cast<int>(min(p.n - i - h, int64_t(8))), b);
-#pragma unroll
-            for (int t = 0; t < 8; ++t) v[h + t] += b[t];
-        }
+        for (int t = 0; t < 8; ++t) v[t] += b[t];
     };
     if (p.bias) add(static_cast<const T*>(p.bias) + i);
 #pragma unroll
-    for (int t = 0; t < N; ++t) v[t] = act_value<ACT, std::is_same<T, bf16>::value>(v[t]);
+    for (int t = 0; t < 8; ++t) v[t] = act_value<ACT, std::is_same<T, bf16>::value>(v[t]);
     if (p.residual) add(static_cast<const T*>(p.residual) + j * p.ldr + i);
 }
 
@@ -241,7 +240,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = align_smem_1024(smem_raw);
     float4* scale_ring = reinterpret_cast<float4*>(smem + S * C::STAGE_BYTES + C::OUT_BYTES);  // [slot][half][row]
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S * C::STAGE_BYTES + C::OUT_BYTES + C::SCALE_BYTES);
+    float* biases = reinterpret_cast<float*>(smem + S * C::STAGE_BYTES + C::OUT_BYTES + C::SCALE_BYTES);  // [slot][column]
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S * C::STAGE_BYTES + C::OUT_BYTES + C::SCALE_BYTES + C::BIAS_BYTES);
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 2 * S + 2 * NB + 2 * kScaleSlots + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
     const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + S);
@@ -407,8 +407,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             __syncwarp();
         } else if (warp == 2) {
             // ---------------- scales ----------------
-            // sx sw of this CTA's rows and each half of the columns, several blocks of k ahead of their use
-            int slot = 0;
+            // sx sw of this CTA's rows and each half of the columns, several blocks of k ahead of their use; a unit's
+            // bias comes with its first ones
+            int slot = 0, bias_slot = 0;
             uint32_t phase = 1;
             bool ok = true;
             for (int u = first; u < units && ok; u += step) {
@@ -440,6 +441,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         for (int r = 0; r < 4; ++r)
                             scale_ring[(2 * slot + h) * kRows + 32 * r + lane] =
                                 make_float4(a[r][0] * b[h][0], a[r][1] * b[h][1], a[r][2] * b[h][2], a[r][3] * b[h][3]);
+                    if (kb == 0 && p.bias && !p.part) {
+#pragma unroll
+                        for (int c = lane; c < BN; c += 32)
+                            if (x.i0 + c < p.n) biases[bias_slot * BN + c] = to_float(static_cast<const T*>(p.bias)[x.i0 + c]);
+                    }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(scale_full0 + 8 * slot);
                     if (++slot == kScaleSlots) {
@@ -447,6 +453,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         phase ^= 1;
                     }
                 }
+                if (++bias_slot == kBiasSlots) bias_slot = 0;
             }
             __syncwarp();
         }
@@ -466,7 +473,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         int buf = 0;
         uint32_t acc_phase = 0;
         bool ok = true;
-        int slot = 0;
+        int slot = 0, bias_slot = 0;
         uint32_t scale_phase = 0;
         for (int u = first; u < units && ok; u += step) {
             const Unit x = unit_of(u);
@@ -572,8 +579,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (lane == 0) raise_abort(abort_flag, p.status);
                 break;
             }
-            // The results go back to the warp's own columns of the last buffer and from there, 16 at a
-            // time, through the epilogue: a loop, where registers would want it written out.
+            // The results go back to the warp's own columns of the last buffer and from there, 64 bytes of
+            // a row at a time, through the epilogue: a loop, where registers would want it written out.
             const uint32_t at = base + last * BN;
             if (there) {
 #pragma unroll
@@ -588,16 +595,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     tmem_st_32x32b_x32(at + kCols * c, v);
                 }
                 tmem_wait_st();
+                float* const bias = biases + bias_slot * BN + C::MINE * half;
+                if (x.nkb == 0 && p.bias)  // no scales came, and no bias with them
+                    for (int c = lane; c < C::MINE && i0 + c < p.n; c += 32) bias[c] = to_float(static_cast<const T*>(p.bias)[i0 + c]);
+                __syncwarp();
                 // The columns as elements TO, 64 bytes of 32 rows at a time.  They change places in shared memory
                 // (16-byte words, swizzled so that eight rows' words fall on all banks), so that four lanes write
-                // a row's 64 bytes together.
-                auto emit = [&](auto element, Rows rows_of, bool vec, auto finish) {
+                // a row's 64 bytes together; the residual comes the same way round before.
+                auto emit = [&](auto element, Rows rows_of, bool vec, const void* residual, auto value) {
                     using TO = decltype(element);
                     constexpr int SPAN = kOutBytes / static_cast<int>(sizeof(TO)), N = static_cast<int>(sizeof(TO)) / 2;
-                    TO* const mine = static_cast<TO*>(rows_of.ptr) + (j < p.t ? j : 0) * rows_of.ld + i0;
-                    TO* const shared_out = static_cast<TO*>(rows_of.ptr) + (row0 + lane / 4) * rows_of.ld + i0 +
-                                           (lane & 3) * (16 / static_cast<int>(sizeof(TO)));
-                    const int rows_left = p.t - row0 - lane / 4;
+                    const int64_t row = row0 + lane / 4;
+                    const int i4 = i0 + (lane & 3) * (16 / static_cast<int>(sizeof(TO))), rows_left = p.t - row0 - lane / 4;
+                    TO* const shared_out = static_cast<TO*>(rows_of.ptr) + row * rows_of.ld + i4;
+                    auto word = [&](int r, int q) {  // 16-byte word q of row r
+                        return reinterpret_cast<uint4*>(out + kOutBytes * r + 16 * (q ^ ((r >> 1) & 3)));
+                    };
+                    uint4 rest[4] = {};  // (left undefined where there is no residual, they cost 336 bytes of spills)
+                    auto fetch = [&](int c) {
+                        if (!residual || !vec || c >= C::MINE || p.n - i0 - c < SPAN) return;
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            if (8 * r < rows_left)
+                                rest[r] = *reinterpret_cast<const uint4*>(static_cast<const TO*>(residual) + (row + 8 * r) * p.ldr + i4 + c);
+                    };
+                    fetch(0);
 #pragma unroll 1
                     for (int c = 0; c < C::MINE && i0 + c < p.n; c += SPAN) {
                         uint32_t v[SPAN];
@@ -606,51 +628,78 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             tmem_ld_32x32b_x32(at + c, v);
                         else
                             tmem_ld_32x32b_x16(at + c, v);
+                        const bool whole = vec && p.n - i0 - c >= SPAN;
+                        if (whole && residual) {
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) *word(8 * r + lane / 4, lane & 3) = rest[r];
+                            __syncwarp();
+                            fetch(c + SPAN);
+                        }
                         tmem_wait_ld(v);
                         float f[SPAN];
 #pragma unroll
                         for (int k = 0; k < SPAN; ++k) f[k] = __uint_as_float(v[k]);
-                        const bool whole = vec && p.n - i0 - c >= SPAN;
-                        finish(i0 + c, whole, f);
+                        value(c, f);
                         if (whole) {
+                            if (residual) {
+#pragma unroll
+                                for (int h = 0; h < SPAN; h += 8) {
+                                    TO e[8];
+#pragma unroll
+                                    for (int k = 0; k < N; ++k) reinterpret_cast<uint4*>(e)[k] = *word(lane, h / 8 * N + k);
+#pragma unroll
+                                    for (int k = 0; k < 8; ++k) f[h + k] += to_float(e[k]);
+                                }
+                            }
 #pragma unroll
                             for (int h = 0; h < SPAN; h += 8) {
                                 TO e[8];
 #pragma unroll
                                 for (int k = 0; k < 8; ++k) e[k] = from_float<TO>(f[h + k]);
 #pragma unroll
-                                for (int k = 0; k < N; ++k)  // N 16-byte words of eight elements
-                                    *reinterpret_cast<uint4*>(out + kOutBytes * lane + 16 * ((h / 8 * N + k) ^ ((lane >> 1) & 3))) =
-                                        reinterpret_cast<const uint4*>(e)[k];
+                                for (int k = 0; k < N; ++k) *word(lane, h / 8 * N + k) = reinterpret_cast<const uint4*>(e)[k];
                             }
                             __syncwarp();
                             uint4 w[4];
 #pragma unroll
-                            for (int r = 0; r < 4; ++r) {
-                                const int row = 8 * r + lane / 4;
-                                w[r] = *reinterpret_cast<const uint4*>(out + kOutBytes * row + 16 * ((lane & 3) ^ ((row >> 1) & 3)));
-                            }
+                            for (int r = 0; r < 4; ++r) w[r] = *word(8 * r + lane / 4, lane & 3);
 #pragma unroll
                             for (int r = 0; r < 4; ++r)
                                 if (8 * r < rows_left) *reinterpret_cast<uint4*>(shared_out + c + 8 * r * rows_of.ld) = w[r];
                         } else if (j < p.t) {
+                            TO* const mine = static_cast<TO*>(rows_of.ptr) + j * rows_of.ld + i0 + c;
 #pragma unroll
                             for (int k = 0; k < SPAN; ++k)
-                                if (i0 + c + k < p.n) mine[c + k] = from_float<TO>(f[k]);
+                                if (i0 + c + k < p.n) {
+                                    if (residual) f[k] += to_float(static_cast<const TO*>(residual)[j * p.ldr + i0 + c + k]);
+                                    mine[k] = from_float<TO>(f[k]);
+                                }
                         }
                     }
                 };
                 if (p.part)
-                    emit(float(), {p.part + static_cast<int64_t>(x.slice) * p.t * p.ldp, p.ldp}, true,
-                         [](int, bool, auto&) {});
+                    emit(float(), {p.part + static_cast<int64_t>(x.slice) * p.t * p.ldp, p.ldp}, true, nullptr, [](int, auto&) {});
                 else
                     with_act(p.act, [&](auto act) {
-                        emit(T(), {p.y, p.ldy}, p.vec != 0, [&](int i, bool whole, auto& f) {
-                            results<T, decltype(act)::value>(p, j < p.t ? j : 0, i, whole, f);
+                        emit(T(), {p.y, p.ldy}, p.vec != 0, p.residual, [&](int c, auto& f) {
+                            constexpr int SPAN = sizeof(f) / sizeof(float);
+                            if (p.bias) {
+#pragma unroll
+                                for (int k = 0; k < SPAN; k += 4) {
+                                    const float4 b = *reinterpret_cast<const float4*>(bias + c + k);
+                                    f[k] += b.x, f[k + 1] += b.y, f[k + 2] += b.z, f[k + 3] += b.w;
+                                }
+                            }
+#pragma unroll
+                            for (int k = 0; k < SPAN; k += 2) {
+                                const float2 y = act_value2<decltype(act)::value, std::is_same<T, bf16>::value>(make_float2(f[k], f[k + 1]));
+                                f[k] = y.x, f[k + 1] = y.y;
+                            }
                         });
                     });
             }
             if (x.nkb > 0) free_buffer(last);
+            if (++bias_slot == kBiasSlots) bias_slot = 0;
         }
     }
 
@@ -680,7 +729,7 @@ __global__ void __launch_bounds__(256) block_sum_kernel(const Params p) {
         v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
     }
     const int valid = static_cast<int>(min(p.n - i, int64_t(8)));
-    with_act(p.act, [&](auto act) { results<T, decltype(act)::value>(p, j, i, p.vec && valid == 8, v); });
+    with_act(p.act, [&](auto act) { results<T, decltype(act)::value>(p, j, i, valid, v); });
     store8(static_cast<T*>(p.y) + j * p.ldy + i, p.vec, valid, v);
 }
 

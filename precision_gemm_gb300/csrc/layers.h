@@ -153,6 +153,29 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
 template <int ACT, bool FAST>
+__device__ __forceinline__ float2 act_value2(float2 z) {
+    if (FAST && (ACT == SGEMM_ACT_SILU || ACT == SGEMM_ACT_GELU_TANH)) {
+        const float2 w = ACT == SGEMM_ACT_SILU ? z
+                                               : mul2(both(1.59576912160573072f), fma2(mul2(mul2(both(0.044715f), z), z), z, z));
+        const float2 u = mul2(both(-1.44269504f), w);
+        const float2 v = add2(make_float2(exp2_approx(u.x), exp2_approx(u.y)), both(1.0f));
+        return mul2(z, make_float2(reciprocal_approx(v.x), reciprocal_approx(v.y)));
+    }
+    if (FAST && ACT == SGEMM_ACT_GELU) {  // as act_value and normal_tail
+        const float2 a = make_float2(fabsf(z.x), fabsf(z.y)), d = fma2(both(0.23164189f), a, both(1.0f));
+        const float2 t = make_float2(reciprocal_approx(d.x), reciprocal_approx(d.y));
+        const float2 u = mul2(mul2(both(-0.72134752f), z), z);
+        float2 q = fma2(both(0.5307027145f), t, both(-0.7265760135f));
+        q = fma2(q, t, both(0.7107068705f));
+        q = fma2(q, t, both(-0.142248368f));
+        q = fma2(q, t, both(0.127414796f));
+        const float2 tail = mul2(mul2(q, t), make_float2(exp2_approx(u.x), exp2_approx(u.y)));
+        return fma2(make_float2(-fminf(a.x, 3.4e38f), -fminf(a.y, 3.4e38f)), tail, make_float2(relu(z.x), relu(z.y)));
+    }
+    return make_float2(act_value<ACT, FAST>(z.x), act_value<ACT, FAST>(z.y));
+}
+
+template <int ACT, bool FAST>
 __device__ __forceinline__ float2 act_derivative2(float2 z) {
     if (FAST && ACT == SGEMM_ACT_SILU) {
         const float2 u = mul2(both(-1.44269504f), z);

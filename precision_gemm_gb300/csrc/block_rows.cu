@@ -1,4 +1,4 @@
-// Products with 8-bit weights (block.cu) for a few rows of x, up to eight: a decoding step.  Reading
+// Products with 8-bit weights (block.cu) for a few rows of x, up to sixteen: a decoding step.  Reading
 // the weights once is all there is to do, so they stream into registers, 16 bytes per lane and load,
 // several loads in flight, and meet x in warp-level matrix instructions (m16n8k32, e4m3, FP32 sums):
 // 16 weight rows by eight rows of x take two of them per 64 k and 1 KiB of weights.
@@ -12,7 +12,7 @@
 // row's k; their sums are added in order.
 //
 // Measured with quantized x (L2 cold): 1 and 8 rows x 8192 x 4096 9.1 and 11.5 us (3.7 and 3.0 TB/s), 32768 x 4096
-// 27.6 and 29.2 us (4.9 and 4.6 TB/s); the tensor-core kernel of block.cu needs 15 and 41 us.
+// 26.4 and 28.5 us (5.1 and 4.7 TB/s); the tensor-core kernel of block.cu needs 15 and 32 us.
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -26,7 +26,7 @@ namespace pg {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kMostRows = 8;     // columns of a matrix instruction
+constexpr int kCols = 8;         // rows of x of a matrix instruction, its columns
 constexpr int kGroup = 16;       // weight rows of a warp
 constexpr int kAhead = 2;        // blocks of 128 k on their way
 constexpr int kBatch = 4;        // blocks of x that a thread rounds together
@@ -69,10 +69,11 @@ __device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-template <typename T>
+// C matrix instructions side by side: 8 C rows of x.
+template <typename T, int C>
 __global__ void __launch_bounds__(32 * kWarps, 2) block_rows_kernel(const RowsParams q) {
     extern __shared__ __align__(16) uint8_t xs[];  // x's rows in e4m3, then their scales
-    __shared__ float sums[kWarps][kGroup][kMostRows + 1];
+    __shared__ float sums[kWarps][kGroup][kCols * C + 1];
     const BlockProduct& p = q.b;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, c4 = lane % 4;
     const int t = static_cast<int>(p.t), kbs = q.kbs;
@@ -148,24 +149,27 @@ __global__ void __launch_bounds__(32 * kWarps, 2) block_rows_kernel(const RowsPa
     __syncthreads();
 
     const float* sw = p.w_scales + min(i0, p.n - 1) / SGEMM_BLOCK * p.ldws;
-    const uint8_t* x_row = xs + min(g, t - 1) * q.x_stride + 16 * c4;
-    const float* sx0 = x_scale + min(2 * c4, t - 1) * kbs;
-    const float* sx1 = x_scale + min(2 * c4 + 1, t - 1) * kbs;
-    float acc[4] = {};
+    const uint8_t* x_row = xs + 16 * c4;
+    float acc[C][4] = {};
     auto add_block = [&](const uint4(&a)[2][2], int kb, float s) {
-        float c[4] = {};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (g < t) x = *reinterpret_cast<const uint4*>(x_row + kb * SGEMM_BLOCK + 64 * h);
-            mma_e4m3(c, a[h][0].x, a[h][1].x, a[h][0].y, a[h][1].y, x.x, x.y);
-            mma_e4m3(c, a[h][0].z, a[h][1].z, a[h][0].w, a[h][1].w, x.z, x.w);
+        for (int m = 0; m < C; ++m) {
+            float c[4] = {};
+            const int row = kCols * m + g;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint4 x = make_uint4(0, 0, 0, 0);
+                if (row < t) x = *reinterpret_cast<const uint4*>(x_row + row * q.x_stride + kb * SGEMM_BLOCK + 64 * h);
+                mma_e4m3(c, a[h][0].x, a[h][1].x, a[h][0].y, a[h][1].y, x.x, x.y);
+                mma_e4m3(c, a[h][0].z, a[h][1].z, a[h][0].w, a[h][1].w, x.z, x.w);
+            }
+            const int first = kCols * m + 2 * c4;
+            const float s0 = x_scale[min(first, t - 1) * kbs + kb] * s, s1 = x_scale[min(first + 1, t - 1) * kbs + kb] * s;
+            acc[m][0] = fmaf(c[0], s0, acc[m][0]);
+            acc[m][1] = fmaf(c[1], s1, acc[m][1]);
+            acc[m][2] = fmaf(c[2], s0, acc[m][2]);
+            acc[m][3] = fmaf(c[3], s1, acc[m][3]);
         }
-        const float s0 = sx0[kb] * s, s1 = sx1[kb] * s;
-        acc[0] = fmaf(c[0], s0, acc[0]);
-        acc[1] = fmaf(c[1], s1, acc[1]);
-        acc[2] = fmaf(c[2], s0, acc[2]);
-        acc[3] = fmaf(c[3], s1, acc[3]);
     };
     float next_sw = kb0 < kb1 ? __ldg(sw + kb0) : 0.0f;
     for (int kb = kb0; kb < whole; kb += kAhead) {
@@ -193,7 +197,9 @@ __global__ void __launch_bounds__(32 * kWarps, 2) block_rows_kernel(const RowsPa
         add_block(a, whole, next_sw);
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) sums[warp][g + 8 * (e / 2)][2 * c4 + e % 2] = acc[e];
+    for (int m = 0; m < C; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sums[warp][g + 8 * (e / 2)][kCols * m + 2 * c4 + e % 2] = acc[m][e];
     __syncthreads();
     const int per_block = kWarps / q.ks * kGroup;
     for (int v = threadIdx.x; v < per_block * t; v += 32 * kWarps) {
@@ -218,7 +224,12 @@ static size_t rows_shared(int64_t t, int64_t k) {
     return static_cast<size_t>(t) * (kbs * SGEMM_BLOCK + 64 + kbs * 4);
 }
 
-bool block_few_rows(int64_t t, int64_t k) { return t <= kMostRows && k > 0 && rows_shared(t, k) <= kMostShared; }
+// Nine to sixteen rows take two instructions side by side, where that beats the tensor-core kernel with its slices
+// of k: 9 and 16 rows of 1024 x 1024 6.3 and 7.9 us (8.2 and 8.2), of 4096 x 4096 10.0 and 11.9 (12.3 and 12.6), of
+// 8192 x 4096 13.1 and 15.3 (15.1 and 16.0), but of 32768 x 4096 31.6 and 35.9 (32.0 and 30.6).
+bool block_few_rows(int64_t t, int64_t n, int64_t k) {
+    return t <= (n * k <= int64_t(1) << 25 ? 2 * kCols : kCols) && k > 0 && rows_shared(t, k) <= kMostShared;
+}
 
 cudaError_t launch_block_rows(const BlockProduct& b, int num_sms, cudaStream_t st) {
     RowsParams q{};
@@ -233,16 +244,19 @@ cudaError_t launch_block_rows(const BlockProduct& b, int num_sms, cudaStream_t s
     while (q.ks < kWarps && groups * q.ks < int64_t(8) * num_sms && q.kbs >= 2 * kAhead * q.ks) q.ks *= 2;
     const int64_t per_block = kWarps / q.ks * kGroup;
     const size_t smem = rows_shared(b.t, b.k);
-    auto go = [&](auto zero) {
+    auto go = [&](auto zero, auto cols) {
         using T = decltype(zero);
-        auto kern = block_rows_kernel<T>;
+        auto kern = block_rows_kernel<T, decltype(cols)::value>;
         static std::atomic<uint64_t> smem_set{0};
         const cudaError_t e = set_smem_limit_once(smem_set, reinterpret_cast<const void*>(kern), static_cast<int>(kMostShared));
         if (e != cudaSuccess) return e;
         return launch_kernel(true, kern, dim3(static_cast<unsigned>((b.n + per_block - 1) / per_block)), dim3(32 * kWarps),
                              smem, st, q);
     };
-    return b.dtype == SGEMM_F32 ? go(float()) : go(bf16());
+    auto with_cols = [&](auto zero) {
+        return b.t <= kCols ? go(zero, std::integral_constant<int, 1>()) : go(zero, std::integral_constant<int, 2>());
+    };
+    return b.dtype == SGEMM_F32 ? with_cols(float()) : with_cols(bf16());
 }
 
 }  // namespace pg

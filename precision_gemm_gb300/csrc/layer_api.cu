@@ -528,7 +528,7 @@ PG_EXPORT int sgemm_block_linear(int dtype, int64_t t, int64_t n, int64_t k, con
     CallContext c;
     PG_CHECK(call_begin(&c));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const bool few = block_few_rows(t, k) && c.force_bn == 0 && c.force_split == 0;
+    const bool few = block_few_rows(t, n, k) && c.force_bn == 0 && c.force_split == 0;
     const BlockPlan plan = plan_block(t, n, k, c.sms, c.force_bn, c.force_split);
     return with_workspace(c, st, [&](Arena& a) {
         BlockProduct p{dtype, t, n, k, static_cast<const uint8_t*>(x), ldx, x_scales, ldxs, 1, w, ldw, w_scales, ldws, bias,

@@ -500,12 +500,12 @@ BlockPlan plan_block(int64_t t, int64_t n, int64_t k, int num_sms, int force_bn,
 int launch_block(const CallContext& c, const BlockProduct& p, const BlockPlan& plan, float* part, cudaStream_t st,
                  int* launches);
 
-// The same for up to eight rows (block_few_rows), x of the call's type (x_scales null) or e4m3.
+// The same for few rows (block_few_rows), x of the call's type (x_scales null) or e4m3.
 // Values of x up to which each thread block rounds them by itself; from there on a kernel before it does.  One row
 // of 1024 / 4096 / 8192 / 16384 values by 1024 / 4096 / 4096 / 512 features: 4.9 / 8.3 / 12.0 / 16.2 us by itself,
 // 6.1 / 9.2 / 11.8 / 12.0 with the kernel.
 constexpr int64_t kRawValues = 4096;
-bool block_few_rows(int64_t t, int64_t k);
+bool block_few_rows(int64_t t, int64_t n, int64_t k);
 cudaError_t launch_block_rows(const BlockProduct& p, int num_sms, cudaStream_t st);
 
 // Layer norm (norm.cu).  part: norm_part_bytes(), read where dw or db is asked for.

@@ -220,6 +220,21 @@ def test_block_residual_in_place(dtype, t, n, k):
     assert torch.equal(r, want)
 
 
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS.get)
+@pytest.mark.parametrize("n,k", [(333, 500), (40, 1030), (1100, 4096), (128, 16)])
+@pytest.mark.parametrize("t", [2, 7, 8, 9, 15, 16, 17])
+def test_block_few_rows(dtype, t, n, k):
+    """Around the numbers of rows where kernels change."""
+    g = _gen(t + n)
+    x, b, r = _draw(g, dtype, t, k), _draw(g, dtype, n), _draw(g, dtype, t, n)
+    w, s = _weights(g, n, k)
+    y = pg.block_linear(x.cuda(), w, s, b.cuda(), "gelu", r.cuda())
+    q, xs = quantized(x, 1)
+    want, _, den = R.linear(values(q, xs, 1), values(w.cpu(), s.cpu(), 128), b, "gelu", r)
+    R.close(y, want, den, dtype)
+    assert torch.equal(pg.block_linear(q.cuda(), w, s, b.cuda(), "gelu", r.cuda(), xs.cuda(), dtype=dtype), y)
+
+
 def test_block_scales_meet_their_blocks():
     """Every block's scale a power of two of its own and small whole numbers as values: each sum
     is exact, so a scale at another block shows."""

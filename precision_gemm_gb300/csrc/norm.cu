@@ -214,6 +214,7 @@ struct NormParams {
     float *mean, *rstd;
     int warps;       // of a team
     bool shared_wb;  // w and b have places in shared memory
+    bool vec;        // rows too wide to be held: all in 16-byte accesses
 };
 
 // V vectors of eight per thread, S rows on their way per team.
@@ -339,9 +340,28 @@ __global__ void __launch_bounds__(NT, kForwardThreads / NT) norm_kernel(const No
     }
 }
 
-// Rows of any width, a block to each: three passes over the row, two of which find it in
-// the caches.
-template <typename T>
+// Rows of any width, a block to each: three passes over the row, two of which find it in the caches.
+// E neighbouring columns of a thread at a time: eight where rows are at 16-byte boundaries, else one (2048 rows of
+// 32768 bfloat16 backwards 200 us, one at a time 385; 300 of 32769, eight at a time, 81, one at a time 49).
+template <typename T, int E>
+__device__ __forceinline__ void load_some(const T* p, int valid, float (&v)[E]) {
+    if constexpr (E == 8)
+        load8(p, true, valid, v);
+    else
+        v[0] = to_float(*p);
+}
+template <typename T, int E>
+__device__ __forceinline__ void store_some(T* p, int valid, const float (&v)[E]) {
+    if constexpr (E == 8)
+        store8(p, true, valid, v);
+    else
+        *p = from_float<T>(v[0]);
+}
+template <int E, typename F>
+__device__ __forceinline__ void for_columns(int64_t n, F f) {  // f(first column, columns there)
+    for (int64_t c = E * threadIdx.x; c < n; c += E * 1024) f(c, static_cast<int>(min(n - c, int64_t(E))));
+}
+template <typename T, int E>
 __global__ void __launch_bounds__(1024) norm_wide_kernel(const NormParams p) {
     __shared__ float slots[2][32];
     pdl_trigger();
@@ -350,24 +370,39 @@ __global__ void __launch_bounds__(1024) norm_wide_kernel(const NormParams p) {
     const T* x = static_cast<const T*>(p.x) + row * p.ldx;
     const T *w = static_cast<const T*>(p.w), *b = static_cast<const T*>(p.b);
     float sum = 0.0f;
-    for (int64_t c = threadIdx.x; c < p.n; c += 1024) sum += to_float(x[c]);
+    for_columns<E>(p.n, [&](int64_t c, int valid) {
+        float v[E];
+        load_some(x + c, valid, v);
+#pragma unroll
+        for (int t = 0; t < E; ++t) sum += v[t];
+    });
     const float count = static_cast<float>(p.n);
     const float mean = block_sum(sum, slots[0]) / count;
     sum = 0.0f;
-    for (int64_t c = threadIdx.x; c < p.n; c += 1024) {
-        const float d = to_float(x[c]) - mean;
-        sum = fmaf(d, d, sum);
-    }
+    for_columns<E>(p.n, [&](int64_t c, int valid) {
+        float v[E];
+        load_some(x + c, valid, v);
+#pragma unroll
+        for (int t = 0; t < E; ++t) {
+            const float d = v[t] - mean;
+            if (t < valid) sum = fmaf(d, d, sum);
+        }
+    });
     const float rstd = 1.0f / sqrtf(block_sum(sum, slots[1]) / count + p.eps);
     if (threadIdx.x == 0) {
         if (p.mean) p.mean[row] = mean;
         if (p.rstd) p.rstd[row] = rstd;
     }
     T* y = static_cast<T*>(p.y) + row * p.ldy;
-    for (int64_t c = threadIdx.x; c < p.n; c += 1024) {
-        const float h = (to_float(x[c]) - mean) * rstd;
-        y[c] = from_float<T>(fmaf(h, w ? to_float(w[c]) : 1.0f, b ? to_float(b[c]) : 0.0f));
-    }
+    for_columns<E>(p.n, [&](int64_t c, int valid) {
+        float v[E], g[E], a[E];
+        load_some(x + c, valid, v);
+        if (w) load_some(w + c, valid, g);
+        if (b) load_some(b + c, valid, a);
+#pragma unroll
+        for (int t = 0; t < E; ++t) v[t] = fmaf((v[t] - mean) * rstd, w ? g[t] : 1.0f, b ? a[t] : 0.0f);
+        store_some(y + c, valid, v);
+    });
 }
 
 struct NormBackwardParams {
@@ -385,6 +420,7 @@ struct NormBackwardParams {
     float* part;  // [block][dw, db][ldp]
     int64_t ldp;  // n to a multiple of four
     int warps;
+    bool vec;     // as in NormParams
 };
 
 template <typename T, int G, int V, int S, int NT, int B>
@@ -535,7 +571,7 @@ __global__ void __launch_bounds__(NT, B)
 }
 
 // dx of rows of any width, a block to each.
-template <typename T>
+template <typename T, int E>
 __global__ void __launch_bounds__(1024) norm_backward_wide_kernel(const NormBackwardParams p) {
     __shared__ float slots[2][32];
     pdl_trigger();
@@ -546,50 +582,82 @@ __global__ void __launch_bounds__(1024) norm_backward_wide_kernel(const NormBack
     const T* w = static_cast<const T*>(p.w);
     const float mean = p.mean[row], rstd = p.rstd[row];
     float s1 = 0.0f, s2 = 0.0f;
-    for (int64_t c = threadIdx.x; c < p.n; c += 1024) {
-        const float g = to_float(dy[c]) * (w ? to_float(w[c]) : 1.0f);
-        s1 += g;
-        s2 = fmaf(g, (to_float(x[c]) - mean) * rstd, s2);
-    }
+    // g = dy w and h of E columns; g is zero past the row's end
+    auto both_of = [&](int64_t c, int valid, float(&g)[E], float(&h)[E]) {
+        float a[E];
+        load_some(x + c, valid, h);
+        load_some(dy + c, valid, g);
+        if (w) load_some(w + c, valid, a);
+#pragma unroll
+        for (int t = 0; t < E; ++t) {
+            if (w) g[t] *= a[t];
+            h[t] = (h[t] - mean) * rstd;
+        }
+    };
+    for_columns<E>(p.n, [&](int64_t c, int valid) {
+        float g[E], h[E];
+        both_of(c, valid, g, h);
+#pragma unroll
+        for (int t = 0; t < E; ++t) {
+            s1 += g[t];
+            if (t < valid) s2 = fmaf(g[t], h[t], s2);
+        }
+    });
     const float inv = 1.0f / static_cast<float>(p.n);
     s1 = block_sum(s1, slots[0]) * inv;
     s2 = block_sum(s2, slots[1]) * inv;
     T* dx = static_cast<T*>(p.dx) + row * p.lddx;
-    const T* r = p.residual ? static_cast<const T*>(p.residual) + row * p.ldr : nullptr;
-    for (int64_t c = threadIdx.x; c < p.n; c += 1024) {
-        const float g = to_float(dy[c]) * (w ? to_float(w[c]) : 1.0f), h = (to_float(x[c]) - mean) * rstd;
-        dx[c] = from_float<T>(fmaf(rstd, g - fmaf(h, s2, s1), r ? to_float(r[c]) : 0.0f));
-    }
+    const T* residual = p.residual ? static_cast<const T*>(p.residual) + row * p.ldr : nullptr;
+    for_columns<E>(p.n, [&](int64_t c, int valid) {
+        float g[E], h[E], r[E];
+        both_of(c, valid, g, h);
+        if (residual) load_some(residual + c, valid, r);
+#pragma unroll
+        for (int t = 0; t < E; ++t) g[t] = fmaf(rstd, g[t] - fmaf(h[t], s2, s1), residual ? r[t] : 0.0f);
+        store_some(dx + c, valid, g);
+    });
 }
 
-// dw and db of 32 columns over a slab of rows, for rows of any width: warp l takes rows l,
-// l + 8, ..., and the warps' sums are added in order.
+// dw and db of 32 E columns, E to a lane, over a slab of rows, for rows of any width: warp l takes rows
+// l, l + 8, ..., and the warps' sums are added in order.
 constexpr int kSlab = 128;
-template <typename T>
+template <typename T, int E>
 __global__ void __launch_bounds__(256) norm_columns_kernel(const NormBackwardParams p) {
-    __shared__ float sums[2][8][kWarp];
+    __shared__ float sums[8][E * kWarp];
     pdl_trigger();
     pdl_wait();
     const int lane = threadIdx.x % kWarp, l = threadIdx.x / kWarp;
-    const int64_t widths = (p.n + kWarp - 1) / kWarp, slab = blockIdx.x / widths;
-    const int64_t c = (blockIdx.x - slab * widths) * kWarp + lane;
-    float dw = 0.0f, db = 0.0f;
+    const int64_t widths = (p.n + E * kWarp - 1) / (E * kWarp), slab = blockIdx.x / widths;
+    const int64_t c0 = (blockIdx.x - slab * widths) * (E * kWarp), c = c0 + E * lane;
+    const int valid = static_cast<int>(min(p.n - c, int64_t(E)));
+    float dw[E] = {}, db[E] = {};
     if (c < p.n) {
         const int64_t end = min((slab + 1) * kSlab, p.rows);
-#pragma unroll 4
+#pragma unroll(E == 8 ? 2 : 4)
         for (int64_t r = slab * kSlab + l; r < end; r += 8) {
-            const float d = to_float(static_cast<const T*>(p.dy)[r * p.lddy + c]);
-            dw = fmaf(d, (to_float(static_cast<const T*>(p.x)[r * p.ldx + c]) - p.mean[r]) * p.rstd[r], dw);
-            db += d;
+            float d[E], v[E];
+            load_some(static_cast<const T*>(p.dy) + r * p.lddy + c, valid, d);
+            load_some(static_cast<const T*>(p.x) + r * p.ldx + c, valid, v);
+            const float mean = p.mean[r], rstd = p.rstd[r];
+#pragma unroll
+            for (int t = 0; t < E; ++t) {
+                dw[t] = fmaf(d[t], (v[t] - mean) * rstd, dw[t]);
+                db[t] += d[t];
+            }
         }
     }
-    sums[0][l][lane] = dw;
-    sums[1][l][lane] = db;
-    __syncthreads();
-    if (l < 2 && c < p.n) {
-        float s = 0.0f;
-        for (int q = 0; q < 8; ++q) s += sums[l][q][lane];
-        p.part[(slab * 2 + l) * p.ldp + c] = s;
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        if (which) __syncthreads();
+#pragma unroll
+        for (int t = 0; t < E; ++t) sums[l][E * lane + t] = which ? db[t] : dw[t];
+        __syncthreads();
+        if (threadIdx.x < E * kWarp && c0 + threadIdx.x < p.n) {
+            float s = 0.0f;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) s += sums[q][threadIdx.x];
+            p.part[(slab * 2 + which) * p.ldp + c0 + threadIdx.x] = s;
+        }
     }
 }
 
@@ -742,7 +810,7 @@ cudaError_t with_shape(int g, int v, F f) {
 template <typename T>
 cudaError_t norm(NormParams p, int num_sms, cudaStream_t st) {
     if (p.n > kHeld)
-        return launch_kernel(true, norm_wide_kernel<T>, dim3(static_cast<unsigned>(p.rows)), dim3(1024), 0, st, p);
+        return launch_kernel(true, p.vec ? norm_wide_kernel<T, 8> : norm_wide_kernel<T, 1>, dim3(static_cast<unsigned>(p.rows)), dim3(1024), 0, st, p);
     const int access = widest<T>(p.n, {{p.x, p.ldx}, {p.y, p.ldy}, {p.w, 0}, {p.b, 0}});
     const Shape s = shape_of<T>(p.rows, p.n, most_vectors(access, 8 / static_cast<int>(sizeof(T))), kForwardThreads / 256,
                                 kForwardThreads / kMostThreads, num_sms);
@@ -772,9 +840,11 @@ cudaError_t backward(const NormBackwardParams& p, T* dw, T* db, int num_sms, cud
     } else if (p.rows > 0) {
         blocks = cdiv(p.rows, kSlab);
         if (p.dx)
-            e = launch_kernel(true, norm_backward_wide_kernel<T>, dim3(static_cast<unsigned>(p.rows)), dim3(1024), 0, st, p);
+            e = launch_kernel(true, p.vec ? norm_backward_wide_kernel<T, 8> : norm_backward_wide_kernel<T, 1>,
+                              dim3(static_cast<unsigned>(p.rows)), dim3(1024), 0, st, p);
         if (sums && e == cudaSuccess)
-            e = launch_kernel(true, norm_columns_kernel<T>, dim3(static_cast<unsigned>(blocks * cdiv(p.n, kWarp))),
+            e = launch_kernel(true, p.vec ? norm_columns_kernel<T, 8> : norm_columns_kernel<T, 1>,
+                              dim3(static_cast<unsigned>(blocks * cdiv(p.n, (p.vec ? 8 : 1) * kWarp))),
                               dim3(256), 0, st, p);
     }
     if (sums && e == cudaSuccess)
@@ -785,9 +855,17 @@ cudaError_t backward(const NormBackwardParams& p, T* dw, T* db, int num_sms, cud
 
 }  // namespace
 
+// Rows and vectors at 16-byte boundaries.
+static bool all_aligned(int dtype, std::initializer_list<std::pair<const void*, int64_t>> rows) {
+    for (const auto& r : rows)
+        if (!(dtype == SGEMM_F32 ? rows_aligned<float>(r.first, r.second) : rows_aligned<bf16>(r.first, r.second))) return false;
+    return true;
+}
+
 cudaError_t launch_norm(int dtype, int64_t rows, int64_t n, const void* x, int64_t ldx, const void* w, const void* b,
                         float eps, void* y, int64_t ldy, float* mean, float* rstd, int num_sms, cudaStream_t st) {
-    const NormParams p{rows, n, x, ldx, w, b, eps, y, ldy, mean, rstd, 1, false};
+    const NormParams p{rows, n,    x,    ldx, w,     b, eps, y, ldy,
+                       mean, rstd, 1,    false, all_aligned(dtype, {{x, ldx}, {y, ldy}, {w, 0}, {b, 0}})};
     return dtype == SGEMM_F32 ? norm<float>(p, num_sms, st) : norm<bf16>(p, num_sms, st);
 }
 
@@ -808,7 +886,8 @@ cudaError_t launch_norm_backward(int dtype, int64_t rows, int64_t n, const void*
                                  const void* residual, int64_t ldr, void* dx, int64_t lddx, void* dw, void* db,
                                  float* part, int num_sms, cudaStream_t st) {
     const NormBackwardParams p{rows, n,        dy,  lddy, x,    ldx,                        w, mean,
-                               rstd, residual, ldr, dx,   lddx, dw || db ? part : nullptr, cdiv(n, 4) * 4, 1};
+                               rstd, residual, ldr, dx,   lddx, dw || db ? part : nullptr, cdiv(n, 4) * 4, 1,
+                               all_aligned(dtype, {{dy, lddy}, {x, ldx}, {w, 0}, {residual, ldr}, {dx, lddx}})};
     return dtype == SGEMM_F32
                ? backward<float>(p, static_cast<float*>(dw), static_cast<float*>(db), num_sms, st)
                : backward<bf16>(p, static_cast<bf16*>(dw), static_cast<bf16*>(db), num_sms, st);

@@ -53,14 +53,15 @@ EXPORTS = ("sgemm", "sgemm_host", "sgemm_host_async", "sgemm_set_host_split", "s
            "sgemm_set_wait_timeout", "sgemm_force_plan", "sgemm_debug_flags", "sgemm_launch_count",
            "sgemm_workspace_release", "sgemm_last_error_string", "sgemm_version",
            "sgemm_linear", "sgemm_linear_backward", "sgemm_gated_linear", "sgemm_gated_linear_backward",
-           "sgemm_quantize", "sgemm_block_linear", "sgemm_layer_norm", "sgemm_layer_norm_backward", "sgemm_route", "sgemm_route_backward", "sgemm_expert_plan",
+           "sgemm_quantize", "sgemm_block_linear", "sgemm_layer_norm", "sgemm_layer_norm_backward",
+           "sgemm_route", "sgemm_route_backward", "sgemm_expert_plan",
            "sgemm_expert_linear", "sgemm_expert_linear_backward", "sgemm_expert_combine",
            "sgemm_expert_combine_backward")
 
 # Layers of language models (layers.py), loaded with torch on first use.
-_LAYERS = ("linear", "linear_backward", "gated_linear", "gated_linear_backward", "quantize",
-           "block_linear", "layer_norm", "layer_norm_backward", "route", "route_backward", "ExpertPlan", "expert_plan", "expert_linear",
-           "expert_linear_backward", "expert_combine", "expert_combine_backward")
+_LAYERS = ("linear", "linear_backward", "gated_linear", "gated_linear_backward", "quantize", "block_linear",
+           "layer_norm", "layer_norm_backward", "route", "route_backward", "ExpertPlan", "expert_plan",
+           "expert_linear", "expert_linear_backward", "expert_combine", "expert_combine_backward")
 
 
 def __getattr__(name):

@@ -104,16 +104,37 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(int64_t rows, int64_
             load8(from + c, false, there && c < cols ? static_cast<int>(min(cols - c, int64_t(8))) : 0, v[k]);
         }
     }
+    // The blocks' largest values: halves of the lanes go on with halves of the blocks, so that a lane ends with one
+    // block's (its lanes / SHARE) and forms that block's divisor alone.
+    constexpr int SHARE = 16 / R;
+    float m[R];
+#pragma unroll
+    for (int k = 0; k < R; ++k) m[k] = largest8(v[k]);
+    int live = R;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) {
+        if (live > 1) {
+            live /= 2;
+            const bool upper = lane & o;
+#pragma unroll
+            for (int k = 0; k < R / 2; ++k) {
+                if (k >= live) break;
+                const float keep = upper ? m[k + live] : m[k], send = upper ? m[k] : m[k + live];
+                m[k] = max_nan(keep, __shfl_xor_sync(0xffffffffu, send, o));
+            }
+        } else {
+            m[0] = max_nan(m[0], __shfl_xor_sync(0xffffffffu, m[0], o));
+        }
+    }
+    const Divisor mine = divisor(block_scale(m[0]));
+    const uint32_t block = first + lane / SHARE;
+    if (there && lane % SHARE == 0 && block < blocks) scales[r * s_row + block * s_block] = mine.scale;
 #pragma unroll
     for (int k = 0; k < R; ++k) {
-        float m = largest8(v[k]);
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const float scale = block_scale(m);
+        const float scale = __shfl_sync(0xffffffffu, mine.scale, k * SHARE, 16), inverse = __shfl_sync(0xffffffffu, mine.r, k * SHARE, 16);
         const int64_t c = c0 + k * kBlock;
-        const uint2 w = round8(v[k], divisor(scale));
+        const uint2 w = round8(v[k], Divisor{scale, inverse, plain(scale)});
         if (there && c < cols) put8(q + r * ldq + c, VEC, VEC ? 8 : static_cast<int>(min(cols - c, int64_t(8))), w);
-        if (there && lane == 0 && first + k < blocks) scales[r * s_row + (first + k) * s_block] = scale;
     }
 }
 
@@ -184,7 +205,9 @@ struct Cfg {
     static constexpr int OUT_BYTES = kEpiWarps * 32 * kOutBytes;
     static constexpr int SCALE_BYTES = kScaleSlots * 2 * kRows * kScales * 4;  // of the rows, for each half of the columns
     static constexpr int BIAS_BYTES = kBiasSlots * BN * 4;
-    static constexpr size_t SMEM = 1024 + static_cast<size_t>(STAGES) * STAGE_BYTES + OUT_BYTES + SCALE_BYTES + BIAS_BYTES + BAR_BYTES;
+    static constexpr size_t SMEM =
+        1024 + static_cast<size_t>(STAGES) * STAGE_BYTES + OUT_BYTES + SCALE_BYTES + BIAS_BYTES + BAR_BYTES;
+    static_assert(kEpiWarps * MINE * 4 <= SCALE_BYTES, "a bias for each warp");
     static_assert(A_BYTES % 1024 == 0 && HALF_BYTES % 1024 == 0, "slots need 1 KiB alignment");
 };
 
@@ -595,9 +618,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     tmem_st_32x32b_x32(at + kCols * c, v);
                 }
                 tmem_wait_st();
-                float* const bias = biases + bias_slot * BN + C::MINE * half;
-                if (x.nkb == 0 && p.bias)  // no scales came, and no bias with them
-                    for (int c = lane; c < C::MINE && i0 + c < p.n; c += 32) bias[c] = to_float(static_cast<const T*>(p.bias)[i0 + c]);
+                // (without blocks of k no scales came, and no bias with them: their place is free)
+                float* const bias = x.nkb > 0 ? biases + bias_slot * BN + C::MINE * half
+                                              : reinterpret_cast<float*>(scale_ring) + C::MINE * (warp - 4);
+                if (x.nkb == 0 && p.bias)
+                    for (int c = lane; c < C::MINE && i0 + c < p.n; c += 32)
+                        bias[c] = to_float(static_cast<const T*>(p.bias)[i0 + c]);
                 __syncwarp();
                 // The columns as elements TO, 64 bytes of 32 rows at a time.  They change places in shared memory
                 // (16-byte words, swizzled so that eight rows' words fall on all banks), so that four lanes write

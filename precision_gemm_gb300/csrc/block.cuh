@@ -33,9 +33,8 @@ struct Divisor {
     float scale, r;
     bool plain;
 };
-__device__ __forceinline__ Divisor divisor(float scale) {
-    return {scale, 1.0f / scale, scale > 8.6736174e-19f && scale < 1.1529215e18f};  // 2^-60, 2^60
-}
+__device__ __forceinline__ bool plain(float scale) { return scale > 8.6736174e-19f && scale < 1.1529215e18f; }  // 2^-60, 2^60
+__device__ __forceinline__ Divisor divisor(float scale) { return {scale, 1.0f / scale, plain(scale)}; }
 __device__ __forceinline__ uint2 round8(const float (&v)[8], const Divisor& d) {
     float2 f[4];
 #pragma unroll

@@ -156,7 +156,7 @@ template <int ACT, bool FAST>
 __device__ __forceinline__ float2 act_value2(float2 z) {
     if (FAST && (ACT == SGEMM_ACT_SILU || ACT == SGEMM_ACT_GELU_TANH)) {
         const float2 w = ACT == SGEMM_ACT_SILU ? z
-                                               : mul2(both(1.59576912160573072f), fma2(mul2(mul2(both(0.044715f), z), z), z, z));
+                                               : mul2(both(1.595769122f), fma2(mul2(mul2(both(0.044715f), z), z), z, z));
         const float2 u = mul2(both(-1.44269504f), w);
         const float2 v = add2(make_float2(exp2_approx(u.x), exp2_approx(u.y)), both(1.0f));
         return mul2(z, make_float2(reciprocal_approx(v.x), reciprocal_approx(v.y)));

@@ -324,6 +324,29 @@ def test_block_empty_extents_and_leading_dimensions(dtype):
     assert torch.equal(y, pg.block_linear(xq, w, s, x_scales=xs, dtype=dtype))
 
 
+@pytest.mark.parametrize("k", [0, 16, 130, 700])
+def test_block_bias_of_many_tiles(k):
+    """Several tiles to a thread block one after another, few or no blocks of k in each: every tile
+    gets its own columns' bias."""
+    t, n, dtype = 700, 9000, torch.bfloat16
+    g = _gen(k)
+    x, b, r = _draw(g, dtype, t, k), _draw(g, dtype, n), _draw(g, dtype, t, n)
+    if k:
+        w, s = _weights(g, n, k)
+    else:
+        w, s = pg.quantize(torch.empty(n, 0, device="cuda"), 128)
+    pg.force_plan(64, 1)
+    try:
+        y = pg.block_linear(x.cuda(), w, s, b.cuda(), "relu", r.cuda())
+    finally:
+        pg.force_plan()
+    if k:
+        want, _, den = R.linear(values(*quantized(x, 1), 1), values(w.cpu(), s.cpu(), 128), b, "relu", r)
+    else:
+        want, _, den = R.linear(torch.zeros(t, 0), torch.zeros(n, 0), b, "relu", r)
+    R.close(y, want, den, dtype)
+
+
 def test_block_repeats_bitwise_on_streams_and_in_graphs():
     g = _gen(4)
     x = _draw(g, torch.bfloat16, 300, 1000).cuda()

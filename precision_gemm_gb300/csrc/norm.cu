@@ -18,8 +18,7 @@
 // each of the passes.
 //
 // Measured (L2 cold), forward and backward without residual: 16384 x 2048 float32 48 and 69 us (5.6 and
-// 5.8 TB/s), 16384 x 4096 bfloat16 65 and 84 us (4.1 and 4.8 TB/s: 15 instructions per 32 elements hold the
-// forward pass up), 512 x 4096 bfloat16 7 and 14 us, 1 x 4096 4 and 6 us.
+// 5.8 TB/s), 16384 x 4096 bfloat16 53 and 84 us (5.1 and 4.8 TB/s), 512 x 4096 bfloat16 7 and 14 us, 1 x 4096 4 and 6 us.
 #include <algorithm>
 #include <initializer_list>
 #include <utility>
@@ -75,31 +74,32 @@ struct Word<8> { using type = uint2; };
 template <>
 struct Word<16> { using type = uint4; };
 
-// Vector j of a row at p, zeros past n (a multiple of G).
-template <typename T, int G>
+// Vector j of a row at p, zeros past n (a multiple of G).  FULL: the team's threads have n columns, and
+// nothing is tested.
+template <typename T, int G, bool FULL = false>
 __device__ __forceinline__ void fetch(const T* p, int n, int tid, int team, int j, Raw<T>& v) {
     using W = typename Word<G * sizeof(T)>::type;
     W* to = reinterpret_cast<W*>(v.q);
 #pragma unroll
     for (int a = 0; a < 8 / G; ++a) {
         const int c = column<G>(tid, team, j, G * a);
-        to[a] = c < n ? *reinterpret_cast<const W*>(p + c) : W{};
+        to[a] = FULL || c < n ? *reinterpret_cast<const W*>(p + c) : W{};
     }
 }
-template <typename T, int G>
+template <typename T, int G, bool FULL = false>
 __device__ __forceinline__ void put(T* p, int n, int tid, int team, int j, const Raw<T>& raw) {
     using W = typename Word<G * sizeof(T)>::type;
 #pragma unroll
     for (int a = 0; a < 8 / G; ++a) {
         const int c = column<G>(tid, team, j, G * a);
-        if (c < n) *reinterpret_cast<W*>(p + c) = reinterpret_cast<const W*>(raw.q)[a];
+        if (FULL || c < n) *reinterpret_cast<W*>(p + c) = reinterpret_cast<const W*>(raw.q)[a];
     }
 }
 
 // A thread's places in shared memory: S stages of A arrays of V vectors, each access beside the
 // neighbouring threads'.  Single bfloat16 elements are too small to be copied asynchronously; such
 // rows are loaded where they are used.
-template <typename T, int G, int V, int A, int S, int NT>
+template <typename T, int G, int V, int A, int S, int NT, bool FULL = false>
 struct Stages {
     static constexpr bool ASYNC = G * sizeof(T) >= 4;
     static constexpr int BYTES = G * static_cast<int>(sizeof(T)), ACCESSES = 8 / G;
@@ -108,7 +108,7 @@ struct Stages {
     uint8_t* base;  // this thread's
     __device__ __forceinline__ explicit Stages(uint8_t* memory, int n, int tid, int team)
         : base(memory + BYTES * threadIdx.x) {
-        if constexpr (BYTES == 16) {  // what lies past the rows' end is zero, and no copy goes there
+        if constexpr (BYTES == 16 && !FULL) {  // what lies past the rows' end is zero, and no copy goes there
             using W = typename Word<BYTES>::type;
 #pragma unroll
             for (int k = 0; k < V * ACCESSES; ++k)
@@ -124,7 +124,7 @@ struct Stages {
             for (int k = 0; k < V * ACCESSES; ++k) {
                 const int c = G * (tid + team * k);
                 if constexpr (BYTES == 16) {
-                    if (c < n)
+                    if (FULL || c < n)
                         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + k * (BYTES * NT)), "l"(p + c) : "memory");
                 } else {  // (a branch for each of many small copies costs more than copies of nothing)
                     asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(to + k * (BYTES * NT)),
@@ -142,7 +142,7 @@ struct Stages {
 #pragma unroll
             for (int a = 0; a < ACCESSES; ++a) reinterpret_cast<W*>(v.q)[a] = *reinterpret_cast<const W*>(from + a * (BYTES * NT));
         } else {
-            fetch<T, G>(p, n, tid, team, j, v);
+            fetch<T, G, FULL>(p, n, tid, team, j, v);
         }
     }
 };
@@ -217,15 +217,16 @@ struct NormParams {
     bool vec;        // rows too wide to be held: all in 16-byte accesses
 };
 
-// V vectors of eight per thread, S rows on their way per team.
-template <typename T, int G, int V, int S, int NT>
+// V vectors of eight per thread, S rows on their way per team.  FULL: rows fill their teams; without tests of columns
+// and their branches 16384 x 4096 bfloat16 takes 53 us instead of 64.
+template <typename T, int G, int V, int S, int NT, bool FULL>
 __global__ void __launch_bounds__(NT, kForwardThreads / NT) norm_kernel(const NormParams p) {
     __shared__ float slots[4][NT / kWarp];
     extern __shared__ __align__(16) uint8_t memory[];
     const Team whole(p.warps);
     const int team = p.warps * kWarp, tid = threadIdx.x - whole.index * team, teams = NT / team;
     const int n = static_cast<int>(p.n);
-    const Stages<T, G, V, 1, S, NT> stages(memory, n, tid, team);
+    const Stages<T, G, V, 1, S, NT, FULL> stages(memory, n, tid, team);
     pdl_trigger();
     pdl_wait();
     const int64_t step = static_cast<int64_t>(gridDim.x) * teams;
@@ -250,8 +251,8 @@ __global__ void __launch_bounds__(NT, kForwardThreads / NT) norm_kernel(const No
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         Raw<T> wj, bj;
-        if (w) fetch<T, G>(w, n, tid, team, j, wj);
-        if (b) fetch<T, G>(b, n, tid, team, j, bj);
+        if (w) fetch<T, G, FULL>(w, n, tid, team, j, wj);
+        if (b) fetch<T, G, FULL>(b, n, tid, team, j, bj);
         if (KEEP) {
             kept_w[KEEP ? j : 0] = wj;
             kept_b[KEEP ? j : 0] = bj;
@@ -287,7 +288,9 @@ __global__ void __launch_bounds__(NT, kForwardThreads / NT) norm_kernel(const No
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 v[j][t] = add2(v[j][t], both(-mean));
-                if (G == 1) {
+                if (FULL) {
+                    sum = fma2(v[j][t], v[j][t], sum);
+                } else if (G == 1) {
                     if (column<G>(tid, team, j, 2 * t) < n) sum.x = fmaf(v[j][t].x, v[j][t].x, sum.x);
                     if (column<G>(tid, team, j, 2 * t + 1) < n) sum.y = fmaf(v[j][t].y, v[j][t].y, sum.y);
                 } else if (column<G>(tid, team, j, 2 * t / G * G) < n) {
@@ -310,8 +313,8 @@ __global__ void __launch_bounds__(NT, kForwardThreads / NT) norm_kernel(const No
                     wj = kept_w[KEEP ? j : 0];
                     bj = kept_b[KEEP ? j : 0];
                 } else if (!p.shared_wb) {
-                    if (W) fetch<T, G>(w, n, tid, team, j, wj);
-                    if (B) fetch<T, G>(b, n, tid, team, j, bj);
+                    if (W) fetch<T, G, FULL>(w, n, tid, team, j, wj);
+                    if (B) fetch<T, G, FULL>(b, n, tid, team, j, bj);
                 } else {
 #pragma unroll
                     for (int a = 0; a < 8 / G; ++a) {
@@ -325,7 +328,7 @@ __global__ void __launch_bounds__(NT, kForwardThreads / NT) norm_kernel(const No
                     o.set(t, W && B ? fma2(h, wj.pair(t), bj.pair(t))
                                     : (W ? mul2(h, wj.pair(t)) : (B ? add2(h, bj.pair(t)) : h)));
                 }
-                put<T, G>(y, n, tid, team, j, o);
+                put<T, G, FULL>(y, n, tid, team, j, o);
             }
         };
         if (w && b)
@@ -763,14 +766,17 @@ cudaError_t launch_rows(F kern, std::atomic<uint64_t>& done, size_t shared, cons
 // two of each of the backward pass's three matrices; more of less, and of twice as much one row.
 template <typename T, int G, int V, int S, int NT>
 cudaError_t run_norm(NormParams p, Shape s, int num_sms, cudaStream_t st) {
-    static std::atomic<uint64_t> done{0};
+    static std::atomic<uint64_t> done[2];
     constexpr int VECTOR = 8 * V * static_cast<int>(sizeof(T));  // bytes of a thread
     s.teams = NT / (s.warps * kWarp);
     s.blocks = std::min<int64_t>(cdiv(p.rows, s.teams), static_cast<int64_t>(kForwardThreads / NT) * num_sms);
     p.shared_wb = VECTOR > 32 && s.teams > 1;
-    auto kern = norm_kernel<T, G, V, S, NT>;
+    auto kern = norm_kernel<T, G, V, S, NT, false>;
+    const bool full = G * sizeof(T) == 16 && p.n == static_cast<int64_t>(8 * V * kWarp) * s.warps;
+    if constexpr (G * sizeof(T) == 16)
+        if (full) kern = norm_kernel<T, G, V, S, NT, true>;
     const size_t most = Stages<T, G, V, 1, S, NT>::SHARED + (VECTOR > 32 ? VECTOR * NT : 0);
-    const cudaError_t e = set_smem_limit_once(done, reinterpret_cast<const void*>(kern), static_cast<int>(most));
+    const cudaError_t e = set_smem_limit_once(done[full], reinterpret_cast<const void*>(kern), static_cast<int>(most));
     if (e != cudaSuccess) return e;
     const size_t smem = Stages<T, G, V, 1, S, NT>::SHARED + (p.shared_wb ? 2 * VECTOR * (s.warps * kWarp) : 0);
     return launch_kernel(true, kern, dim3(static_cast<unsigned>(s.blocks)), dim3(NT), smem, st, p);

@@ -426,7 +426,7 @@ struct NormBackwardParams {
     bool vec;     // as in NormParams
 };
 
-template <typename T, int G, int V, int S, int NT, int B>
+template <typename T, int G, int V, int S, int NT, int B, bool FULL>
 __global__ void __launch_bounds__(NT, B)
     norm_backward_kernel(const NormBackwardParams p) {
     __shared__ float2 slots[2][NT / kWarp];
@@ -434,7 +434,7 @@ __global__ void __launch_bounds__(NT, B)
     const Team whole(p.warps);
     const int team = p.warps * kWarp, tid = threadIdx.x - whole.index * team, teams = NT / team;
     const int n = static_cast<int>(p.n);
-    const Stages<T, G, V, 3, S, NT> stages(memory, n, tid, team);
+    const Stages<T, G, V, 3, S, NT, FULL> stages(memory, n, tid, team);
     pdl_trigger();
     pdl_wait();
     const int64_t step = static_cast<int64_t>(gridDim.x) * teams;
@@ -455,7 +455,7 @@ __global__ void __launch_bounds__(NT, B)
     float2 kept[KEEP ? V : 1][4], dw[V][4] = {}, db[V][4] = {};
     auto weights = [&](int j, float2(&w)[4]) {
         Raw<T> raw;
-        if (p.w) fetch<T, G>(static_cast<const T*>(p.w), n, tid, team, j, raw);
+        if (p.w) fetch<T, G, FULL>(static_cast<const T*>(p.w), n, tid, team, j, raw);
 #pragma unroll
         for (int t = 0; t < 4; ++t) w[t] = p.w ? raw.pair(t) : both(1.0f);
     };
@@ -528,7 +528,7 @@ __global__ void __launch_bounds__(NT, B)
                         o.set(t, add2(y, r.pair(t)));
                     }
                 });
-                put<T, G>(dx, n, tid, team, j, o);
+                put<T, G, FULL>(dx, n, tid, team, j, o);
             }
         }
         stage = stage + 1 == S ? 0 : stage + 1;
@@ -551,7 +551,7 @@ __global__ void __launch_bounds__(NT, B)
             for (int q = threadIdx.x; q < 8 * V * team; q += blockDim.x) {
                 const int jt = q / team;
                 const int c = column<G>(q % team, team, jt / 8, jt % 8);
-                if (c >= n) continue;
+                if (!FULL && c >= n) continue;
                 float s = 0.0f;
                 for (int k = 0; k < teams; ++k) s += sums[k * (8 * V) * team + q];
                 out[c] = s;
@@ -562,7 +562,7 @@ __global__ void __launch_bounds__(NT, B)
 #pragma unroll
                 for (int t = 0; t < 8; t += G == 1 ? 1 : 4) {
                     const int c = column<G>(tid, team, j, t);
-                    if (c >= n) continue;
+                    if (!FULL && c >= n) continue;
                     if constexpr (G == 1)
                         out[c] = value(j, t);
                     else
@@ -789,19 +789,28 @@ cudaError_t run_norm(const NormParams& p, const Shape& s, int num_sms, cudaStrea
     return s.threads > 256 ? run_norm<T, G, V, S, kMostThreads>(p, s, num_sms, st)
                            : run_norm<T, G, V, S, SMALL>(p, s, num_sms, st);
 }
-template <typename T, int G, int V>
+template <typename T, int G, int V, bool FULL>
 cudaError_t run_backward(const NormBackwardParams& p, const Shape& s, cudaStream_t st) {
     constexpr int BYTES = 8 * V * static_cast<int>(sizeof(T)), S = BYTES > 64 ? 1 : 128 / BYTES;
     if (s.threads > 256) {
         static std::atomic<uint64_t> done{0};
-        return launch_rows(norm_backward_kernel<T, G, V, S, kMostThreads, 1>, done, Stages<T, G, V, 3, S, kMostThreads>::SHARED,
-                           p, s, st);
+        return launch_rows(norm_backward_kernel<T, G, V, S, kMostThreads, 1, FULL>, done,
+                           Stages<T, G, V, 3, S, kMostThreads>::SHARED, p, s, st);
     }
     constexpr int B = kBackwardBlocks;
     static std::atomic<uint64_t> done{0};
     // the teams' sums use the same memory
-    return launch_rows(norm_backward_kernel<T, G, V, S, 256, B>, done,
+    return launch_rows(norm_backward_kernel<T, G, V, S, 256, B, FULL>, done,
                        std::max(Stages<T, G, V, 3, S, 256>::SHARED, static_cast<size_t>(256) * 8 * V * 4), p, s, st);
+}
+// Without tests of columns where 32 columns per thread fill their teams: 4096 x 16384 with residual 116 us instead of
+// 130 (bfloat16), 211 instead of 233 (float32).  Fewer columns per thread run better with the tests (16384 x 4096
+// bfloat16 92 us, 116 without), whose branches keep the loads of a row's parts apart.
+template <typename T, int G, int V>
+cudaError_t run_backward(const NormBackwardParams& p, const Shape& s, cudaStream_t st) {
+    if constexpr (G * sizeof(T) == 16 && V == 4)
+        if (p.n == static_cast<int64_t>(8 * V * kWarp) * s.warps) return run_backward<T, G, V, true>(p, s, st);
+    return run_backward<T, G, V, false>(p, s, st);
 }
 // f(widest access, vectors per thread) as constants
 template <typename T, typename F>

@@ -158,11 +158,23 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// A team of `warps` warps (a power of two, 16 at most) of a block.
+// A team of `warps` warps (a power of two, 16 at most) of a block, or of 8 or 16 lanes of a warp (PARTS, whose
+// kernels alone pay for it).
+template <bool PARTS>
 struct Team {
-    int warps, index, warp, lane;
-    __device__ __forceinline__ explicit Team(int w)
-        : warps(w), index(threadIdx.x / (w * kWarp)), warp(threadIdx.x / kWarp), lane(threadIdx.x % kWarp) {}
+    int warps, threads, index, warp, lane;
+    __device__ __forceinline__ Team(int w, int lanes)
+        : warps(w), threads(PARTS ? lanes : w * kWarp), index(threadIdx.x / threads), warp(threadIdx.x / kWarp),
+          lane(threadIdx.x % kWarp) {}
+    // how far this team's row lies ahead of that of its warp's first team, which decides for the warp
+    __device__ __forceinline__ int ahead() const { return PARTS ? lane / threads : 0; }
+    __device__ __forceinline__ float part_sum(float v) const {  // over up to a warp
+        if (threads > 16) v += __shfl_xor_sync(0xffffffffu, v, 16);
+        if (threads > 8) v += __shfl_xor_sync(0xffffffffu, v, 8);
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        return v;
+    }
     // a barrier of its threads alone (at most eight teams have several warps; barrier 0 is the block's)
     __device__ __forceinline__ void barrier() const {
         asm volatile("bar.sync %0, %1;" ::"r"(1 + index), "r"(warps * kWarp) : "memory");
@@ -170,6 +182,7 @@ struct Team {
     // The sum of v over the team, the same in each thread; `slots` holds a place for each warp of the block
     // and is free again after the team's next barrier.
     __device__ __forceinline__ float sum(float v, float* slots) const {
+        if (PARTS) return part_sum(v);
         v = warp_sum(v);
         if (warps == 1) return v;
         if (lane == 0) slots[warp] = v;
@@ -180,6 +193,7 @@ struct Team {
     }
     // Two sums at once, one in each half of a warp.
     __device__ __forceinline__ float2 sum2(float2 v, float2* slots) const {
+        if (PARTS) return make_float2(part_sum(v.x), part_sum(v.y));
         const bool upper = lane >= 16;
         float s = (upper ? v.y : v.x) + __shfl_xor_sync(0xffffffffu, upper ? v.x : v.y, 16);
 #pragma unroll
@@ -212,19 +226,19 @@ struct NormParams {
     void* y;
     int64_t ldy;
     float *mean, *rstd;
-    int warps;       // of a team
+    int warps, lanes;  // of a team: lanes where they are no warp
     bool shared_wb;  // w and b have places in shared memory
     bool vec;        // rows too wide to be held: all in 16-byte accesses
 };
 
 // V vectors of eight per thread, S rows on their way per team.  FULL: rows fill their teams; without tests of columns
 // and their branches 16384 x 4096 bfloat16 takes 53 us instead of 64.
-template <typename T, int G, int V, int S, int NT, bool FULL>
+template <typename T, int G, int V, int S, int NT, bool FULL, bool PARTS>
 __global__ void __launch_bounds__(NT, kForwardThreads / NT) norm_kernel(const NormParams p) {
     __shared__ float slots[4][NT / kWarp];
     extern __shared__ __align__(16) uint8_t memory[];
-    const Team whole(p.warps);
-    const int team = p.warps * kWarp, tid = threadIdx.x - whole.index * team, teams = NT / team;
+    const Team<PARTS> whole(p.warps, p.lanes);
+    const int team = whole.threads, tid = threadIdx.x - whole.index * team, teams = NT / team;
     const int n = static_cast<int>(p.n);
     const Stages<T, G, V, 1, S, NT, FULL> stages(memory, n, tid, team);
     pdl_trigger();
@@ -266,14 +280,15 @@ __global__ void __launch_bounds__(NT, kForwardThreads / NT) norm_kernel(const No
     }
     const float inv = 1.0f / static_cast<float>(n);
     int stage = 0, turn = 0;
-    for (; row < p.rows; row += step) {
+    for (; row - whole.ahead() < p.rows; row += step) {
+        const bool mine = !PARTS || row < p.rows;
         start(stage == 0 ? S - 1 : stage - 1, row + (S - 1) * step);
         wait_copies<S - 1>();
         float2 v[V][4], sum = both(0.0f);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             Raw<T> raw;
-            stages.read(stage, 0, static_cast<const T*>(p.x) + row * p.ldx, n, tid, team, j, raw);
+            stages.read(stage, 0, static_cast<const T*>(p.x) + (mine ? row : 0) * p.ldx, n, tid, team, j, raw);
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 v[j][t] = raw.pair(t);
@@ -299,7 +314,7 @@ __global__ void __launch_bounds__(NT, kForwardThreads / NT) norm_kernel(const No
             }
         const float rstd = 1.0f / sqrtf(whole.sum(sum.x + sum.y, slots[turn + 1]) * inv + p.eps);
         turn ^= 2;
-        if (tid == 0) {
+        if (tid == 0 && mine) {
             if (p.mean) p.mean[row] = mean;
             if (p.rstd) p.rstd[row] = rstd;
         }
@@ -331,7 +346,9 @@ __global__ void __launch_bounds__(NT, kForwardThreads / NT) norm_kernel(const No
                 put<T, G, FULL>(y, n, tid, team, j, o);
             }
         };
-        if (w && b)
+        if (!mine) {
+            // (this warp's other rows are there)
+        } else if (w && b)
             write(std::true_type(), std::true_type());
         else if (w)
             write(std::true_type(), std::false_type());
@@ -422,17 +439,17 @@ struct NormBackwardParams {
     int64_t lddx;
     float* part;  // [block][dw, db][ldp]
     int64_t ldp;  // n to a multiple of four
-    int warps;
+    int warps, lanes;  // of a team
     bool vec;     // as in NormParams
 };
 
-template <typename T, int G, int V, int S, int NT, int B, bool FULL>
+template <typename T, int G, int V, int S, int NT, int B, bool FULL, bool PARTS>
 __global__ void __launch_bounds__(NT, B)
     norm_backward_kernel(const NormBackwardParams p) {
     __shared__ float2 slots[2][NT / kWarp];
     extern __shared__ __align__(16) uint8_t memory[];
-    const Team whole(p.warps);
-    const int team = p.warps * kWarp, tid = threadIdx.x - whole.index * team, teams = NT / team;
+    const Team<PARTS> whole(p.warps, p.lanes);
+    const int team = whole.threads, tid = threadIdx.x - whole.index * team, teams = NT / team;
     const int n = static_cast<int>(p.n);
     const Stages<T, G, V, 3, S, NT, FULL> stages(memory, n, tid, team);
     pdl_trigger();
@@ -450,7 +467,7 @@ __global__ void __launch_bounds__(NT, B)
 #pragma unroll
     for (int s = 0; s + 1 < S; ++s) start(s, row + s * step);
     // w and the sums of 32 columns of a thread do not fit in its registers: bfloat16 w then comes from L1 and L2
-    // (4096 rows of 16384: 137 -> 118 us; float32, with a single row on its way, 205 -> 239)
+    // (4096 rows of 16384: 137 -> 118 us; float32, with a single row on its way, 160 -> 168)
     constexpr bool KEEP = V < 4 || sizeof(T) == 4;
     float2 kept[KEEP ? V : 1][4], dw[V][4] = {}, db[V][4] = {};
     auto weights = [&](int j, float2(&w)[4]) {
@@ -480,18 +497,21 @@ __global__ void __launch_bounds__(NT, B)
     statistics(row);
     const float inv = 1.0f / static_cast<float>(n);
     int stage = 0, turn = 0;
-    for (; row < p.rows; row += step) {
+    for (; row - whole.ahead() < p.rows; row += step) {
+        const bool mine = !PARTS || row < p.rows;
+        const int64_t at = mine ? row : 0;
         start(stage == 0 ? S - 1 : stage - 1, row + (S - 1) * step);
         const float mean = next_mean, rstd = next_rstd;
         statistics(row + step);
         wait_copies<S - 1>();
         auto read = [&](int j, Raw<T>& x, Raw<T>& dy) {
-            stages.read(stage, 0, static_cast<const T*>(p.x) + row * p.ldx, n, tid, team, j, x);
-            stages.read(stage, 1, static_cast<const T*>(p.dy) + row * p.lddy, n, tid, team, j, dy);
+            stages.read(stage, 0, static_cast<const T*>(p.x) + at * p.ldx, n, tid, team, j, x);
+            stages.read(stage, 1, static_cast<const T*>(p.dy) + at * p.lddy, n, tid, team, j, dy);
         };
         float2 s1 = both(0.0f), s2 = both(0.0f);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
+            if (!mine) break;
             Raw<T> x, dy;
             read(j, x, dy);
             with_weights(j, [&](float2(&w)[4]) {
@@ -515,10 +535,11 @@ __global__ void __launch_bounds__(NT, B)
             T* dx = static_cast<T*>(p.dx) + row * p.lddx;
 #pragma unroll
             for (int j = 0; j < V; ++j) {
+                if (!mine) break;
                 Raw<T> x, dy, r{};
                 read(j, x, dy);
                 if (p.residual)
-                    stages.read(stage, 2, static_cast<const T*>(p.residual) + row * p.ldr, n, tid, team, j, r);
+                    stages.read(stage, 2, static_cast<const T*>(p.residual) + at * p.ldr, n, tid, team, j, r);
                 Raw<T> o;
                 with_weights(j, [&](float2(&w)[4]) {
 #pragma unroll
@@ -702,18 +723,19 @@ __global__ void __launch_bounds__(256) norm_sum_kernel(int64_t n, int64_t blocks
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Warps that hold a row of n with v vectors per thread: a power of two.
-int team_warps(int64_t n, int v) {
-    int w = 1;
-    while (static_cast<int64_t>(w) * kWarp * 8 * v < n) w *= 2;
-    return w;
+// Threads that hold a row of n with v vectors per thread: a power of two, whole warps or, for rows of at most
+// 128, 8 or 16 lanes (65536 rows of 64 bfloat16: 6.4 us, 16 by a warp each; backwards 14.5 and 27).
+int team_threads(int64_t n, int v) {
+    int t = 8;
+    while (static_cast<int64_t>(t) * 8 * v < n) t *= 2;
+    return v > 1 && t < kWarp ? kWarp : t;
 }
 
 // Rows are held by teams: 64 bytes per thread, less where one warp then holds the row, twice as much
 // where 512 threads hold it no other way.
 constexpr int64_t kHeld = 16384;
 struct Shape {
-    int v, threads, warps, teams;
+    int v, threads, team, teams;
     int64_t blocks;
 };
 template <typename T>
@@ -722,9 +744,9 @@ Shape shape_of(int64_t rows, int64_t n, int most_v, int small_blocks, int large_
     s.v = 1;
     while (s.v < most_v && s.v * kWarp * 8 < n) s.v *= 2;
     while (s.v * kMostThreads * 8 < n) s.v *= 2;
-    s.warps = team_warps(n, s.v);
-    s.threads = std::max(s.warps * kWarp, 256);
-    s.teams = s.threads / (s.warps * kWarp);
+    s.team = team_threads(n, s.v);
+    s.threads = std::max(s.team, 256);
+    s.teams = s.threads / s.team;
     s.blocks = std::min<int64_t>(cdiv(rows, s.teams), static_cast<int64_t>(s.threads > 256 ? large_blocks : small_blocks) * num_sms);
     return s;
 }
@@ -766,19 +788,22 @@ cudaError_t launch_rows(F kern, std::atomic<uint64_t>& done, size_t shared, cons
 // two of each of the backward pass's three matrices; more of less, and of twice as much one row.
 template <typename T, int G, int V, int S, int NT>
 cudaError_t run_norm(NormParams p, Shape s, int num_sms, cudaStream_t st) {
-    static std::atomic<uint64_t> done[2];
+    static std::atomic<uint64_t> done[3];
     constexpr int VECTOR = 8 * V * static_cast<int>(sizeof(T));  // bytes of a thread
-    s.teams = NT / (s.warps * kWarp);
+    s.teams = NT / s.team;
     s.blocks = std::min<int64_t>(cdiv(p.rows, s.teams), static_cast<int64_t>(kForwardThreads / NT) * num_sms);
     p.shared_wb = VECTOR > 32 && s.teams > 1;
-    auto kern = norm_kernel<T, G, V, S, NT, false>;
-    const bool full = G * sizeof(T) == 16 && p.n == static_cast<int64_t>(8 * V * kWarp) * s.warps;
+    auto kern = norm_kernel<T, G, V, S, NT, false, false>;
+    const bool parts = s.team < kWarp, full = !parts && G * sizeof(T) == 16 && p.n == static_cast<int64_t>(8 * V) * s.team;
     if constexpr (G * sizeof(T) == 16)
-        if (full) kern = norm_kernel<T, G, V, S, NT, true>;
+        if (full) kern = norm_kernel<T, G, V, S, NT, true, false>;
+    if constexpr (V == 1 && NT == 256)
+        if (parts) kern = norm_kernel<T, G, V, S, NT, false, true>;
     const size_t most = Stages<T, G, V, 1, S, NT>::SHARED + (VECTOR > 32 ? VECTOR * NT : 0);
-    const cudaError_t e = set_smem_limit_once(done[full], reinterpret_cast<const void*>(kern), static_cast<int>(most));
+    const cudaError_t e =
+        set_smem_limit_once(done[parts ? 2 : full], reinterpret_cast<const void*>(kern), static_cast<int>(most));
     if (e != cudaSuccess) return e;
-    const size_t smem = Stages<T, G, V, 1, S, NT>::SHARED + (p.shared_wb ? 2 * VECTOR * (s.warps * kWarp) : 0);
+    const size_t smem = Stages<T, G, V, 1, S, NT>::SHARED + (p.shared_wb ? 2 * VECTOR * s.team : 0);
     return launch_kernel(true, kern, dim3(static_cast<unsigned>(s.blocks)), dim3(NT), smem, st, p);
 }
 // 64 bytes per thread: blocks of 512, so that more teams share w and b.
@@ -789,28 +814,31 @@ cudaError_t run_norm(const NormParams& p, const Shape& s, int num_sms, cudaStrea
     return s.threads > 256 ? run_norm<T, G, V, S, kMostThreads>(p, s, num_sms, st)
                            : run_norm<T, G, V, S, SMALL>(p, s, num_sms, st);
 }
-template <typename T, int G, int V, bool FULL>
+template <typename T, int G, int V, bool FULL, bool PARTS>
 cudaError_t run_backward(const NormBackwardParams& p, const Shape& s, cudaStream_t st) {
     constexpr int BYTES = 8 * V * static_cast<int>(sizeof(T)), S = BYTES > 64 ? 1 : 128 / BYTES;
-    if (s.threads > 256) {
-        static std::atomic<uint64_t> done{0};
-        return launch_rows(norm_backward_kernel<T, G, V, S, kMostThreads, 1, FULL>, done,
-                           Stages<T, G, V, 3, S, kMostThreads>::SHARED, p, s, st);
-    }
+    if constexpr (!PARTS)
+        if (s.threads > 256) {
+            static std::atomic<uint64_t> done{0};
+            return launch_rows(norm_backward_kernel<T, G, V, S, kMostThreads, 1, FULL, false>, done,
+                               Stages<T, G, V, 3, S, kMostThreads>::SHARED, p, s, st);
+        }
     constexpr int B = kBackwardBlocks;
     static std::atomic<uint64_t> done{0};
     // the teams' sums use the same memory
-    return launch_rows(norm_backward_kernel<T, G, V, S, 256, B, FULL>, done,
+    return launch_rows(norm_backward_kernel<T, G, V, S, 256, B, FULL, PARTS>, done,
                        std::max(Stages<T, G, V, 3, S, 256>::SHARED, static_cast<size_t>(256) * 8 * V * 4), p, s, st);
 }
-// Without tests of columns where 32 columns per thread fill their teams: 4096 x 16384 with residual 116 us instead of
-// 130 (bfloat16), 211 instead of 233 (float32).  Fewer columns per thread run better with the tests (16384 x 4096
-// bfloat16 92 us, 116 without), whose branches keep the loads of a row's parts apart.
+// Without tests of columns where 32 columns per thread fill their teams: 4096 x 16384 with residual 128 us instead of
+// 174 (bfloat16), 194 instead of 233 (float32).  Fewer columns per thread run better with the tests (16384 x 4096 bfloat16
+// 92 us, 116 without), whose branches keep the loads of a row's parts apart.
 template <typename T, int G, int V>
 cudaError_t run_backward(const NormBackwardParams& p, const Shape& s, cudaStream_t st) {
     if constexpr (G * sizeof(T) == 16 && V == 4)
-        if (p.n == static_cast<int64_t>(8 * V * kWarp) * s.warps) return run_backward<T, G, V, true>(p, s, st);
-    return run_backward<T, G, V, false>(p, s, st);
+        if (p.n == static_cast<int64_t>(8 * V) * s.team) return run_backward<T, G, V, true, false>(p, s, st);
+    if constexpr (V == 1)
+        if (s.team < kWarp) return run_backward<T, G, V, false, true>(p, s, st);
+    return run_backward<T, G, V, false, false>(p, s, st);
 }
 // f(widest access, vectors per thread) as constants
 template <typename T, typename F>
@@ -829,14 +857,16 @@ cudaError_t norm(NormParams p, int num_sms, cudaStream_t st) {
     const int access = widest<T>(p.n, {{p.x, p.ldx}, {p.y, p.ldy}, {p.w, 0}, {p.b, 0}});
     const Shape s = shape_of<T>(p.rows, p.n, most_vectors(access, 8 / static_cast<int>(sizeof(T))), kForwardThreads / 256,
                                 kForwardThreads / kMostThreads, num_sms);
-    p.warps = s.warps;
+    p.warps = std::max(s.team / kWarp, 1);
+    p.lanes = s.team;
     return with_shape<T>(access, s.v, [&](auto g, auto v) {
         return run_norm<T, decltype(g)::value, decltype(v)::value>(p, s, num_sms, st);
     });
 }
 template <typename T>
 cudaError_t norm_backward(NormBackwardParams p, const Shape& s, int access, cudaStream_t st) {
-    p.warps = s.warps;
+    p.warps = std::max(s.team / kWarp, 1);
+    p.lanes = s.team;
     return with_shape<T>(access, s.v, [&](auto g, auto v) {
         return run_backward<T, decltype(g)::value, decltype(v)::value>(p, s, st);
     });
@@ -880,7 +910,7 @@ static bool all_aligned(int dtype, std::initializer_list<std::pair<const void*, 
 cudaError_t launch_norm(int dtype, int64_t rows, int64_t n, const void* x, int64_t ldx, const void* w, const void* b,
                         float eps, void* y, int64_t ldy, float* mean, float* rstd, int num_sms, cudaStream_t st) {
     const NormParams p{rows, n,    x,    ldx, w,     b, eps, y, ldy,
-                       mean, rstd, 1,    false, all_aligned(dtype, {{x, ldx}, {y, ldy}, {w, 0}, {b, 0}})};
+                       mean, rstd, 1,    0,    false, all_aligned(dtype, {{x, ldx}, {y, ldy}, {w, 0}, {b, 0}})};
     return dtype == SGEMM_F32 ? norm<float>(p, num_sms, st) : norm<bf16>(p, num_sms, st);
 }
 
@@ -901,7 +931,7 @@ cudaError_t launch_norm_backward(int dtype, int64_t rows, int64_t n, const void*
                                  const void* residual, int64_t ldr, void* dx, int64_t lddx, void* dw, void* db,
                                  float* part, int num_sms, cudaStream_t st) {
     const NormBackwardParams p{rows, n,        dy,  lddy, x,    ldx,                        w, mean,
-                               rstd, residual, ldr, dx,   lddx, dw || db ? part : nullptr, cdiv(n, 4) * 4, 1,
+                               rstd, residual, ldr, dx,   lddx, dw || db ? part : nullptr, cdiv(n, 4) * 4, 1, 0,
                                all_aligned(dtype, {{dy, lddy}, {x, ldx}, {w, 0}, {residual, ldr}, {dx, lddx}})};
     return dtype == SGEMM_F32
                ? backward<float>(p, static_cast<float*>(dw), static_cast<float*>(db), num_sms, st)

@@ -112,6 +112,14 @@ def test_norm_many_rows(dtype, t, n):
     _check(torch.Generator().manual_seed(n), dtype, t, n)
 
 
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS.get)
+@pytest.mark.parametrize("t", [1, 3, 33, 4099])
+@pytest.mark.parametrize("n", [2, 9, 63, 64, 65, 100, 128, 129])
+def test_norm_narrow_rows(dtype, t, n):
+    """Rows that a part of a warp holds, several of them to a warp, whose last ones may be missing."""
+    _check(torch.Generator().manual_seed(t + n), dtype, t, n)
+
+
 @pytest.mark.parametrize("n", [100, 4096, 9000])
 def test_norm_mean_far_from_zero(n):
     """A mean a thousand times the spread: the squares are taken around it."""

@@ -168,8 +168,7 @@ struct Team {
           lane(threadIdx.x % kWarp) {}
     // how far this team's row lies ahead of that of its warp's first team, which decides for the warp
     __device__ __forceinline__ int ahead() const { return PARTS ? lane / threads : 0; }
-    __device__ __forceinline__ float part_sum(float v) const {  // over up to a warp
-        if (threads > 16) v += __shfl_xor_sync(0xffffffffu, v, 16);
+    __device__ __forceinline__ float part_sum(float v) const {
         if (threads > 8) v += __shfl_xor_sync(0xffffffffu, v, 8);
 #pragma unroll
         for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -227,8 +226,8 @@ struct NormParams {
     int64_t ldy;
     float *mean, *rstd;
     int warps, lanes;  // of a team: lanes where they are no warp
-    bool shared_wb;  // w and b have places in shared memory
-    bool vec;        // rows too wide to be held: all in 16-byte accesses
+    bool shared_wb;    // w and b have places in shared memory
+    bool vec;          // rows too wide to be held: all in 16-byte accesses
 };
 
 // V vectors of eight per thread, S rows on their way per team.  FULL: rows fill their teams; without tests of columns

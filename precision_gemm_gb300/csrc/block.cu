@@ -13,19 +13,18 @@
 // block's promotion is one FMA per element, two elements to an instruction.  Warp 0 loads (TMA),
 // warp 1 issues the MMAs, warp 2 multiplies the scales, several blocks ahead, into shared memory;
 // warps 4 to 11 promote and finish, each its quarter of the lanes and half of the columns, whose
-// sums take half of the register file (setmaxnreg).  From 129 rows on two CTAs of a cluster take
-// neighbouring 128 rows and each brings half of the tile's w for both by multicast; each runs its
-// own MMAs (one cta_group::2 MMA for both moves a third less through shared memory, but its two
-// CTAs then wait for one another's promotion of every block: 760 to 845 cycles each against 785).
+// sums take half of the register file (setmaxnreg).  Every CTA loads its own tiles and runs its own
+// MMAs (one cta_group::2 MMA for two CTAs moves a third less through shared memory, but the two
+// then wait for one another's promotion of every block, 760 to 845 cycles each).
 //
 // For few tiles their k is cut into slices, whose scaled sums are added in slice order by
 // block_sum_kernel.
 //
 // Bound: what a CTA's shared memory gives its MMAs.  A block of 128 x 256 x 128 reads 48 KiB of
-// operands that TMA wrote there before (768 cycles at 128 bytes each); it takes 785.
-// Measured with quantized x, bfloat16 results (L2 cold): 4096 x 8192 x 4096 127 us (2.2 PFLOP/s), of
-// which a unit's loop takes four fifths; with bias and gelu 148, with bias, silu and residual 145 (180 while
-// each lane read its own row's); 1024 x 4096 x 4096 26 us, 64 x 4096 x 4096 14 us.
+// operands that TMA wrote there before: 768 cycles at 128 bytes each, 0.37 us at 2.07 GHz; it takes 0.40.
+// Measured with quantized x, bfloat16 results (L2 cold): 4096 x 8192 x 4096 126 us (2.2 PFLOP/s), of
+// which a unit's loop takes four fifths; with bias and gelu 145, with bias, silu and residual 144 (180 while
+// each lane read its own row's); 1024 x 4096 x 4096 24 us, 64 x 4096 x 4096 13 us.
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -33,7 +32,6 @@
 
 #include "block.cuh"
 #include "layers.h"
-#include "pair.cuh"
 #include "ptx.cuh"
 
 namespace pg {
@@ -51,7 +49,7 @@ constexpr int kScales = 4;      // blocks of k whose scales come together
 constexpr int kScaleSlots = 2;  // such groups ready or on their way
 constexpr int kBiasSlots = 3;   // units whose bias is there or in use: the scales run two groups ahead, of two units at most
 constexpr int kOutBytes = 64;   // of each row of a warp's results, on their way out together
-constexpr int kGroupTiles = 8;
+constexpr int kGroupTiles = 8;  // rasterisation: tiles of rows walked before the next tile of features
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -200,7 +198,6 @@ struct Cfg {
     static constexpr int MINE = BN / 2;                // columns of an epilogue warp: a half of the tile's
     static constexpr int BUFFERS = BN == 256 ? 2 : 4;  // of TMEM: blocks of k on their way
     static constexpr uint32_t TMEM_COLS = BUFFERS * BN;
-    static constexpr int HALF_BYTES = B_BYTES / 2;     // of w in a slot
     static constexpr int BAR_BYTES = (2 * STAGES + 2 * BUFFERS + 2 * kScaleSlots + 1) * 8 + 16;
     static constexpr int OUT_BYTES = kEpiWarps * 32 * kOutBytes;
     static constexpr int SCALE_BYTES = kScaleSlots * 2 * kRows * kScales * 4;  // of the rows, for each half of the columns
@@ -208,13 +205,12 @@ struct Cfg {
     static constexpr size_t SMEM =
         1024 + static_cast<size_t>(STAGES) * STAGE_BYTES + OUT_BYTES + SCALE_BYTES + BIAS_BYTES + BAR_BYTES;
     static_assert(kEpiWarps * MINE * 4 <= SCALE_BYTES, "a bias for each warp");
-    static_assert(A_BYTES % 1024 == 0 && HALF_BYTES % 1024 == 0, "slots need 1 KiB alignment");
+    static_assert(A_BYTES % 1024 == 0 && B_BYTES % 1024 == 0, "slots need 1 KiB alignment");
 };
 
 struct Params {
     int32_t t, n, kbs;
-    int32_t tiles_t, tiles_n;  // tiles of 256 rows, whose halves a pair of CTAs shares (paired), or of 128
-    int32_t paired;
+    int32_t tiles_t, tiles_n;
     float inv_split, inv_t;    // reciprocals of split and tiles_t
     int32_t split, split_kb;
     const float* x_scales;
@@ -256,7 +252,7 @@ __device__ __forceinline__ void results(const Params& p, int64_t j, int64_t i, i
 }
 
 template <int BN, typename T>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     block_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, const Params p) {
     using C = Cfg<BN>;
     constexpr int S = C::STAGES, NB = C::BUFFERS;
@@ -274,13 +270,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);  // known to be uniform
     const int lane = threadIdx.x & 31;
-    const uint32_t rank = __shfl_sync(0xffffffffu, cluster_rank(), 0);
-    const int first = p.paired ? blockIdx.x >> 1 : blockIdx.x, step = p.paired ? gridDim.x >> 1 : gridDim.x;
+    const int first = blockIdx.x, step = gridDim.x;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
             mbar_init(full0 + 8 * s, 1);
-            mbar_init(empty0 + 8 * s, p.paired ? 2 : 1);
+            mbar_init(empty0 + 8 * s, 1);
         }
         for (int b = 0; b < NB; ++b) {
             mbar_init(acc_full0 + 8 * b, 1);
@@ -301,7 +296,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     pdl_wait();
     tc_fence_before_sync();
     __syncthreads();
-    cluster_sync_all();  // every CTA's barriers exist before any cross-CTA traffic
     tc_fence_after_sync();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_holder, 0);
     const int units = p.tiles_t * p.tiles_n * p.split;
@@ -326,7 +320,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tn = divide(tile, p.tiles_t, p.inv_t, tt);
         else
             tile_coords(tile, p.tiles_t, p.tiles_n, kGroupTiles, tt, tn);
-        x.j0 = p.paired ? tt * (2 * kRows) + kRows * static_cast<int>(rank) : tt * kRows;
+        x.j0 = tt * kRows;
         x.i0 = tn * BN;
         x.kb0 = x.slice * p.split_kb;
         x.nkb = max(min(x.kb0 + p.split_kb, p.kbs) - x.kb0, 0);
@@ -354,15 +348,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         const uint32_t bar = full0 + 8 * slot_i;
                         if (lane == 0) mbar_arrive_expect_tx(bar, C::STAGE_BYTES);
                         const uint32_t slot = smem_u32(smem) + slot_i * C::STAGE_BYTES;
-                        const uint32_t w_slot = slot + C::A_BYTES + C::HALF_BYTES * rank;
                         const int k0 = (kb0 + kb) * kBlock;
                         tma_load_3d_warp(slot, &tmX, k0, ja, 0, bar);
-                        if (p.paired) {  // each CTA brings half of w's rows for both
-                            tma_load_3d_multicast_warp(w_slot, &tmW, k0, ib + C::MINE * static_cast<int>(rank), 0, bar, 3);
-                        } else {
-                            tma_load_3d_warp(slot + C::A_BYTES, &tmW, k0, ib, 0, bar);
-                            tma_load_3d_warp(slot + C::A_BYTES + C::HALF_BYTES, &tmW, k0, ib + C::MINE, 0, bar);
-                        }
+                        tma_load_3d_warp(slot + C::A_BYTES, &tmW, k0, ib, 0, bar);
                         if (++slot_i == S) {
                             slot_i = 0;
                             phase ^= 1;
@@ -371,12 +359,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 if (lane == 0) pdl_trigger();
                 if (lane == 0) {
-                    // Let every copy land before the CTA may retire, the other CTA's among them.
+                    // Let every copy land before the CTA may retire.
                     for (int q = max(0, it - S); q < it; ++q)
                         mbar_wait_bounded(full0 + 8 * (q % S), (q / S) & 1, p.timeout_ns, nullptr);
-                    // ... and the other CTA's releases of the slots, which arrive in this one's barriers.
-                    for (int q = max(0, it - S); q < it && p.paired && ok; ++q)
-                        ok = mbar_wait_bounded(empty0 + 8 * (q % S), (q / S) & 1, p.timeout_ns, abort_flag);
                 }
             }
             __syncwarp();
@@ -418,10 +403,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     for (int kk = 0; kk < kBlock / 32; ++kk)
                         mma_e4m3_warp(tmem + b * BN, a_desc0 + (o + 2 * kk), b_desc0 + (o + 2 * kk), idesc, kk > 0);
                     mma_commit_warp(acc_full0 + 8 * b);
-                    if (p.paired)
-                        mma_commit_multicast_warp(empty, 3);
-                    else
-                        mma_commit_warp(empty);
+                    mma_commit_warp(empty);
                 }
             }
             if (!ok && lane == 0) raise_abort(abort_flag, p.status);
@@ -731,7 +713,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
     tc_fence_before_sync();
     __syncthreads();
-    cluster_sync_all();  // no CTA leaves while its peer may still read its shared memory or barriers
     if (warp == 1) {
         tc_fence_after_sync();
         tmem_dealloc(tmem, C::TMEM_COLS);
@@ -766,11 +747,8 @@ cudaError_t run(const CUtensorMap (&m)[2], const Params& p, int num_sms, cudaStr
     static std::atomic<uint64_t> smem_set{0};
     cudaError_t e = set_smem_limit_once(smem_set, reinterpret_cast<const void*>(kern), static_cast<int>(C::SMEM));
     if (e != cudaSuccess) return e;
-    static std::atomic<int> resident[64];
-    const int most = resident_pairs(reinterpret_cast<const void*>(kern), kThreads, C::SMEM, num_sms, resident);
     const int64_t units = static_cast<int64_t>(p.tiles_t) * p.tiles_n * p.split;
-    const int64_t clusters = std::min<int64_t>(p.paired ? units : cdiv(units, 2), most);
-    return launch_kernel(true, kern, dim3(static_cast<unsigned>(2 * clusters)), dim3(kThreads),
+    return launch_kernel(true, kern, dim3(static_cast<unsigned>(std::min<int64_t>(units, num_sms))), dim3(kThreads),
                          C::SMEM, st, m[0], m[1], p);
 }
 
@@ -807,16 +785,15 @@ cudaError_t launch_copy_bytes(const uint8_t* src, int64_t ld, int64_t rows, int6
 }
 
 BlockPlan plan_block(int64_t t, int64_t n, int64_t k, int num_sms, int force_bn, int force_split) {
-    const bool paired = t > kRows;
-    const int at_once = std::max(paired ? num_sms / 2 : num_sms, 1);
+    const int at_once = std::max(num_sms, 1);
     const int64_t kb = cdiv(k, kBlock);
     BlockPlan best{};
     double best_us = 0.0;
     for (int bn : {256, 128, 64}) {
         if (force_bn && force_bn <= 256 && bn != force_bn) continue;
-        // microseconds of a block of k and of a tile's ends, measured at 1024 x 4096 by k of 4096 and 14336
+        // microseconds of a block of k and of a tile's ends, measured at 1024 x 4096 by k of 2048 to 14336
         const double step = bn == 256 ? 0.40 : (bn == 128 ? 0.22 : 0.18), end = bn == 256 ? 3.2 : (bn == 128 ? 1.9 : 1.5);
-        const int64_t tiles = cdiv(t, paired ? 2 * kRows : kRows) * cdiv(n, bn);
+        const int64_t tiles = cdiv(t, kRows) * cdiv(n, bn);
         const int64_t forced = std::min<int64_t>(force_split, std::max<int64_t>(kb, 1));
         const int64_t most = force_split ? forced : std::max<int64_t>(std::min<int64_t>(kb, 3 * at_once / tiles), 1);
         for (int64_t want = force_split ? forced : 1; want <= most; ++want) {
@@ -839,8 +816,7 @@ int launch_block(const CallContext& c, const BlockProduct& b, const BlockPlan& p
     p.t = static_cast<int32_t>(b.t);
     p.n = static_cast<int32_t>(b.n);
     p.kbs = static_cast<int32_t>(cdiv(b.k, kBlock));
-    p.paired = b.t > kRows;
-    p.tiles_t = static_cast<int32_t>(cdiv(b.t, p.paired ? 2 * kRows : kRows));
+    p.tiles_t = static_cast<int32_t>(cdiv(b.t, kRows));
     p.tiles_n = static_cast<int32_t>(cdiv(b.n, plan.bn));
     p.split = plan.split;
     p.inv_split = 1.0f / static_cast<float>(p.split);
@@ -870,7 +846,7 @@ int launch_block(const CallContext& c, const BlockProduct& b, const BlockPlan& p
     if (b.k > 0) {
         int rc;
         if ((rc = call_encode_u8(&m[0], b.x, b.k, b.t, b.ldx, kRows))) return rc;
-        if ((rc = call_encode_u8(&m[1], b.w, b.k, b.n, b.ldw, static_cast<uint32_t>(plan.bn / 2)))) return rc;
+        if ((rc = call_encode_u8(&m[1], b.w, b.k, b.n, b.ldw, static_cast<uint32_t>(plan.bn)))) return rc;
     }
     auto go = [&](auto zero) {
         using T = decltype(zero);

@@ -315,17 +315,6 @@ __device__ __forceinline__ void tma_load_3d_warp(uint32_t dst, const CUtensorMap
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
-// To the same place in the CTAs of the cluster that `mask` names, completing on each one's barrier.
-__device__ __forceinline__ void tma_load_3d_multicast_warp(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y,
-                                                           int32_t z, uint32_t bar, uint16_t mask) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\t"
-        "elect.sync _|q, 0xffffffff;\n\t"
-        "@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
-        " [%0], [%1, {%2, %3, %4}], [%5], %6;\n\t}" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar), "h"(mask)
-        : "memory");
-}
 
 // 2-D tiled store of the shared-memory box at `src` to (x, y) of the tensor (x
 // contiguous, a multiple of 4 elements, never negative); elements of the box
@@ -410,16 +399,6 @@ __device__ __forceinline__ void mma_commit_warp(uint32_t bar) {
         "{\n\t.reg .pred q;\n\t"
         "elect.sync _|q, 0xffffffff;\n\t"
         "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
-        : "memory");
-}
-// On the barrier at the same place in the CTAs of the cluster that `mask` names.
-__device__ __forceinline__ void mma_commit_multicast_warp(uint32_t bar, uint16_t mask) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\t"
-        "elect.sync _|q, 0xffffffff;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
-            bar),
-        "h"(mask)
         : "memory");
 }
 

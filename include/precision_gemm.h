@@ -510,7 +510,8 @@ int sgemm_block_linear(int dtype, int64_t t, int64_t n, int64_t k, const void *x
 
 /*
  * sgemm_layer_norm -- of each row of x: mean = sum x / n, rstd = (sum (x - mean)^2 / n +
- * eps)^-1/2, y = (x - mean) rstd w + bias, the squares taken around the mean.
+ * eps)^-1/2, y = (x - mean) rstd w + bias, the squares taken around the mean, which is off
+ * by no more than the sums' rounding is worth in y, however far from zero it lies.
  *
  *   dtype (1); t >= 0, n >= 1 (2, 3): x and y are t x n; x, ldx (4, 5); w and bias, n
  *   elements each, or NULL for ones and zeros (6, 7); eps >= 0 (8); y, which may be x

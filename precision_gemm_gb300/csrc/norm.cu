@@ -9,16 +9,22 @@
 // per thread where the row is long enough, and walks on by as many rows as there are teams; a
 // row's sums cost two or three trips through a team's warps, which other teams' rows hide.  The
 // next rows are on their way meanwhile, by asynchronous copies into places in shared memory that
-// only the thread itself reads: no barrier is needed for them, and no registers are held.  The
-// mean is formed first and then the squares around it, so that a mean far from zero costs no bits.
+// only the thread itself reads: no barrier is needed for them, and no registers are held.
+//
+// The mean is formed first and then the squares around it.  A mean m is off by a few 2^-24 m, which in
+// h counts as a few 2^-24 m rstd: nothing, unless the mean is farther from zero than h's unit, 1 / rstd.
+// Such a row (far_mean) takes the mean of its differences from m, which are exact, and goes on with
+// what they differ from that, so that a mean far from zero costs no bits; equal values give zeros.
 //
 // In the backward pass a thread's columns stay the same from row to row, so the sums for dw and
 // db stay in its registers; a block's teams add theirs in order, and norm_sum_kernel adds the
 // blocks' sums in order: equal inputs give equal bits.  Rows too wide for that are read again for
 // each of the passes.
 //
-// Measured (L2 cold), forward and backward without residual: 16384 x 2048 float32 48 and 69 us (5.6 and
-// 5.8 TB/s), 16384 x 4096 bfloat16 53 and 84 us (5.1 and 4.8 TB/s), 512 x 4096 bfloat16 7 and 14 us, 1 x 4096 4 and 6 us.
+// Measured (L2 cold), forward and backward without residual: 16384 x 2048 float32 51 and 69 us (5.3 and
+// 5.8 TB/s), 16384 x 4096 bfloat16 56 and 84 us (4.8 TB/s), 512 x 4096 bfloat16 7 and 14 us, 1 x 4096 4 and 6 us.
+// The test for far means costs the forward pass 2 to 4 % of that (rows finished again after their results are
+// written: 15 %); far from zero they take 57 and 69 us.
 #include <algorithm>
 #include <initializer_list>
 #include <utility>
@@ -216,6 +222,9 @@ __device__ __forceinline__ float block_sum(float v, float* slots) {
     return warp_sum(slots[threadIdx.x % kWarp]);
 }
 
+// (var = 1 / rstd^2: nothing waits for the root)
+__device__ __forceinline__ bool far_mean(float mean, float var) { return mean * mean > var; }
+
 struct NormParams {
     int64_t rows, n;
     const void* x;
@@ -231,7 +240,7 @@ struct NormParams {
 };
 
 // V vectors of eight per thread, S rows on their way per team.  FULL: rows fill their teams; without tests of columns
-// and their branches 16384 x 4096 bfloat16 takes 53 us instead of 64.
+// and their branches 16384 x 4096 bfloat16 takes a sixth less time.
 template <typename T, int G, int V, int S, int NT, bool FULL, bool PARTS>
 __global__ void __launch_bounds__(NT, kForwardThreads / NT) norm_kernel(const NormParams p) {
     __shared__ float slots[4][NT / kWarp];
@@ -295,23 +304,37 @@ __global__ void __launch_bounds__(NT, kForwardThreads / NT) norm_kernel(const No
             }
         }
         // two places for each sum, taken in turn: one barrier per sum
-        const float mean = whole.sum(sum.x + sum.y, slots[turn]) * inv;
-        sum = both(0.0f);
+        float mean = whole.sum(sum.x + sum.y, slots[turn]) * inv;
+        // v -= by, and the sum over the row of v or (SQUARES) of v^2
+        auto without = [&](float by, auto squares) {
+            constexpr bool SQUARES = decltype(squares)::value;
+            sum = both(0.0f);
 #pragma unroll
-        for (int j = 0; j < V; ++j)
+            for (int j = 0; j < V; ++j)
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                v[j][t] = add2(v[j][t], both(-mean));
-                if (FULL) {
-                    sum = fma2(v[j][t], v[j][t], sum);
-                } else if (G == 1) {
-                    if (column<G>(tid, team, j, 2 * t) < n) sum.x = fmaf(v[j][t].x, v[j][t].x, sum.x);
-                    if (column<G>(tid, team, j, 2 * t + 1) < n) sum.y = fmaf(v[j][t].y, v[j][t].y, sum.y);
-                } else if (column<G>(tid, team, j, 2 * t / G * G) < n) {
-                    sum = fma2(v[j][t], v[j][t], sum);
+                for (int t = 0; t < 4; ++t) {
+                    const float2 d = v[j][t] = add2(v[j][t], both(-by));
+                    if (FULL) {
+                        sum = SQUARES ? fma2(d, d, sum) : add2(d, sum);
+                    } else if (G == 1) {
+                        if (column<G>(tid, team, j, 2 * t) < n) sum.x = SQUARES ? fmaf(d.x, d.x, sum.x) : d.x + sum.x;
+                        if (column<G>(tid, team, j, 2 * t + 1) < n) sum.y = SQUARES ? fmaf(d.y, d.y, sum.y) : d.y + sum.y;
+                    } else if (column<G>(tid, team, j, 2 * t / G * G) < n) {
+                        sum = SQUARES ? fma2(d, d, sum) : add2(d, sum);
+                    }
                 }
-            }
-        const float rstd = 1.0f / sqrtf(whole.sum(sum.x + sum.y, slots[turn + 1]) * inv + p.eps);
+            return sum.x + sum.y;
+        };
+        float var = fmaf(whole.sum(without(mean, std::true_type()), slots[turn + 1]), inv, p.eps);
+        // (teams of a warp decide together, and one whose mean is near keeps its bits)
+        const bool far = far_mean(mean, var);
+        if (PARTS ? __any_sync(0xffffffffu, far) : far) {
+            float rest = whole.sum(without(0.0f, std::false_type()), slots[turn]) / static_cast<float>(n);
+            if (PARTS && !far) rest = 0.0f;
+            var = fmaf(whole.sum(without(rest, std::true_type()), slots[turn + 1]), inv, p.eps);
+            mean += rest;
+        }
+        const float rstd = 1.0f / sqrtf(var);
         turn ^= 2;
         if (tid == 0 && mine) {
             if (p.mean) p.mean[row] = mean;
@@ -397,19 +420,28 @@ __global__ void __launch_bounds__(1024) norm_wide_kernel(const NormParams p) {
     });
     const float count = static_cast<float>(p.n);
     const float mean = block_sum(sum, slots[0]) / count;
-    sum = 0.0f;
-    for_columns<E>(p.n, [&](int64_t c, int valid) {
-        float v[E];
-        load_some(x + c, valid, v);
+    float rest = 0.0f;  // of the mean
+    auto sum_of = [&](auto squares) {  // of x - mean - rest, or its squares
+        float s = 0.0f;
+        for_columns<E>(p.n, [&](int64_t c, int valid) {
+            float v[E];
+            load_some(x + c, valid, v);
 #pragma unroll
-        for (int t = 0; t < E; ++t) {
-            const float d = v[t] - mean;
-            if (t < valid) sum = fmaf(d, d, sum);
-        }
-    });
-    const float rstd = 1.0f / sqrtf(block_sum(sum, slots[1]) / count + p.eps);
+            for (int t = 0; t < E; ++t) {
+                const float d = v[t] - mean - rest;
+                if (t < valid) s = decltype(squares)::value ? fmaf(d, d, s) : s + d;
+            }
+        });
+        return s;
+    };
+    float var = block_sum(sum_of(std::true_type()), slots[1]) / count + p.eps;
+    if (far_mean(mean, var)) {
+        rest = block_sum(sum_of(std::false_type()), slots[0]) / count;
+        var = block_sum(sum_of(std::true_type()), slots[1]) / count + p.eps;
+    }
+    const float rstd = 1.0f / sqrtf(var);
     if (threadIdx.x == 0) {
-        if (p.mean) p.mean[row] = mean;
+        if (p.mean) p.mean[row] = mean + rest;
         if (p.rstd) p.rstd[row] = rstd;
     }
     T* y = static_cast<T*>(p.y) + row * p.ldy;
@@ -419,7 +451,7 @@ __global__ void __launch_bounds__(1024) norm_wide_kernel(const NormParams p) {
         if (w) load_some(w + c, valid, g);
         if (b) load_some(b + c, valid, a);
 #pragma unroll
-        for (int t = 0; t < E; ++t) v[t] = fmaf((v[t] - mean) * rstd, w ? g[t] : 1.0f, b ? a[t] : 0.0f);
+        for (int t = 0; t < E; ++t) v[t] = fmaf((v[t] - mean - rest) * rstd, w ? g[t] : 1.0f, b ? a[t] : 0.0f);
         store_some(y + c, valid, v);
     });
 }

@@ -327,3 +327,35 @@ def test_norm_binding_refuses_mismatched_tensors():
     with pytest.raises(pg.SgemmError):
         pg.layer_norm(x[:, :0])
     assert pg.launch_count() == before
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS.get)
+@pytest.mark.parametrize("n", [3, 64, 100, 777, 1000, 4095, 7168, 9001, 16384, 20000, 32769])
+def test_norm_equal_values_are_their_mean(dtype, n):
+    """Rows of one value each: it is their mean to the bit, and every h is zero, whatever 1 / n and the
+    sums round to (the values' differences from any float near them are few of its last places, whose
+    sums are exact)."""
+    x = torch.tensor([3.25, 1000.0, 100.1, -777.7, 7.0, 12345.6]).to(dtype)[:, None].expand(6, n).contiguous().cuda()
+    b = _draw(torch.Generator().manual_seed(n), dtype, n).cuda()
+    y, mean, rstd = pg.layer_norm(x, stats=True)
+    assert not y.any() and torch.equal(mean, x[:, 0].float())
+    assert torch.allclose(rstd, torch.full_like(rstd, 1e-5 ** -0.5), rtol=1e-6)
+    assert torch.equal(pg.layer_norm(x, None, b), b.expand(6, n))
+    near = torch.full((9, n), 2.0 ** -10, dtype=dtype, device="cuda")  # a mean within h's unit, beside others
+    near[4] = 1000
+    assert torch.equal(pg.layer_norm(near)[3], pg.layer_norm(near[:4])[3])
+
+
+@pytest.mark.parametrize("dtype,shift", [(torch.float32, 1e3), (torch.float32, -1e5), (torch.bfloat16, 100.0)])
+@pytest.mark.parametrize("t,n", [(40, 100), (3, 1000), (30, 4096), (9, 7169), (6, 16384), (4, 20000), (3, 32771)])
+def test_norm_mean_far_from_zero_costs_no_bits(dtype, shift, t, n):
+    """The values' differences from a float near their mean are exact, so h is off by the sums of such
+    differences alone: UNITS of their mean magnitude, which is at most 1 / rstd, and UNITS of h for
+    rstd; the mean that is returned is rounded once more."""
+    g = torch.Generator().manual_seed(n)
+    x = (torch.randn(t, n, generator=g) + shift).to(dtype)
+    y, mean, rstd = pg.layer_norm(x.cuda(), eps=1e-6, stats=True)
+    (want, m, r), _ = forward(x, None, None, 1e-6)
+    close(y, want, 1 + 2 * want.abs(), dtype)
+    assert ((mean.double().cpu() - m).abs() <= 2.0 ** -24 * m.abs() + UNITS / r).all()
+    assert ((rstd.double().cpu() - r).abs() <= UNITS * r).all()

@@ -236,8 +236,6 @@ int backward_steps(const CallContext& c, const Backward& b, Arena& a, cudaStream
         dz.ptr = dz_own = static_cast<bf16*>(a.take(static_cast<size_t>(dz.parts) * dz.stride * 2));
     }
     if (b.gated && (own_dz || (b.dbias && b.n > 0))) {
-        // (dz is formed for its sums alone too: its place is then the call's own)
-        if (!own_dz) dz_own = static_cast<bf16*>(a.take(static_cast<size_t>(b.dtype == SGEMM_F32 ? 3 : 1) * b.rows * packed_ld(b.n) * 2));
         float* part = b.dbias ? static_cast<float*>(a.take(gate_part_bytes(b.rows, b.n / 2, c.sms))) : nullptr;
         if (!a.dry()) {
             if ((e = launch_dgate(b.dtype, b.rows, b.n / 2, b.dy, b.lddy, b.z, b.ldz, b.act, dz_own, packed_ld(b.n),

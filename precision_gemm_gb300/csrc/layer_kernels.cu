@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(256, 4) dact_kernel(int64_t rows, int64_t n, c
 // sums of its 2 n columns in part (slabs x 2 n), with the threads laid out as in dact_kernel: thread
 // (l, c) takes rows l, l + 8, ... and eight columns, neighbouring ones where all rows are whole eights at
 // 16-byte boundaries (VEC), else every 32nd, so that a warp's single elements are neighbours.
-// HBM-bound: reads dy and z, writes dz.  bfloat16 runs best with as many threads as fit (8192 x 4096, gelu, with
+// dz null: the sums alone.  HBM-bound: reads dy and z, writes dz.  bfloat16 runs best with as many threads as fit (8192 x 4096, gelu, with
 // dbias: 64 us, 5.2 TB/s; 79 with half as many of two rows' loads each), float32, whose dz are three parts,
 // with half of them (147 us, 5.5 TB/s; 163).
 template <typename T, int PARTS, bool VEC>
@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2)
     const int64_t r0 = slab * slab_size, r1 = rows - r0 < slab_size ? rows : r0 + slab_size;
     dy += c0;
     z += c0;
-    dz += c0;
+    if (dz) dz += c0;
     float sum[2][8] = {};
     auto one = [&](auto f, int64_t r, const float(&d)[8], const float(&g)[8], const float(&v)[8]) {
         float dg[8], dv[8];
@@ -153,6 +153,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2)
             sum[0][t] += dg[t];
             sum[1][t] += dv[t];
         }
+        if (!dz) return;
         bf16* at = dz + r * lddz + column(0);
         if (VEC) {
             store_parts8<PARTS>(at, rows * lddz, dg);

@@ -452,7 +452,7 @@ cudaError_t launch_dact(int dtype, int64_t rows, int64_t n, const void* dy, int6
                         int num_sms, cudaStream_t st);
 int dact_launches(bool with_bias);
 // The same for out = act(g) v: z = [g v] and dz = [dy v act'(g), dy act(g)] have 2 n columns, dbias 2 n
-// entries (one group).
+// entries (one group).  dz null: the sums alone.
 size_t gate_part_bytes(int64_t rows, int64_t n, int num_sms);
 cudaError_t launch_dgate(int dtype, int64_t rows, int64_t n, const void* dy, int64_t lddy, const void* z, int64_t ldz,
                          int act, bf16* dz, int64_t lddz, void* dbias, float* part, int num_sms, cudaStream_t st);

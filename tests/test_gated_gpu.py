@@ -343,3 +343,25 @@ def test_gated_binding_refuses_mismatched_tensors():
         with pytest.raises(ValueError):
             call()
     assert pg.launch_count() == before
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS.get)
+@pytest.mark.parametrize("t,n", [(2000, 512), (1999, 333)])
+def test_gated_bias_gradient_alone_forms_no_dz(dtype, t, n):
+    """The sums alone need a workspace of their partial sums, far less than dz, and have the full
+    call's bits."""
+    g = _gen(t)
+    x, w, dy = (_draw(g, dtype, *s).cuda() for s in ((t, 40), (2 * n, 40), (t, n)))
+    z = _draw(g, dtype, t, 2 * n, std=2.0).cuda()
+    want = pg.gated_linear_backward(dy, x, w, z, "gelu")[2]
+    space = torch.empty(5 << 18, dtype=torch.uint8, device="cuda")
+    assert space.numel() < t * 2 * n * 2
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    pg.set_workspace(space, stream=s)
+    try:
+        dx, dw, db = pg.gated_linear_backward(dy, x, w, z, "gelu", need_dx=False, need_dw=False, stream=s)
+        s.synchronize()
+    finally:
+        pg.set_workspace(None, stream=s)
+    assert dx is None and dw is None and torch.equal(db, want)

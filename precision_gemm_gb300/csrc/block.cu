@@ -431,9 +431,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int d = 0; d < kScales; ++d) {
                         const int at = min(kb + d, x.nkb - 1);
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) a[r][d] = __ldg(sx[r] + at * p.xs_block);
+                        for (int r = 0; r < 4; ++r) a[r][d] = sx[r][at * p.xs_block];
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) b[h][d] = __ldg(sw[h] + at);
+                        for (int h = 0; h < 2; ++h) b[h][d] = sw[h][at];
                     }
                     ok = mbar_wait_short_warp(scale_empty0 + 8 * slot, phase, p.timeout_ns, abort_flag);
                     if (!ok) {

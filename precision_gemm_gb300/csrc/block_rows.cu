@@ -41,9 +41,11 @@ struct RowsParams {
     int x_stride;  // of the rows of x in shared memory, bytes: the banks of two rows differ
 };
 
+// 16 bytes of a weight row, which no other load reads.  (A coherent load: the block may be there while an
+// earlier kernel still writes the weights, and a load that takes them for constant is not for such data.)
 __device__ __forceinline__ uint4 stream16(const void* p) {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(p));
     return v;
@@ -171,13 +173,13 @@ __global__ void __launch_bounds__(32 * kWarps, 2) block_rows_kernel(const RowsPa
             acc[m][3] = fmaf(c[3], s1, acc[m][3]);
         }
     };
-    float next_sw = kb0 < kb1 ? __ldg(sw + kb0) : 0.0f;
+    float next_sw = kb0 < kb1 ? sw[kb0] : 0.0f;
     for (int kb = kb0; kb < whole; kb += kAhead) {
 #pragma unroll
         for (int d = 0; d < kAhead; ++d) {
             if (kb + d >= whole) break;
             const float s = next_sw;
-            if (kb + d + 1 < kb1) next_sw = __ldg(sw + kb + d + 1);
+            if (kb + d + 1 < kb1) next_sw = sw[kb + d + 1];
             add_block(raw[d], kb + d, s);
             fetch(raw[d], kb + d + kAhead);
         }

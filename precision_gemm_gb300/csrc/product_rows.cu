@@ -23,10 +23,11 @@ struct RowsParams {
     int ks;      // warps that share a weight row's k, 1 to kWarps
 };
 
-// 16 bytes of a weight row: read once, so they take no place in L1, which holds x.
+// 16 bytes of a weight row: read once, so they take no place in L1, which holds x.  (A coherent load: the
+// block may be there while an earlier kernel still writes the weights.)
 __device__ __forceinline__ uint4 stream16(const void* p) {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(p));
     return v;

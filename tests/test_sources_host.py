@@ -23,3 +23,11 @@ def test_no_bulk_load_is_multicast(path):
     memory: every bulk copy goes to one thread block's shared memory."""
     for statement in re.findall(r"cp\.async\.bulk[^;]*;", _code(path)):
         assert "multicast" not in statement, statement
+
+
+@pytest.mark.parametrize("path", SOURCES, ids=os.path.basename)
+def test_no_load_takes_its_data_for_constant(path):
+    """Kernels start while the one before them still writes what they read (programmatic launches), and
+    wait for it inside: a non-coherent load is for data that is constant while its kernel runs."""
+    code = _code(path)
+    assert "ld.global.nc" not in code and not re.search(r"\b__ldg\s*\(", code)

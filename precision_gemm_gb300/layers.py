@@ -353,7 +353,8 @@ def block_linear(x, w, scales, bias=None, act="none", residual=None, x_scales=No
     (ceil(n / 128), ceil(k / 128)) as quantize(_, 128) makes them.  x (..., k) is float32 or
     bfloat16, which the call rounds to e4m3 as quantize does, or e4m3 with x_scales (...,
     ceil(k / 128)); the result is of x's type, or of `dtype` (bfloat16) for an e4m3 x, and so
-    are bias (n) and residual (..., n).  residual and out may be the same tensor."""
+    are bias (n) and residual (..., n).  residual and out may be the same tensor.  A product of
+    two blocks' scales below 2^-126 costs the result bits, one above 3.4e38 makes it infinite or NaN."""
     if stream is not None:
         return _on(stream, block_linear, x, w, scales, bias, act, residual, x_scales, out, dtype)
     lib = load_library()

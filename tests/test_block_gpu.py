@@ -412,3 +412,22 @@ def test_block_binding_refuses_mismatched_tensors():
     with pytest.raises(pg.SgemmError):
         pg.quantize(x, 64)
     assert pg.launch_count() == before
+
+
+def _e4m3(g, *shape):
+    """Every finite value as likely as the next."""
+    v = torch.randint(0, 255, shape, generator=g, dtype=torch.uint8)
+    return torch.where(v % 128 == 127, v - 1, v).view(E4M3)
+
+
+@pytest.mark.parametrize("power", [-63, 40])
+@pytest.mark.parametrize("t", [1, 9, 40, 300])
+def test_block_scales_up_to_their_stated_range(t, power):
+    """Products of two scales from the smallest normal floats on, and large ones: all their bits count."""
+    n, k = 200, 700
+    g = _gen(t)
+    xq, wq = _e4m3(g, t, k), _e4m3(g, n, k)
+    xs, ws = (torch.exp2(power + torch.rand(s, generator=g)) for s in ((t, 6), (2, 6)))
+    y = pg.block_linear(xq.cuda(), wq.cuda(), ws.cuda(), x_scales=xs.cuda(), dtype=torch.float32).double().cpu()
+    want, den = product(xq, xs, wq, ws, None, "none", None)
+    assert ((y - want).abs() <= R.NORM * den).all(), float(((y - want).abs() / den).max())

@@ -431,3 +431,36 @@ def test_block_scales_up_to_their_stated_range(t, power):
     y = pg.block_linear(xq.cuda(), wq.cuda(), ws.cuda(), x_scales=xs.cuda(), dtype=torch.float32).double().cpu()
     want, den = product(xq, xs, wq, ws, None, "none", None)
     assert ((y - want).abs() <= R.NORM * den).all(), float(((y - want).abs() / den).max())
+
+
+@pytest.mark.parametrize("mixed", [False, True], ids=["halves", "mixed"])
+@pytest.mark.parametrize("t", [1, 9, 40, 130])
+def test_block_sums_keep_what_cancels(t, mixed):
+    """In each block of 128, 60 terms of 448^2, 60 of -448^2 and eight small ones: whole numbers whose
+    partial sums stay below 2^24 in any order, so a sum in FP32 is exact, while one that is cut to 22 bits
+    after every 32 k is not.  Every element has to be equal."""
+    n, k = 200, 512
+    g = _gen(t)
+    x, w = torch.full((t, 4, 128), 448.0), torch.full((n, 4, 128), 448.0)
+    x[1::2] *= -1
+    for b in range(4):
+        at = torch.randperm(128, generator=g) if mixed else torch.arange(128)
+        small = at[torch.arange(7, 128, 16)]
+        large = at[torch.arange(128) % 16 != 7]
+        x[:, b, small] = torch.randint(1, 4, (t, 8), generator=g).float()
+        w[:, b, small] = torch.randint(-3, 4, (n, 8), generator=g).float()
+        w[:, b, large[60:]] *= -1
+    assert (x.abs().double().view(t, k) @ w.abs().double().view(n, k).t()).max() / 8 < 2 ** 24  # a half of a block's
+    want = x.double().view(t, k) @ w.double().view(n, k).t()
+    cut = torch.zeros(t, n, dtype=torch.float64)
+    for b in range(4):
+        s = torch.zeros(t, n, dtype=torch.float64)
+        for c in range(0, 128, 32):
+            s += x[:, b, c:c + 32].double() @ w[:, b, c:c + 32].double().t()
+            step = torch.exp2(torch.floor(torch.log2(s.abs().clamp_min(1))) - 21)
+            s = torch.trunc(s / step) * step
+        cut += s
+    assert mixed or not torch.equal(cut, want)
+    y = pg.block_linear(x.view(t, k).to(E4M3).cuda(), w.view(n, k).to(E4M3).cuda(), torch.ones(2, 4, device="cuda"),
+                        x_scales=torch.ones(t, 4, device="cuda"), dtype=torch.float32)
+    assert torch.equal(y.double().cpu(), want)

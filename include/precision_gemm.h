@@ -536,7 +536,7 @@ int sgemm_layer_norm(int dtype, int64_t t, int64_t n, const void *x, int64_t ldx
  *   dtype, t, n (1-3); dy, lddy (4, 5); x, ldx (6, 7); w or NULL (8); mean, rstd
  *   (9, 10); residual, t x n, or NULL: a gradient that reaches x past the norm, added to
  *   dx; ldr (11, 12); dx, lddx (13, 14), dw (15), dbias (16): each may be NULL, which
- *   skips it.  residual may be dx itself.  Sums run in a fixed order.
+ *   skips it.  dx may be residual, dy or x with its ld.  Sums run in a fixed order.
  */
 int sgemm_layer_norm_backward(int dtype, int64_t t, int64_t n, const void *dy, int64_t lddy,
                               const void *x, int64_t ldx, const void *w, const float *mean,

@@ -915,13 +915,13 @@ cudaError_t backward(const NormBackwardParams& p, T* dw, T* db, int num_sms, cud
         e = norm_backward<T>(p, s, access, st);
     } else if (p.rows > 0) {
         blocks = cdiv(p.rows, kSlab);
-        if (p.dx)
-            e = launch_kernel(true, p.vec ? norm_backward_wide_kernel<T, 8> : norm_backward_wide_kernel<T, 1>,
-                              dim3(static_cast<unsigned>(p.rows)), dim3(1024), 0, st, p);
-        if (sums && e == cudaSuccess)
+        if (sums)  // first: dx may lie over x or dy
             e = launch_kernel(true, p.vec ? norm_columns_kernel<T, 8> : norm_columns_kernel<T, 1>,
                               dim3(static_cast<unsigned>(blocks * cdiv(p.n, (p.vec ? 8 : 1) * kWarp))),
                               dim3(256), 0, st, p);
+        if (p.dx && e == cudaSuccess)
+            e = launch_kernel(true, p.vec ? norm_backward_wide_kernel<T, 8> : norm_backward_wide_kernel<T, 1>,
+                              dim3(static_cast<unsigned>(p.rows)), dim3(1024), 0, st, p);
     }
     if (sums && e == cudaSuccess)
         e = launch_kernel(true, norm_sum_kernel<T>, dim3(static_cast<unsigned>(cdiv(p.n, kWarp)), 2), dim3(256), 0, st,

@@ -359,3 +359,22 @@ def test_norm_mean_far_from_zero_costs_no_bits(dtype, shift, t, n):
     close(y, want, 1 + 2 * want.abs(), dtype)
     assert ((mean.double().cpu() - m).abs() <= 2.0 ** -24 * m.abs() + UNITS / r).all()
     assert ((rstd.double().cpu() - r).abs() <= UNITS * r).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS.get)
+@pytest.mark.parametrize("t,n", [(5, 64), (300, 777), (700, 4096), (130, 16384), (140, 16386), (300, 32768)])
+def test_norm_backward_in_place(dtype, t, n):
+    """dx over x, over dy and over the gradient that is added to it: the three gradients are what they are apart."""
+    g = torch.Generator().manual_seed(n)
+    x, dy, r = (_draw(g, dtype, t, n).cuda() for _ in range(3))
+    w = _draw(g, dtype, n).cuda()
+    _, mean, rstd = pg.layer_norm(x, w, stats=True)
+    want = pg.layer_norm_backward(dy, x, w, mean, rstd, r)
+    lib, code = pg.load_library(), 0 if dtype == torch.float32 else 1
+    for over in range(3):
+        at = [v.clone() for v in (x, dy, r)]
+        dw, db = torch.empty_like(w), torch.empty_like(w)
+        rc = lib.sgemm_layer_norm_backward(code, t, n, at[1].data_ptr(), n, at[0].data_ptr(), n, w.data_ptr(),
+                                           mean.data_ptr(), rstd.data_ptr(), at[2].data_ptr(), n, at[over].data_ptr(), n,
+                                           dw.data_ptr(), db.data_ptr(), torch.cuda.current_stream().cuda_stream)
+        assert rc == 0 and all(torch.equal(a, b) for a, b in zip((at[over], dw, db), want)), over

@@ -783,10 +783,22 @@ Shape shape_of(int64_t rows, int64_t n, int most_v, int small_blocks, int large_
 }
 
 // Rows of single elements take eight per thread: their addresses are many.
-int most_vectors(int access, int most) { return access == 1 ? 1 : most; }
+constexpr int most_vectors(int access, int most) { return access == 1 ? 1 : most; }
+template <typename T>
+constexpr int kForwardVectors = 8 / static_cast<int>(sizeof(T));
+constexpr int kBackwardVectors = 2;
+// f(512 threads to a block?): fewer than the most vectors per thread mean a row that a warp holds, more of them one that
+// 512 threads hold no other way.
+template <int V, int MOST, typename F>
+cudaError_t with_threads(const Shape& s, F f) {
+    if constexpr (V == MOST)
+        return s.threads > 256 ? f(std::true_type()) : f(std::false_type());
+    else
+        return f(std::integral_constant<bool, (V > MOST)>());
+}
 template <typename T>
 Shape backward_shape(int64_t rows, int64_t n, int access, int num_sms) {
-    return shape_of<T>(rows, n, most_vectors(access, 2), kBackwardBlocks, 1, num_sms);
+    return shape_of<T>(rows, n, most_vectors(access, kBackwardVectors), kBackwardBlocks, 1, num_sms);
 }
 
 // The widest access (elements) that every row allows.
@@ -841,24 +853,27 @@ cudaError_t run_norm(NormParams p, Shape s, int num_sms, cudaStream_t st) {
 template <typename T, int G, int V>
 cudaError_t run_norm(const NormParams& p, const Shape& s, int num_sms, cudaStream_t st) {
     constexpr int VECTOR = 8 * V * static_cast<int>(sizeof(T)), S = VECTOR > 64 ? 1 : (VECTOR == 64 ? 2 : 6);
-    constexpr int SMALL = (VECTOR > 32) ? kMostThreads : 256;
-    return s.threads > 256 ? run_norm<T, G, V, S, kMostThreads>(p, s, num_sms, st)
-                           : run_norm<T, G, V, S, SMALL>(p, s, num_sms, st);
+    return with_threads<V, most_vectors(G, kForwardVectors<T>)>(s, [&](auto many) {
+        constexpr int NT = decltype(many)::value || VECTOR > 32 ? kMostThreads : 256;
+        return run_norm<T, G, V, S, NT>(p, s, num_sms, st);
+    });
 }
 template <typename T, int G, int V, bool FULL, bool PARTS>
 cudaError_t run_backward(const NormBackwardParams& p, const Shape& s, cudaStream_t st) {
     constexpr int BYTES = 8 * V * static_cast<int>(sizeof(T)), S = BYTES > 64 ? 1 : 128 / BYTES;
-    if constexpr (!PARTS)
-        if (s.threads > 256) {
+    return with_threads<V, most_vectors(G, kBackwardVectors)>(s, [&](auto many) {
+        constexpr bool MANY = decltype(many)::value;
+        constexpr int NT = MANY ? kMostThreads : 256, B = MANY ? 1 : kBackwardBlocks;
+        if constexpr (MANY && PARTS) {
+            return cudaErrorInvalidValue;  // (parts of a warp hold their rows)
+        } else {
             static std::atomic<uint64_t> done{0};
-            return launch_rows(norm_backward_kernel<T, G, V, S, kMostThreads, 1, FULL, false>, done,
-                               Stages<T, G, V, 3, S, kMostThreads>::SHARED, p, s, st);
+            // teams of fewer than all threads add their sums in the same memory
+            const size_t sums = MANY ? 0 : static_cast<size_t>(NT) * 8 * V * 4;
+            return launch_rows(norm_backward_kernel<T, G, V, S, NT, B, FULL, PARTS>, done,
+                               std::max(Stages<T, G, V, 3, S, NT>::SHARED, sums), p, s, st);
         }
-    constexpr int B = kBackwardBlocks;
-    static std::atomic<uint64_t> done{0};
-    // the teams' sums use the same memory
-    return launch_rows(norm_backward_kernel<T, G, V, S, 256, B, FULL, PARTS>, done,
-                       std::max(Stages<T, G, V, 3, S, 256>::SHARED, static_cast<size_t>(256) * 8 * V * 4), p, s, st);
+    });
 }
 // Without tests of columns where 32 columns per thread fill their teams: 4096 x 16384 with residual 128 us instead of
 // 174 (bfloat16), 194 instead of 233 (float32).  Fewer columns per thread run better with the tests (16384 x 4096 bfloat16
@@ -886,7 +901,7 @@ cudaError_t norm(NormParams p, int num_sms, cudaStream_t st) {
     if (p.n > kHeld)
         return launch_kernel(true, p.vec ? norm_wide_kernel<T, 8> : norm_wide_kernel<T, 1>, dim3(static_cast<unsigned>(p.rows)), dim3(1024), 0, st, p);
     const int access = widest<T>(p.n, {{p.x, p.ldx}, {p.y, p.ldy}, {p.w, 0}, {p.b, 0}});
-    const Shape s = shape_of<T>(p.rows, p.n, most_vectors(access, 8 / static_cast<int>(sizeof(T))), kForwardThreads / 256,
+    const Shape s = shape_of<T>(p.rows, p.n, most_vectors(access, kForwardVectors<T>), kForwardThreads / 256,
                                 kForwardThreads / kMostThreads, num_sms);
     p.warps = std::max(s.team / kWarp, 1);
     p.lanes = s.team;

@@ -219,28 +219,28 @@ cudaError_t dispatch(const Product& p, int rows, int num_sms, cudaStream_t st) {
     // 4096 x 4096 bfloat16: 8.7, 8.1, 9.5).  bfloat16 loaded one by one would spill.
     constexpr bool f32 = sizeof(T) == 4;
     constexpr int F = f32 || VEC ? 8 : 4, U = f32 ? 1 : 2;
-    switch (rows) {
-        case 1: return run<T, VEC, GATED, 1, F, U, 2>(p, num_sms, st);
-        case 2: return run<T, VEC, GATED, 2, F, U, 2>(p, num_sms, st);
-        case 3: return run<T, VEC, GATED, 3, f32 ? 8 : 4, f32 ? 1 : (VEC ? 4 : 2), 2>(p, num_sms, st);
-        default: break;
-    }
-    // more than four rows of bfloat16 are a longer list's, in further passes (few_rows)
-    if constexpr (std::is_same<T, float>::value) {
-        switch (rows) {
-            case 4: break;
-            case 5: return run<T, VEC, GATED, 5, 4, 2, 2>(p, num_sms, st);
-            case 6: return run<T, VEC, GATED, 6, 4, 2, 2>(p, num_sms, st);
-            case 7:
-            case 8: return run<T, VEC, GATED, 8, 4, 2, 2>(p, num_sms, st);
-            case 9:
-            case 10:
-            case 11:
-            case 12: return run<T, VEC, GATED, 12, 4, 1, 2>(p, num_sms, st);
-            default: return run<T, VEC, GATED, 16, 4, 1, 2>(p, num_sms, st);
+    if (rows == 1) return run<T, VEC, GATED, 1, F, U, 2>(p, num_sms, st);
+    if (rows == 2 || (GATED && VEC && !f32)) return run<T, VEC, GATED, 2, F, U, 2>(p, num_sms, st);  // no more (few_rows)
+    if constexpr (!(GATED && VEC && !f32)) {
+        if (rows == 3) return run<T, VEC, GATED, 3, f32 ? 8 : 4, f32 ? 1 : (VEC ? 4 : 2), 2>(p, num_sms, st);
+        // more than four rows of bfloat16 are a longer list's, in further passes (few_rows)
+        if constexpr (f32) {
+            switch (rows) {
+                case 4: break;
+                case 5: return run<T, VEC, GATED, 5, 4, 2, 2>(p, num_sms, st);
+                case 6: return run<T, VEC, GATED, 6, 4, 2, 2>(p, num_sms, st);
+                case 7:
+                case 8: return run<T, VEC, GATED, 8, 4, 2, 2>(p, num_sms, st);
+                case 9:
+                case 10:
+                case 11:
+                case 12: return run<T, VEC, GATED, 12, 4, 1, 2>(p, num_sms, st);
+                default: return run<T, VEC, GATED, 16, 4, 1, 2>(p, num_sms, st);
+            }
         }
+        return run<T, VEC, GATED, 4, 4, 2, 2>(p, num_sms, st);
     }
-    return run<T, VEC, GATED, 4, 4, 2, 2>(p, num_sms, st);
+    return cudaErrorInvalidValue;
 }
 
 template <typename T>

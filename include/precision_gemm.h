@@ -520,7 +520,9 @@ int sgemm_block_linear(int dtype, int64_t t, int64_t n, int64_t k, const void *x
  *   with its ld, ldy (9, 10); mean and rstd, t floats each, or NULL (11, 12):
  *   sgemm_layer_norm_backward reads them.
  *
- * A NaN or infinity makes its own row NaN.
+ * A NaN or infinity makes its own row NaN, and so does a sum of x beyond FP32's largest
+ * number; where only the squares' sum is beyond it (a spread of 1e19 / sqrt(n) and more)
+ * rstd is 0 and y is bias.
  */
 int sgemm_layer_norm(int dtype, int64_t t, int64_t n, const void *x, int64_t ldx, const void *w,
                      const void *bias, float eps, void *y, int64_t ldy, float *mean, float *rstd,

@@ -404,7 +404,8 @@ def layer_norm(x, w=None, bias=None, eps=1e-5, stats=False, out=None, stream=Non
     """y = (x - mean) rstd w + bias for the rows of x (..., n), w and bias (n) or None,
     with rstd = (variance + eps)^-1/2; returns y.  stats=True also returns mean and rstd
     (float32, one of each row), which layer_norm_backward reads; a tensor given as out,
-    which may be x, is written instead."""
+    which may be x, is written instead.  Sums are float32: rows whose sum leaves its range
+    are NaN, rows whose squares' sum alone does have rstd 0."""
     if stream is not None:
         return _on(stream, layer_norm, x, w, bias, eps, stats, out)
     lib = load_library()

@@ -378,3 +378,18 @@ def test_norm_backward_in_place(dtype, t, n):
                                            mean.data_ptr(), rstd.data_ptr(), at[2].data_ptr(), n, at[over].data_ptr(), n,
                                            dw.data_ptr(), db.data_ptr(), torch.cuda.current_stream().cuda_stream)
         assert rc == 0 and all(torch.equal(a, b) for a, b in zip((at[over], dw, db), want)), over
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS.get)
+@pytest.mark.parametrize("n", [64, 777, 4096, 20000])
+def test_norm_sums_beyond_float32(dtype, n):
+    """Rows of large values beside ordinary ones: a sum beyond the range makes its row NaN, squares beyond
+    it make rstd 0 and the row its bias."""
+    g = torch.Generator().manual_seed(n)
+    x, b = _draw(g, dtype, 6, n), _draw(g, dtype, n).cuda()
+    want = pg.layer_norm(x.cuda(), None, b)
+    x[1], x[4] = 3e38, x[4] * 1e30
+    y, mean, rstd = pg.layer_norm(x.cuda(), None, b, stats=True)
+    assert torch.isnan(y[1]).all() and rstd[4] == 0 and torch.equal(y[4], b)
+    keep = [0, 2, 3, 5]
+    assert torch.equal(y[keep], want[keep])

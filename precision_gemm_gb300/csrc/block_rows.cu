@@ -11,8 +11,8 @@
 // (kRawValues), while the first weights are on their way from HBM.  Up to eight warps share a weight
 // row's k; their sums are added in order.
 //
-// Measured with quantized x (L2 cold): 1 and 8 rows x 8192 x 4096 9.1 and 11.5 us (3.7 and 3.0 TB/s), 32768 x 4096
-// 26.4 and 28.5 us (5.1 and 4.7 TB/s); the tensor-core kernel of block.cu needs 15 and 32 us.
+// Measured with quantized x (L2 cold): 1 and 8 rows x 8192 x 4096 9.4 and 10.7 us (3.6 and 3.1 TB/s), 32768 x 4096
+// 27.0 and 29.3 us (5.0 and 4.6 TB/s); the tensor-core kernel of block.cu needs 14 and 32 us.
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -227,8 +227,8 @@ static size_t rows_shared(int64_t t, int64_t k) {
 }
 
 // Nine to sixteen rows take two instructions side by side, where that beats the tensor-core kernel with its slices
-// of k: 9 and 16 rows of 1024 x 1024 6.3 and 7.9 us (8.2 and 8.2), of 4096 x 4096 10.0 and 11.9 (12.3 and 12.6), of
-// 8192 x 4096 13.1 and 15.3 (15.1 and 16.0), but of 32768 x 4096 31.6 and 35.9 (32.0 and 30.6).
+// of k: 9 and 16 rows of 1024 x 1024 6.3 and 7.7 us (7.2 and 7.5), of 4096 x 4096 8.8 and 11.3 (11.6 and 12.0), of
+// 8192 x 4096 12.6 and 14.7 (14.6 and 14.8), but of 32768 x 4096 31.6 and 35.9 (32.7 and 31.0).
 bool block_few_rows(int64_t t, int64_t n, int64_t k) {
     return t <= (n * k <= int64_t(1) << 25 ? 2 * kCols : kCols) && k > 0 && rows_shared(t, k) <= kMostShared;
 }

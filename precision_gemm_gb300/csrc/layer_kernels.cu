@@ -122,9 +122,15 @@ __global__ void __launch_bounds__(256, 4) dact_kernel(int64_t rows, int64_t n, c
 // sums of its 2 n columns in part (slabs x 2 n), with the threads laid out as in dact_kernel: thread
 // (l, c) takes rows l, l + 8, ... and eight columns, neighbouring ones where all rows are whole eights at
 // 16-byte boundaries (VEC), else every 32nd, so that a warp's single elements are neighbours.
-// dz null: the sums alone.  HBM-bound: reads dy and z, writes dz.  bfloat16 runs best with as many threads as fit (8192 x 4096, gelu, with
-// dbias: 64 us, 5.2 TB/s; 79 with half as many of two rows' loads each), float32, whose dz are three parts,
-// with half of them (147 us, 5.5 TB/s; 163).
+// dz null: the sums alone.
+//
+// For bfloat16 dz is rounded to it, the type of the products' operands: dx and dw then carry two
+// roundings, 0.0023 of their size where one is 0.0017.  A second part of dz would keep it and double both
+// products' time.  The sums take dz unrounded.
+//
+// HBM-bound: reads dy and z, writes dz.  bfloat16 runs best with as many threads as fit (8192 x 4096, gelu, with
+// dbias: 63 us, 5.3 TB/s; 79 with half as many of two rows' loads each), float32, whose dz are three parts,
+// with half of them (147 us, 5.5 TB/s; 163).  The sums alone take 41 us of the 63.
 template <typename T, int PARTS, bool VEC>
 __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2)
     dgate_kernel(int64_t rows, int64_t n, const T* dy, int64_t lddy, const T* z, int64_t ldz, int act, bf16* dz,

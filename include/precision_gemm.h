@@ -512,8 +512,9 @@ int sgemm_block_linear(int dtype, int64_t t, int64_t n, int64_t k, const void *x
 
 /*
  * sgemm_layer_norm -- of each row of x: mean = sum x / n, rstd = (sum (x - mean)^2 / n +
- * eps)^-1/2, y = (x - mean) rstd w + bias, the squares taken around the mean, which is off
- * by no more than the sums' rounding is worth in y, however far from zero it lies.
+ * eps)^-1/2, y = (x - mean) rstd w + bias.  The differences from the mean have FP32's accuracy
+ * of their own size, however far from zero the mean lies; the mean that is returned is one
+ * FP32 number.
  *
  *   dtype (1); t >= 0, n >= 1 (2, 3): x and y are t x n; x, ldx (4, 5); w and bias, n
  *   elements each, or NULL for ones and zeros (6, 7); eps >= 0 (8); y, which may be x
@@ -534,6 +535,8 @@ int sgemm_layer_norm(int dtype, int64_t t, int64_t n, const void *x, int64_t ldx
  *
  *     dx = rstd (g - sum g / n - h sum(g h) / n) + residual,
  *     dw = the sum over rows of dy h,   dbias = the sum of dy's rows.
+ *
+ * h is formed from the mean given, whose rounding to FP32 counts 2^-24 |mean| rstd in it.
  *
  *   dtype, t, n (1-3); dy, lddy (4, 5); x, ldx (6, 7); w or NULL (8); mean, rstd
  *   (9, 10); residual, t x n, or NULL: a gradient that reaches x past the norm, added to

@@ -502,8 +502,9 @@ int sgemm_quantize(int dtype, int64_t t, int64_t k, int block_rows, const void *
  * A block's products are summed by the tensor cores, the blocks' sums multiplied by the
  * product of their two scales and added in FP32 in the order of k.  The scales' product is
  * an FP32 number itself: where it lies below 2^-126 (rows of x near 2^-126, say, and small
- * weights) results lose bits, where it overflows they are infinite or NaN.  e4m3 rows that start at 16-byte boundaries (address and ld) are
- * read in place, others copied first.  k == 0 leaves the product zero.
+ * weights) results lose bits, where it overflows they are infinite or NaN.  e4m3 rows that
+ * start at 16-byte boundaries (address and ld) are read in place, others copied first.
+ * k == 0 leaves the product zero.
  */
 int sgemm_block_linear(int dtype, int64_t t, int64_t n, int64_t k, const void *x, int64_t ldx,
                        const float *x_scales, int64_t ldxs, const uint8_t *w, int64_t ldw,
